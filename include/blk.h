@@ -322,6 +322,110 @@ blk_status blk_attn_gqa(blk_handle* h, const void* q, const void* k, const void*
 blk_status blk_mlp(blk_handle* h, const void* resid, const void* h_normed, const blk_weights* w,
                    int rows, void* out, void* workspace, size_t workspace_bytes, void* stream);
 
+/* ---- Packed, mixed-length batches and a KV cache held in 4 bits ----
+ * Prompts of different lengths packed into one run of token rows, and single tokens over
+ * their cache: blk_qk_norm_rope, then blk_attn_packed and blk_kv4_store for the prompts;
+ * blk_qk_norm_rope, blk_kv4_store and blk_attn_decode_kv4 for a token per sequence. The
+ * pages have no cache and pad their batches; the arithmetic is the block's. The plain
+ * projections come from blk_qkv_rope of a no_rope handle without qk_norm (batch 1).
+ * These calls run on the device their handle was created on, which must be current
+ * (INVALID_ARG). Two calls may run at the same time on different streams as long as they
+ * share no workspace and no output. */
+
+/* Head rows of packed tokens: element (row r, head j, channel c) at
+ * ptr + r * row_stride + j * head_stride + c, strides in elements, multiples of 16 bytes
+ * and not negative (those of a dimension of one element are ignored). Both [rows, heads, d]
+ * and [heads, rows, d] layouts, and columns of a fused projection, can be passed. Rows
+ * that a call writes must not overlap each other (INVALID_ARG) nor any input, unless the
+ * call says so. */
+typedef struct {
+  void* ptr;
+  long long row_stride;
+  long long head_stride;
+} blk_head_rows;
+
+/* Rotary positions with several axes (time, height, width of images and video): pair i (of
+ * d/2) turns by its axis's position. n_axes 1..4; sections[a] >= 0 pairs belong to axis a,
+ * d/2 in all. interleaved == 0: the sections follow one another. interleaved == 1: the axes
+ * are dealt out in turn: pair i belongs to axis a = i % n_axes if a > 0 and
+ * i < n_axes * sections[a], else to axis 0 (which must give sections[a] pairs to each axis:
+ * n_axes * (sections[a] - 1) + a < d/2 for a > 0). */
+typedef struct {
+  int n_axes;
+  int sections[4];
+  int interleaved;
+} blk_rope_axes;
+
+/* Stage: per-head RMSNorm of q and k (when the handle has qk_norm; gains q_gain, k_gain [d],
+ * else ignored) and the handle's rotary (unless no_rope) in one pass, both dtypes:
+ * q, q_out [rows, n_heads, d], k, k_out [rows, n_kv_heads, d]. pos: device int32
+ * [n_axes, rows] (ignored with no_rope), each in [0, max_seq): another value is clamped and
+ * sets the status word to INVALID_ARG (blk_last_status). axes NULL: one axis. q_out may be
+ * q and k_out k (same pointer and strides: in place). fp32 handles need head_dim % 8 == 0.
+ * Errors: INVALID_ARG, UNSUPPORTED, ALIGNMENT, CUDA. */
+blk_status blk_qk_norm_rope(blk_handle* h, const blk_head_rows* q, const blk_head_rows* k, int rows, const int* pos,
+                            const blk_rope_axes* axes, const void* q_gain, const void* k_gain,
+                            const blk_head_rows* q_out, const blk_head_rows* k_out, void* stream);
+
+/* Stage: causal grouped-query attention over packed whole prompts (bf16 handles). Sequence
+ * b < batch is rows cu_seqlens[b] .. cu_seqlens[b+1]-1 of q, o [rows, n_heads, 128] and k, v
+ * [rows, n_kv_heads, 128]; its query i sees its keys j <= i (i - j < sliding_window when the
+ * handle has one). cu_seqlens: device int32 [batch + 1], rising from >= 0 to <= rows; another
+ * one sets the status word to INVALID_ARG and is read clamped. Sequences may be empty; rows of
+ * no sequence are neither used nor written: what they hold, NaN included, reaches no
+ * output. (Within a sequence a NaN or infinity in v reaches the outputs of its 128-row tile
+ * of keys, as 0 * NaN does.) workspace: blk_attn_packed_workspace_bytes(h, rows, batch).
+ * Errors: INVALID_ARG, UNSUPPORTED (fp32 handle), ALIGNMENT, WORKSPACE, CUDA. */
+size_t blk_attn_packed_workspace_bytes(const blk_handle* h, int rows, int batch);
+blk_status blk_attn_packed(blk_handle* h, const blk_head_rows* q, const blk_head_rows* k, const blk_head_rows* v,
+                           int rows, const int* cu_seqlens, int batch, const blk_head_rows* o, void* workspace,
+                           size_t workspace_bytes, void* stream);
+
+/* A KV cache in 4 bits (5 with its scales): k, v [batch, Hkv, capacity, 64] code bytes,
+ * k_scale, v_scale [batch, Hkv, capacity, 8] bf16, lens [batch] device int32, positions
+ * filled. A row is 128 channels in four groups of 32. A group with least value lo and
+ * greatest hi keeps scale = bf16((hi - lo) / 15), offset = lo and the codes
+ * clamp(rint((x - offset) / scale), 0, 15) (0 where the scale is 0; fp32 arithmetic); a code
+ * stands for offset + scale * code. A group with a NaN or an infinity, or whose hi - lo
+ * passes the fp32 range, stands for NaN. A row's 8 scale numbers are its four scales, then
+ * its four offsets. Code byte 16 t + 4 j + 2 u + e holds channel 16 (2 j + e) + 2 t + u in
+ * its low nibble and the channel 8 further in its high one. */
+typedef struct {
+  void *k, *k_scale, *v, *v_scale;
+  int capacity;
+  int* lens;
+} blk_kv4_cache;
+
+/* Quantises the bf16 rows k, v [rows, n_kv_heads, 128] into the cache. Sequence b's rows
+ * cu_seqlens[b] .. cu_seqlens[b+1]-1 (cu_seqlens NULL: row b alone, rows == batch) go to its slots
+ * starts[b], starts[b]+1, ... (starts NULL: lens[b], an append), and lens[b] becomes the slot
+ * behind the last one. starts may not overlap lens unless it is lens (an append). Rows of no
+ * sequence are ignored; a row whose slot is outside the cache is left out, lens stops at the
+ * capacity and the status word says CACHE_FULL (or, when the caller passes
+ * host_lens_max >= 0, the largest slot behind the last one of this call, the call itself).
+ * Errors: INVALID_ARG, UNSUPPORTED (fp32 handle), ALIGNMENT, CACHE_FULL, CUDA. */
+blk_status blk_kv4_store(blk_handle* h, const blk_head_rows* k, const blk_head_rows* v, int rows,
+                         const int* cu_seqlens, const int* starts, int batch, const blk_kv4_cache* cache,
+                         int host_lens_max, void* stream);
+
+/* The reverse: the values of slots starts[b], ... (starts NULL: 0, ...) as bf16 rows, packed
+ * by cu_seqlens (NULL: one row per sequence, rows == batch). lens is not looked at; a slot outside
+ * the cache gives zeros and sets the status word to INVALID_ARG. Rows of no sequence are left as
+ * they were. Errors: INVALID_ARG, UNSUPPORTED, ALIGNMENT, CUDA. */
+blk_status blk_kv4_load(blk_handle* h, const blk_kv4_cache* cache, const int* cu_seqlens, const int* starts, int batch,
+                        int rows, const blk_head_rows* k, const blk_head_rows* v, void* stream);
+
+/* Stage: one query per sequence over the 4-bit cache: o[b, h, :] = softmax(q[b, h] . k^ /
+ * sqrt(128)) v^ over slots s < lens[b] (the last sliding_window of them when the handle has
+ * a window), k^ and v^ the values the codes stand for. q, o [batch, n_heads, 128] bf16, a row
+ * per sequence. lens[b] == 0 gives a zero row; lens beyond the capacity is read as the
+ * capacity. What unused slots hold reaches no output. workspace:
+ * blk_attn_decode_kv4_workspace_bytes(h, batch).
+ * Errors: INVALID_ARG, UNSUPPORTED (fp32 handle), ALIGNMENT, WORKSPACE, CUDA. */
+size_t blk_attn_decode_kv4_workspace_bytes(const blk_handle* h, int batch);
+blk_status blk_attn_decode_kv4(blk_handle* h, const blk_head_rows* q, const blk_kv4_cache* cache, int batch,
+                               const blk_head_rows* o, void* workspace, size_t workspace_bytes, void* stream);
+
 /* Scratch bytes a stage entry point needs for `rows` token rows. */
 size_t blk_stage_workspace_bytes(const blk_handle* h, int rows);
 

@@ -54,6 +54,21 @@ class blk_taps(ctypes.Structure):
     _fields_ = [(n, c_void_p) for n in TAP_NAMES]
 
 
+class blk_head_rows(ctypes.Structure):
+    _fields_ = [("ptr", c_void_p), ("row_stride", c_longlong), ("head_stride", c_longlong)]
+
+
+class blk_rope_axes(ctypes.Structure):
+    _fields_ = [("n_axes", c_int), ("sections", c_int * 4), ("interleaved", c_int)]
+
+
+class blk_kv4_cache(ctypes.Structure):
+    _fields_ = [("k", c_void_p), ("k_scale", c_void_p), ("v", c_void_p), ("v_scale", c_void_p), ("capacity", c_int),
+                ("lens", c_void_p)]
+
+
+_ROWS = POINTER(blk_head_rows)
+
 # name -> (restype, argtypes); the exported symbols of include/blk.h
 SIGNATURES = {
     "blk_create": (c_int, [POINTER(blk_desc), POINTER(c_void_p)]),
@@ -70,6 +85,18 @@ SIGNATURES = {
                              c_void_p, c_size_t, c_void_p]),
     "blk_mlp": (c_int, [c_void_p, c_void_p, c_void_p, POINTER(blk_weights), c_int, c_void_p, c_void_p, c_size_t,
                         c_void_p]),
+    "blk_qk_norm_rope": (c_int, [c_void_p, _ROWS, _ROWS, c_int, c_void_p, POINTER(blk_rope_axes), c_void_p, c_void_p,
+                                 _ROWS, _ROWS, c_void_p]),
+    "blk_attn_packed_workspace_bytes": (c_size_t, [c_void_p, c_int, c_int]),
+    "blk_attn_packed": (c_int, [c_void_p, _ROWS, _ROWS, _ROWS, c_int, c_void_p, c_int, _ROWS, c_void_p, c_size_t,
+                                c_void_p]),
+    "blk_kv4_store": (c_int, [c_void_p, _ROWS, _ROWS, c_int, c_void_p, c_void_p, c_int, POINTER(blk_kv4_cache), c_int,
+                              c_void_p]),
+    "blk_kv4_load": (c_int, [c_void_p, POINTER(blk_kv4_cache), c_void_p, c_void_p, c_int, c_int, _ROWS, _ROWS,
+                             c_void_p]),
+    "blk_attn_decode_kv4_workspace_bytes": (c_size_t, [c_void_p, c_int]),
+    "blk_attn_decode_kv4": (c_int, [c_void_p, _ROWS, POINTER(blk_kv4_cache), c_int, _ROWS, c_void_p, c_size_t,
+                                    c_void_p]),
     "blk_stage_workspace_bytes": (c_size_t, [c_void_p, c_int]),
     "blk_last_status": (c_int, [c_void_p]),
     "blk_xielu_effective": (None, [c_float, c_float, c_float, POINTER(c_float), POINTER(c_float)]),
@@ -139,6 +166,44 @@ def _stream_ptr(stream):
     return c_void_p(stream.cuda_stream)
 
 
+def _on_stream(device, stream):
+    """The device and stream that a call's own tensors (outputs, workspace) are made on and
+    its kernels run on: the given stream, or the device's current one."""
+    import torch
+    return torch.cuda.device(device) if stream is None else torch.cuda.stream(stream)
+
+
+def _check_tensor(t, name, dtype, device, shape=None):
+    if t.dtype != dtype or t.device != device:
+        raise ValueError(f"{name}: {dtype} on {device} is wanted, got {t.dtype} on {t.device}")
+    if shape is not None and (t.dim() != len(shape) or
+                              any(want is not None and have != want for have, want in zip(t.shape, shape))):
+        raise ValueError(f"{name}: shape {list(shape)} is wanted, got {list(t.shape)}")
+
+
+def _head_rows(t, name, dtype, device, rows, heads, d):
+    """A [rows, heads, d] tensor, of any row and head strides, as blk_head_rows."""
+    _check_tensor(t, name, dtype, device, (rows, heads, d))
+    rs, hs, cs = t.stride()
+    if cs != 1:
+        raise ValueError(f"{name}: the channels must be contiguous")
+    return blk_head_rows(t.data_ptr(), rs, hs)
+
+
+def _int32(t, name, device, n):
+    if t is None:
+        return None
+    _check_tensor(t, name, _torch().int32, device, (n,))
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: must be contiguous")
+    return c_void_p(t.data_ptr())
+
+
+def _torch():
+    import torch
+    return torch
+
+
 def xielu_effective(raw_alpha_p, raw_alpha_n, beta=0.5):
     ap, an = c_float(), c_float()
     lib().blk_xielu_effective(raw_alpha_p, raw_alpha_n, beta, ctypes.byref(ap), ctypes.byref(an))
@@ -179,6 +244,9 @@ class DecoderBlock:
         _check(lib().blk_create(ctypes.byref(self.desc), ctypes.byref(h)))
         self.handle = h
         self._ws = None
+        torch = _torch()
+        self._device = torch.device("cuda", torch.cuda.current_device())  # where the handle's tables live
+        self._dtype = torch.bfloat16 if self.desc.dtype == 1 else torch.float32
 
     @classmethod
     def from_workload(cls, wl, max_batch=None, max_seq=None):
@@ -310,6 +378,140 @@ class DecoderBlock:
         ws = self._workspace(self.stage_workspace_bytes(B * Tq), q.device)
         _check(lib().blk_attn_gqa(self.handle, _ptr(q), _ptr(k), _ptr(v), B, Tq, kv_stride, _ptr(kv_lens), _ptr(o),
                                   _ptr(ws), ws.numel(), _stream_ptr(stream)))
+
+    # Packed, mixed-length batches and the 4-bit cache. Outputs not passed, and every
+    # workspace, are made for the call on its stream: calls on several streams, and captured
+    # graphs, share none.
+
+    def _rows(self, t, name, rows, heads):
+        return _head_rows(t, name, self._dtype, self._device, rows, heads, self.desc.head_dim)
+
+    def qk_norm_rope(self, q, k, positions, q_gain=None, k_gain=None, sections=None, interleaved=False, q_out=None,
+                     k_out=None, stream=None):
+        """Per-head RMSNorm (a qk_norm handle, with gains [d]) and rotary of packed rows q [N, H, d]
+        and k [N, Hkv, d], of any row and head strides. positions: int32 [N], or [axes, N] with
+        `sections`, the rotary pairs of each axis (one after the other, or interleaved). Returns
+        (q_out, k_out), [N, heads, d]; pass q and k as outputs to work in place."""
+        torch = _torch()
+        d, n = self.desc, q.shape[0]
+        axes, pos = None, None
+        if not d.no_rope:
+            n_axes = 1 if sections is None else len(sections)
+            if not 1 <= n_axes <= 4:
+                raise ValueError("sections: 1 to 4 position axes")
+            p = positions.view(1, -1) if positions.dim() == 1 else positions
+            _check_tensor(p, "positions", torch.int32, self._device, (n_axes, n))
+            if not p.is_contiguous():
+                raise ValueError("positions: must be contiguous")
+            pos = c_void_p(p.data_ptr())
+            if sections is not None:
+                axes = ctypes.byref(blk_rope_axes(n_axes, (c_int * 4)(*sections), int(bool(interleaved))))
+        if d.qk_norm:
+            for name, g in (("q_gain", q_gain), ("k_gain", k_gain)):
+                if g is None:
+                    raise ValueError(f"{name}: the handle norms queries and keys")
+                _check_tensor(g, name, self._dtype, self._device, (d.head_dim,))
+                if not g.is_contiguous():
+                    raise ValueError(f"{name}: must be contiguous")
+        with _on_stream(self._device, stream):
+            if q_out is None:
+                q_out = torch.empty(n, d.n_heads, d.head_dim, dtype=self._dtype, device=self._device)
+            if k_out is None:
+                k_out = torch.empty(n, d.n_kv_heads, d.head_dim, dtype=self._dtype, device=self._device)
+            _check(lib().blk_qk_norm_rope(self.handle, self._rows(q, "q", n, d.n_heads),
+                                          self._rows(k, "k", n, d.n_kv_heads), n, pos, axes,
+                                          _ptr(q_gain) if d.qk_norm else None, _ptr(k_gain) if d.qk_norm else None,
+                                          self._rows(q_out, "q_out", n, d.n_heads),
+                                          self._rows(k_out, "k_out", n, d.n_kv_heads), _stream_ptr(stream)))
+        return q_out, k_out
+
+    def attn_packed(self, q, k, v, cu_seqlens, out=None, stream=None):
+        """Causal attention over packed whole prompts: q [N, H, d], k, v [N, Hkv, d], of any row and
+        head strides; cu_seqlens int32 [B + 1]: sequence b is rows cu_seqlens[b] .. cu_seqlens[b + 1] - 1.
+        Returns out [N, H, d]; rows of no sequence are left as they were (undefined in an out
+        made here)."""
+        torch = _torch()
+        d, n, batch = self.desc, q.shape[0], cu_seqlens.numel() - 1
+        cu = _int32(cu_seqlens, "cu_seqlens", self._device, batch + 1)
+        with _on_stream(self._device, stream):
+            if out is None:
+                out = torch.empty(n, d.n_heads, d.head_dim, dtype=self._dtype, device=self._device)
+            ws = torch.empty(lib().blk_attn_packed_workspace_bytes(self.handle, n, batch), dtype=torch.uint8,
+                             device=self._device)
+            _check(lib().blk_attn_packed(self.handle, self._rows(q, "q", n, d.n_heads),
+                                         self._rows(k, "k", n, d.n_kv_heads), self._rows(v, "v", n, d.n_kv_heads), n,
+                                         cu, batch, self._rows(out, "out", n, d.n_heads), c_void_p(ws.data_ptr()),
+                                         ws.numel(), _stream_ptr(stream)))
+        return out
+
+    def kv4_cache(self, batch, capacity):
+        """An empty KV cache in 4 bits: dict(k, k_scale, v, v_scale, lens)."""
+        torch = _torch()
+        n = (batch, self.desc.n_kv_heads, capacity)
+        c = {"lens": torch.zeros(batch, dtype=torch.int32, device=self._device)}
+        for x in ("k", "v"):
+            c[x] = torch.zeros(*n, 64, dtype=torch.uint8, device=self._device)
+            c[x + "_scale"] = torch.zeros(*n, 8, dtype=torch.bfloat16, device=self._device)
+        return c
+
+    def _kv4(self, cache):
+        torch = _torch()
+        batch, _, cap, _ = cache["k"].shape
+        for name, t, last in (("k", torch.uint8, 64), ("k_scale", torch.bfloat16, 8), ("v", torch.uint8, 64),
+                              ("v_scale", torch.bfloat16, 8)):
+            _check_tensor(cache[name], name, t, self._device, (batch, self.desc.n_kv_heads, cap, last))
+            if not cache[name].is_contiguous():
+                raise ValueError(f"cache {name}: must be contiguous")
+        lens = _int32(cache["lens"], "lens", self._device, batch)
+        return blk_kv4_cache(cache["k"].data_ptr(), cache["k_scale"].data_ptr(), cache["v"].data_ptr(),
+                             cache["v_scale"].data_ptr(), cap, lens), batch
+
+    def kv4_store(self, cache, k, v, cu_seqlens=None, starts=None, host_lens_max=-1, stream=None):
+        """Quantises rows k, v [N, Hkv, 128] into the cache: sequence b's rows (cu_seqlens as in
+        attn_packed; None: row b alone) to slots starts[b], ... (None: lens[b], an append), and sets
+        lens[b] behind them. host_lens_max: the largest new length, to have the capacity checked
+        here; else rows that do not fit are left out and last_status() says so."""
+        c, batch = self._kv4(cache)
+        n, hkv = k.shape[0], self.desc.n_kv_heads
+        cu = _int32(cu_seqlens, "cu_seqlens", self._device, batch + 1)
+        st = _int32(starts, "starts", self._device, batch)
+        with _on_stream(self._device, stream):
+            _check(lib().blk_kv4_store(self.handle, self._rows(k, "k", n, hkv), self._rows(v, "v", n, hkv), n, cu, st,
+                                       batch, ctypes.byref(c), int(host_lens_max), _stream_ptr(stream)))
+
+    def kv4_load(self, cache, cu_seqlens=None, rows=None, starts=None, k_out=None, v_out=None, stream=None):
+        """The values of the cache's slots starts[b], ... (None: 0, ...) as packed bf16 rows (k, v)
+        [rows, Hkv, 128]: the rows that cu_seqlens gives each sequence (None: one each)."""
+        torch = _torch()
+        c, batch = self._kv4(cache)
+        n, d = batch if rows is None else rows, self.desc
+        cu = _int32(cu_seqlens, "cu_seqlens", self._device, batch + 1)
+        st = _int32(starts, "starts", self._device, batch)
+        with _on_stream(self._device, stream):
+            if k_out is None:
+                k_out = torch.empty(n, d.n_kv_heads, d.head_dim, dtype=self._dtype, device=self._device)
+            if v_out is None:
+                v_out = torch.empty(n, d.n_kv_heads, d.head_dim, dtype=self._dtype, device=self._device)
+            _check(lib().blk_kv4_load(self.handle, ctypes.byref(c), cu, st, batch, n,
+                                      self._rows(k_out, "k_out", n, d.n_kv_heads),
+                                      self._rows(v_out, "v_out", n, d.n_kv_heads), _stream_ptr(stream)))
+        return k_out, v_out
+
+    def attn_decode_kv4(self, q, cache, out=None, stream=None):
+        """One query per sequence, q [B, H, 128], over the lens[b] slots of the 4-bit cache (the last
+        sliding_window of them). Returns out [B, H, 128]; a sequence without keys gets zeros."""
+        torch = _torch()
+        d = self.desc
+        c, batch = self._kv4(cache)
+        with _on_stream(self._device, stream):
+            if out is None:
+                out = torch.empty(batch, d.n_heads, d.head_dim, dtype=self._dtype, device=self._device)
+            ws = torch.empty(lib().blk_attn_decode_kv4_workspace_bytes(self.handle, batch), dtype=torch.uint8,
+                             device=self._device)
+            _check(lib().blk_attn_decode_kv4(self.handle, self._rows(q, "q", batch, d.n_heads), ctypes.byref(c), batch,
+                                             self._rows(out, "out", batch, d.n_heads), c_void_p(ws.data_ptr()),
+                                             ws.numel(), _stream_ptr(stream)))
+        return out
 
     def mlp(self, resid, h_normed, weights, out, stream=None):
         rows = resid.numel() // resid.shape[-1]

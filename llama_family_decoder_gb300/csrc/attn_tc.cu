@@ -66,6 +66,11 @@ constexpr float kLog2e = 1.4426950408889634f;
 static_assert(kSmem <= 227 * 1024, "shared memory");
 static_assert(kQSub == kKVSub && kKStages == 2 && kVStages == 2, "the MMA issuers' descriptor steps and stage selects");
 
+// A query tile (or, without head pairs, a pair of them) of a packed sequence.
+struct __align__(16) PackedWork {
+  int row0, len, tile, unused;
+};
+
 struct AttnParams {
   CUtensorMap tq, tk, tv;
   void* o;
@@ -86,6 +91,11 @@ struct AttnParams {
   float sl2;
   DevStatus* status;
   unsigned long long wait_ns;
+  // packed sequences: the work list (heaviest first) and its length, both on the device, and
+  // the output's strides
+  const PackedWork* work;
+  const int* n_work;
+  long long o_row, o_head;
 };
 
 // 2^x on the MUFU unit (one instruction; -inf gives +0).
@@ -150,13 +160,28 @@ struct Slot {
 struct Item {
   Slot sl[kSlots];
   int b, kv_row, off, kv_lo, kv_hi, n_keys, t0, n_tiles;
+  int kvh, T;  // the KV head, the sequence's queries
 };
 
 // Item id, heaviest first: the far query tiles (more keys) get the small ids. Reads
 // the cache positions and key ranges, so it runs after pdl_wait.
+template <bool PACKED>
 __device__ __forceinline__ Item item_of(const AttnParams& p, int id) {
   Item it;
-  if (p.head_pairs) {
+  it.T = p.T;
+  if constexpr (PACKED) {
+    const int units = p.head_pairs ? p.H / 2 : p.H;  // items of one work entry
+    const PackedWork w = p.work[id / units];
+    const int r = id % units;
+    it.T = w.len;
+    it.b = w.row0;
+#pragma unroll
+    for (int g = 0; g < kSlots; ++g) {
+      const int qt = p.head_pairs ? w.tile : 2 * w.tile + g;
+      const int ok = qt * kBQ < w.len;
+      it.sl[g] = {p.head_pairs ? 2 * r + g : r, ok ? qt : 2 * w.tile, (ok ? qt : 2 * w.tile) * kBQ, ok};
+    }
+  } else if (p.head_pairs) {
     const int hp_n = p.H / 2;
     const int qt = p.n_qtiles - 1 - id / (p.B * hp_n);
     const int r = id % (p.B * hp_n);
@@ -177,18 +202,24 @@ __device__ __forceinline__ Item item_of(const AttnParams& p, int id) {
       it.sl[g] = {h, ok ? qt : 2 * k, (ok ? qt : 2 * k) * kBQ, ok};
     }
   }
-  const int kvh = it.sl[0].h / (p.H / p.Hkv);
-  it.kv_row = (it.b * p.Hkv + kvh) * p.kv_stride;
-  it.off = p.q_off ? p.q_off[it.b] : 0;  // keys 0 .. off - 1 are earlier positions in the cache
-  // visible keys: [kv_lo, kv_hi) (an attention_mask's run of real tokens, else all)
-  const int2 kr = p.key_range ? p.key_range[it.b] : make_int2(0, it.off + p.T);
-  it.kv_lo = kr.x;
-  it.kv_hi = kr.y;
+  it.kvh = it.sl[0].h / (p.H / p.Hkv);
+  if constexpr (PACKED) {
+    it.kv_row = it.b;  // the sequence's first row: keys and queries are the same rows
+    it.off = it.kv_lo = 0;
+    it.kv_hi = it.T;
+  } else {
+    it.kv_row = (it.b * p.Hkv + it.kvh) * p.kv_stride;
+    it.off = p.q_off ? p.q_off[it.b] : 0;  // keys 0 .. off - 1 are earlier positions in the cache
+    // visible keys: [kv_lo, kv_hi) (an attention_mask's run of real tokens, else all)
+    const int2 kr = p.key_range ? p.key_range[it.b] : make_int2(0, it.off + p.T);
+    it.kv_lo = kr.x;
+    it.kv_hi = kr.y;
+  }
   // the key tiles the item needs: the union of both slots' ranges
   int n_keys = 0, first_key = 1 << 30;
 #pragma unroll
   for (int g = 0; g < kSlots; ++g) {
-    const int kv_end = min(p.T, it.sl[g].m0 + kBQ);
+    const int kv_end = min(it.T, it.sl[g].m0 + kBQ);
     n_keys = max(n_keys, min(it.off + kv_end, it.kv_hi));
     first_key = min(first_key, max(it.kv_lo, p.window > 0 ? it.off + it.sl[g].m0 - p.window + 1 : 0));
   }
@@ -206,7 +237,9 @@ __device__ __forceinline__ int item_id(int k, int G, int c) { return k * G + ((k
 // item_id(0, G, c), item_id(1, G, c), ... Barrier phases and ring positions run on
 // across items, so that the next item's Q, first K/V tiles and first score products
 // overlap the current item's last softmax, PV and output store.
-template <bool F16>
+// PACKED: sequences of different lengths packed into one run of rows (see AttnParams::work);
+// q, k and v are 3-D maps (channel, head, row).
+template <bool F16, bool PACKED>
 __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_constant__ AttnParams p) {
   pdl_launch_dependents();
   extern __shared__ uint8_t smem_raw[];
@@ -236,6 +269,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const unsigned long long budget = p.wait_ns;
   const int G = gridDim.x, cta = blockIdx.x;
+  // one 64-channel half of a Q (or K, V) tile: rows from `row` of a head
+  auto load_half = [&](uint32_t dst, const CUtensorMap* m, int half, int head, int row, uint32_t bar) {
+    if constexpr (PACKED)
+      tma_load_3d(dst, m, 64 * half, head, row, bar);
+    else
+      tma_load_2d(dst, m, 64 * half, row, bar);
+  };
 
   if (threadIdx.x == 0) {
     mbar_init(q_full, 1);
@@ -271,6 +311,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
   __syncthreads();
   tc_fence_after();
   pdl_wait();  // q, k, v (and the cache positions, the key ranges) come from earlier kernels
+  const int n_items = PACKED ? *p.n_work * (p.head_pairs ? p.H / 2 : p.H) : p.n_items;
   const uint32_t tmem = *tmem_holder;  // S[g] (and P[g] over its first 64 columns): cols 128 g; O[g]: 256 + 128 g
   // What the producer lanes and the MMA lanes have in flight, for the drain after an
   // abort: the ring stages issued (with the parity of their last phase), the last Q
@@ -285,8 +326,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
       int J = 0;  // K tiles issued over all items
       for (int k = 0; !failed; ++k) {
         const int id = item_id(k, G, cta);
-        if (id >= p.n_items) break;
-        const Item it = item_of(p, id);
+        if (id >= n_items) break;
+        const Item it = item_of<PACKED>(p, id);
         // the Q buffer is free once both slots' score products of the previous item are done
         if (!mbar_wait(q_empty, (k & 1) ^ 1, budget, abort_flag)) {
           failed = true;
@@ -295,9 +336,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
         mbar_arrive_expect_tx(q_full, kSlots * kQBytes);
 #pragma unroll
         for (int g = 0; g < kSlots; ++g) {
-          const int q_row = (it.b * p.H + it.sl[g].h) * p.T + it.sl[g].m0;
-          tma_load_2d(smem_u32(sQ + g * kQBytes), &p.tq, 0, q_row, q_full);
-          tma_load_2d(smem_u32(sQ + g * kQBytes + kQSub), &p.tq, 64, q_row, q_full);
+          const int q_row = PACKED ? it.b + it.sl[g].m0 : (it.b * p.H + it.sl[g].h) * p.T + it.sl[g].m0;
+          load_half(smem_u32(sQ + g * kQBytes), &p.tq, 0, it.sl[g].h, q_row, q_full);
+          load_half(smem_u32(sQ + g * kQBytes + kQSub), &p.tq, 1, it.sl[g].h, q_row, q_full);
         }
         q_issued = true;
         q_parity = k & 1;
@@ -310,8 +351,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
           }
           mbar_arrive_expect_tx(k_full(s), kKVBytes);
           const int row = it.kv_row + (it.t0 + j) * kBK;
-          tma_load_2d(smem_u32(sK + s * kKVBytes), &p.tk, 0, row, k_full(s));
-          tma_load_2d(smem_u32(sK + s * kKVBytes + kKVSub), &p.tk, 64, row, k_full(s));
+          load_half(smem_u32(sK + s * kKVBytes), &p.tk, 0, it.kvh, row, k_full(s));
+          load_half(smem_u32(sK + s * kKVBytes + kKVSub), &p.tk, 1, it.kvh, row, k_full(s));
           issued |= 1u << s;
           parity = (parity & ~(1u << s)) | (ph << s);
         }
@@ -326,8 +367,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
       int J = 0;
       for (int k = 0; !failed; ++k) {
         const int id = item_id(k, G, cta);
-        if (id >= p.n_items) break;
-        const Item it = item_of(p, id);
+        if (id >= n_items) break;
+        const Item it = item_of<PACKED>(p, id);
         for (int j = 0; j < it.n_tiles; ++j, ++J) {
           const int s = J % kVStages;
           const uint32_t ph = (J / kVStages) & 1;
@@ -337,8 +378,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
           }
           mbar_arrive_expect_tx(v_full(s), kKVBytes);
           const int row = it.kv_row + (it.t0 + j) * kBK;
-          tma_load_2d(smem_u32(sV + s * kKVBytes), &p.tv, 0, row, v_full(s));
-          tma_load_2d(smem_u32(sV + s * kKVBytes + kKVSub), &p.tv, 64, row, v_full(s));
+          load_half(smem_u32(sV + s * kKVBytes), &p.tv, 0, it.kvh, row, v_full(s));
+          load_half(smem_u32(sV + s * kKVBytes + kKVSub), &p.tv, 1, it.kvh, row, v_full(s));
           issued |= 1u << s;
           parity = (parity & ~(1u << s)) | (ph << s);
         }
@@ -382,8 +423,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
       int J = 0;  // tiles over all items
       for (int k = 0; !failed; ++k) {
         const int id = item_id(k, G, cta);
-        if (id >= p.n_items) break;
-        const Item it = item_of(p, id);
+        if (id >= n_items) break;
+        const Item it = item_of<PACKED>(p, id);
         if (!mbar_wait(q_full, k & 1, budget, abort_flag)) {
           failed = true;
           break;
@@ -458,12 +499,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
     int J = 0;  // tiles over all items
     for (int k = 0; !failed; ++k) {
       const int id = item_id(k, G, cta);
-      if (id >= p.n_items) break;
-      const Item it = item_of(p, id);
+      if (id >= n_items) break;
+      const Item it = item_of<PACKED>(p, id);
       const Slot me = g == 0 ? it.sl[0] : it.sl[1];  // a select, not a run-time index into local memory
       const int m0 = me.m0;
       const int qi = m0 + r;
-      const int qc = min(qi, p.T - 1);
+      const int qc = min(qi, it.T - 1);
       const int off = it.off, kv_lo = it.kv_lo, kv_hi = it.kv_hi, n_keys = it.n_keys;
       float m_ref = -INFINITY, l = 0.f;
       for (int j = 0; j < it.n_tiles; ++j, ++J) {
@@ -493,7 +534,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
         // raw scores: masked entries become -inf (tiles on the diagonal, past the last key,
         // before the first visible key, or before the window)
         if ((n0 + kBK - 1 > off + m0) || (n0 + kBK > kv_hi) || n0 < kv_lo ||
-            (p.window > 0 && n0 < off + min(m0 + kBQ - 1, p.T - 1) - p.window + 1)) {
+            (p.window > 0 && n0 < off + min(m0 + kBQ - 1, it.T - 1) - p.window + 1)) {
           const int causal = off + qc - n0;                    // keys n0 + c with c <= causal are not ahead
           const int lim = min(causal, kv_hi - 1 - n0);         // ... nor padding after the run
           const int first = max(p.window > 0 ? causal - p.window + 1 : -kBK, kv_lo - n0);  // c >= first
@@ -592,10 +633,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
       tc_fence_after();
       const bool seen = l > 0.f;  // false: a padding query that sees no key (its output is 0)
       const float inv = seen ? 1.f / l : 0.f;
-      const size_t orow_i = (((size_t)it.b * p.T + qi) * p.H + me.h) * kD;
+      const size_t orow_i = PACKED ? (size_t)(it.b + qi) * p.o_row + (size_t)me.h * p.o_head
+                                   : (((size_t)it.b * p.T + qi) * p.H + me.h) * kD;
       uint16_t* orow = static_cast<uint16_t*>(p.o) + orow_i;
       const bool of16 = p.o_f16 != 0;
-      const bool store = me.valid && qi < p.T;
+      const bool store = me.valid && qi < it.T;
       auto pack16 = [](const float (&v)[16], bool f16, uint4& w0, uint4& w1) {
         w0 = make_uint4(pack2(v[0], v[1], f16), pack2(v[2], v[3], f16), pack2(v[4], v[5], f16),
                         pack2(v[6], v[7], f16));
@@ -713,8 +755,8 @@ cudaError_t launch_attn_prefill_tc(const void* q, const void* k, const void* v, 
   p.status = st;
   p.wait_ns = wait_ns;
   static std::atomic<unsigned long long> configured[2];  // per instantiation, one bit per device
-  cudaError_t ce = f16 ? set_smem_limit_once(reinterpret_cast<const void*>(attn_tc_kernel<true>), kSmem, configured[1])
-                       : set_smem_limit_once(reinterpret_cast<const void*>(attn_tc_kernel<false>), kSmem, configured[0]);
+  cudaError_t ce = f16 ? set_smem_limit_once(reinterpret_cast<const void*>(attn_tc_kernel<true, false>), kSmem, configured[1])
+                       : set_smem_limit_once(reinterpret_cast<const void*>(attn_tc_kernel<false, false>), kSmem, configured[0]);
   if (ce != cudaSuccess) return ce;
   // persistent: one CTA per SM (at most one per item) walks the items
   int dev = 0, sms = 0;
@@ -723,10 +765,132 @@ cudaError_t launch_attn_prefill_tc(const void* q, const void* k, const void* v, 
   if (ce != cudaSuccess) return ce;
   const int grid = std::min(p.n_items, sms);
   if (f16)
-    launch_pdl(attn_tc_kernel<true>, grid, kThreads, kSmem, s, p);
+    launch_pdl(attn_tc_kernel<true, false>, grid, kThreads, kSmem, s, p);
   else
-    launch_pdl(attn_tc_kernel<false>, grid, kThreads, kSmem, s, p);
+    launch_pdl(attn_tc_kernel<false, false>, grid, kThreads, kSmem, s, p);
   return cudaGetLastError();
+}
+
+// ------------------------------------------------------------------ packed sequences
+
+namespace {
+
+constexpr int kPlanThreads = 1024;
+constexpr int kPlanBins = 4096;
+constexpr int kStatusInvalidArg = 1;  // == BLK_ERR_INVALID_ARG
+
+// The work list of packed sequences, heaviest first: an entry per query tile (or pair of
+// tiles) of `step` queries, ordered by its place in its sequence, which its key count grows
+// with. One CTA counts the entries of each place, sums the counts from the far places
+// down, and deals the entries out; the order within a place does not matter (items are
+// independent, so no result depends on it). A cu that does not rise from 0 to at most
+// `rows` records INVALID_ARG and is read clamped.
+__global__ void __launch_bounds__(kPlanThreads) packed_plan_kernel(const int* __restrict__ cu, int B, int rows, int step,
+                                                                   int cap, PackedWork* __restrict__ work,
+                                                                   int* __restrict__ n_work, DevStatus* st) {
+  pdl_launch_dependents();
+  pdl_wait();
+  __shared__ int count[kPlanBins];
+  __shared__ int warp_sums[kPlanThreads / 32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int places = (rows + step - 1) / step;
+  const int per_bin = (places + kPlanBins - 1) / kPlanBins;
+  for (int i = tid; i < kPlanBins; i += kPlanThreads) count[i] = 0;
+  __syncthreads();
+  bool bad = false;
+  for (int pass = 0; pass < 2; ++pass) {
+    for (int b = warp; b < B; b += kPlanThreads / 32) {  // a warp per sequence
+      const int a = cu[b], e = cu[b + 1];
+      const int lo = min(max(a, 0), rows), hi = min(max(e, lo), rows);
+      bad |= lo != a || hi != e;
+      const int n = (hi - lo + step - 1) / step;
+      for (int t = lane; t < n; t += 32) {
+        const int at = atomicAdd(&count[t / per_bin], 1);
+        if (pass == 1 && at < cap) work[at] = {lo, hi - lo, t, 0};
+      }
+    }
+    __syncthreads();
+    if (pass == 0) {
+      // count[i] := the entries of all farther places (an exclusive sum from the far end)
+      constexpr int kPer = kPlanBins / kPlanThreads;
+      int v[kPer], sum = 0;
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        v[i] = count[kPlanBins - 1 - (tid * kPer + i)];
+        sum += v[i];
+      }
+      int run = sum;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(0xffffffffu, run, o);
+        if (lane >= o) run += u;
+      }
+      if (lane == 31) warp_sums[warp] = run;
+      __syncthreads();
+      int before = 0;
+      for (int w = 0; w < warp; ++w) before += warp_sums[w];
+      if (tid == kPlanThreads - 1) *n_work = min(before + run, cap);
+      int x = before + run - sum;
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        count[kPlanBins - 1 - (tid * kPer + i)] = x;
+        x += v[i];
+      }
+      __syncthreads();
+    }
+  }
+  if (bad && st) atomicCAS(&st->code, 0, kStatusInvalidArg);
+}
+
+int packed_work_cap(int rows, int B) { return rows / kBQ + B; }
+constexpr size_t kPackedHead = 256;  // bytes before the work list: its length
+
+}  // namespace
+
+size_t attn_packed_ws_bytes(int rows, int B) {
+  return kPackedHead + (size_t)packed_work_cap(rows, B) * sizeof(PackedWork);
+}
+
+cudaError_t launch_attn_packed(const HeadRows& q, const HeadRows& k, const HeadRows& v, const HeadRows& o, int rows,
+                               const int* cu, int B, int H, int Hkv, int d, int window, void* ws, int num_sms,
+                               DevStatus* st, unsigned long long wait_ns, cudaStream_t s, const char** why) {
+  if (d != kD) {
+    *why = "tcgen05 attention: head_dim must be 128";
+    return cudaErrorInvalidValue;
+  }
+  if (B <= 0 || rows <= 0) return cudaSuccess;
+  AttnParams p;
+  memset(static_cast<void*>(&p), 0, sizeof(p));
+  if (!make_tma_heads_bf16(&p.tq, q, rows, H, kD, kBQ) || !make_tma_heads_bf16(&p.tk, k, rows, Hkv, kD, kBK) ||
+      !make_tma_heads_bf16(&p.tv, v, rows, Hkv, kD, kBK)) {
+    *why = "cuTensorMapEncodeTiled failed for q/k/v";
+    return cudaErrorInvalidValue;
+  }
+  p.o = o.ptr;
+  p.o_row = o.row;
+  p.o_head = o.head;
+  p.B = B;
+  p.H = H;
+  p.Hkv = Hkv;
+  p.T = rows;
+  p.window = window > 0 ? window : 0;
+  p.head_pairs = (H / Hkv) % 2 == 0 ? 1 : 0;
+  p.sl2 = kLog2e / sqrtf((float)kD);
+  p.status = st;
+  p.wait_ns = wait_ns;
+  p.n_work = static_cast<int*>(ws);
+  PackedWork* work = reinterpret_cast<PackedWork*>(static_cast<uint8_t*>(ws) + kPackedHead);
+  p.work = work;
+  static std::atomic<unsigned long long> configured{0};
+  cudaError_t e = set_smem_limit_once(reinterpret_cast<const void*>(attn_tc_kernel<false, true>), kSmem, configured);
+  if (e != cudaSuccess) return e;
+  const int cap = packed_work_cap(rows, B);
+  e = launch_pdl(packed_plan_kernel, 1, kPlanThreads, 0, s, cu, B, rows, p.head_pairs ? kBQ : 2 * kBQ, cap, work,
+                 static_cast<int*>(ws), st);
+  if (e != cudaSuccess) return e;
+  const long long most = (long long)cap * (p.head_pairs ? H / 2 : H);
+  return launch_pdl(attn_tc_kernel<false, true>, dim3((unsigned)std::min<long long>(most, num_sms)), kThreads, kSmem, s,
+                    p);
 }
 
 }  // namespace blk

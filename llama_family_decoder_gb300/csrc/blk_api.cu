@@ -1435,6 +1435,216 @@ blk_status blk_attn_gqa(blk_handle* h, const void* q, const void* k, const void*
                     "decode attention", why);
 }
 
+// ------------------------------------------------------------------ packed batches, 4-bit cache
+
+namespace {
+// The handle's device is the current one (its tables and status word live there).
+blk_status check_device(const blk_handle* h) {
+  int dev = -1;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return cuda_fail(e, "device query");
+  if (dev != h->device) return fail(BLK_ERR_INVALID_ARG, "the current device is not the handle's");
+  return BLK_OK;
+}
+
+blk_status check_rows(const blk_handle* h, const blk_head_rows* x, int rows, int heads, bool written, const char* name) {
+  const std::string n(name);
+  if (!x || (!x->ptr && rows > 0)) return fail(BLK_ERR_INVALID_ARG, n + " is NULL");
+  const long long vec = 16 / (long long)esize(h->d), d = h->d.head_dim;
+  const long long rs = rows > 1 ? x->row_stride : 0, hs = heads > 1 ? x->head_stride : 0;
+  if (rs < 0 || hs < 0) return fail(BLK_ERR_INVALID_ARG, n + ": negative stride");
+  if (!aligned16(x->ptr) || rs % vec || hs % vec)
+    return fail(BLK_ERR_ALIGNMENT, n + ": pointer and strides must be multiples of 16 bytes");
+  if (rs >= 1ll << 37 || hs >= 1ll << 37) return fail(BLK_ERR_UNSUPPORTED, n + ": stride too large");
+  // written rows: each a stretch of d of its own
+  const __int128 row_span = (__int128)(heads - 1) * hs + d, head_span = (__int128)(rows > 1 ? rows - 1 : 0) * rs + d;
+  if (written && rows > 0 &&
+      !((heads == 1 || hs >= d) && (rows <= 1 || rs >= row_span)) &&
+      !((rows <= 1 || rs >= d) && (heads == 1 || hs >= head_span)))
+    return fail(BLK_ERR_INVALID_ARG, n + ": its rows overlap");
+  return BLK_OK;
+}
+
+HeadRows head_rows(const blk_head_rows* x) { return {x->ptr, x->row_stride, x->head_stride}; }
+
+blk_status check_kv4(const blk_handle* h, const blk_kv4_cache* c) {
+  if (h->d.dtype != BLK_BF16) return fail(BLK_ERR_UNSUPPORTED, "the 4-bit cache takes bf16 handles");
+  if (!c || !c->k || !c->k_scale || !c->v || !c->v_scale || !c->lens)
+    return fail(BLK_ERR_INVALID_ARG, "cache: NULL member");
+  if (c->capacity <= 0) return fail(BLK_ERR_INVALID_ARG, "cache: capacity must be positive");
+  if (!aligned16(c->k) || !aligned16(c->k_scale) || !aligned16(c->v) || !aligned16(c->v_scale))
+    return fail(BLK_ERR_ALIGNMENT, "cache: k, v and their scales must be 16-byte aligned");
+  return BLK_OK;
+}
+
+Kv4Cache kv4_cache(const blk_kv4_cache* c) {
+  return {static_cast<uint8_t*>(c->k), static_cast<uint8_t*>(c->k_scale), static_cast<uint8_t*>(c->v),
+          static_cast<uint8_t*>(c->v_scale), c->lens, c->capacity};
+}
+}  // namespace
+
+blk_status blk_qk_norm_rope(blk_handle* h, const blk_head_rows* q, const blk_head_rows* k, int rows, const int* pos,
+                            const blk_rope_axes* axes, const void* q_gain, const void* k_gain,
+                            const blk_head_rows* q_out, const blk_head_rows* k_out, void* stream) {
+  if (!h) return fail(BLK_ERR_INVALID_ARG, "NULL handle");
+  const blk_desc& d = h->d;
+  if (rows < 0) return fail(BLK_ERR_INVALID_ARG, "rows must not be negative");
+  if (d.head_dim % 8) return fail(BLK_ERR_UNSUPPORTED, "q/k norm and rotary: head_dim must be a multiple of 8");
+  BLK_TRY(check_rows(h, q, rows, d.n_heads, false, "q"));
+  BLK_TRY(check_rows(h, k, rows, d.n_kv_heads, false, "k"));
+  BLK_TRY(check_rows(h, q_out, rows, d.n_heads, true, "q_out"));
+  BLK_TRY(check_rows(h, k_out, rows, d.n_kv_heads, true, "k_out"));
+  const blk_head_rows* const in[2] = {q, k};
+  const blk_head_rows* const to[2] = {q_out, k_out};
+  for (int i = 0; i < 2; ++i)
+    if (rows > 0 && to[i]->ptr == in[i]->ptr &&
+        ((rows > 1 && to[i]->row_stride != in[i]->row_stride) ||
+         ((i ? d.n_kv_heads : d.n_heads) > 1 && to[i]->head_stride != in[i]->head_stride)))
+      return fail(BLK_ERR_INVALID_ARG, "in place: input and output strides must be the same");
+  if (rows > 0 && q_out->ptr == k_out->ptr) return fail(BLK_ERR_INVALID_ARG, "q_out and k_out are the same rows");
+  if (d.qk_norm) {
+    if (!q_gain || !k_gain) return fail(BLK_ERR_INVALID_ARG, "q/k norm gains NULL");
+    if (!aligned16(q_gain) || !aligned16(k_gain)) return fail(BLK_ERR_ALIGNMENT, "q/k norm gains not 16-byte aligned");
+  }
+  if (!d.no_rope && !pos && rows > 0) return fail(BLK_ERR_INVALID_ARG, "pos is NULL");
+  const int half = d.head_dim / 2;
+  PairAxes pa{};
+  int n_axes = 1;
+  if (axes) {
+    n_axes = axes->n_axes;
+    if (n_axes < 1 || n_axes > 4) return fail(BLK_ERR_INVALID_ARG, "rotary axes: 1 to 4");
+    if (axes->interleaved & ~1) return fail(BLK_ERR_INVALID_ARG, "rotary axes: interleaved is 0 or 1");
+    long long sum = 0;
+    for (int a = 0; a < n_axes; ++a) {
+      if (axes->sections[a] < 0) return fail(BLK_ERR_INVALID_ARG, "rotary axes: negative section");
+      sum += axes->sections[a];
+    }
+    if (sum != half) return fail(BLK_ERR_INVALID_ARG, "rotary axes: the sections must add up to head_dim / 2");
+    if (axes->interleaved)
+      for (int a = 1; a < n_axes; ++a)
+        if (axes->sections[a] > 0 && n_axes * (axes->sections[a] - 1) + a >= half)
+          return fail(BLK_ERR_INVALID_ARG, "rotary axes: an interleaved section does not fit");
+    for (int i = 0, a = 0, left = axes->sections[0]; i < half; ++i) {
+      int axis;
+      if (axes->interleaved) {
+        axis = i % n_axes;
+        if (i >= n_axes * axes->sections[axis]) axis = 0;
+      } else {
+        while (left == 0) left = axes->sections[++a];
+        --left;
+        axis = a;
+      }
+      pa.w[i >> 4] |= (uint32_t)axis << (2 * (i & 15));
+    }
+  }
+  BLK_TRY(check_device(h));
+  return check_cuda(launch_qk_norm_rope(head_rows(q), head_rows(k), head_rows(q_out), head_rows(k_out), rows,
+                                        d.n_heads, d.n_kv_heads, d.head_dim, pos, n_axes, pa,
+                                        d.qk_norm ? q_gain : nullptr, d.qk_norm ? k_gain : nullptr, d.eps,
+                                        d.no_rope ? nullptr : h->rope, d.max_seq, d.dtype == BLK_BF16, h->num_sms,
+                                        h->status, static_cast<cudaStream_t>(stream)),
+                    "q/k norm and rotary");
+}
+
+size_t blk_attn_packed_workspace_bytes(const blk_handle* h, int rows, int batch) {
+  if (!h || rows < 0 || batch < 0) return 0;
+  return attn_packed_ws_bytes(rows, batch);
+}
+
+blk_status blk_attn_packed(blk_handle* h, const blk_head_rows* q, const blk_head_rows* k, const blk_head_rows* v,
+                           int rows, const int* cu_seqlens, int batch, const blk_head_rows* o, void* workspace,
+                           size_t workspace_bytes, void* stream) {
+  if (!h) return fail(BLK_ERR_INVALID_ARG, "NULL handle");
+  const blk_desc& d = h->d;
+  if (d.dtype != BLK_BF16) return fail(BLK_ERR_UNSUPPORTED, "packed attention takes bf16 handles");
+  if (rows < 0 || batch < 0) return fail(BLK_ERR_INVALID_ARG, "rows and batch must not be negative");
+  if (batch > 0 && !cu_seqlens) return fail(BLK_ERR_INVALID_ARG, "cu_seqlens is NULL");
+  BLK_TRY(check_rows(h, q, rows, d.n_heads, false, "q"));
+  BLK_TRY(check_rows(h, k, rows, d.n_kv_heads, false, "k"));
+  BLK_TRY(check_rows(h, v, rows, d.n_kv_heads, false, "v"));
+  BLK_TRY(check_rows(h, o, rows, d.n_heads, true, "o"));
+  if (rows == 0 || batch == 0) return BLK_OK;
+  for (const blk_head_rows* x : {q, k, v}) {
+    const int heads = x == q ? d.n_heads : d.n_kv_heads;
+    if ((rows > 1 && x->row_stride == 0) || (heads > 1 && x->head_stride == 0))
+      return fail(BLK_ERR_UNSUPPORTED, "packed attention: broadcast (zero) strides");
+    if (x->ptr == o->ptr) return fail(BLK_ERR_INVALID_ARG, "o must not be an input");
+  }
+  if (!workspace || workspace_bytes < attn_packed_ws_bytes(rows, batch))
+    return fail(BLK_ERR_WORKSPACE, "packed attention: workspace missing or too small");
+  if (!aligned16(workspace)) return fail(BLK_ERR_ALIGNMENT, "workspace not 16-byte aligned");
+  BLK_TRY(check_device(h));
+  const char* why = nullptr;
+  return check_cuda(launch_attn_packed(head_rows(q), head_rows(k), head_rows(v), head_rows(o), rows, cu_seqlens, batch,
+                                       d.n_heads, d.n_kv_heads, d.head_dim, d.sliding_window, workspace, h->num_sms,
+                                       h->status, (unsigned long long)g_wait_ns.load(),
+                                       static_cast<cudaStream_t>(stream), &why),
+                    "packed attention", why);
+}
+
+blk_status blk_kv4_store(blk_handle* h, const blk_head_rows* k, const blk_head_rows* v, int rows,
+                         const int* cu_seqlens, const int* starts, int batch, const blk_kv4_cache* cache,
+                         int host_lens_max, void* stream) {
+  if (!h) return fail(BLK_ERR_INVALID_ARG, "NULL handle");
+  BLK_TRY(check_kv4(h, cache));
+  const blk_desc& d = h->d;
+  if (rows < 0 || batch < 0) return fail(BLK_ERR_INVALID_ARG, "rows and batch must not be negative");
+  if (!cu_seqlens && rows != batch) return fail(BLK_ERR_INVALID_ARG, "without cu_seqlens: a row per sequence");
+  BLK_TRY(check_rows(h, k, rows, d.n_kv_heads, false, "k"));
+  BLK_TRY(check_rows(h, v, rows, d.n_kv_heads, false, "v"));
+  if (host_lens_max > cache->capacity) return fail(BLK_ERR_CACHE_FULL, "the rows do not fit the cache");
+  if (batch == 0) return BLK_OK;
+  BLK_TRY(check_device(h));
+  return check_cuda(launch_kv4_store(head_rows(k), head_rows(v), rows, cu_seqlens, starts, batch, d.n_kv_heads,
+                                     kv4_cache(cache), h->status, static_cast<cudaStream_t>(stream)),
+                    "4-bit store");
+}
+
+blk_status blk_kv4_load(blk_handle* h, const blk_kv4_cache* cache, const int* cu_seqlens, const int* starts, int batch,
+                        int rows, const blk_head_rows* k, const blk_head_rows* v, void* stream) {
+  if (!h) return fail(BLK_ERR_INVALID_ARG, "NULL handle");
+  BLK_TRY(check_kv4(h, cache));
+  const blk_desc& d = h->d;
+  if (rows < 0 || batch < 0) return fail(BLK_ERR_INVALID_ARG, "rows and batch must not be negative");
+  if (!cu_seqlens && rows != batch) return fail(BLK_ERR_INVALID_ARG, "without cu_seqlens: a row per sequence");
+  BLK_TRY(check_rows(h, k, rows, d.n_kv_heads, true, "k"));
+  BLK_TRY(check_rows(h, v, rows, d.n_kv_heads, true, "v"));
+  if (rows == 0 || batch == 0) return BLK_OK;
+  if (k->ptr == v->ptr) return fail(BLK_ERR_INVALID_ARG, "k and v are the same rows");
+  BLK_TRY(check_device(h));
+  return check_cuda(launch_kv4_load(head_rows(k), head_rows(v), rows, cu_seqlens, starts, batch, d.n_kv_heads,
+                                    kv4_cache(cache), h->status, static_cast<cudaStream_t>(stream)),
+                    "4-bit load");
+}
+
+size_t blk_attn_decode_kv4_workspace_bytes(const blk_handle* h, int batch) {
+  if (!h || batch < 0) return 0;
+  return attn_kv4_ws_bytes(batch, h->d.n_heads, h->d.n_kv_heads, h->num_sms);
+}
+
+blk_status blk_attn_decode_kv4(blk_handle* h, const blk_head_rows* q, const blk_kv4_cache* cache, int batch,
+                               const blk_head_rows* o, void* workspace, size_t workspace_bytes, void* stream) {
+  if (!h) return fail(BLK_ERR_INVALID_ARG, "NULL handle");
+  BLK_TRY(check_kv4(h, cache));
+  const blk_desc& d = h->d;
+  if (batch < 0) return fail(BLK_ERR_INVALID_ARG, "batch must not be negative");
+  BLK_TRY(check_rows(h, q, batch, d.n_heads, false, "q"));
+  BLK_TRY(check_rows(h, o, batch, d.n_heads, true, "o"));
+  if (batch == 0) return BLK_OK;
+  if (q->ptr == o->ptr) return fail(BLK_ERR_INVALID_ARG, "o must not be an input");
+  const size_t need = attn_kv4_ws_bytes(batch, d.n_heads, d.n_kv_heads, h->num_sms);
+  if (need > 0 && (!workspace || workspace_bytes < need))
+    return fail(BLK_ERR_WORKSPACE, "4-bit decode attention: workspace missing or too small");
+  if (!aligned16(workspace)) return fail(BLK_ERR_ALIGNMENT, "workspace not 16-byte aligned");
+  BLK_TRY(check_device(h));
+  const char* why = nullptr;
+  return check_cuda(launch_attn_decode_kv4(head_rows(q), kv4_cache(cache), head_rows(o), batch, d.n_heads,
+                                           d.n_kv_heads, d.sliding_window, workspace, h->num_sms, h->status,
+                                           (unsigned long long)g_wait_ns.load(), static_cast<cudaStream_t>(stream),
+                                           &why),
+                    "4-bit decode attention", why);
+}
+
 blk_status blk_mlp(blk_handle* h, const void* resid, const void* h_normed, const blk_weights* w, int rows, void* out,
                    void* workspace, size_t workspace_bytes, void* stream) {
   if (!h || !resid || !h_normed || !w || !out) return fail(BLK_ERR_INVALID_ARG, "NULL argument");

@@ -25,6 +25,43 @@ cudaError_t launch_rmsnorm(const void* x, const void* g, int rows, int n, float 
 cudaError_t launch_norm_prep(const void* x, const void* g, int rows, int n, float eps, void* xg, float* row_scale,
                              float* zero_rows, cudaStream_t s);
 
+// ---------------------------------------------------------------- packed token rows
+// Element (row r, head j, channel c) at ptr + r * row + j * head + c (strides in elements).
+struct HeadRows {
+  void* ptr;
+  long long row, head;
+};
+
+// The position axis of each rotary pair, two bits a pair (up to 128 pairs, 4 axes).
+struct PairAxes {
+  uint32_t w[8];
+};
+
+// Per-head RMSNorm (gains null: none) and the rotary (table null: none) of rows of q and k.
+// pos [n_axes][rows]; a position outside [0, max_pos) is clamped and records INVALID_ARG.
+cudaError_t launch_qk_norm_rope(const HeadRows& q, const HeadRows& k, const HeadRows& qo, const HeadRows& ko, int rows,
+                                int H, int Hkv, int d, const int* pos, int n_axes, const PairAxes& axes,
+                                const void* q_gain, const void* k_gain, float eps, const float2* table, int max_pos,
+                                bool bf16, int num_sms, DevStatus* st, cudaStream_t s);
+
+// ---------------------------------------------------------------- 4-bit KV cache (head_dim 128)
+// k, v [B, Hkv, capacity, 64] code bytes, k_scale, v_scale [B, Hkv, capacity, 8] bf16.
+struct Kv4Cache {
+  uint8_t *k, *k_scale, *v, *v_scale;
+  int* lens;
+  int capacity;
+};
+
+// Packed bf16 rows cu[b] .. cu[b + 1] (cu null: row b) -> slots starts[b] .. of sequence b
+// (starts null: lens[b], an append); lens[b] becomes the slot behind the last one. Rows that
+// do not fit are left out, lens stops at the capacity and the status word records CACHE_FULL.
+cudaError_t launch_kv4_store(const HeadRows& k, const HeadRows& v, int rows, const int* cu, const int* starts, int B,
+                             int Hkv, const Kv4Cache& c, DevStatus* st, cudaStream_t s);
+// The reverse: slots starts[b] .. (null: 0 ..) as bf16 rows; slots outside the cache give
+// zeros and record INVALID_ARG.
+cudaError_t launch_kv4_load(const HeadRows& k, const HeadRows& v, int rows, const int* cu, const int* starts, int B,
+                            int Hkv, const Kv4Cache& c, DevStatus* st, cudaStream_t s);
+
 // ---------------------------------------------------------------- embedding
 // out[r, :] = table[tokens[r], :] (row_bytes per row, a multiple of 16); ids outside
 // [0, vocab) give zero rows and set the status word to INVALID_ARG.
@@ -169,6 +206,10 @@ struct TcGemmDesc {
 // columns x box_rows rows, 128-byte swizzle, zero fill out of bounds.
 bool make_tma_2d_16b(CUtensorMap* m, const void* ptr, int rows, int cols, int box_rows, bool f16);
 
+// 3-D TMA map over bf16 head rows: boxes of 64 channels x 1 head x box_rows rows, 128-byte
+// swizzle, zero fill out of bounds. Strides in multiples of 8 elements.
+bool make_tma_heads_bf16(CUtensorMap* m, const HeadRows& x, int rows, int heads, int d, int box_rows);
+
 cudaError_t launch_tc_gemm(const TcGemmDesc& d, int max_ctas, DevStatus* st, unsigned long long wait_ns,
                            cudaStream_t s, const char** why);
 
@@ -240,6 +281,14 @@ cudaError_t launch_attn_prefill_tc(const void* q, const void* k, const void* v, 
                                    cudaStream_t s, const char** why, const int* q_off = nullptr,
                                    int kv_stride = 0, const AttnOpts& opt = AttnOpts());
 
+// The same attention over packed sequences (bf16): rows cu[b] .. cu[b + 1] of q, k, v and o
+// are sequence b, whole prompts (key count = query count). Rows outside every sequence are
+// left as they were. ws: attn_packed_ws_bytes, holding the work list a first small kernel makes.
+size_t attn_packed_ws_bytes(int rows, int B);
+cudaError_t launch_attn_packed(const HeadRows& q, const HeadRows& k, const HeadRows& v, const HeadRows& o, int rows,
+                               const int* cu, int B, int H, int Hkv, int d, int window, void* ws, int num_sms,
+                               DevStatus* st, unsigned long long wait_ns, cudaStream_t s, const char** why);
+
 // Decode (Tq == 1), split over the keys: partial results in ws, combined into o.
 // The decode attention workspace starts with its unit counter (kAttnCounterBytes,
 // an int the attention kernel counts up from 0), then the split partials.
@@ -257,6 +306,13 @@ int attn_decode_splits(int B, int Hkv, int max_len, int num_sms);
 // The splits a workspace holds for keys up to max_len (512-key units, at most 64): the
 // bound attn_decode_splits is clamped to, and the allocation-free path's split rule.
 int attn_decode_split_cap(int max_len);
+
+// Decode over the 4-bit cache: q, o [B, H, 128] bf16 (a row per sequence), keys lens[b]
+// (at most the capacity; the last `window` of them with a window). ws: attn_kv4_ws_bytes.
+size_t attn_kv4_ws_bytes(int B, int H, int Hkv, int num_sms);
+cudaError_t launch_attn_decode_kv4(const HeadRows& q, const Kv4Cache& c, const HeadRows& o, int B, int H, int Hkv,
+                                   int window, void* ws, int num_sms, DevStatus* st, unsigned long long wait_ns,
+                                   cudaStream_t s, const char** why);
 
 // Decode attention with its split partials in a fixed file-scope device array
 // (no workspace, no allocation); kv_lens[b] keys per sequence, <= kv_stride.

@@ -1,0 +1,17 @@
+// Row format of the 4-bit KV cache (see kv4.cu).
+#pragma once
+
+#include <stdint.h>
+
+namespace blk {
+
+constexpr int kKv4Codes = 64;   // code bytes of a row
+constexpr int kKv4Scales = 16;  // 4 bf16 scales, then 4 bf16 offsets
+
+// The channel in the low nibble of code byte b; the high nibble holds the one 8 further.
+// Byte b = 16 t + 4 j + 2 u + e: block 2 j + e of 16 channels, element 2 t + u of its lower 8.
+__host__ __device__ constexpr int kv4_byte_channel(int b) {
+  return 16 * (2 * ((b >> 2) & 3) + (b & 1)) + 2 * (b >> 4) + ((b >> 1) & 1);
+}
+
+}  // namespace blk

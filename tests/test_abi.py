@@ -104,3 +104,18 @@ def test_debug_gemm_argument_checks_on_host(L):
     assert gemm(a, b, c, 256, 256, 64, 128, 1, 1, None) == 1   # ... and tiles of 192 columns or more
     assert b"pair" in L.blk_last_error_message()
     assert gemm(ctypes.c_void_p(0x1008), b, c, 256, 256, 64, 256, 1, 1, None) == 3  # misaligned
+
+
+def test_packed_stage_argument_checks_on_host(L):
+    # without a handle nothing is looked at, and sizes of nothing are 0
+    from llama_family_decoder_gb300 import binding as b
+    r = b.blk_head_rows(0x1000, 512, 128)
+    c = b.blk_kv4_cache(0x1000, 0x1000, 0x1000, 0x1000, 8, 0x1000)
+    assert L.blk_qk_norm_rope(None, r, r, 1, None, None, None, None, r, r, None) == 1
+    assert L.blk_attn_packed(None, r, r, r, 1, None, 1, r, None, 0, None) == 1
+    assert L.blk_kv4_store(None, r, r, 1, None, None, 1, c, -1, None) == 1
+    assert L.blk_kv4_load(None, c, None, None, 1, 1, r, r, None) == 1
+    assert L.blk_attn_decode_kv4(None, r, c, 1, r, None, 0, None) == 1
+    assert b"NULL handle" in L.blk_last_error_message()
+    assert L.blk_attn_packed_workspace_bytes(None, 8, 1) == 0
+    assert L.blk_attn_decode_kv4_workspace_bytes(None, 1) == 0
