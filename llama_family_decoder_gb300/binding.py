@@ -8,6 +8,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from ctypes import POINTER, c_char_p, c_float, c_int, c_longlong, c_size_t, c_void_p
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -54,20 +55,17 @@ class blk_taps(ctypes.Structure):
     _fields_ = [(n, c_void_p) for n in TAP_NAMES]
 
 
-class blk_head_rows(ctypes.Structure):
-    _fields_ = [("ptr", c_void_p), ("row_stride", c_longlong), ("head_stride", c_longlong)]
+# blk_head_rows (pointer, row and head stride in elements) and blk_kv4_cache as bytes: packing
+# them costs a tenth of building ctypes structures, which these short calls would feel
+head_rows = struct.Struct("@Pqq").pack
+kv4_cache_struct = struct.Struct("@PPPPiP").pack  # k, k_scale, v, v_scale, capacity, lens
 
 
 class blk_rope_axes(ctypes.Structure):
     _fields_ = [("n_axes", c_int), ("sections", c_int * 4), ("interleaved", c_int)]
 
 
-class blk_kv4_cache(ctypes.Structure):
-    _fields_ = [("k", c_void_p), ("k_scale", c_void_p), ("v", c_void_p), ("v_scale", c_void_p), ("capacity", c_int),
-                ("lens", c_void_p)]
-
-
-_ROWS = POINTER(blk_head_rows)
+_ROWS = _KV4 = c_char_p  # see head_rows and kv4_cache_struct
 
 # name -> (restype, argtypes); the exported symbols of include/blk.h
 SIGNATURES = {
@@ -90,12 +88,12 @@ SIGNATURES = {
     "blk_attn_packed_workspace_bytes": (c_size_t, [c_void_p, c_int, c_int]),
     "blk_attn_packed": (c_int, [c_void_p, _ROWS, _ROWS, _ROWS, c_int, c_void_p, c_int, _ROWS, c_void_p, c_size_t,
                                 c_void_p]),
-    "blk_kv4_store": (c_int, [c_void_p, _ROWS, _ROWS, c_int, c_void_p, c_void_p, c_int, POINTER(blk_kv4_cache), c_int,
+    "blk_kv4_store": (c_int, [c_void_p, _ROWS, _ROWS, c_int, c_void_p, c_void_p, c_int, _KV4, c_int,
                               c_void_p]),
-    "blk_kv4_load": (c_int, [c_void_p, POINTER(blk_kv4_cache), c_void_p, c_void_p, c_int, c_int, _ROWS, _ROWS,
+    "blk_kv4_load": (c_int, [c_void_p, _KV4, c_void_p, c_void_p, c_int, c_int, _ROWS, _ROWS,
                              c_void_p]),
     "blk_attn_decode_kv4_workspace_bytes": (c_size_t, [c_void_p, c_int]),
-    "blk_attn_decode_kv4": (c_int, [c_void_p, _ROWS, POINTER(blk_kv4_cache), c_int, _ROWS, c_void_p, c_size_t,
+    "blk_attn_decode_kv4": (c_int, [c_void_p, _ROWS, _KV4, c_int, _ROWS, c_void_p, c_size_t,
                                     c_void_p]),
     "blk_stage_workspace_bytes": (c_size_t, [c_void_p, c_int]),
     "blk_last_status": (c_int, [c_void_p]),
@@ -173,35 +171,19 @@ def _on_stream(device, stream):
     return torch.cuda.device(device) if stream is None else torch.cuda.stream(stream)
 
 
-def _check_tensor(t, name, dtype, device, shape=None):
-    if t.dtype != dtype or t.device != device:
-        raise ValueError(f"{name}: {dtype} on {device} is wanted, got {t.dtype} on {t.device}")
-    if shape is not None and (t.dim() != len(shape) or
-                              any(want is not None and have != want for have, want in zip(t.shape, shape))):
-        raise ValueError(f"{name}: shape {list(shape)} is wanted, got {list(t.shape)}")
+def _check_tensor(t, name, dtype, dev, shape):
+    """The packed calls' check of a tensor: type, device (its number) and shape."""
+    if t.dtype is not dtype or t.get_device() != dev or t.shape != shape:
+        raise ValueError(f"{name}: {dtype} {list(shape)} on cuda:{dev} is wanted, got {t.dtype} {list(t.shape)} "
+                         f"on {t.device}")
 
 
-def _head_rows(t, name, dtype, device, rows, heads, d):
-    """A [rows, heads, d] tensor, of any row and head strides, as blk_head_rows."""
-    _check_tensor(t, name, dtype, device, (rows, heads, d))
-    rs, hs, cs = t.stride()
-    if cs != 1:
-        raise ValueError(f"{name}: the channels must be contiguous")
-    return blk_head_rows(t.data_ptr(), rs, hs)
-
-
-def _int32(t, name, device, n):
-    if t is None:
-        return None
-    _check_tensor(t, name, _torch().int32, device, (n,))
+def _contiguous(t, name, dtype, dev, shape):
+    """The address of a contiguous tensor of this type and shape."""
+    _check_tensor(t, name, dtype, dev, shape)
     if not t.is_contiguous():
         raise ValueError(f"{name}: must be contiguous")
-    return c_void_p(t.data_ptr())
-
-
-def _torch():
-    import torch
-    return torch
+    return t.data_ptr()
 
 
 def xielu_effective(raw_alpha_p, raw_alpha_n, beta=0.5):
@@ -244,9 +226,14 @@ class DecoderBlock:
         _check(lib().blk_create(ctypes.byref(self.desc), ctypes.byref(h)))
         self.handle = h
         self._ws = None
-        torch = _torch()
-        self._device = torch.device("cuda", torch.cuda.current_device())  # where the handle's tables live
+        import torch
+        self._torch = torch
+        self._dev = torch.cuda.current_device()  # where the handle's tables live
+        self._device = torch.device("cuda", self._dev)
         self._dtype = torch.bfloat16 if self.desc.dtype == 1 else torch.float32
+        # the current stream's handle, without building a Stream object where torch has the short way
+        self._raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+            (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 
     @classmethod
     def from_workload(cls, wl, max_batch=None, max_seq=None):
@@ -384,7 +371,26 @@ class DecoderBlock:
     # graphs, share none.
 
     def _rows(self, t, name, rows, heads):
-        return _head_rows(t, name, self._dtype, self._device, rows, heads, self.desc.head_dim)
+        """A [rows, heads, d] tensor, of any row and head strides, as blk_head_rows."""
+        if t.dtype is not self._dtype or t.get_device() != self._dev or t.shape != (rows, heads, self.desc.head_dim):
+            _check_tensor(t, name, self._dtype, self._dev, (rows, heads, self.desc.head_dim))
+        rs, hs, cs = t.stride()
+        if cs != 1:
+            raise ValueError(f"{name}: the channels must be contiguous")
+        return head_rows(t.data_ptr(), rs, hs)
+
+    def _out(self, rows, heads):
+        return self._torch.empty(rows, heads, self.desc.head_dim, dtype=self._dtype, device=self._device)
+
+    def _scratch(self, nbytes):
+        return self._torch.empty(nbytes, dtype=self._torch.uint8, device=self._device)
+
+    def _int32(self, t, name, n):
+        return None if t is None else _contiguous(t, name, self._torch.int32, self._dev, (n,))
+
+    def _elsewhere(self, stream):
+        """Whether a call has to switch to its stream or to the handle's device first."""
+        return stream is not None or self._torch.cuda.current_device() != self._dev
 
     def qk_norm_rope(self, q, k, positions, q_gain=None, k_gain=None, sections=None, interleaved=False, q_out=None,
                      k_out=None, stream=None):
@@ -392,37 +398,32 @@ class DecoderBlock:
         and k [N, Hkv, d], of any row and head strides. positions: int32 [N], or [axes, N] with
         `sections`, the rotary pairs of each axis (one after the other, or interleaved). Returns
         (q_out, k_out), [N, heads, d]; pass q and k as outputs to work in place."""
-        torch = _torch()
+        if self._elsewhere(stream):
+            with _on_stream(self._device, stream):
+                return self.qk_norm_rope(q, k, positions, q_gain, k_gain, sections, interleaved, q_out, k_out)
         d, n = self.desc, q.shape[0]
-        axes, pos = None, None
+        H, Hkv = d.n_heads, d.n_kv_heads
+        axes = pos = gq = gk = None
         if not d.no_rope:
             n_axes = 1 if sections is None else len(sections)
             if not 1 <= n_axes <= 4:
                 raise ValueError("sections: 1 to 4 position axes")
-            p = positions.view(1, -1) if positions.dim() == 1 else positions
-            _check_tensor(p, "positions", torch.int32, self._device, (n_axes, n))
-            if not p.is_contiguous():
-                raise ValueError("positions: must be contiguous")
-            pos = c_void_p(p.data_ptr())
+            shape = (n,) if n_axes == 1 and positions.dim() == 1 else (n_axes, n)
+            pos = _contiguous(positions, "positions", self._torch.int32, self._dev, shape)
             if sections is not None:
                 axes = ctypes.byref(blk_rope_axes(n_axes, (c_int * 4)(*sections), int(bool(interleaved))))
         if d.qk_norm:
-            for name, g in (("q_gain", q_gain), ("k_gain", k_gain)):
-                if g is None:
-                    raise ValueError(f"{name}: the handle norms queries and keys")
-                _check_tensor(g, name, self._dtype, self._device, (d.head_dim,))
-                if not g.is_contiguous():
-                    raise ValueError(f"{name}: must be contiguous")
-        with _on_stream(self._device, stream):
-            if q_out is None:
-                q_out = torch.empty(n, d.n_heads, d.head_dim, dtype=self._dtype, device=self._device)
-            if k_out is None:
-                k_out = torch.empty(n, d.n_kv_heads, d.head_dim, dtype=self._dtype, device=self._device)
-            _check(lib().blk_qk_norm_rope(self.handle, self._rows(q, "q", n, d.n_heads),
-                                          self._rows(k, "k", n, d.n_kv_heads), n, pos, axes,
-                                          _ptr(q_gain) if d.qk_norm else None, _ptr(k_gain) if d.qk_norm else None,
-                                          self._rows(q_out, "q_out", n, d.n_heads),
-                                          self._rows(k_out, "k_out", n, d.n_kv_heads), _stream_ptr(stream)))
+            if q_gain is None or k_gain is None:
+                raise ValueError("q_gain, k_gain: the handle norms queries and keys")
+            gq = _contiguous(q_gain, "q_gain", self._dtype, self._dev, (d.head_dim,))
+            gk = _contiguous(k_gain, "k_gain", self._dtype, self._dev, (d.head_dim,))
+        qi, ki = self._rows(q, "q", n, H), self._rows(k, "k", n, Hkv)
+        if q_out is None:
+            q_out = self._out(n, H)
+        if k_out is None:
+            k_out = self._out(n, Hkv)
+        _check(lib().blk_qk_norm_rope(self.handle, qi, ki, n, pos, axes, gq, gk, self._rows(q_out, "q_out", n, H),
+                                      self._rows(k_out, "k_out", n, Hkv), self._raw_stream(self._dev)))
         return q_out, k_out
 
     def attn_packed(self, q, k, v, cu_seqlens, out=None, stream=None):
@@ -430,23 +431,24 @@ class DecoderBlock:
         head strides; cu_seqlens int32 [B + 1]: sequence b is rows cu_seqlens[b] .. cu_seqlens[b + 1] - 1.
         Returns out [N, H, d]; rows of no sequence are left as they were (undefined in an out
         made here)."""
-        torch = _torch()
+        if self._elsewhere(stream):
+            with _on_stream(self._device, stream):
+                return self.attn_packed(q, k, v, cu_seqlens, out)
         d, n, batch = self.desc, q.shape[0], cu_seqlens.numel() - 1
-        cu = _int32(cu_seqlens, "cu_seqlens", self._device, batch + 1)
-        with _on_stream(self._device, stream):
-            if out is None:
-                out = torch.empty(n, d.n_heads, d.head_dim, dtype=self._dtype, device=self._device)
-            ws = torch.empty(lib().blk_attn_packed_workspace_bytes(self.handle, n, batch), dtype=torch.uint8,
-                             device=self._device)
-            _check(lib().blk_attn_packed(self.handle, self._rows(q, "q", n, d.n_heads),
-                                         self._rows(k, "k", n, d.n_kv_heads), self._rows(v, "v", n, d.n_kv_heads), n,
-                                         cu, batch, self._rows(out, "out", n, d.n_heads), c_void_p(ws.data_ptr()),
-                                         ws.numel(), _stream_ptr(stream)))
+        H, Hkv = d.n_heads, d.n_kv_heads
+        cu = self._int32(cu_seqlens, "cu_seqlens", batch + 1)
+        rows = self._rows(q, "q", n, H), self._rows(k, "k", n, Hkv), self._rows(v, "v", n, Hkv)
+        if out is None:
+            out = self._out(n, H)
+        nbytes = lib().blk_attn_packed_workspace_bytes(self.handle, n, batch)
+        ws = self._scratch(nbytes)
+        _check(lib().blk_attn_packed(self.handle, *rows, n, cu, batch, self._rows(out, "out", n, H), ws.data_ptr(),
+                                     nbytes, self._raw_stream(self._dev)))
         return out
 
     def kv4_cache(self, batch, capacity):
         """An empty KV cache in 4 bits: dict(k, k_scale, v, v_scale, lens)."""
-        torch = _torch()
+        torch = self._torch
         n = (batch, self.desc.n_kv_heads, capacity)
         c = {"lens": torch.zeros(batch, dtype=torch.int32, device=self._device)}
         for x in ("k", "v"):
@@ -455,62 +457,62 @@ class DecoderBlock:
         return c
 
     def _kv4(self, cache):
-        torch = _torch()
+        torch, dev = self._torch, self._dev
         batch, _, cap, _ = cache["k"].shape
-        for name, t, last in (("k", torch.uint8, 64), ("k_scale", torch.bfloat16, 8), ("v", torch.uint8, 64),
-                              ("v_scale", torch.bfloat16, 8)):
-            _check_tensor(cache[name], name, t, self._device, (batch, self.desc.n_kv_heads, cap, last))
-            if not cache[name].is_contiguous():
-                raise ValueError(f"cache {name}: must be contiguous")
-        lens = _int32(cache["lens"], "lens", self._device, batch)
-        return blk_kv4_cache(cache["k"].data_ptr(), cache["k_scale"].data_ptr(), cache["v"].data_ptr(),
-                             cache["v_scale"].data_ptr(), cap, lens), batch
+        codes, scales = (batch, self.desc.n_kv_heads, cap, 64), (batch, self.desc.n_kv_heads, cap, 8)
+        return kv4_cache_struct(_contiguous(cache["k"], "cache k", torch.uint8, dev, codes),
+                                _contiguous(cache["k_scale"], "cache k_scale", torch.bfloat16, dev, scales),
+                                _contiguous(cache["v"], "cache v", torch.uint8, dev, codes),
+                                _contiguous(cache["v_scale"], "cache v_scale", torch.bfloat16, dev, scales), cap,
+                                _contiguous(cache["lens"], "cache lens", torch.int32, dev, (batch,))), batch
 
     def kv4_store(self, cache, k, v, cu_seqlens=None, starts=None, host_lens_max=-1, stream=None):
         """Quantises rows k, v [N, Hkv, 128] into the cache: sequence b's rows (cu_seqlens as in
         attn_packed; None: row b alone) to slots starts[b], ... (None: lens[b], an append), and sets
         lens[b] behind them. host_lens_max: the largest new length, to have the capacity checked
         here; else rows that do not fit are left out and last_status() says so."""
+        if self._elsewhere(stream):
+            with _on_stream(self._device, stream):
+                return self.kv4_store(cache, k, v, cu_seqlens, starts, host_lens_max)
         c, batch = self._kv4(cache)
         n, hkv = k.shape[0], self.desc.n_kv_heads
-        cu = _int32(cu_seqlens, "cu_seqlens", self._device, batch + 1)
-        st = _int32(starts, "starts", self._device, batch)
-        with _on_stream(self._device, stream):
-            _check(lib().blk_kv4_store(self.handle, self._rows(k, "k", n, hkv), self._rows(v, "v", n, hkv), n, cu, st,
-                                       batch, ctypes.byref(c), int(host_lens_max), _stream_ptr(stream)))
+        _check(lib().blk_kv4_store(self.handle, self._rows(k, "k", n, hkv), self._rows(v, "v", n, hkv), n,
+                                   self._int32(cu_seqlens, "cu_seqlens", batch + 1),
+                                   self._int32(starts, "starts", batch), batch, c, host_lens_max,
+                                   self._raw_stream(self._dev)))
 
     def kv4_load(self, cache, cu_seqlens=None, rows=None, starts=None, k_out=None, v_out=None, stream=None):
         """The values of the cache's slots starts[b], ... (None: 0, ...) as packed bf16 rows (k, v)
         [rows, Hkv, 128]: the rows that cu_seqlens gives each sequence (None: one each)."""
-        torch = _torch()
+        if self._elsewhere(stream):
+            with _on_stream(self._device, stream):
+                return self.kv4_load(cache, cu_seqlens, rows, starts, k_out, v_out)
         c, batch = self._kv4(cache)
-        n, d = batch if rows is None else rows, self.desc
-        cu = _int32(cu_seqlens, "cu_seqlens", self._device, batch + 1)
-        st = _int32(starts, "starts", self._device, batch)
-        with _on_stream(self._device, stream):
-            if k_out is None:
-                k_out = torch.empty(n, d.n_kv_heads, d.head_dim, dtype=self._dtype, device=self._device)
-            if v_out is None:
-                v_out = torch.empty(n, d.n_kv_heads, d.head_dim, dtype=self._dtype, device=self._device)
-            _check(lib().blk_kv4_load(self.handle, ctypes.byref(c), cu, st, batch, n,
-                                      self._rows(k_out, "k_out", n, d.n_kv_heads),
-                                      self._rows(v_out, "v_out", n, d.n_kv_heads), _stream_ptr(stream)))
+        n, hkv = batch if rows is None else rows, self.desc.n_kv_heads
+        cu, st = self._int32(cu_seqlens, "cu_seqlens", batch + 1), self._int32(starts, "starts", batch)
+        if k_out is None:
+            k_out = self._out(n, hkv)
+        if v_out is None:
+            v_out = self._out(n, hkv)
+        _check(lib().blk_kv4_load(self.handle, c, cu, st, batch, n, self._rows(k_out, "k_out", n, hkv),
+                                  self._rows(v_out, "v_out", n, hkv), self._raw_stream(self._dev)))
         return k_out, v_out
 
     def attn_decode_kv4(self, q, cache, out=None, stream=None):
         """One query per sequence, q [B, H, 128], over the lens[b] slots of the 4-bit cache (the last
         sliding_window of them). Returns out [B, H, 128]; a sequence without keys gets zeros."""
-        torch = _torch()
-        d = self.desc
+        if self._elsewhere(stream):
+            with _on_stream(self._device, stream):
+                return self.attn_decode_kv4(q, cache, out)
         c, batch = self._kv4(cache)
-        with _on_stream(self._device, stream):
-            if out is None:
-                out = torch.empty(batch, d.n_heads, d.head_dim, dtype=self._dtype, device=self._device)
-            ws = torch.empty(lib().blk_attn_decode_kv4_workspace_bytes(self.handle, batch), dtype=torch.uint8,
-                             device=self._device)
-            _check(lib().blk_attn_decode_kv4(self.handle, self._rows(q, "q", batch, d.n_heads), ctypes.byref(c), batch,
-                                             self._rows(out, "out", batch, d.n_heads), c_void_p(ws.data_ptr()),
-                                             ws.numel(), _stream_ptr(stream)))
+        H = self.desc.n_heads
+        qi = self._rows(q, "q", batch, H)
+        if out is None:
+            out = self._out(batch, H)
+        nbytes = lib().blk_attn_decode_kv4_workspace_bytes(self.handle, batch)
+        ws = self._scratch(nbytes)
+        _check(lib().blk_attn_decode_kv4(self.handle, qi, c, batch, self._rows(out, "out", batch, H), ws.data_ptr(),
+                                         nbytes, self._raw_stream(self._dev)))
         return out
 
     def mlp(self, resid, h_normed, weights, out, stream=None):

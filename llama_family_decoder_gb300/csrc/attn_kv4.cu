@@ -1,9 +1,31 @@
 // Decode attention over the 4-bit KV cache: one query per sequence,
 //   o[b, h, :] = softmax_s(q[b, h] . k^[b, j, s] / sqrt(128)) v^[b, j, s],  j = h / (H / Hkv),
-// with k^, v^ = offset + scale * code (see kv4.cu for the rows).
+// with k^, v^ = offset + scale * code, a scale and an offset per 32 channels (kv4.cu).
 //
-// A warp per (sequence, head) walks the keys; a lane holds two code bytes of each row
-// (four channels).
+// The codes never become scaled values: with the group's scale s_g and offset z_g of a key,
+//   q . k^  = sum_g s_g (sum_{c in g} q_c code_c) + sum_g z_g qsum_g,   qsum_g = sum_{c in g} q_c
+//   out_c   = sum_s (p_s s_g) code_c + sum_s p_s z_g
+// so the tensor core multiplies codes, which bf16 holds exactly, and scales touch one score
+// per key and group (or one probability) instead of 32 values. A code becomes the bf16 number
+// 128 + code by placing its nibble under the exponent of 128 (one shift, one and-or for two
+// codes); the 128s are taken off again in fp32: -128 qsum_g starts each group's score sum,
+// and -128 sum_s (p_s s_g) is gathered by one product with a constant operand per group.
+//
+// Keys sit on the rows of the products and the group's query heads on their columns
+// (m16n8k16: S^T = K q^T, out^T = V^T P^T), so that 8 heads cost what one does. The score
+// tile turns into the second product's operand with two 8x8 transposes.
+//
+// Work: the 64-key tiles of all (sequence, KV head) pairs form one line, cut into equal
+// stretches, one per CTA, whatever the lengths; a pair that lies within one stretch is
+// finished there, one that is cut leaves partial results (at most two per CTA) that a small
+// second kernel joins. No counter, no atomics: the same to the bit on every run.
+// Per CTA: a producer lane streams tiles (codes and scales of K and V, 10 KB) through a
+// ring of bulk copies; four compute warps own 16 keys of every tile, with a softmax state
+// each, merged when the pair's stretch ends.
+// HBM-bound: 160 bytes a key and KV head.
+#include <algorithm>
+#include <cstring>
+
 #include "common.cuh"
 #include "kernels.h"
 #include "kv4.cuh"
@@ -13,68 +35,668 @@ namespace blk {
 namespace {
 
 constexpr int kD = 128;
+constexpr int kTile = 64;                           // keys per tile
+constexpr int kCodeBytes = kTile * kKv4Codes;       // 4 KB
+constexpr int kScaleBytes = kTile * kKv4Scales;     // 1 KB
+constexpr int kStageBytes = 2 * (kCodeBytes + kScaleBytes);
+constexpr int kWarps = 4;                           // compute warps; one more issues the copies
+constexpr int kThreads = (kWarps + 1) * 32;
+constexpr int kMinTiles = 4;                        // tiles a CTA takes at least, while there are enough
+constexpr float kRescaleLog2 = 8.0f;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr unsigned long long kDrainNs = 2000000000ULL;
+
+// NT: tiles of 8 query heads (one for groups of up to 8 heads, two for up to 16)
+template <int NT>
+struct Cfg {
+  static constexpr int kStages = 5;
+  static constexpr int kCtas = NT == 1 ? 3 : 2;     // per SM
+  static constexpr int kMergeFloats = kWarps * 8 * NT * (kD + 2);
+  static constexpr int kSmem = 128 + kStages * kStageBytes + kMergeFloats * 4 + 256;
+};
 
 struct Kv4Params {
   HeadRows q, o;
   Kv4Cache c;
   int B, H, Hkv, window;
-  float sl;
+  int* prefix;    // [B + 1] tiles of one KV head before each sequence; then the stretches' count
+  float* part_ml; // [2 * grid][G][2]
+  float* part_o;  // [2 * grid][G][128]
+  float sl2;
+  DevStatus* status;
+  unsigned long long wait_ns;
 };
 
-__global__ void __launch_bounds__(128) attn_kv4_kernel(const __grid_constant__ Kv4Params p) {
+// The keys of sequence b: the last `window` of its lens[b] slots.
+__device__ __forceinline__ void keys_of(const Kv4Params& p, int b, int& first, int& n) {
+  const int len = max(0, min(p.c.lens[b], p.c.capacity));
+  first = p.window > 0 ? max(0, len - p.window) : 0;
+  n = len - first;
+}
+__device__ __forceinline__ int tiles(int keys) { return (keys + kTile - 1) / kTile; }
+
+// How many stretches `total` tiles are cut into, where stretch c begins, whose tile x is in.
+__device__ __forceinline__ int stretches(long long total, int grid) {
+  return (int)max(1ll, min((long long)grid, total / kMinTiles));
+}
+__device__ __forceinline__ long long stretch_begin(long long total, int n, int c) { return total * c / n; }
+__device__ __forceinline__ int stretch_of(long long total, int n, long long x) {
+  return (int)(((x + 1) * n + total - 1) / total) - 1;
+}
+
+// One (sequence, KV head) after the other along the line of tiles.
+struct Walk {
+  int b, kvh, t, n_tiles, first, keys;
+  __device__ __forceinline__ void enter(const Kv4Params& p) {  // from b on, the first sequence with keys
+    for (;; ++b) {
+      keys_of(p, b, first, keys);
+      n_tiles = tiles(keys);
+      if (n_tiles > 0) return;
+    }
+  }
+  __device__ __forceinline__ void next(const Kv4Params& p) {
+    t = 0;
+    if (++kvh == p.Hkv) {
+      kvh = 0;
+      ++b;
+      enter(p);
+    }
+  }
+};
+
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, [%3], %4;" ::"r"(dst),
+      "l"(src), "r"(bytes), "r"(bar), "l"(policy)
+      : "memory");
+}
+
+__device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// The 8x8 transpose of a 16-bit fragment (lane 4 r + c holds row r, columns 2c, 2c + 1).
+__device__ __forceinline__ uint32_t transpose8(uint32_t v) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
+}
+
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+  const __nv_bfloat162 r = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// nibbles at bits 0-3 and 16-19 -> the bf16 pair (128 + code, 128 + code)
+__device__ __forceinline__ uint32_t code_pair(uint32_t w) { return (w & 0x000F000Fu) | 0x43004300u; }
+__device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+
+__device__ __forceinline__ uint4 ld_shared_u4(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint2 ld_shared_u2(uint32_t a) {
+  uint2 v;
+  asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint32_t ld_shared_u1(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint32_t ld_shared_u16(uint32_t a) {
+  uint16_t v;
+  asm volatile("ld.shared.b16 %0, [%1];" : "=h"(v) : "r"(a));
+  return v;
+}
+
+// The key (of a warp's 16) on row r of the products: chosen so that the rows that one
+// phase of a 16-byte shared load touches (two neighbouring rows for K, four even or four
+// odd ones for V) are as even and odd keys, whose 64-byte rows sit on different banks.
+__device__ __forceinline__ int key_of_row(int r) { return r ^ ((r >> 1) & 1); }
+
+template <int NT>
+__global__ void __launch_bounds__(kThreads, Cfg<NT>::kCtas) attn_kv4_kernel(const __grid_constant__ Kv4Params p) {
+  constexpr int kStages = Cfg<NT>::kStages;
+  pdl_launch_dependents();
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~uintptr_t(127));
+  uint8_t* ring = smem;
+  float* merge = reinterpret_cast<float*>(ring + kStages * kStageBytes);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(merge + Cfg<NT>::kMergeFloats);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(bars + 2 * kStages + 1);
+  auto full = [&](int s) { return smem_u32(&bars[s]); };
+  auto empty = [&](int s) { return smem_u32(&bars[kStages + s]); };
+  const uint32_t csync = smem_u32(&bars[2 * kStages]);
+  __shared__ int warp_sums[kThreads / 32];
+  __shared__ int start[3];  // b, kvh, t of the CTA's first tile
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const unsigned long long budget = p.wait_ns;
+
+  if (tid == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(full(s), 1);
+      mbar_init(empty(s), kWarps);
+    }
+    mbar_init(csync, kWarps * 32);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  pdl_wait();
+  // the tiles before each thread's run of sequences
+  const int per = (p.B + kThreads - 1) / kThreads;
+  const int b_lo = min(p.B, tid * per), b_hi = min(p.B, b_lo + per);
+  int mine = 0;
+  for (int b = b_lo; b < b_hi; ++b) {
+    int first, n;
+    keys_of(p, b, first, n);
+    mine += tiles(n);
+  }
+  int run = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int u = __shfl_up_sync(0xffffffffu, run, o);
+    if (lane >= o) run += u;
+  }
+  if (lane == 31) warp_sums[warp] = run;
+  __syncthreads();
+  int before = run - mine, all = 0;
+#pragma unroll
+  for (int w = 0; w < kThreads / 32; ++w) {
+    if (w < warp) before += warp_sums[w];
+    all += warp_sums[w];
+  }
+  const long long total = (long long)all * p.Hkv;
+  const int n_str = total > 0 ? stretches(total, gridDim.x) : 0;
+  const int cta = blockIdx.x;
+  const long long t_lo = cta < n_str ? stretch_begin(total, n_str, cta) : 0;
+  const int n_mine = cta < n_str ? (int)(stretch_begin(total, n_str, cta + 1) - t_lo) : 0;
+  {
+    int acc = before;
+    for (int b = b_lo; b < b_hi; ++b) {
+      int first, n;
+      keys_of(p, b, first, n);
+      const int nt = tiles(n);
+      if (cta == 0) p.prefix[b] = acc;
+      const long long lo = (long long)acc * p.Hkv;
+      if (nt > 0 && t_lo >= lo && t_lo < lo + (long long)nt * p.Hkv) {
+        const int off = (int)(t_lo - lo);
+        start[0] = b;
+        start[1] = off / nt;
+        start[2] = off % nt;
+      }
+      acc += nt;
+    }
+    if (cta == 0 && tid == kThreads - 1) {
+      p.prefix[p.B] = all;
+      p.prefix[p.B + 1] = n_str;
+    }
+  }
+  __syncthreads();
+  if (n_mine == 0) return;
+
+  uint32_t issued = 0, parity = 0;  // stages in flight, for the drain after an abort
+  Walk w;
+  w.b = start[0];
+  w.enter(p);
+  w.kvh = start[1];
+  w.t = start[2];
+
+  if (warp == kWarps) {
+    if (lane == 0) {
+      // ---------------- producer
+      const uint64_t once = l2_policy_evict_first();  // the cache is read once per step
+      int stage = 0;
+      uint32_t ph = 0;
+      bool failed = false;
+      for (int i = 0; i < n_mine; ++i) {
+        if (!mbar_wait(empty(stage), ph ^ 1, budget, abort_flag)) {
+          failed = true;
+          break;
+        }
+        const int rows = min(kTile, w.keys - w.t * kTile);  // only filled slots are read
+        const size_t at = ((size_t)w.b * p.Hkv + w.kvh) * p.c.capacity + w.first + w.t * kTile;
+        const uint32_t dst = smem_u32(ring + stage * kStageBytes);
+        mbar_arrive_expect_tx(full(stage), rows * 2 * (kKv4Codes + kKv4Scales));
+        bulk_load(dst, p.c.k + at * kKv4Codes, rows * kKv4Codes, full(stage), once);
+        bulk_load(dst + 2 * kCodeBytes, p.c.k_scale + at * kKv4Scales, rows * kKv4Scales, full(stage), once);
+        bulk_load(dst + kCodeBytes, p.c.v + at * kKv4Codes, rows * kKv4Codes, full(stage), once);
+        bulk_load(dst + 2 * kCodeBytes + kScaleBytes, p.c.v_scale + at * kKv4Scales, rows * kKv4Scales, full(stage),
+                  once);
+        issued |= 1u << stage;
+        parity = (parity & ~(1u << stage)) | (ph << stage);
+        if (++stage == kStages) {
+          stage = 0;
+          ph ^= 1;
+        }
+        if (++w.t == w.n_tiles && i + 1 < n_mine) w.next(p);
+      }
+      if (failed) {
+        *abort_flag = 1;
+        report_timeout(p.status, 0x40);
+      }
+    }
+  } else {
+    // ---------------- compute warps
+    const int G = p.H / p.Hkv;
+    const int g = lane >> 2, tq = lane & 3;
+    int stage = 0, n_sync = 0, left = n_mine;
+    uint32_t ph = 0;
+    bool failed = false;
+    auto sync_all = [&]() {  // the compute threads meet (bounded)
+      mbar_arrive(csync);
+      const bool ok = __all_sync(0xffffffffu, mbar_wait(csync, n_sync & 1, budget, abort_flag));
+      ++n_sync;
+      return ok;
+    };
+    // this lane's rows of a tile: keys (within the tile) of product rows g, g + 8 (K) and of
+    // the operand pairs 2 tq, 2 tq + 1, 2 tq + 8, 2 tq + 9 (V)
+    const int k_lo = warp * 16 + key_of_row(g), k_hi = warp * 16 + 8 + key_of_row(g);
+    const int v_key[4] = {warp * 16 + key_of_row(2 * tq), warp * 16 + key_of_row(2 * tq + 1),
+                          warp * 16 + 8 + key_of_row(2 * tq), warp * 16 + 8 + key_of_row(2 * tq + 1)};
+    const uint32_t half = (g & 1) ? 0x7632u : 0x5410u;  // which bytes of a word are this row's
+    while (left > 0 && !failed) {
+      const int whole = w.n_tiles, t_first = w.t;
+      const int cnt = min(left, whole - t_first);
+      // Q as the column operand: head g (+ 8), channels 16 i + 2 tq, + 1 and the two 8 further
+      uint32_t qf[NT][8][2], qz[NT][2];
+      float q128[NT][4][2];  // -128 qsum of the heads on this lane's columns
+      {
+        const __nv_bfloat16* qg = static_cast<const __nv_bfloat16*>(p.q.ptr) + w.b * p.q.row;
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          const int h = 8 * n + g;
+          const __nv_bfloat16* qh = qg + (long long)(w.kvh * G + h) * p.q.head + 2 * tq;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            qf[n][i][0] = h < G ? *reinterpret_cast<const uint32_t*>(qh + 16 * i) : 0u;
+            qf[n][i][1] = h < G ? *reinterpret_cast<const uint32_t*>(qh + 16 * i + 8) : 0u;
+          }
+          float sum[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            sum[j] = 0.f;
+#pragma unroll
+            for (int i = 2 * j; i < 2 * j + 2; ++i)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) sum[j] += bf16_lo(qf[n][i][e]) + bf16_hi(qf[n][i][e]);
+            sum[j] += __shfl_xor_sync(0xffffffffu, sum[j], 1);
+            sum[j] += __shfl_xor_sync(0xffffffffu, sum[j], 2);
+            q128[n][j][0] = -128.f * __shfl_sync(0xffffffffu, sum[j], 8 * tq);
+            q128[n][j][1] = -128.f * __shfl_sync(0xffffffffu, sum[j], 8 * tq + 4);
+          }
+          // qsum in three bf16 parts (24 bits): product columns 2 tq, 2 tq + 1 carry groups
+          // 2 (tq & 1), + 1, the high part for tq < 2, the middle one above; + 8: the low part
+          const float x0 = (tq & 1) ? sum[2] : sum[0], x1 = (tq & 1) ? sum[3] : sum[1];
+          const float h0 = round_to<__nv_bfloat16>(x0), h1 = round_to<__nv_bfloat16>(x1);
+          const float m0 = round_to<__nv_bfloat16>(x0 - h0), m1 = round_to<__nv_bfloat16>(x1 - h1);
+          qz[n][0] = tq < 2 ? pack_bf16x2(h0, h1) : pack_bf16x2(m0, m1);
+          qz[n][1] = tq < 2 ? pack_bf16x2(x0 - h0 - m0, x1 - h1 - m1) : 0u;
+        }
+      }
+      float acc[NT][8][4], corr[NT][4][4], zacc[NT][4], m[NT][2], l[NT][2];
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) acc[n][i][0] = acc[n][i][1] = acc[n][i][2] = acc[n][i][3] = 0.f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) corr[n][j][0] = corr[n][j][1] = corr[n][j][2] = corr[n][j][3] = 0.f;
+        zacc[n][0] = zacc[n][1] = zacc[n][2] = zacc[n][3] = 0.f;
+        m[n][0] = m[n][1] = -INFINITY;
+        l[n][0] = l[n][1] = 0.f;
+      }
+      for (int t = t_first; t < t_first + cnt; ++t) {
+        if (!__all_sync(0xffffffffu, mbar_wait(full(stage), ph, budget, abort_flag))) {
+          failed = true;
+          break;
+        }
+        const uint32_t sK = smem_u32(ring + stage * kStageBytes), sV = sK + kCodeBytes;
+        const uint32_t sKs = sK + 2 * kCodeBytes, sVs = sKs + kScaleBytes;
+        const int valid = w.keys - t * kTile;  // keys of this tile (or more): rows past them are stale
+        // ---- scores S^T: rows keys, columns heads
+        float sc[NT][4];
+        {
+          const uint32_t z_lo = ld_shared_u1(sKs + k_lo * kKv4Scales + 8 + 4 * (tq & 1));
+          const uint32_t z_hi = ld_shared_u1(sKs + k_hi * kKv4Scales + 8 + 4 * (tq & 1));
+          const uint2 s_lo = ld_shared_u2(sKs + k_lo * kKv4Scales), s_hi = ld_shared_u2(sKs + k_hi * kKv4Scales);
+          const uint4 c_lo = ld_shared_u4(sK + k_lo * kKv4Codes + 16 * tq);
+          const uint4 c_hi = ld_shared_u4(sK + k_hi * kKv4Codes + 16 * tq);
+          const uint32_t za[4] = {z_lo, z_hi, z_lo, z_hi};
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            sc[n][0] = sc[n][1] = sc[n][2] = sc[n][3] = 0.f;
+            mma_bf16(sc[n], za, qz[n][0], qz[n][1]);
+          }
+          const uint32_t wl[4] = {c_lo.x, c_lo.y, c_lo.z, c_lo.w}, wh[4] = {c_hi.x, c_hi.y, c_hi.z, c_hi.w};
+          const float fl[4] = {bf16_lo(s_lo.x), bf16_hi(s_lo.x), bf16_lo(s_lo.y), bf16_hi(s_lo.y)};
+          const float fh[4] = {bf16_lo(s_hi.x), bf16_hi(s_hi.x), bf16_lo(s_hi.y), bf16_hi(s_hi.y)};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const uint32_t a0[4] = {code_pair(wl[j]), code_pair(wh[j]), code_pair(wl[j] >> 4), code_pair(wh[j] >> 4)};
+            const uint32_t a1[4] = {code_pair(wl[j] >> 8), code_pair(wh[j] >> 8), code_pair(wl[j] >> 12),
+                                    code_pair(wh[j] >> 12)};
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+              float d[4] = {q128[n][j][0], q128[n][j][1], q128[n][j][0], q128[n][j][1]};
+              mma_bf16(d, a0, qf[n][2 * j][0], qf[n][2 * j][1]);
+              mma_bf16(d, a1, qf[n][2 * j + 1][0], qf[n][2 * j + 1][1]);
+              sc[n][0] += fl[j] * d[0];
+              sc[n][1] += fl[j] * d[1];
+              sc[n][2] += fh[j] * d[2];
+              sc[n][3] += fh[j] * d[3];
+            }
+          }
+        }
+        // ---- probabilities against a running reference, moved only when a score passes it
+        // by 2^8 (exact: the softmax does not depend on the reference)
+        const bool tail = valid < warp * 16 + 16;
+        float e[NT][4];
+        bool need = false;
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) e[n][i] = fmaf(sc[n][i], p.sl2, -m[n][i & 1]);
+          if (tail) {
+            if (k_lo >= valid) e[n][0] = e[n][1] = -INFINITY;
+            if (k_hi >= valid) e[n][2] = e[n][3] = -INFINITY;
+          }
+          need |= fmaxf(fmaxf(e[n][0], e[n][1]), fmaxf(e[n][2], e[n][3])) > kRescaleLog2;
+        }
+        if (__any_sync(0xffffffffu, need)) {
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            float mx[2], al[2];
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+              float a = sc[n][r] * p.sl2, b = sc[n][r + 2] * p.sl2;
+              if (tail) {
+                if (k_lo >= valid) a = -INFINITY;
+                if (k_hi >= valid) b = -INFINITY;
+              }
+              mx[r] = fmaxf(a, b);
+#pragma unroll
+              for (int o = 4; o < 32; o <<= 1) mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], o));
+              mx[r] = fmaxf(mx[r], m[n][r]);
+              al[r] = m[n][r] == -INFINITY ? 0.f : ex2(m[n][r] - mx[r]);
+              m[n][r] = mx[r];
+              l[n][r] *= al[r];
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              e[n][i] = sc[n][i] * p.sl2 - m[n][i & 1];
+              zacc[n][i] *= al[i & 1];
+#pragma unroll
+              for (int j = 0; j < 4; ++j) corr[n][j][i] *= al[i & 1];
+#pragma unroll
+              for (int j = 0; j < 8; ++j) acc[n][j][i] *= al[i & 1];
+            }
+            if (tail) {
+              if (k_lo >= valid) e[n][0] = e[n][1] = -INFINITY;
+              if (k_hi >= valid) e[n][2] = e[n][3] = -INFINITY;
+            }
+          }
+        }
+        uint32_t pb[NT][2];  // P^T as the column operand: keys 2 tq, 2 tq + 1 (+ 8) of head g
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) e[n][i] = ex2(e[n][i]);
+          l[n][0] += e[n][0] + e[n][2];
+          l[n][1] += e[n][1] + e[n][3];
+          pb[n][0] = transpose8(pack_bf16x2(e[n][0], e[n][1]));
+          pb[n][1] = transpose8(pack_bf16x2(e[n][2], e[n][3]));
+        }
+        // ---- out^T += V^T P^T: rows channels, columns heads
+        uint2 vs[4];
+        uint32_t vz[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          vs[i] = ld_shared_u2(sVs + v_key[i] * kKv4Scales);
+          vz[i] = ld_shared_u16(sVs + v_key[i] * kKv4Scales + 8 + 2 * (g & 3));
+          if (g >= 4) vz[i] = 0;
+          if (tail && v_key[i] >= valid) {  // what a stale row holds may be a NaN
+            vs[i] = make_uint2(0, 0);
+            vz[i] = 0;
+          }
+        }
+        {
+          const uint32_t za[4] = {vz[0] | vz[1] << 16, 0u, vz[2] | vz[3] << 16, 0u};
+#pragma unroll
+          for (int n = 0; n < NT; ++n) mma_bf16(zacc[n], za, pb[n][0], pb[n][1]);
+        }
+        uint4 cv[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) cv[i] = ld_shared_u4(sV + v_key[i] * kKv4Codes + 16 * (g >> 1));
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint32_t word[4] = {j == 0 ? cv[0].x : j == 1 ? cv[0].y : j == 2 ? cv[0].z : cv[0].w,
+                                    j == 0 ? cv[1].x : j == 1 ? cv[1].y : j == 2 ? cv[1].z : cv[1].w,
+                                    j == 0 ? cv[2].x : j == 1 ? cv[2].y : j == 2 ? cv[2].z : cv[2].w,
+                                    j == 0 ? cv[3].x : j == 1 ? cv[3].y : j == 2 ? cv[3].z : cv[3].w};
+          const uint32_t x = __byte_perm(word[0], word[1], half), y = __byte_perm(word[2], word[3], half);
+          const uint32_t sel = (j & 1) ? 0x7632u : 0x5410u;
+          const uint32_t s0 = __byte_perm(j < 2 ? vs[0].x : vs[0].y, j < 2 ? vs[1].x : vs[1].y, sel);
+          const uint32_t s1 = __byte_perm(j < 2 ? vs[2].x : vs[2].y, j < 2 ? vs[3].x : vs[3].y, sel);
+          const uint32_t a0[4] = {code_pair(x), code_pair(x >> 4), code_pair(y), code_pair(y >> 4)};
+          const uint32_t a1[4] = {code_pair(x >> 8), code_pair(x >> 12), code_pair(y >> 8), code_pair(y >> 12)};
+          const uint32_t minus128[4] = {0xC300C300u, 0xC300C300u, 0xC300C300u, 0xC300C300u};
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            const uint32_t p0 = mul_bf16x2(pb[n][0], s0), p1 = mul_bf16x2(pb[n][1], s1);
+            mma_bf16(acc[n][2 * j], a0, p0, p1);
+            mma_bf16(acc[n][2 * j + 1], a1, p0, p1);
+            mma_bf16(corr[n][j], minus128, p0, p1);
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(empty(stage));
+        if (++stage == kStages) {
+          stage = 0;
+          ph ^= 1;
+        }
+      }
+      if (failed) break;
+      // ---- the pair's stretch ends: merge the warps' states
+      float* sm_m = merge;                              // [warp][8 NT]
+      float* sm_l = merge + kWarps * 8 * NT;
+      float* sm_o = merge + 2 * kWarps * 8 * NT;        // [warp][8 NT][128]
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+#pragma unroll
+          for (int o = 4; o < 32; o <<= 1) l[n][r] += __shfl_xor_sync(0xffffffffu, l[n][r], o);
+          const int h = 8 * n + 2 * tq + r;
+          if (g == 0) {
+            sm_m[warp * 8 * NT + h] = m[n][r];
+            sm_l[warp * 8 * NT + h] = l[n][r];
+          }
+          float* so = sm_o + (size_t)(warp * 8 * NT + h) * kD;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float add = corr[n][j][r] + __shfl_sync(0xffffffffu, zacc[n][r], 4 * j + tq);
+#pragma unroll
+            for (int i = 2 * j; i < 2 * j + 2; ++i) {
+              so[16 * i + g] = acc[n][i][r] + add;
+              so[16 * i + g + 8] = acc[n][i][r + 2] + add;
+            }
+          }
+        }
+      if (!sync_all()) {
+        failed = true;
+        break;
+      }
+      const bool complete = cnt == whole;
+      const int slot = 2 * cta + (left == n_mine ? 0 : 1);
+      for (int h = warp; h < G; h += kWarps) {  // a warp per head, four channels a lane
+        float mm = -INFINITY;
+#pragma unroll
+        for (int v = 0; v < kWarps; ++v) mm = fmaxf(mm, sm_m[v * 8 * NT + h]);
+        const float mu = mm == -INFINITY ? 0.f : mm;
+        float ll = 0.f;
+        float4 oo = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int v = 0; v < kWarps; ++v) {
+          const float f = ex2(sm_m[v * 8 * NT + h] - mu);
+          const float4 x = *reinterpret_cast<const float4*>(sm_o + (size_t)(v * 8 * NT + h) * kD + 4 * lane);
+          ll += sm_l[v * 8 * NT + h] * f;
+          oo = make_float4(oo.x + x.x * f, oo.y + x.y * f, oo.z + x.z * f, oo.w + x.w * f);
+        }
+        if (complete) {
+          const float inv = 1.f / ll;
+          __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.o.ptr) + w.b * p.o.row +
+                             (long long)(w.kvh * G + h) * p.o.head + 4 * lane;
+          *reinterpret_cast<uint2*>(o) = make_uint2(pack_bf16x2(oo.x * inv, oo.y * inv), pack_bf16x2(oo.z * inv, oo.w * inv));
+        } else {
+          const size_t at = (size_t)slot * G + h;
+          *reinterpret_cast<float4*>(p.part_o + at * kD + 4 * lane) = oo;
+          if (lane == 0) *reinterpret_cast<float2*>(p.part_ml + 2 * at) = make_float2(mm, ll);
+        }
+      }
+      if (!sync_all()) {  // the merge buffer is reused by the next pair
+        failed = true;
+        break;
+      }
+      left -= cnt;
+      if (left > 0) w.next(p);
+    }
+    if (failed) {
+      *abort_flag = 1;
+      if (lane == 0) report_timeout(p.status, 0x41);
+    }
+  }
+  __syncthreads();
+  // After an abort, tiles that nobody waited for may still be landing: they complete
+  // before the CTA exits (every thread reads the same flag).
+  if (*abort_flag && warp == kWarps && lane == 0) {
+    volatile int never = 0;
+    for (int s = 0; s < kStages; ++s)
+      if (issued & (1u << s)) mbar_wait(full(s), (parity >> s) & 1, kDrainNs, &never);
+  }
+}
+
+// Joins the partial results of the pairs that were cut, a warp per query head; a sequence
+// without keys gets its zeros here.
+constexpr int kJoinThreads = 256;
+constexpr int kJoinBatch = 8;  // partials whose loads are issued together
+
+__global__ void __launch_bounds__(kJoinThreads) attn_kv4_join_kernel(const __grid_constant__ Kv4Params p) {
   pdl_launch_dependents();
   pdl_wait();
-  const int lane = threadIdx.x & 31;
-  const long long u = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
-  if (u >= (long long)p.B * p.H) return;
-  const int b = (int)(u / p.H), h = (int)(u % p.H), j = h / (p.H / p.Hkv);
-  const int len = max(0, min(p.c.lens[b], p.c.capacity));
-  const int first = p.window > 0 ? max(0, len - p.window) : 0;
-  const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.q.ptr) + b * p.q.row + h * p.q.head;
-  int ch[4];
-  float qv[4], acc[4] = {0.f, 0.f, 0.f, 0.f}, m = -INFINITY, l = 0.f;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    ch[i] = kv4_byte_channel(2 * lane + (i >> 1)) + 8 * (i & 1);
-    qv[i] = __bfloat162float(q[ch[i]]);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int G = p.H / p.Hkv;
+  const long long total = (long long)p.prefix[p.B] * p.Hkv;
+  const int n_str = p.prefix[p.B + 1];
+  const long long pair = (long long)blockIdx.x * (kJoinThreads / 32) + warp;
+  if (pair >= (long long)p.B * p.H) return;
+  const int b = (int)(pair / p.H), h = (int)(pair % p.H), kvh = h / G, hg = h % G;
+  __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.o.ptr) + b * p.o.row + h * p.o.head + 4 * lane;
+  const int nt = p.prefix[b + 1] - p.prefix[b];
+  if (nt == 0) {
+    *reinterpret_cast<uint2*>(o) = make_uint2(0, 0);
+    return;
   }
-  const size_t row0 = ((size_t)b * p.Hkv + j) * p.c.capacity;
-  auto values = [&](const uint8_t* codes, const uint8_t* scales, size_t row, float (&x)[4]) {
-    const uint32_t w = *reinterpret_cast<const uint16_t*>(codes + row * kKv4Codes + 2 * lane);
-    const __nv_bfloat16* sc = reinterpret_cast<const __nv_bfloat16*>(scales + row * kKv4Scales);
+  const long long s0 = (long long)p.prefix[b] * p.Hkv + (long long)kvh * nt;
+  const int c0 = stretch_of(total, n_str, s0), c1 = stretch_of(total, n_str, s0 + nt - 1);
+  if (c0 == c1) return;
+  float m = -INFINITY, l = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int c = c0; c <= c1; c += kJoinBatch) {
+    float2 ml[kJoinBatch];
+    float4 ov[kJoinBatch];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int g = ch[i] >> 5;
-      x[i] = __bfloat162float(sc[4 + g]) + __bfloat162float(sc[g]) * (float)(w >> (4 * i) & 15u);
+    for (int i = 0; i < kJoinBatch; ++i) {
+      ml[i] = make_float2(-INFINITY, 0.f);
+      ov[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (c + i <= c1) {
+        // the pair is the stretch's first one unless it begins inside of it
+        const int slot = 2 * (c + i) + (s0 > stretch_begin(total, n_str, c + i) ? 1 : 0);
+        const size_t at = (size_t)slot * G + hg;
+        ml[i] = *reinterpret_cast<const float2*>(p.part_ml + 2 * at);
+        ov[i] = *reinterpret_cast<const float4*>(p.part_o + at * kD + 4 * lane);
+      }
     }
-  };
-  for (int s = first; s < len; ++s) {
-    float x[4], dot = 0.f;
-    values(p.c.k, p.c.k_scale, row0 + s, x);
+    float gm = m;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) dot += qv[i] * x[i];
-    dot = warp_sum(dot) * p.sl;
-    const float mn = fmaxf(m, dot), a = __expf(m - mn), e = __expf(dot - mn);
-    m = mn;
-    values(p.c.v, p.c.v_scale, row0 + s, x);
-    l = l * a + e;
+    for (int i = 0; i < kJoinBatch; ++i) gm = fmaxf(gm, ml[i].x);
+    const float mu = gm == -INFINITY ? 0.f : gm;
+    const float sc = ex2(m - mu);  // 0 for the first group
+    l *= sc;
+    acc = make_float4(acc.x * sc, acc.y * sc, acc.z * sc, acc.w * sc);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) acc[i] = acc[i] * a + e * x[i];
+    for (int i = 0; i < kJoinBatch; ++i) {
+      const float f = ex2(ml[i].x - mu);
+      l += ml[i].y * f;
+      acc = make_float4(acc.x + ov[i].x * f, acc.y + ov[i].y * f, acc.z + ov[i].z * f, acc.w + ov[i].w * f);
+    }
+    m = gm;
   }
-  __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.o.ptr) + b * p.o.row + h * p.o.head;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) o[ch[i]] = __float2bfloat16_rn(len > first ? acc[i] / l : 0.f);
+  const float inv = 1.f / l;
+  *reinterpret_cast<uint2*>(o) = make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+}
+
+int kv4_grid(int H, int Hkv, int num_sms) { return num_sms * (H / Hkv <= 8 ? Cfg<1>::kCtas : Cfg<2>::kCtas); }
+
+struct Kv4Ws {
+  size_t prefix, ml, o, bytes;
+};
+Kv4Ws kv4_ws(int B, int H, int Hkv, int num_sms) {
+  auto up = [](size_t x) { return (x + 255) & ~size_t(255); };
+  const size_t slots = (size_t)2 * kv4_grid(H, Hkv, num_sms) * (H / Hkv);
+  Kv4Ws w;
+  w.prefix = 0;
+  w.ml = up(((size_t)B + 2) * sizeof(int));
+  w.o = w.ml + up(slots * 2 * sizeof(float));
+  w.bytes = w.o + slots * kD * sizeof(float);
+  return w;
+}
+
+template <int NT>
+cudaError_t launch_nt(const Kv4Params& p, int grid, cudaStream_t s) {
+  static std::atomic<unsigned long long> configured{0};  // one bit per device
+  cudaError_t e = set_smem_limit_once(reinterpret_cast<const void*>(attn_kv4_kernel<NT>), Cfg<NT>::kSmem, configured);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(attn_kv4_kernel<NT>, grid, kThreads, Cfg<NT>::kSmem, s, p);
 }
 
 }  // namespace
 
-size_t attn_kv4_ws_bytes(int B, int H, int Hkv, int num_sms) { return 0; }
+size_t attn_kv4_ws_bytes(int B, int H, int Hkv, int num_sms) { return kv4_ws(B, H, Hkv, num_sms).bytes; }
 
 cudaError_t launch_attn_decode_kv4(const HeadRows& q, const Kv4Cache& c, const HeadRows& o, int B, int H, int Hkv,
                                    int window, void* ws, int num_sms, DevStatus* st, unsigned long long wait_ns,
                                    cudaStream_t s, const char** why) {
-  Kv4Params p{q, o, c, B, H, Hkv, window, 1.f / sqrtf((float)kD)};
-  return launch_pdl(attn_kv4_kernel, dim3((unsigned)(((long long)B * H + 3) / 4)), 128, 0, s, p);
+  if (H / Hkv > 16) {
+    *why = "4-bit decode attention: at most 16 query heads per KV head";
+    return cudaErrorInvalidValue;
+  }
+  if (B <= 0) return cudaSuccess;
+  const Kv4Ws w = kv4_ws(B, H, Hkv, num_sms);
+  uint8_t* base = static_cast<uint8_t*>(ws);
+  Kv4Params p{q, o, c, B, H, Hkv, window > 0 ? window : 0, reinterpret_cast<int*>(base + w.prefix),
+              reinterpret_cast<float*>(base + w.ml), reinterpret_cast<float*>(base + w.o), kLog2e / sqrtf((float)kD),
+              st, wait_ns};
+  // a CTA per kMinTiles tiles of the largest cache this could be
+  const long long most = (long long)B * Hkv * ((c.capacity + kTile - 1) / kTile);
+  const int grid = (int)std::max(1ll, std::min<long long>(kv4_grid(H, Hkv, num_sms), most / kMinTiles));
+  cudaError_t e = H / Hkv <= 8 ? launch_nt<1>(p, grid, s) : launch_nt<2>(p, grid, s);
+  if (e != cudaSuccess) return e;
+  const long long pairs = (long long)B * H;
+  return launch_pdl(attn_kv4_join_kernel, dim3((unsigned)((pairs + kJoinThreads / 32 - 1) / (kJoinThreads / 32))),
+                    kJoinThreads, 0, s, p);
 }
 
 }  // namespace blk

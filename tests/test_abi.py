@@ -109,8 +109,8 @@ def test_debug_gemm_argument_checks_on_host(L):
 def test_packed_stage_argument_checks_on_host(L):
     # without a handle nothing is looked at, and sizes of nothing are 0
     from llama_family_decoder_gb300 import binding as b
-    r = b.blk_head_rows(0x1000, 512, 128)
-    c = b.blk_kv4_cache(0x1000, 0x1000, 0x1000, 0x1000, 8, 0x1000)
+    r = b.head_rows(0x1000, 512, 128)
+    c = b.kv4_cache_struct(0x1000, 0x1000, 0x1000, 0x1000, 8, 0x1000)
     assert L.blk_qk_norm_rope(None, r, r, 1, None, None, None, None, r, r, None) == 1
     assert L.blk_attn_packed(None, r, r, r, 1, None, 1, r, None, 0, None) == 1
     assert L.blk_kv4_store(None, r, r, 1, None, None, 1, c, -1, None) == 1

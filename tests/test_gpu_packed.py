@@ -710,7 +710,7 @@ def test_refusals():
     # the C calls, with too small a workspace
     from llama_family_decoder_gb300 import binding as b
     L = b.lib()
-    r = lambda t: b.blk_head_rows(t.data_ptr(), t.stride(0), t.stride(1))  # noqa: E731
+    r = lambda t: b.head_rows(t.data_ptr(), t.stride(0), t.stride(1))  # noqa: E731
     o, ws = torch.empty_like(q), torch.empty(4096, dtype=torch.uint8, device=DEV)
     cu = ints([0, 8])
     need = L.blk_attn_packed_workspace_bytes(blk.handle, 8, 1)
