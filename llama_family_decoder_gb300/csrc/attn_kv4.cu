@@ -5,11 +5,13 @@
 // The codes never become scaled values: with the group's scale s_g and offset z_g of a key,
 //   q . k^  = sum_g s_g (sum_{c in g} q_c code_c) + sum_g z_g qsum_g,   qsum_g = sum_{c in g} q_c
 //   out_c   = sum_s (p_s s_g) code_c + sum_s p_s z_g
-// so the tensor core multiplies codes, which bf16 holds exactly, and scales touch one score
-// per key and group (or one probability) instead of 32 values. A code becomes the bf16 number
-// 128 + code by placing its nibble under the exponent of 128 (one shift, one and-or for two
-// codes); the 128s are taken off again in fp32: -128 qsum_g starts each group's score sum,
-// and -128 sum_s (p_s s_g) is gathered by one product with a constant operand per group.
+// so the tensor core multiplies codes, which 16-bit floats hold exactly, and scales touch one
+// score per key and group (or one probability) instead of 32 values. A code becomes a number
+// by placing its nibble under an exponent (an and-or for two codes) and taking the exponent's
+// value off again (one packed add, on the otherwise idle fp32 pipe; the integer pipe is what
+// bounds the unpacking). K in fp16, whose mantissa also takes a nibble 4 bits up without a
+// shift (1024 + 16 code); q is scaled by a power of two per head to use fp16's whole range.
+// V in bf16 (128 + code): p s_g keeps its exponent range whatever the values' size.
 //
 // Keys sit on the rows of the products and the group's query heads on their columns
 // (m16n8k16: S^T = K q^T, out^T = V^T P^T), so that 8 heads cost what one does. The score
@@ -23,6 +25,8 @@
 // ring of bulk copies; four compute warps own 16 keys of every tile, with a softmax state
 // each, merged when the pair's stretch ends.
 // HBM-bound: 160 bytes a key and KV head.
+#include <cuda_fp16.h>
+
 #include <algorithm>
 #include <cstring>
 
@@ -111,6 +115,16 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
       : "memory");
 }
 
+// D = A B + C on fp16 operands
+__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1,
+                                        const float (&c)[4]) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%10,%11,%12,%13};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
+}
+
 __device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile(
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
@@ -137,8 +151,25 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-// nibbles at bits 0-3 and 16-19 -> the bf16 pair (128 + code, 128 + code)
-__device__ __forceinline__ uint32_t code_pair(uint32_t w) { return (w & 0x000F000Fu) | 0x43004300u; }
+// The codes in the nibbles at bits 0-3 and 16-19 as a pair of bf16, from 128 + code.
+__device__ __forceinline__ uint32_t codes_bf16(uint32_t w) {
+  const uint32_t v = (w & 0x000F000Fu) | 0x43004300u, c = 0xC300C300u;
+  const __nv_bfloat162 r = __hadd2(*reinterpret_cast<const __nv_bfloat162*>(&v), *reinterpret_cast<const __nv_bfloat162*>(&c));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+// The same as fp16, from 1024 + code, and for the nibbles at bits 4-7 and 20-23, from
+// (1024 + 16 code) / 16 - 64 (exact).
+__device__ __forceinline__ uint32_t codes_f16_lo(uint32_t w) {
+  const uint32_t v = (w & 0x000F000Fu) | 0x64006400u, c = 0xE400E400u;
+  const __half2 r = __hadd2(*reinterpret_cast<const __half2*>(&v), *reinterpret_cast<const __half2*>(&c));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+__device__ __forceinline__ uint32_t codes_f16_hi(uint32_t w) {
+  const uint32_t v = (w & 0x00F000F0u) | 0x64006400u, a = 0x2C002C00u, c = 0xD400D400u;
+  const __half2 r = __hfma2(*reinterpret_cast<const __half2*>(&v), *reinterpret_cast<const __half2*>(&a),
+                            *reinterpret_cast<const __half2*>(&c));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 
@@ -167,6 +198,21 @@ __device__ __forceinline__ uint32_t ld_shared_u16(uint32_t a) {
 // phase of a 16-byte shared load touches (two neighbouring rows for K, four even or four
 // odd ones for V) are as even and odd keys, whose 64-byte rows sit on different banks.
 __device__ __forceinline__ int key_of_row(int r) { return r ^ ((r >> 1) & 1); }
+
+// mbar_wait for a wait that is expected to be long: the limit is looked at once in 32 tries,
+// so that the waiting lane takes few issue slots from the computing warps.
+__device__ __forceinline__ bool mbar_wait_long(uint32_t bar, uint32_t parity, unsigned long long budget_ns,
+                                               volatile int* abort) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const unsigned long long t0 = globaltimer_ns();
+  while (true) {
+#pragma unroll 1
+    for (int i = 0; i < 32; ++i)
+      if (mbar_try_wait(bar, parity)) return true;
+    if (*abort) return false;
+    if (globaltimer_ns() - t0 > budget_ns) return false;
+  }
+}
 
 template <int NT>
 __global__ void __launch_bounds__(kThreads, Cfg<NT>::kCtas) attn_kv4_kernel(const __grid_constant__ Kv4Params p) {
@@ -263,7 +309,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<NT>::kCtas) attn_kv4_kernel(cons
       uint32_t ph = 0;
       bool failed = false;
       for (int i = 0; i < n_mine; ++i) {
-        if (!mbar_wait(empty(stage), ph ^ 1, budget, abort_flag)) {
+        if (!mbar_wait_long(empty(stage), ph ^ 1, budget, abort_flag)) {
           failed = true;
           break;
         }
@@ -312,8 +358,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<NT>::kCtas) attn_kv4_kernel(cons
       const int whole = w.n_tiles, t_first = w.t;
       const int cnt = min(left, whole - t_first);
       // Q as the column operand: head g (+ 8), channels 16 i + 2 tq, + 1 and the two 8 further
+      // fp16, times a power of two per head that puts the head's largest channel at 2^14
       uint32_t qf[NT][8][2], qz[NT][2];
-      float q128[NT][4][2];  // -128 qsum of the heads on this lane's columns
+      float sl2[NT][2];  // log2(e) / sqrt(128) over that power, for the heads on this lane's columns
       {
         const __nv_bfloat16* qg = static_cast<const __nv_bfloat16*>(p.q.ptr) + w.b * p.q.row;
 #pragma unroll
@@ -325,6 +372,19 @@ __global__ void __launch_bounds__(kThreads, Cfg<NT>::kCtas) attn_kv4_kernel(cons
             qf[n][i][0] = h < G ? *reinterpret_cast<const uint32_t*>(qh + 16 * i) : 0u;
             qf[n][i][1] = h < G ? *reinterpret_cast<const uint32_t*>(qh + 16 * i + 8) : 0u;
           }
+          float top = 0.f;
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) top = fmaxf(top, fmaxf(fabsf(bf16_lo(qf[n][i][e])), fabsf(bf16_hi(qf[n][i][e]))));
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+          // 2^(14 - exponent of top), both powers kept normal numbers; an infinity stays one
+          const int ex = min(max((int)(__float_as_uint(top) >> 23), 15), 254);  // biased
+          const float up = __uint_as_float((uint32_t)(min(127 + 14 + 127 - ex, 254)) << 23);
+          const float down = __uint_as_float((uint32_t)(254 - min(127 + 14 + 127 - ex, 253)) << 23);
+          sl2[n][0] = p.sl2 * __shfl_sync(0xffffffffu, down, 8 * tq);
+          sl2[n][1] = p.sl2 * __shfl_sync(0xffffffffu, down, 8 * tq + 4);
           float sum[4];
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
@@ -332,11 +392,14 @@ __global__ void __launch_bounds__(kThreads, Cfg<NT>::kCtas) attn_kv4_kernel(cons
 #pragma unroll
             for (int i = 2 * j; i < 2 * j + 2; ++i)
 #pragma unroll
-              for (int e = 0; e < 2; ++e) sum[j] += bf16_lo(qf[n][i][e]) + bf16_hi(qf[n][i][e]);
+              for (int e = 0; e < 2; ++e) {
+                const float a = bf16_lo(qf[n][i][e]) * up, b = bf16_hi(qf[n][i][e]) * up;
+                const __half2 hh = __floats2half2_rn(a, b);
+                qf[n][i][e] = *reinterpret_cast<const uint32_t*>(&hh);
+                sum[j] += a + b;
+              }
             sum[j] += __shfl_xor_sync(0xffffffffu, sum[j], 1);
             sum[j] += __shfl_xor_sync(0xffffffffu, sum[j], 2);
-            q128[n][j][0] = -128.f * __shfl_sync(0xffffffffu, sum[j], 8 * tq);
-            q128[n][j][1] = -128.f * __shfl_sync(0xffffffffu, sum[j], 8 * tq + 4);
           }
           // qsum in three bf16 parts (24 bits): product columns 2 tq, 2 tq + 1 carry groups
           // 2 (tq & 1), + 1, the high part for tq < 2, the middle one above; + 8: the low part
@@ -347,13 +410,11 @@ __global__ void __launch_bounds__(kThreads, Cfg<NT>::kCtas) attn_kv4_kernel(cons
           qz[n][1] = tq < 2 ? pack_bf16x2(x0 - h0 - m0, x1 - h1 - m1) : 0u;
         }
       }
-      float acc[NT][8][4], corr[NT][4][4], zacc[NT][4], m[NT][2], l[NT][2];
+      float acc[NT][8][4], zacc[NT][4], m[NT][2], l[NT][2];
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) acc[n][i][0] = acc[n][i][1] = acc[n][i][2] = acc[n][i][3] = 0.f;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) corr[n][j][0] = corr[n][j][1] = corr[n][j][2] = corr[n][j][3] = 0.f;
         zacc[n][0] = zacc[n][1] = zacc[n][2] = zacc[n][3] = 0.f;
         m[n][0] = m[n][1] = -INFINITY;
         l[n][0] = l[n][1] = 0.f;
@@ -385,14 +446,15 @@ __global__ void __launch_bounds__(kThreads, Cfg<NT>::kCtas) attn_kv4_kernel(cons
           const float fh[4] = {bf16_lo(s_hi.x), bf16_hi(s_hi.x), bf16_lo(s_hi.y), bf16_hi(s_hi.y)};
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            const uint32_t a0[4] = {code_pair(wl[j]), code_pair(wh[j]), code_pair(wl[j] >> 4), code_pair(wh[j] >> 4)};
-            const uint32_t a1[4] = {code_pair(wl[j] >> 8), code_pair(wh[j] >> 8), code_pair(wl[j] >> 12),
-                                    code_pair(wh[j] >> 12)};
+            const uint32_t xl = wl[j] >> 8, xh = wh[j] >> 8;
+            const uint32_t a0[4] = {codes_f16_lo(wl[j]), codes_f16_lo(wh[j]), codes_f16_hi(wl[j]), codes_f16_hi(wh[j])};
+            const uint32_t a1[4] = {codes_f16_lo(xl), codes_f16_lo(xh), codes_f16_hi(xl), codes_f16_hi(xh)};
+            const float zero[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
-              float d[4] = {q128[n][j][0], q128[n][j][1], q128[n][j][0], q128[n][j][1]};
-              mma_bf16(d, a0, qf[n][2 * j][0], qf[n][2 * j][1]);
-              mma_bf16(d, a1, qf[n][2 * j + 1][0], qf[n][2 * j + 1][1]);
+              float d[4];
+              mma_f16(d, a0, qf[n][2 * j][0], qf[n][2 * j][1], zero);
+              mma_f16(d, a1, qf[n][2 * j + 1][0], qf[n][2 * j + 1][1], d);
               sc[n][0] += fl[j] * d[0];
               sc[n][1] += fl[j] * d[1];
               sc[n][2] += fh[j] * d[2];
@@ -408,7 +470,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<NT>::kCtas) attn_kv4_kernel(cons
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) e[n][i] = fmaf(sc[n][i], p.sl2, -m[n][i & 1]);
+          for (int i = 0; i < 4; ++i) e[n][i] = fmaf(sc[n][i], sl2[n][i & 1], -m[n][i & 1]);
           if (tail) {
             if (k_lo >= valid) e[n][0] = e[n][1] = -INFINITY;
             if (k_hi >= valid) e[n][2] = e[n][3] = -INFINITY;
@@ -421,7 +483,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<NT>::kCtas) attn_kv4_kernel(cons
             float mx[2], al[2];
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
-              float a = sc[n][r] * p.sl2, b = sc[n][r + 2] * p.sl2;
+              float a = sc[n][r] * sl2[n][r], b = sc[n][r + 2] * sl2[n][r];
               if (tail) {
                 if (k_lo >= valid) a = -INFINITY;
                 if (k_hi >= valid) b = -INFINITY;
@@ -436,10 +498,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<NT>::kCtas) attn_kv4_kernel(cons
             }
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              e[n][i] = sc[n][i] * p.sl2 - m[n][i & 1];
+              e[n][i] = fmaf(sc[n][i], sl2[n][i & 1], -m[n][i & 1]);
               zacc[n][i] *= al[i & 1];
-#pragma unroll
-              for (int j = 0; j < 4; ++j) corr[n][j][i] *= al[i & 1];
 #pragma unroll
               for (int j = 0; j < 8; ++j) acc[n][j][i] *= al[i & 1];
             }
@@ -490,15 +550,13 @@ __global__ void __launch_bounds__(kThreads, Cfg<NT>::kCtas) attn_kv4_kernel(cons
           const uint32_t sel = (j & 1) ? 0x7632u : 0x5410u;
           const uint32_t s0 = __byte_perm(j < 2 ? vs[0].x : vs[0].y, j < 2 ? vs[1].x : vs[1].y, sel);
           const uint32_t s1 = __byte_perm(j < 2 ? vs[2].x : vs[2].y, j < 2 ? vs[3].x : vs[3].y, sel);
-          const uint32_t a0[4] = {code_pair(x), code_pair(x >> 4), code_pair(y), code_pair(y >> 4)};
-          const uint32_t a1[4] = {code_pair(x >> 8), code_pair(x >> 12), code_pair(y >> 8), code_pair(y >> 12)};
-          const uint32_t minus128[4] = {0xC300C300u, 0xC300C300u, 0xC300C300u, 0xC300C300u};
+          const uint32_t a0[4] = {codes_bf16(x), codes_bf16(x >> 4), codes_bf16(y), codes_bf16(y >> 4)};
+          const uint32_t a1[4] = {codes_bf16(x >> 8), codes_bf16(x >> 12), codes_bf16(y >> 8), codes_bf16(y >> 12)};
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
             const uint32_t p0 = mul_bf16x2(pb[n][0], s0), p1 = mul_bf16x2(pb[n][1], s1);
             mma_bf16(acc[n][2 * j], a0, p0, p1);
             mma_bf16(acc[n][2 * j + 1], a1, p0, p1);
-            mma_bf16(corr[n][j], minus128, p0, p1);
           }
         }
         __syncwarp();
@@ -527,7 +585,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<NT>::kCtas) attn_kv4_kernel(cons
           float* so = sm_o + (size_t)(warp * 8 * NT + h) * kD;
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            const float add = corr[n][j][r] + __shfl_sync(0xffffffffu, zacc[n][r], 4 * j + tq);
+            const float add = __shfl_sync(0xffffffffu, zacc[n][r], 4 * j + tq);
 #pragma unroll
             for (int i = 2 * j; i < 2 * j + 2; ++i) {
               so[16 * i + g] = acc[n][i][r] + add;

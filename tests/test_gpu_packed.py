@@ -13,8 +13,9 @@ Bounds count roundings. bf16 rounds by at most u = 2^-8 of the value (half a ste
    most 128 * 2^-23 sum|q k| / sqrt(128); exp adds 2^-22. Both under 2e-4 of sum(p |v|) at
    these inputs.
  - decode over 4 bits: p and then p * scale are rounded to bf16 (2 u (1 + u) of the code part
-   p scale code), p alone for the offsets, the output once; the scores carry the codes with
-   an offset of 128, so that up to 2^-21 sum|q| (143 scale + |offset|) / sqrt(128) is lost.
+   p scale code), p alone for the offsets, the output once; a score is a sum of exact products
+   (of a group's sum of q in 24 bits with its offset) in fp32, off by at most
+   2^-21 sum|q| (15 scale + |offset|) / sqrt(128).
 """
 import numpy as np
 import pytest
@@ -496,7 +497,7 @@ def check_decode(out, q, k, v, lens, window=0):
             p = np.exp(s - s.max())
             p /= p.sum()
             qa = np.abs(qh).reshape(4, 32).sum(-1)
-            delta = 2.0 ** -21 * ((143 * ks[:, j] + np.abs(kz[:, j])) @ qa).max() / np.sqrt(D) + 1e-6
+            delta = 2.0 ** -21 * ((15 * ks[:, j] + np.abs(kz[:, j])) @ qa).max() / np.sqrt(D) + 1e-6
             ref = p @ V[:, j]
             bound = 2 * U * (1 + U) * (p @ code[:, j]) + U * (p @ off[:, j]) + U * np.abs(ref) + \
                 np.expm1(2 * delta) * (p @ (code[:, j] + off[:, j]))
