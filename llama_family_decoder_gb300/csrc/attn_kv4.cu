@@ -29,6 +29,7 @@
 
 #include <algorithm>
 #include <cstring>
+#include <type_traits>
 
 #include "common.cuh"
 #include "kernels.h"
@@ -118,25 +119,26 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
 // D = A B + C on fp16 operands
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1,
                                         const float (&c)[4]) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
       "{%10,%11,%12,%13};"
       : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
 }
 
-__device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
-      "{%0,%1,%2,%3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+// The same on bf16 operands
+__device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1,
+                                         const float (&c)[4]) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%10,%11,%12,%13};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
 }
 
 // The 8x8 transpose of a 16-bit fragment (lane 4 r + c holds row r, columns 2c, 2c + 1).
 __device__ __forceinline__ uint32_t transpose8(uint32_t v) {
   uint32_t r;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
   return r;
 }
 
@@ -151,21 +153,35 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+// (w & mask) | bits in one instruction: the mask in a register (see nibble_mask), as an
+// instruction has room for one constant only.
+template <uint32_t BITS>
+__device__ __forceinline__ uint32_t and_or(uint32_t w, uint32_t mask) {
+  uint32_t r;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(w), "r"(mask), "n"(BITS));
+  return r;
+}
+// A constant that the compiler keeps in a register instead of folding it.
+__device__ __forceinline__ uint32_t nibble_mask(uint32_t c) {
+  uint32_t r;
+  asm volatile("mov.b32 %0, %1;" : "=r"(r) : "r"(c));
+  return r;
+}
 // The codes in the nibbles at bits 0-3 and 16-19 as a pair of bf16, from 128 + code.
-__device__ __forceinline__ uint32_t codes_bf16(uint32_t w) {
-  const uint32_t v = (w & 0x000F000Fu) | 0x43004300u, c = 0xC300C300u;
+__device__ __forceinline__ uint32_t codes_bf16(uint32_t w, uint32_t mask) {
+  const uint32_t v = and_or<0x43004300u>(w, mask), c = 0xC300C300u;
   const __nv_bfloat162 r = __hadd2(*reinterpret_cast<const __nv_bfloat162*>(&v), *reinterpret_cast<const __nv_bfloat162*>(&c));
   return *reinterpret_cast<const uint32_t*>(&r);
 }
-// The same as fp16, from 1024 + code, and for the nibbles at bits 4-7 and 20-23, from
-// (1024 + 16 code) / 16 - 64 (exact).
-__device__ __forceinline__ uint32_t codes_f16_lo(uint32_t w) {
-  const uint32_t v = (w & 0x000F000Fu) | 0x64006400u, c = 0xE400E400u;
+// The same as fp16, from 1024 + code, and for the nibbles at bits 4-7 and 20-23 (mask << 4),
+// from (1024 + 16 code) / 16 - 64 (exact).
+__device__ __forceinline__ uint32_t codes_f16_lo(uint32_t w, uint32_t mask) {
+  const uint32_t v = and_or<0x64006400u>(w, mask), c = 0xE400E400u;
   const __half2 r = __hadd2(*reinterpret_cast<const __half2*>(&v), *reinterpret_cast<const __half2*>(&c));
   return *reinterpret_cast<const uint32_t*>(&r);
 }
-__device__ __forceinline__ uint32_t codes_f16_hi(uint32_t w) {
-  const uint32_t v = (w & 0x00F000F0u) | 0x64006400u, a = 0x2C002C00u, c = 0xD400D400u;
+__device__ __forceinline__ uint32_t codes_f16_hi(uint32_t w, uint32_t mask_hi) {
+  const uint32_t v = and_or<0x64006400u>(w, mask_hi), a = 0x2C002C00u, c = 0xD400D400u;
   const __half2 r = __hfma2(*reinterpret_cast<const __half2*>(&v), *reinterpret_cast<const __half2*>(&a),
                             *reinterpret_cast<const __half2*>(&c));
   return *reinterpret_cast<const uint32_t*>(&r);
@@ -173,25 +189,9 @@ __device__ __forceinline__ uint32_t codes_f16_hi(uint32_t w) {
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 
-__device__ __forceinline__ uint4 ld_shared_u4(uint32_t a) {
-  uint4 v;
-  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
-  return v;
-}
-__device__ __forceinline__ uint2 ld_shared_u2(uint32_t a) {
-  uint2 v;
-  asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
-  return v;
-}
-__device__ __forceinline__ uint32_t ld_shared_u1(uint32_t a) {
-  uint32_t v;
-  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(a));
-  return v;
-}
-__device__ __forceinline__ uint32_t ld_shared_u16(uint32_t a) {
-  uint16_t v;
-  asm volatile("ld.shared.b16 %0, [%1];" : "=h"(v) : "r"(a));
-  return v;
+template <typename T>
+__device__ __forceinline__ T ld(const uint8_t* p) {
+  return *reinterpret_cast<const T*>(p);
 }
 
 // The key (of a warp's 16) on row r of the products: chosen so that the rows that one
@@ -350,9 +350,20 @@ __global__ void __launch_bounds__(kThreads, Cfg<NT>::kCtas) attn_kv4_kernel(cons
     };
     // this lane's rows of a tile: keys (within the tile) of product rows g, g + 8 (K) and of
     // the operand pairs 2 tq, 2 tq + 1, 2 tq + 8, 2 tq + 9 (V)
-    const int k_lo = warp * 16 + key_of_row(g), k_hi = warp * 16 + 8 + key_of_row(g);
+    const int k_lo = warp * 16 + key_of_row(g), k_hi = k_lo + 8;
     const int v_key[4] = {warp * 16 + key_of_row(2 * tq), warp * 16 + key_of_row(2 * tq + 1),
                           warp * 16 + 8 + key_of_row(2 * tq), warp * 16 + 8 + key_of_row(2 * tq + 1)};
+    // their places in a stage: everything else is a constant further
+    const uint32_t at_k = k_lo * kKv4Codes + 16 * tq, at_ks = 2 * kCodeBytes + k_lo * kKv4Scales,
+                   at_kz = at_ks + 8 + 4 * (tq & 1);
+    uint32_t at_v[2], at_vs[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      at_v[i] = kCodeBytes + v_key[i] * kKv4Codes + 16 * (g >> 1);
+      at_vs[i] = 2 * kCodeBytes + kScaleBytes + v_key[i] * kKv4Scales;
+    }
+    const uint32_t z_off = 8 + 2 * (g & 3);
+    const uint32_t mask = nibble_mask(0x000F000Fu), mask_hi = nibble_mask(0x00F000F0u);
     const uint32_t half = (g & 1) ? 0x7632u : 0x5410u;  // which bytes of a word are this row's
     while (left > 0 && !failed) {
       const int whole = w.n_tiles, t_first = w.t;
@@ -419,37 +430,31 @@ __global__ void __launch_bounds__(kThreads, Cfg<NT>::kCtas) attn_kv4_kernel(cons
         m[n][0] = m[n][1] = -INFINITY;
         l[n][0] = l[n][1] = 0.f;
       }
-      for (int t = t_first; t < t_first + cnt; ++t) {
-        if (!__all_sync(0xffffffffu, mbar_wait(full(stage), ph, budget, abort_flag))) {
-          failed = true;
-          break;
-        }
-        const uint32_t sK = smem_u32(ring + stage * kStageBytes), sV = sK + kCodeBytes;
-        const uint32_t sKs = sK + 2 * kCodeBytes, sVs = sKs + kScaleBytes;
-        const int valid = w.keys - t * kTile;  // keys of this tile (or more): rows past them are stale
+      // one tile: TAIL when some of this warp's 16 keys lie behind the pair's last one (rows of
+      // the stage from `valid` on are stale)
+      auto tile = [&](auto tail_tag, int valid) {
+        constexpr bool tail = decltype(tail_tag)::value;
+        const uint8_t* st = ring + stage * kStageBytes;
         // ---- scores S^T: rows keys, columns heads
+        const float zero[4] = {0.f, 0.f, 0.f, 0.f};
         float sc[NT][4];
         {
-          const uint32_t z_lo = ld_shared_u1(sKs + k_lo * kKv4Scales + 8 + 4 * (tq & 1));
-          const uint32_t z_hi = ld_shared_u1(sKs + k_hi * kKv4Scales + 8 + 4 * (tq & 1));
-          const uint2 s_lo = ld_shared_u2(sKs + k_lo * kKv4Scales), s_hi = ld_shared_u2(sKs + k_hi * kKv4Scales);
-          const uint4 c_lo = ld_shared_u4(sK + k_lo * kKv4Codes + 16 * tq);
-          const uint4 c_hi = ld_shared_u4(sK + k_hi * kKv4Codes + 16 * tq);
+          const uint32_t z_lo = ld<uint32_t>(st + at_kz), z_hi = ld<uint32_t>(st + at_kz + 8 * kKv4Scales);
+          const uint2 s_lo = ld<uint2>(st + at_ks), s_hi = ld<uint2>(st + at_ks + 8 * kKv4Scales);
+          const uint4 c_lo = ld<uint4>(st + at_k), c_hi = ld<uint4>(st + at_k + 8 * kKv4Codes);
           const uint32_t za[4] = {z_lo, z_hi, z_lo, z_hi};
 #pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            sc[n][0] = sc[n][1] = sc[n][2] = sc[n][3] = 0.f;
-            mma_bf16(sc[n], za, qz[n][0], qz[n][1]);
-          }
+          for (int n = 0; n < NT; ++n) mma_bf16(sc[n], za, qz[n][0], qz[n][1], zero);
           const uint32_t wl[4] = {c_lo.x, c_lo.y, c_lo.z, c_lo.w}, wh[4] = {c_hi.x, c_hi.y, c_hi.z, c_hi.w};
           const float fl[4] = {bf16_lo(s_lo.x), bf16_hi(s_lo.x), bf16_lo(s_lo.y), bf16_hi(s_lo.y)};
           const float fh[4] = {bf16_lo(s_hi.x), bf16_hi(s_hi.x), bf16_lo(s_hi.y), bf16_hi(s_hi.y)};
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             const uint32_t xl = wl[j] >> 8, xh = wh[j] >> 8;
-            const uint32_t a0[4] = {codes_f16_lo(wl[j]), codes_f16_lo(wh[j]), codes_f16_hi(wl[j]), codes_f16_hi(wh[j])};
-            const uint32_t a1[4] = {codes_f16_lo(xl), codes_f16_lo(xh), codes_f16_hi(xl), codes_f16_hi(xh)};
-            const float zero[4] = {0.f, 0.f, 0.f, 0.f};
+            const uint32_t a0[4] = {codes_f16_lo(wl[j], mask), codes_f16_lo(wh[j], mask), codes_f16_hi(wl[j], mask_hi),
+                                    codes_f16_hi(wh[j], mask_hi)};
+            const uint32_t a1[4] = {codes_f16_lo(xl, mask), codes_f16_lo(xh, mask), codes_f16_hi(xl, mask_hi),
+                                    codes_f16_hi(xh, mask_hi)};
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
               float d[4];
@@ -464,14 +469,13 @@ __global__ void __launch_bounds__(kThreads, Cfg<NT>::kCtas) attn_kv4_kernel(cons
         }
         // ---- probabilities against a running reference, moved only when a score passes it
         // by 2^8 (exact: the softmax does not depend on the reference)
-        const bool tail = valid < warp * 16 + 16;
         float e[NT][4];
         bool need = false;
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) e[n][i] = fmaf(sc[n][i], sl2[n][i & 1], -m[n][i & 1]);
-          if (tail) {
+          if constexpr (tail) {
             if (k_lo >= valid) e[n][0] = e[n][1] = -INFINITY;
             if (k_hi >= valid) e[n][2] = e[n][3] = -INFINITY;
           }
@@ -484,7 +488,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<NT>::kCtas) attn_kv4_kernel(cons
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
               float a = sc[n][r] * sl2[n][r], b = sc[n][r + 2] * sl2[n][r];
-              if (tail) {
+              if constexpr (tail) {
                 if (k_lo >= valid) a = -INFINITY;
                 if (k_hi >= valid) b = -INFINITY;
               }
@@ -503,7 +507,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<NT>::kCtas) attn_kv4_kernel(cons
 #pragma unroll
               for (int j = 0; j < 8; ++j) acc[n][j][i] *= al[i & 1];
             }
-            if (tail) {
+            if constexpr (tail) {
               if (k_lo >= valid) e[n][0] = e[n][1] = -INFINITY;
               if (k_hi >= valid) e[n][2] = e[n][3] = -INFINITY;
             }
@@ -524,22 +528,24 @@ __global__ void __launch_bounds__(kThreads, Cfg<NT>::kCtas) attn_kv4_kernel(cons
         uint32_t vz[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          vs[i] = ld_shared_u2(sVs + v_key[i] * kKv4Scales);
-          vz[i] = ld_shared_u16(sVs + v_key[i] * kKv4Scales + 8 + 2 * (g & 3));
-          if (g >= 4) vz[i] = 0;
-          if (tail && v_key[i] >= valid) {  // what a stale row holds may be a NaN
-            vs[i] = make_uint2(0, 0);
-            vz[i] = 0;
+          const uint8_t* a = st + at_vs[i & 1] + (i >> 1) * 8 * kKv4Scales;
+          vs[i] = ld<uint2>(a);
+          vz[i] = ld<uint16_t>(a + z_off);  // rows 4-7 of the product repeat rows 0-3: nobody looks
+          if constexpr (tail) {
+            if (v_key[i] >= valid) {  // what a stale row holds may be a NaN
+              vs[i] = make_uint2(0, 0);
+              vz[i] = 0;
+            }
           }
         }
         {
-          const uint32_t za[4] = {vz[0] | vz[1] << 16, 0u, vz[2] | vz[3] << 16, 0u};
+          const uint32_t za[4] = {__byte_perm(vz[0], vz[1], 0x5410), 0u, __byte_perm(vz[2], vz[3], 0x5410), 0u};
 #pragma unroll
-          for (int n = 0; n < NT; ++n) mma_bf16(zacc[n], za, pb[n][0], pb[n][1]);
+          for (int n = 0; n < NT; ++n) mma_bf16(zacc[n], za, pb[n][0], pb[n][1], zacc[n]);
         }
         uint4 cv[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) cv[i] = ld_shared_u4(sV + v_key[i] * kKv4Codes + 16 * (g >> 1));
+        for (int i = 0; i < 4; ++i) cv[i] = ld<uint4>(st + at_v[i & 1] + (i >> 1) * 8 * kKv4Codes);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const uint32_t word[4] = {j == 0 ? cv[0].x : j == 1 ? cv[0].y : j == 2 ? cv[0].z : cv[0].w,
@@ -550,15 +556,28 @@ __global__ void __launch_bounds__(kThreads, Cfg<NT>::kCtas) attn_kv4_kernel(cons
           const uint32_t sel = (j & 1) ? 0x7632u : 0x5410u;
           const uint32_t s0 = __byte_perm(j < 2 ? vs[0].x : vs[0].y, j < 2 ? vs[1].x : vs[1].y, sel);
           const uint32_t s1 = __byte_perm(j < 2 ? vs[2].x : vs[2].y, j < 2 ? vs[3].x : vs[3].y, sel);
-          const uint32_t a0[4] = {codes_bf16(x), codes_bf16(x >> 4), codes_bf16(y), codes_bf16(y >> 4)};
-          const uint32_t a1[4] = {codes_bf16(x >> 8), codes_bf16(x >> 12), codes_bf16(y >> 8), codes_bf16(y >> 12)};
+          const uint32_t a0[4] = {codes_bf16(x, mask), codes_bf16(x >> 4, mask), codes_bf16(y, mask),
+                                  codes_bf16(y >> 4, mask)};
+          const uint32_t a1[4] = {codes_bf16(x >> 8, mask), codes_bf16(x >> 12, mask), codes_bf16(y >> 8, mask),
+                                  codes_bf16(y >> 12, mask)};
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
             const uint32_t p0 = mul_bf16x2(pb[n][0], s0), p1 = mul_bf16x2(pb[n][1], s1);
-            mma_bf16(acc[n][2 * j], a0, p0, p1);
-            mma_bf16(acc[n][2 * j + 1], a1, p0, p1);
+            mma_bf16(acc[n][2 * j], a0, p0, p1, acc[n][2 * j]);
+            mma_bf16(acc[n][2 * j + 1], a1, p0, p1, acc[n][2 * j + 1]);
           }
         }
+      };
+      for (int t = t_first; t < t_first + cnt; ++t) {
+        if (!__all_sync(0xffffffffu, mbar_wait(full(stage), ph, budget, abort_flag))) {
+          failed = true;
+          break;
+        }
+        const int valid = w.keys - t * kTile;
+        if (valid >= warp * 16 + 16)
+          tile(std::false_type(), valid);
+        else
+          tile(std::true_type(), valid);
         __syncwarp();
         if (lane == 0) mbar_arrive(empty(stage));
         if (++stage == kStages) {
