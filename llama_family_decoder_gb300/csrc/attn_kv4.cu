@@ -17,13 +17,14 @@
 // (m16n8k16: S^T = K q^T, out^T = V^T P^T), so that 8 heads cost what one does. The score
 // tile turns into the second product's operand with two 8x8 transposes.
 //
-// Work: the 64-key tiles of all (sequence, KV head) pairs form one line, cut into equal
+// Work: the 128-key tiles of all (sequence, KV head) pairs form one line, cut into equal
 // stretches, one per CTA, whatever the lengths; a pair that lies within one stretch is
 // finished there, one that is cut leaves partial results (at most two per CTA) that a small
 // second kernel joins. No counter, no atomics: the same to the bit on every run.
-// Per CTA: a producer lane streams tiles (codes and scales of K and V, 10 KB) through a
-// ring of bulk copies; four compute warps own 16 keys of every tile, with a softmax state
-// each, merged when the pair's stretch ends.
+// A CTA is four warps, each of which owns 32 keys of every tile: it copies their codes and
+// scales (5 KB) into its own two-stage ring with 16-byte asynchronous copies, a tile ahead,
+// and meets the other warps only when a pair's stretch ends, to merge their softmax states.
+// Rows behind the last key are filled with zeros, so nothing they hold is ever read.
 // HBM-bound: 160 bytes a key and KV head.
 #include <cuda_fp16.h>
 
@@ -40,25 +41,34 @@ namespace blk {
 namespace {
 
 constexpr int kD = 128;
-constexpr int kTile = 64;                           // keys per tile
-constexpr int kCodeBytes = kTile * kKv4Codes;       // 4 KB
-constexpr int kScaleBytes = kTile * kKv4Scales;     // 1 KB
+constexpr int kWarps = 4;
+constexpr int kThreads = kWarps * 32;
+constexpr int kSub = 2;                             // runs of 16 keys a warp owns of every tile
+constexpr int kKeys = 16 * kSub;                    // ... and their number
+constexpr int kTile = kWarps * kKeys;               // keys per tile
+constexpr int kCodeBytes = kKeys * kKv4Codes;       // of a warp's stage: K codes, V codes,
+constexpr int kScaleBytes = kKeys * kKv4Scales;     // K scales, V scales
 constexpr int kStageBytes = 2 * (kCodeBytes + kScaleBytes);
-constexpr int kWarps = 4;                           // compute warps; one more issues the copies
-constexpr int kThreads = (kWarps + 1) * 32;
-constexpr int kMinTiles = 4;                        // tiles a CTA takes at least, while there are enough
+constexpr int kStages = 2;                          // per warp
+constexpr int kMergeHeads = 4;                      // heads merged at a time
+constexpr int kMergeFloats = kWarps * kMergeHeads * (kD + 2);
+constexpr int kMinTiles = 2;                        // tiles a CTA takes at least, while there are enough
 constexpr float kRescaleLog2 = 8.0f;
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr unsigned long long kDrainNs = 2000000000ULL;
 
 // NT: tiles of 8 query heads (one for groups of up to 8 heads, two for up to 16)
 template <int NT>
 struct Cfg {
-  static constexpr int kStages = 5;
-  static constexpr int kCtas = NT == 1 ? 3 : 2;     // per SM
-  static constexpr int kMergeFloats = kWarps * 8 * NT * (kD + 2);
-  static constexpr int kSmem = 128 + kStages * kStageBytes + kMergeFloats * 4 + 256;
+  static constexpr int kCtas = NT == 1 ? 4 : 2;  // per SM (128 or 255 registers)
+  static constexpr int kSmem = kWarps * kStages * kStageBytes + kMergeFloats * 4 + kWarps * kStages * 16;
 };
+
+// What a warp's stage holds: how many of its keys are real, whose they are, and whether the
+// tile is the CTA's first or last one of its pair, or the pair lies within the CTA.
+struct __align__(16) TileInfo {
+  int valid, b, kvh, flags;
+};
+constexpr int kFirst = 1, kLast = 2, kWhole = 4;
 
 struct Kv4Params {
   HeadRows q, o;
@@ -68,8 +78,6 @@ struct Kv4Params {
   float* part_ml; // [2 * grid][G][2]
   float* part_o;  // [2 * grid][G][128]
   float sl2;
-  DevStatus* status;
-  unsigned long long wait_ns;
 };
 
 // The keys of sequence b: the last `window` of its lens[b] slots.
@@ -109,11 +117,17 @@ struct Walk {
   }
 };
 
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar, uint64_t policy) {
-  asm volatile(
-      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, [%3], %4;" ::"r"(dst),
-      "l"(src), "r"(bytes), "r"(bar), "l"(policy)
-      : "memory");
+// 16 bytes global -> shared, of which the first n (16 or 0) are read and the rest are zeros. The
+// cache is read once per step: evict it first.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, int n, uint64_t policy) {
+  asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2, %3;" ::"r"(dst), "l"(src),
+               "r"(n), "l"(policy)
+               : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 // D = A B + C on fp16 operands
@@ -199,48 +213,16 @@ __device__ __forceinline__ T ld(const uint8_t* p) {
 // odd ones for V) are as even and odd keys, whose 64-byte rows sit on different banks.
 __device__ __forceinline__ int key_of_row(int r) { return r ^ ((r >> 1) & 1); }
 
-// mbar_wait for a wait that is expected to be long: the limit is looked at once in 32 tries,
-// so that the waiting lane takes few issue slots from the computing warps.
-__device__ __forceinline__ bool mbar_wait_long(uint32_t bar, uint32_t parity, unsigned long long budget_ns,
-                                               volatile int* abort) {
-  if (mbar_try_wait(bar, parity)) return true;
-  const unsigned long long t0 = globaltimer_ns();
-  while (true) {
-#pragma unroll 1
-    for (int i = 0; i < 32; ++i)
-      if (mbar_try_wait(bar, parity)) return true;
-    if (*abort) return false;
-    if (globaltimer_ns() - t0 > budget_ns) return false;
-  }
-}
-
 template <int NT>
 __global__ void __launch_bounds__(kThreads, Cfg<NT>::kCtas) attn_kv4_kernel(const __grid_constant__ Kv4Params p) {
-  constexpr int kStages = Cfg<NT>::kStages;
   pdl_launch_dependents();
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~uintptr_t(127));
-  uint8_t* ring = smem;
-  float* merge = reinterpret_cast<float*>(ring + kStages * kStageBytes);
-  uint64_t* bars = reinterpret_cast<uint64_t*>(merge + Cfg<NT>::kMergeFloats);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(bars + 2 * kStages + 1);
-  auto full = [&](int s) { return smem_u32(&bars[s]); };
-  auto empty = [&](int s) { return smem_u32(&bars[kStages + s]); };
-  const uint32_t csync = smem_u32(&bars[2 * kStages]);
-  __shared__ int warp_sums[kThreads / 32];
+  extern __shared__ __align__(128) uint8_t smem[];
+  float* merge = reinterpret_cast<float*>(smem + kWarps * kStages * kStageBytes);
+  __shared__ int warp_sums[kWarps];
   __shared__ int start[3];  // b, kvh, t of the CTA's first tile
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const unsigned long long budget = p.wait_ns;
-
-  if (tid == 0) {
-    for (int s = 0; s < kStages; ++s) {
-      mbar_init(full(s), 1);
-      mbar_init(empty(s), kWarps);
-    }
-    mbar_init(csync, kWarps * 32);
-    *abort_flag = 0;
-    fence_mbar_init();
-  }
+  uint8_t* ring = smem + warp * kStages * kStageBytes;
+  TileInfo* info = reinterpret_cast<TileInfo*>(merge + kMergeFloats) + warp * kStages;
   pdl_wait();
   // the tiles before each thread's run of sequences
   const int per = (p.B + kThreads - 1) / kThreads;
@@ -261,7 +243,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<NT>::kCtas) attn_kv4_kernel(cons
   __syncthreads();
   int before = run - mine, all = 0;
 #pragma unroll
-  for (int w = 0; w < kThreads / 32; ++w) {
+  for (int w = 0; w < kWarps; ++w) {
     if (w < warp) before += warp_sums[w];
     all += warp_sums[w];
   }
@@ -294,90 +276,101 @@ __global__ void __launch_bounds__(kThreads, Cfg<NT>::kCtas) attn_kv4_kernel(cons
   __syncthreads();
   if (n_mine == 0) return;
 
-  uint32_t issued = 0, parity = 0;  // stages in flight, for the drain after an abort
+  // ---- this warp's copies, a tile ahead of its products
   Walk w;
   w.b = start[0];
   w.enter(p);
   w.kvh = start[1];
   w.t = start[2];
-
-  if (warp == kWarps) {
-    if (lane == 0) {
-      // ---------------- producer
-      const uint64_t once = l2_policy_evict_first();  // the cache is read once per step
-      int stage = 0;
-      uint32_t ph = 0;
-      bool failed = false;
-      for (int i = 0; i < n_mine; ++i) {
-        if (!mbar_wait_long(empty(stage), ph ^ 1, budget, abort_flag)) {
-          failed = true;
-          break;
-        }
-        const int rows = min(kTile, w.keys - w.t * kTile);  // only filled slots are read
-        const size_t at = ((size_t)w.b * p.Hkv + w.kvh) * p.c.capacity + w.first + w.t * kTile;
-        const uint32_t dst = smem_u32(ring + stage * kStageBytes);
-        mbar_arrive_expect_tx(full(stage), rows * 2 * (kKv4Codes + kKv4Scales));
-        bulk_load(dst, p.c.k + at * kKv4Codes, rows * kKv4Codes, full(stage), once);
-        bulk_load(dst + 2 * kCodeBytes, p.c.k_scale + at * kKv4Scales, rows * kKv4Scales, full(stage), once);
-        bulk_load(dst + kCodeBytes, p.c.v + at * kKv4Codes, rows * kKv4Codes, full(stage), once);
-        bulk_load(dst + 2 * kCodeBytes + kScaleBytes, p.c.v_scale + at * kKv4Scales, rows * kKv4Scales, full(stage),
-                  once);
-        issued |= 1u << stage;
-        parity = (parity & ~(1u << stage)) | (ph << stage);
-        if (++stage == kStages) {
-          stage = 0;
-          ph ^= 1;
-        }
-        if (++w.t == w.n_tiles && i + 1 < n_mine) w.next(p);
-      }
-      if (failed) {
-        *abort_flag = 1;
-        report_timeout(p.status, 0x40);
-      }
-    }
-  } else {
-    // ---------------- compute warps
-    const int G = p.H / p.Hkv;
-    const int g = lane >> 2, tq = lane & 3;
-    int stage = 0, n_sync = 0, left = n_mine;
-    uint32_t ph = 0;
-    bool failed = false;
-    auto sync_all = [&]() {  // the compute threads meet (bounded)
-      mbar_arrive(csync);
-      const bool ok = __all_sync(0xffffffffu, mbar_wait(csync, n_sync & 1, budget, abort_flag));
-      ++n_sync;
-      return ok;
-    };
-    // this lane's rows of a tile: keys (within the tile) of product rows g, g + 8 (K) and of
-    // the operand pairs 2 tq, 2 tq + 1, 2 tq + 8, 2 tq + 9 (V)
-    const int k_lo = warp * 16 + key_of_row(g), k_hi = k_lo + 8;
-    const int v_key[4] = {warp * 16 + key_of_row(2 * tq), warp * 16 + key_of_row(2 * tq + 1),
-                          warp * 16 + 8 + key_of_row(2 * tq), warp * 16 + 8 + key_of_row(2 * tq + 1)};
-    // their places in a stage: everything else is a constant further
-    const uint32_t at_k = k_lo * kKv4Codes + 16 * tq, at_ks = 2 * kCodeBytes + k_lo * kKv4Scales,
-                   at_kz = at_ks + 8 + 4 * (tq & 1);
-    uint32_t at_v[2], at_vs[2];
+  const uint64_t once = l2_policy_evict_first();
+  // byte offset of this lane's first copy of codes: a row of codes is four lanes' copies, and a
+  // row of scales, a quarter as long, one lane's
+  auto row_of = [&] {
+    const size_t at = ((size_t)w.b * p.Hkv + w.kvh) * p.c.capacity + w.first + w.t * kTile + warp * kKeys;
+    return at * kKv4Codes + 16 * lane;
+  };
+  size_t row = row_of();
+  int loaded = 0;
+  bool first = true;
+  auto load = [&](int stage) {
+    if (loaded < n_mine) {
+      const int valid = w.keys - w.t * kTile - warp * kKeys;
+      const uint32_t dst = smem_u32(ring + stage * kStageBytes) + 16 * lane;
+      const uint8_t *k = p.c.k + row, *v = p.c.v + row, *ks = p.c.k_scale + (row >> 2) + 12 * lane,
+                    *vs = p.c.v_scale + (row >> 2) + 12 * lane;
+      if (valid >= kKeys) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      at_v[i] = kCodeBytes + v_key[i] * kKv4Codes + 16 * (g >> 1);
-      at_vs[i] = 2 * kCodeBytes + kScaleBytes + v_key[i] * kKv4Scales;
+        for (int i = 0; i < kCodeBytes / 512; ++i) {
+          copy16(dst + 512 * i, k + 512 * i, 16, once);
+          copy16(dst + kCodeBytes + 512 * i, v + 512 * i, 16, once);
+        }
+        copy16(dst + 2 * kCodeBytes, ks, 16, once);  // kKeys == 32: a row's scales per lane
+        copy16(dst + 2 * kCodeBytes + kScaleBytes, vs, 16, once);
+      } else {  // rows that do not exist are not read
+#pragma unroll
+        for (int i = 0; i < kCodeBytes / 512; ++i) {
+          const bool on = (lane >> 2) + 8 * i < valid;
+          copy16(dst + 512 * i, on ? k + 512 * i : p.c.k, on ? 16 : 0, once);
+          copy16(dst + kCodeBytes + 512 * i, on ? v + 512 * i : p.c.v, on ? 16 : 0, once);
+        }
+        const bool on = lane < valid;
+        copy16(dst + 2 * kCodeBytes, on ? ks : p.c.k_scale, on ? 16 : 0, once);
+        copy16(dst + 2 * kCodeBytes + kScaleBytes, on ? vs : p.c.v_scale, on ? 16 : 0, once);
+      }
+      ++loaded;
+      const bool pair_ends = w.t + 1 == w.n_tiles, last = pair_ends || loaded == n_mine;
+      if (w.t == 0 || loaded == 1) first = w.t == 0;  // whether the CTA has the pair from its first tile on
+      if (lane == 0)
+        info[stage] = {valid, w.b, w.kvh,
+                       (w.t == 0 || loaded == 1 ? kFirst : 0) | (last ? kLast : 0) | (pair_ends && first ? kWhole : 0)};
+      ++w.t;
+      row += (size_t)kTile * kKv4Codes;
+      if (pair_ends && loaded < n_mine) {
+        w.next(p);
+        row = row_of();
+      }
     }
-    const uint32_t z_off = 8 + 2 * (g & 3);
-    const uint32_t mask = nibble_mask(0x000F000Fu), mask_hi = nibble_mask(0x00F000F0u);
-    const uint32_t half = (g & 1) ? 0x7632u : 0x5410u;  // which bytes of a word are this row's
-    while (left > 0 && !failed) {
-      const int whole = w.n_tiles, t_first = w.t;
-      const int cnt = min(left, whole - t_first);
+    copies_commit();
+  };
+#pragma unroll
+  for (int i = 0; i < kStages - 1; ++i) load(i);
+
+  const int G = p.H / p.Hkv;
+  const int g = lane >> 2, tq = lane & 3;
+  // this lane's rows of 16 keys: of product rows g, g + 8 (K) and of the operand pairs 2 tq,
+  // 2 tq + 1, 2 tq + 8, 2 tq + 9 (V), and their places in a stage
+  const int k_lo = key_of_row(g), k_hi = k_lo + 8;
+  const int v_key[2] = {key_of_row(2 * tq), key_of_row(2 * tq + 1)};  // and 8 further
+  const uint32_t at_k = k_lo * kKv4Codes + 16 * tq, at_ks = 2 * kCodeBytes + k_lo * kKv4Scales,
+                 at_kz = at_ks + 8 + 4 * (tq & 1);
+  uint32_t at_v[2], at_vs[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    at_v[i] = kCodeBytes + v_key[i] * kKv4Codes + 16 * (g >> 1);
+    at_vs[i] = 2 * kCodeBytes + kScaleBytes + v_key[i] * kKv4Scales;
+  }
+  const uint32_t z_off = 8 + 2 * (g & 3);
+  const uint32_t mask = nibble_mask(0x000F000Fu), mask_hi = nibble_mask(0x00F000F0u);
+  const uint32_t half = (g & 1) ? 0x7632u : 0x5410u;  // which bytes of a word are this row's
+
+  uint32_t qf[NT][8][2], qz[NT][2];
+  float sl2[NT][2];  // log2(e) / sqrt(128) over q's power of two, for the heads on this lane's columns
+  float acc[NT][8][4], zacc[NT][4], m[NT][2], l[NT][2];
+  int stage = 0, parts = 0;  // parts: stretches of pairs finished so far
+  for (int it = 0; it < n_mine; ++it) {
+    load(stage == 0 ? kStages - 1 : stage - 1);  // the stage that the last tile was in
+    copies_wait<kStages - 1>();
+    __syncwarp();
+    const TileInfo ti = info[stage];
+    if (ti.flags & kFirst) {
       // Q as the column operand: head g (+ 8), channels 16 i + 2 tq, + 1 and the two 8 further
       // fp16, times a power of two per head that puts the head's largest channel at 2^14
-      uint32_t qf[NT][8][2], qz[NT][2];
-      float sl2[NT][2];  // log2(e) / sqrt(128) over that power, for the heads on this lane's columns
       {
-        const __nv_bfloat16* qg = static_cast<const __nv_bfloat16*>(p.q.ptr) + w.b * p.q.row;
+        const __nv_bfloat16* qg = static_cast<const __nv_bfloat16*>(p.q.ptr) + ti.b * p.q.row;
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
           const int h = 8 * n + g;
-          const __nv_bfloat16* qh = qg + (long long)(w.kvh * G + h) * p.q.head + 2 * tq;
+          const __nv_bfloat16* qh = qg + (long long)(ti.kvh * G + h) * p.q.head + 2 * tq;
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             qf[n][i][0] = h < G ? *reinterpret_cast<const uint32_t*>(qh + 16 * i) : 0u;
@@ -421,7 +414,6 @@ __global__ void __launch_bounds__(kThreads, Cfg<NT>::kCtas) attn_kv4_kernel(cons
           qz[n][1] = tq < 2 ? pack_bf16x2(x0 - h0 - m0, x1 - h1 - m1) : 0u;
         }
       }
-      float acc[NT][8][4], zacc[NT][4], m[NT][2], l[NT][2];
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
 #pragma unroll
@@ -430,21 +422,22 @@ __global__ void __launch_bounds__(kThreads, Cfg<NT>::kCtas) attn_kv4_kernel(cons
         m[n][0] = m[n][1] = -INFINITY;
         l[n][0] = l[n][1] = 0.f;
       }
-      // one tile: TAIL when some of this warp's 16 keys lie behind the pair's last one (rows of
-      // the stage from `valid` on are stale)
-      auto tile = [&](auto tail_tag, int valid) {
-        constexpr bool tail = decltype(tail_tag)::value;
-        const uint8_t* st = ring + stage * kStageBytes;
+    }
+    const uint8_t* st = ring + stage * kStageBytes;
+    {
         // ---- scores S^T: rows keys, columns heads
         const float zero[4] = {0.f, 0.f, 0.f, 0.f};
-        float sc[NT][4];
-        {
-          const uint32_t z_lo = ld<uint32_t>(st + at_kz), z_hi = ld<uint32_t>(st + at_kz + 8 * kKv4Scales);
-          const uint2 s_lo = ld<uint2>(st + at_ks), s_hi = ld<uint2>(st + at_ks + 8 * kKv4Scales);
-          const uint4 c_lo = ld<uint4>(st + at_k), c_hi = ld<uint4>(st + at_k + 8 * kKv4Codes);
+        float sc[kSub][NT][4];
+#pragma unroll
+        for (int u = 0; u < kSub; ++u) {
+          const uint8_t *sk = st + at_k + u * 16 * kKv4Codes, *ss = st + at_ks + u * 16 * kKv4Scales,
+                        *sz = st + at_kz + u * 16 * kKv4Scales;
+          const uint32_t z_lo = ld<uint32_t>(sz), z_hi = ld<uint32_t>(sz + 8 * kKv4Scales);
+          const uint2 s_lo = ld<uint2>(ss), s_hi = ld<uint2>(ss + 8 * kKv4Scales);
+          const uint4 c_lo = ld<uint4>(sk), c_hi = ld<uint4>(sk + 8 * kKv4Codes);
           const uint32_t za[4] = {z_lo, z_hi, z_lo, z_hi};
 #pragma unroll
-          for (int n = 0; n < NT; ++n) mma_bf16(sc[n], za, qz[n][0], qz[n][1], zero);
+          for (int n = 0; n < NT; ++n) mma_bf16(sc[u][n], za, qz[n][0], qz[n][1], zero);
           const uint32_t wl[4] = {c_lo.x, c_lo.y, c_lo.z, c_lo.w}, wh[4] = {c_hi.x, c_hi.y, c_hi.z, c_hi.w};
           const float fl[4] = {bf16_lo(s_lo.x), bf16_hi(s_lo.x), bf16_lo(s_lo.y), bf16_hi(s_lo.y)};
           const float fh[4] = {bf16_lo(s_hi.x), bf16_hi(s_hi.x), bf16_lo(s_hi.y), bf16_hi(s_hi.y)};
@@ -460,208 +453,201 @@ __global__ void __launch_bounds__(kThreads, Cfg<NT>::kCtas) attn_kv4_kernel(cons
               float d[4];
               mma_f16(d, a0, qf[n][2 * j][0], qf[n][2 * j][1], zero);
               mma_f16(d, a1, qf[n][2 * j + 1][0], qf[n][2 * j + 1][1], d);
-              sc[n][0] += fl[j] * d[0];
-              sc[n][1] += fl[j] * d[1];
-              sc[n][2] += fh[j] * d[2];
-              sc[n][3] += fh[j] * d[3];
+              sc[u][n][0] += fl[j] * d[0];
+              sc[u][n][1] += fl[j] * d[1];
+              sc[u][n][2] += fh[j] * d[2];
+              sc[u][n][3] += fh[j] * d[3];
             }
           }
         }
         // ---- probabilities against a running reference, moved only when a score passes it
         // by 2^8 (exact: the softmax does not depend on the reference)
-        float e[NT][4];
-        bool need = false;
+        float e[kSub][NT][4];
+        auto hide = [&](float (&x)[NT][4], int u) {  // rows behind the last key
+          if (ti.valid < kKeys) {
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) e[n][i] = fmaf(sc[n][i], sl2[n][i & 1], -m[n][i & 1]);
-          if constexpr (tail) {
-            if (k_lo >= valid) e[n][0] = e[n][1] = -INFINITY;
-            if (k_hi >= valid) e[n][2] = e[n][3] = -INFINITY;
+            for (int n = 0; n < NT; ++n) {
+              if (k_lo + 16 * u >= ti.valid) x[n][0] = x[n][1] = -INFINITY;
+              if (k_hi + 16 * u >= ti.valid) x[n][2] = x[n][3] = -INFINITY;
+            }
           }
-          need |= fmaxf(fmaxf(e[n][0], e[n][1]), fmaxf(e[n][2], e[n][3])) > kRescaleLog2;
+        };
+        float most = -INFINITY;
+#pragma unroll
+        for (int u = 0; u < kSub; ++u) {
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) e[u][n][i] = fmaf(sc[u][n][i], sl2[n][i & 1], -m[n][i & 1]);
+          hide(e[u], u);
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+            most = fmaxf(most, fmaxf(fmaxf(e[u][n][0], e[u][n][1]), fmaxf(e[u][n][2], e[u][n][3])));
         }
-        if (__any_sync(0xffffffffu, need)) {
+        if (__any_sync(0xffffffffu, most > kRescaleLog2)) {
+#pragma unroll
+          for (int u = 0; u < kSub; ++u) {
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) e[u][n][i] = sc[u][n][i] * sl2[n][i & 1];
+            hide(e[u], u);
+          }
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
-            float mx[2], al[2];
+            float al[2];
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
-              float a = sc[n][r] * sl2[n][r], b = sc[n][r + 2] * sl2[n][r];
-              if constexpr (tail) {
-                if (k_lo >= valid) a = -INFINITY;
-                if (k_hi >= valid) b = -INFINITY;
-              }
-              mx[r] = fmaxf(a, b);
+              float mx = m[n][r];
 #pragma unroll
-              for (int o = 4; o < 32; o <<= 1) mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], o));
-              mx[r] = fmaxf(mx[r], m[n][r]);
-              al[r] = m[n][r] == -INFINITY ? 0.f : ex2(m[n][r] - mx[r]);
-              m[n][r] = mx[r];
+              for (int u = 0; u < kSub; ++u) mx = fmaxf(mx, fmaxf(e[u][n][r], e[u][n][r + 2]));
+#pragma unroll
+              for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+              al[r] = m[n][r] == -INFINITY ? 0.f : ex2(m[n][r] - mx);
+              m[n][r] = mx;
               l[n][r] *= al[r];
             }
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              e[n][i] = fmaf(sc[n][i], sl2[n][i & 1], -m[n][i & 1]);
               zacc[n][i] *= al[i & 1];
 #pragma unroll
               for (int j = 0; j < 8; ++j) acc[n][j][i] *= al[i & 1];
             }
-            if constexpr (tail) {
-              if (k_lo >= valid) e[n][0] = e[n][1] = -INFINITY;
-              if (k_hi >= valid) e[n][2] = e[n][3] = -INFINITY;
-            }
+          }
+#pragma unroll
+          for (int u = 0; u < kSub; ++u) {
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) e[u][n][i] = fmaf(sc[u][n][i], sl2[n][i & 1], -m[n][i & 1]);
+            hide(e[u], u);
           }
         }
-        uint32_t pb[NT][2];  // P^T as the column operand: keys 2 tq, 2 tq + 1 (+ 8) of head g
+        uint32_t pb[kSub][NT][2];  // P^T as the column operand: keys 2 tq, 2 tq + 1 (+ 8) of head g
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) e[n][i] = ex2(e[n][i]);
-          l[n][0] += e[n][0] + e[n][2];
-          l[n][1] += e[n][1] + e[n][3];
-          pb[n][0] = transpose8(pack_bf16x2(e[n][0], e[n][1]));
-          pb[n][1] = transpose8(pack_bf16x2(e[n][2], e[n][3]));
-        }
-        // ---- out^T += V^T P^T: rows channels, columns heads
-        uint2 vs[4];
-        uint32_t vz[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint8_t* a = st + at_vs[i & 1] + (i >> 1) * 8 * kKv4Scales;
-          vs[i] = ld<uint2>(a);
-          vz[i] = ld<uint16_t>(a + z_off);  // rows 4-7 of the product repeat rows 0-3: nobody looks
-          if constexpr (tail) {
-            if (v_key[i] >= valid) {  // what a stale row holds may be a NaN
-              vs[i] = make_uint2(0, 0);
-              vz[i] = 0;
-            }
-          }
-        }
-        {
-          const uint32_t za[4] = {__byte_perm(vz[0], vz[1], 0x5410), 0u, __byte_perm(vz[2], vz[3], 0x5410), 0u};
-#pragma unroll
-          for (int n = 0; n < NT; ++n) mma_bf16(zacc[n], za, pb[n][0], pb[n][1], zacc[n]);
-        }
-        uint4 cv[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) cv[i] = ld<uint4>(st + at_v[i & 1] + (i >> 1) * 8 * kKv4Codes);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const uint32_t word[4] = {j == 0 ? cv[0].x : j == 1 ? cv[0].y : j == 2 ? cv[0].z : cv[0].w,
-                                    j == 0 ? cv[1].x : j == 1 ? cv[1].y : j == 2 ? cv[1].z : cv[1].w,
-                                    j == 0 ? cv[2].x : j == 1 ? cv[2].y : j == 2 ? cv[2].z : cv[2].w,
-                                    j == 0 ? cv[3].x : j == 1 ? cv[3].y : j == 2 ? cv[3].z : cv[3].w};
-          const uint32_t x = __byte_perm(word[0], word[1], half), y = __byte_perm(word[2], word[3], half);
-          const uint32_t sel = (j & 1) ? 0x7632u : 0x5410u;
-          const uint32_t s0 = __byte_perm(j < 2 ? vs[0].x : vs[0].y, j < 2 ? vs[1].x : vs[1].y, sel);
-          const uint32_t s1 = __byte_perm(j < 2 ? vs[2].x : vs[2].y, j < 2 ? vs[3].x : vs[3].y, sel);
-          const uint32_t a0[4] = {codes_bf16(x, mask), codes_bf16(x >> 4, mask), codes_bf16(y, mask),
-                                  codes_bf16(y >> 4, mask)};
-          const uint32_t a1[4] = {codes_bf16(x >> 8, mask), codes_bf16(x >> 12, mask), codes_bf16(y >> 8, mask),
-                                  codes_bf16(y >> 12, mask)};
+        for (int u = 0; u < kSub; ++u)
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
-            const uint32_t p0 = mul_bf16x2(pb[n][0], s0), p1 = mul_bf16x2(pb[n][1], s1);
-            mma_bf16(acc[n][2 * j], a0, p0, p1, acc[n][2 * j]);
-            mma_bf16(acc[n][2 * j + 1], a1, p0, p1, acc[n][2 * j + 1]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) e[u][n][i] = ex2(e[u][n][i]);
+            l[n][0] += e[u][n][0] + e[u][n][2];
+            l[n][1] += e[u][n][1] + e[u][n][3];
+            pb[u][n][0] = transpose8(pack_bf16x2(e[u][n][0], e[u][n][1]));
+            pb[u][n][1] = transpose8(pack_bf16x2(e[u][n][2], e[u][n][3]));
+          }
+        // ---- out^T += V^T P^T: rows channels, columns heads
+#pragma unroll
+        for (int u = 0; u < kSub; ++u) {
+          uint2 vs[4];
+          uint32_t vz[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint8_t* a = st + at_vs[i & 1] + (16 * u + (i >> 1) * 8) * kKv4Scales;
+            vs[i] = ld<uint2>(a);
+            vz[i] = ld<uint16_t>(a + z_off);  // rows 4-7 of the product repeat rows 0-3: nobody looks
+          }
+          {
+            const uint32_t za[4] = {__byte_perm(vz[0], vz[1], 0x5410), 0u, __byte_perm(vz[2], vz[3], 0x5410), 0u};
+#pragma unroll
+            for (int n = 0; n < NT; ++n) mma_bf16(zacc[n], za, pb[u][n][0], pb[u][n][1], zacc[n]);
+          }
+          uint4 cv[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) cv[i] = ld<uint4>(st + at_v[i & 1] + (16 * u + (i >> 1) * 8) * kKv4Codes);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const uint32_t word[4] = {j == 0 ? cv[0].x : j == 1 ? cv[0].y : j == 2 ? cv[0].z : cv[0].w,
+                                      j == 0 ? cv[1].x : j == 1 ? cv[1].y : j == 2 ? cv[1].z : cv[1].w,
+                                      j == 0 ? cv[2].x : j == 1 ? cv[2].y : j == 2 ? cv[2].z : cv[2].w,
+                                      j == 0 ? cv[3].x : j == 1 ? cv[3].y : j == 2 ? cv[3].z : cv[3].w};
+            const uint32_t x = __byte_perm(word[0], word[1], half), y = __byte_perm(word[2], word[3], half);
+            const uint32_t sel = (j & 1) ? 0x7632u : 0x5410u;
+            const uint32_t s0 = __byte_perm(j < 2 ? vs[0].x : vs[0].y, j < 2 ? vs[1].x : vs[1].y, sel);
+            const uint32_t s1 = __byte_perm(j < 2 ? vs[2].x : vs[2].y, j < 2 ? vs[3].x : vs[3].y, sel);
+            const uint32_t a0[4] = {codes_bf16(x, mask), codes_bf16(x >> 4, mask), codes_bf16(y, mask),
+                                    codes_bf16(y >> 4, mask)};
+            const uint32_t a1[4] = {codes_bf16(x >> 8, mask), codes_bf16(x >> 12, mask), codes_bf16(y >> 8, mask),
+                                    codes_bf16(y >> 12, mask)};
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+              const uint32_t p0 = mul_bf16x2(pb[u][n][0], s0), p1 = mul_bf16x2(pb[u][n][1], s1);
+              mma_bf16(acc[n][2 * j], a0, p0, p1, acc[n][2 * j]);
+              mma_bf16(acc[n][2 * j + 1], a1, p0, p1, acc[n][2 * j + 1]);
+            }
           }
         }
-      };
-      for (int t = t_first; t < t_first + cnt; ++t) {
-        if (!__all_sync(0xffffffffu, mbar_wait(full(stage), ph, budget, abort_flag))) {
-          failed = true;
-          break;
-        }
-        const int valid = w.keys - t * kTile;
-        if (valid >= warp * 16 + 16)
-          tile(std::false_type(), valid);
-        else
-          tile(std::true_type(), valid);
-        __syncwarp();
-        if (lane == 0) mbar_arrive(empty(stage));
-        if (++stage == kStages) {
-          stage = 0;
-          ph ^= 1;
-        }
-      }
-      if (failed) break;
-      // ---- the pair's stretch ends: merge the warps' states
-      float* sm_m = merge;                              // [warp][8 NT]
-      float* sm_l = merge + kWarps * 8 * NT;
-      float* sm_o = merge + 2 * kWarps * 8 * NT;        // [warp][8 NT][128]
+    }
+    if (ti.flags & kLast) {
+      // ---- the pair's stretch ends: merge the warps' states, a few heads at a time
+      float* sm_ml = merge;                                // [warp][head][2]
+      float* sm_o = merge + 2 * kWarps * kMergeHeads;      // [warp][head][128]
+      const int slot = 2 * cta + (parts == 0 ? 0 : 1);
+      ++parts;
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
+        for (int r = 0; r < 2; ++r)
 #pragma unroll
           for (int o = 4; o < 32; o <<= 1) l[n][r] += __shfl_xor_sync(0xffffffffu, l[n][r], o);
-          const int h = 8 * n + 2 * tq + r;
-          if (g == 0) {
-            sm_m[warp * 8 * NT + h] = m[n][r];
-            sm_l[warp * 8 * NT + h] = l[n][r];
-          }
-          float* so = sm_o + (size_t)(warp * 8 * NT + h) * kD;
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float add = __shfl_sync(0xffffffffu, zacc[n][r], 4 * j + tq);
+      for (int c = 0; c < 2 * NT; ++c) {
+        if (c * kMergeHeads >= G) break;
+        const int n = c >> 1;
+        float zj[4][2];
 #pragma unroll
-            for (int i = 2 * j; i < 2 * j + 2; ++i) {
-              so[16 * i + g] = acc[n][i][r] + add;
-              so[16 * i + g + 8] = acc[n][i][r + 2] + add;
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int r = 0; r < 2; ++r) zj[j][r] = __shfl_sync(0xffffffffu, zacc[n][r], 4 * j + tq);
+        if ((tq >> 1) == (c & 1)) {  // the lanes whose columns are these heads
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            const int hh = warp * kMergeHeads + 2 * (tq & 1) + r;
+            if (g == 0) {
+              sm_ml[2 * hh] = m[n][r];
+              sm_ml[2 * hh + 1] = l[n][r];
+            }
+            float* so = sm_o + hh * kD + g;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              so[16 * i] = acc[n][i][r] + zj[i >> 1][r];
+              so[16 * i + 8] = acc[n][i][r + 2] + zj[i >> 1][r];
             }
           }
         }
-      if (!sync_all()) {
-        failed = true;
-        break;
-      }
-      const bool complete = cnt == whole;
-      const int slot = 2 * cta + (left == n_mine ? 0 : 1);
-      for (int h = warp; h < G; h += kWarps) {  // a warp per head, four channels a lane
-        float mm = -INFINITY;
+        __syncthreads();
+        const int h = c * kMergeHeads + warp;  // a warp per head, four channels a lane
+        if (h < G) {
+          float mm = -INFINITY;
 #pragma unroll
-        for (int v = 0; v < kWarps; ++v) mm = fmaxf(mm, sm_m[v * 8 * NT + h]);
-        const float mu = mm == -INFINITY ? 0.f : mm;
-        float ll = 0.f;
-        float4 oo = make_float4(0.f, 0.f, 0.f, 0.f);
+          for (int v = 0; v < kWarps; ++v) mm = fmaxf(mm, sm_ml[2 * (v * kMergeHeads + warp)]);
+          const float mu = mm == -INFINITY ? 0.f : mm;
+          float ll = 0.f;
+          float4 oo = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-        for (int v = 0; v < kWarps; ++v) {
-          const float f = ex2(sm_m[v * 8 * NT + h] - mu);
-          const float4 x = *reinterpret_cast<const float4*>(sm_o + (size_t)(v * 8 * NT + h) * kD + 4 * lane);
-          ll += sm_l[v * 8 * NT + h] * f;
-          oo = make_float4(oo.x + x.x * f, oo.y + x.y * f, oo.z + x.z * f, oo.w + x.w * f);
+          for (int v = 0; v < kWarps; ++v) {
+            const int hh = v * kMergeHeads + warp;
+            const float f = ex2(sm_ml[2 * hh] - mu);
+            const float4 x = *reinterpret_cast<const float4*>(sm_o + hh * kD + 4 * lane);
+            ll += sm_ml[2 * hh + 1] * f;
+            oo = make_float4(oo.x + x.x * f, oo.y + x.y * f, oo.z + x.z * f, oo.w + x.w * f);
+          }
+          if (ti.flags & kWhole) {
+            const float inv = 1.f / ll;
+            __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.o.ptr) + ti.b * p.o.row +
+                               (long long)(ti.kvh * G + h) * p.o.head + 4 * lane;
+            *reinterpret_cast<uint2*>(o) =
+                make_uint2(pack_bf16x2(oo.x * inv, oo.y * inv), pack_bf16x2(oo.z * inv, oo.w * inv));
+          } else {
+            const size_t at = (size_t)slot * G + h;
+            *reinterpret_cast<float4*>(p.part_o + at * kD + 4 * lane) = oo;
+            if (lane == 0) *reinterpret_cast<float2*>(p.part_ml + 2 * at) = make_float2(mm, ll);
+          }
         }
-        if (complete) {
-          const float inv = 1.f / ll;
-          __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.o.ptr) + w.b * p.o.row +
-                             (long long)(w.kvh * G + h) * p.o.head + 4 * lane;
-          *reinterpret_cast<uint2*>(o) = make_uint2(pack_bf16x2(oo.x * inv, oo.y * inv), pack_bf16x2(oo.z * inv, oo.w * inv));
-        } else {
-          const size_t at = (size_t)slot * G + h;
-          *reinterpret_cast<float4*>(p.part_o + at * kD + 4 * lane) = oo;
-          if (lane == 0) *reinterpret_cast<float2*>(p.part_ml + 2 * at) = make_float2(mm, ll);
-        }
+        __syncthreads();  // the buffer is reused
       }
-      if (!sync_all()) {  // the merge buffer is reused by the next pair
-        failed = true;
-        break;
-      }
-      left -= cnt;
-      if (left > 0) w.next(p);
     }
-    if (failed) {
-      *abort_flag = 1;
-      if (lane == 0) report_timeout(p.status, 0x41);
-    }
-  }
-  __syncthreads();
-  // After an abort, tiles that nobody waited for may still be landing: they complete
-  // before the CTA exits (every thread reads the same flag).
-  if (*abort_flag && warp == kWarps && lane == 0) {
-    volatile int never = 0;
-    for (int s = 0; s < kStages; ++s)
-      if (issued & (1u << s)) mbar_wait(full(s), (parity >> s) & 1, kDrainNs, &never);
+    __syncwarp();  // every lane is done with the stage: the next copies may overwrite it
+    if (++stage == kStages) stage = 0;
   }
 }
 
@@ -754,8 +740,7 @@ cudaError_t launch_nt(const Kv4Params& p, int grid, cudaStream_t s) {
 size_t attn_kv4_ws_bytes(int B, int H, int Hkv, int num_sms) { return kv4_ws(B, H, Hkv, num_sms).bytes; }
 
 cudaError_t launch_attn_decode_kv4(const HeadRows& q, const Kv4Cache& c, const HeadRows& o, int B, int H, int Hkv,
-                                   int window, void* ws, int num_sms, DevStatus* st, unsigned long long wait_ns,
-                                   cudaStream_t s, const char** why) {
+                                   int window, void* ws, int num_sms, cudaStream_t s, const char** why) {
   if (H / Hkv > 16) {
     *why = "4-bit decode attention: at most 16 query heads per KV head";
     return cudaErrorInvalidValue;
@@ -764,8 +749,7 @@ cudaError_t launch_attn_decode_kv4(const HeadRows& q, const Kv4Cache& c, const H
   const Kv4Ws w = kv4_ws(B, H, Hkv, num_sms);
   uint8_t* base = static_cast<uint8_t*>(ws);
   Kv4Params p{q, o, c, B, H, Hkv, window > 0 ? window : 0, reinterpret_cast<int*>(base + w.prefix),
-              reinterpret_cast<float*>(base + w.ml), reinterpret_cast<float*>(base + w.o), kLog2e / sqrtf((float)kD),
-              st, wait_ns};
+              reinterpret_cast<float*>(base + w.ml), reinterpret_cast<float*>(base + w.o), kLog2e / sqrtf((float)kD)};
   // a CTA per kMinTiles tiles of the largest cache this could be
   const long long most = (long long)B * Hkv * ((c.capacity + kTile - 1) / kTile);
   const int grid = (int)std::max(1ll, std::min<long long>(kv4_grid(H, Hkv, num_sms), most / kMinTiles));

@@ -1639,9 +1639,8 @@ blk_status blk_attn_decode_kv4(blk_handle* h, const blk_head_rows* q, const blk_
   BLK_TRY(check_device(h));
   const char* why = nullptr;
   return check_cuda(launch_attn_decode_kv4(head_rows(q), kv4_cache(cache), head_rows(o), batch, d.n_heads,
-                                           d.n_kv_heads, d.sliding_window, workspace, h->num_sms, h->status,
-                                           (unsigned long long)g_wait_ns.load(), static_cast<cudaStream_t>(stream),
-                                           &why),
+                                           d.n_kv_heads, d.sliding_window, workspace, h->num_sms,
+                                           static_cast<cudaStream_t>(stream), &why),
                     "4-bit decode attention", why);
 }
 

@@ -311,8 +311,7 @@ int attn_decode_split_cap(int max_len);
 // (at most the capacity; the last `window` of them with a window). ws: attn_kv4_ws_bytes.
 size_t attn_kv4_ws_bytes(int B, int H, int Hkv, int num_sms);
 cudaError_t launch_attn_decode_kv4(const HeadRows& q, const Kv4Cache& c, const HeadRows& o, int B, int H, int Hkv,
-                                   int window, void* ws, int num_sms, DevStatus* st, unsigned long long wait_ns,
-                                   cudaStream_t s, const char** why);
+                                   int window, void* ws, int num_sms, cudaStream_t s, const char** why);
 
 // Decode attention with its split partials in a fixed file-scope device array
 // (no workspace, no allocation); kv_lens[b] keys per sequence, <= kv_stride.
