@@ -167,20 +167,6 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-// (w & mask) | bits in one instruction: the mask in a register (see nibble_mask), as an
-// instruction has room for one constant only.
-template <uint32_t BITS>
-__device__ __forceinline__ uint32_t and_or(uint32_t w, uint32_t mask) {
-  uint32_t r;
-  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(w), "r"(mask), "n"(BITS));
-  return r;
-}
-// A constant that the compiler keeps in a register instead of folding it.
-__device__ __forceinline__ uint32_t nibble_mask(uint32_t c) {
-  uint32_t r;
-  asm volatile("mov.b32 %0, %1;" : "=r"(r) : "r"(c));
-  return r;
-}
 // The codes in the nibbles at bits 0-3 and 16-19 as a pair of bf16, from 128 + code.
 __device__ __forceinline__ uint32_t codes_bf16(uint32_t w, uint32_t mask) {
   const uint32_t v = and_or<0x43004300u>(w, mask), c = 0xC300C300u;
@@ -350,7 +336,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<NT>::kCtas) attn_kv4_kernel(cons
     at_vs[i] = 2 * kCodeBytes + kScaleBytes + v_key[i] * kKv4Scales;
   }
   const uint32_t z_off = 8 + 2 * (g & 3);
-  const uint32_t mask = nibble_mask(0x000F000Fu), mask_hi = nibble_mask(0x00F000F0u);
+  const uint32_t mask = kept_constant(0x000F000Fu), mask_hi = kept_constant(0x00F000F0u);
   const uint32_t half = (g & 1) ? 0x7632u : 0x5410u;  // which bytes of a word are this row's
 
   uint32_t qf[NT][8][2], qz[NT][2];

@@ -1596,7 +1596,7 @@ blk_status blk_kv4_store(blk_handle* h, const blk_head_rows* k, const blk_head_r
   if (batch == 0) return BLK_OK;
   BLK_TRY(check_device(h));
   return check_cuda(launch_kv4_store(head_rows(k), head_rows(v), rows, cu_seqlens, starts, batch, d.n_kv_heads,
-                                     kv4_cache(cache), h->status, static_cast<cudaStream_t>(stream)),
+                                     kv4_cache(cache), h->num_sms, h->status, static_cast<cudaStream_t>(stream)),
                     "4-bit store");
 }
 
@@ -1613,7 +1613,7 @@ blk_status blk_kv4_load(blk_handle* h, const blk_kv4_cache* cache, const int* cu
   if (k->ptr == v->ptr) return fail(BLK_ERR_INVALID_ARG, "k and v are the same rows");
   BLK_TRY(check_device(h));
   return check_cuda(launch_kv4_load(head_rows(k), head_rows(v), rows, cu_seqlens, starts, batch, d.n_kv_heads,
-                                    kv4_cache(cache), h->status, static_cast<cudaStream_t>(stream)),
+                                    kv4_cache(cache), h->num_sms, h->status, static_cast<cudaStream_t>(stream)),
                     "4-bit load");
 }
 

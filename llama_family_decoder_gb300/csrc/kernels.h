@@ -56,11 +56,11 @@ struct Kv4Cache {
 // (starts null: lens[b], an append); lens[b] becomes the slot behind the last one. Rows that
 // do not fit are left out, lens stops at the capacity and the status word records CACHE_FULL.
 cudaError_t launch_kv4_store(const HeadRows& k, const HeadRows& v, int rows, const int* cu, const int* starts, int B,
-                             int Hkv, const Kv4Cache& c, DevStatus* st, cudaStream_t s);
+                             int Hkv, const Kv4Cache& c, int num_sms, DevStatus* st, cudaStream_t s);
 // The reverse: slots starts[b] .. (null: 0 ..) as bf16 rows; slots outside the cache give
 // zeros and record INVALID_ARG.
 cudaError_t launch_kv4_load(const HeadRows& k, const HeadRows& v, int rows, const int* cu, const int* starts, int B,
-                            int Hkv, const Kv4Cache& c, DevStatus* st, cudaStream_t s);
+                            int Hkv, const Kv4Cache& c, int num_sms, DevStatus* st, cudaStream_t s);
 
 // ---------------------------------------------------------------- embedding
 // out[r, :] = table[tokens[r], :] (row_bytes per row, a multiple of 16); ids outside

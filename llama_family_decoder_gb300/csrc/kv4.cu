@@ -12,7 +12,9 @@
 //
 // HBM-bound, one pass: 16 lanes hold a row, 8 neighbouring channels each; a group is 4
 // lanes (two shuffles for its extremes), and four more shuffles in the same 4 lanes
-// turn their codes into the row's words.
+// turn their codes into the row's words. A block takes a few token rows, all heads: it looks
+// up their slots once (a binary search of cu_seqlens in shared memory) while its first rows
+// are already on the way, and loads a row ahead of the one it converts.
 #include "common.cuh"
 #include "kernels.h"
 #include "kv4.cuh"
@@ -25,86 +27,183 @@ constexpr int kThreads = 256;
 constexpr int kStatusInvalidArg = 1;  // == BLK_ERR_INVALID_ARG
 constexpr int kStatusCacheFull = 4;   // == BLK_ERR_CACHE_FULL
 
-struct StoreParams {
+constexpr int kMaxBlockRows = 64;     // token rows of a block, at most
+constexpr int kSharedSeqs = 1024;     // sequences whose cu_seqlens a block copies to shared memory
+
+// Rows of packed tokens and their slots.
+struct RowParams {
   HeadRows k, v;
   const int* cu;      // [B + 1], or null: row b is sequence b
-  const int* starts;  // [B] first slots, or null
+  const int* starts;  // [B] first slots, or null: 0
   Kv4Cache c;
-  int rows, B, Hkv, warps_per_row;
-  int first_slot_lens;  // starts is c.lens itself (an append)
+  int rows, B, Hkv, block_rows;
   DevStatus* status;
 };
 
-// The sequence of packed row r: the number of entries of cu[1 .. B] that are <= r,
-// found by a warp 32 at a time. Returns -1 for rows before cu[0] or behind cu[B].
-__device__ __forceinline__ int sequence_of_row(const int* cu, int B, int r, int lane) {
-  if (r < cu[0] || r >= cu[B]) return -1;
-  int lo = 0, n = B;  // the answer is in [lo, lo + n)
-  while (n > 1) {
-    const int step = (n + 31) / 32;
-    // cu[lo + step * (lane + 1)] <= r: the answer is at or past that entry
-    const int at = lo + step * (lane + 1);
-    const bool past = at < lo + n && cu[at] <= r;
-    const int k = __popc(__ballot_sync(0xffffffffu, past));
-    const int base = lo + step * k;
-    n = min(step, lo + n - base);
-    lo = base;
+// What a half warp works on in turn: K and V of one row (of the block) and head, and where they
+// are. Both halves of a warp take the same number of turns; row >= the block's rows: nothing
+// left.
+struct Unit {
+  int row, head, turns, rows_on, heads_on;
+  long long k, v, plane;          // element offsets into k, v; slots before the head's plane
+  long long k_on, v_on, plane_on;  // ... from one turn to the next, and on when the head wraps
+  long long k_wrap, v_wrap, plane_wrap;
+  __device__ __forceinline__ Unit(const RowParams& p, int r0, int n) {
+    const int halves = blockDim.x / 16, u = threadIdx.x / 16;
+    row = u / p.Hkv;
+    head = u - row * p.Hkv;
+    rows_on = halves / p.Hkv;
+    heads_on = halves - rows_on * p.Hkv;
+    turns = (n * p.Hkv - (u & ~1) + halves - 1) / halves;
+    k = (r0 + row) * p.k.row + head * p.k.head + 8 * (threadIdx.x & 15);
+    v = (r0 + row) * p.v.row + head * p.v.head + 8 * (threadIdx.x & 15);
+    plane = (long long)head * p.c.capacity;
+    k_on = rows_on * p.k.row + heads_on * p.k.head;
+    v_on = rows_on * p.v.row + heads_on * p.v.head;
+    plane_on = (long long)heads_on * p.c.capacity;
+    k_wrap = p.k.row - p.Hkv * p.k.head;
+    v_wrap = p.v.row - p.Hkv * p.v.head;
+    plane_wrap = -(long long)p.Hkv * p.c.capacity;
   }
-  return lo;
+  __device__ __forceinline__ void next(const RowParams& p) {
+    row += rows_on;
+    k += k_on;
+    v += v_on;
+    if (heads_on != 0) {  // the same for all
+      head += heads_on;
+      plane += plane_on;
+      if (head >= p.Hkv) {
+        head -= p.Hkv;
+        ++row;
+        k += k_wrap;
+        v += v_wrap;
+        plane += plane_wrap;
+      }
+    }
+  }
+};
+
+// at[i] := the slot of the block's row i, counted over the whole cache for KV head 0 (-1: a row
+// of no sequence, -2: a slot outside the cache).
+__device__ __forceinline__ void find_slots(const RowParams& p, int r0, int n, long long* at, int* s_cu) {
+  const int tid = threadIdx.x;
+  const int* cu = p.cu;
+  if (cu && p.B <= kSharedSeqs) {
+    for (int i = tid; i <= p.B; i += blockDim.x) s_cu[i] = cu[i];
+    __syncthreads();
+    cu = s_cu;
+  }
+  if (tid < n) {
+    const int r = r0 + tid;
+    int b = r, i = 0;
+    bool in = true;
+    if (cu) {
+      in = r >= cu[0] && r < cu[p.B];
+      int lo = 0, hi = p.B;  // the last sequence that begins at or before r
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) / 2;
+        if (cu[mid] <= r)
+          lo = mid;
+        else
+          hi = mid;
+      }
+      b = lo;
+      i = r - cu[lo];
+    }
+    long long a = -1;
+    if (in) {
+      const long long slot = (long long)(p.starts ? p.starts[b] : 0) + i;
+      a = slot >= 0 && slot < p.c.capacity ? (long long)b * p.Hkv * p.c.capacity + slot : -2;
+    }
+    at[tid] = a;
+  }
+  __syncthreads();
 }
 
 __device__ __forceinline__ uint32_t bf16_bits(float f) { return __bfloat16_as_ushort(__float2bfloat16_rn(f)); }
 
-// One row by 16 lanes (m = lane & 15: channels 8 m .. 8 m + 7), all 32 lanes converged.
-__device__ __forceinline__ void store_row(const __nv_bfloat16* src, uint8_t* codes, uint8_t* scales, bool on, int lane) {
+// The correctly rounded quotient d / s from inv = (1 / s)(1 + e), |e| <= 2^-23, s of at most 8
+// significant bits, all of them normal numbers: q = RN(d inv) is within a relative 2^-22 of it,
+// the remainder d - q s is exact in one fused multiply-add, and q + rem inv misses d / s by a
+// relative 2^-45 at most before its rounding (the correction step of Markstein 1990). A
+// quotient of a 24-bit by an 8-bit number keeps a relative 2^-34 away from the middle between
+// two fp32 numbers, so the rounding is that of d / s.
+__device__ __forceinline__ float quotient(float d, float s, float inv) {
+  const float q = d * inv;
+  return fmaf(fmaf(-q, s, d), inv, q);
+}
+__device__ __forceinline__ float reciprocal(float s) {  // documented to be within 2^-23
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
+  return r;
+}
+
+// Packed bf16 least and greatest; a NaN in either operand wins.
+__device__ __forceinline__ uint32_t min2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+// One row by 16 lanes (m = lane & 15: channels 8 m .. 8 m + 7, in u), all 32 lanes converged.
+__device__ __forceinline__ void store_row(const uint4& u, uint8_t* codes, uint8_t* scales, bool on, int lane) {
   const int m = lane & 15, q = lane & 3, j = m >> 2;
+  uint32_t lo2 = min2(min2(u.x, u.y), min2(u.z, u.w)), hi2 = max2(max2(u.x, u.y), max2(u.z, u.w));
+#pragma unroll
+  for (int o = 1; o <= 2; o <<= 1) {
+    lo2 = min2(lo2, __shfl_xor_sync(0xffffffffu, lo2, o));
+    hi2 = max2(hi2, __shfl_xor_sync(0xffffffffu, hi2, o));
+  }
+  const uint32_t zb = min2(lo2, lo2 >> 16) & 0xffffu, tb = max2(hi2, hi2 >> 16);
+  const float z = __uint_as_float(zb << 16), span = __uint_as_float(tb << 16) - z;
   float x[8];
   {
-    const uint4 u = on ? *reinterpret_cast<const uint4*>(src + 8 * m) : make_uint4(0, 0, 0, 0);
     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const float2 t = unpack_bf16x2(w[i]);
-      x[2 * i] = t.x;
-      x[2 * i + 1] = t.y;
+      x[2 * i] = __uint_as_float(w[i] << 16) - z;
+      x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u) - z;
     }
   }
-  float lo = x[0], hi = x[0];
-  bool nan = x[0] != x[0];
+  uint32_t w = 0, sz;
+  if (span >= 1e-28f && span <= 3.402823466e38f) {
+    const uint32_t sb = bf16_bits(quotient(span, 15.f, 1.f / 15.f));
+    const float s = __uint_as_float(sb << 16), inv = reciprocal(s);
+    // adding 1.5 * 2^23 rounds a quotient (at most 15.1) to its code, in the sum's low bits; the
+    // bits are added up as integers, each 4 bits further, and 0x4B400000 (8 times, likewise
+    // shifted: 0x4B400000 * 0x11111111) is taken off
 #pragma unroll
-  for (int i = 1; i < 8; ++i) {
-    lo = fminf(lo, x[i]);
-    hi = fmaxf(hi, x[i]);
-    nan |= x[i] != x[i];
-  }
+    for (int i = 7; i >= 0; --i) w = w * 16u + __float_as_uint(quotient(x[i], s, inv) + 12582912.f);
+    w -= 0x4B400000u * 0x11111111u;
+    sz = sb | zb << 16;
+  } else if (span < 1e-28f) {  // quotients and reciprocals may leave the normal numbers
+    const uint32_t sb = bf16_bits(span / 15.f);
+    const float s = __uint_as_float(sb << 16);
+    if (s > 0.f)
+#pragma unroll 1
+      for (int i = 0; i < 8; ++i) {
+        w |= (uint32_t)fminf(rintf(x[0] / s), 15.f) << (4 * i);
 #pragma unroll
-  for (int o = 1; o <= 2; o <<= 1) {
-    lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
-    hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
-  }
-  const uint32_t nans = __ballot_sync(0xffffffffu, nan);
-  const float span = hi - lo;
-  const bool finite = ((nans >> (lane & ~3)) & 15u) == 0 && span <= 3.402823466e38f;
-  const uint32_t sb = finite ? bf16_bits(span / 15.f) : 0u;
-  const uint32_t zb = finite ? bf16_bits(lo) : 0x7fc0u;
-  const float s = __uint_as_float(sb << 16), z = __uint_as_float(zb << 16);
-  uint32_t w = 0;
-  if (s > 0.f) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float c = fminf(fmaxf(rintf((x[i] - z) / s), 0.f), 15.f);
-      w |= (uint32_t)c << (4 * i);
-    }
+        for (int k = 0; k < 7; ++k) x[k] = x[k + 1];
+      }
+    sz = sb | zb << 16;
+  } else {  // a NaN or an infinity, or a span past fp32
+    sz = 0x7fc00000u;
   }
   // lanes q = 0, 1 of the group hold the low and high nibbles of its bytes e = 0, lanes
-  // 2, 3 those of e = 1 (nibble g = 2 t + u); lane q writes word t = q
-  uint32_t a[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) a[i] = __shfl_sync(0xffffffffu, w, (lane & ~3) + i) >> (8 * q);
-  const uint32_t word = (a[0] & 15u) | (a[1] & 15u) << 4 | (a[2] & 15u) << 8 | (a[3] & 15u) << 12 |
-                        (a[0] >> 4 & 15u) << 16 | (a[1] >> 4 & 15u) << 20 | (a[2] >> 4 & 15u) << 24 |
-                        (a[3] >> 4 & 15u) << 28;
-  const uint32_t sz = sb | zb << 16;
+  // 2, 3 those of e = 1 (nibble g = 2 t + u); lane q writes word t = q: byte q of the four
+  // lanes' words, their low nibbles (u = 0) side by side, then their high ones
+  const uint32_t w0 = __shfl_sync(0xffffffffu, w, lane & ~3), w1 = __shfl_sync(0xffffffffu, w, (lane & ~3) + 1),
+                 w2 = __shfl_sync(0xffffffffu, w, (lane & ~3) + 2), w3 = __shfl_sync(0xffffffffu, w, lane | 3);
+  const uint32_t pick = q | (4 + q) << 4;
+  const uint32_t y = __byte_perm(__byte_perm(w0, w1, pick), __byte_perm(w2, w3, pick), 0x5410);
+  const uint32_t n0 = y & 0x0F0F0F0Fu, n1 = y >> 4 & 0x0F0F0F0Fu;
+  const uint32_t word = __byte_perm(n0 | n0 >> 4, n1 | n1 >> 4, 0x6420);
   const int pair = (lane & 16) + 8 * (q & 1);  // the groups 2 (q & 1) and 2 (q & 1) + 1
   const uint32_t g0 = __shfl_sync(0xffffffffu, sz, pair), g1 = __shfl_sync(0xffffffffu, sz, pair + 4);
   if (on) {
@@ -114,41 +213,43 @@ __device__ __forceinline__ void store_row(const __nv_bfloat16* src, uint8_t* cod
   }
 }
 
-// A warp takes two KV heads of one row, K and V of both.
-__global__ void __launch_bounds__(kThreads) kv4_store_kernel(const __grid_constant__ StoreParams p) {
+// append: starts is lens itself. Without cu its blocks hold a row each and move lens on; with cu
+// a second kernel does.
+__global__ void __launch_bounds__(kThreads) kv4_store_kernel(const __grid_constant__ RowParams p, int append) {
   pdl_launch_dependents();
   pdl_wait();
-  const int lane = threadIdx.x & 31;
-  const long long gw = (long long)blockIdx.x * (blockDim.x / 32) + (threadIdx.x >> 5);
-  const int row = (int)(gw / p.warps_per_row), part = (int)(gw % p.warps_per_row);
-  int b = -1, slot = 0;
-  if (row < p.rows) {
-    b = p.cu ? sequence_of_row(p.cu, p.B, row, lane) : row;
-    if (b >= 0) slot = p.starts[b] + (p.cu ? row - p.cu[b] : 0);
-  }
-  const bool fits = b >= 0 && slot >= 0 && slot < p.c.capacity;
-  if (b >= 0 && !fits && lane == 0 && p.status) atomicCAS(&p.status->code, 0, kStatusCacheFull);
-  if (fits) {
-    for (int h0 = 2 * part; h0 < p.Hkv; h0 += 2 * p.warps_per_row) {
-      const int h = h0 + (lane >> 4);
-      const bool on = h < p.Hkv;
-      const size_t at = ((size_t)b * p.Hkv + (on ? h : 0)) * p.c.capacity + slot;
-      const long long off = on ? h : 0;
-      store_row(static_cast<const __nv_bfloat16*>(p.k.ptr) + row * p.k.row + off * p.k.head, p.c.k + at * kKv4Codes,
-                p.c.k_scale + at * kKv4Scales, on, lane);
-      store_row(static_cast<const __nv_bfloat16*>(p.v.ptr) + row * p.v.row + off * p.v.head, p.c.v + at * kKv4Codes,
-                p.c.v_scale + at * kKv4Scales, on, lane);
+  __shared__ long long at[kMaxBlockRows];
+  __shared__ int s_cu[kSharedSeqs + 1];
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int r0 = blockIdx.x * p.block_rows, n = max(0, min(p.block_rows, p.rows - r0));
+  Unit un(p, r0, n);
+  uint4 k = make_uint4(0, 0, 0, 0), v = k;
+  auto fetch = [&] {
+    if (un.row < n) {
+      k = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.k.ptr) + un.k);
+      v = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.v.ptr) + un.v);
     }
+  };
+  fetch();
+  find_slots(p, r0, n, at, s_cu);
+  if (tid < n && at[tid] == -2 && p.status) atomicCAS(&p.status->code, 0, kStatusCacheFull);
+  for (int turn = 0; turn < un.turns; ++turn) {
+    const uint4 ku = k, vu = v;
+    const long long a = un.row < n ? at[un.row] : -1;
+    const size_t to = a >= 0 ? (size_t)(a + un.plane) : 0;
+    un.next(p);
+    fetch();
+    store_row(ku, p.c.k + to * kKv4Codes, p.c.k_scale + to * kKv4Scales, a >= 0, lane);
+    store_row(vu, p.c.v + to * kKv4Codes, p.c.v_scale + to * kKv4Scales, a >= 0, lane);
   }
-  if (!p.first_slot_lens) {  // the new lengths: nobody reads lens here
+  if (!append) {  // the new lengths: nobody reads lens here
     if (blockIdx.x == 0)
-      for (int i = threadIdx.x; i < p.B; i += blockDim.x) {
-        const long long n = (long long)p.starts[i] + (p.cu ? p.cu[i + 1] - p.cu[i] : 1);
-        p.c.lens[i] = (int)(n < 0 ? 0 : n < p.c.capacity ? n : p.c.capacity);
+      for (int i = tid; i < p.B; i += blockDim.x) {
+        const long long e = (long long)p.starts[i] + (p.cu ? p.cu[i + 1] - p.cu[i] : 1);
+        p.c.lens[i] = (int)(e < 0 ? 0 : e < p.c.capacity ? e : p.c.capacity);
       }
-  } else if (!p.cu) {  // one row per sequence, one block per row: every warp has read its slot
-    __syncthreads();
-    if (threadIdx.x == 0 && fits) p.c.lens[b] = slot + 1;
+  } else if (!p.cu && tid == 0 && n > 0 && at[0] >= 0) {  // the block has read its slot (find_slots)
+    p.c.lens[r0] += 1;
   }
 }
 
@@ -162,85 +263,88 @@ __global__ void kv4_lens_kernel(const int* cu, int* lens, int B, int capacity) {
   }
 }
 
-struct LoadParams {
-  HeadRows k, v;
-  const int* cu;
-  const int* starts;  // [B], or null: slot 0
-  Kv4Cache c;
-  int rows, B, Hkv, warps_per_row;
-  DevStatus* status;
-};
-
-__device__ __forceinline__ void load_row(__nv_bfloat16* dst, const uint8_t* codes, const uint8_t* scales, bool on,
-                                         bool valid, int lane) {
-  const int m = lane & 15, q = lane & 3, j = m >> 2;
-  uint32_t word = 0;
-  float s = 0.f, z = 0.f;
-  if (on && valid) {
-    word = *reinterpret_cast<const uint32_t*>(codes + 16 * q + 4 * j);
-    s = __uint_as_float((uint32_t) * reinterpret_cast<const uint16_t*>(scales + 2 * j) << 16);
-    z = __uint_as_float((uint32_t) * reinterpret_cast<const uint16_t*>(scales + 8 + 2 * j) << 16);
-  }
+// One row by 16 lanes: the code word and the scale and offset bits that a lane holds -> its 8
+// channels. All 32 lanes converged.
+__device__ __forceinline__ void load_row(__nv_bfloat16* dst, uint32_t word, uint32_t sb, uint32_t zb, bool on, int lane,
+                                         uint32_t mask) {
+  const int q = lane & 3;
+  const float s = __uint_as_float(sb << 16), z = __uint_as_float(zb << 16);
   // lane q wants nibble q (of each 16-bit half: channels g = 2 t, 2 t + 1) of the 4 words t
   float x[8];
 #pragma unroll
   for (int t = 0; t < 4; ++t) {
     const uint32_t w = __shfl_sync(0xffffffffu, word, (lane & ~3) + t) >> (4 * q);
-    x[2 * t] = z + s * (float)(w & 15u);
-    x[2 * t + 1] = z + s * (float)(w >> 16 & 15u);
+    // a code under the exponent of 2^23, taken off again
+    x[2 * t] = fmaf(s, __uint_as_float(and_or<0x4B000000u>(w, mask)) - 8388608.f, z);
+    x[2 * t + 1] = fmaf(s, __uint_as_float(and_or<0x4B000000u>(w >> 16, mask)) - 8388608.f, z);
   }
   if (on)
-    *reinterpret_cast<uint4*>(dst + 8 * m) = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]),
-                                                        pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
+    *reinterpret_cast<uint4*>(dst) = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]),
+                                                pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
 }
 
-__global__ void __launch_bounds__(kThreads) kv4_load_kernel(const __grid_constant__ LoadParams p) {
+__global__ void __launch_bounds__(kThreads) kv4_load_kernel(const __grid_constant__ RowParams p) {
   pdl_launch_dependents();
   pdl_wait();
-  const int lane = threadIdx.x & 31;
-  const long long gw = (long long)blockIdx.x * (blockDim.x / 32) + (threadIdx.x >> 5);
-  const int row = (int)(gw / p.warps_per_row), part = (int)(gw % p.warps_per_row);
-  if (row >= p.rows) return;
-  const int b = p.cu ? sequence_of_row(p.cu, p.B, row, lane) : row;
-  if (b < 0) return;  // a row of no sequence is left as it was
-  const int slot = (p.starts ? p.starts[b] : 0) + (p.cu ? row - p.cu[b] : 0);
-  const bool valid = slot >= 0 && slot < p.c.capacity;
-  if (!valid && lane == 0 && p.status) atomicCAS(&p.status->code, 0, kStatusInvalidArg);
-  for (int h0 = 2 * part; h0 < p.Hkv; h0 += 2 * p.warps_per_row) {
-    const int h = h0 + (lane >> 4);
-    const bool on = h < p.Hkv;
-    const long long off = on ? h : 0;
-    const size_t at = ((size_t)b * p.Hkv + off) * p.c.capacity + (valid ? slot : 0);
-    load_row(static_cast<__nv_bfloat16*>(p.k.ptr) + row * p.k.row + off * p.k.head, p.c.k + at * kKv4Codes,
-             p.c.k_scale + at * kKv4Scales, on, valid, lane);
-    load_row(static_cast<__nv_bfloat16*>(p.v.ptr) + row * p.v.row + off * p.v.head, p.c.v + at * kKv4Codes,
-             p.c.v_scale + at * kKv4Scales, on, valid, lane);
+  __shared__ long long at[kMaxBlockRows];
+  __shared__ int s_cu[kSharedSeqs + 1];
+  const int tid = threadIdx.x, lane = tid & 31, q = lane & 3, j = (lane & 15) >> 2;
+  const int r0 = blockIdx.x * p.block_rows, n = max(0, min(p.block_rows, p.rows - r0));
+  Unit un(p, r0, n);
+  find_slots(p, r0, n, at, s_cu);
+  if (tid < n && at[tid] == -2 && p.status) atomicCAS(&p.status->code, 0, kStatusInvalidArg);
+  const uint32_t mask = kept_constant(15u);
+  uint32_t kw = 0, ks = 0, kz = 0, vw = 0, vs = 0, vz = 0;
+  auto fetch = [&] {
+    kw = ks = kz = vw = vs = vz = 0;
+    const long long a = un.row < n ? at[un.row] : -1;
+    if (a >= 0) {
+      const size_t from = (size_t)(a + un.plane);
+      kw = *reinterpret_cast<const uint32_t*>(p.c.k + from * kKv4Codes + 16 * q + 4 * j);
+      vw = *reinterpret_cast<const uint32_t*>(p.c.v + from * kKv4Codes + 16 * q + 4 * j);
+      const uint16_t* sk = reinterpret_cast<const uint16_t*>(p.c.k_scale + from * kKv4Scales) + j;
+      const uint16_t* sv = reinterpret_cast<const uint16_t*>(p.c.v_scale + from * kKv4Scales) + j;
+      ks = sk[0], kz = sk[4], vs = sv[0], vz = sv[4];
+    }
+  };
+  fetch();
+  for (int turn = 0; turn < un.turns; ++turn) {
+    const uint32_t kw0 = kw, ks0 = ks, kz0 = kz, vw0 = vw, vs0 = vs, vz0 = vz;
+    const bool on = un.row < n && at[un.row] != -1;  // a row of no sequence is left as it was
+    const long long k_to = un.k, v_to = un.v;
+    un.next(p);
+    fetch();
+    load_row(static_cast<__nv_bfloat16*>(p.k.ptr) + k_to, kw0, ks0, kz0, on, lane, mask);
+    load_row(static_cast<__nv_bfloat16*>(p.v.ptr) + v_to, vw0, vs0, vz0, on, lane, mask);
   }
+}
+
+// Token rows per block: a few, so that a block's look-up serves many rows, but at least about
+// four blocks per SM while there are enough.
+int block_rows(int rows, int Hkv, int num_sms) {
+  const int most = Hkv >= 64 ? 1 : 64 / Hkv;  // 64 units, four turns of a block's 16 half warps
+  const int fill = rows / (4 * num_sms);
+  return fill < 1 ? 1 : fill < most ? fill : most;
 }
 
 }  // namespace
 
 cudaError_t launch_kv4_store(const HeadRows& k, const HeadRows& v, int rows, const int* cu, const int* starts, int B,
-                             int Hkv, const Kv4Cache& c, DevStatus* st, cudaStream_t s) {
+                             int Hkv, const Kv4Cache& c, int num_sms, DevStatus* st, cudaStream_t s) {
   const bool append = starts == nullptr || starts == c.lens;
-  StoreParams p{k, v, cu, append ? c.lens : starts, c, rows, B, Hkv, (Hkv + 1) / 2, append ? 1 : 0, st};
-  if (append && !cu) {  // a block per row
-    p.warps_per_row = p.warps_per_row < kThreads / 32 ? p.warps_per_row : kThreads / 32;
-    return rows > 0 ? launch_pdl(kv4_store_kernel, rows, p.warps_per_row * 32, 0, s, p) : cudaSuccess;
-  }
-  const long long warps = (long long)rows * p.warps_per_row;
-  const long long grid = (warps + kThreads / 32 - 1) / (kThreads / 32);
-  cudaError_t e = launch_pdl(kv4_store_kernel, dim3((unsigned)(grid > 0 ? grid : 1)), kThreads, 0, s, p);
-  if (e != cudaSuccess || !append) return e;
+  RowParams p{k, v, cu, append ? c.lens : starts, c, rows, B, Hkv, block_rows(rows, Hkv, num_sms), st};
+  if (append && !cu) p.block_rows = 1;
+  const int grid = rows > 0 ? (rows + p.block_rows - 1) / p.block_rows : 1;
+  cudaError_t e = launch_pdl(kv4_store_kernel, grid, kThreads, 0, s, p, append ? 1 : 0);
+  if (e != cudaSuccess || !append || !cu) return e;
   return launch_pdl(kv4_lens_kernel, (B + 255) / 256, 256, 0, s, cu, c.lens, B, c.capacity);
 }
 
 cudaError_t launch_kv4_load(const HeadRows& k, const HeadRows& v, int rows, const int* cu, const int* starts, int B,
-                            int Hkv, const Kv4Cache& c, DevStatus* st, cudaStream_t s) {
+                            int Hkv, const Kv4Cache& c, int num_sms, DevStatus* st, cudaStream_t s) {
   if (rows <= 0) return cudaSuccess;
-  LoadParams p{k, v, cu, starts, c, rows, B, Hkv, (Hkv + 1) / 2, st};
-  const long long warps = (long long)rows * p.warps_per_row;
-  return launch_pdl(kv4_load_kernel, dim3((unsigned)((warps + kThreads / 32 - 1) / (kThreads / 32))), kThreads, 0, s, p);
+  const RowParams p{k, v, cu, starts, c, rows, B, Hkv, block_rows(rows, Hkv, num_sms), st};
+  return launch_pdl(kv4_load_kernel, (rows + p.block_rows - 1) / p.block_rows, kThreads, 0, s, p);
 }
 
 }  // namespace blk
