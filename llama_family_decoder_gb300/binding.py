@@ -231,6 +231,8 @@ class DecoderBlock:
         self._dev = torch.cuda.current_device()  # where the handle's tables live
         self._device = torch.device("cuda", self._dev)
         self._dtype = torch.bfloat16 if self.desc.dtype == 1 else torch.float32
+        self._sizes = n_heads, n_kv_heads, head_dim
+        self._axes = {}  # (sections, interleaved) -> blk_rope_axes
         # the current stream's handle, without building a Stream object where torch has the short way
         self._raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
             (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
@@ -370,20 +372,21 @@ class DecoderBlock:
     # workspace, are made for the call on its stream: calls on several streams, and captured
     # graphs, share none.
 
-    def _rows(self, t, name, rows, heads):
+    def _rows(self, t, name, shape):
         """A [rows, heads, d] tensor, of any row and head strides, as blk_head_rows."""
-        if t.dtype is not self._dtype or t.get_device() != self._dev or t.shape != (rows, heads, self.desc.head_dim):
-            _check_tensor(t, name, self._dtype, self._dev, (rows, heads, self.desc.head_dim))
+        if t.dtype is not self._dtype or t.get_device() != self._dev or t.shape != shape:
+            _check_tensor(t, name, self._dtype, self._dev, shape)
         rs, hs, cs = t.stride()
         if cs != 1:
             raise ValueError(f"{name}: the channels must be contiguous")
         return head_rows(t.data_ptr(), rs, hs)
 
-    def _out(self, rows, heads):
-        return self._torch.empty(rows, heads, self.desc.head_dim, dtype=self._dtype, device=self._device)
-
-    def _scratch(self, nbytes):
-        return self._torch.empty(nbytes, dtype=self._torch.uint8, device=self._device)
+    def _out(self, t, name, shape):
+        """An output and its blk_head_rows: the given tensor, or a new one."""
+        if t is not None:
+            return t, self._rows(t, name, shape)
+        t = self._torch.empty(shape, dtype=self._dtype, device=self._device)
+        return t, head_rows(t.data_ptr(), shape[1] * shape[2], shape[2])
 
     def _int32(self, t, name, n):
         return None if t is None else _contiguous(t, name, self._torch.int32, self._dev, (n,))
@@ -401,29 +404,31 @@ class DecoderBlock:
         if self._elsewhere(stream):
             with _on_stream(self._device, stream):
                 return self.qk_norm_rope(q, k, positions, q_gain, k_gain, sections, interleaved, q_out, k_out)
-        d, n = self.desc, q.shape[0]
-        H, Hkv = d.n_heads, d.n_kv_heads
+        H, Hkv, d = self._sizes
+        n = q.shape[0]
         axes = pos = gq = gk = None
-        if not d.no_rope:
-            n_axes = 1 if sections is None else len(sections)
-            if not 1 <= n_axes <= 4:
-                raise ValueError("sections: 1 to 4 position axes")
+        if not self.desc.no_rope:
+            n_axes = 1
+            if sections is not None:
+                key = (*sections, bool(interleaved))
+                axes = self._axes.get(key)
+                n_axes = len(key) - 1
+                if axes is None:
+                    if not 1 <= n_axes <= 4:
+                        raise ValueError("sections: 1 to 4 position axes")
+                    axes = self._axes[key] = blk_rope_axes(n_axes, (c_int * 4)(*sections), int(key[-1]))
             shape = (n,) if n_axes == 1 and positions.dim() == 1 else (n_axes, n)
             pos = _contiguous(positions, "positions", self._torch.int32, self._dev, shape)
-            if sections is not None:
-                axes = ctypes.byref(blk_rope_axes(n_axes, (c_int * 4)(*sections), int(bool(interleaved))))
-        if d.qk_norm:
+        if self.desc.qk_norm:
             if q_gain is None or k_gain is None:
                 raise ValueError("q_gain, k_gain: the handle norms queries and keys")
-            gq = _contiguous(q_gain, "q_gain", self._dtype, self._dev, (d.head_dim,))
-            gk = _contiguous(k_gain, "k_gain", self._dtype, self._dev, (d.head_dim,))
-        qi, ki = self._rows(q, "q", n, H), self._rows(k, "k", n, Hkv)
-        if q_out is None:
-            q_out = self._out(n, H)
-        if k_out is None:
-            k_out = self._out(n, Hkv)
-        _check(lib().blk_qk_norm_rope(self.handle, qi, ki, n, pos, axes, gq, gk, self._rows(q_out, "q_out", n, H),
-                                      self._rows(k_out, "k_out", n, Hkv), self._raw_stream(self._dev)))
+            gq = _contiguous(q_gain, "q_gain", self._dtype, self._dev, (d,))
+            gk = _contiguous(k_gain, "k_gain", self._dtype, self._dev, (d,))
+        qs, ks = (n, H, d), (n, Hkv, d)
+        qi, ki = self._rows(q, "q", qs), self._rows(k, "k", ks)
+        q_out, qo = self._out(q_out, "q_out", qs)
+        k_out, ko = self._out(k_out, "k_out", ks)
+        _check(lib().blk_qk_norm_rope(self.handle, qi, ki, n, pos, axes, gq, gk, qo, ko, self._raw_stream(self._dev)))
         return q_out, k_out
 
     def attn_packed(self, q, k, v, cu_seqlens, out=None, stream=None):
@@ -434,22 +439,22 @@ class DecoderBlock:
         if self._elsewhere(stream):
             with _on_stream(self._device, stream):
                 return self.attn_packed(q, k, v, cu_seqlens, out)
-        d, n, batch = self.desc, q.shape[0], cu_seqlens.numel() - 1
-        H, Hkv = d.n_heads, d.n_kv_heads
+        H, Hkv, d = self._sizes
+        n, batch = q.shape[0], cu_seqlens.numel() - 1
+        qs, ks = (n, H, d), (n, Hkv, d)
         cu = self._int32(cu_seqlens, "cu_seqlens", batch + 1)
-        rows = self._rows(q, "q", n, H), self._rows(k, "k", n, Hkv), self._rows(v, "v", n, Hkv)
-        if out is None:
-            out = self._out(n, H)
+        qi, ki, vi = self._rows(q, "q", qs), self._rows(k, "k", ks), self._rows(v, "v", ks)
+        out, o = self._out(out, "out", qs)
         nbytes = lib().blk_attn_packed_workspace_bytes(self.handle, n, batch)
-        ws = self._scratch(nbytes)
-        _check(lib().blk_attn_packed(self.handle, *rows, n, cu, batch, self._rows(out, "out", n, H), ws.data_ptr(),
-                                     nbytes, self._raw_stream(self._dev)))
+        ws = self._torch.empty(nbytes, dtype=self._torch.uint8, device=self._device)
+        _check(lib().blk_attn_packed(self.handle, qi, ki, vi, n, cu, batch, o, ws.data_ptr(), nbytes,
+                                     self._raw_stream(self._dev)))
         return out
 
     def kv4_cache(self, batch, capacity):
         """An empty KV cache in 4 bits: dict(k, k_scale, v, v_scale, lens)."""
         torch = self._torch
-        n = (batch, self.desc.n_kv_heads, capacity)
+        n = (batch, self._sizes[1], capacity)
         c = {"lens": torch.zeros(batch, dtype=torch.int32, device=self._device)}
         for x in ("k", "v"):
             c[x] = torch.zeros(*n, 64, dtype=torch.uint8, device=self._device)
@@ -458,8 +463,10 @@ class DecoderBlock:
 
     def _kv4(self, cache):
         torch, dev = self._torch, self._dev
-        batch, _, cap, _ = cache["k"].shape
-        codes, scales = (batch, self.desc.n_kv_heads, cap, 64), (batch, self.desc.n_kv_heads, cap, 8)
+        batch, Hkv, cap, _ = cache["k"].shape
+        if Hkv != self._sizes[1]:
+            raise ValueError(f"cache: {self._sizes[1]} KV heads are wanted, got {Hkv}")
+        codes, scales = (batch, Hkv, cap, 64), (batch, Hkv, cap, 8)
         return kv4_cache_struct(_contiguous(cache["k"], "cache k", torch.uint8, dev, codes),
                                 _contiguous(cache["k_scale"], "cache k_scale", torch.bfloat16, dev, scales),
                                 _contiguous(cache["v"], "cache v", torch.uint8, dev, codes),
@@ -475,8 +482,9 @@ class DecoderBlock:
             with _on_stream(self._device, stream):
                 return self.kv4_store(cache, k, v, cu_seqlens, starts, host_lens_max)
         c, batch = self._kv4(cache)
-        n, hkv = k.shape[0], self.desc.n_kv_heads
-        _check(lib().blk_kv4_store(self.handle, self._rows(k, "k", n, hkv), self._rows(v, "v", n, hkv), n,
+        n = k.shape[0]
+        shape = (n, *self._sizes[1:])
+        _check(lib().blk_kv4_store(self.handle, self._rows(k, "k", shape), self._rows(v, "v", shape), n,
                                    self._int32(cu_seqlens, "cu_seqlens", batch + 1),
                                    self._int32(starts, "starts", batch), batch, c, host_lens_max,
                                    self._raw_stream(self._dev)))
@@ -488,14 +496,12 @@ class DecoderBlock:
             with _on_stream(self._device, stream):
                 return self.kv4_load(cache, cu_seqlens, rows, starts, k_out, v_out)
         c, batch = self._kv4(cache)
-        n, hkv = batch if rows is None else rows, self.desc.n_kv_heads
+        n = batch if rows is None else rows
+        shape = (n, *self._sizes[1:])
         cu, st = self._int32(cu_seqlens, "cu_seqlens", batch + 1), self._int32(starts, "starts", batch)
-        if k_out is None:
-            k_out = self._out(n, hkv)
-        if v_out is None:
-            v_out = self._out(n, hkv)
-        _check(lib().blk_kv4_load(self.handle, c, cu, st, batch, n, self._rows(k_out, "k_out", n, hkv),
-                                  self._rows(v_out, "v_out", n, hkv), self._raw_stream(self._dev)))
+        k_out, ko = self._out(k_out, "k_out", shape)
+        v_out, vo = self._out(v_out, "v_out", shape)
+        _check(lib().blk_kv4_load(self.handle, c, cu, st, batch, n, ko, vo, self._raw_stream(self._dev)))
         return k_out, v_out
 
     def attn_decode_kv4(self, q, cache, out=None, stream=None):
@@ -505,14 +511,13 @@ class DecoderBlock:
             with _on_stream(self._device, stream):
                 return self.attn_decode_kv4(q, cache, out)
         c, batch = self._kv4(cache)
-        H = self.desc.n_heads
-        qi = self._rows(q, "q", batch, H)
-        if out is None:
-            out = self._out(batch, H)
+        H, _, d = self._sizes
+        qi = self._rows(q, "q", (batch, H, d))
+        out, o = self._out(out, "out", (batch, H, d))
         nbytes = lib().blk_attn_decode_kv4_workspace_bytes(self.handle, batch)
-        ws = self._scratch(nbytes)
-        _check(lib().blk_attn_decode_kv4(self.handle, qi, c, batch, self._rows(out, "out", batch, H), ws.data_ptr(),
-                                         nbytes, self._raw_stream(self._dev)))
+        ws = self._torch.empty(nbytes, dtype=self._torch.uint8, device=self._device)
+        _check(lib().blk_attn_decode_kv4(self.handle, qi, c, batch, o, ws.data_ptr(), nbytes,
+                                         self._raw_stream(self._dev)))
         return out
 
     def mlp(self, resid, h_normed, weights, out, stream=None):

@@ -23,7 +23,7 @@ namespace blk {
 
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 constexpr int kStatusInvalidArg = 1;  // == BLK_ERR_INVALID_ARG
 constexpr int kStatusCacheFull = 4;   // == BLK_ERR_CACHE_FULL
 
@@ -320,10 +320,10 @@ __global__ void __launch_bounds__(kThreads) kv4_load_kernel(const __grid_constan
 }
 
 // Token rows per block: a few, so that a block's look-up serves many rows, but at least about
-// four blocks per SM while there are enough.
+// twelve blocks per SM while there are enough.
 int block_rows(int rows, int Hkv, int num_sms) {
-  const int most = Hkv >= 64 ? 1 : 64 / Hkv;  // 64 units, four turns of a block's 16 half warps
-  const int fill = rows / (4 * num_sms);
+  const int most = Hkv >= 32 ? 1 : 32 / Hkv;  // 32 units, four turns of a block's 8 half warps
+  const int fill = rows / (12 * num_sms);
   return fill < 1 ? 1 : fill < most ? fill : most;
 }
 
