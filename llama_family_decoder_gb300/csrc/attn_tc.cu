@@ -60,15 +60,18 @@ constexpr int kKVBytes = 2 * kKVSub;        // 128 keys x 128 dims
 constexpr int kKStages = 2;                 // K ring
 constexpr int kVStages = 2;                 // V ring
 constexpr int kSmem = 1024 + kSlots * kQBytes + (kKStages + kVStages) * kKVBytes + 256;
+constexpr int kSmemSplit = kSmem + kBQ * 8;  // + slot 1's softmax states
+static_assert(kSmemSplit <= 227 * 1024, "shared memory");
 constexpr float kRescaleLog2 = 8.0f;
 constexpr unsigned long long kDrainNs = 2000000000ULL;
 constexpr float kLog2e = 1.4426950408889634f;
 static_assert(kSmem <= 227 * 1024, "shared memory");
 static_assert(kQSub == kKVSub && kKStages == 2 && kVStages == 2, "the MMA issuers' descriptor steps and stage selects");
 
-// A query tile (or, without head pairs, a pair of them) of a packed sequence.
+// A query tile of a packed sequence (or, not split, two of them): queries from `query` on of the
+// sequence whose len rows start at row0.
 struct __align__(16) PackedWork {
-  int row0, len, tile, unused;
+  int row0, len, query, unused;
 };
 
 struct AttnParams {
@@ -96,6 +99,9 @@ struct AttnParams {
   const PackedWork* work;
   const int* n_work;
   long long o_row, o_head;
+  // 2^fold query heads of a KV head share a slot's 128 rows: row r is head r % 2^fold of query
+  // r / 2^fold
+  int fold;
 };
 
 // 2^x on the MUFU unit (one instruction; -inf gives +0).
@@ -160,26 +166,26 @@ struct Slot {
 struct Item {
   Slot sl[kSlots];
   int b, kv_row, off, kv_lo, kv_hi, n_keys, t0, n_tiles;
-  int kvh, T;  // the KV head, the sequence's queries
+  int kvh, T, tq;  // the KV head, the sequence's queries, a slot's queries
 };
 
 // Item id, heaviest first: the far query tiles (more keys) get the small ids. Reads
-// the cache positions and key ranges, so it runs after pdl_wait.
-template <bool PACKED>
-__device__ __forceinline__ Item item_of(const AttnParams& p, int id) {
+// the cache positions and key ranges, so it runs after pdl_wait. PACKED: of work entry `w`.
+template <bool PACKED, bool SPLIT>
+__device__ __forceinline__ Item item_of(const AttnParams& p, int id, const PackedWork& w) {
   Item it;
   it.T = p.T;
+  it.tq = kBQ;
   if constexpr (PACKED) {
-    const int units = p.head_pairs ? p.H / 2 : p.H;  // items of one work entry
-    const PackedWork w = p.work[id / units];
-    const int r = id % units;
+    const int h = (id % (p.H >> p.fold)) << p.fold;
+    it.tq = kBQ >> p.fold;
     it.T = w.len;
     it.b = w.row0;
 #pragma unroll
     for (int g = 0; g < kSlots; ++g) {
-      const int qt = p.head_pairs ? w.tile : 2 * w.tile + g;
-      const int ok = qt * kBQ < w.len;
-      it.sl[g] = {p.head_pairs ? 2 * r + g : r, ok ? qt : 2 * w.tile, (ok ? qt : 2 * w.tile) * kBQ, ok};
+      const int m0 = SPLIT ? w.query : w.query + g * it.tq;
+      const int ok = m0 < w.len;
+      it.sl[g] = {h, 0, ok ? m0 : w.query, ok};
     }
   } else if (p.head_pairs) {
     const int hp_n = p.H / 2;
@@ -219,7 +225,7 @@ __device__ __forceinline__ Item item_of(const AttnParams& p, int id) {
   int n_keys = 0, first_key = 1 << 30;
 #pragma unroll
   for (int g = 0; g < kSlots; ++g) {
-    const int kv_end = min(it.T, it.sl[g].m0 + kBQ);
+    const int kv_end = min(it.T, it.sl[g].m0 + it.tq);
     n_keys = max(n_keys, min(it.off + kv_end, it.kv_hi));
     first_key = min(first_key, max(it.kv_lo, p.window > 0 ? it.off + it.sl[g].m0 - p.window + 1 : 0));
   }
@@ -238,8 +244,13 @@ __device__ __forceinline__ int item_id(int k, int G, int c) { return k * G + ((k
 // across items, so that the next item's Q, first K/V tiles and first score products
 // overlap the current item's last softmax, PV and output store.
 // PACKED: sequences of different lengths packed into one run of rows (see AttnParams::work);
-// q, k and v are 3-D maps (channel, head, row).
-template <bool F16, bool PACKED>
+// q, k and v are 3-D maps (channel, head, row), and a slot's rows hold the query heads of a KV
+// head side by side (AttnParams::fold): a box of the Q map is 2^fold heads of 128 / 2^fold
+// queries, so that short sequences fill the tile and all rows of it share the K/V tiles.
+// SPLIT: both slots work on the same queries, slot g on the key tiles j % 2 == g through its own
+// K and V stage; slot 0 joins the two results from tensor memory. Twice as many items of half
+// the length, for batches whose items are too few to fill the SMs evenly.
+template <bool F16, bool PACKED, bool SPLIT>
 __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_constant__ AttnParams p) {
   pdl_launch_dependents();
   extern __shared__ uint8_t smem_raw[];
@@ -252,6 +263,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
   // o_done[2], o_free[2], drain[2]
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + 26);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
+  // SPLIT: slot 1's reference and sum of each row, for slot 0, and the barrier that announces them
+  float2* ml1 = reinterpret_cast<float2*>(bars + 32);
+  const uint32_t ml_ready = smem_u32(&bars[28]);
+  static_assert(26 * 8 + 8 <= 28 * 8, "barriers, the TMEM address, the abort flag");
   const uint32_t q_full = smem_u32(&bars[0]);
   const uint32_t q_empty = smem_u32(&bars[1]);
   auto k_full = [&](int s) { return smem_u32(&bars[2 + s]); };
@@ -282,11 +297,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
     mbar_init(q_empty, kSlots);  // one commit from each slot's MMA issuer after its item's last S
     for (int s = 0; s < kKStages; ++s) {
       mbar_init(k_full(s), 1);
-      mbar_init(k_empty(s), kSlots);  // one commit from each slot's MMA issuer
+      mbar_init(k_empty(s), SPLIT ? 1 : kSlots);  // one commit from each slot's MMA issuer
     }
     for (int s = 0; s < kVStages; ++s) {
       mbar_init(v_full(s), 1);
-      mbar_init(v_empty(s), kSlots);
+      mbar_init(v_empty(s), SPLIT ? 1 : kSlots);
     }
     for (int g = 0; g < kSlots; ++g) {
       mbar_init(s_full(g), 1);
@@ -295,6 +310,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
       mbar_init(o_free(g), 128);  // the slot's softmax threads, once they have read O out
       mbar_init(drain(g), 1);
     }
+    if constexpr (SPLIT) mbar_init(ml_ready, 128);
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -311,7 +327,22 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
   __syncthreads();
   tc_fence_after();
   pdl_wait();  // q, k, v (and the cache positions, the key ranges) come from earlier kernels
-  const int n_items = PACKED ? *p.n_work * (p.head_pairs ? p.H / 2 : p.H) : p.n_items;
+  const int units = PACKED ? p.H >> p.fold : 1;  // items of a work entry
+  const int n_items = PACKED ? *p.n_work * units : p.n_items;
+  // the work entry of this CTA's item k, read a turn ahead of its use
+  auto entry = [&](int k) {
+    PackedWork w{};
+    if constexpr (PACKED) {
+      const int id = item_id(k, G, cta);
+      if (id < n_items) {
+        const int4 v = *reinterpret_cast<const int4*>(p.work + id / units);
+        w = {v.x, v.y, v.z, v.w};
+      }
+    }
+    return w;
+  };
+  // this slot's share of an item's key tiles
+  auto my_tiles = [&](const Item& it, int g) { return SPLIT ? (it.n_tiles + 1 - g) / 2 : it.n_tiles; };
   const uint32_t tmem = *tmem_holder;  // S[g] (and P[g] over its first 64 columns): cols 128 g; O[g]: 256 + 128 g
   // What the producer lanes and the MMA lanes have in flight, for the drain after an
   // abort: the ring stages issued (with the parity of their last phase), the last Q
@@ -324,18 +355,21 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
       // ---------------- TMA producer: each item's Q, then its K tiles through the ring
       bool failed = false;
       int J = 0;  // K tiles issued over all items
+      uint32_t used = 0;  // SPLIT: the parity of each stage's next phase
+      PackedWork ahead = entry(0);
       for (int k = 0; !failed; ++k) {
         const int id = item_id(k, G, cta);
         if (id >= n_items) break;
-        const Item it = item_of<PACKED>(p, id);
+        const Item it = item_of<PACKED, SPLIT>(p, id, ahead);
+        ahead = entry(k + 1);
         // the Q buffer is free once both slots' score products of the previous item are done
         if (!mbar_wait(q_empty, (k & 1) ^ 1, budget, abort_flag)) {
           failed = true;
           break;
         }
-        mbar_arrive_expect_tx(q_full, kSlots * kQBytes);
+        mbar_arrive_expect_tx(q_full, (SPLIT ? 1 : kSlots) * kQBytes);
 #pragma unroll
-        for (int g = 0; g < kSlots; ++g) {
+        for (int g = 0; g < (SPLIT ? 1 : kSlots); ++g) {
           const int q_row = PACKED ? it.b + it.sl[g].m0 : (it.b * p.H + it.sl[g].h) * p.T + it.sl[g].m0;
           load_half(smem_u32(sQ + g * kQBytes), &p.tq, 0, it.sl[g].h, q_row, q_full);
           load_half(smem_u32(sQ + g * kQBytes + kQSub), &p.tq, 1, it.sl[g].h, q_row, q_full);
@@ -343,8 +377,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
         q_issued = true;
         q_parity = k & 1;
         for (int j = 0; j < it.n_tiles; ++j, ++J) {
-          const int s = J % kKStages;
-          const uint32_t ph = (J / kKStages) & 1;
+          const int s = SPLIT ? j & 1 : J % kKStages;
+          const uint32_t ph = SPLIT ? (used >> s) & 1 : (J / kKStages) & 1;
+          if constexpr (SPLIT) used ^= 1u << s;
           if (!mbar_wait(k_empty(s), ph ^ 1, budget, abort_flag)) {
             failed = true;
             break;
@@ -365,13 +400,17 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
       // ---------------- TMA producer: the V ring (its own thread, so that K never waits behind V)
       bool failed = false;
       int J = 0;
+      uint32_t used = 0;
+      PackedWork ahead = entry(0);
       for (int k = 0; !failed; ++k) {
         const int id = item_id(k, G, cta);
         if (id >= n_items) break;
-        const Item it = item_of<PACKED>(p, id);
+        const Item it = item_of<PACKED, SPLIT>(p, id, ahead);
+        ahead = entry(k + 1);
         for (int j = 0; j < it.n_tiles; ++j, ++J) {
-          const int s = J % kVStages;
-          const uint32_t ph = (J / kVStages) & 1;
+          const int s = SPLIT ? j & 1 : J % kVStages;
+          const uint32_t ph = SPLIT ? (used >> s) & 1 : (J / kVStages) & 1;
+          if constexpr (SPLIT) used ^= 1u << s;
           if (!mbar_wait(v_empty(s), ph ^ 1, budget, abort_flag)) {
             failed = true;
             break;
@@ -402,7 +441,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
       // Shared-memory descriptors, built once: a descriptor's start-address field counts
       // 16-byte units, so K step kk of a 128-byte-swizzled operand sits (kk / 4) halves of
       // 16 KB and (kk % 4) 32-byte steps further; V's 16-key steps are 2 KB apart.
-      const uint64_t dq = smem_desc_sw128(smem_u32(sQ + g * kQBytes));
+      const uint64_t dq = smem_desc_sw128(smem_u32(sQ + (SPLIT ? 0 : g) * kQBytes));
       uint64_t dk[kKStages], dv[kVStages];
 #pragma unroll
       for (int st = 0; st < kKStages; ++st) dk[st] = smem_desc_sw128(smem_u32(sK + st * kKVBytes));
@@ -410,8 +449,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
       for (int st = 0; st < kVStages; ++st) dv[st] = smem_desc_sw128_mn(smem_u32(sV + st * kKVBytes), kKVSub, 1024);
       auto kstep = [](int kk) { return (uint64_t)((kk >> 2) * (kQSub >> 4) + (kk & 3) * 2); };
       const uint32_t s_tmem = tmem + g * kBK, o_tmem = tmem + 256 + g * kD;
-      auto issue_s = [&](int J) {  // S of global tile J (K stage J % 2) into the slot's score buffer
-        const int s = J % kKStages;
+      // the ring stage of this slot's tile J (counted over all items) and its phase: the slots share
+      // two stages, or (SPLIT) each has one
+      auto stage_of = [&](int J) { return SPLIT ? g : J % kKStages; };
+      auto phase_of = [&](int J) { return (uint32_t)(SPLIT ? J & 1 : (J / kKStages) & 1); };
+      auto issue_s = [&](int J) {  // S of global tile J into the slot's score buffer
+        const int s = stage_of(J);
         const uint64_t dks = s == 0 ? dk[0] : dk[1];
 #pragma unroll
         for (int kk = 0; kk < kD / 16; ++kk) tc_mma_bf16(s_tmem, dq + kstep(kk), dks + kstep(kk), idesc_s, kk > 0 ? 1u : 0u);
@@ -421,28 +464,31 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
       };
       bool failed = false;
       int J = 0;  // tiles over all items
+      PackedWork ahead = entry(0);
       for (int k = 0; !failed; ++k) {
         const int id = item_id(k, G, cta);
         if (id >= n_items) break;
-        const Item it = item_of<PACKED>(p, id);
+        const Item it = item_of<PACKED, SPLIT>(p, id, ahead);
+        ahead = entry(k + 1);
         if (!mbar_wait(q_full, k & 1, budget, abort_flag)) {
           failed = true;
           break;
         }
-        if (it.n_tiles > 0) {
-          if (!mbar_wait(k_full(J % kKStages), (J / kKStages) & 1, budget, abort_flag)) {
+        const int n_my = my_tiles(it, g);
+        if (n_my > 0) {
+          if (!mbar_wait(k_full(stage_of(J)), phase_of(J), budget, abort_flag)) {
             failed = true;
             break;
           }
           tc_fence_after();
           issue_s(J);
         }
-        if (it.n_tiles <= 1) tc_commit(q_empty);  // no further score product of this item reads Q
-        for (int j = 0; j < it.n_tiles; ++j, ++J) {
+        if (n_my <= 1) tc_commit(q_empty);  // no further score product of this item reads Q
+        for (int j = 0; j < n_my; ++j, ++J) {
           // PV_j as soon as V_j has landed, O is free (the previous item's output read out)
           // and each quarter of P_j is in tensor memory ...
-          const int vs = J % kVStages;
-          if (!mbar_wait(v_full(vs), (J / kVStages) & 1, budget, abort_flag) ||
+          const int vs = stage_of(J);
+          if (!mbar_wait(v_full(vs), phase_of(J), budget, abort_flag) ||
               (j == 0 && k >= 1 && !mbar_wait(o_free(g), (k - 1) & 1, budget, abort_flag))) {
             failed = true;
             break;
@@ -463,20 +509,20 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
           if (failed) break;
           tc_commit(v_empty(vs));  // this slot is done with the V stage once PV_j is
           // ... then S_{j+1}, which overwrites P_j after PV_j has read it (issue order)
-          if (j + 1 < it.n_tiles) {
-            if (!mbar_wait(k_full((J + 1) % kKStages), ((J + 1) / kKStages) & 1, budget, abort_flag)) {
+          if (j + 1 < n_my) {
+            if (!mbar_wait(k_full(stage_of(J + 1)), phase_of(J + 1), budget, abort_flag)) {
               failed = true;
               break;
             }
             tc_fence_after();
             issue_s(J + 1);
-            if (j + 2 == it.n_tiles) tc_commit(q_empty);  // that was the item's last score product
+            if (j + 2 == n_my) tc_commit(q_empty);  // that was the item's last score product
           }
         }
         if (failed) break;
         // An item without key tiles has no PV that waited for the previous item's O to be
         // read out: wait here, so that o_done runs at most one phase ahead of its waiter.
-        if (it.n_tiles == 0 && k >= 1 && !mbar_wait(o_free(g), (k - 1) & 1, budget, abort_flag)) {
+        if (n_my == 0 && k >= 1 && !mbar_wait(o_free(g), (k - 1) & 1, budget, abort_flag)) {
           failed = true;
           break;
         }
@@ -497,22 +543,26 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
     const uint32_t o_taddr = tmem + lane_off + 256 + g * kD;
     bool failed = false;
     int J = 0;  // tiles over all items
+    PackedWork ahead = entry(0);
     for (int k = 0; !failed; ++k) {
       const int id = item_id(k, G, cta);
       if (id >= n_items) break;
-      const Item it = item_of<PACKED>(p, id);
+      const Item it = item_of<PACKED, SPLIT>(p, id, ahead);
+      ahead = entry(k + 1);
       const Slot me = g == 0 ? it.sl[0] : it.sl[1];  // a select, not a run-time index into local memory
       const int m0 = me.m0;
-      const int qi = m0 + r;
+      const int qi = m0 + (PACKED ? r >> p.fold : r);
+      const int head = PACKED ? me.h + (r & ((1 << p.fold) - 1)) : me.h;
+      const int n_my = my_tiles(it, g);
       const int qc = min(qi, it.T - 1);
       const int off = it.off, kv_lo = it.kv_lo, kv_hi = it.kv_hi, n_keys = it.n_keys;
       float m_ref = -INFINITY, l = 0.f;
-      for (int j = 0; j < it.n_tiles; ++j, ++J) {
+      for (int j = 0; j < n_my; ++j, ++J) {
         // The slots take turns (slot 0 tile J, slot 1 tile J, slot 0 tile J + 1, ...): each
         // softmax runs alone on the SM's exponential units while the tensor core works on
         // the other slot's PV and next scores. Slot 1 starts tile J once slot 0's P_J is
-        // written, slot 0 starts tile J + 1 once slot 1's P_J is.
-        if (g == 1 || J >= 1) {
+        // written, slot 0 starts tile J + 1 once slot 1's P_J is. (SPLIT: they run at their own pace.)
+        if (!SPLIT && (g == 1 || J >= 1)) {
           if (!__all_sync(0xffffffffu, mbar_wait(p_ready(1 - g, 3), (g == 1 ? J : J - 1) & 1, budget, abort_flag))) {
             failed = true;
             break;
@@ -530,11 +580,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
 #pragma unroll
         for (int c = 0; c < kBK; c += 16) tmem_ld16(s_taddr + c, *reinterpret_cast<float(*)[16]>(&x[c]));
         tc_wait_ld();
-        const int n0 = (it.t0 + j) * kBK;
+        const int n0 = (it.t0 + (SPLIT ? 2 * j + g : j)) * kBK;
         // raw scores: masked entries become -inf (tiles on the diagonal, past the last key,
         // before the first visible key, or before the window)
         if ((n0 + kBK - 1 > off + m0) || (n0 + kBK > kv_hi) || n0 < kv_lo ||
-            (p.window > 0 && n0 < off + min(m0 + kBQ - 1, it.T - 1) - p.window + 1)) {
+            (p.window > 0 && n0 < off + min(m0 + it.tq - 1, it.T - 1) - p.window + 1)) {
           const int causal = off + qc - n0;                    // keys n0 + c with c <= causal are not ahead
           const int lim = min(causal, kv_hi - 1 - n0);         // ... nor padding after the run
           const int first = max(p.window > 0 ? causal - p.window + 1 : -kBK, kv_lo - n0);  // c >= first
@@ -574,8 +624,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
           // so that P = 0 meets finite values, once the tile has landed. Both slots write the
           // same zeros, each before its own p_ready (the fence below), as either slot's PV
           // may run first
-          const int vs = J % kVStages;
-          if (!__all_sync(0xffffffffu, mbar_wait(v_full(vs), (J / kVStages) & 1, budget, abort_flag))) {
+          const int vs = SPLIT ? g : J % kVStages;
+          if (!__all_sync(0xffffffffu, mbar_wait(v_full(vs), SPLIT ? J & 1 : (J / kVStages) & 1, budget, abort_flag))) {
             failed = true;
             break;
           }
@@ -631,9 +681,29 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
       }
       __syncwarp();
       tc_fence_after();
+      float w0 = 1.f, w1 = 0.f;  // SPLIT: the weights of the slots' outputs
+      if constexpr (SPLIT) {
+        if (g == 1) {  // slot 0 stores, and frees O_1 once it has read it
+          ml1[r] = make_float2(m_ref, l);
+          tc_fence_before();
+          mbar_arrive(ml_ready);
+          continue;
+        }
+        if (!__all_sync(0xffffffffu, mbar_wait(ml_ready, k & 1, budget, abort_flag))) {
+          failed = true;
+          break;
+        }
+        __syncwarp();
+        tc_fence_after();
+        const float2 o1 = ml1[r];
+        const float m = fmaxf(m_ref, o1.x), mu = m == -INFINITY ? 0.f : m;
+        w0 = ex2_approx(m_ref - mu);
+        w1 = ex2_approx(o1.x - mu);
+        l = l * w0 + o1.y * w1;
+      }
       const bool seen = l > 0.f;  // false: a padding query that sees no key (its output is 0)
       const float inv = seen ? 1.f / l : 0.f;
-      const size_t orow_i = PACKED ? (size_t)(it.b + qi) * p.o_row + (size_t)me.h * p.o_head
+      const size_t orow_i = PACKED ? (size_t)(it.b + qi) * p.o_row + (size_t)head * p.o_head
                                    : (((size_t)it.b * p.T + qi) * p.H + me.h) * kD;
       uint16_t* orow = static_cast<uint16_t*>(p.o) + orow_i;
       const bool of16 = p.o_f16 != 0;
@@ -649,6 +719,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
         float ov[16];
         tmem_ld16(o_taddr + c, ov);
         tc_wait_ld();
+        if (SPLIT && it.n_tiles > 1) {  // O_1 (128 columns on) holds something
+          float o1[16];
+          tmem_ld16(o_taddr + kD + c, o1);
+          tc_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 16; ++i) ov[i] = ov[i] * w0 + o1[i] * w1;
+        }
         if (store) {
 #pragma unroll
           for (int i = 0; i < 16; ++i) ov[i] = seen ? ov[i] * inv : 0.f;
@@ -676,6 +753,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
       }
       tc_fence_before();
       mbar_arrive(o_free(g));  // O is read out: the next item's first PV may overwrite it
+      if constexpr (SPLIT) mbar_arrive(o_free(1));
     }
     if (failed) {
       *abort_flag = 1;
@@ -755,8 +833,8 @@ cudaError_t launch_attn_prefill_tc(const void* q, const void* k, const void* v, 
   p.status = st;
   p.wait_ns = wait_ns;
   static std::atomic<unsigned long long> configured[2];  // per instantiation, one bit per device
-  cudaError_t ce = f16 ? set_smem_limit_once(reinterpret_cast<const void*>(attn_tc_kernel<true, false>), kSmem, configured[1])
-                       : set_smem_limit_once(reinterpret_cast<const void*>(attn_tc_kernel<false, false>), kSmem, configured[0]);
+  cudaError_t ce = f16 ? set_smem_limit_once(reinterpret_cast<const void*>(attn_tc_kernel<true, false, false>), kSmem, configured[1])
+                       : set_smem_limit_once(reinterpret_cast<const void*>(attn_tc_kernel<false, false, false>), kSmem, configured[0]);
   if (ce != cudaSuccess) return ce;
   // persistent: one CTA per SM (at most one per item) walks the items
   int dev = 0, sms = 0;
@@ -765,9 +843,9 @@ cudaError_t launch_attn_prefill_tc(const void* q, const void* k, const void* v, 
   if (ce != cudaSuccess) return ce;
   const int grid = std::min(p.n_items, sms);
   if (f16)
-    launch_pdl(attn_tc_kernel<true, false>, grid, kThreads, kSmem, s, p);
+    launch_pdl(attn_tc_kernel<true, false, false>, grid, kThreads, kSmem, s, p);
   else
-    launch_pdl(attn_tc_kernel<false, false>, grid, kThreads, kSmem, s, p);
+    launch_pdl(attn_tc_kernel<false, false, false>, grid, kThreads, kSmem, s, p);
   return cudaGetLastError();
 }
 
@@ -779,8 +857,7 @@ constexpr int kPlanThreads = 1024;
 constexpr int kPlanBins = 4096;
 constexpr int kStatusInvalidArg = 1;  // == BLK_ERR_INVALID_ARG
 
-// The work list of packed sequences, heaviest first: an entry per query tile (or pair of
-// tiles) of `step` queries, ordered by its place in its sequence, which its key count grows
+// The work list of packed sequences, heaviest first: an entry per `step` queries, ordered by its place in its sequence, which its key count grows
 // with. One CTA counts the entries of each place, sums the counts from the far places
 // down, and deals the entries out; the order within a place does not matter (items are
 // independent, so no result depends on it). A cu that does not rise from 0 to at most
@@ -806,7 +883,7 @@ __global__ void __launch_bounds__(kPlanThreads) packed_plan_kernel(const int* __
       const int n = (hi - lo + step - 1) / step;
       for (int t = lane; t < n; t += 32) {
         const int at = atomicAdd(&count[t / per_bin], 1);
-        if (pass == 1 && at < cap) work[at] = {lo, hi - lo, t, 0};
+        if (pass == 1 && at < cap) work[at] = {lo, hi - lo, t * step, 0};
       }
     }
     __syncthreads();
@@ -842,13 +919,16 @@ __global__ void __launch_bounds__(kPlanThreads) packed_plan_kernel(const int* __
   if (bad && st) atomicCAS(&st->code, 0, kStatusInvalidArg);
 }
 
-int packed_work_cap(int rows, int B) { return rows / kBQ + B; }
+// Entries of at least 8 queries (16 heads folded, split).
+int packed_work_cap(int rows, int B, int step) { return rows / step + B; }
+constexpr int kMinStep = kBQ / 16;
+constexpr int kSplitBelow = 3;       // items per SM
 constexpr size_t kPackedHead = 256;  // bytes before the work list: its length
 
 }  // namespace
 
 size_t attn_packed_ws_bytes(int rows, int B) {
-  return kPackedHead + (size_t)packed_work_cap(rows, B) * sizeof(PackedWork);
+  return kPackedHead + (size_t)packed_work_cap(rows, B, kMinStep) * sizeof(PackedWork);
 }
 
 cudaError_t launch_attn_packed(const HeadRows& q, const HeadRows& k, const HeadRows& v, const HeadRows& o, int rows,
@@ -861,8 +941,12 @@ cudaError_t launch_attn_packed(const HeadRows& q, const HeadRows& k, const HeadR
   if (B <= 0 || rows <= 0) return cudaSuccess;
   AttnParams p;
   memset(static_cast<void*>(&p), 0, sizeof(p));
-  if (!make_tma_heads_bf16(&p.tq, q, rows, H, kD, kBQ) || !make_tma_heads_bf16(&p.tk, k, rows, Hkv, kD, kBK) ||
-      !make_tma_heads_bf16(&p.tv, v, rows, Hkv, kD, kBK)) {
+  while (p.fold < 4 && (H / Hkv) % (2 << p.fold) == 0) ++p.fold;
+  const int tq = kBQ >> p.fold, units = H >> p.fold;
+  // Two query tiles an item while that gives every SM enough of them to even out; else split.
+  const bool split = (long long)packed_work_cap(rows, B, 2 * tq) * units < kSplitBelow * num_sms;
+  if (!make_tma_heads_bf16(&p.tq, q, rows, H, kD, 1 << p.fold, tq) ||
+      !make_tma_heads_bf16(&p.tk, k, rows, Hkv, kD, 1, kBK) || !make_tma_heads_bf16(&p.tv, v, rows, Hkv, kD, 1, kBK)) {
     *why = "cuTensorMapEncodeTiled failed for q/k/v";
     return cudaErrorInvalidValue;
   }
@@ -874,23 +958,21 @@ cudaError_t launch_attn_packed(const HeadRows& q, const HeadRows& k, const HeadR
   p.Hkv = Hkv;
   p.T = rows;
   p.window = window > 0 ? window : 0;
-  p.head_pairs = (H / Hkv) % 2 == 0 ? 1 : 0;
   p.sl2 = kLog2e / sqrtf((float)kD);
   p.status = st;
   p.wait_ns = wait_ns;
   p.n_work = static_cast<int*>(ws);
   PackedWork* work = reinterpret_cast<PackedWork*>(static_cast<uint8_t*>(ws) + kPackedHead);
   p.work = work;
-  static std::atomic<unsigned long long> configured{0};
-  cudaError_t e = set_smem_limit_once(reinterpret_cast<const void*>(attn_tc_kernel<false, true>), kSmem, configured);
+  const auto kernel = split ? attn_tc_kernel<false, true, true> : attn_tc_kernel<false, true, false>;
+  const int smem = split ? kSmemSplit : kSmem;
+  static std::atomic<unsigned long long> configured[2];
+  cudaError_t e = set_smem_limit_once(reinterpret_cast<const void*>(kernel), smem, configured[split]);
   if (e != cudaSuccess) return e;
-  const int cap = packed_work_cap(rows, B);
-  e = launch_pdl(packed_plan_kernel, 1, kPlanThreads, 0, s, cu, B, rows, p.head_pairs ? kBQ : 2 * kBQ, cap, work,
-                 static_cast<int*>(ws), st);
+  const int step = split ? tq : 2 * tq, cap = packed_work_cap(rows, B, step);
+  e = launch_pdl(packed_plan_kernel, 1, kPlanThreads, 0, s, cu, B, rows, step, cap, work, static_cast<int*>(ws), st);
   if (e != cudaSuccess) return e;
-  const long long most = (long long)cap * (p.head_pairs ? H / 2 : H);
-  return launch_pdl(attn_tc_kernel<false, true>, dim3((unsigned)std::min<long long>(most, num_sms)), kThreads, kSmem, s,
-                    p);
+  return launch_pdl(kernel, dim3((unsigned)std::min<long long>((long long)cap * units, num_sms)), kThreads, smem, s, p);
 }
 
 }  // namespace blk

@@ -277,12 +277,25 @@ def test_attn_packed_layouts():
 
 
 def test_attn_packed_one_sequence_is_the_prefill_stage():
-    n = 333
-    blk = block(4, 2)
-    q, k, v = randn(1, n, 4, D), randn(2, n, 2, D), randn(3, n, 2, D)
-    o = torch.empty(1, n, 4, D, dtype=torch.bfloat16, device=DEV)
+    """With enough query tiles to fill the GPU the keys of a tile are not split, and every row
+    goes through the same products in the same order as in the prefill stage."""
+    n, H, Hkv = 4000, 32, 8
+    blk = block(H, Hkv)
+    q, k, v = randn(1, n, H, D), randn(2, n, Hkv, D), randn(3, n, Hkv, D)
+    o = torch.empty(1, n, H, D, dtype=torch.bfloat16, device=DEV)
     blk.attn_gqa(*[x.transpose(0, 1).contiguous()[None] for x in (q, k, v)], o)
     assert torch.equal(blk.attn_packed(q, k, v, ints([0, n])), o[0])
+
+
+@pytest.mark.parametrize("H,Hkv,window", [(32, 8, 0), (16, 16, 0), (12, 2, 0), (32, 2, 300), (20, 4, 0), (16, 1, 0)])
+def test_attn_packed_many_tiles(H, Hkv, window):
+    """Batches large enough for two query tiles an item (keys not split), ragged and with single tokens."""
+    lens = [1400, 1, 700, 0, 129, 2, 1, 900, 333, 1, 64]
+    n = sum(lens)
+    blk = block(H, Hkv, sliding_window=window)
+    q, k, v = randn(1, n, H, D), randn(2, n, Hkv, D), randn(3, n, Hkv, D)
+    check_packed(blk.attn_packed(q, k, v, cu_of(lens)), q, k, v, lens, window=window)
+    assert blk.last_status() == 0
 
 
 def test_attn_packed_bad_sequences_are_clamped():
