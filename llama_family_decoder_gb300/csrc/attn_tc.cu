@@ -40,6 +40,7 @@
 #include <cuda_fp16.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "common.cuh"
 #include "kernels.h"
@@ -53,6 +54,12 @@ constexpr int kBQ = 128;                    // queries per slot (MMA M)
 constexpr int kBK = 128;                    // keys per tile
 constexpr int kSlots = 2;
 constexpr int kThreads = 64 + kSlots * 128 + 32;  // + warp 10: the second slot's MMA issuer
+// Packed sequences: 12 warps, the softmax in warps 0..7 (two whole warpgroups), then the TMA
+// producers, the two MMA issuers and an idle warp, so that registers can move from the last
+// warpgroup to the first two, whose scores (128 a thread) and addresses do not fit 168.
+constexpr int kPackedThreads = 384;
+constexpr int kLaunchRegs = 168, kSoftmaxRegs = 200, kControlRegs = 96;
+static_assert(2 * kSoftmaxRegs + kControlRegs <= 3 * kLaunchRegs, "the registers the block is launched with");
 constexpr int kQSub = kBQ * 128;            // one 64-column half of a Q tile (bytes)
 constexpr int kQBytes = 2 * kQSub;          // 128 queries x 128 dims
 constexpr int kKVSub = kBK * 128;           // one 64-column half of a K or V tile
@@ -102,6 +109,7 @@ struct AttnParams {
   // 2^fold query heads of a KV head share a slot's 128 rows: row r is head r % 2^fold of query
   // r / 2^fold
   int fold;
+  int o_wide;  // the output's rows start on 32-byte boundaries
 };
 
 // 2^x on the MUFU unit (one instruction; -inf gives +0).
@@ -156,6 +164,14 @@ __device__ __forceinline__ void tc_mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint
       "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
       "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
       : "memory");
+}
+
+// 32 bytes in one store (a 32-byte boundary): a warp's stores of 32 separate rows are bound by
+// the rows they touch, so half as many instructions take half the time.
+__device__ __forceinline__ void st_global_32(void* p, const uint4& a, const uint4& b) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(a.x), "r"(a.y), "r"(a.z),
+               "r"(a.w), "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w)
+               : "memory");
 }
 
 struct Slot {
@@ -251,7 +267,7 @@ __device__ __forceinline__ int item_id(int k, int G, int c) { return k * G + ((k
 // K and V stage; slot 0 joins the two results from tensor memory. Twice as many items of half
 // the length, for batches whose items are too few to fill the SMs evenly.
 template <bool F16, bool PACKED, bool SPLIT>
-__global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_constant__ AttnParams p) {
+__global__ void __launch_bounds__(PACKED ? kPackedThreads : kThreads, 1) attn_tc_kernel(const __grid_constant__ AttnParams p) {
   pdl_launch_dependents();
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -281,7 +297,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
   auto o_free = [&](int g) { return smem_u32(&bars[22 + g]); };
   auto drain = [&](int g) { return smem_u32(&bars[24 + g]); };
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // warp: its role, 0 TMA, 1 and 10 MMA, 2..9 softmax (11 none)
+  const int pw = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = !PACKED ? pw : pw < 8 ? pw + 2 : pw == 8 ? 0 : pw == 9 ? 1 : pw;
   const unsigned long long budget = p.wait_ns;
   const int G = gridDim.x, cta = blockIdx.x;
   // one 64-channel half of a Q (or K, V) tile: rows from `row` of a head
@@ -341,6 +359,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
     }
     return w;
   };
+  // the ring stage of slot g's tile J (counted over all items) and its phase: the slots share two
+  // stages, or (SPLIT) each has one
+  auto stage_of = [](int J, int g) { return SPLIT ? g : J % kKStages; };
+  auto phase_of = [](int J) { return (uint32_t)(SPLIT ? J & 1 : (J / kKStages) & 1); };
+  // quarters (32 keys) of the tile at key n0 that some query of the slot at m0 sees, at least one
+  auto quarters = [](const Item& it, int m0, int n0) {
+    return min(4, max(1, (min(it.T, m0 + it.tq) - n0 + 31) >> 5));
+  };
   // this slot's share of an item's key tiles
   auto my_tiles = [&](const Item& it, int g) { return SPLIT ? (it.n_tiles + 1 - g) / 2 : it.n_tiles; };
   const uint32_t tmem = *tmem_holder;  // S[g] (and P[g] over its first 64 columns): cols 128 g; O[g]: 256 + 128 g
@@ -350,6 +376,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
   uint32_t issued = 0, parity = 0, q_parity = 0;
   bool q_issued = false, mma_issued = false;
 
+  if (warp < 2 || warp >= 10) {
+  if constexpr (PACKED) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kControlRegs));
   if (warp == 0) {
     if (lane == 0) {
       // ---------------- TMA producer: each item's Q, then its K tiles through the ring
@@ -428,7 +456,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
         report_timeout(p.status, 0x20 + 3);
       }
     }
-  } else if (warp == 1 || warp == kThreads / 32 - 1) {
+  } else if (warp == 1 || warp == 10) {
     if (lane == 0) {
       // ---------------- MMA issuer of slot g (warp 1: slot 0, the last warp: slot 1). Each
       // slot has its own issuing thread, so that a slot whose P is ready never waits
@@ -449,12 +477,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
       for (int st = 0; st < kVStages; ++st) dv[st] = smem_desc_sw128_mn(smem_u32(sV + st * kKVBytes), kKVSub, 1024);
       auto kstep = [](int kk) { return (uint64_t)((kk >> 2) * (kQSub >> 4) + (kk & 3) * 2); };
       const uint32_t s_tmem = tmem + g * kBK, o_tmem = tmem + 256 + g * kD;
-      // the ring stage of this slot's tile J (counted over all items) and its phase: the slots share
-      // two stages, or (SPLIT) each has one
-      auto stage_of = [&](int J) { return SPLIT ? g : J % kKStages; };
-      auto phase_of = [&](int J) { return (uint32_t)(SPLIT ? J & 1 : (J / kKStages) & 1); };
       auto issue_s = [&](int J) {  // S of global tile J into the slot's score buffer
-        const int s = stage_of(J);
+        const int s = stage_of(J, g);
         const uint64_t dks = s == 0 ? dk[0] : dk[1];
 #pragma unroll
         for (int kk = 0; kk < kD / 16; ++kk) tc_mma_bf16(s_tmem, dq + kstep(kk), dks + kstep(kk), idesc_s, kk > 0 ? 1u : 0u);
@@ -475,8 +499,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
           break;
         }
         const int n_my = my_tiles(it, g);
+        const int m0 = g == 0 ? it.sl[0].m0 : it.sl[1].m0;  // a select, not a run-time index into local memory
         if (n_my > 0) {
-          if (!mbar_wait(k_full(stage_of(J)), phase_of(J), budget, abort_flag)) {
+          if (!mbar_wait(k_full(stage_of(J, g)), phase_of(J), budget, abort_flag)) {
             failed = true;
             break;
           }
@@ -485,32 +510,40 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
         }
         if (n_my <= 1) tc_commit(q_empty);  // no further score product of this item reads Q
         for (int j = 0; j < n_my; ++j, ++J) {
+          const int nq = PACKED ? quarters(it, m0, (it.t0 + (SPLIT ? 2 * j + g : j)) * kBK) : 4;
           // PV_j as soon as V_j has landed, O is free (the previous item's output read out)
           // and each quarter of P_j is in tensor memory ...
-          const int vs = stage_of(J);
+          const int vs = stage_of(J, g);
           if (!mbar_wait(v_full(vs), phase_of(J), budget, abort_flag) ||
               (j == 0 && k >= 1 && !mbar_wait(o_free(g), (k - 1) & 1, budget, abort_flag))) {
             failed = true;
             break;
           }
           const uint64_t dvs = vs == 0 ? dv[0] : dv[1];
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            if (!mbar_wait(p_ready(g, q), J & 1, budget, abort_flag)) {
-              failed = true;
-              break;
-            }
+          auto pv = [&](int q) {  // a quarter's two K = 16 steps once P's quarter is there
+            if (!mbar_wait(p_ready(g, q), J & 1, budget, abort_flag)) return false;
             tc_fence_after();
 #pragma unroll
             for (int kk = 2 * q; kk < 2 * q + 2; ++kk)
               tc_mma_ts(o_tmem, s_tmem + kk * 8, dvs + (uint64_t)(kk * (16 * 128 >> 4)), idesc_pv,
                         (j > 0 || kk > 0) ? 1u : 0u);
+            return true;
+          };
+          if (!PACKED || nq == 4) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              if (!failed && !pv(q)) failed = true;
+          } else {
+            // the softmax still arrives for a quarter left out, before it arrives for the next
+            // tile's first one: no barrier falls a phase behind
+            for (int q = 0; q < nq; ++q)
+              if (!failed && !pv(q)) failed = true;
           }
           if (failed) break;
           tc_commit(v_empty(vs));  // this slot is done with the V stage once PV_j is
           // ... then S_{j+1}, which overwrites P_j after PV_j has read it (issue order)
           if (j + 1 < n_my) {
-            if (!mbar_wait(k_full(stage_of(J + 1)), phase_of(J + 1), budget, abort_flag)) {
+            if (!mbar_wait(k_full(stage_of(J + 1, g)), phase_of(J + 1), budget, abort_flag)) {
               failed = true;
               break;
             }
@@ -533,10 +566,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
         report_timeout(p.status, 0x20 + 1);
       }
     }
+  }
   } else {
+    if constexpr (PACKED) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
     // ---------------- softmax / correction / epilogue: slot g, one query row per thread
     const int g = (warp - 2) / 4;
-    const int quarter = warp & 3;
+    const int quarter = pw & 3;  // the tensor-memory lanes a warp can reach
     const int r = quarter * 32 + lane;
     const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
     const uint32_t s_taddr = tmem + lane_off + g * kBK;
@@ -557,7 +592,93 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
       const int qc = min(qi, it.T - 1);
       const int off = it.off, kv_lo = it.kv_lo, kv_hi = it.kv_hi, n_keys = it.n_keys;
       float m_ref = -INFINITY, l = 0.f;
+      // whether any of this warp's rows is a query (packed sequences)
+      const bool live = me.valid && (!PACKED || m0 + ((quarter * 32) >> p.fold) < it.T);
+      // tiles that start in [plain_lo, plain_hi] have no masked score
+      const int plain_lo = p.window > 0 ? min(m0 + it.tq - 1, it.T - 1) - p.window + 1 : 0;
+      const int plain_hi = live ? min(m0 + 1, it.T) - kBK : -1;
+      // Moves the row's reference up to mt where a score passes it by 2^8; PV_{J-1} is done (S_J is
+      // ready), so this warp's O rows can be rescaled. Returns the factor.
+      auto rescale = [&](float mt, int j) {
+        const bool need = mt > m_ref + kRescaleLog2;
+        const bool any = __any_sync(0xffffffffu, need);
+        float alpha = 1.f;
+        if (need) {
+          alpha = ex2_approx(m_ref - mt);
+          m_ref = mt;
+        }
+        if (j >= 1 && any) {
+#pragma unroll 1
+          for (int c = 0; c < kD; c += 16) {
+            float ov[16];
+            tmem_ld16(o_taddr + c, ov);
+            tc_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 16; ++i) ov[i] *= alpha;
+            tmem_st16(o_taddr + c, ov);
+          }
+        }
+        return alpha;
+      };
+      // A masked tile of a packed sequence: keys n0 + c are seen for c in [first, lim]. Quarter by
+      // quarter of 32 keys, each read twice from tensor memory (cheap) instead of held, only the
+      // nq that some row of the slot sees, the mask as bits that select each score. P's quarter
+      // goes to the first 64 columns, over scores that have been read.
+      auto masked_tile = [&](int j, int nq, int lim, int first) {
+        auto scores = [&](int q4, float (&x)[32]) {
+          tmem_ld16(s_taddr + 32 * q4, *reinterpret_cast<float(*)[16]>(&x[0]));
+          tmem_ld16(s_taddr + 32 * q4 + 16, *reinterpret_cast<float(*)[16]>(&x[16]));
+          const int a = lim - 32 * q4, b = first - 32 * q4;
+          const uint32_t bits = (a >= 31 ? ~0u : a < 0 ? 0u : (2u << a) - 1u) & (b <= 0 ? ~0u : b > 31 ? 0u : ~0u << b);
+          tc_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            if (!(bits & (1u << i))) x[i] = -INFINITY;
+        };
+        float mraw = -INFINITY;
+#pragma unroll 1
+        for (int q4 = 0; q4 < nq; ++q4) {
+          float x[32];
+          scores(q4, x);
+          float mx[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) mx[i] = x[i];
+#pragma unroll
+          for (int c = 4; c < 32; c += 2) mx[(c >> 1) & 3] = fmax3(mx[(c >> 1) & 3], x[c], x[c + 1]);
+          mraw = fmaxf(mraw, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
+        }
+        const float alpha = rescale(mraw * p.sl2, j);
+        const float neg_mu = m_ref == -INFINITY ? 0.f : -m_ref;
+        const f32x2 sl2x2 = f2_make(p.sl2, p.sl2), mu2 = f2_make(neg_mu, neg_mu);
+        f32x2 ls2[2] = {f2_make(0.f, 0.f), f2_make(0.f, 0.f)};
+#pragma unroll 1
+        for (int q4 = 0; q4 < nq; ++q4) {
+          float x[32], w[16];
+          scores(q4, x);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            float t0, t1;
+            f2_split(f2_fma(f2_make(x[2 * i], x[2 * i + 1]), sl2x2, mu2), t0, t1);
+            const float p0 = ex2_approx(t0);
+            const float p1 = ex2_approx(t1);
+            ls2[i & 1] = f2_add(ls2[i & 1], f2_make(p0, p1));
+            w[i] = __uint_as_float(pack2(p0, p1, F16));
+          }
+          tmem_st16(s_taddr + q4 * 16, w);
+          tc_wait_st();
+          tc_fence_before();
+          mbar_arrive(p_ready(g, q4));
+        }
+        for (int q4 = nq; q4 < 4; ++q4) mbar_arrive(p_ready(g, q4));
+        float ls[4];
+        f2_split(ls2[0], ls[0], ls[1]);
+        f2_split(ls2[1], ls[2], ls[3]);
+        l = l * alpha + ((ls[0] + ls[1]) + (ls[2] + ls[3]));
+      };
       for (int j = 0; j < n_my; ++j, ++J) {
+        // what needs no score is known before the wait for them
+        const int n0 = (it.t0 + (SPLIT ? 2 * j + g : j)) * kBK;
+        const bool plain = PACKED && n0 >= plain_lo && n0 <= plain_hi;
         // The slots take turns (slot 0 tile J, slot 1 tile J, slot 0 tile J + 1, ...): each
         // softmax runs alone on the SM's exponential units while the tensor core works on
         // the other slot's PV and next scores. Slot 1 starts tile J once slot 0's P_J is
@@ -576,15 +697,44 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
         }
         __syncwarp();
         tc_fence_after();
+        if (PACKED && !plain) {
+          const int nq = quarters(it, m0, n0);
+          if (n0 + kBK > n_keys && nq * 32 > n_keys - n0) {
+            // V rows behind the sequence belong to another one, or to none: zero those that P = 0
+            // will meet (see below). The 8 chunks of a row in an order that starts at the row's
+            // number: eight neighbouring rows' stores go to all banks.
+            const int vs = stage_of(J, g);
+            if (!__all_sync(0xffffffffu, mbar_wait(v_full(vs), phase_of(J), budget, abort_flag))) {
+              failed = true;
+              break;
+            }
+            if (r >= n_keys - n0 && r < nq * 32) {
+              uint8_t* vrow = sV + vs * kKVBytes + r * 128;
+#pragma unroll
+              for (int c = 0; c < 8; ++c)
+#pragma unroll
+                for (int hb = 0; hb < 2; ++hb)
+                  *reinterpret_cast<uint4*>(vrow + hb * kKVSub + ((c + r) & 7) * 16) = make_uint4(0, 0, 0, 0);
+            }
+            fence_proxy_async_smem();
+          }
+          if (!live) {  // nobody reads these rows: whatever the score buffer holds may stand for P
+            tc_fence_before();
+#pragma unroll
+            for (int q = 0; q < 4; ++q) mbar_arrive(p_ready(g, q));
+            continue;
+          }
+          masked_tile(j, nq, qc - n0, p.window > 0 ? qc - n0 - p.window + 1 : -kBK);
+          continue;
+        }
         float x[kBK];
 #pragma unroll
         for (int c = 0; c < kBK; c += 16) tmem_ld16(s_taddr + c, *reinterpret_cast<float(*)[16]>(&x[c]));
         tc_wait_ld();
-        const int n0 = (it.t0 + (SPLIT ? 2 * j + g : j)) * kBK;
         // raw scores: masked entries become -inf (tiles on the diagonal, past the last key,
         // before the first visible key, or before the window)
-        if ((n0 + kBK - 1 > off + m0) || (n0 + kBK > kv_hi) || n0 < kv_lo ||
-            (p.window > 0 && n0 < off + min(m0 + it.tq - 1, it.T - 1) - p.window + 1)) {
+        if (!PACKED && ((n0 + kBK - 1 > off + m0) || (n0 + kBK > kv_hi) || n0 < kv_lo ||
+            (p.window > 0 && n0 < off + min(m0 + it.tq - 1, it.T - 1) - p.window + 1))) {
           const int causal = off + qc - n0;                    // keys n0 + c with c <= causal are not ahead
           const int lim = min(causal, kv_hi - 1 - n0);         // ... nor padding after the run
           const int first = max(p.window > 0 ? causal - p.window + 1 : -kBK, kv_lo - n0);  // c >= first
@@ -619,13 +769,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
             tmem_st16(o_taddr + c, ov);
           }
         }
-        if (n0 + kBK > n_keys) {
+        if (!PACKED && n0 + kBK > n_keys) {
           // V rows past the item's last key may hold anything (unused cache slots): zero them,
           // so that P = 0 meets finite values, once the tile has landed. Both slots write the
           // same zeros, each before its own p_ready (the fence below), as either slot's PV
           // may run first
-          const int vs = SPLIT ? g : J % kVStages;
-          if (!__all_sync(0xffffffffu, mbar_wait(v_full(vs), SPLIT ? J & 1 : (J / kVStages) & 1, budget, abort_flag))) {
+          const int vs = J % kVStages;
+          if (!__all_sync(0xffffffffu, mbar_wait(v_full(vs), (J / kVStages) & 1, budget, abort_flag))) {
             failed = true;
             break;
           }
@@ -701,6 +851,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
         w1 = ex2_approx(o1.x - mu);
         l = l * w0 + o1.y * w1;
       }
+      if (PACKED && !live) {
+        tc_fence_before();
+        mbar_arrive(o_free(g));
+        if constexpr (SPLIT) mbar_arrive(o_free(1));
+        continue;
+      }
       const bool seen = l > 0.f;  // false: a padding query that sees no key (its output is 0)
       const float inv = seen ? 1.f / l : 0.f;
       const size_t orow_i = PACKED ? (size_t)(it.b + qi) * p.o_row + (size_t)head * p.o_head
@@ -730,12 +886,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
 #pragma unroll
           for (int i = 0; i < 16; ++i) ov[i] = seen ? ov[i] * inv : 0.f;
           uint4 w0, w1;
-          if (p.ungated) {  // the head outputs before the gate (bf16)
+          if (!PACKED && p.ungated) {  // the head outputs before the gate (bf16)
             pack16(ov, false, w0, w1);
             reinterpret_cast<uint4*>(p.ungated + orow_i + c)[0] = w0;
             reinterpret_cast<uint4*>(p.ungated + orow_i + c)[1] = w1;
           }
-          if (p.gate) {
+          if (!PACKED && p.gate) {
             const uint4* g4 = reinterpret_cast<const uint4*>(p.gate + orow_i + c);
             const uint4 ga = g4[0], gb = g4[1];
             const uint32_t gw[8] = {ga.x, ga.y, ga.z, ga.w, gb.x, gb.y, gb.z, gb.w};
@@ -747,8 +903,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
             }
           }
           pack16(ov, of16, w0, w1);
-          reinterpret_cast<uint4*>(orow + c)[0] = w0;
-          reinterpret_cast<uint4*>(orow + c)[1] = w1;
+          if (PACKED && p.o_wide) {
+            st_global_32(orow + c, w0, w1);
+          } else {
+            reinterpret_cast<uint4*>(orow + c)[0] = w0;
+            reinterpret_cast<uint4*>(orow + c)[1] = w1;
+          }
         }
       }
       tc_fence_before();
@@ -775,7 +935,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
     } else if (warp == 0 && lane == 1) {
       for (int s = 0; s < kVStages; ++s)
         if (issued & (1u << s)) mbar_wait(v_full(s), (parity >> s) & 1, kDrainNs, &never);
-    } else if ((warp == 1 || warp == kThreads / 32 - 1) && lane == 0 && mma_issued) {
+    } else if ((warp == 1 || warp == 10) && lane == 0 && mma_issued) {
       const int g = warp == 1 ? 0 : 1;
       tc_commit(drain(g));
       mbar_wait(drain(g), 0, kDrainNs, &never);
@@ -953,6 +1113,7 @@ cudaError_t launch_attn_packed(const HeadRows& q, const HeadRows& k, const HeadR
   p.o = o.ptr;
   p.o_row = o.row;
   p.o_head = o.head;
+  p.o_wide = reinterpret_cast<uintptr_t>(o.ptr) % 32 == 0 && (rows == 1 || o.row % 16 == 0) && (H == 1 || o.head % 16 == 0);
   p.B = B;
   p.H = H;
   p.Hkv = Hkv;
@@ -969,10 +1130,19 @@ cudaError_t launch_attn_packed(const HeadRows& q, const HeadRows& k, const HeadR
   static std::atomic<unsigned long long> configured[2];
   cudaError_t e = set_smem_limit_once(reinterpret_cast<const void*>(kernel), smem, configured[split]);
   if (e != cudaSuccess) return e;
+  // the kernel moves registers between its warpgroups: the launch has to bring as many as it
+  // gives out, or the wait for them would not end
+  cudaFuncAttributes fa;
+  e = cudaFuncGetAttributes(&fa, reinterpret_cast<const void*>(kernel));
+  if (e != cudaSuccess) return e;
+  if (fa.numRegs < kLaunchRegs) {
+    *why = "packed attention: the kernel was built with fewer registers than it redistributes";
+    return cudaErrorLaunchOutOfResources;
+  }
   const int step = split ? tq : 2 * tq, cap = packed_work_cap(rows, B, step);
   e = launch_pdl(packed_plan_kernel, 1, kPlanThreads, 0, s, cu, B, rows, step, cap, work, static_cast<int*>(ws), st);
   if (e != cudaSuccess) return e;
-  return launch_pdl(kernel, dim3((unsigned)std::min<long long>((long long)cap * units, num_sms)), kThreads, smem, s, p);
+  return launch_pdl(kernel, dim3((unsigned)std::min<long long>((long long)cap * units, num_sms)), kPackedThreads, smem, s, p);
 }
 
 }  // namespace blk
