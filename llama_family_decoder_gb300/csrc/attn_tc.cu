@@ -54,12 +54,14 @@ constexpr int kBQ = 128;                    // queries per slot (MMA M)
 constexpr int kBK = 128;                    // keys per tile
 constexpr int kSlots = 2;
 constexpr int kThreads = 64 + kSlots * 128 + 32;  // + warp 10: the second slot's MMA issuer
-// Packed sequences: 12 warps, the softmax in warps 0..7 (two whole warpgroups), then the TMA
-// producers, the two MMA issuers and an idle warp, so that registers can move from the last
-// warpgroup to the first two, whose scores (128 a thread) and addresses do not fit 168.
-constexpr int kPackedThreads = 384;
-constexpr int kLaunchRegs = 168, kSoftmaxRegs = 200, kControlRegs = 96;
-static_assert(2 * kSoftmaxRegs + kControlRegs <= 3 * kLaunchRegs, "the registers the block is launched with");
+// Packed sequences: four warpgroups, the softmax in the first two (warps 0..7), then the TMA
+// producers, the two MMA issuers and an idle warp, then the epilogue, which reads an item's
+// outputs out while the softmax is at the next item (with the softmax warps storing, an item
+// boundary took 8500 cycles, two and a half tiles' time). Registers move from the last two to
+// the first two, whose scores (128 a thread) and addresses do not fit 128.
+constexpr int kPackedThreads = 512;
+constexpr int kLaunchRegs = 128, kSoftmaxRegs = 192, kControlRegs = 80, kEpilogueRegs = 48;
+static_assert(2 * kSoftmaxRegs + kControlRegs + kEpilogueRegs <= 4 * kLaunchRegs, "the registers the block is launched with");
 constexpr int kQSub = kBQ * 128;            // one 64-column half of a Q tile (bytes)
 constexpr int kQBytes = 2 * kQSub;          // 128 queries x 128 dims
 constexpr int kKVSub = kBK * 128;           // one 64-column half of a K or V tile
@@ -67,8 +69,8 @@ constexpr int kKVBytes = 2 * kKVSub;        // 128 keys x 128 dims
 constexpr int kKStages = 2;                 // K ring
 constexpr int kVStages = 2;                 // V ring
 constexpr int kSmem = 1024 + kSlots * kQBytes + (kKStages + kVStages) * kKVBytes + 256;
-constexpr int kSmemSplit = kSmem + kBQ * 8;  // + slot 1's softmax states
-static_assert(kSmemSplit <= 227 * 1024, "shared memory");
+constexpr int kSmemPacked = kSmem + kSlots * kBQ * 8;  // + the slots' softmax states of an item
+static_assert(kSmemPacked <= 227 * 1024, "shared memory");
 constexpr float kRescaleLog2 = 8.0f;
 constexpr unsigned long long kDrainNs = 2000000000ULL;
 constexpr float kLog2e = 1.4426950408889634f;
@@ -279,9 +281,10 @@ __global__ void __launch_bounds__(PACKED ? kPackedThreads : kThreads, 1) attn_tc
   // o_done[2], o_free[2], drain[2]
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + 26);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
-  // SPLIT: slot 1's reference and sum of each row, for slot 0, and the barrier that announces them
-  float2* ml1 = reinterpret_cast<float2*>(bars + 32);
-  const uint32_t ml_ready = smem_u32(&bars[28]);
+  // PACKED: each slot's reference and sum of each row, for the epilogue, and the barriers that
+  // announce them
+  float2* ml = reinterpret_cast<float2*>(bars + 32);
+  auto ml_ready = [&](int g) { return smem_u32(&bars[28 + g]); };
   static_assert(26 * 8 + 8 <= 28 * 8, "barriers, the TMEM address, the abort flag");
   const uint32_t q_full = smem_u32(&bars[0]);
   const uint32_t q_empty = smem_u32(&bars[1]);
@@ -297,7 +300,7 @@ __global__ void __launch_bounds__(PACKED ? kPackedThreads : kThreads, 1) attn_tc
   auto o_free = [&](int g) { return smem_u32(&bars[22 + g]); };
   auto drain = [&](int g) { return smem_u32(&bars[24 + g]); };
 
-  // warp: its role, 0 TMA, 1 and 10 MMA, 2..9 softmax (11 none)
+  // warp: its role, 0 TMA, 1 and 10 MMA, 2..9 softmax, 12..15 the epilogue of PACKED (11 none)
   const int pw = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int warp = !PACKED ? pw : pw < 8 ? pw + 2 : pw == 8 ? 0 : pw == 9 ? 1 : pw;
   const unsigned long long budget = p.wait_ns;
@@ -328,7 +331,10 @@ __global__ void __launch_bounds__(PACKED ? kPackedThreads : kThreads, 1) attn_tc
       mbar_init(o_free(g), 128);  // the slot's softmax threads, once they have read O out
       mbar_init(drain(g), 1);
     }
-    if constexpr (SPLIT) mbar_init(ml_ready, 128);
+    if constexpr (PACKED) {
+      mbar_init(ml_ready(0), 128);
+      mbar_init(ml_ready(1), 128);
+    }
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -376,7 +382,87 @@ __global__ void __launch_bounds__(PACKED ? kPackedThreads : kThreads, 1) attn_tc
   uint32_t issued = 0, parity = 0, q_parity = 0;
   bool q_issued = false, mma_issued = false;
 
-  if (warp < 2 || warp >= 10) {
+  if (PACKED && warp >= 12) {
+    if constexpr (PACKED) {
+      // ---------------- epilogue: an item's outputs from tensor memory to their rows
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kEpilogueRegs));
+      const int quarter = pw & 3, r = quarter * 32 + lane;
+      const uint32_t taddr = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + 256;
+      auto ready = [&](int g, int k) {  // O_g is complete and its rows' sums are known
+        const bool ok = mbar_wait(ml_ready(g), k & 1, budget, abort_flag) && mbar_wait(o_done(g), k & 1, budget, abort_flag);
+        return __all_sync(0xffffffffu, ok);
+      };
+      bool failed = false;
+      PackedWork ahead = entry(0);
+      for (int k = 0; !failed; ++k) {
+        const int id = item_id(k, G, cta);
+        if (id >= n_items) break;
+        const Item it = item_of<PACKED, SPLIT>(p, id, ahead);
+        ahead = entry(k + 1);
+#pragma unroll
+        for (int g = 0; g < (SPLIT ? 1 : kSlots); ++g) {
+          if (!ready(g, k) || (SPLIT && !ready(1, k))) {
+            failed = true;
+            break;
+          }
+          __syncwarp();
+          tc_fence_after();
+          const float2 s0 = ml[g * kBQ + r];
+          float w0 = 1.f, w1 = 0.f, l = s0.y;  // the weights of the slots' outputs
+          if constexpr (SPLIT) {
+            const float2 s1 = ml[kBQ + r];
+            const float m = fmaxf(s0.x, s1.x), mu = m == -INFINITY ? 0.f : m;
+            w0 = ex2_approx(s0.x - mu);
+            w1 = ex2_approx(s1.x - mu);
+            l = s0.y * w0 + s1.y * w1;
+          }
+          const bool seen = l > 0.f;
+          const float inv = seen ? 1.f / l : 0.f;
+          w0 *= inv;
+          w1 *= inv;
+          const int query = it.sl[g].m0 + (r >> p.fold), h = it.sl[g].h + (r & ((1 << p.fold) - 1));
+          const bool store = it.sl[g].valid && query < it.T;
+          uint16_t* const o = static_cast<uint16_t*>(p.o) + (size_t)(it.b + query) * p.o_row + (size_t)h * p.o_head;
+          if (__any_sync(0xffffffffu, store)) {
+#pragma unroll 1
+            for (int c = 0; c < kD; c += 16) {
+              float ov[16];
+              tmem_ld16(taddr + g * kD + c, ov);
+              tc_wait_ld();
+#pragma unroll
+              for (int i = 0; i < 16; ++i) ov[i] = seen ? ov[i] * w0 : 0.f;
+              if (SPLIT && it.n_tiles > 1) {  // O_1 holds something
+                float o1[16];
+                tmem_ld16(taddr + kD + c, o1);
+                tc_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 16; ++i) ov[i] = seen ? fmaf(o1[i], w1, ov[i]) : 0.f;
+              }
+              if (store) {
+                const uint4 a = make_uint4(pack_bf16x2(ov[0], ov[1]), pack_bf16x2(ov[2], ov[3]),
+                                           pack_bf16x2(ov[4], ov[5]), pack_bf16x2(ov[6], ov[7]));
+                const uint4 b = make_uint4(pack_bf16x2(ov[8], ov[9]), pack_bf16x2(ov[10], ov[11]),
+                                           pack_bf16x2(ov[12], ov[13]), pack_bf16x2(ov[14], ov[15]));
+                if (p.o_wide) {
+                  st_global_32(o + c, a, b);
+                } else {
+                  reinterpret_cast<uint4*>(o + c)[0] = a;
+                  reinterpret_cast<uint4*>(o + c)[1] = b;
+                }
+              }
+            }
+          }
+          tc_fence_before();
+          mbar_arrive(o_free(g));  // O is read out: the next item's first PV may overwrite it
+          if constexpr (SPLIT) mbar_arrive(o_free(1));
+        }
+      }
+      if (failed) {
+        *abort_flag = 1;
+        if (lane == 0) report_timeout(p.status, 0x20 + 4);
+      }
+    }
+  } else if (warp < 2 || warp >= 10) {
   if constexpr (PACKED) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kControlRegs));
   if (warp == 0) {
     if (lane == 0) {
@@ -587,7 +673,6 @@ __global__ void __launch_bounds__(PACKED ? kPackedThreads : kThreads, 1) attn_tc
       const Slot me = g == 0 ? it.sl[0] : it.sl[1];  // a select, not a run-time index into local memory
       const int m0 = me.m0;
       const int qi = m0 + (PACKED ? r >> p.fold : r);
-      const int head = PACKED ? me.h + (r & ((1 << p.fold) - 1)) : me.h;
       const int n_my = my_tiles(it, g);
       const int qc = min(qi, it.T - 1);
       const int off = it.off, kv_lo = it.kv_lo, kv_hi = it.kv_hi, n_keys = it.n_keys;
@@ -824,6 +909,16 @@ __global__ void __launch_bounds__(PACKED ? kPackedThreads : kThreads, 1) attn_tc
         l = l * alpha + ((ls[0] + ls[1]) + (ls[2] + ls[3]));
       }
       if (failed) break;
+      if constexpr (PACKED) {
+        // the epilogue takes over; it has read this slot's last states once it frees its O
+        if (k >= 1 && !__all_sync(0xffffffffu, mbar_wait(o_free(g), (k - 1) & 1, budget, abort_flag))) {
+          failed = true;
+          break;
+        }
+        ml[g * kBQ + r] = make_float2(m_ref, l);
+        mbar_arrive(ml_ready(g));
+        continue;
+      }
       // the slot's last PV of this item is complete (every item commits, with tiles or not)
       if (!__all_sync(0xffffffffu, mbar_wait(o_done(g), k & 1, budget, abort_flag))) {
         failed = true;
@@ -831,36 +926,9 @@ __global__ void __launch_bounds__(PACKED ? kPackedThreads : kThreads, 1) attn_tc
       }
       __syncwarp();
       tc_fence_after();
-      float w0 = 1.f, w1 = 0.f;  // SPLIT: the weights of the slots' outputs
-      if constexpr (SPLIT) {
-        if (g == 1) {  // slot 0 stores, and frees O_1 once it has read it
-          ml1[r] = make_float2(m_ref, l);
-          tc_fence_before();
-          mbar_arrive(ml_ready);
-          continue;
-        }
-        if (!__all_sync(0xffffffffu, mbar_wait(ml_ready, k & 1, budget, abort_flag))) {
-          failed = true;
-          break;
-        }
-        __syncwarp();
-        tc_fence_after();
-        const float2 o1 = ml1[r];
-        const float m = fmaxf(m_ref, o1.x), mu = m == -INFINITY ? 0.f : m;
-        w0 = ex2_approx(m_ref - mu);
-        w1 = ex2_approx(o1.x - mu);
-        l = l * w0 + o1.y * w1;
-      }
-      if (PACKED && !live) {
-        tc_fence_before();
-        mbar_arrive(o_free(g));
-        if constexpr (SPLIT) mbar_arrive(o_free(1));
-        continue;
-      }
       const bool seen = l > 0.f;  // false: a padding query that sees no key (its output is 0)
       const float inv = seen ? 1.f / l : 0.f;
-      const size_t orow_i = PACKED ? (size_t)(it.b + qi) * p.o_row + (size_t)head * p.o_head
-                                   : (((size_t)it.b * p.T + qi) * p.H + me.h) * kD;
+      const size_t orow_i = (((size_t)it.b * p.T + qi) * p.H + me.h) * kD;
       uint16_t* orow = static_cast<uint16_t*>(p.o) + orow_i;
       const bool of16 = p.o_f16 != 0;
       const bool store = me.valid && qi < it.T;
@@ -875,23 +943,16 @@ __global__ void __launch_bounds__(PACKED ? kPackedThreads : kThreads, 1) attn_tc
         float ov[16];
         tmem_ld16(o_taddr + c, ov);
         tc_wait_ld();
-        if (SPLIT && it.n_tiles > 1) {  // O_1 (128 columns on) holds something
-          float o1[16];
-          tmem_ld16(o_taddr + kD + c, o1);
-          tc_wait_ld();
-#pragma unroll
-          for (int i = 0; i < 16; ++i) ov[i] = ov[i] * w0 + o1[i] * w1;
-        }
         if (store) {
 #pragma unroll
           for (int i = 0; i < 16; ++i) ov[i] = seen ? ov[i] * inv : 0.f;
           uint4 w0, w1;
-          if (!PACKED && p.ungated) {  // the head outputs before the gate (bf16)
+          if (p.ungated) {  // the head outputs before the gate (bf16)
             pack16(ov, false, w0, w1);
             reinterpret_cast<uint4*>(p.ungated + orow_i + c)[0] = w0;
             reinterpret_cast<uint4*>(p.ungated + orow_i + c)[1] = w1;
           }
-          if (!PACKED && p.gate) {
+          if (p.gate) {
             const uint4* g4 = reinterpret_cast<const uint4*>(p.gate + orow_i + c);
             const uint4 ga = g4[0], gb = g4[1];
             const uint32_t gw[8] = {ga.x, ga.y, ga.z, ga.w, gb.x, gb.y, gb.z, gb.w};
@@ -903,17 +964,12 @@ __global__ void __launch_bounds__(PACKED ? kPackedThreads : kThreads, 1) attn_tc
             }
           }
           pack16(ov, of16, w0, w1);
-          if (PACKED && p.o_wide) {
-            st_global_32(orow + c, w0, w1);
-          } else {
-            reinterpret_cast<uint4*>(orow + c)[0] = w0;
-            reinterpret_cast<uint4*>(orow + c)[1] = w1;
-          }
+          reinterpret_cast<uint4*>(orow + c)[0] = w0;
+          reinterpret_cast<uint4*>(orow + c)[1] = w1;
         }
       }
       tc_fence_before();
       mbar_arrive(o_free(g));  // O is read out: the next item's first PV may overwrite it
-      if constexpr (SPLIT) mbar_arrive(o_free(1));
     }
     if (failed) {
       *abort_flag = 1;
@@ -1126,9 +1182,8 @@ cudaError_t launch_attn_packed(const HeadRows& q, const HeadRows& k, const HeadR
   PackedWork* work = reinterpret_cast<PackedWork*>(static_cast<uint8_t*>(ws) + kPackedHead);
   p.work = work;
   const auto kernel = split ? attn_tc_kernel<false, true, true> : attn_tc_kernel<false, true, false>;
-  const int smem = split ? kSmemSplit : kSmem;
   static std::atomic<unsigned long long> configured[2];
-  cudaError_t e = set_smem_limit_once(reinterpret_cast<const void*>(kernel), smem, configured[split]);
+  cudaError_t e = set_smem_limit_once(reinterpret_cast<const void*>(kernel), kSmemPacked, configured[split]);
   if (e != cudaSuccess) return e;
   // the kernel moves registers between its warpgroups: the launch has to bring as many as it
   // gives out, or the wait for them would not end
@@ -1142,7 +1197,7 @@ cudaError_t launch_attn_packed(const HeadRows& q, const HeadRows& k, const HeadR
   const int step = split ? tq : 2 * tq, cap = packed_work_cap(rows, B, step);
   e = launch_pdl(packed_plan_kernel, 1, kPlanThreads, 0, s, cu, B, rows, step, cap, work, static_cast<int*>(ws), st);
   if (e != cudaSuccess) return e;
-  return launch_pdl(kernel, dim3((unsigned)std::min<long long>((long long)cap * units, num_sms)), kPackedThreads, smem, s, p);
+  return launch_pdl(kernel, dim3((unsigned)std::min<long long>((long long)cap * units, num_sms)), kPackedThreads, kSmemPacked, s, p);
 }
 
 }  // namespace blk
