@@ -60,7 +60,7 @@ constexpr int kThreads = 64 + kSlots * 128 + 32;  // + warp 10: the second slot'
 // boundary took 8500 cycles, two and a half tiles' time). Registers move from the last two to
 // the first two, whose scores (128 a thread) and addresses do not fit 128.
 constexpr int kPackedThreads = 512;
-constexpr int kLaunchRegs = 128, kSoftmaxRegs = 192, kControlRegs = 80, kEpilogueRegs = 48;
+constexpr int kLaunchRegs = 128, kSoftmaxRegs = 184, kControlRegs = 96, kEpilogueRegs = 48;
 static_assert(2 * kSoftmaxRegs + kControlRegs + kEpilogueRegs <= 4 * kLaunchRegs, "the registers the block is launched with");
 constexpr int kQSub = kBQ * 128;            // one 64-column half of a Q tile (bytes)
 constexpr int kQBytes = 2 * kQSub;          // 128 queries x 128 dims
