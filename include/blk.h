@@ -374,7 +374,8 @@ blk_status blk_qk_norm_rope(blk_handle* h, const blk_head_rows* q, const blk_hea
  * one sets the status word to INVALID_ARG and is read clamped. Sequences may be empty; rows of
  * no sequence are neither used nor written: what they hold, NaN included, reaches no
  * output. (Within a sequence a NaN or infinity in v reaches the outputs of its 128-row tile
- * of keys, as 0 * NaN does.) workspace: blk_attn_packed_workspace_bytes(h, rows, batch).
+ * of keys, as 0 * NaN does.) workspace: blk_attn_packed_workspace_bytes(h, rows, batch), 0 for
+ * all but large batches (then it may be NULL).
  * Errors: INVALID_ARG, UNSUPPORTED (fp32 handle), ALIGNMENT, WORKSPACE, CUDA. */
 size_t blk_attn_packed_workspace_bytes(const blk_handle* h, int rows, int batch);
 blk_status blk_attn_packed(blk_handle* h, const blk_head_rows* q, const blk_head_rows* k, const blk_head_rows* v,

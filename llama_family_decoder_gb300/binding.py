@@ -446,9 +446,9 @@ class DecoderBlock:
         qi, ki, vi = self._rows(q, "q", qs), self._rows(k, "k", ks), self._rows(v, "v", ks)
         out, o = self._out(out, "out", qs)
         nbytes = lib().blk_attn_packed_workspace_bytes(self.handle, n, batch)
-        ws = self._torch.empty(nbytes, dtype=self._torch.uint8, device=self._device)
-        _check(lib().blk_attn_packed(self.handle, qi, ki, vi, n, cu, batch, o, ws.data_ptr(), nbytes,
-                                     self._raw_stream(self._dev)))
+        ws = self._torch.empty(nbytes, dtype=self._torch.uint8, device=self._device) if nbytes else None
+        _check(lib().blk_attn_packed(self.handle, qi, ki, vi, n, cu, batch, o, ws.data_ptr() if nbytes else None,
+                                     nbytes, self._raw_stream(self._dev)))
         return out
 
     def kv4_cache(self, batch, capacity):

@@ -69,9 +69,12 @@ constexpr int kKVBytes = 2 * kKVSub;        // 128 keys x 128 dims
 constexpr int kKStages = 2;                 // K ring
 constexpr int kVStages = 2;                 // V ring
 constexpr int kSmem = 1024 + kSlots * kQBytes + (kKStages + kVStages) * kKVBytes + 256;
-constexpr int kSmemPacked = kSmem + kSlots * kBQ * 8;  // + the slots' softmax states of an item
+// + more barriers, the slots' softmax states of an item, and the CTA's own work entries
+constexpr int kOwnItems = 256;
+constexpr int kSmemPacked = kSmem + 32 + kSlots * kBQ * 8 + kOwnItems * 16;
 static_assert(kSmemPacked <= 227 * 1024, "shared memory");
 constexpr float kRescaleLog2 = 8.0f;
+constexpr int kStatusInvalidArg = 1;        // == BLK_ERR_INVALID_ARG
 constexpr unsigned long long kDrainNs = 2000000000ULL;
 constexpr float kLog2e = 1.4426950408889634f;
 static_assert(kSmem <= 227 * 1024, "shared memory");
@@ -105,8 +108,10 @@ struct AttnParams {
   unsigned long long wait_ns;
   // packed sequences: the work list (heaviest first) and its length, both on the device, and
   // the output's strides
-  const PackedWork* work;
+  const PackedWork* work;  // null: every CTA makes the list itself from cu (see own_work)
   const int* n_work;
+  const int* cu;
+  int step;
   long long o_row, o_head;
   // 2^fold query heads of a KV head share a slot's 128 rows: row r is head r % 2^fold of query
   // r / 2^fold
@@ -257,6 +262,80 @@ __device__ __forceinline__ Item item_of(const AttnParams& p, int id, const Packe
 // 2G - 1 - c, ...), so that every CTA's rounds sum to about the same work.
 __device__ __forceinline__ int item_id(int k, int G, int c) { return k * G + ((k & 1) ? G - 1 - c : c); }
 
+// The work list of packed sequences (heaviest first, an entry per `step` queries, ordered by its
+// place in its sequence, which its key count grows with, then by sequence), made by a whole CTA
+// in `scratch`; mine[k] := the entry of the CTA's item k. Returns the number of items. The order
+// is the same in every CTA: ballots over the sequences rank those that reach a place. A cu that
+// does not rise from 0 to at most the rows records INVALID_ARG and is read clamped.
+constexpr int kOwnSeqs = 2048, kOwnEntries = 8192;
+__device__ __noinline__ int own_work(const AttnParams& p, uint8_t* scratch, int units, PackedWork* mine) {
+  int* first = reinterpret_cast<int*>(scratch);  // [B] a sequence's first row, its length, its entries
+  int* len = first + kOwnSeqs;
+  int* n_of = len + kOwnSeqs;
+  int* at = n_of + kOwnSeqs;                     // [places] entries of a place, then of all farther ones
+  int* list = at + kOwnEntries;                  // sequence + place * kOwnSeqs
+  int* top = list + kOwnEntries;
+  static_assert((3 * kOwnSeqs + 2 * kOwnEntries + 2) * 4 <= (kKStages + kVStages) * kKVBytes, "scratch");
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;
+  if (tid == 0) top[0] = 0;
+  __syncthreads();
+  bool bad = false;
+  for (int b = tid; b < p.B; b += blockDim.x) {
+    const int a = p.cu[b], e = p.cu[b + 1];
+    const int lo = min(max(a, 0), p.T), hi = min(max(e, lo), p.T);
+    bad |= lo != a || hi != e;
+    first[b] = lo;
+    len[b] = hi - lo;
+    n_of[b] = (hi - lo + p.step - 1) / p.step;
+    atomicMax(&top[0], n_of[b]);
+  }
+  if (bad && blockIdx.x == 0 && p.status) atomicCAS(&p.status->code, 0, kStatusInvalidArg);
+  __syncthreads();
+  const int places = min(top[0], kOwnEntries);
+  for (int t = warp; t < places; t += warps) {
+    int n = 0;
+    for (int b = lane; b - lane < p.B; b += 32) n += __popc(__ballot_sync(0xffffffffu, b < p.B && n_of[b] > t));
+    if (lane == 0) at[t] = n;
+  }
+  __syncthreads();
+  if (warp == 0) {  // the entries of all farther places, from the last place down
+    int before = 0;
+    for (int t0 = places - 1; t0 >= 0; t0 -= 32) {
+      const int t = t0 - lane, n = t >= 0 ? at[t] : 0;
+      int run = n;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(0xffffffffu, run, o);
+        if (lane >= o) run += u;
+      }
+      if (t >= 0) at[t] = before + run - n;
+      before += __shfl_sync(0xffffffffu, run, 31);
+    }
+    if (lane == 0) top[1] = min(before, kOwnEntries);
+  }
+  __syncthreads();
+  for (int t = warp; t < places; t += warps) {
+    int to = at[t];
+    for (int b = lane; b - lane < p.B; b += 32) {
+      const bool in = b < p.B && n_of[b] > t;
+      const uint32_t all = __ballot_sync(0xffffffffu, in);
+      const int i = to + __popc(all & ((1u << lane) - 1u));
+      if (in && i < kOwnEntries) list[i] = b + t * kOwnSeqs;
+      to += __popc(all);
+    }
+  }
+  __syncthreads();
+  const int n_items = top[1] * units;
+  for (int k = tid; k < kOwnItems; k += blockDim.x) {
+    const int id = item_id(k, gridDim.x, blockIdx.x);
+    if (id < n_items) {
+      const int e = list[id / units], b = e % kOwnSeqs;
+      mine[k] = {first[b], len[b], e / kOwnSeqs * p.step, 0};
+    }
+  }
+  return n_items;
+}
+
 // F16: q, k, v (and so P) are fp16; otherwise bf16. Persistent: CTA c runs items
 // item_id(0, G, c), item_id(1, G, c), ... Barrier phases and ring positions run on
 // across items, so that the next item's Q, first K/V tiles and first score products
@@ -283,8 +362,9 @@ __global__ void __launch_bounds__(PACKED ? kPackedThreads : kThreads, 1) attn_tc
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
   // PACKED: each slot's reference and sum of each row, for the epilogue, and the barriers that
   // announce them
-  float2* ml = reinterpret_cast<float2*>(bars + 32);
+  float2* ml = reinterpret_cast<float2*>(bars + 36);
   auto ml_ready = [&](int g) { return smem_u32(&bars[28 + g]); };
+  PackedWork* mine = reinterpret_cast<PackedWork*>(ml + kSlots * kBQ);  // PACKED: the CTA's entries, item by item
   static_assert(26 * 8 + 8 <= 28 * 8, "barriers, the TMEM address, the abort flag");
   const uint32_t q_full = smem_u32(&bars[0]);
   const uint32_t q_empty = smem_u32(&bars[1]);
@@ -352,17 +432,23 @@ __global__ void __launch_bounds__(PACKED ? kPackedThreads : kThreads, 1) attn_tc
   tc_fence_after();
   pdl_wait();  // q, k, v (and the cache positions, the key ranges) come from earlier kernels
   const int units = PACKED ? p.H >> p.fold : 1;  // items of a work entry
-  const int n_items = PACKED ? *p.n_work * units : p.n_items;
-  // the work entry of this CTA's item k, read a turn ahead of its use
-  auto entry = [&](int k) {
-    PackedWork w{};
-    if constexpr (PACKED) {
-      const int id = item_id(k, G, cta);
-      if (id < n_items) {
-        const int4 v = *reinterpret_cast<const int4*>(p.work + id / units);
-        w = {v.x, v.y, v.z, v.w};
+  int n_items = p.n_items;
+  if constexpr (PACKED) {
+    if (p.work) {
+      n_items = *p.n_work * units;
+      for (int k = threadIdx.x; k < kOwnItems; k += blockDim.x) {
+        const int id = item_id(k, G, cta);
+        if (id < n_items) mine[k] = p.work[id / units];
       }
+    } else {
+      n_items = own_work(p, sK, units, mine);
+      fence_proxy_async_smem();  // the K and V stages served as scratch
     }
+    __syncthreads();
+  }
+  auto entry = [&](int k) {  // the work entry of this CTA's item k
+    PackedWork w{};
+    if constexpr (PACKED) w = mine[k];
     return w;
   };
   // the ring stage of slot g's tile J (counted over all items) and its phase: the slots share two
@@ -393,12 +479,10 @@ __global__ void __launch_bounds__(PACKED ? kPackedThreads : kThreads, 1) attn_tc
         return __all_sync(0xffffffffu, ok);
       };
       bool failed = false;
-      PackedWork ahead = entry(0);
       for (int k = 0; !failed; ++k) {
         const int id = item_id(k, G, cta);
         if (id >= n_items) break;
-        const Item it = item_of<PACKED, SPLIT>(p, id, ahead);
-        ahead = entry(k + 1);
+        const Item it = item_of<PACKED, SPLIT>(p, id, entry(k));
 #pragma unroll
         for (int g = 0; g < (SPLIT ? 1 : kSlots); ++g) {
           if (!ready(g, k) || (SPLIT && !ready(1, k))) {
@@ -470,12 +554,10 @@ __global__ void __launch_bounds__(PACKED ? kPackedThreads : kThreads, 1) attn_tc
       bool failed = false;
       int J = 0;  // K tiles issued over all items
       uint32_t used = 0;  // SPLIT: the parity of each stage's next phase
-      PackedWork ahead = entry(0);
       for (int k = 0; !failed; ++k) {
         const int id = item_id(k, G, cta);
         if (id >= n_items) break;
-        const Item it = item_of<PACKED, SPLIT>(p, id, ahead);
-        ahead = entry(k + 1);
+        const Item it = item_of<PACKED, SPLIT>(p, id, entry(k));
         // the Q buffer is free once both slots' score products of the previous item are done
         if (!mbar_wait(q_empty, (k & 1) ^ 1, budget, abort_flag)) {
           failed = true;
@@ -515,12 +597,10 @@ __global__ void __launch_bounds__(PACKED ? kPackedThreads : kThreads, 1) attn_tc
       bool failed = false;
       int J = 0;
       uint32_t used = 0;
-      PackedWork ahead = entry(0);
       for (int k = 0; !failed; ++k) {
         const int id = item_id(k, G, cta);
         if (id >= n_items) break;
-        const Item it = item_of<PACKED, SPLIT>(p, id, ahead);
-        ahead = entry(k + 1);
+        const Item it = item_of<PACKED, SPLIT>(p, id, entry(k));
         for (int j = 0; j < it.n_tiles; ++j, ++J) {
           const int s = SPLIT ? j & 1 : J % kVStages;
           const uint32_t ph = SPLIT ? (used >> s) & 1 : (J / kVStages) & 1;
@@ -574,12 +654,10 @@ __global__ void __launch_bounds__(PACKED ? kPackedThreads : kThreads, 1) attn_tc
       };
       bool failed = false;
       int J = 0;  // tiles over all items
-      PackedWork ahead = entry(0);
       for (int k = 0; !failed; ++k) {
         const int id = item_id(k, G, cta);
         if (id >= n_items) break;
-        const Item it = item_of<PACKED, SPLIT>(p, id, ahead);
-        ahead = entry(k + 1);
+        const Item it = item_of<PACKED, SPLIT>(p, id, entry(k));
         if (!mbar_wait(q_full, k & 1, budget, abort_flag)) {
           failed = true;
           break;
@@ -664,12 +742,10 @@ __global__ void __launch_bounds__(PACKED ? kPackedThreads : kThreads, 1) attn_tc
     const uint32_t o_taddr = tmem + lane_off + 256 + g * kD;
     bool failed = false;
     int J = 0;  // tiles over all items
-    PackedWork ahead = entry(0);
     for (int k = 0; !failed; ++k) {
       const int id = item_id(k, G, cta);
       if (id >= n_items) break;
-      const Item it = item_of<PACKED, SPLIT>(p, id, ahead);
-      ahead = entry(k + 1);
+      const Item it = item_of<PACKED, SPLIT>(p, id, entry(k));
       const Slot me = g == 0 ? it.sl[0] : it.sl[1];  // a select, not a run-time index into local memory
       const int m0 = me.m0;
       const int qi = m0 + (PACKED ? r >> p.fold : r);
@@ -1071,8 +1147,6 @@ namespace {
 
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanBins = 4096;
-constexpr int kStatusInvalidArg = 1;  // == BLK_ERR_INVALID_ARG
-
 // The work list of packed sequences, heaviest first: an entry per `step` queries, ordered by its place in its sequence, which its key count grows
 // with. One CTA counts the entries of each place, sums the counts from the far places
 // down, and deals the entries out; the order within a place does not matter (items are
@@ -1135,16 +1209,39 @@ __global__ void __launch_bounds__(kPlanThreads) packed_plan_kernel(const int* __
   if (bad && st) atomicCAS(&st->code, 0, kStatusInvalidArg);
 }
 
-// Entries of at least 8 queries (16 heads folded, split).
-int packed_work_cap(int rows, int B, int step) { return rows / step + B; }
-constexpr int kMinStep = kBQ / 16;
 constexpr int kSplitBelow = 3;       // items per SM
 constexpr size_t kPackedHead = 256;  // bytes before the work list: its length
 
+// How a packed batch is cut into items, from what the host knows of it.
+struct PackedPlan {
+  int fold, step, units, cap, grid;
+  bool split, own;  // own: every CTA makes the work list itself
+};
+PackedPlan packed_plan(int rows, int B, int H, int Hkv, int num_sms) {
+  PackedPlan p{};
+  while (p.fold < 4 && (H / Hkv) % (2 << p.fold) == 0) ++p.fold;
+  p.units = H >> p.fold;
+  const int tq = kBQ >> p.fold;
+  // Two query tiles an item while that gives every SM enough of them to even out; else split.
+  p.split = (long long)(rows / (2 * tq) + B) * p.units < kSplitBelow * num_sms;
+  p.step = p.split ? tq : 2 * tq;
+  p.cap = rows / p.step + B;
+  // one CTA per SM, more only where a CTA would have more items than it keeps entries for
+  const long long most = (long long)p.cap * p.units;
+  p.grid = (int)std::max(std::min<long long>(most, num_sms), (most + kOwnItems - 1) / kOwnItems);
+  // The list costs its ballots (about 30 cycles, 16 warps at once) in every CTA, or a launch of its
+  // own before the attention: B = 1, one token: %%TINY%% us a call with, %%TINY0%% without that launch.
+  const long long ballots = (long long)((rows + p.step - 1) / p.step) * ((B + 31) / 32);
+  p.own = B <= kOwnSeqs && p.cap <= kOwnEntries && ballots <= 2048;
+  return p;
+}
+
 }  // namespace
 
-size_t attn_packed_ws_bytes(int rows, int B) {
-  return kPackedHead + (size_t)packed_work_cap(rows, B, kMinStep) * sizeof(PackedWork);
+size_t attn_packed_ws_bytes(int rows, int B, int H, int Hkv, int num_sms) {
+  if (rows <= 0 || B <= 0) return 0;
+  const PackedPlan pl = packed_plan(rows, B, H, Hkv, num_sms);
+  return pl.own ? 0 : kPackedHead + (size_t)pl.cap * sizeof(PackedWork);
 }
 
 cudaError_t launch_attn_packed(const HeadRows& q, const HeadRows& k, const HeadRows& v, const HeadRows& o, int rows,
@@ -1157,10 +1254,9 @@ cudaError_t launch_attn_packed(const HeadRows& q, const HeadRows& k, const HeadR
   if (B <= 0 || rows <= 0) return cudaSuccess;
   AttnParams p;
   memset(static_cast<void*>(&p), 0, sizeof(p));
-  while (p.fold < 4 && (H / Hkv) % (2 << p.fold) == 0) ++p.fold;
-  const int tq = kBQ >> p.fold, units = H >> p.fold;
-  // Two query tiles an item while that gives every SM enough of them to even out; else split.
-  const bool split = (long long)packed_work_cap(rows, B, 2 * tq) * units < kSplitBelow * num_sms;
+  const PackedPlan pl = packed_plan(rows, B, H, Hkv, num_sms);
+  p.fold = pl.fold;
+  const int tq = kBQ >> p.fold;
   if (!make_tma_heads_bf16(&p.tq, q, rows, H, kD, 1 << p.fold, tq) ||
       !make_tma_heads_bf16(&p.tk, k, rows, Hkv, kD, 1, kBK) || !make_tma_heads_bf16(&p.tv, v, rows, Hkv, kD, 1, kBK)) {
     *why = "cuTensorMapEncodeTiled failed for q/k/v";
@@ -1178,26 +1274,36 @@ cudaError_t launch_attn_packed(const HeadRows& q, const HeadRows& k, const HeadR
   p.sl2 = kLog2e / sqrtf((float)kD);
   p.status = st;
   p.wait_ns = wait_ns;
-  p.n_work = static_cast<int*>(ws);
-  PackedWork* work = reinterpret_cast<PackedWork*>(static_cast<uint8_t*>(ws) + kPackedHead);
-  p.work = work;
+  p.cu = cu;
+  p.step = pl.step;
+  if (!pl.own) {
+    p.n_work = static_cast<int*>(ws);
+    p.work = reinterpret_cast<PackedWork*>(static_cast<uint8_t*>(ws) + kPackedHead);
+  }
+  const int split = pl.split ? 1 : 0;
   const auto kernel = split ? attn_tc_kernel<false, true, true> : attn_tc_kernel<false, true, false>;
   static std::atomic<unsigned long long> configured[2];
   cudaError_t e = set_smem_limit_once(reinterpret_cast<const void*>(kernel), kSmemPacked, configured[split]);
   if (e != cudaSuccess) return e;
   // the kernel moves registers between its warpgroups: the launch has to bring as many as it
   // gives out, or the wait for them would not end
-  cudaFuncAttributes fa;
-  e = cudaFuncGetAttributes(&fa, reinterpret_cast<const void*>(kernel));
-  if (e != cudaSuccess) return e;
-  if (fa.numRegs < kLaunchRegs) {
+  static std::atomic<int> regs[2];
+  if (regs[split].load(std::memory_order_relaxed) == 0) {
+    cudaFuncAttributes fa;
+    e = cudaFuncGetAttributes(&fa, reinterpret_cast<const void*>(kernel));
+    if (e != cudaSuccess) return e;
+    regs[split].store(fa.numRegs, std::memory_order_relaxed);
+  }
+  if (regs[split].load(std::memory_order_relaxed) < kLaunchRegs) {
     *why = "packed attention: the kernel was built with fewer registers than it redistributes";
     return cudaErrorLaunchOutOfResources;
   }
-  const int step = split ? tq : 2 * tq, cap = packed_work_cap(rows, B, step);
-  e = launch_pdl(packed_plan_kernel, 1, kPlanThreads, 0, s, cu, B, rows, step, cap, work, static_cast<int*>(ws), st);
-  if (e != cudaSuccess) return e;
-  return launch_pdl(kernel, dim3((unsigned)std::min<long long>((long long)cap * units, num_sms)), kPackedThreads, kSmemPacked, s, p);
+  if (!pl.own) {
+    e = launch_pdl(packed_plan_kernel, 1, kPlanThreads, 0, s, cu, B, rows, pl.step, pl.cap,
+                   const_cast<PackedWork*>(p.work), static_cast<int*>(ws), st);
+    if (e != cudaSuccess) return e;
+  }
+  return launch_pdl(kernel, pl.grid, kPackedThreads, kSmemPacked, s, p);
 }
 
 }  // namespace blk

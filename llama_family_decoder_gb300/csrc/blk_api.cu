@@ -1548,7 +1548,7 @@ blk_status blk_qk_norm_rope(blk_handle* h, const blk_head_rows* q, const blk_hea
 
 size_t blk_attn_packed_workspace_bytes(const blk_handle* h, int rows, int batch) {
   if (!h || rows < 0 || batch < 0) return 0;
-  return attn_packed_ws_bytes(rows, batch);
+  return attn_packed_ws_bytes(rows, batch, h->d.n_heads, h->d.n_kv_heads, h->num_sms);
 }
 
 blk_status blk_attn_packed(blk_handle* h, const blk_head_rows* q, const blk_head_rows* k, const blk_head_rows* v,
@@ -1570,7 +1570,8 @@ blk_status blk_attn_packed(blk_handle* h, const blk_head_rows* q, const blk_head
       return fail(BLK_ERR_UNSUPPORTED, "packed attention: broadcast (zero) strides");
     if (x->ptr == o->ptr) return fail(BLK_ERR_INVALID_ARG, "o must not be an input");
   }
-  if (!workspace || workspace_bytes < attn_packed_ws_bytes(rows, batch))
+  const size_t need = attn_packed_ws_bytes(rows, batch, d.n_heads, d.n_kv_heads, h->num_sms);
+  if (need > 0 && (!workspace || workspace_bytes < need))
     return fail(BLK_ERR_WORKSPACE, "packed attention: workspace missing or too small");
   if (!aligned16(workspace)) return fail(BLK_ERR_ALIGNMENT, "workspace not 16-byte aligned");
   BLK_TRY(check_device(h));

@@ -283,8 +283,9 @@ cudaError_t launch_attn_prefill_tc(const void* q, const void* k, const void* v, 
 
 // The same attention over packed sequences (bf16): rows cu[b] .. cu[b + 1] of q, k, v and o
 // are sequence b, whole prompts (key count = query count). Rows outside every sequence are
-// left as they were. ws: attn_packed_ws_bytes, holding the work list a first small kernel makes.
-size_t attn_packed_ws_bytes(int rows, int B);
+// left as they were. ws: attn_packed_ws_bytes (0 for most batches: then the kernel's CTAs make
+// their work list themselves, else a first small kernel does, into ws).
+size_t attn_packed_ws_bytes(int rows, int B, int H, int Hkv, int num_sms);
 cudaError_t launch_attn_packed(const HeadRows& q, const HeadRows& k, const HeadRows& v, const HeadRows& o, int rows,
                                const int* cu, int B, int H, int Hkv, int d, int window, void* ws, int num_sms,
                                DevStatus* st, unsigned long long wait_ns, cudaStream_t s, const char** why);

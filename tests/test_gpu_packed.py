@@ -231,6 +231,17 @@ def test_attn_packed(lens, H, Hkv):
     check_packed(out, q, k, v, lens)
 
 
+@pytest.mark.parametrize("lens", [[1] * 3000, [0] * 2500 + [300, 5] + [0] * 10, [3] * 700 + [140] * 20, [600] * 40])
+def test_attn_packed_many_sequences(lens):
+    """Batches whose work list a kernel of its own makes, and some near that border."""
+    n, H, Hkv = sum(lens), 4, 1
+    blk = block(H, Hkv)
+    q, k, v = randn(1, n, H, D), randn(2, n, Hkv, D), randn(3, n, Hkv, D)
+    out = blk.attn_packed(q, k, v, cu_of(lens))
+    assert blk.last_status() == 0
+    check_packed(out, q, k, v, lens)
+
+
 @pytest.mark.parametrize("window", [1, 5, 128, 200, 5000])
 def test_attn_packed_window(window):
     lens = [300, 1, 129, 520]
@@ -725,14 +736,27 @@ def test_refusals():
     from llama_family_decoder_gb300 import binding as b
     L = b.lib()
     r = lambda t: b.head_rows(t.data_ptr(), t.stride(0), t.stride(1))  # noqa: E731
-    o, ws = torch.empty_like(q), torch.empty(4096, dtype=torch.uint8, device=DEV)
+    o = torch.empty_like(q)
     cu = ints([0, 8])
-    need = L.blk_attn_packed_workspace_bytes(blk.handle, 8, 1)
     args = (blk.handle, r(q), r(k), r(k), 8, cu.data_ptr(), 1, r(o))
+    assert L.blk_attn_packed_workspace_bytes(blk.handle, 8, 1) == 0  # a small batch needs none
+    assert L.blk_attn_packed(*args, None, 0, None) == 0
+    assert L.blk_attn_packed(*args[:5], None, *args[6:], None, 0, None) == 1
+    assert L.blk_attn_packed(*args[:4], -1, *args[5:], None, 0, None) == 1
+    many = ints([0] * 3000 + [8])
+    need = L.blk_attn_packed_workspace_bytes(blk.handle, 8, 3000)
+    assert need > 0
+    ws = torch.empty(need + 16, dtype=torch.uint8, device=DEV)
+    args = (*args[:5], many.data_ptr(), 3000, args[7])
     assert L.blk_attn_packed(*args, ws.data_ptr(), need - 1, None) == 7
     assert L.blk_attn_packed(*args, None, need, None) == 7
     assert L.blk_attn_packed(*args, ws.data_ptr() + 8, need, None) == 3
     assert L.blk_attn_packed(*args, ws.data_ptr(), need, None) == 0
-    assert L.blk_attn_packed(*args[:5], None, *args[6:], ws.data_ptr(), need, None) == 1
-    assert L.blk_attn_packed(*args[:4], -1, *args[5:], ws.data_ptr(), need, None) == 1
+    need = L.blk_attn_decode_kv4_workspace_bytes(blk.handle, 8)
+    c = blk.kv4_cache(8, 4)
+    kc = b.kv4_cache_struct(c["k"].data_ptr(), c["k_scale"].data_ptr(), c["v"].data_ptr(), c["v_scale"].data_ptr(), 4,
+                            c["lens"].data_ptr())
+    ws = torch.empty(need, dtype=torch.uint8, device=DEV)
+    assert L.blk_attn_decode_kv4(blk.handle, r(q), kc, 8, r(o), ws.data_ptr(), need - 1, None) == 7
+    assert L.blk_attn_decode_kv4(blk.handle, r(q), kc, 8, r(o), ws.data_ptr(), need, None) == 0
     torch.cuda.synchronize()
