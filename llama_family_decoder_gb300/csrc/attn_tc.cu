@@ -60,7 +60,7 @@ constexpr int kThreads = 64 + kSlots * 128 + 32;  // + warp 10: the second slot'
 // boundary took 8500 cycles, two and a half tiles' time). Registers move from the last two to
 // the first two, whose scores (128 a thread) and addresses do not fit 128.
 constexpr int kPackedThreads = 512;
-constexpr int kLaunchRegs = 128, kSoftmaxRegs = 184, kControlRegs = 96, kEpilogueRegs = 48;
+constexpr int kLaunchRegs = 128, kSoftmaxRegs = 176, kControlRegs = 112, kEpilogueRegs = 48;
 static_assert(2 * kSoftmaxRegs + kControlRegs + kEpilogueRegs <= 4 * kLaunchRegs, "the registers the block is launched with");
 constexpr int kQSub = kBQ * 128;            // one 64-column half of a Q tile (bytes)
 constexpr int kQBytes = 2 * kQSub;          // 128 queries x 128 dims
@@ -1209,7 +1209,6 @@ __global__ void __launch_bounds__(kPlanThreads) packed_plan_kernel(const int* __
   if (bad && st) atomicCAS(&st->code, 0, kStatusInvalidArg);
 }
 
-constexpr int kSplitBelow = 3;       // items per SM
 constexpr size_t kPackedHead = 256;  // bytes before the work list: its length
 
 // How a packed batch is cut into items, from what the host knows of it.
@@ -1222,15 +1221,17 @@ PackedPlan packed_plan(int rows, int B, int H, int Hkv, int num_sms) {
   while (p.fold < 4 && (H / Hkv) % (2 << p.fold) == 0) ++p.fold;
   p.units = H >> p.fold;
   const int tq = kBQ >> p.fold;
-  // Two query tiles an item while that gives every SM enough of them to even out; else split.
-  p.split = (long long)(rows / (2 * tq) + B) * p.units < kSplitBelow * num_sms;
+  // Two query tiles an item; split when that leaves SMs idle, or with one long item each: below
+  // 5/4 items per SM (8 heads over 2: 2000 queries 34.7 -> 25.0 us, 4000 61.9 -> 43.4; above it
+  // the split's shorter items do not make up for its second read of K and V: 8000 115 -> 132).
+  p.split = 4 * (long long)(rows / (2 * tq) + B) * p.units < 5 * num_sms;
   p.step = p.split ? tq : 2 * tq;
   p.cap = rows / p.step + B;
   // one CTA per SM, more only where a CTA would have more items than it keeps entries for
   const long long most = (long long)p.cap * p.units;
   p.grid = (int)std::max(std::min<long long>(most, num_sms), (most + kOwnItems - 1) / kOwnItems);
   // The list costs its ballots (about 30 cycles, 16 warps at once) in every CTA, or a launch of its
-  // own before the attention: B = 1, one token: %%TINY%% us a call with, %%TINY0%% without that launch.
+  // own before the attention (48 turns of 10 to 200 queries: 24.9 us, 27.2 with that launch).
   const long long ballots = (long long)((rows + p.step - 1) / p.step) * ((B + 31) / 32);
   p.own = B <= kOwnSeqs && p.cap <= kOwnEntries && ballots <= 2048;
   return p;
