@@ -4,14 +4,18 @@
 //
 // The codes never become scaled values: with the group's scale s_g and offset z_g of a key,
 //   q . k^  = sum_g s_g (sum_{c in g} q_c code_c) + sum_g z_g qsum_g,   qsum_g = sum_{c in g} q_c
-//   out_c   = sum_s (p_s s_g) code_c + sum_s p_s z_g
+//   out_c   = sum_s (p_s s_g) (code_c - 8) + sum_s p_s z_g + 8 sum_s p_s s_g   (8: smaller numbers)
 // so the tensor core multiplies codes, which 16-bit floats hold exactly, and scales touch one
 // score per key and group (or one probability) instead of 32 values. A code becomes a number
 // by placing its nibble under an exponent (an and-or for two codes) and taking the exponent's
 // value off again (one packed add, on the otherwise idle fp32 pipe; the integer pipe is what
 // bounds the unpacking). K in fp16, whose mantissa also takes a nibble 4 bits up without a
 // shift (1024 + 16 code); q is scaled by a power of two per head to use fp16's whole range.
-// V in bf16 (128 + code): p s_g keeps its exponent range whatever the values' size.
+// V in bf16 (128 + code): p s_g keeps its exponent range whatever the values' size. p is rounded
+// to bf16 once, for all terms of a value alike; the 16-bit product p s_g goes in as two bf16
+// numbers, its rounding and the rest (8 products and 8 packed operations more for 16 keys; with
+// p s_g rounded, and codes counted from the end of their range, the mean error of an output was
+// 0.0050 of it, so 0.0022, of which storing it in bf16 takes 0.0016).
 //
 // Keys sit on the rows of the products and the group's query heads on their columns
 // (m16n8k16: S^T = K q^T, out^T = V^T P^T), so that 8 heads cost what one does. The score
@@ -161,15 +165,22 @@ __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
   return *reinterpret_cast<const uint32_t*>(&r);
 }
 
+// a b - c exactly, for c = the rounded product a b
+__device__ __forceinline__ uint32_t rest_bf16x2(uint32_t a, uint32_t b, uint32_t c) {
+  const __nv_bfloat162 r = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b),
+                                   __hneg2(*reinterpret_cast<const __nv_bfloat162*>(&c)));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
 
-// The codes in the nibbles at bits 0-3 and 16-19 as a pair of bf16, from 128 + code.
+// The codes in the nibbles at bits 0-3 and 16-19, less 8, as a pair of bf16, from 128 + code.
 __device__ __forceinline__ uint32_t codes_bf16(uint32_t w, uint32_t mask) {
-  const uint32_t v = and_or<0x43004300u>(w, mask), c = 0xC300C300u;
+  const uint32_t v = and_or<0x43004300u>(w, mask), c = 0xC308C308u;
   const __nv_bfloat162 r = __hadd2(*reinterpret_cast<const __nv_bfloat162*>(&v), *reinterpret_cast<const __nv_bfloat162*>(&c));
   return *reinterpret_cast<const uint32_t*>(&r);
 }
@@ -335,7 +346,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<NT>::kCtas) attn_kv4_kernel(cons
     at_v[i] = kCodeBytes + v_key[i] * kKv4Codes + 16 * (g >> 1);
     at_vs[i] = 2 * kCodeBytes + kScaleBytes + v_key[i] * kKv4Scales;
   }
-  const uint32_t z_off = 8 + 2 * (g & 3);
+  const uint32_t z_off = g < 4 ? 8 + 2 * g : 2 * (g - 4);  // the offset of group g, the scale of group g - 4
   const uint32_t mask = kept_constant(0x000F000Fu), mask_hi = kept_constant(0x00F000F0u);
   const uint32_t half = (g & 1) ? 0x7632u : 0x5410u;  // which bytes of a word are this row's
 
@@ -530,7 +541,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<NT>::kCtas) attn_kv4_kernel(cons
           for (int i = 0; i < 4; ++i) {
             const uint8_t* a = st + at_vs[i & 1] + (16 * u + (i >> 1) * 8) * kKv4Scales;
             vs[i] = ld<uint2>(a);
-            vz[i] = ld<uint16_t>(a + z_off);  // rows 4-7 of the product repeat rows 0-3: nobody looks
+            vz[i] = ld<uint16_t>(a + z_off);
           }
           {
             const uint32_t za[4] = {__byte_perm(vz[0], vz[1], 0x5410), 0u, __byte_perm(vz[2], vz[3], 0x5410), 0u};
@@ -559,6 +570,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<NT>::kCtas) attn_kv4_kernel(cons
               const uint32_t p0 = mul_bf16x2(pb[u][n][0], s0), p1 = mul_bf16x2(pb[u][n][1], s1);
               mma_bf16(acc[n][2 * j], a0, p0, p1, acc[n][2 * j]);
               mma_bf16(acc[n][2 * j + 1], a1, p0, p1, acc[n][2 * j + 1]);
+              const uint32_t r0 = rest_bf16x2(pb[u][n][0], s0, p0), r1 = rest_bf16x2(pb[u][n][1], s1, p1);
+              mma_bf16(acc[n][2 * j], a0, r0, r1, acc[n][2 * j]);
+              mma_bf16(acc[n][2 * j + 1], a1, r0, r1, acc[n][2 * j + 1]);
             }
           }
         }
@@ -583,7 +597,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<NT>::kCtas) attn_kv4_kernel(cons
 #pragma unroll
         for (int j = 0; j < 4; ++j)
 #pragma unroll
-          for (int r = 0; r < 2; ++r) zj[j][r] = __shfl_sync(0xffffffffu, zacc[n][r], 4 * j + tq);
+          for (int r = 0; r < 2; ++r)
+            zj[j][r] = fmaf(8.f, __shfl_sync(0xffffffffu, zacc[n][r], 4 * (j + 4) + tq),
+                            __shfl_sync(0xffffffffu, zacc[n][r], 4 * j + tq));
         if ((tq >> 1) == (c & 1)) {  // the lanes whose columns are these heads
 #pragma unroll
           for (int r = 0; r < 2; ++r) {

@@ -12,8 +12,8 @@ Bounds count roundings. bf16 rounds by at most u = 2^-8 of the value (half a ste
    output once: u sum(p |v|) + u |o|. Scores are sums of 128 exact products in fp32, off by at
    most 128 * 2^-23 sum|q k| / sqrt(128); exp adds 2^-22. Both under 2e-4 of sum(p |v|) at
    these inputs.
- - decode over 4 bits: p and then p * scale are rounded to bf16 (2 u (1 + u) of the code part
-   p scale code), p alone for the offsets, the output once; a score is a sum of exact products
+ - decode over 4 bits: p is rounded to bf16 for all terms of a value (u |value|), p * scale once
+   more (u scale |code - 8|), the output once; a score is a sum of exact products
    (of a group's sum of q in 24 bits with its offset) in fp32, off by at most
    2^-21 sum|q| (15 scale + |offset|) / sqrt(128).
 """
@@ -512,8 +512,8 @@ def check_decode(out, q, k, v, lens, window=0):
         K, V = values(kk).double().numpy(), values(vv).double().numpy()
         _, ks, kz = (x.double().numpy() for x in quantise(kk))
         vc, vs, vz = (x.double().numpy() for x in quantise(vv))
-        code = np.repeat(vs, 32, -1) * vc
-        off = np.abs(np.repeat(vz, 32, -1))
+        code = np.repeat(vs, 32, -1) * np.abs(vc - 8)
+        parts = code + np.abs(np.repeat(vz, 32, -1)) + 8 * np.repeat(vs, 32, -1)  # what fp32 adds up
         for h in range(H):
             j = h // per
             qh = np64(q[b, h])
@@ -523,8 +523,8 @@ def check_decode(out, q, k, v, lens, window=0):
             qa = np.abs(qh).reshape(4, 32).sum(-1)
             delta = 2.0 ** -21 * ((15 * ks[:, j] + np.abs(kz[:, j])) @ qa).max() / np.sqrt(D) + 1e-6
             ref = p @ V[:, j]
-            bound = 2 * U * (1 + U) * (p @ code[:, j]) + U * (p @ off[:, j]) + U * np.abs(ref) + \
-                np.expm1(2 * delta) * (p @ (code[:, j] + off[:, j]))
+            bound = U * (p @ np.abs(V[:, j])) + U * (1 + U) * (p @ code[:, j]) + U * np.abs(ref) + \
+                np.expm1(2 * delta) * (p @ np.abs(V[:, j])) + 2.0 ** -18 * (p @ parts[:, j])
             err = np.abs(np64(out[b, h]) - ref)
             assert np.all(err <= bound), (b, h, float((err / bound).max()))
         at += n
