@@ -421,9 +421,11 @@ blk_status blk_kv4_load(blk_handle* h, const blk_kv4_cache* cache, const int* cu
  * a window), k^ and v^ the values the codes stand for. q, o [batch, n_heads, 128] bf16, a row
  * per sequence. lens[b] == 0 gives a zero row; lens beyond the capacity is read as the
  * capacity. What unused slots hold reaches no output. workspace:
- * blk_attn_decode_kv4_workspace_bytes(h, batch).
+ * blk_attn_decode_kv4_workspace_bytes(h, batch, capacity), 0 for small batches over small caches
+ * (then it may be NULL). Values are summed up to 2^8 times their size and 16 of a group's
+ * scale: values up to about 1e30 stay finite.
  * Errors: INVALID_ARG, UNSUPPORTED (fp32 handle), ALIGNMENT, WORKSPACE, CUDA. */
-size_t blk_attn_decode_kv4_workspace_bytes(const blk_handle* h, int batch);
+size_t blk_attn_decode_kv4_workspace_bytes(const blk_handle* h, int batch, int capacity);
 blk_status blk_attn_decode_kv4(blk_handle* h, const blk_head_rows* q, const blk_kv4_cache* cache, int batch,
                                const blk_head_rows* o, void* workspace, size_t workspace_bytes, void* stream);
 

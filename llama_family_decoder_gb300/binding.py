@@ -92,7 +92,7 @@ SIGNATURES = {
                               c_void_p]),
     "blk_kv4_load": (c_int, [c_void_p, _KV4, c_void_p, c_void_p, c_int, c_int, _ROWS, _ROWS,
                              c_void_p]),
-    "blk_attn_decode_kv4_workspace_bytes": (c_size_t, [c_void_p, c_int]),
+    "blk_attn_decode_kv4_workspace_bytes": (c_size_t, [c_void_p, c_int, c_int]),
     "blk_attn_decode_kv4": (c_int, [c_void_p, _ROWS, _KV4, c_int, _ROWS, c_void_p, c_size_t,
                                     c_void_p]),
     "blk_stage_workspace_bytes": (c_size_t, [c_void_p, c_int]),
@@ -514,9 +514,9 @@ class DecoderBlock:
         H, _, d = self._sizes
         qi = self._rows(q, "q", (batch, H, d))
         out, o = self._out(out, "out", (batch, H, d))
-        nbytes = lib().blk_attn_decode_kv4_workspace_bytes(self.handle, batch)
-        ws = self._torch.empty(nbytes, dtype=self._torch.uint8, device=self._device)
-        _check(lib().blk_attn_decode_kv4(self.handle, qi, c, batch, o, ws.data_ptr(), nbytes,
+        nbytes = lib().blk_attn_decode_kv4_workspace_bytes(self.handle, batch, cache["k"].shape[2])
+        ws = self._torch.empty(nbytes, dtype=self._torch.uint8, device=self._device) if nbytes else None
+        _check(lib().blk_attn_decode_kv4(self.handle, qi, c, batch, o, ws.data_ptr() if nbytes else None, nbytes,
                                          self._raw_stream(self._dev)))
         return out
 

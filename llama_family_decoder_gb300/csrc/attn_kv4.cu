@@ -210,7 +210,10 @@ __device__ __forceinline__ T ld(const uint8_t* p) {
 // odd ones for V) are as even and odd keys, whose 64-byte rows sit on different banks.
 __device__ __forceinline__ int key_of_row(int r) { return r ^ ((r >> 1) & 1); }
 
-template <int NT>
+// CL: the CTAs of a cluster that share one (sequence, KV head), for small batches: equal shares of
+// its tiles, joined through their shared memory, so that no second kernel and no workspace
+// is needed. CL == 1: a stretch of the line of all tiles per CTA.
+template <int NT, int CL>
 __global__ void __launch_bounds__(kThreads, Cfg<NT>::kCtas) attn_kv4_kernel(const __grid_constant__ Kv4Params p) {
   pdl_launch_dependents();
   extern __shared__ __align__(128) uint8_t smem[];
@@ -221,64 +224,76 @@ __global__ void __launch_bounds__(kThreads, Cfg<NT>::kCtas) attn_kv4_kernel(cons
   uint8_t* ring = smem + warp * kStages * kStageBytes;
   TileInfo* info = reinterpret_cast<TileInfo*>(merge + kMergeFloats) + warp * kStages;
   pdl_wait();
-  // the tiles before each thread's run of sequences
-  const int per = (p.B + kThreads - 1) / kThreads;
-  const int b_lo = min(p.B, tid * per), b_hi = min(p.B, b_lo + per);
-  int mine = 0;
-  for (int b = b_lo; b < b_hi; ++b) {
-    int first, n;
-    keys_of(p, b, first, n);
-    mine += tiles(n);
-  }
-  int run = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int u = __shfl_up_sync(0xffffffffu, run, o);
-    if (lane >= o) run += u;
-  }
-  if (lane == 31) warp_sums[warp] = run;
-  __syncthreads();
-  int before = run - mine, all = 0;
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    if (w < warp) before += warp_sums[w];
-    all += warp_sums[w];
-  }
-  const long long total = (long long)all * p.Hkv;
-  const int n_str = total > 0 ? stretches(total, gridDim.x) : 0;
-  const int cta = blockIdx.x;
-  const long long t_lo = cta < n_str ? stretch_begin(total, n_str, cta) : 0;
-  const int n_mine = cta < n_str ? (int)(stretch_begin(total, n_str, cta + 1) - t_lo) : 0;
-  {
-    int acc = before;
+  const int cta = blockIdx.x, rank = CL > 1 ? (int)cluster_ctarank() : 0;
+  int n_mine;
+  Walk w;
+  if constexpr (CL > 1) {
+    w.b = cta / CL / p.Hkv;
+    w.kvh = cta / CL % p.Hkv;
+    keys_of(p, w.b, w.first, w.keys);
+    w.n_tiles = tiles(w.keys);
+    w.t = w.n_tiles * rank / CL;
+    n_mine = w.n_tiles * (rank + 1) / CL - w.t;
+  } else {
+    // the tiles before each thread's run of sequences
+    const int per = (p.B + kThreads - 1) / kThreads;
+    const int b_lo = min(p.B, tid * per), b_hi = min(p.B, b_lo + per);
+    int mine = 0;
     for (int b = b_lo; b < b_hi; ++b) {
       int first, n;
       keys_of(p, b, first, n);
-      const int nt = tiles(n);
-      if (cta == 0) p.prefix[b] = acc;
-      const long long lo = (long long)acc * p.Hkv;
-      if (nt > 0 && t_lo >= lo && t_lo < lo + (long long)nt * p.Hkv) {
-        const int off = (int)(t_lo - lo);
-        start[0] = b;
-        start[1] = off / nt;
-        start[2] = off % nt;
+      mine += tiles(n);
+    }
+    int run = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, run, o);
+      if (lane >= o) run += u;
+    }
+    if (lane == 31) warp_sums[warp] = run;
+    __syncthreads();
+    int before = run - mine, all = 0;
+#pragma unroll
+    for (int i = 0; i < kWarps; ++i) {
+      if (i < warp) before += warp_sums[i];
+      all += warp_sums[i];
+    }
+    const long long total = (long long)all * p.Hkv;
+    const int n_str = total > 0 ? stretches(total, gridDim.x) : 0;
+    const long long t_lo = cta < n_str ? stretch_begin(total, n_str, cta) : 0;
+    n_mine = cta < n_str ? (int)(stretch_begin(total, n_str, cta + 1) - t_lo) : 0;
+    {
+      int acc = before;
+      for (int b = b_lo; b < b_hi; ++b) {
+        int first, n;
+        keys_of(p, b, first, n);
+        const int nt = tiles(n);
+        if (cta == 0) p.prefix[b] = acc;
+        const long long lo = (long long)acc * p.Hkv;
+        if (nt > 0 && t_lo >= lo && t_lo < lo + (long long)nt * p.Hkv) {
+          const int off = (int)(t_lo - lo);
+          start[0] = b;
+          start[1] = off / nt;
+          start[2] = off % nt;
+        }
+        acc += nt;
       }
-      acc += nt;
+      if (cta == 0 && tid == kThreads - 1) {
+        p.prefix[p.B] = all;
+        p.prefix[p.B + 1] = n_str;
+      }
     }
-    if (cta == 0 && tid == kThreads - 1) {
-      p.prefix[p.B] = all;
-      p.prefix[p.B + 1] = n_str;
-    }
+    __syncthreads();
+    if (n_mine == 0) return;
+    w.b = start[0];
+    w.enter(p);
+    w.kvh = start[1];
+    w.t = start[2];
   }
-  __syncthreads();
-  if (n_mine == 0) return;
+  const int pair_b = w.b, pair_kvh = w.kvh;  // CL > 1: the cluster's pair
+  float* const shared_out = reinterpret_cast<float*>(smem);  // ... and this CTA's share of it, [head][128 + 4]
 
   // ---- this warp's copies, a tile ahead of its products
-  Walk w;
-  w.b = start[0];
-  w.enter(p);
-  w.kvh = start[1];
-  w.t = start[2];
   const uint64_t once = l2_policy_evict_first();
   // byte offset of this lane's first copy of codes: a row of codes is four lanes' copies, and a
   // row of scales, a quarter as long, one lane's
@@ -633,7 +648,11 @@ __global__ void __launch_bounds__(kThreads, Cfg<NT>::kCtas) attn_kv4_kernel(cons
             ll += sm_ml[2 * hh + 1] * f;
             oo = make_float4(oo.x + x.x * f, oo.y + x.y * f, oo.z + x.z * f, oo.w + x.w * f);
           }
-          if (ti.flags & kWhole) {
+          if constexpr (CL > 1) {  // over the stages, which are done with
+            float* to = shared_out + h * (kD + 4);
+            *reinterpret_cast<float4*>(to + 4 * lane) = oo;
+            if (lane == 0) *reinterpret_cast<float2*>(to + kD) = make_float2(mm, ll);
+          } else if (ti.flags & kWhole) {
             const float inv = 1.f / ll;
             __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.o.ptr) + ti.b * p.o.row +
                                (long long)(ti.kvh * G + h) * p.o.head + 4 * lane;
@@ -650,6 +669,37 @@ __global__ void __launch_bounds__(kThreads, Cfg<NT>::kCtas) attn_kv4_kernel(cons
     }
     __syncwarp();  // every lane is done with the stage: the next copies may overwrite it
     if (++stage == kStages) stage = 0;
+  }
+  if constexpr (CL > 1) {
+    if (n_mine == 0)  // nothing, as a share
+      for (int i = tid; i < G * (kD + 4); i += kThreads) shared_out[i] = i % (kD + 4) == kD ? -INFINITY : 0.f;
+    cluster_sync_all();
+    for (int h = rank + CL * warp; h < G; h += CL * kWarps) {  // a warp per head, four channels a lane
+      const uint32_t mine = smem_u32(shared_out + h * (kD + 4));
+      float4 ov[CL], ml[CL];
+#pragma unroll
+      for (int v = 0; v < CL; ++v) {
+        const uint32_t at = map_shared_rank(mine, v);
+        ov[v] = ld_dsmem_f4(at + 16 * lane);
+        ml[v] = ld_dsmem_f4(at + 4 * kD);
+      }
+      float mm = -INFINITY, ll = 0.f;
+#pragma unroll
+      for (int v = 0; v < CL; ++v) mm = fmaxf(mm, ml[v].x);
+      const float mu = mm == -INFINITY ? 0.f : mm;
+      float4 oo = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int v = 0; v < CL; ++v) {
+        const float f = ex2(ml[v].x - mu);
+        ll += ml[v].y * f;
+        oo = make_float4(oo.x + ov[v].x * f, oo.y + ov[v].y * f, oo.z + ov[v].z * f, oo.w + ov[v].w * f);
+      }
+      const float inv = w.n_tiles > 0 ? 1.f / ll : 0.f;  // no keys: a zero row
+      __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.o.ptr) + pair_b * p.o.row +
+                         (long long)(pair_kvh * G + h) * p.o.head + 4 * lane;
+      *reinterpret_cast<uint2*>(o) = make_uint2(pack_bf16x2(oo.x * inv, oo.y * inv), pack_bf16x2(oo.z * inv, oo.w * inv));
+    }
+    cluster_sync_all();  // nobody leaves while its share may be read
   }
 }
 
@@ -729,17 +779,48 @@ Kv4Ws kv4_ws(int B, int H, int Hkv, int num_sms) {
   return w;
 }
 
-template <int NT>
+// Clusters for small batches: CTAs that share a pair when there are few pairs, each with few
+// enough tiles; 1 otherwise.
+constexpr int kClusterCtas = 8, kClusterTiles = 8;
+int kv4_cluster(int B, int Hkv, int capacity, int window, int num_sms) {
+  const int span = window > 0 && window < capacity ? window : capacity;
+  const bool few = (long long)B * Hkv * kClusterCtas <= 2ll * num_sms;
+  return few && (span + kTile - 1) / kTile <= kClusterCtas * kClusterTiles ? kClusterCtas : 1;
+}
+
+template <int NT, int CL>
 cudaError_t launch_nt(const Kv4Params& p, int grid, cudaStream_t s) {
   static std::atomic<unsigned long long> configured{0};  // one bit per device
-  cudaError_t e = set_smem_limit_once(reinterpret_cast<const void*>(attn_kv4_kernel<NT>), Cfg<NT>::kSmem, configured);
+  const auto kernel = attn_kv4_kernel<NT, CL>;
+  cudaError_t e = set_smem_limit_once(reinterpret_cast<const void*>(kernel), Cfg<NT>::kSmem, configured);
   if (e != cudaSuccess) return e;
-  return launch_pdl(attn_kv4_kernel<NT>, grid, kThreads, Cfg<NT>::kSmem, s, p);
+  if constexpr (CL == 1) {
+    return launch_pdl(kernel, grid, kThreads, Cfg<NT>::kSmem, s, p);
+  } else {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = Cfg<NT>::kSmem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = CL;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kernel, p);
+  }
 }
 
 }  // namespace
 
-size_t attn_kv4_ws_bytes(int B, int H, int Hkv, int num_sms) { return kv4_ws(B, H, Hkv, num_sms).bytes; }
+size_t attn_kv4_ws_bytes(int B, int H, int Hkv, int capacity, int window, int num_sms) {
+  if (B <= 0 || kv4_cluster(B, Hkv, capacity, window, num_sms) > 1) return 0;
+  return kv4_ws(B, H, Hkv, num_sms).bytes;
+}
 
 cudaError_t launch_attn_decode_kv4(const HeadRows& q, const Kv4Cache& c, const HeadRows& o, int B, int H, int Hkv,
                                    int window, void* ws, int num_sms, cudaStream_t s, const char** why) {
@@ -748,14 +829,21 @@ cudaError_t launch_attn_decode_kv4(const HeadRows& q, const Kv4Cache& c, const H
     return cudaErrorInvalidValue;
   }
   if (B <= 0) return cudaSuccess;
+  Kv4Params p{q, o, c, B, H, Hkv, window > 0 ? window : 0, nullptr, nullptr, nullptr, kLog2e / sqrtf((float)kD)};
+  const bool wide = H / Hkv > 8;
+  if (kv4_cluster(B, Hkv, c.capacity, window, num_sms) > 1) {
+    const int grid = B * Hkv * kClusterCtas;
+    return wide ? launch_nt<2, kClusterCtas>(p, grid, s) : launch_nt<1, kClusterCtas>(p, grid, s);
+  }
   const Kv4Ws w = kv4_ws(B, H, Hkv, num_sms);
   uint8_t* base = static_cast<uint8_t*>(ws);
-  Kv4Params p{q, o, c, B, H, Hkv, window > 0 ? window : 0, reinterpret_cast<int*>(base + w.prefix),
-              reinterpret_cast<float*>(base + w.ml), reinterpret_cast<float*>(base + w.o), kLog2e / sqrtf((float)kD)};
+  p.prefix = reinterpret_cast<int*>(base + w.prefix);
+  p.part_ml = reinterpret_cast<float*>(base + w.ml);
+  p.part_o = reinterpret_cast<float*>(base + w.o);
   // a CTA per kMinTiles tiles of the largest cache this could be
   const long long most = (long long)B * Hkv * ((c.capacity + kTile - 1) / kTile);
   const int grid = (int)std::max(1ll, std::min<long long>(kv4_grid(H, Hkv, num_sms), most / kMinTiles));
-  cudaError_t e = H / Hkv <= 8 ? launch_nt<1>(p, grid, s) : launch_nt<2>(p, grid, s);
+  cudaError_t e = wide ? launch_nt<2, 1>(p, grid, s) : launch_nt<1, 1>(p, grid, s);
   if (e != cudaSuccess) return e;
   const long long pairs = (long long)B * H;
   return launch_pdl(attn_kv4_join_kernel, dim3((unsigned)((pairs + kJoinThreads / 32 - 1) / (kJoinThreads / 32))),

@@ -1618,9 +1618,9 @@ blk_status blk_kv4_load(blk_handle* h, const blk_kv4_cache* cache, const int* cu
                     "4-bit load");
 }
 
-size_t blk_attn_decode_kv4_workspace_bytes(const blk_handle* h, int batch) {
-  if (!h || batch < 0) return 0;
-  return attn_kv4_ws_bytes(batch, h->d.n_heads, h->d.n_kv_heads, h->num_sms);
+size_t blk_attn_decode_kv4_workspace_bytes(const blk_handle* h, int batch, int capacity) {
+  if (!h || batch < 0 || capacity <= 0) return 0;
+  return attn_kv4_ws_bytes(batch, h->d.n_heads, h->d.n_kv_heads, capacity, h->d.sliding_window, h->num_sms);
 }
 
 blk_status blk_attn_decode_kv4(blk_handle* h, const blk_head_rows* q, const blk_kv4_cache* cache, int batch,
@@ -1633,7 +1633,7 @@ blk_status blk_attn_decode_kv4(blk_handle* h, const blk_head_rows* q, const blk_
   BLK_TRY(check_rows(h, o, batch, d.n_heads, true, "o"));
   if (batch == 0) return BLK_OK;
   if (q->ptr == o->ptr) return fail(BLK_ERR_INVALID_ARG, "o must not be an input");
-  const size_t need = attn_kv4_ws_bytes(batch, d.n_heads, d.n_kv_heads, h->num_sms);
+  const size_t need = attn_kv4_ws_bytes(batch, d.n_heads, d.n_kv_heads, cache->capacity, d.sliding_window, h->num_sms);
   if (need > 0 && (!workspace || workspace_bytes < need))
     return fail(BLK_ERR_WORKSPACE, "4-bit decode attention: workspace missing or too small");
   if (!aligned16(workspace)) return fail(BLK_ERR_ALIGNMENT, "workspace not 16-byte aligned");

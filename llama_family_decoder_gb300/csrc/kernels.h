@@ -309,8 +309,9 @@ int attn_decode_splits(int B, int Hkv, int max_len, int num_sms);
 int attn_decode_split_cap(int max_len);
 
 // Decode over the 4-bit cache: q, o [B, H, 128] bf16 (a row per sequence), keys lens[b]
-// (at most the capacity; the last `window` of them with a window). ws: attn_kv4_ws_bytes.
-size_t attn_kv4_ws_bytes(int B, int H, int Hkv, int num_sms);
+// (at most the capacity; the last `window` of them with a window). ws: attn_kv4_ws_bytes, 0 for
+// small batches over small caches.
+size_t attn_kv4_ws_bytes(int B, int H, int Hkv, int capacity, int window, int num_sms);
 cudaError_t launch_attn_decode_kv4(const HeadRows& q, const Kv4Cache& c, const HeadRows& o, int B, int H, int Hkv,
                                    int window, void* ws, int num_sms, cudaStream_t s, const char** why);
 

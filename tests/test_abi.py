@@ -118,4 +118,4 @@ def test_packed_stage_argument_checks_on_host(L):
     assert L.blk_attn_decode_kv4(None, r, c, 1, r, None, 0, None) == 1
     assert b"NULL handle" in L.blk_last_error_message()
     assert L.blk_attn_packed_workspace_bytes(None, 8, 1) == 0
-    assert L.blk_attn_decode_kv4_workspace_bytes(None, 1) == 0
+    assert L.blk_attn_decode_kv4_workspace_bytes(None, 1, 8) == 0

@@ -752,11 +752,16 @@ def test_refusals():
     assert L.blk_attn_packed(*args, None, need, None) == 7
     assert L.blk_attn_packed(*args, ws.data_ptr() + 8, need, None) == 3
     assert L.blk_attn_packed(*args, ws.data_ptr(), need, None) == 0
-    need = L.blk_attn_decode_kv4_workspace_bytes(blk.handle, 8)
+    kv4 = lambda c: b.kv4_cache_struct(*[c[x].data_ptr() for x in ("k", "k_scale", "v", "v_scale")], c["k"].shape[2],  # noqa: E731
+                                       c["lens"].data_ptr())
     c = blk.kv4_cache(8, 4)
-    kc = b.kv4_cache_struct(c["k"].data_ptr(), c["k_scale"].data_ptr(), c["v"].data_ptr(), c["v_scale"].data_ptr(), 4,
-                            c["lens"].data_ptr())
+    assert L.blk_attn_decode_kv4_workspace_bytes(blk.handle, 8, 4) == 0  # few pairs, few keys: none
+    assert L.blk_attn_decode_kv4(blk.handle, r(q), kv4(c), 8, r(o), None, 0, None) == 0
+    q, o, c = randn(1, 500, 4, D), randn(1, 500, 4, D), blk.kv4_cache(500, 4)
+    need = L.blk_attn_decode_kv4_workspace_bytes(blk.handle, 500, 4)
+    assert need > 0
     ws = torch.empty(need, dtype=torch.uint8, device=DEV)
-    assert L.blk_attn_decode_kv4(blk.handle, r(q), kc, 8, r(o), ws.data_ptr(), need - 1, None) == 7
-    assert L.blk_attn_decode_kv4(blk.handle, r(q), kc, 8, r(o), ws.data_ptr(), need, None) == 0
+    assert L.blk_attn_decode_kv4(blk.handle, r(q), kv4(c), 500, r(o), ws.data_ptr(), need - 1, None) == 7
+    assert L.blk_attn_decode_kv4(blk.handle, r(q), kv4(c), 500, r(o), None, need, None) == 7
+    assert L.blk_attn_decode_kv4(blk.handle, r(q), kv4(c), 500, r(o), ws.data_ptr(), need, None) == 0
     torch.cuda.synchronize()
