@@ -111,7 +111,7 @@ struct AttnParams {
   const PackedWork* work;  // null: every CTA makes the list itself from cu (see own_work)
   const int* n_work;
   const int* cu;
-  int step;
+  int step, cap;  // queries of an entry, entries of rising sequences at most
   long long o_row, o_head;
   // 2^fold query heads of a KV head share a slot's 128 rows: row r is head r % 2^fold of query
   // r / 2^fold
@@ -311,7 +311,7 @@ __device__ __noinline__ int own_work(const AttnParams& p, uint8_t* scratch, int 
       if (t >= 0) at[t] = before + run - n;
       before += __shfl_sync(0xffffffffu, run, 31);
     }
-    if (lane == 0) top[1] = min(before, kOwnEntries);
+    if (lane == 0) top[1] = min(before, p.cap);  // sequences that overlap could have more
   }
   __syncthreads();
   for (int t = warp; t < places; t += warps) {
@@ -1277,6 +1277,7 @@ cudaError_t launch_attn_packed(const HeadRows& q, const HeadRows& k, const HeadR
   p.wait_ns = wait_ns;
   p.cu = cu;
   p.step = pl.step;
+  p.cap = pl.cap;
   if (!pl.own) {
     p.n_work = static_cast<int*>(ws);
     p.work = reinterpret_cast<PackedWork*>(static_cast<uint8_t*>(ws) + kPackedHead);

@@ -324,6 +324,38 @@ def test_attn_packed_bad_sequences_are_clamped():
     assert blk.attn_packed(q[:0], k[:0], v[:0], ints([0, 0])).shape == (0, 4, D)
 
 
+def test_attn_packed_overlapping_sequences_stay_in_bounds():
+    """Sequences that claim the same rows many times over have more work than any valid batch."""
+    n = 6000
+    blk = block(16, 2)
+    q, k, v = randn(1, n, 16, D), randn(2, n, 2, D), randn(3, n, 2, D)
+    out = torch.full((n + 64, 16, D), 3.0, dtype=torch.bfloat16, device=DEV)
+    for pairs in (5, 60, 1500):
+        blk.attn_packed(q, k, v, ints([0, n] * pairs + [0]), out=out[:n])
+        assert blk.last_status() == 1
+        assert torch.isfinite(out[:n]).all() and torch.all(out[n:] == 3)
+    lens = [n]
+    check_packed(blk.attn_packed(q, k, v, ints([0, n])), q, k, v, lens)
+
+
+@pytest.mark.parametrize("H,Hkv,lens", [(4, 2, [300, 200]), (32, 8, [2000, 50, 1500])])  # split and not
+def test_attn_packed_wait_runs_out_then_recovers(H, Hkv, lens):
+    """A wait limit far below a copy's latency: the kernel stops, says so and leaves everything usable."""
+    from llama_family_decoder_gb300.binding import set_wait_timeout_ns
+    n = sum(lens)
+    blk = block(H, Hkv)
+    q, k, v = randn(1, n, H, D), randn(2, n, Hkv, D), randn(3, n, Hkv, D)
+    set_wait_timeout_ns(100)
+    try:
+        blk.attn_packed(q, k, v, cu_of(lens))
+        assert blk.last_status() == 6 and blk.last_status() == 0
+    finally:
+        set_wait_timeout_ns(0)
+    for _ in range(2):
+        check_packed(blk.attn_packed(q, k, v, cu_of(lens)), q, k, v, lens)
+        assert blk.last_status() == 0
+
+
 def test_attn_packed_large_scores():
     """One key takes all the weight, scores in the thousands."""
     lens = [200, 130]
