@@ -142,6 +142,21 @@ def lib():
     return _lib_handle
 
 
+_fast_module = None
+
+
+def fastcall():
+    """The compiled argument handling of the packed calls (csrc/fastcall.cpp), built with the
+    library and linked to it."""
+    global _fast_module
+    if _fast_module is None:
+        import torch  # noqa: F401  (its libraries, which the module uses)
+        lib()
+        from . import _fastcall
+        _fast_module = _fastcall
+    return _fast_module
+
+
 class BlkError(RuntimeError):
     def __init__(self, status, msg=""):
         self.status = status
@@ -233,6 +248,10 @@ class DecoderBlock:
         self._dtype = torch.bfloat16 if self.desc.dtype == 1 else torch.float32
         self._sizes = n_heads, n_kv_heads, head_dim
         self._axes = {}  # (sections, interleaved) -> blk_rope_axes
+        # the packed calls' short way; what it returns None for takes the long one
+        self._fast = fastcall()
+        self._block = self._fast.block(h.value, n_heads, n_kv_heads, head_dim, self.desc.dtype == 1, self._dev,
+                                       self.desc.qk_norm, self.desc.no_rope)
         # the current stream's handle, without building a Stream object where torch has the short way
         self._raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
             (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
@@ -248,6 +267,7 @@ class DecoderBlock:
 
     def close(self):
         if self.handle:
+            self._block = None  # the short way is closed with the handle
             lib().blk_destroy(self.handle)
             self.handle = None
 
@@ -401,6 +421,10 @@ class DecoderBlock:
         and k [N, Hkv, d], of any row and head strides. positions: int32 [N], or [axes, N] with
         `sections`, the rotary pairs of each axis (one after the other, or interleaved). Returns
         (q_out, k_out), [N, heads, d]; pass q and k as outputs to work in place."""
+        if stream is None:
+            r = self._fast.qk_norm_rope(self._block, q, k, positions, q_gain, k_gain, sections, interleaved, q_out, k_out)
+            if r is not None:
+                return r
         if self._elsewhere(stream):
             with _on_stream(self._device, stream):
                 return self.qk_norm_rope(q, k, positions, q_gain, k_gain, sections, interleaved, q_out, k_out)
@@ -436,6 +460,10 @@ class DecoderBlock:
         head strides; cu_seqlens int32 [B + 1]: sequence b is rows cu_seqlens[b] .. cu_seqlens[b + 1] - 1.
         Returns out [N, H, d]; rows of no sequence are left as they were (undefined in an out
         made here)."""
+        if stream is None:
+            r = self._fast.attn_packed(self._block, q, k, v, cu_seqlens, out)
+            if r is not None:
+                return r
         if self._elsewhere(stream):
             with _on_stream(self._device, stream):
                 return self.attn_packed(q, k, v, cu_seqlens, out)
@@ -478,6 +506,8 @@ class DecoderBlock:
         attn_packed; None: row b alone) to slots starts[b], ... (None: lens[b], an append), and sets
         lens[b] behind them. host_lens_max: the largest new length, to have the capacity checked
         here; else rows that do not fit are left out and last_status() says so."""
+        if stream is None and self._fast.kv4_store(self._block, cache, k, v, cu_seqlens, starts, host_lens_max):
+            return
         if self._elsewhere(stream):
             with _on_stream(self._device, stream):
                 return self.kv4_store(cache, k, v, cu_seqlens, starts, host_lens_max)
@@ -492,6 +522,10 @@ class DecoderBlock:
     def kv4_load(self, cache, cu_seqlens=None, rows=None, starts=None, k_out=None, v_out=None, stream=None):
         """The values of the cache's slots starts[b], ... (None: 0, ...) as packed bf16 rows (k, v)
         [rows, Hkv, 128]: the rows that cu_seqlens gives each sequence (None: one each)."""
+        if stream is None:
+            r = self._fast.kv4_load(self._block, cache, cu_seqlens, rows, starts, k_out, v_out)
+            if r is not None:
+                return r
         if self._elsewhere(stream):
             with _on_stream(self._device, stream):
                 return self.kv4_load(cache, cu_seqlens, rows, starts, k_out, v_out)
@@ -507,6 +541,10 @@ class DecoderBlock:
     def attn_decode_kv4(self, q, cache, out=None, stream=None):
         """One query per sequence, q [B, H, 128], over the lens[b] slots of the 4-bit cache (the last
         sliding_window of them). Returns out [B, H, 128]; a sequence without keys gets zeros."""
+        if stream is None:
+            r = self._fast.attn_decode_kv4(self._block, q, cache, out)
+            if r is not None:
+                return r
         if self._elsewhere(stream):
             with _on_stream(self._device, stream):
                 return self.attn_decode_kv4(q, cache, out)

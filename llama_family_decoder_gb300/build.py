@@ -1,8 +1,10 @@
-"""Builds libblk.so (the C-ABI library) in-tree for sm_103a with nvcc.
+"""Builds libblk.so (the C-ABI library) in-tree for sm_103a with nvcc, and _fastcall.so.
 
 Each .cu translation unit compiles in parallel to an object under _build/, then
 nvcc links the shared library next to this file. A unit is recompiled only when
-it, or a header it includes, is newer than its object.
+it, or a header it includes, is newer than its object. _fastcall.so, the compiled
+argument handling of the packed calls (csrc/fastcall.cpp), is built beside it
+against the installed torch.
 """
 from __future__ import annotations
 
@@ -17,6 +19,9 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libblk.so")
+FAST_SRC = os.path.join(CSRC, "fastcall.cpp")
+FAST_OBJ = os.path.join(BUILD, "fastcall.o")
+FAST = os.path.join(HERE, "_fastcall.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
          "-I", os.path.join(ROOT, "include")]
@@ -41,10 +46,39 @@ def _stale(src, obj, headers):
     return any(os.path.getmtime(f) > t for f in [src, *headers])
 
 
+def _compile_fastcall() -> subprocess.Popen | None:
+    """Starts the compiler on fastcall.cpp if its object is older than its sources."""
+    import sysconfig
+
+    import torch
+
+    if not _stale(FAST_SRC, FAST_OBJ, glob.glob(os.path.join(ROOT, "include", "*.h")) + [torch.__file__]):
+        return None
+    root = os.path.join(os.path.dirname(torch.__file__), "include")
+    cuda = os.path.join(os.path.dirname(os.path.dirname(_nvcc())), "include")
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-I", sysconfig.get_paths()["include"], "-I", root, "-I", os.path.join(root, "torch", "csrc", "api", "include"),
+           "-I", cuda, "-c", FAST_SRC, "-o", FAST_OBJ]
+    return subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
+
+
+def _link_fastcall():
+    """Links _fastcall.so against the libblk.so beside it and the installed torch."""
+    import torch
+
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    cmd = ["g++", "-shared", FAST_OBJ, "-o", FAST, "-L", HERE, "-l:libblk.so", "-L", lib, "-ltorch_python", "-ltorch_cpu",
+           "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+
+
 def build(verbose: bool = False, jobs: int | None = None) -> str:
     """Compiles the CUDA sources and links libblk.so; returns its path."""
     os.makedirs(BUILD, exist_ok=True)
     nvcc = _nvcc()
+    fast = _compile_fastcall()
     srcs = sorted(glob.glob(os.path.join(CSRC, "*.cu")))
     headers = _headers()
     objs = [os.path.join(BUILD, os.path.basename(s)[:-3] + ".o") for s in srcs]
@@ -68,6 +102,12 @@ def build(verbose: bool = False, jobs: int | None = None) -> str:
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
             raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+    if fast is not None:
+        out, _ = fast.communicate()
+        if fast.returncode != 0:
+            raise RuntimeError(f"g++ failed on {os.path.basename(FAST_SRC)}:\n{out}")
+    if _stale(FAST_OBJ, FAST, []):
+        _link_fastcall()
     return LIB
 
 

@@ -119,3 +119,21 @@ def test_packed_stage_argument_checks_on_host(L):
     assert b"NULL handle" in L.blk_last_error_message()
     assert L.blk_attn_packed_workspace_bytes(None, 8, 1) == 0
     assert L.blk_attn_decode_kv4_workspace_bytes(None, 1, 8) == 0
+
+
+def test_compiled_argument_handling_leaves_what_is_not_plain(L):
+    # None, without an exception, for whatever the long way has to look at
+    import torch
+
+    from llama_family_decoder_gb300 import binding as b
+    f = b.fastcall()
+    blk = f.block(0, 4, 2, 128, 1, 0, 0, 0)
+    x = torch.zeros(8, 4, 128, dtype=torch.bfloat16)
+    for first in (None, blk, 3, "block"):
+        for a in (None, x, "x", {}, {"k": x}):
+            assert f.qk_norm_rope(first, a, a, a, a, a, a, a, a, a) is None
+            assert f.attn_packed(first, a, a, a, a, a) is None
+            assert f.kv4_store(first, a, a, a, a, a, a) is None
+            assert f.kv4_load(first, a, a, a, a, a, a) is None
+            assert f.attn_decode_kv4(first, a, a, a) is None
+    assert f.attn_packed() is None  # not the number of arguments

@@ -12,8 +12,8 @@ Bounds count roundings. bf16 rounds by at most u = 2^-8 of the value (half a ste
    output once: u sum(p |v|) + u |o|. Scores are sums of 128 exact products in fp32, off by at
    most 128 * 2^-23 sum|q k| / sqrt(128); exp adds 2^-22. Both under 2e-4 of sum(p |v|) at
    these inputs.
- - decode over 4 bits: p is rounded to bf16 for all terms of a value (u |value|), p * scale once
-   more (u scale |code - 8|), the output once; a score is a sum of exact products
+ - decode over 4 bits: p is rounded to bf16 for all terms of a value (u |value|), p * scale goes
+   in as two bf16 numbers (u^2 scale |code - 8|), the output is rounded once; a score is a sum of exact products
    (of a group's sum of q in 24 bits with its offset) in fp32, off by at most
    2^-21 sum|q| (15 scale + |offset|) / sqrt(128).
 """
@@ -555,7 +555,7 @@ def check_decode(out, q, k, v, lens, window=0):
             qa = np.abs(qh).reshape(4, 32).sum(-1)
             delta = 2.0 ** -21 * ((15 * ks[:, j] + np.abs(kz[:, j])) @ qa).max() / np.sqrt(D) + 1e-6
             ref = p @ V[:, j]
-            bound = U * (p @ np.abs(V[:, j])) + U * (1 + U) * (p @ code[:, j]) + U * np.abs(ref) + \
+            bound = U * (p @ np.abs(V[:, j])) + U * U * (1 + U) * (p @ code[:, j]) + U * np.abs(ref) + \
                 np.expm1(2 * delta) * (p @ np.abs(V[:, j])) + 2.0 ** -18 * (p @ parts[:, j])
             err = np.abs(np64(out[b, h]) - ref)
             assert np.all(err <= bound), (b, h, float((err / bound).max()))
@@ -797,3 +797,60 @@ def test_refusals():
     assert L.blk_attn_decode_kv4(blk.handle, r(q), kv4(c), 500, r(o), None, need, None) == 7
     assert L.blk_attn_decode_kv4(blk.handle, r(q), kv4(c), 500, r(o), ws.data_ptr(), need, None) == 0
     torch.cuda.synchronize()
+
+
+def test_short_and_long_way_agree(monkeypatch):
+    """The compiled argument handling takes every plain call, and what it leaves out (here: all of
+    them) gives the same to the bit; it keeps no argument or output alive."""
+    import sys
+
+    class Nothing:
+        def __getattr__(self, name):
+            return lambda *a: None
+
+    H, Hkv, lens = 8, 2, [5, 0, 70, 1]
+    n = sum(lens)
+    blk = block(H, Hkv, qk_norm=True)
+    qkv, g, cu = randn(1, n, H + 2 * Hkv, D), randn(2, 2, D), cu_of(lens)
+    q, k, v = qkv[:, :H], qkv[:, H:H + Hkv], qkv[:, H + Hkv:]
+    pos, axes, q1, starts = ints(list(range(n))), ints([list(range(n))] * 3), randn(3, len(lens), H, D), ints([3, 0, 1, 0])
+
+    def calls():
+        c = blk.kv4_cache(len(lens), 90)
+        res = [*blk.qk_norm_rope(q, k, pos, g[0], g[1]),
+               *blk.qk_norm_rope(q, k, axes, g[0], g[1], sections=[24, 20, 20], interleaved=True),
+               *blk.qk_norm_rope(q, k, axes, g[0], g[1], sections=(24, 20, 20)),
+               blk.attn_packed(q, k, v, cu)]
+        assert blk.kv4_store(c, k, v, cu, host_lens_max=70) is None
+        blk.kv4_store(c, q1[:, :Hkv], q1[:, Hkv:2 * Hkv])
+        blk.kv4_store(c, k, v, cu, starts=starts)
+        return res + [*blk.kv4_load(c, cu, n, starts=starts), *blk.kv4_load(c), blk.attn_decode_kv4(q1, c),
+                      *[c[x] for x in ("k", "k_scale", "v", "v_scale", "lens")]]
+
+    fast, taken = blk._fast, []
+
+    class Counted:
+        def __getattr__(self, name):
+            return lambda *a: (taken.append((r := getattr(fast, name)(*a)) is not None), r)[1]
+
+    held = [q, k, v, cu, pos, axes, q1, starts, g]
+    before = [sys.getrefcount(x) for x in held]
+    monkeypatch.setattr(blk, "_fast", Counted())
+    short = calls()
+    assert len(taken) == 10 and all(taken)
+    monkeypatch.setattr(blk, "_fast", Nothing())
+    long = calls()
+    for a, b in zip(short, long, strict=True):
+        assert torch.equal(a, b) and a.shape == b.shape and a.stride() == b.stride()
+    assert before == [sys.getrefcount(x) for x in held]
+    # given outputs come back as they are
+    monkeypatch.setattr(blk, "_fast", fast)
+    out = torch.empty_like(short[6])
+    count = sys.getrefcount(out)
+    assert blk.attn_packed(q, k, v, cu, out=out) is out and torch.equal(out, short[6])
+    assert sys.getrefcount(out) == count
+    # a closed handle is refused
+    blk.close()
+    with pytest.raises(BlkError) as e:
+        blk.attn_packed(q, k, v, cu)
+    assert e.value.status == 1
