@@ -35,6 +35,15 @@
 // over the last W positions (key tiles before the first query's oldest key are
 // skipped, the rest masked), and a per-channel gate on the output; a padded batch
 // hides the keys outside each sequence's run of real tokens.
+// Packed sequences (PACKED) go through the same loop with 512 threads (see kPackedThreads):
+// whole prompts of any lengths, the heads of a KV head folded into a tile's rows. Bound by the
+// chain of a tile pair (scores, softmax, PV: 3250 cycles, of which the tensor core works 2048),
+// by the tiles on the diagonal and by item boundaries (4000 cycles): 412 us, 1.33 PFLOP/s, for
+// one sequence of 8190 (32 heads of their own), 113 us, 1.0 PFLOP/s, for 8 ragged ones of up to
+// 2048 (32 heads over 8). Measured and not kept: sixteen softmax warps, two threads a row, with
+// the scores read twice from tensor memory (498 us for the long one; held in registers they
+// spill, and shared memory leaves too little L1 for that: 1167); outputs staged in shared
+// memory for whole-row stores (48 short turns 39 -> 41 us); a third Q buffer (27 -> 28 us).
 // Every wait is bounded; on expiry the CTA records a timeout, drains its own
 // copies and MMAs, frees its TMEM and returns.
 #include <cuda_fp16.h>
@@ -126,27 +135,6 @@ __device__ __forceinline__ float ex2_approx(float x) {
   return y;
 }
 
-// Blackwell's packed fp32 arithmetic: two lanes of fp32 in one 64-bit register pair,
-// one instruction for both (each lane rounded as its scalar form would be).
-typedef unsigned long long f32x2;
-__device__ __forceinline__ f32x2 f2_make(float lo, float hi) {
-  f32x2 r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-  return r;
-}
-__device__ __forceinline__ void f2_split(f32x2 v, float& lo, float& hi) {
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
-}
-__device__ __forceinline__ f32x2 f2_fma(f32x2 a, f32x2 b, f32x2 c) {
-  f32x2 d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-  return d;
-}
-__device__ __forceinline__ f32x2 f2_add(f32x2 a, f32x2 b) {
-  f32x2 d;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
 // max of three (one instruction; like fmaxf, a NaN operand is ignored)
 __device__ __forceinline__ float fmax3(float a, float b, float c) {
   float d;
@@ -345,8 +333,8 @@ __device__ __noinline__ int own_work(const AttnParams& p, uint8_t* scratch, int 
 // head side by side (AttnParams::fold): a box of the Q map is 2^fold heads of 128 / 2^fold
 // queries, so that short sequences fill the tile and all rows of it share the K/V tiles.
 // SPLIT: both slots work on the same queries, slot g on the key tiles j % 2 == g through its own
-// K and V stage; slot 0 joins the two results from tensor memory. Twice as many items of half
-// the length, for batches whose items are too few to fill the SMs evenly.
+// K and V stage; the epilogue joins the two results from tensor memory. Twice as many items of
+// half the length, for batches whose items are too few to fill the SMs evenly.
 template <bool F16, bool PACKED, bool SPLIT>
 __global__ void __launch_bounds__(PACKED ? kPackedThreads : kThreads, 1) attn_tc_kernel(const __grid_constant__ AttnParams p) {
   pdl_launch_dependents();
@@ -1147,11 +1135,11 @@ namespace {
 
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanBins = 4096;
-// The work list of packed sequences, heaviest first: an entry per `step` queries, ordered by its place in its sequence, which its key count grows
-// with. One CTA counts the entries of each place, sums the counts from the far places
-// down, and deals the entries out; the order within a place does not matter (items are
-// independent, so no result depends on it). A cu that does not rise from 0 to at most
-// `rows` records INVALID_ARG and is read clamped.
+// The work list of packed sequences, heaviest first: an entry per `step` queries, ordered by its
+// place in its sequence, which its key count grows with. One CTA counts the entries of each
+// place, sums the counts from the far places down, and deals the entries out; the order within
+// a place does not matter (items are independent, so no result depends on it). A cu that does
+// not rise from 0 to at most `rows` records INVALID_ARG and is read clamped.
 __global__ void __launch_bounds__(kPlanThreads) packed_plan_kernel(const int* __restrict__ cu, int B, int rows, int step,
                                                                    int cap, PackedWork* __restrict__ work,
                                                                    int* __restrict__ n_work, DevStatus* st) {
