@@ -32,9 +32,9 @@
 // Small batches take clusters instead (see CL below). 160 bytes a key and KV head: HBM bounds it,
 // then the integer pipe, which unpacks the codes (51% busy, and half-rate). 64 ragged sequences
 // of up to 8192 keys, 32 heads over 8: 98.1 us, 4.3 TB/s; one of 4000 keys: 7.8 us. Measured and
-// not kept, when the kernel took 90.5 us: a producer warp with a ring for all (93), three stages
-// (91.5), two CTAs of 200 registers (95), eight warps a CTA (98); and e4m3 operands, one product
-// of which takes as long as the two fp16 ones that it would stand for.
+// not kept: a producer warp with a ring for all warps (93 us against 90.5); before that, against
+// 96 us, three stages (97), two CTAs of 200 registers (100), one of eight warps (103); and e4m3
+// operands, one product of which takes as long as the two fp16 ones that it would stand for.
 #include <cuda_fp16.h>
 
 #include <algorithm>

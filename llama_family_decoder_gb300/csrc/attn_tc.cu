@@ -46,6 +46,7 @@
 // memory for whole-row stores (48 short turns 39 -> 41 us); a third Q buffer (27 -> 28 us).
 // Every wait is bounded; on expiry the CTA records a timeout, drains its own
 // copies and MMAs, frees its TMEM and returns.
+#include <cudaTypedefs.h>
 #include <cuda_fp16.h>
 
 #include <algorithm>
@@ -1132,6 +1133,28 @@ cudaError_t launch_attn_prefill_tc(const void* q, const void* k, const void* v, 
 // ------------------------------------------------------------------ packed sequences
 
 namespace {
+
+// 3-D TMA map over bf16 head rows: boxes of 64 channels x box_heads x box_rows rows, 128-byte
+// swizzle, zero fill out of bounds. Strides in multiples of 8 elements.
+bool make_tma_heads_bf16(CUtensorMap* m, const HeadRows& x, int rows, int heads, int d, int box_heads, int box_rows) {
+  static const PFN_cuTensorMapEncodeTiled_v12000 encode = [] {
+    void* ptr = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q);
+    return e == cudaSuccess && q == cudaDriverEntryPointSuccess ? reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr)
+                                                                : nullptr;
+  }();
+  if (!encode) return false;
+  // the stride of a dimension of one element is never used, but has to be a valid one
+  const long long head = heads > 1 ? x.head : d, row = rows > 1 ? x.row : (long long)d * heads;
+  const cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)heads, (cuuint64_t)rows};
+  const cuuint64_t strides[2] = {(cuuint64_t)head * 2, (cuuint64_t)row * 2};
+  const cuuint32_t box[3] = {64, (cuuint32_t)box_heads, (cuuint32_t)box_rows};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, x.ptr, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
 
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanBins = 4096;

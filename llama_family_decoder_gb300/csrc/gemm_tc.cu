@@ -1583,20 +1583,6 @@ bool make_tma_2d_16b(CUtensorMap* m, const void* ptr, int rows, int cols, int bo
   return make_map(m, ptr, rows, cols, box_rows, f16);
 }
 
-bool make_tma_heads_bf16(CUtensorMap* m, const HeadRows& x, int rows, int heads, int d, int box_heads, int box_rows) {
-  auto fn = encode_fn();
-  if (!fn) return false;
-  // the stride of a dimension of one element is never used, but has to be a valid one
-  const long long head = heads > 1 ? x.head : d, row = rows > 1 ? x.row : (long long)d * heads;
-  cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)heads, (cuuint64_t)rows};
-  cuuint64_t strides[2] = {(cuuint64_t)head * 2, (cuuint64_t)row * 2};
-  cuuint32_t box[3] = {64, (cuuint32_t)box_heads, (cuuint32_t)box_rows};
-  cuuint32_t estr[3] = {1, 1, 1};
-  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, x.ptr, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 namespace {
 
 template <int BN, int EPI, bool PAIR = false>

@@ -206,10 +206,6 @@ struct TcGemmDesc {
 // columns x box_rows rows, 128-byte swizzle, zero fill out of bounds.
 bool make_tma_2d_16b(CUtensorMap* m, const void* ptr, int rows, int cols, int box_rows, bool f16);
 
-// 3-D TMA map over bf16 head rows: boxes of 64 channels x box_heads x box_rows rows, 128-byte
-// swizzle, zero fill out of bounds. Strides in multiples of 8 elements.
-bool make_tma_heads_bf16(CUtensorMap* m, const HeadRows& x, int rows, int heads, int d, int box_heads, int box_rows);
-
 cudaError_t launch_tc_gemm(const TcGemmDesc& d, int max_ctas, DevStatus* st, unsigned long long wait_ns,
                            cudaStream_t s, const char** why);
 
