@@ -799,6 +799,45 @@ def test_refusals():
     torch.cuda.synchronize()
 
 
+def test_far_rows_and_slots():
+    """Rows more than 2^31 elements apart and slots behind 2^31 bytes give what near ones do, and
+    nothing else is written."""
+    n, H, Hkv, cap, lens = 70, 4, 2, 1 << 25, [40, 30]
+    blk = block(H, Hkv, qk_norm=True)
+    step = (1 << 25) + 64
+    far = torch.zeros(n * step, dtype=torch.bfloat16, device=DEV)
+
+    def rows(first, heads):
+        return far.as_strided((n, heads, D), (step, D, 1), first * D)
+
+    q, k, v = randn(1, n, H, D), randn(2, n, Hkv, D), randn(3, n, Hkv, D)
+    fq, fk, fv, fo = rows(0, H), rows(H, Hkv), rows(H + Hkv, Hkv), rows(H + 2 * Hkv, H)
+    for a, b in ((fq, q), (fk, k), (fv, v)):
+        a.copy_(b)
+    pos, g, cu = ints(list(range(n))), randn(4, 2, D), cu_of(lens)
+    q, k = blk.qk_norm_rope(q, k, pos, g[0], g[1])
+    blk.qk_norm_rope(fq, fk, pos, g[0], g[1], q_out=fq, k_out=fk)
+    assert torch.equal(fq, q) and torch.equal(fk, k)
+    o = blk.attn_packed(q, k, v, cu)
+    blk.attn_packed(fq, fk, fv, cu, out=fo)
+    assert torch.equal(fo, o)
+    near, big = blk.kv4_cache(2, 64), blk.kv4_cache(2, cap)  # 2^25 slots of 64 bytes: a plane of 2^31
+    starts = ints([cap - 64, cap - 50])
+    blk.kv4_store(near, k, v, cu)
+    blk.kv4_store(big, fk, fv, cu, starts=starts)
+    assert big["lens"].tolist() == [cap - 24, cap - 20]
+    for x in ("k", "k_scale", "v", "v_scale"):
+        for b, (f, m) in enumerate(zip(starts.tolist(), lens)):
+            assert torch.equal(big[x][b, :, f:f + m], near[x][b, :, :m])
+            assert not big[x][b, :, f + m:].any() and not big[x][b, :, f - 64:f].any()
+    kk, vv = blk.kv4_load(near, cu, n)
+    blk.kv4_load(big, cu, n, starts=starts, k_out=fk, v_out=fv)
+    assert torch.equal(fk, kk) and torch.equal(fv, vv)
+    assert blk.last_status() == 0
+    used = (2 * H + 2 * Hkv) * D
+    assert not far.as_strided((n - 1, 4096), (step, 1), used).any()  # behind each row's channels
+
+
 def test_short_and_long_way_agree(monkeypatch):
     """The compiled argument handling takes every plain call, and what it leaves out (here: all of
     them) gives the same to the bit; it keeps no argument or output alive."""
