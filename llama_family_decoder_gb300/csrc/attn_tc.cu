@@ -252,74 +252,59 @@ __device__ __forceinline__ Item item_of(const AttnParams& p, int id, const Packe
 __device__ __forceinline__ int item_id(int k, int G, int c) { return k * G + ((k & 1) ? G - 1 - c : c); }
 
 // The work list of packed sequences (heaviest first, an entry per `step` queries, ordered by its
-// place in its sequence, which its key count grows with, then by sequence), made by a whole CTA
-// in `scratch`; mine[k] := the entry of the CTA's item k. Returns the number of items. The order
-// is the same in every CTA: ballots over the sequences rank those that reach a place. A cu that
-// does not rise from 0 to at most the rows records INVALID_ARG and is read clamped.
-constexpr int kOwnSeqs = 2048, kOwnEntries = 8192;
+// place in its sequence, which its key count grows with, then by sequence), as far as a CTA
+// needs it: mine[k] := the entry of the CTA's item k. Returns the number of items. The order
+// is the same in every CTA. F(t), the entries at places t and farther, falls with t: the place
+// of entry e is the last t with F(t) > e, found by halving, and its sequence is the one number
+// e - F(t + 1) of those that reach t. A warp finds an item at a time; `scratch` holds the
+// sequences. A cu that does not rise from 0 to at most the rows records INVALID_ARG and is read
+// clamped.
+constexpr int kOwnSeqs = 2048;
 __device__ __noinline__ int own_work(const AttnParams& p, uint8_t* scratch, int units, PackedWork* mine) {
-  int* first = reinterpret_cast<int*>(scratch);  // [B] a sequence's first row, its length, its entries
-  int* len = first + kOwnSeqs;
-  int* n_of = len + kOwnSeqs;
-  int* at = n_of + kOwnSeqs;                     // [places] entries of a place, then of all farther ones
-  int* list = at + kOwnEntries;                  // sequence + place * kOwnSeqs
-  int* top = list + kOwnEntries;
-  static_assert((3 * kOwnSeqs + 2 * kOwnEntries + 2) * 4 <= (kKStages + kVStages) * kKVBytes, "scratch");
+  int* n_of = reinterpret_cast<int*>(scratch);                 // [B] a sequence's entries
+  int2* rows = reinterpret_cast<int2*>(n_of + kOwnSeqs);       // its first row and its length
+  static_assert(kOwnSeqs * 12 <= (kKStages + kVStages) * kKVBytes, "scratch");
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;
-  if (tid == 0) top[0] = 0;
-  __syncthreads();
   bool bad = false;
   for (int b = tid; b < p.B; b += blockDim.x) {
     const int a = p.cu[b], e = p.cu[b + 1];
     const int lo = min(max(a, 0), p.T), hi = min(max(e, lo), p.T);
     bad |= lo != a || hi != e;
-    first[b] = lo;
-    len[b] = hi - lo;
+    rows[b] = make_int2(lo, hi - lo);
     n_of[b] = (hi - lo + p.step - 1) / p.step;
-    atomicMax(&top[0], n_of[b]);
   }
   if (bad && blockIdx.x == 0 && p.status) atomicCAS(&p.status->code, 0, kStatusInvalidArg);
   __syncthreads();
-  const int places = min(top[0], kOwnEntries);
-  for (int t = warp; t < places; t += warps) {
+  auto from = [&](int t) {  // F(t)
     int n = 0;
-    for (int b = lane; b - lane < p.B; b += 32) n += __popc(__ballot_sync(0xffffffffu, b < p.B && n_of[b] > t));
-    if (lane == 0) at[t] = n;
-  }
-  __syncthreads();
-  if (warp == 0) {  // the entries of all farther places, from the last place down
-    int before = 0;
-    for (int t0 = places - 1; t0 >= 0; t0 -= 32) {
-      const int t = t0 - lane, n = t >= 0 ? at[t] : 0;
-      int run = n;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int u = __shfl_up_sync(0xffffffffu, run, o);
-        if (lane >= o) run += u;
-      }
-      if (t >= 0) at[t] = before + run - n;
-      before += __shfl_sync(0xffffffffu, run, 31);
-    }
-    if (lane == 0) top[1] = min(before, p.cap);  // sequences that overlap could have more
-  }
-  __syncthreads();
-  for (int t = warp; t < places; t += warps) {
-    int to = at[t];
-    for (int b = lane; b - lane < p.B; b += 32) {
-      const bool in = b < p.B && n_of[b] > t;
-      const uint32_t all = __ballot_sync(0xffffffffu, in);
-      const int i = to + __popc(all & ((1u << lane) - 1u));
-      if (in && i < kOwnEntries) list[i] = b + t * kOwnSeqs;
-      to += __popc(all);
-    }
-  }
-  __syncthreads();
-  const int n_items = top[1] * units;
-  for (int k = tid; k < kOwnItems; k += blockDim.x) {
+#pragma unroll 4
+    for (int b = lane; b < p.B; b += 32) n += max(n_of[b] - t, 0);
+    return (int)__reduce_add_sync(0xffffffffu, n);
+  };
+  int places = 0;
+  for (int b = lane; b < p.B; b += 32) places = max(places, n_of[b]);
+  places = __reduce_max_sync(0xffffffffu, places);
+  const int n_items = min(from(0), p.cap) * units;  // sequences that overlap could have more
+  for (int k = warp; k < kOwnItems; k += warps) {
     const int id = item_id(k, gridDim.x, blockIdx.x);
-    if (id < n_items) {
-      const int e = list[id / units], b = e % kOwnSeqs;
-      mine[k] = {first[b], len[b], e / kOwnSeqs * p.step, 0};
+    if (id >= n_items) break;
+    const int e = id / units;
+    int lo = 0, hi = places, before = 0;  // F(lo) > e >= F(hi) == before
+    while (hi - lo > 1) {
+      const int t = (lo + hi) / 2, n = from(t);
+      if (n > e) {
+        lo = t;
+      } else {
+        hi = t;
+        before = n;
+      }
+    }
+    int left = e - before;
+    for (int b = lane; left >= 0 && b - lane < p.B; b += 32) {
+      const bool in = b < p.B && n_of[b] > lo;
+      const uint32_t all = __ballot_sync(0xffffffffu, in);
+      if (in && __popc(all & ((1u << lane) - 1u)) == left) mine[k] = {rows[b].x, rows[b].y, lo * p.step, 0};
+      left -= __popc(all);
     }
   }
   return n_items;
@@ -781,9 +766,11 @@ __global__ void __launch_bounds__(PACKED ? kPackedThreads : kThreads, 1) attn_tc
           const int a = lim - 32 * q4, b = first - 32 * q4;
           const uint32_t bits = (a >= 31 ? ~0u : a < 0 ? 0u : (2u << a) - 1u) & (b <= 0 ? ~0u : b > 31 ? 0u : ~0u << b);
           tc_wait_ld();
+          if (!__all_sync(0xffffffffu, bits == ~0u)) {
 #pragma unroll
-          for (int i = 0; i < 32; ++i)
-            if (!(bits & (1u << i))) x[i] = -INFINITY;
+            for (int i = 0; i < 32; ++i)
+              if (!(bits & (1u << i))) x[i] = -INFINITY;
+          }
         };
         float mraw = -INFINITY;
 #pragma unroll 1
@@ -1177,14 +1164,18 @@ __global__ void __launch_bounds__(kPlanThreads) packed_plan_kernel(const int* __
   __syncthreads();
   bool bad = false;
   for (int pass = 0; pass < 2; ++pass) {
-    for (int b = warp; b < B; b += kPlanThreads / 32) {  // a warp per sequence
-      const int a = cu[b], e = cu[b + 1];
-      const int lo = min(max(a, 0), rows), hi = min(max(e, lo), rows);
-      bad |= lo != a || hi != e;
-      const int n = (hi - lo + step - 1) / step;
-      for (int t = lane; t < n; t += 32) {
-        const int at = atomicAdd(&count[t / per_bin], 1);
-        if (pass == 1 && at < cap) work[at] = {lo, hi - lo, t * step, 0};
+    for (int b0 = 32 * warp; b0 < B; b0 += kPlanThreads) {  // 32 sequences a warp, one after another
+      const int b = b0 + lane, a = b < B ? cu[b] : 0, e = b < B ? cu[b + 1] : 0;
+      const int lo = min(max(a, 0), rows), len = min(max(e, lo), rows) - lo;
+      bad |= lo != a || lo + len != e;
+      const int n = (len + step - 1) / step;
+      for (int i = 0; i < min(32, B - b0); ++i) {
+        const int row0 = __shfl_sync(0xffffffffu, lo, i), its = __shfl_sync(0xffffffffu, len, i);
+        const int last = __shfl_sync(0xffffffffu, n, i);
+        for (int t = lane; t < last; t += 32) {
+          const int at = atomicAdd(&count[t / per_bin], 1);
+          if (pass == 1 && at < cap) work[at] = {row0, its, t * step, 0};
+        }
       }
     }
     __syncthreads();
@@ -1241,10 +1232,10 @@ PackedPlan packed_plan(int rows, int B, int H, int Hkv, int num_sms) {
   // one CTA per SM, more only where a CTA would have more items than it keeps entries for
   const long long most = (long long)p.cap * p.units;
   p.grid = (int)std::max(std::min<long long>(most, num_sms), (most + kOwnItems - 1) / kOwnItems);
-  // The list costs its ballots (about 30 cycles, 16 warps at once) in every CTA, or a launch of its
-  // own before the attention (48 turns of 10 to 200 queries: 24.9 us, 27.2 with that launch).
-  const long long ballots = (long long)((rows + p.step - 1) / p.step) * ((B + 31) / 32);
-  p.own = B <= kOwnSeqs && p.cap <= kOwnEntries && ballots <= 2048;
+  // The list costs its sums in every CTA, or a launch of its own before the attention: 48 turns of
+  // 10 to 200 queries 25.2 us, 27.5 with that launch; 2000 sequences of 10 (8 heads over 2) 81 and
+  // 113; 4000 of 60 (32 over 8) 1479 and 1405. And the sums have to fit 32 bits.
+  p.own = B <= kOwnSeqs && B * (long long)((rows + p.step - 1) / p.step) <= INT32_MAX;
   return p;
 }
 

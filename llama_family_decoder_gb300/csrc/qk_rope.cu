@@ -162,9 +162,11 @@ __global__ void __launch_bounds__(kThreads, kBlocks) qk_norm_rope_kernel(const _
 template <typename T, int L>
 cudaError_t launch_l(RopeParams p, int num_sms, cudaStream_t s) {
   const int groups = (p.H + p.Hkv + 32 / L - 1) / (32 / L);  // warp loads of a row
-  // one warp per row when the rows alone fill the SMs (32 warps each), more when they do not
+  // one warp per row when the rows alone bring 24 warps to each SM, more when they do not.
+  // 1200 bf16 rows of 40 heads 6.6 us, 2000 in fp32 9.3; with 32 warps an SM 7.9 and 10.1, with 12
+  // 7.4 and 11.9.
   int w = 1;
-  while (w < groups && (long long)p.rows * w < 32ll * num_sms) w *= 2;
+  while (w < groups && (long long)p.rows * w < 24ll * num_sms) w *= 2;
   p.warps_per_row = w < groups ? w : groups;
   const long long warps = (long long)p.rows * p.warps_per_row;
   const long long grid = (warps + kThreads / 32 - 1) / (kThreads / 32);

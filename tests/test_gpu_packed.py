@@ -231,7 +231,8 @@ def test_attn_packed(lens, H, Hkv):
     check_packed(out, q, k, v, lens)
 
 
-@pytest.mark.parametrize("lens", [[1] * 3000, [0] * 2500 + [300, 5] + [0] * 10, [3] * 700 + [140] * 20, [600] * 40])
+@pytest.mark.parametrize("lens", [[1] * 3000, [0] * 2500 + [300, 5] + [0] * 10, [3] * 700 + [140] * 20, [600] * 40,
+                                  [1] * 9000, [0] * 8180 + [300, 5, 64, 1] + [0] * 8, [0] * 8180 + [300, 5, 64, 1] + [0] * 9])
 def test_attn_packed_many_sequences(lens):
     """Batches whose work list a kernel of its own makes, and some near that border."""
     n, H, Hkv = sum(lens), 4, 1
@@ -775,11 +776,11 @@ def test_refusals():
     assert L.blk_attn_packed(*args, None, 0, None) == 0
     assert L.blk_attn_packed(*args[:5], None, *args[6:], None, 0, None) == 1
     assert L.blk_attn_packed(*args[:4], -1, *args[5:], None, 0, None) == 1
-    many = ints([0] * 3000 + [8])
-    need = L.blk_attn_packed_workspace_bytes(blk.handle, 8, 3000)
+    many = ints([0] * 9000 + [8])
+    need = L.blk_attn_packed_workspace_bytes(blk.handle, 8, 9000)
     assert need > 0
     ws = torch.empty(need + 16, dtype=torch.uint8, device=DEV)
-    args = (*args[:5], many.data_ptr(), 3000, args[7])
+    args = (*args[:5], many.data_ptr(), 9000, args[7])
     assert L.blk_attn_packed(*args, ws.data_ptr(), need - 1, None) == 7
     assert L.blk_attn_packed(*args, None, need, None) == 7
     assert L.blk_attn_packed(*args, ws.data_ptr() + 8, need, None) == 3
