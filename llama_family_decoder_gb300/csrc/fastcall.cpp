@@ -112,7 +112,10 @@ struct Call {
   }
 };
 
-PyObject* none() { Py_RETURN_NONE; }
+PyObject* none() {
+  PyErr_Clear();
+  Py_RETURN_NONE;
+}
 
 // A launch waits when the GPU's queue is full: other threads have the interpreter meanwhile.
 template <class F>
@@ -130,10 +133,10 @@ PyObject* given(PyObject* o, const at::Tensor& made) {
 }
 
 PyObject* pair(PyObject* a, const at::Tensor& ta, PyObject* b, const at::Tensor& tb) {
-  PyObject* r = PyTuple_New(2);
-  if (!r) return nullptr;
-  PyTuple_SET_ITEM(r, 0, given(a, ta));
-  PyTuple_SET_ITEM(r, 1, given(b, tb));
+  PyObject *x = given(a, ta), *y = x ? given(b, tb) : nullptr;
+  PyObject* r = y ? PyTuple_Pack(2, x, y) : nullptr;
+  Py_XDECREF(x);
+  Py_XDECREF(y);
   return r;
 }
 
@@ -171,10 +174,7 @@ PyObject* qk_norm_rope(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
           axes.sections[i] = static_cast<int>(x);
         }
         const int inter = PyObject_IsTrue(a[7]);
-        if (inter < 0) {
-          PyErr_Clear();
-          return none();
-        }
+        if (inter < 0) return none();
         axes.interleaved = inter;
       }
       const at::Tensor* t = c.tensor(a[3], at::kInt);
@@ -239,10 +239,7 @@ PyObject* kv4_store(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
     const int* cu = c.ints(a[4], batch + 1);
     const int* starts = c.ints(a[5], batch);
     const long most = PyLong_AsLong(a[6]);
-    if (PyErr_Occurred()) {
-      PyErr_Clear();
-      return none();
-    }
+    if (PyErr_Occurred()) return none();
     if (!c.ok || most > INT32_MAX || most < INT32_MIN || !launched([&] {
           return blk_kv4_store(c.b->h, &k, &v, static_cast<int>(n), cu, starts, static_cast<int>(batch), &cache,
                                static_cast<int>(most), c.stream);
