@@ -81,6 +81,12 @@ constexpr int kVStages = 2;                 // V ring
 constexpr int kSmem = 1024 + kSlots * kQBytes + (kKStages + kVStages) * kKVBytes + 256;
 // + more barriers, the slots' softmax states of an item, and the CTA's own work entries
 constexpr int kOwnItems = 256;
+// The slots take turns (see the softmax) in a CTA with a sequence longer than this. Tiles that are
+// mostly masked are bound by latency, which the slots hide for each other: 64 prompts of 150
+// 101.7 us in turns, 91.4 at their own pace (32 heads of their own), of 400 245 and 231; in the
+// plain tiles of long ones they fall into step (8190 queries 408 and 489, 32 prompts of 800 in 8
+// heads over 2 59.4 and 61.4).
+constexpr int kTurnKeys = 512;
 constexpr int kSmemPacked = kSmem + 32 + kSlots * kBQ * 8 + kOwnItems * 16;
 static_assert(kSmemPacked <= 227 * 1024, "shared memory");
 constexpr float kRescaleLog2 = 8.0f;
@@ -253,14 +259,15 @@ __device__ __forceinline__ int item_id(int k, int G, int c) { return k * G + ((k
 
 // The work list of packed sequences (heaviest first, an entry per `step` queries, ordered by its
 // place in its sequence, which its key count grows with, then by sequence), as far as a CTA
-// needs it: mine[k] := the entry of the CTA's item k. Returns the number of items. The order
+// needs it: mine[k] := the entry of the CTA's item k, longest := the longest of their
+// sequences. Returns the number of items. The order
 // is the same in every CTA. F(t), the entries at places t and farther, falls with t: the place
 // of entry e is the last t with F(t) > e, found by halving, and its sequence is the one number
 // e - F(t + 1) of those that reach t. A warp finds an item at a time; `scratch` holds the
 // sequences. A cu that does not rise from 0 to at most the rows records INVALID_ARG and is read
 // clamped.
 constexpr int kOwnSeqs = 2048;
-__device__ __noinline__ int own_work(const AttnParams& p, uint8_t* scratch, int units, PackedWork* mine) {
+__device__ __noinline__ int own_work(const AttnParams& p, uint8_t* scratch, int units, PackedWork* mine, int* longest) {
   int* n_of = reinterpret_cast<int*>(scratch);                 // [B] a sequence's entries
   int2* rows = reinterpret_cast<int2*>(n_of + kOwnSeqs);       // its first row and its length
   static_assert(kOwnSeqs * 12 <= (kKStages + kVStages) * kKVBytes, "scratch");
@@ -303,7 +310,10 @@ __device__ __noinline__ int own_work(const AttnParams& p, uint8_t* scratch, int 
     for (int b = lane; left >= 0 && b - lane < p.B; b += 32) {
       const bool in = b < p.B && n_of[b] > lo;
       const uint32_t all = __ballot_sync(0xffffffffu, in);
-      if (in && __popc(all & ((1u << lane) - 1u)) == left) mine[k] = {rows[b].x, rows[b].y, lo * p.step, 0};
+      if (in && __popc(all & ((1u << lane) - 1u)) == left) {
+        mine[k] = {rows[b].x, rows[b].y, lo * p.step, 0};
+        atomicMax(longest, rows[b].y);
+      }
       left -= __popc(all);
     }
   }
@@ -334,12 +344,13 @@ __global__ void __launch_bounds__(PACKED ? kPackedThreads : kThreads, 1) attn_tc
   // o_done[2], o_free[2], drain[2]
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + 26);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
+  int* longest = reinterpret_cast<int*>(bars + 27);  // PACKED: the longest sequence of the CTA's items
   // PACKED: each slot's reference and sum of each row, for the epilogue, and the barriers that
   // announce them
   float2* ml = reinterpret_cast<float2*>(bars + 36);
   auto ml_ready = [&](int g) { return smem_u32(&bars[28 + g]); };
   PackedWork* mine = reinterpret_cast<PackedWork*>(ml + kSlots * kBQ);  // PACKED: the CTA's entries, item by item
-  static_assert(26 * 8 + 8 <= 28 * 8, "barriers, the TMEM address, the abort flag");
+  static_assert(27 * 8 + 4 <= 28 * 8, "barriers, the TMEM address, the abort flag, the longest sequence");
   const uint32_t q_full = smem_u32(&bars[0]);
   const uint32_t q_empty = smem_u32(&bars[1]);
   auto k_full = [&](int s) { return smem_u32(&bars[2 + s]); };
@@ -390,6 +401,7 @@ __global__ void __launch_bounds__(PACKED ? kPackedThreads : kThreads, 1) attn_tc
       mbar_init(ml_ready(1), 128);
     }
     *abort_flag = 0;
+    if constexpr (PACKED) *longest = 0;
     fence_mbar_init();
   }
   if (warp == 0 && lane == 0) {
@@ -412,10 +424,13 @@ __global__ void __launch_bounds__(PACKED ? kPackedThreads : kThreads, 1) attn_tc
       n_items = *p.n_work * units;
       for (int k = threadIdx.x; k < kOwnItems; k += blockDim.x) {
         const int id = item_id(k, G, cta);
-        if (id < n_items) mine[k] = p.work[id / units];
+        if (id < n_items) {
+          mine[k] = p.work[id / units];
+          atomicMax(longest, mine[k].len);
+        }
       }
     } else {
-      n_items = own_work(p, sK, units, mine);
+      n_items = own_work(p, sK, units, mine, longest);
       fence_proxy_async_smem();  // the K and V stages served as scratch
     }
     __syncthreads();
@@ -819,8 +834,8 @@ __global__ void __launch_bounds__(PACKED ? kPackedThreads : kThreads, 1) attn_tc
         // The slots take turns (slot 0 tile J, slot 1 tile J, slot 0 tile J + 1, ...): each
         // softmax runs alone on the SM's exponential units while the tensor core works on
         // the other slot's PV and next scores. Slot 1 starts tile J once slot 0's P_J is
-        // written, slot 0 starts tile J + 1 once slot 1's P_J is. (SPLIT: they run at their own pace.)
-        if (!SPLIT && (g == 1 || J >= 1)) {
+        // written, slot 0 starts tile J + 1 once slot 1's P_J is. (At their own pace: see kTurnKeys.)
+        if ((!PACKED || (!SPLIT && *static_cast<volatile int*>(longest) > kTurnKeys)) && (g == 1 || J >= 1)) {
           if (!__all_sync(0xffffffffu, mbar_wait(p_ready(1 - g, 3), (g == 1 ? J : J - 1) & 1, budget, abort_flag))) {
             failed = true;
             break;
