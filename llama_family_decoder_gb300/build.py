@@ -67,7 +67,7 @@ def _link_fastcall():
     import torch
 
     lib = os.path.join(os.path.dirname(torch.__file__), "lib")
-    cmd = ["g++", "-shared", FAST_OBJ, "-o", FAST, "-L", HERE, "-l:libblk.so", "-L", lib, "-ltorch_python", "-ltorch_cpu",
+    cmd = ["g++", "-shared", FAST_OBJ, "-o", FAST, "-L", HERE, "-l:libblk.so", "-L", lib, "-ltorch_python", "-ltorch_cpu", "-ltorch_cuda",
            "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:

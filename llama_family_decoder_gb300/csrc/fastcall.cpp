@@ -1,14 +1,15 @@
 // The packed calls' short way from Python: the checks, outputs and structs that binding.py
 // makes for them, in compiled code. Calls on a few tokens take the GPU 2 to 8 us, so what the
 // host does for them is what they cost: through binding.py a call in a row of such calls took
-// 13 to 16 us, here 5.5 (norm and rotary of 64 tokens) to 8.7 (decode attention; a store with a
-// load 8.8, before 23). Each function returns its outputs, or None for whatever is not a plain call
-// that succeeds: then binding.py makes the call itself and says what is wrong with it. The
-// kernels and their checks are those of the C ABI (blk.h) either way.
+// 13 to 16 us, here 4.3 (norm and rotary of 64 tokens: 1.5 the launch, 2 the two outputs); a store
+// with a load 23, here 6.5; decode attention 14, here 3.2 beside 8 on the GPU. Each function
+// returns its outputs, or None for whatever is not a plain call that succeeds: then binding.py
+// makes the call itself and says what is wrong with it. The kernels and their checks are those
+// of the C ABI (blk.h) either way.
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
-#include <ATen/ops/empty.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -68,8 +69,12 @@ struct Call {
   const int* ints(PyObject* o, int64_t n) {  // None: null
     return o == Py_None ? nullptr : static_cast<const int*>(contiguous(o, at::kInt, n));
   }
+  // torch.empty without its dispatch
+  at::Tensor fresh(at::IntArrayRef size, at::ScalarType type) const {
+    return at::Tensor(at::detail::empty_cuda(size, type, at::Device(at::kCUDA, static_cast<at::DeviceIndex>(b->dev)), std::nullopt));
+  }
   at::Tensor make(int64_t n, int64_t heads) const {
-    return at::empty({n, heads, b->d}, at::TensorOptions().dtype(b->type).device(at::kCUDA, b->dev));
+    return fresh({n, heads, b->d}, b->type);
   }
   // an output: the given tensor, or a new one (kept in `made`)
   blk_head_rows out(PyObject* o, int64_t n, int64_t heads, at::Tensor& made) {
@@ -79,7 +84,7 @@ struct Call {
     return {made.data_ptr(), heads * b->d, b->d};
   }
   at::Tensor scratch(size_t bytes) const {
-    return at::empty({static_cast<int64_t>(bytes)}, at::TensorOptions().dtype(at::kByte).device(at::kCUDA, b->dev));
+    return fresh({static_cast<int64_t>(bytes)}, at::kByte);
   }
   blk_kv4_cache cache(PyObject* o, int64_t& batch) {
     blk_kv4_cache c{};
