@@ -31,7 +31,7 @@
 // Rows behind the last key are filled with zeros, so nothing they hold is ever read.
 // Small batches take clusters instead (see CL below). 160 bytes a key and KV head: HBM bounds it,
 // then the integer pipe, which unpacks the codes (51% busy, and half-rate). 64 ragged sequences
-// of up to 8192 keys, 32 heads over 8: 98.1 us, 4.3 TB/s; one of 4000 keys: 7.8 us. Measured and
+// of up to 8192 keys, 32 heads over 8: 98.1 us, 4.3 TB/s; one of 4000 keys: 7.1 us. Measured and
 // not kept: a producer warp with a ring for all warps (93 us against 90.5); before that, against
 // 96 us, three stages (97), two CTAs of 200 registers (100), one of eight warps (103); and e4m3
 // operands, one product of which takes as long as the two fp16 ones that it would stand for.
@@ -681,23 +681,29 @@ __global__ void __launch_bounds__(kThreads, Cfg<NT>::kCtas) attn_kv4_kernel(cons
     cluster_sync_all();
     for (int h = rank + CL * warp; h < G; h += CL * kWarps) {  // a warp per head, four channels a lane
       const uint32_t mine = smem_u32(shared_out + h * (kD + 4));
-      float4 ov[CL], ml[CL];
+      float m_of[CL], l_of[CL];
 #pragma unroll
       for (int v = 0; v < CL; ++v) {
-        const uint32_t at = map_shared_rank(mine, v);
-        ov[v] = ld_dsmem_f4(at + 16 * lane);
-        ml[v] = ld_dsmem_f4(at + 4 * kD);
+        const float4 x = ld_dsmem_f4(map_shared_rank(mine, v) + 4 * kD);
+        m_of[v] = x.x;
+        l_of[v] = x.y;
       }
       float mm = -INFINITY, ll = 0.f;
 #pragma unroll
-      for (int v = 0; v < CL; ++v) mm = fmaxf(mm, ml[v].x);
+      for (int v = 0; v < CL; ++v) mm = fmaxf(mm, m_of[v]);
       const float mu = mm == -INFINITY ? 0.f : mm;
       float4 oo = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-      for (int v = 0; v < CL; ++v) {
-        const float f = ex2(ml[v].x - mu);
-        ll += ml[v].y * f;
-        oo = make_float4(oo.x + ov[v].x * f, oo.y + ov[v].y * f, oo.z + ov[v].z * f, oo.w + ov[v].w * f);
+      for (int v0 = 0; v0 < CL; v0 += 8) {
+        float4 ov[8];
+#pragma unroll
+        for (int v = 0; v < 8; ++v) ov[v] = ld_dsmem_f4(map_shared_rank(mine, v0 + v) + 16 * lane);
+#pragma unroll
+        for (int v = 0; v < 8; ++v) {
+          const float f = ex2(m_of[v0 + v] - mu);
+          ll += l_of[v0 + v] * f;
+          oo = make_float4(oo.x + ov[v].x * f, oo.y + ov[v].y * f, oo.z + ov[v].z * f, oo.w + ov[v].w * f);
+        }
       }
       const float inv = w.n_tiles > 0 ? 1.f / ll : 0.f;  // no keys: a zero row
       __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.o.ptr) + pair_b * p.o.row +
@@ -784,13 +790,31 @@ Kv4Ws kv4_ws(int B, int H, int Hkv, int num_sms) {
   return w;
 }
 
-// Clusters for small batches: CTAs that share a pair when there are few pairs, each with few
-// enough tiles; 1 otherwise.
-constexpr int kClusterCtas = 8, kClusterTiles = 8;
-int kv4_cluster(int B, int Hkv, int capacity, int window, int num_sms) {
+// Clusters for small batches: how many CTAs share a pair, 1 for none. 16 for longer caches, while
+// the clusters are all resident at once with room to spare in each GPC; 8 for shorter ones; none
+// where the tiles of a CTA would be many. us with 32 heads, for 16 | 8 | 1 CTAs a pair: one
+// sequence of 512 keys over 8 KV heads 5.3 | 4.6, 4000 keys 7.1 | 7.8, 16384 15.1 | 20.1 | 23.9,
+// 32768 26.5 | 37.8 | 33.3, 131072 93 | | 58; four of 8192 17.1 | 23.0. Groups of 16 heads (2 KV
+// heads), whose CTAs take half an SM: 8 sequences of 8192 23.8 | 20.3, 16 of 1024 25.0 | 8.6.
+int kv4_cluster(int B, int H, int Hkv, int capacity, int window, int num_sms) {
   const int span = window > 0 && window < capacity ? window : capacity;
-  const bool few = (long long)B * Hkv * kClusterCtas <= 2ll * num_sms;
-  return few && (span + kTile - 1) / kTile <= kClusterCtas * kClusterTiles ? kClusterCtas : 1;
+  const int n = (span + kTile - 1) / kTile;
+  const long long pairs = (long long)B * Hkv;
+  const bool fits16 = H / Hkv <= 8 ? 2 * 16 * pairs <= 7ll * num_sms : 16 * pairs <= num_sms;
+  if (fits16 && n >= 16 && n <= 256) return 16;
+  return 8 * pairs <= 2ll * num_sms && n <= 64 ? 8 : 1;
+}
+
+// Clusters of more than 8 CTAs, allowed once per device (a bit each).
+cudaError_t allow_large_clusters_once(const void* kernel, std::atomic<unsigned long long>& done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const unsigned long long bit = dev >= 0 && dev < 64 ? 1ull << dev : 0ull;
+  if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_acq_rel);
+  return e;
 }
 
 template <int NT, int CL>
@@ -802,6 +826,11 @@ cudaError_t launch_nt(const Kv4Params& p, int grid, cudaStream_t s) {
   if constexpr (CL == 1) {
     return launch_pdl(kernel, grid, kThreads, Cfg<NT>::kSmem, s, p);
   } else {
+    if (CL > 8) {
+      static std::atomic<unsigned long long> large{0};
+      e = allow_large_clusters_once(reinterpret_cast<const void*>(kernel), large);
+      if (e != cudaSuccess) return e;
+    }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid);
     cfg.blockDim = dim3(kThreads);
@@ -823,7 +852,7 @@ cudaError_t launch_nt(const Kv4Params& p, int grid, cudaStream_t s) {
 }  // namespace
 
 size_t attn_kv4_ws_bytes(int B, int H, int Hkv, int capacity, int window, int num_sms) {
-  if (B <= 0 || kv4_cluster(B, Hkv, capacity, window, num_sms) > 1) return 0;
+  if (B <= 0 || kv4_cluster(B, H, Hkv, capacity, window, num_sms) > 1) return 0;
   return kv4_ws(B, H, Hkv, num_sms).bytes;
 }
 
@@ -836,10 +865,9 @@ cudaError_t launch_attn_decode_kv4(const HeadRows& q, const Kv4Cache& c, const H
   if (B <= 0) return cudaSuccess;
   Kv4Params p{q, o, c, B, H, Hkv, window > 0 ? window : 0, nullptr, nullptr, nullptr, kLog2e / sqrtf((float)kD)};
   const bool wide = H / Hkv > 8;
-  if (kv4_cluster(B, Hkv, c.capacity, window, num_sms) > 1) {
-    const int grid = B * Hkv * kClusterCtas;
-    return wide ? launch_nt<2, kClusterCtas>(p, grid, s) : launch_nt<1, kClusterCtas>(p, grid, s);
-  }
+  const int cluster = kv4_cluster(B, H, Hkv, c.capacity, window, num_sms);
+  if (cluster == 16) return wide ? launch_nt<2, 16>(p, B * Hkv * 16, s) : launch_nt<1, 16>(p, B * Hkv * 16, s);
+  if (cluster == 8) return wide ? launch_nt<2, 8>(p, B * Hkv * 8, s) : launch_nt<1, 8>(p, B * Hkv * 8, s);
   const Kv4Ws w = kv4_ws(B, H, Hkv, num_sms);
   uint8_t* base = static_cast<uint8_t*>(ws);
   p.prefix = reinterpret_cast<int*>(base + w.prefix);

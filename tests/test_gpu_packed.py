@@ -575,6 +575,20 @@ def test_attn_decode_kv4(H, Hkv, cap, lens):
     assert torch.equal(out, blk.attn_decode_kv4(q, c))  # the same to the bit
 
 
+@pytest.mark.parametrize("cap", [5000, 40000])
+@pytest.mark.parametrize("H,Hkv", [(8, 2), (16, 1), (9, 1), (32, 8), (8, 8)])
+def test_attn_decode_kv4_few_sequences(H, Hkv, cap):
+    """A few sequences over long caches: a cluster of CTAs for each KV head, or stretches of all
+    their tiles."""
+    lens = [5000, 0, 1, 2177]
+    blk = block(H, Hkv)
+    c, k, v = filled_cache(blk, 1, Hkv, cap, lens)
+    q = randn(9, len(lens), H, D)
+    out = blk.attn_decode_kv4(q, c)
+    check_decode(out, q, k, v, lens)
+    assert torch.equal(out, blk.attn_decode_kv4(q, c))
+
+
 def test_attn_decode_kv4_long():
     """Thousands of keys: a sequence's keys are split over many CTAs and joined."""
     lens = [20000, 1, 7000, 0, 12345]
