@@ -714,11 +714,12 @@ __global__ void __launch_bounds__(kThreads, Cfg<NT>::kCtas) attn_kv4_kernel(cons
   }
 }
 
-// Joins the partial results of the pairs that were cut, a warp per query head; a sequence
-// without keys gets its zeros here.
+// Joins the partial results of the pairs that were cut, W warps per query head (8: a block, for
+// long sequences, which many stretches share); a sequence without keys gets its zeros here.
 constexpr int kJoinThreads = 256;
 constexpr int kJoinBatch = 8;  // partials whose loads are issued together
 
+template <int W>
 __global__ void __launch_bounds__(kJoinThreads) attn_kv4_join_kernel(const __grid_constant__ Kv4Params p) {
   pdl_launch_dependents();
   pdl_wait();
@@ -726,7 +727,9 @@ __global__ void __launch_bounds__(kJoinThreads) attn_kv4_join_kernel(const __gri
   const int G = p.H / p.Hkv;
   const long long total = (long long)p.prefix[p.B] * p.Hkv;
   const int n_str = p.prefix[p.B + 1];
-  const long long pair = (long long)blockIdx.x * (kJoinThreads / 32) + warp;
+  static_assert(W == 1 || W == kJoinThreads / 32, "a block's warps share one head, or none");
+  const long long pair = W == 1 ? (long long)blockIdx.x * (kJoinThreads / 32) + warp : blockIdx.x;
+  const int part = W == 1 ? 0 : warp;
   if (pair >= (long long)p.B * p.H) return;
   const int b = (int)(pair / p.H), h = (int)(pair % p.H), kvh = h / G, hg = h % G;
   __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.o.ptr) + b * p.o.row + h * p.o.head + 4 * lane;
@@ -740,7 +743,7 @@ __global__ void __launch_bounds__(kJoinThreads) attn_kv4_join_kernel(const __gri
   if (c0 == c1) return;
   float m = -INFINITY, l = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int c = c0; c <= c1; c += kJoinBatch) {
+  for (int c = c0 + part * kJoinBatch; c <= c1; c += W * kJoinBatch) {
     float2 ml[kJoinBatch];
     float4 ov[kJoinBatch];
 #pragma unroll
@@ -770,6 +773,27 @@ __global__ void __launch_bounds__(kJoinThreads) attn_kv4_join_kernel(const __gri
     }
     m = gm;
   }
+  if constexpr (W > 1) {
+    __shared__ float2 part_ml[W];
+    __shared__ float4 part_o[W][32];
+    if (lane == 0) part_ml[part] = make_float2(m, l);
+    part_o[part][lane] = acc;
+    __syncthreads();
+    if (part != 0) return;
+    float gm = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < W; ++i) gm = fmaxf(gm, part_ml[i].x);
+    const float mu = gm == -INFINITY ? 0.f : gm;
+    l = 0.f;
+    acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+      const float f = ex2(part_ml[i].x - mu);
+      const float4 x = part_o[i][lane];
+      l += part_ml[i].y * f;
+      acc = make_float4(acc.x + x.x * f, acc.y + x.y * f, acc.z + x.z * f, acc.w + x.w * f);
+    }
+  }
   const float inv = 1.f / l;
   *reinterpret_cast<uint2*>(o) = make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
 }
@@ -793,16 +817,17 @@ Kv4Ws kv4_ws(int B, int H, int Hkv, int num_sms) {
 // Clusters for small batches: how many CTAs share a pair, 1 for none. 16 for longer caches, while
 // the clusters are all resident at once with room to spare in each GPC; 8 for shorter ones; none
 // where the tiles of a CTA would be many. us with 32 heads, for 16 | 8 | 1 CTAs a pair: one
-// sequence of 512 keys over 8 KV heads 5.3 | 4.6, 4000 keys 7.1 | 7.8, 16384 15.1 | 20.1 | 23.9,
-// 32768 26.5 | 37.8 | 33.3, 131072 93 | | 58; four of 8192 17.1 | 23.0. Groups of 16 heads (2 KV
-// heads), whose CTAs take half an SM: 8 sequences of 8192 23.8 | 20.3, 16 of 1024 25.0 | 8.6.
+// sequence over 8 KV heads of 512 keys 5.3 | 4.6, 4000 keys 7.1 | 7.8, 12000 12.4 | | 13.1, 16384
+// 15.2 | | 13.4; four of 8192 17.1 | 23.0 | 21.6. Groups of 16 heads (2 KV heads), whose CTAs take
+// half an SM: one sequence of 8192 10.7 | | 11.9, 8 of them 23.8 | 20.4 | 17.4, 16 of 1024 25.0 |
+// 8.6.
 int kv4_cluster(int B, int H, int Hkv, int capacity, int window, int num_sms) {
   const int span = window > 0 && window < capacity ? window : capacity;
   const int n = (span + kTile - 1) / kTile;
   const long long pairs = (long long)B * Hkv;
   const bool fits16 = H / Hkv <= 8 ? 2 * 16 * pairs <= 7ll * num_sms : 16 * pairs <= num_sms;
-  if (fits16 && n >= 16 && n <= 256) return 16;
-  return 8 * pairs <= 2ll * num_sms && n <= 64 ? 8 : 1;
+  if (fits16 && n >= 16 && n <= 96) return 16;
+  return 8 * pairs <= 2ll * num_sms && n <= 32 ? 8 : 1;
 }
 
 // Clusters of more than 8 CTAs, allowed once per device (a bit each).
@@ -878,8 +903,12 @@ cudaError_t launch_attn_decode_kv4(const HeadRows& q, const Kv4Cache& c, const H
   const int grid = (int)std::max(1ll, std::min<long long>(kv4_grid(H, Hkv, num_sms), most / kMinTiles));
   cudaError_t e = wide ? launch_nt<2, 1>(p, grid, s) : launch_nt<1, 1>(p, grid, s);
   if (e != cudaSuccess) return e;
-  const long long pairs = (long long)B * H;
-  return launch_pdl(attn_kv4_join_kernel, dim3((unsigned)((pairs + kJoinThreads / 32 - 1) / (kJoinThreads / 32))),
+  // a block per head where a pair may be cut into more stretches than a warp loads at once (one
+  // sequence of 65536 keys 41.2 -> 29.7 us)
+  const long long heads = (long long)B * H;
+  if (grid >= (long long)kJoinBatch * B * Hkv)
+    return launch_pdl(attn_kv4_join_kernel<kJoinThreads / 32>, dim3((unsigned)heads), kJoinThreads, 0, s, p);
+  return launch_pdl(attn_kv4_join_kernel<1>, dim3((unsigned)((heads + kJoinThreads / 32 - 1) / (kJoinThreads / 32))),
                     kJoinThreads, 0, s, p);
 }
 
