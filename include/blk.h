@@ -373,8 +373,10 @@ blk_status blk_qk_norm_rope(blk_handle* h, const blk_head_rows* q, const blk_hea
  * handle has one). cu_seqlens: device int32 [batch + 1], rising from >= 0 to <= rows; another
  * one sets the status word to INVALID_ARG and is read clamped. Sequences may be empty; rows of
  * no sequence are neither used nor written: what they hold, NaN included, reaches no
- * output. (Within a sequence a NaN or infinity in v reaches the outputs of its 128-row tile
- * of keys, as 0 * NaN does.) workspace: blk_attn_packed_workspace_bytes(h, rows, batch), 0 for
+ * output. Within a sequence a score that is NaN or +inf gives its query NaN, as the formula
+ * does, and a NaN or infinity in v reaches the outputs of its 128-row tile of keys (0 * NaN).
+ * The probabilities are rounded to bf16 for their product with v, as in blk_attn_gqa, the
+ * output to bf16; everything between is fp32. workspace: blk_attn_packed_workspace_bytes(h, rows, batch), 0 for
  * all but large batches (then it may be NULL).
  * Errors: INVALID_ARG, UNSUPPORTED (fp32 handle), ALIGNMENT, WORKSPACE, CUDA. */
 size_t blk_attn_packed_workspace_bytes(const blk_handle* h, int rows, int batch);

@@ -491,8 +491,9 @@ __global__ void __launch_bounds__(PACKED ? kPackedThreads : kThreads, 1) attn_tc
             w1 = ex2_approx(s1.x - mu);
             l = s0.y * w0 + s1.y * w1;
           }
-          const bool seen = l > 0.f;
-          const float inv = seen ? 1.f / l : 0.f;
+          // a query sees itself at least: a sum that is NaN (a NaN or infinity in its scores), or 0 (all of
+          // them -inf), gives NaN, as the formula does
+          const float inv = 1.f / l;
           w0 *= inv;
           w1 *= inv;
           const int query = it.sl[g].m0 + (r >> p.fold), h = it.sl[g].h + (r & ((1 << p.fold) - 1));
@@ -505,13 +506,13 @@ __global__ void __launch_bounds__(PACKED ? kPackedThreads : kThreads, 1) attn_tc
               tmem_ld16(taddr + g * kD + c, ov);
               tc_wait_ld();
 #pragma unroll
-              for (int i = 0; i < 16; ++i) ov[i] = seen ? ov[i] * w0 : 0.f;
+              for (int i = 0; i < 16; ++i) ov[i] *= w0;
               if (SPLIT && it.n_tiles > 1) {  // O_1 holds something
                 float o1[16];
                 tmem_ld16(taddr + kD + c, o1);
                 tc_wait_ld();
 #pragma unroll
-                for (int i = 0; i < 16; ++i) ov[i] = seen ? fmaf(o1[i], w1, ov[i]) : 0.f;
+                for (int i = 0; i < 16; ++i) ov[i] = fmaf(o1[i], w1, ov[i]);
               }
               if (store) {
                 const uint4 a = make_uint4(pack_bf16x2(ov[0], ov[1]), pack_bf16x2(ov[2], ov[3]),
