@@ -86,6 +86,22 @@ struct Unit {
   }
 };
 
+// A number of cu_seqlens as it is read.
+__device__ __forceinline__ int clamped(int x, int rows) { return min(max(x, 0), rows); }
+
+// Whether cu_seqlens falls somewhere; one that does, or leaves [0, rows], sets the status word (of
+// one block's threads that call this). All threads of the block.
+__device__ __forceinline__ bool list_falls(const int* cu, int B, int rows, DevStatus* st) {
+  bool bad = false, falls = false;
+  for (int i = threadIdx.x; i < B; i += blockDim.x) {
+    const int a = cu[i], e = cu[i + 1];
+    falls |= e < a;
+    bad |= e < a || a < 0 || e > rows;
+  }
+  if (bad && st) atomicCAS(&st->code, 0, kStatusInvalidArg);
+  return __syncthreads_or(falls);
+}
+
 // at[i] := the slot of the block's row i, counted over the whole cache for KV head 0 (-1: a row
 // of no sequence, -2: a slot outside the cache).
 __device__ __forceinline__ void find_slots(const RowParams& p, int r0, int n, long long* at, int* s_cu) {
@@ -111,7 +127,7 @@ __device__ __forceinline__ void find_slots(const RowParams& p, int r0, int n, lo
           hi = mid;
       }
       b = lo;
-      i = r - cu[lo];
+      i = r - max(cu[lo], 0);
     }
     long long a = -1;
     if (in) {
@@ -255,9 +271,9 @@ __global__ void __launch_bounds__(kThreads) kv4_store_kernel(const __grid_consta
     store_row(vu, p.c.v + to * kKv4Codes, p.c.v_scale + to * kKv4Scales, a >= 0, lane);
   }
   if (!append) {  // the new lengths: nobody reads lens here
-    if (blockIdx.x == 0)
+    if (blockIdx.x == 0 && !(p.cu && list_falls(p.cu, p.B, p.rows, p.status)))
       for (int i = tid; i < p.B; i += blockDim.x) {
-        const long long e = (long long)p.starts[i] + (p.cu ? p.cu[i + 1] - p.cu[i] : 1);
+        const long long e = (long long)p.starts[i] + (p.cu ? clamped(p.cu[i + 1], p.rows) - clamped(p.cu[i], p.rows) : 1);
         p.c.lens[i] = (int)(e < 0 ? 0 : e < p.c.capacity ? e : p.c.capacity);
       }
   } else if (!p.cu && tid == 0 && n > 0 && at[0] >= 0) {  // the block has read its slot (find_slots)
@@ -265,12 +281,14 @@ __global__ void __launch_bounds__(kThreads) kv4_store_kernel(const __grid_consta
   }
 }
 
-// lens[b] += the rows of sequence b, after a store that read them as first slots
-__global__ void kv4_lens_kernel(const int* cu, int* lens, int B, int capacity) {
+// lens[b] += the rows of sequence b, after a store that read them as first slots. Every block
+// looks the list over.
+__global__ void kv4_lens_kernel(const int* cu, int* lens, int B, int rows, int capacity, DevStatus* st) {
   pdl_launch_dependents();
   pdl_wait();
+  if (list_falls(cu, B, rows, st)) return;
   for (int b = blockIdx.x * blockDim.x + threadIdx.x; b < B; b += gridDim.x * blockDim.x) {
-    const long long n = (long long)lens[b] + cu[b + 1] - cu[b];
+    const long long n = (long long)lens[b] + clamped(cu[b + 1], rows) - clamped(cu[b], rows);
     lens[b] = (int)(n < 0 ? 0 : n < capacity ? n : capacity);
   }
 }
@@ -307,6 +325,7 @@ __global__ void __launch_bounds__(kThreads) kv4_load_kernel(const __grid_constan
   Unit un(p, r0, n);
   find_slots(p, r0, n, at, s_cu);
   if (tid < n && at[tid] == -2 && p.status) atomicCAS(&p.status->code, 0, kStatusInvalidArg);
+  if (blockIdx.x == 0 && p.cu) list_falls(p.cu, p.B, p.rows, p.status);
   const uint32_t mask = kept_constant(15u);
   uint32_t kw = 0, ks = 0, kz = 0, vw = 0, vs = 0, vz = 0;
   auto fetch = [&] {
@@ -351,7 +370,7 @@ cudaError_t launch_kv4_store(const HeadRows& k, const HeadRows& v, int rows, con
   const int grid = rows > 0 ? (rows + p.block_rows - 1) / p.block_rows : 1;
   cudaError_t e = launch_pdl(kv4_store_kernel, grid, kThreads, 0, s, p, append ? 1 : 0);
   if (e != cudaSuccess || !append || !cu) return e;
-  return launch_pdl(kv4_lens_kernel, (B + 255) / 256, 256, 0, s, cu, c.lens, B, c.capacity);
+  return launch_pdl(kv4_lens_kernel, (B + 255) / 256, 256, 0, s, cu, c.lens, B, rows, c.capacity, st);
 }
 
 cudaError_t launch_kv4_load(const HeadRows& k, const HeadRows& v, int rows, const int* cu, const int* starts, int B,

@@ -1,10 +1,10 @@
-"""Packed calls on inputs that are not all numbers."""
+"""Packed calls on inputs that are not all numbers, and on lists of sequences that are not valid."""
 import numpy as np
 import pytest
 import torch
 
 from tests.helpers import np64
-from tests.test_gpu_packed import D, U, attn_ref, block, cu_of, randn
+from tests.test_gpu_packed import D, DEV, U, attn_ref, block, cu_of, ints, randn, values
 
 pytestmark = pytest.mark.gpu
 
@@ -38,3 +38,59 @@ def test_attn_packed_nan_and_infinities(H, Hkv, lens, window, which, bad):
             seen += nan.sum()
             at += m
     assert seen > 0  # the corner is there
+
+
+# ------------------------------------------------------------------ lists that are not valid
+
+# cu_seqlens of 200 rows, and how it is read
+BAD_LISTS = [([0, 60, 500], [0, 60, 200]), ([-5, -1, 50], [0, 0, 50]), ([-7, 20, 60], [0, 20, 60]), ([0, 250, 300], [0, 200, 200]),
+             ([*range(180), 201], [*range(180), 200]), ([0] * 1500 + [150, 2**31 - 1], [0] * 1500 + [150, 200]),
+             ([-2**31] * 1500 + [150, 190], [0] * 1500 + [150, 190])]
+
+
+@pytest.mark.parametrize("cu,read", BAD_LISTS)
+@pytest.mark.parametrize("append", [False, True])
+def test_kv4_lists_outside_the_rows_are_clamped(cu, read, append):
+    """The lengths move by the rows that were stored, and the status word says INVALID_ARG."""
+    B, n, Hkv, cap = len(cu) - 1, 200, 2, 700
+    blk = block(Hkv, Hkv)
+    k, v = randn(1, n, Hkv, D), randn(2, n, Hkv, D)
+    first = [3 + b % 5 for b in range(B)]
+    caches = []
+    for c in (cu, read):
+        cache = blk.kv4_cache(B, cap)
+        for x in ("k", "v", "k_scale", "v_scale"):
+            cache[x].view(torch.uint8).fill_(0xA5)
+        cache["lens"].copy_(ints(first))
+        blk.kv4_store(cache, k, v, ints(c), starts=None if append else ints(first))
+        assert blk.last_status() == (1 if c is cu else 0)
+        assert cache["lens"].tolist() == [f + b - a for f, a, b in zip(first, read, read[1:])]
+        caches.append(cache)
+    for x in ("k", "v", "k_scale", "v_scale"):
+        assert torch.equal(caches[0][x].view(torch.uint8), caches[1][x].view(torch.uint8))
+    outs = []
+    for c in (cu, read):
+        out = torch.full((2, n, Hkv, D), 3.0, dtype=torch.bfloat16, device=DEV)
+        blk.kv4_load(caches[1], ints(c), n, starts=ints(first), k_out=out[0], v_out=out[1])
+        assert blk.last_status() == (1 if c is cu else 0)
+        outs.append(out)
+    assert torch.equal(*outs)
+    assert torch.equal(outs[0][0, read[0]:read[-1]].cpu(), values(k[read[0]:read[-1]]).bfloat16())
+
+
+@pytest.mark.parametrize("cu", [[0, 100, 50, 200], [0, 60, 20], [200, 0], [*range(100), 0, *range(100, 1500)]])
+@pytest.mark.parametrize("append", [False, True])
+def test_kv4_lists_that_fall_move_no_length(cu, append):
+    B, n, Hkv, cap = len(cu) - 1, 200, 2, 400
+    blk = block(Hkv, Hkv)
+    k, v = randn(1, n, Hkv, D), randn(2, n, Hkv, D)
+    cache = blk.kv4_cache(B, cap)
+    first = [3 + b % 5 for b in range(B)]
+    cache["lens"].copy_(ints(first))
+    blk.kv4_store(cache, k, v, ints(cu), starts=None if append else ints([9] * B))
+    assert blk.last_status() == 1 and cache["lens"].tolist() == first
+    for x in ("k", "v", "k_scale", "v_scale"):  # the slots in use are as they were
+        for b in range(min(B, 50)):
+            assert not cache[x][b, :, :first[b]].any()
+    blk.kv4_load(cache, ints(cu), n)
+    assert blk.last_status() == 1
