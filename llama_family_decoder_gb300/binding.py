@@ -521,7 +521,8 @@ class DecoderBlock:
 
     def kv4_load(self, cache, cu_seqlens=None, rows=None, starts=None, k_out=None, v_out=None, stream=None):
         """The values of the cache's slots starts[b], ... (None: 0, ...) as packed bf16 rows (k, v)
-        [rows, Hkv, 128]: the rows that cu_seqlens gives each sequence (None: one each)."""
+        [rows, Hkv, 128]: the rows that cu_seqlens gives each sequence (None: one each). cu_seqlens
+        is on the device, so with it the number of rows is wanted."""
         if stream is None:
             r = self._fast.kv4_load(self._block, cache, cu_seqlens, rows, starts, k_out, v_out)
             if r is not None:
@@ -529,6 +530,8 @@ class DecoderBlock:
         if self._elsewhere(stream):
             with _on_stream(self._device, stream):
                 return self.kv4_load(cache, cu_seqlens, rows, starts, k_out, v_out)
+        if cu_seqlens is not None and rows is None:
+            raise ValueError("rows: how many packed rows cu_seqlens stands for is wanted")
         c, batch = self._kv4(cache)
         n = batch if rows is None else rows
         shape = (n, *self._sizes[1:])

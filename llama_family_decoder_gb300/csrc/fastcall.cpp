@@ -266,7 +266,9 @@ PyObject* kv4_load(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
     const int* cu = c.ints(a[2], batch + 1);
     const int* starts = c.ints(a[4], batch);
     int64_t n = batch;
-    if (a[3] != Py_None) {
+    if (a[3] == Py_None) {
+      if (a[2] != Py_None) return none();  // packed rows, but how many?
+    } else {
       n = PyLong_AsLong(a[3]);
       if (PyErr_Occurred()) PyErr_Clear();  // then n is -1, and refused
     }

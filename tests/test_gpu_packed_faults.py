@@ -94,3 +94,18 @@ def test_kv4_lists_that_fall_move_no_length(cu, append):
             assert not cache[x][b, :, :first[b]].any()
     blk.kv4_load(cache, ints(cu), n)
     assert blk.last_status() == 1
+
+
+def test_kv4_load_of_packed_rows_needs_their_number():
+    """cu_seqlens is on the device: without `rows` the call would have to guess how many there are."""
+    blk = block(2, 2)
+    k = randn(1, 10, 2, D)
+    cache, cu = blk.kv4_cache(2, 8), ints([0, 3, 10])
+    blk.kv4_store(cache, k, k, cu)
+    with pytest.raises(ValueError):
+        blk.kv4_load(cache, cu)
+    out = torch.empty_like(k[:2])
+    with pytest.raises(ValueError):
+        blk.kv4_load(cache, cu, k_out=out, v_out=out.clone())
+    assert torch.equal(blk.kv4_load(cache, cu, 10)[0].cpu(), values(k).bfloat16())
+    assert torch.equal(blk.kv4_load(cache)[1].cpu(), values(k[[0, 3]]).bfloat16())
