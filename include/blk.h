@@ -371,7 +371,8 @@ blk_status blk_qk_norm_rope(blk_handle* h, const blk_head_rows* q, const blk_hea
  * b < batch is rows cu_seqlens[b] .. cu_seqlens[b+1]-1 of q, o [rows, n_heads, 128] and k, v
  * [rows, n_kv_heads, 128]; its query i sees its keys j <= i (i - j < sliding_window when the
  * handle has one). cu_seqlens: device int32 [batch + 1], rising from >= 0 to <= rows; another
- * one sets the status word to INVALID_ARG and is read clamped. Sequences may be empty; rows of
+ * one sets the status word to INVALID_ARG and is read as the running maximum of its numbers,
+ * clamped to 0 .. rows. Sequences may be empty; rows of
  * no sequence are neither used nor written: what they hold, NaN included, reaches no
  * output. Within a sequence a score that is NaN or +inf gives its query NaN, as the formula
  * does, and a NaN or infinity in v reaches the outputs of its 128-row tile of keys (0 * NaN).

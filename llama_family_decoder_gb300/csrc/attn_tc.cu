@@ -129,7 +129,7 @@ struct AttnParams {
   const PackedWork* work;  // null: every CTA makes the list itself from cu (see own_work)
   const int* n_work;
   const int* cu;
-  int step, cap;  // queries of an entry, entries of rising sequences at most
+  int step, cap;  // queries of an entry, entries at most
   long long o_row, o_head;
   // 2^fold query heads of a KV head share a slot's 128 rows: row r is head r % 2^fold of query
   // r / 2^fold
@@ -266,24 +266,47 @@ __device__ __forceinline__ int item_id(int k, int G, int c) { return k * G + ((k
 // is the same in every CTA. F(t), the entries at places t and farther, falls with t: the place
 // of entry e is the last t with F(t) > e, found by halving, and its sequence is the one number
 // e - F(t + 1) of those that reach t. A warp finds an item at a time; `scratch` holds the
-// sequences. A cu that does not rise from 0 to at most the rows records INVALID_ARG and is read
-// clamped.
+// sequences. A cu that does not rise from >= 0 to at most the rows records INVALID_ARG and is read
+// as the running maximum of its clamped numbers: sequences never overlap, so that there are at most
+// p.cap entries, and the sums fit.
 constexpr int kOwnSeqs = 2048;
+__device__ __forceinline__ int running_max(int x, int lane) {  // over the lanes up to this one
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int u = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x = max(x, u);
+  }
+  return x;
+}
 __device__ __noinline__ int own_work(const AttnParams& p, uint8_t* scratch, int units, PackedWork* mine, int* longest) {
   int* n_of = reinterpret_cast<int*>(scratch);                 // [B] a sequence's entries
   int2* rows = reinterpret_cast<int2*>(n_of + kOwnSeqs);       // its first row and its length
   static_assert(kOwnSeqs * 12 <= (kKStages + kVStages) * kKVBytes, "scratch");
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;
-  bool bad = false;
+  bool bad = false, falls = false;
+  auto put = [&](int b, int lo, int hi) {
+    rows[b] = make_int2(lo, hi - lo);
+    n_of[b] = (hi - lo + p.step - 1) / p.step;
+  };
   for (int b = tid; b < p.B; b += blockDim.x) {
     const int a = p.cu[b], e = p.cu[b + 1];
     const int lo = min(max(a, 0), p.T), hi = min(max(e, lo), p.T);
     bad |= lo != a || hi != e;
-    rows[b] = make_int2(lo, hi - lo);
-    n_of[b] = (hi - lo + p.step - 1) / p.step;
+    falls |= e < a;
+    put(b, lo, hi);
   }
   if (bad && blockIdx.x == 0 && p.status) atomicCAS(&p.status->code, 0, kStatusInvalidArg);
-  __syncthreads();
+  if (__syncthreads_or(falls)) {
+    if (warp == 0) {
+      int top = 0;
+      for (int b0 = 0; b0 < p.B; b0 += 32) {
+        const int b = b0 + lane, lo = max(top, running_max(b < p.B ? min(max(p.cu[b], 0), p.T) : 0, lane));
+        if (b < p.B) put(b, lo, max(lo, min(max(p.cu[b + 1], 0), p.T)));
+        top = __shfl_sync(0xffffffffu, lo, 31);
+      }
+    }
+    __syncthreads();
+  }
   auto from = [&](int t) {  // F(t)
     int n = 0;
 #pragma unroll 4
@@ -293,7 +316,7 @@ __device__ __noinline__ int own_work(const AttnParams& p, uint8_t* scratch, int 
   int places = 0;
   for (int b = lane; b < p.B; b += 32) places = max(places, n_of[b]);
   places = __reduce_max_sync(0xffffffffu, places);
-  const int n_items = min(from(0), p.cap) * units;  // sequences that overlap could have more
+  const int n_items = min(from(0), p.cap) * units;  // never more than a CTA keeps entries for
   for (int k = warp; k < kOwnItems; k += warps) {
     const int id = item_id(k, gridDim.x, blockIdx.x);
     if (id >= n_items) break;
@@ -1166,8 +1189,8 @@ constexpr int kPlanBins = 4096;
 // The work list of packed sequences, heaviest first: an entry per `step` queries, ordered by its
 // place in its sequence, which its key count grows with. One CTA counts the entries of each
 // place, sums the counts from the far places down, and deals the entries out; the order within
-// a place does not matter (items are independent, so no result depends on it). A cu that does
-// not rise from 0 to at most `rows` records INVALID_ARG and is read clamped.
+// a place does not matter (items are independent, so no result depends on it). A cu that is not
+// valid is read as by own_work, 1024 sequences at a time.
 __global__ void __launch_bounds__(kPlanThreads) packed_plan_kernel(const int* __restrict__ cu, int B, int rows, int step,
                                                                    int cap, PackedWork* __restrict__ work,
                                                                    int* __restrict__ n_work, DevStatus* st) {
@@ -1180,19 +1203,35 @@ __global__ void __launch_bounds__(kPlanThreads) packed_plan_kernel(const int* __
   const int per_bin = (places + kPlanBins - 1) / kPlanBins;
   for (int i = tid; i < kPlanBins; i += kPlanThreads) count[i] = 0;
   __syncthreads();
-  bool bad = false;
+  bool bad = false, falls = false;
+  for (int b = tid; b < B; b += kPlanThreads) falls |= cu[b + 1] < cu[b];
+  falls = __syncthreads_or(falls);
   for (int pass = 0; pass < 2; ++pass) {
-    for (int b0 = 32 * warp; b0 < B; b0 += kPlanThreads) {  // 32 sequences a warp, one after another
-      const int b = b0 + lane, a = b < B ? cu[b] : 0, e = b < B ? cu[b + 1] : 0;
-      const int lo = min(max(a, 0), rows), len = min(max(e, lo), rows) - lo;
-      bad |= lo != a || lo + len != e;
+    int top = 0;  // of the sequences before (a list that falls)
+    for (long long base = 0; base < B; base += kPlanThreads) {  // 32 sequences a warp, one after another
+      const long long b0 = base + 32 * warp, b = b0 + lane;
+      const int a = b < B ? cu[b] : 0, e = b < B ? cu[b + 1] : 0;
+      int lo = min(max(a, 0), rows);
+      if (falls) {
+        lo = max(top, running_max(lo, lane));
+        if (lane == 31) warp_sums[warp] = lo;
+        __syncthreads();
+        for (int w = 0; w < kPlanThreads / 32; ++w) {
+          if (w < warp) lo = max(lo, warp_sums[w]);
+          top = max(top, warp_sums[w]);
+        }
+        __syncthreads();
+      }
+      const int len = min(max(e, lo), rows) - lo;
+      bad |= b < B && (lo != a || lo + len != e);
       const int n = (len + step - 1) / step;
-      for (int i = 0; i < min(32, B - b0); ++i) {
+      const int seqs = (int)min(32ll, B - b0);  // none when it is not positive
+      for (int i = 0; i < seqs; ++i) {
         const int row0 = __shfl_sync(0xffffffffu, lo, i), its = __shfl_sync(0xffffffffu, len, i);
         const int last = __shfl_sync(0xffffffffu, n, i);
         for (int t = lane; t < last; t += 32) {
           const int at = atomicAdd(&count[t / per_bin], 1);
-          if (pass == 1 && at < cap) work[at] = {row0, its, t * step, 0};
+          if (pass == 1 && (unsigned)at < (unsigned)cap) work[at] = {row0, its, t * step, 0};
         }
       }
     }
@@ -1246,14 +1285,14 @@ PackedPlan packed_plan(int rows, int B, int H, int Hkv, int num_sms) {
   // the split's shorter items do not make up for its second read of K and V: 8000 115 -> 132).
   p.split = 4 * (long long)(rows / (2 * tq) + B) * p.units < 5 * num_sms;
   p.step = p.split ? tq : 2 * tq;
-  p.cap = rows / p.step + B;
+  p.cap = rows / p.step + std::min(B, rows);  // a sequence's rows are its own, and an empty one has no entry
   // one CTA per SM, more only where a CTA would have more items than it keeps entries for
   const long long most = (long long)p.cap * p.units;
   p.grid = (int)std::max(std::min<long long>(most, num_sms), (most + kOwnItems - 1) / kOwnItems);
   // The list costs its sums in every CTA, or a launch of its own before the attention: 48 turns of
   // 10 to 200 queries 25.2 us, 27.5 with that launch; 2000 sequences of 10 (8 heads over 2) 81 and
-  // 113; 4000 of 60 (32 over 8) 1479 and 1405. And the sums have to fit 32 bits.
-  p.own = B <= kOwnSeqs && B * (long long)((rows + p.step - 1) / p.step) <= INT32_MAX;
+  // 113; 4000 of 60 (32 over 8) 1479 and 1405.
+  p.own = B <= kOwnSeqs;
   return p;
 }
 

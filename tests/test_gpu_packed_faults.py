@@ -4,7 +4,7 @@ import pytest
 import torch
 
 from tests.helpers import np64
-from tests.test_gpu_packed import D, DEV, U, attn_ref, block, cu_of, ints, randn, values
+from tests.test_gpu_packed import D, DEV, U, attn_ref, block, check_packed, cu_of, ints, randn, values
 
 pytestmark = pytest.mark.gpu
 
@@ -109,3 +109,37 @@ def test_kv4_load_of_packed_rows_needs_their_number():
         blk.kv4_load(cache, cu, k_out=out, v_out=out.clone())
     assert torch.equal(blk.kv4_load(cache, cu, 10)[0].cpu(), values(k).bfloat16())
     assert torch.equal(blk.kv4_load(cache)[1].cpu(), values(k[[0, 3]]).bfloat16())
+
+
+def running(cu, rows):
+    return np.clip(np.maximum.accumulate(cu), 0, rows).tolist()
+
+
+@pytest.mark.parametrize("cu", [[0, 100, 50, 200], [0, 200, 0, 200, 0], [150, 30, 170, 20], [-9, 60, 500, 40], [200, 0],
+                                [*range(60), 0, 150, *range(60, 160)], [0, 200] * 1500 + [0], [*range(100), 0] * 30])
+@pytest.mark.parametrize("H,Hkv", [(4, 2), (16, 1)])
+def test_attn_packed_lists_that_fall(cu, H, Hkv):
+    """Sequences that claim the same rows are read as ones that do not: the first one keeps them."""
+    n = 200
+    blk = block(H, Hkv)
+    q, k, v = randn(1, n, H, D), randn(2, n, Hkv, D), randn(3, n, Hkv, D)
+    out = torch.full((2, n, H, D), 3.0, dtype=torch.bfloat16, device=DEV)
+    read = running(cu, n)
+    blk.attn_packed(q, k, v, ints(cu), out=out[0])
+    assert blk.last_status() == 1
+    blk.attn_packed(q, k, v, ints(read), out=out[1])
+    assert blk.last_status() == 0
+    assert torch.equal(out[0], out[1])
+    check_packed(out[0], q, k, v, np.diff(read).tolist(), read[0])
+
+
+def test_attn_packed_more_claims_than_32_bits_count():
+    """2^19 sequences that each claim all rows, 2^13 tiles of them: read as one."""
+    n, H, Hkv = 1 << 17, 16, 1
+    blk = block(H, Hkv)
+    q, k, v = randn(1, n, H, D), randn(2, n, Hkv, D), randn(3, n, Hkv, D)
+    want = blk.attn_packed(q, k, v, ints([0, n]))
+    assert blk.last_status() == 0
+    cu = ints([0, n]).repeat(1 << 19)
+    assert torch.equal(blk.attn_packed(q, k, v, cu), want)
+    assert blk.last_status() == 1
