@@ -678,6 +678,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<NT>::kCtas) attn_kv4_kernel(cons
   if constexpr (CL > 1) {
     if (n_mine == 0)  // nothing, as a share
       for (int i = tid; i < G * (kD + 4); i += kThreads) shared_out[i] = i % (kD + 4) == kD ? -INFINITY : 0.f;
+    __syncwarp();  // the loop's last turn may be half a warp's, and the barrier wants it whole
     cluster_sync_all();
     for (int h = rank + CL * warp; h < G; h += CL * kWarps) {  // a warp per head, four channels a lane
       const uint32_t mine = smem_u32(shared_out + h * (kD + 4));
@@ -710,6 +711,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<NT>::kCtas) attn_kv4_kernel(cons
                          (long long)(pair_kvh * G + h) * p.o.head + 4 * lane;
       *reinterpret_cast<uint2*>(o) = make_uint2(pack_bf16x2(oo.x * inv, oo.y * inv), pack_bf16x2(oo.z * inv, oo.w * inv));
     }
+    __syncwarp();
     cluster_sync_all();  // nobody leaves while its share may be read
   }
 }

@@ -4,7 +4,8 @@ import pytest
 import torch
 
 from tests.helpers import np64
-from tests.test_gpu_packed import D, DEV, U, attn_ref, block, check_packed, cu_of, ints, randn, values
+from tests.test_gpu_packed import (D, DEV, U, attn_ref, block, check_decode, check_packed, cu_of, filled_cache, ints, randn,
+                                   values)
 
 pytestmark = pytest.mark.gpu
 
@@ -143,3 +144,18 @@ def test_attn_packed_more_claims_than_32_bits_count():
     cu = ints([0, n]).repeat(1 << 19)
     assert torch.equal(blk.attn_packed(q, k, v, cu), want)
     assert blk.last_status() == 1
+
+
+# ------------------------------------------------------------------ shares of nothing
+
+@pytest.mark.parametrize("H,Hkv", [(1, 1), (3, 1), (4, 1), (4, 4), (5, 1), (8, 1), (9, 1), (12, 1), (16, 1)])
+@pytest.mark.parametrize("cap", [130, 4000, 12000])
+def test_attn_decode_kv4_more_ctas_than_tiles(H, Hkv, cap):
+    """Short sequences in caches that clusters of 8 and of 16 CTAs work on: most or all of a
+    cluster's CTAs have no keys, and groups of any size leave half a warp over in filling their shares."""
+    for lens in ([0], [1], [129], [0, 128, 1, 0]):
+        blk = block(H, Hkv)
+        c, k, v = filled_cache(blk, 1, Hkv, cap, lens)
+        q = randn(9, len(lens), H, D)
+        check_decode(blk.attn_decode_kv4(q, c), q, k, v, lens)
+        assert blk.last_status() == 0
