@@ -159,3 +159,34 @@ def test_attn_decode_kv4_more_ctas_than_tiles(H, Hkv, cap):
         q = randn(9, len(lens), H, D)
         check_decode(blk.attn_decode_kv4(q, c), q, k, v, lens)
         assert blk.last_status() == 0
+
+
+# ------------------------------------------------------------------ large scores, exactly known
+
+@pytest.mark.parametrize("H,Hkv,lens", [(4, 2, [200, 130]), (3, 3, [300]), (32, 8, [900, 50, 700])])  # keys split; split; not
+@pytest.mark.parametrize("top,slope", [(90, 0), (90, 1), (12, 0), (12, 1), (4, 1)])
+@pytest.mark.parametrize("window", [0, 150])
+def test_attn_packed_large_scores_of_whole_numbers(H, Hkv, lens, top, slope, window):
+    """Scores in the thousands, most rows one-hot or nearly so, and references that move from tile to
+    tile (with a slope, later keys score higher and higher).
+
+    q and k are whole numbers up to 90: every product and every partial sum of 128 of them is below
+    128 * 90^2 < 2^24, so a raw score x has no rounding at all. A probability is 2^(x c - m), c =
+    log2(e) / sqrt(128) to within 2^-22 of itself, m a number that is the same for all keys of a row (or
+    is moved by its exact difference): x c - m is one fused operation, off by 2^-24 of its own size.
+    A key that counts has x c within 30 of the largest (2^-30 of the weight), m within 8 of that: at most
+    38 * 2^-24 + 30 * 2^-22 in the exponent, and 2^-22 for the exponential: below 2e-5 of a probability, so
+    the bound of ordinary scores (2e-4) holds, and keys that lead alone are exact to the roundings."""
+    n = sum(lens)
+    blk = block(H, Hkv, sliding_window=window)
+    g = torch.Generator(device=DEV).manual_seed(7)
+    q = torch.randint(-top, top + 1, (n, H, D), generator=g, device=DEV).float()
+    k = torch.randint(-top, top + 1, (n, Hkv, D), generator=g, device=DEV).float()
+    if slope:  # the first 32 channels carry it: q positive there, k's part grows with the key's place
+        q[..., :32] = q[..., :32].abs()
+        place = torch.cat([torch.linspace(0, 1, m, device=DEV) for m in lens])
+        k[..., :32] = (k[..., :32].abs() * place[:, None, None]).round()
+    q, k, v = q.bfloat16(), k.bfloat16(), randn(3, n, Hkv, D)
+    out = blk.attn_packed(q, k, v, cu_of(lens))
+    assert blk.last_status() == 0
+    check_packed(out, q, k, v, lens, window=window)
