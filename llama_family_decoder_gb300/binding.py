@@ -183,7 +183,11 @@ def _on_stream(device, stream):
     """The device and stream that a call's own tensors (outputs, workspace) are made on and
     its kernels run on: the given stream, or the device's current one."""
     import torch
-    return torch.cuda.device(device) if stream is None else torch.cuda.stream(stream)
+    if stream is None:
+        return torch.cuda.device(device)
+    if stream.device != device:
+        raise ValueError(f"stream: one of {device}, where the handle is, is wanted, got one of {stream.device}")
+    return torch.cuda.stream(stream)
 
 
 def _check_tensor(t, name, dtype, dev, shape):

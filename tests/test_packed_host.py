@@ -1,0 +1,29 @@
+"""What the packed calls' host side does before anything is launched (no GPU)."""
+import types
+
+import pytest
+import torch
+
+from llama_family_decoder_gb300 import binding
+
+
+def bare_block(monkeypatch, dev=0):
+    """A DecoderBlock without a handle, whose own calls are recorded; `dev` is current."""
+    blk = object.__new__(binding.DecoderBlock)
+    blk.handle = None
+    blk._torch, blk._dev, blk._device = torch, dev, torch.device("cuda", dev)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: dev)
+    return blk
+
+
+@pytest.mark.parametrize("call,n_args", [("qk_norm_rope", 3), ("attn_packed", 4), ("kv4_store", 3), ("kv4_load", 1),
+                                         ("attn_decode_kv4", 2)])
+def test_a_stream_of_another_device_is_refused(monkeypatch, call, n_args):
+    """... and not dropped for the current stream of the handle's device."""
+    blk = bare_block(monkeypatch)
+    blk._fast = types.SimpleNamespace(**{call: lambda *a: "ran on another stream"})
+    blk._block = None
+    monkeypatch.setattr(torch.cuda, "stream", lambda s: torch.no_grad())  # any context: nothing is launched here
+    other = types.SimpleNamespace(device=torch.device("cuda", 1), cuda_stream=0)
+    with pytest.raises(ValueError, match="stream"):
+        getattr(blk, call)(*[None] * n_args, stream=other)
