@@ -2,11 +2,13 @@
 
 PyTorch provides device memory and streams; every step of the block runs in
 the library's CUDA kernels. There is no fallback: if libblk.so is missing the
-first call raises.
+first call raises, and so does the first packed call if _fastcall.so, which
+handles these calls' arguments, is.
 """
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import struct
 from ctypes import POINTER, c_char_p, c_float, c_int, c_longlong, c_size_t, c_void_p
@@ -252,10 +254,6 @@ class DecoderBlock:
         self._dtype = torch.bfloat16 if self.desc.dtype == 1 else torch.float32
         self._sizes = n_heads, n_kv_heads, head_dim
         self._axes = {}  # (sections, interleaved) -> blk_rope_axes
-        # the packed calls' short way; what it returns None for takes the long one
-        self._fast = fastcall()
-        self._block = self._fast.block(h.value, n_heads, n_kv_heads, head_dim, self.desc.dtype == 1, self._dev,
-                                       self.desc.qk_norm, self.desc.no_rope)
         # the current stream's handle, without building a Stream object where torch has the short way
         self._raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
             (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
@@ -268,6 +266,17 @@ class DecoderBlock:
                    max_batch=max_batch or wl.batch, max_seq=max_seq or wl.cache_len + wl.seq,
                    rope_scaling=wl.rope_scaling, sliding_window=wl.sliding_window, use_rope=wl.use_rope,
                    attn_gate=wl.attn_gate, sandwich_norm=wl.sandwich_norm)
+
+    @functools.cached_property
+    def _fast(self):
+        """The packed calls' short way, loaded at the first of them; what it returns None for takes the
+        long one."""
+        return fastcall()
+
+    @functools.cached_property
+    def _block(self):
+        return self._fast.block(self.handle.value, *self._sizes, self.desc.dtype == 1, self._dev, self.desc.qk_norm,
+                                self.desc.no_rope) if self.handle else None
 
     def close(self):
         if self.handle:

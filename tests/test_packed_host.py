@@ -27,3 +27,20 @@ def test_a_stream_of_another_device_is_refused(monkeypatch, call, n_args):
     other = types.SimpleNamespace(device=torch.device("cuda", 1), cuda_stream=0)
     with pytest.raises(ValueError, match="stream"):
         getattr(blk, call)(*[None] * n_args, stream=other)
+
+
+def test_only_the_packed_calls_need_their_compiled_module(monkeypatch):
+    """A handle, and every call but the packed ones, works without _fastcall.so; those say what is missing."""
+    def missing():
+        raise ImportError("_fastcall is not there")
+
+    made = []
+    monkeypatch.setattr(binding, "lib", lambda: types.SimpleNamespace(blk_create=lambda d, h: made.append(d) or 0,
+                                                                      blk_workspace_bytes=lambda *a: 64))
+    monkeypatch.setattr(binding, "fastcall", missing)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    blk = binding.DecoderBlock(hidden=256, n_heads=2, n_kv_heads=1, head_dim=128, ffn=512)
+    assert len(made) == 1 and blk.workspace_bytes(1, 1) == 64
+    for call, n in (("qk_norm_rope", 3), ("attn_packed", 4), ("kv4_store", 3), ("kv4_load", 1), ("attn_decode_kv4", 2)):
+        with pytest.raises(ImportError, match="_fastcall"):
+            getattr(blk, call)(*[None] * n)
