@@ -10,8 +10,10 @@ from __future__ import annotations
 
 import glob
 import os
+import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -46,19 +48,38 @@ def _stale(src, obj, headers):
     return any(os.path.getmtime(f) > t for f in [src, *headers])
 
 
-def _compile_fastcall() -> subprocess.Popen | None:
-    """Starts the compiler on fastcall.cpp if its object is older than its sources."""
-    import sysconfig
-
+def _fastcall_for() -> str:
+    """What _fastcall.so's binary interface depends on; _build/fastcall.for says what it was built for."""
     import torch
 
-    if not _stale(FAST_SRC, FAST_OBJ, glob.glob(os.path.join(ROOT, "include", "*.h")) + [torch.__file__]):
+    return f"torch {torch.__version__} in {os.path.dirname(torch.__file__)}, C++11 ABI " \
+           f"{int(torch._C._GLIBCXX_USE_CXX11_ABI)}, python {sysconfig.get_config_var('EXT_SUFFIX')}"
+
+
+def _built_for() -> str | None:
+    try:
+        with open(os.path.join(BUILD, "fastcall.for")) as f:
+            return f.read()
+    except OSError:
+        return None
+
+
+def _cuda_include() -> str:
+    nvcc = _nvcc()
+    return os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(shutil.which(nvcc) or nvcc))), "include")
+
+
+def _compile_fastcall() -> subprocess.Popen | None:
+    """Starts the compiler on fastcall.cpp if its object is older than its sources, or made for another
+    torch or Python."""
+    import torch
+
+    if _built_for() == _fastcall_for() and not _stale(FAST_SRC, FAST_OBJ, glob.glob(os.path.join(ROOT, "include", "*.h"))):
         return None
     root = os.path.join(os.path.dirname(torch.__file__), "include")
-    cuda = os.path.join(os.path.dirname(os.path.dirname(_nvcc())), "include")
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
            "-I", sysconfig.get_paths()["include"], "-I", root, "-I", os.path.join(root, "torch", "csrc", "api", "include"),
-           "-I", cuda, "-c", FAST_SRC, "-o", FAST_OBJ]
+           "-I", _cuda_include(), "-c", FAST_SRC, "-o", FAST_OBJ]
     return subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
 
 
@@ -106,8 +127,11 @@ def build(verbose: bool = False, jobs: int | None = None) -> str:
         out, _ = fast.communicate()
         if fast.returncode != 0:
             raise RuntimeError(f"g++ failed on {os.path.basename(FAST_SRC)}:\n{out}")
-    if _stale(FAST_OBJ, FAST, []):
+    if fast is not None or _stale(FAST_OBJ, FAST, []):
         _link_fastcall()
+    if fast is not None:
+        with open(os.path.join(BUILD, "fastcall.for"), "w") as f:
+            f.write(_fastcall_for())
     return LIB
 
 

@@ -44,3 +44,53 @@ def test_only_the_packed_calls_need_their_compiled_module(monkeypatch):
     for call, n in (("qk_norm_rope", 3), ("attn_packed", 4), ("kv4_store", 3), ("kv4_load", 1), ("attn_decode_kv4", 2)):
         with pytest.raises(ImportError, match="_fastcall"):
             getattr(blk, call)(*[None] * n)
+
+
+def test_the_compiled_module_is_rebuilt_for_another_torch_or_python(monkeypatch, tmp_path):
+    """Times of files say nothing about these: an install may keep older ones."""
+    import os
+    import sysconfig
+
+    from llama_family_decoder_gb300 import build
+    runs = []
+
+    class Ran:  # a compiler that writes its output file
+        returncode, stdout, stderr = 0, "", ""
+
+        def __init__(self, cmd, **kw):
+            runs.append(cmd)
+            with open(cmd[cmd.index("-o") + 1], "w"):
+                pass
+
+        def communicate(self):
+            return "", None
+
+    monkeypatch.setattr(build, "BUILD", str(tmp_path))
+    monkeypatch.setattr(build, "LIB", str(tmp_path / "libblk.so"))
+    monkeypatch.setattr(build, "FAST_OBJ", str(tmp_path / "fastcall.o"))
+    monkeypatch.setattr(build, "FAST", str(tmp_path / "_fastcall.so"))
+    monkeypatch.setattr(build.subprocess, "Popen", Ran)
+    monkeypatch.setattr(build.subprocess, "run", Ran)
+
+    def compiled():
+        del runs[:]
+        build.build()
+        return sum(build.FAST_SRC in cmd for cmd in runs), sum(build.FAST in cmd for cmd in runs)
+
+    assert compiled() == (1, 1) and compiled() == (0, 0)
+    with monkeypatch.context() as m:
+        m.setattr(torch, "__version__", "2.0.0+other")
+        assert compiled() == (1, 1) and compiled() == (0, 0)
+    assert compiled() == (1, 1)
+    with monkeypatch.context() as m:
+        m.setattr(sysconfig, "get_config_var", lambda name: ".other-abi.so")
+        assert compiled() == (1, 1)
+    # a compiler found on the search path only: its includes are beside it, not under "include"
+    there = tmp_path / "cuda" / "bin"
+    there.mkdir(parents=True)
+    (there / "nvcc").write_text("")
+    os.chmod(there / "nvcc", 0o755)
+    monkeypatch.setattr(build, "_nvcc", lambda: "nvcc")
+    monkeypatch.setenv("PATH", str(there))
+    assert compiled() == (1, 1)
+    assert str(tmp_path / "cuda" / "include") in next(cmd for cmd in runs if build.FAST_SRC in cmd)
