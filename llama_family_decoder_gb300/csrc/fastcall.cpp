@@ -122,13 +122,16 @@ PyObject* none() {
   Py_RETURN_NONE;
 }
 
-// A launch waits when the GPU's queue is full: other threads have the interpreter meanwhile.
+// A launch waits when the GPU's queue is full: other threads have the interpreter meanwhile. It is
+// taken back before anything here goes on, also when the call throws (a message that finds no memory).
+struct WithoutInterpreter {
+  PyThreadState* const t = PyEval_SaveThread();
+  ~WithoutInterpreter() { PyEval_RestoreThread(t); }
+};
 template <class F>
 bool launched(F call) {
-  PyThreadState* t = PyEval_SaveThread();
-  const int status = call();
-  PyEval_RestoreThread(t);
-  return status == BLK_OK;
+  const WithoutInterpreter scope;
+  return call() == BLK_OK;
 }
 
 PyObject* given(PyObject* o, const at::Tensor& made) {
