@@ -549,6 +549,7 @@ __global__ void __launch_bounds__(PACKED ? kPackedThreads : kThreads, 1) attn_tc
                   reinterpret_cast<uint4*>(o + c)[1] = b;
                 }
               }
+              __syncwarp();  // whole again for the next tensor-memory load
             }
           }
           tc_fence_before();
@@ -783,6 +784,7 @@ __global__ void __launch_bounds__(PACKED ? kPackedThreads : kThreads, 1) attn_tc
           alpha = ex2_approx(m_ref - mt);
           m_ref = mt;
         }
+        __syncwarp();
         if (j >= 1 && any) {
 #pragma unroll 1
           for (int c = 0; c < kD; c += 16) {
@@ -895,6 +897,7 @@ __global__ void __launch_bounds__(PACKED ? kPackedThreads : kThreads, 1) attn_tc
                   *reinterpret_cast<uint4*>(vrow + hb * kKVSub + ((c + r) & 7) * 16) = make_uint4(0, 0, 0, 0);
             }
             fence_proxy_async_smem();
+            __syncwarp();  // whole again for the tensor-memory loads, which want that
           }
           if (!live) {  // nobody reads these rows: whatever the score buffer holds may stand for P
             tc_fence_before();
