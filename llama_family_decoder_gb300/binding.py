@@ -275,7 +275,7 @@ class DecoderBlock:
 
     @functools.cached_property
     def _block(self):
-        return self._fast.block(self.handle.value, *self._sizes, self.desc.dtype == 1, self._dev, self.desc.qk_norm,
+        return fastcall().block(self.handle.value, *self._sizes, self.desc.dtype == 1, self._dev, self.desc.qk_norm,
                                 self.desc.no_rope) if self.handle else None
 
     def close(self):
