@@ -1593,6 +1593,11 @@ blk_status blk_kv4_store(blk_handle* h, const blk_head_rows* k, const blk_head_r
   if (!cu_seqlens && rows != batch) return fail(BLK_ERR_INVALID_ARG, "without cu_seqlens: a row per sequence");
   BLK_TRY(check_rows(h, k, rows, d.n_kv_heads, false, "k"));
   BLK_TRY(check_rows(h, v, rows, d.n_kv_heads, false, "v"));
+  // lens is written while other blocks read these
+  const int* const lens = cache->lens;
+  auto on_lens = [&](const int* x, int n) { return x && x < lens + batch && lens < x + n; };
+  if ((starts != lens && on_lens(starts, batch)) || on_lens(cu_seqlens, batch + 1))
+    return fail(BLK_ERR_INVALID_ARG, "starts or cu_seqlens overlaps lens");
   if (host_lens_max > cache->capacity) return fail(BLK_ERR_CACHE_FULL, "the rows do not fit the cache");
   if (batch == 0) return BLK_OK;
   BLK_TRY(check_device(h));

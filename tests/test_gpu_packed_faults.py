@@ -3,6 +3,7 @@ import numpy as np
 import pytest
 import torch
 
+from llama_family_decoder_gb300 import BlkError
 from tests.helpers import np64
 from tests.test_gpu_packed import (D, DEV, U, attn_ref, block, check_decode, check_packed, cu_of, filled_cache, ints, randn,
                                    values)
@@ -190,3 +191,23 @@ def test_attn_packed_large_scores_of_whole_numbers(H, Hkv, lens, top, slope, win
     out = blk.attn_packed(q, k, v, cu_of(lens))
     assert blk.last_status() == 0
     check_packed(out, q, k, v, lens, window=window)
+
+
+def test_kv4_store_refuses_lists_that_overlap_the_lengths():
+    """The lengths are written while other blocks still read their first slots or the list."""
+    blk = block(2, 2)
+    k, shared = randn(1, 4, 2, D), ints([0, 1, 2, 3, 4, 5, 6, 7, 8])
+    cache = blk.kv4_cache(4, 20)
+    cache["lens"] = shared[2:6]
+    for kw in (dict(starts=shared[1:5]), dict(starts=shared[3:7]), dict(cu_seqlens=shared[0:5]), dict(cu_seqlens=shared[4:9]),
+               dict(cu_seqlens=shared[2:7], starts=shared[:4].clone())):
+        with pytest.raises(BlkError) as e:
+            blk.kv4_store(cache, k, k, **kw)
+        assert e.value.status == 1
+    assert shared.tolist() == list(range(9))
+    blk.kv4_store(cache, k, k, starts=cache["lens"])  # an append
+    blk.kv4_store(cache, k[:2], k[:2], ints([0, 1, 1, 1, 2]), starts=shared[2:6])
+    assert shared.tolist() == [0, 1, 4, 4, 5, 7, 6, 7, 8]
+    cache["lens"] = shared[4:8]
+    blk.kv4_store(cache, k, k, starts=shared[:4])  # beside them
+    assert shared.tolist() == [0, 1, 4, 4, 1, 2, 5, 5, 8] and blk.last_status() == 0
