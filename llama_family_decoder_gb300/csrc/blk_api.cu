@@ -1501,6 +1501,8 @@ blk_status blk_qk_norm_rope(blk_handle* h, const blk_head_rows* q, const blk_hea
         ((rows > 1 && to[i]->row_stride != in[i]->row_stride) ||
          ((i ? d.n_kv_heads : d.n_heads) > 1 && to[i]->head_stride != in[i]->head_stride)))
       return fail(BLK_ERR_INVALID_ARG, "in place: input and output strides must be the same");
+  if (rows > 0 && (q_out->ptr == k->ptr || k_out->ptr == q->ptr))
+    return fail(BLK_ERR_INVALID_ARG, "an output is the other rows' input");
   if (rows > 0 && q_out->ptr == k_out->ptr) return fail(BLK_ERR_INVALID_ARG, "q_out and k_out are the same rows");
   if (d.qk_norm) {
     if (!q_gain || !k_gain) return fail(BLK_ERR_INVALID_ARG, "q/k norm gains NULL");

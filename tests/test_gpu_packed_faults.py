@@ -211,3 +211,17 @@ def test_kv4_store_refuses_lists_that_overlap_the_lengths():
     cache["lens"] = shared[4:8]
     blk.kv4_store(cache, k, k, starts=shared[:4])  # beside them
     assert shared.tolist() == [0, 1, 4, 4, 1, 2, 5, 5, 8] and blk.last_status() == 0
+
+
+def test_qk_norm_rope_refuses_an_output_over_the_other_input():
+    """In place means q over q and k over k: a warp may still read k while another writes q's rows there."""
+    blk = block(2, 2, qk_norm=True)
+    q, k, g, pos = randn(1, 8, 2, D), randn(2, 8, 2, D), randn(3, D), ints(list(range(8)))
+    want = blk.qk_norm_rope(q, k, pos, g, g)
+    for args, kw in (((q, k), dict(q_out=k)), ((q, k), dict(k_out=q)), ((q, k), dict(q_out=k, k_out=q)),
+                     ((q, q), dict(q_out=q)), ((q, q), dict(k_out=q))):
+        with pytest.raises(BlkError) as e:
+            blk.qk_norm_rope(*args, pos, g, g, **kw)
+        assert e.value.status == 1
+    blk.qk_norm_rope(q, k, pos, g, g, q_out=q, k_out=k)
+    assert torch.equal(q, want[0]) and torch.equal(k, want[1])
