@@ -8,8 +8,9 @@
 // so the tensor core multiplies codes, which 16-bit floats hold exactly, and scales touch one
 // score per key and group (or one probability) instead of 32 values. A code becomes a number
 // by placing its nibble under an exponent (an and-or for two codes) and taking the exponent's
-// value off again (one packed add, on the otherwise idle fp32 pipe; the integer pipe is what
-// bounds the unpacking). K in fp16, whose mantissa also takes a nibble 4 bits up without a
+// value off again (one packed add, on the otherwise idle fp32 pipe; the integer pipe has the most
+// to do in the unpacking): the known way from an integer to a float without a conversion, published
+// for 4-bit weights by Kim et al. 2022 ("Who Says Elephants Can't Run"). K in fp16, whose mantissa also takes a nibble 4 bits up without a
 // shift (1024 + 16 code); q is scaled by a power of two per head to use fp16's whole range.
 // V in bf16 (128 + code): p s_g keeps its exponent range whatever the values' size. p is rounded
 // to bf16 once, for all terms of a value alike; the 16-bit product p s_g goes in as two bf16
@@ -29,9 +30,12 @@
 // scales (5 KB) into its own two-stage ring with 16-byte asynchronous copies, a tile ahead,
 // and meets the other warps only when a pair's stretch ends, to merge their softmax states.
 // Rows behind the last key are filled with zeros, so nothing they hold is ever read.
-// Small batches take clusters instead (see CL below). 160 bytes a key and KV head: HBM bounds it,
-// then the integer pipe, which unpacks the codes (51% busy, and half-rate). 64 ragged sequences
-// of up to 8192 keys, 32 heads over 8: 98.1 us, 4.3 TB/s; one of 4000 keys: 7.1 us. Measured and
+// Small batches take clusters instead (see CL below). 160 bytes a key and KV head. No unit is at its
+// limit: DRAM 64% of the copy rate, issue slots 62%, the integer pipe 54%, the matrix pipe about
+// 31%; what is left are the four warps of a scheduler, each a chain of dependent steps (scores,
+// softmax, transposes, products). 64 ragged sequences of up to 8192 keys, 32 heads over 8: 98.2 us,
+// 4.3 TB/s; one of 4000 keys in a cache of that capacity: 7.0 us (the kernel is chosen by the
+// capacity, which the host knows: 1000 keys take 7.8 us in a cache of 32768). Measured and
 // not kept: a producer warp with a ring for all warps (93 us against 90.5); before that, against
 // 96 us, three stages (97), two CTAs of 200 registers (100), one of eight warps (103); and e4m3
 // operands, one product of which takes as long as the two fp16 ones that it would stand for.

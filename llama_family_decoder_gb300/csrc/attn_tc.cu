@@ -37,15 +37,16 @@
 // hides the keys outside each sequence's run of real tokens.
 // Packed sequences (PACKED) go through the same loop with 512 threads (see kPackedThreads):
 // whole prompts of any lengths, the heads of a KV head folded into a tile's rows. Bound by the
-// chain of a tile pair (scores, softmax, PV: 3250 cycles, of which the tensor core works 2048),
-// by the tiles on the diagonal and by item boundaries (4000 cycles): 409 us, 1.34 PFLOP/s, for
-// one sequence of 8190 (32 heads of their own), 112 us, 1.0 PFLOP/s, for 8 ragged ones of up to
-// 2048 (32 heads over 8), 24.7 us for 48 turns of up to 200. Measured and not kept: sixteen softmax warps, two threads a row, with
-// the scores read twice from tensor memory (498 us for the long one; held in registers they
-// spill, and shared memory leaves too little L1 for that: 1167); outputs staged in shared
-// memory for whole-row stores (48 short turns 39 -> 41 us); a third Q buffer (27 -> 28 us); masked
-// tiles read by 64 keys (24.7 -> 26.8 us) or a quarter ahead (27.4, spills); turns for the
-// exponentials alone (the long one 448 us).
+// chain of a tile pair (scores, softmax, PV: 3400 cycles by clock reads in the kernel, of which the
+// tensor core works 2048), and by an item's masked tiles and the start of the next one (3900 cycles
+// more than plain tiles take): 410 to 420 us, 1.3 PFLOP/s, for one sequence of 8190 (32 heads of
+// their own), 112 us, 1.0 PFLOP/s, for 8 ragged ones of up to 2048 (32 heads over 8), 24.5 us for 48
+// turns of up to 200. Measured and not kept: sixteen softmax warps, two threads a row, with the
+// scores read twice from tensor memory (498 us for the long one; held in registers they spill, and
+// shared memory leaves too little L1 for that: 1167); outputs staged in shared memory for whole-row
+// stores (48 short turns 39 -> 41 us); a third Q buffer (27 -> 28 us); masked tiles read by 64 keys
+// (24.7 -> 26.8 us) or a quarter ahead (27.4, spills); turns for the exponentials alone (the long
+// one 448 us).
 // Every wait is bounded; on expiry the CTA records a timeout, drains its own
 // copies and MMAs, frees its TMEM and returns.
 #include <cudaTypedefs.h>

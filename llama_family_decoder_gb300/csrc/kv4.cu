@@ -2,15 +2,16 @@
 // stand for). A row is one key or value of one KV head, 128 channels in four groups
 // of 32. A group keeps scale = bf16((hi - lo) / 15) and offset = bf16(lo) and the
 // codes clamp(rint((x - offset) / scale), 0, 15); a code stands for
-// offset + scale * code. bf16 scales share the inputs' exponent range, so no finite
-// group can overflow them; a group whose span hi - lo is not finite (a NaN or an
-// infinity in it) keeps the offset NaN, and one whose scale underflows keeps codes 0.
+// offset + scale * code. bf16 scales share the inputs' exponent range, so no scale
+// overflows; a group with a NaN or an infinity in it, or whose span hi - lo passes fp32's
+// range (from -3.3e38 to 3.3e38), keeps the offset NaN, and one whose scale underflows keeps
+// codes 0.
 //
 // The order of a row's 64 code bytes is the one the decode attention's tensor-core
 // fragments want (see kv4_byte_channel): a lane of an 8-row fragment finds all its
 // codes of a key in one 16-byte chunk, word j of it holding group j alone.
 //
-// HBM-bound, one pass: 16 lanes hold a row, 8 neighbouring channels each; a group is 4
+// One pass over the rows: 16 lanes hold a row, 8 neighbouring channels each; a group is 4
 // lanes (two shuffles for its extremes), and four more shuffles in the same 4 lanes
 // turn their codes into the row's words. A block takes a few token rows, all heads: it looks
 // up their slots once (a binary search of cu_seqlens in shared memory) while its first rows
