@@ -405,10 +405,11 @@ typedef struct {
  * starts[b], starts[b]+1, ... (starts NULL: lens[b], an append), and lens[b] becomes the slot
  * behind the last one. starts may not overlap lens unless it is lens (an append), nor may
  * cu_seqlens (INVALID_ARG). cu_seqlens rises from >= 0 to <= rows; another one sets the status
- * word to INVALID_ARG: numbers outside are read clamped, and with one that falls no length changes
- * and a row that several sequences claim goes to one of them. Rows of no sequence are ignored; a
- * row whose slot is outside the cache is left out, lens stops at the capacity and the status word says CACHE_FULL (or, when the caller
- * passes host_lens_max >= 0, the largest slot behind the last one of this call, the call itself).
+ * word to INVALID_ARG (over a CACHE_FULL): numbers outside are read clamped, and with one that
+ * falls no length changes and a row that several sequences claim goes to one of them. Rows of no
+ * sequence are ignored; a row whose slot is outside the cache is left out, lens stops at the
+ * capacity and the status word says CACHE_FULL (or, when the caller passes host_lens_max >= 0, the
+ * largest slot behind the last one of this call, the call itself).
  * Errors: INVALID_ARG, UNSUPPORTED (fp32 handle), ALIGNMENT, CACHE_FULL, CUDA. */
 blk_status blk_kv4_store(blk_handle* h, const blk_head_rows* k, const blk_head_rows* v, int rows,
                          const int* cu_seqlens, const int* starts, int batch, const blk_kv4_cache* cache,

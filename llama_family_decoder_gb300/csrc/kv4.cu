@@ -19,6 +19,8 @@
 // issue of instructions (70% of the slots, DRAM half busy), about 150 for two rows of a warp:
 // hence the packed arithmetic, the extremes on bf16 pairs and the running offsets. 9155 rows of
 // 8 KV heads, stored and then loaded: 27.4 us, 3.6 TB/s.
+#include <algorithm>
+
 #include "common.cuh"
 #include "kernels.h"
 #include "kv4.cuh"
@@ -90,8 +92,8 @@ struct Unit {
 // A number of cu_seqlens as it is read.
 __device__ __forceinline__ int clamped(int x, int rows) { return min(max(x, 0), rows); }
 
-// Whether cu_seqlens falls somewhere; one that does, or leaves [0, rows], sets the status word (of
-// one block's threads that call this). All threads of the block.
+// Whether cu_seqlens falls somewhere; one that does, or leaves [0, rows], sets the status word, also
+// where rows that it misplaced found no slot (CACHE_FULL) first. All threads of the block.
 __device__ __forceinline__ bool list_falls(const int* cu, int B, int rows, DevStatus* st) {
   bool bad = false, falls = false;
   for (int i = threadIdx.x; i < B; i += blockDim.x) {
@@ -99,7 +101,8 @@ __device__ __forceinline__ bool list_falls(const int* cu, int B, int rows, DevSt
     falls |= e < a;
     bad |= e < a || a < 0 || e > rows;
   }
-  if (bad && st) atomicCAS(&st->code, 0, kStatusInvalidArg);
+  if (bad && st && atomicCAS(&st->code, 0, kStatusInvalidArg) == kStatusCacheFull)
+    atomicCAS(&st->code, kStatusCacheFull, kStatusInvalidArg);
   return __syncthreads_or(falls);
 }
 
@@ -285,7 +288,7 @@ __global__ void __launch_bounds__(kThreads) kv4_store_kernel(const __grid_consta
 }
 
 // lens[b] += the rows of sequence b, after a store that read them as first slots. Every block
-// looks the list over.
+// looks the whole list over, so there is one per SM at most.
 __global__ void kv4_lens_kernel(const int* cu, int* lens, int B, int rows, int capacity, DevStatus* st) {
   pdl_launch_dependents();
   pdl_wait();
@@ -373,7 +376,7 @@ cudaError_t launch_kv4_store(const HeadRows& k, const HeadRows& v, int rows, con
   const int grid = rows > 0 ? (rows + p.block_rows - 1) / p.block_rows + (append ? 0 : 1) : 1;
   cudaError_t e = launch_pdl(kv4_store_kernel, grid, kThreads, 0, s, p, append ? 1 : 0);
   if (e != cudaSuccess || !append || !cu) return e;
-  return launch_pdl(kv4_lens_kernel, (B + 255) / 256, 256, 0, s, cu, c.lens, B, rows, c.capacity, st);
+  return launch_pdl(kv4_lens_kernel, std::min((B - 1) / 256 + 1, num_sms), 256, 0, s, cu, c.lens, B, rows, c.capacity, st);
 }
 
 cudaError_t launch_kv4_load(const HeadRows& k, const HeadRows& v, int rows, const int* cu, const int* starts, int B,

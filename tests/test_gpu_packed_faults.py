@@ -225,3 +225,23 @@ def test_qk_norm_rope_refuses_an_output_over_the_other_input():
         assert e.value.status == 1
     blk.qk_norm_rope(q, k, pos, g, g, q_out=q, k_out=k)
     assert torch.equal(q, want[0]) and torch.equal(k, want[1])
+
+
+def test_kv4_append_to_very_many_sequences():
+    """More sequences than the blocks that move the lengths on have threads, and more than a block copies."""
+    B, Hkv, cap = 100_000, 1, 4
+    blk = block(Hkv, Hkv)
+    k, v = randn(1, B, Hkv, D), randn(2, B, Hkv, D)
+    cache = blk.kv4_cache(B, cap)
+    cu = torch.arange(B + 1, device=DEV, dtype=torch.int32)
+    blk.kv4_store(cache, k, v, cu)
+    blk.kv4_store(cache, v, k, cu)
+    assert blk.last_status() == 0 and torch.all(cache["lens"] == 2)
+    ko, vo = blk.kv4_load(cache, cu, B, starts=cache["lens"] - 1)
+    assert torch.equal(ko.cpu(), values(v).bfloat16()) and torch.equal(vo.cpu(), values(k).bfloat16())
+    cu[-1] = B + 7
+    blk.kv4_store(cache, k, v, cu)
+    assert blk.last_status() == 1 and torch.all(cache["lens"] == 3)
+    cu[70_000] = 3
+    blk.kv4_store(cache, k, v, cu)
+    assert blk.last_status() == 1 and torch.all(cache["lens"] == 3)
