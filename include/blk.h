@@ -436,6 +436,117 @@ size_t blk_attn_decode_kv4_workspace_bytes(const blk_handle* h, int batch, int c
 blk_status blk_attn_decode_kv4(blk_handle* h, const blk_head_rows* q, const blk_kv4_cache* cache, int batch,
                                const blk_head_rows* o, void* workspace, size_t workspace_bytes, void* stream);
 
+/* ---- Speculative decoding over a paged cache ----
+ * A step forwards several new rows of each sequence at once: one token, a chain of drafted tokens,
+ * or a tree of them: blk_paged_append and blk_attn_paged per layer, blk_verify_drafts on the
+ * target's probabilities, blk_paged_keep for the rows that stay. (A prompt is appended and kept
+ * the same way; its attention may be blk_attn_packed's.) Rows are packed: sequence b's are rows
+ * cu_seqlens[b] .. cu_seqlens[b+1]-1, its row i being number i; cu_seqlens NULL: row b alone
+ * (rows == batch). cu_seqlens (device int32 [batch + 1]) rises from >= 0 to <= rows; another list
+ * sets the status word to INVALID_ARG, is read clamped, and what a row that several sequences
+ * claim gets is that of one of them. Rows of no sequence are ignored and their outputs left as
+ * they were. Calls run on the handle's device, which must be current; two calls may run at once
+ * on different streams if they share no workspace, no output and no cache that either writes.
+ *
+ * A paged KV cache in the handle's dtype: k, v [n_pages, n_kv_heads, page_size, head_dim],
+ * page_size 16, 32, 64, 128 or 256. Slot s of sequence b is row s % page_size of page
+ * pages[b * max_pages + s / page_size]. lens[b] slots are filled and kept: a call's new rows go to
+ * the slots from lens[b] on, and only blk_paged_keep moves lens. pages and lens are device int32,
+ * pages [batch, max_pages]; entries that no row of a call needs are not looked at. An entry that
+ * is needed and is not in [0, n_pages) sets the status word to INVALID_ARG; no memory outside the
+ * cache is read or written. Two sequences may share pages that no row is written to. */
+typedef struct {
+  void *k, *v;
+  const int* pages;
+  int* lens;
+  int n_pages, page_size, max_pages;
+} blk_paged_cache;
+
+/* The rotary of blk_paged_append: pair j < dims / 2 turns by the angle whose (cos, sin) is
+ * table[pos * dims / 2 + j] (device fp32 pairs [max_pos, dims / 2], 16-byte aligned), channels from
+ * dims on stay as they are. interleaved == 0: pair j is channels (j, j + dims / 2); 1: (2j, 2j + 1).
+ * table NULL: the handle's table (dims == head_dim, max_pos ignored). */
+typedef struct {
+  const void* table;
+  int dims, max_pos, interleaved;
+} blk_rope_layout;
+
+/* The (cos, sin) table of the handle's rotary (theta and scaling) over the first dims channels:
+ * inv_freq_j = rope_theta^(-2j/dims), stretched as by blk_create with dims in head_dim's place.
+ * table: device, max_pos * dims / 2 pairs of fp32, computed in double. dims is even, at most
+ * head_dim. Copies to the device on `stream` and waits for it. Errors: INVALID_ARG, UNSUPPORTED
+ * (a no_rope handle), ALIGNMENT, CUDA. */
+blk_status blk_rope_table(blk_handle* h, int dims, int max_pos, void* table, void* stream);
+
+/* Stage: per-head RMSNorm of q and k (when the handle has qk_norm, gains [head_dim]), the rotary of
+ * both (unless no_rope) and the append to the cache, both dtypes. q [rows, n_heads, d], k, v
+ * [rows, n_kv_heads, d]; row i of sequence b turns by position lens[b] + depths[row] (depths: device
+ * int32 [rows], e.g. the depth of a tree's node; NULL: lens[b] + i); the turned query goes to q_out
+ * (which may be q), the key and the value to slot lens[b] + i. lens does not move. A position
+ * outside [0, max_seq) (max_pos of a table) is clamped and sets the status word to INVALID_ARG. A
+ * row behind the page list is not written to the cache and sets it to CACHE_FULL, one
+ * whose page is none to INVALID_ARG. host_lens_max: the largest slot behind a row of this call, to have the
+ * capacity (max_pages * page_size) checked here, or -1. rope NULL: the handle's table, halves. Rows of
+ * dims / 2 pairs must be 16-byte multiples: bf16 dims % 16 == 0, fp32 dims % 8 == 0 and head_dim % 8 == 0.
+ * Errors: INVALID_ARG, UNSUPPORTED, ALIGNMENT, CACHE_FULL, CUDA. */
+blk_status blk_paged_append(blk_handle* h, const blk_head_rows* q, const blk_head_rows* k, const blk_head_rows* v,
+                            int rows, const int* cu_seqlens, const int* depths, int batch,
+                            const blk_paged_cache* cache, const blk_rope_layout* rope, const void* q_gain,
+                            const void* k_gain, const blk_head_rows* q_out, int host_lens_max, void* stream);
+
+/* Stage: attention of the appended rows (bf16 handles): row i of sequence b sees the slots below
+ * lens[b] and, at slots lens[b] + j, its ancestors j and itself. parents: device int32 [rows], the
+ * number of each row's parent within its sequence (below its own number), or negative: none; then a
+ * sequence has at most 64 rows, further ones get no output. Another parent is read as none. NULL: a
+ * chain, j <= i, of any length. (Either sets the status word to INVALID_ARG.) With a sliding_window
+ * W a row at depth e (its ancestors; of a chain, i) sees the positions from lens[b] + e - W + 1 on, an
+ * ancestor's position being lens[b] + its depth. q, o [rows, n_heads, 128]. A sequence whose rows pass
+ * its page list gets no output and sets the status word to CACHE_FULL; a page that is none makes
+ * the outputs of its sequence meaningless.
+ * What unused slots and pages hold reaches no output. A score that is NaN or +inf, or all of them
+ * -inf, gives the row NaN, as the formula does; a NaN or infinity in v of a slot that some row of the sequence
+ * sees may reach the others (0 * NaN). The probabilities are rounded to bf16 for
+ * their product with v, the output to bf16; everything between is fp32.
+ * workspace: blk_attn_paged_workspace_bytes(h, rows, batch); it may be NULL where that is 0.
+ * Errors: INVALID_ARG, UNSUPPORTED (fp32 handle), ALIGNMENT, WORKSPACE, CUDA. */
+size_t blk_attn_paged_workspace_bytes(const blk_handle* h, int rows, int batch);
+blk_status blk_attn_paged(blk_handle* h, const blk_head_rows* q, int rows, const int* cu_seqlens, const int* parents,
+                          int batch, const blk_paged_cache* cache, const blk_head_rows* o, void* workspace,
+                          size_t workspace_bytes, void* stream);
+
+/* Stage: speculative sampling over each sequence's rows (at most 64: more sets the status word to
+ * INVALID_ARG and keeps none). Row 0 is the sequence's last token, the others are drafts, tokens
+ * [rows], in the order of parents (as in blk_attn_paged; NULL: a chain; rows without a parent other
+ * than row 0 are never reached; neither is one with a parent or a token that is none, which sets the
+ * status word to INVALID_ARG). target: device fp32 [rows, vocab], row r the target's
+ * probabilities of what follows row r; draft NULL, or likewise the distribution that row r's
+ * children were each drawn from. u [rows] and u_next [batch]: uniform random numbers in [0, 1),
+ * fp32. The walk starts at row 0; at row r with P = target[r], c = 1, its children x, in order:
+ *   accepted if u[x] c q(x) < P(x) and P(x) > 0 (q = draft[r], without one q(x) = 1): the walk goes on from x;
+ *   else, with draft P := max(0, P - c q), c := sum P; without, c := c - P(x), P(x) := 0.
+ * When no child is accepted the next token is the first v with sum_{w <= v} P(w) > u_next sum P (P =
+ * target[r] where P is 0 everywhere), which makes the tokens distributed as the target's own.
+ * counts[b]: rows of the walk, row 0 among them; path [rows]: their numbers at
+ * cu_seqlens[b] + 0 .. counts[b] - 1, -1 behind; next[b]: the token. A sequence without
+ * rows: 0 and -1. Sums are carried to 2^-45 and compared in double. Row strides in elements, >= vocab
+ * (any, of one row). All outputs differ from the inputs and each other.
+ * Errors: INVALID_ARG, UNSUPPORTED (vocab above 2^22), CUDA; arrays are aligned as their elements are. */
+blk_status blk_verify_drafts(blk_handle* h, const float* target, long long target_stride, const float* draft,
+                             long long draft_stride, int rows, int vocab, const int* tokens, const int* parents,
+                             const int* cu_seqlens, const float* u, const float* u_next, int batch, int* counts,
+                             int* path, int* next, void* stream);
+
+/* Keeps the first counts[b] rows of path (device int32 [rows], as blk_verify_drafts gives it: rising, path[j] >= j) of
+ * each sequence: slot start + path[j] -> start + j in all n_caches (host array: the layers' caches, which
+ * share pages, lens and sizes and differ in k and v), lens[b] = start + counts[b]; start = starts[b], or
+ * lens[b] with starts NULL. path NULL: lens alone moves (a chain's first rows, a prompt's; cu_seqlens and rows are then
+ * ignored). A sequence with a path that is not rising in its rows, a negative count or start, or
+ * more rows than it has is left as it is (status word INVALID_ARG), as is one that the page
+ * list has no room for (CACHE_FULL). counts, path, cu_seqlens and starts may not overlap lens, unless starts is lens.
+ * Errors: INVALID_ARG, ALIGNMENT, CUDA. */
+blk_status blk_paged_keep(blk_handle* h, const blk_paged_cache* caches, int n_caches, const int* counts, const int* path,
+                          const int* cu_seqlens, const int* starts, int batch, int rows, void* stream);
+
 /* Scratch bytes a stage entry point needs for `rows` token rows. */
 size_t blk_stage_workspace_bytes(const blk_handle* h, int rows);
 

@@ -67,7 +67,13 @@ class blk_rope_axes(ctypes.Structure):
     _fields_ = [("n_axes", c_int), ("sections", c_int * 4), ("interleaved", c_int)]
 
 
-_ROWS = _KV4 = c_char_p  # see head_rows and kv4_cache_struct
+# blk_paged_cache (k, v, pages, lens, n_pages, page_size, max_pages) and blk_rope_layout (table, dims, max_pos,
+# interleaved), likewise
+paged_cache_struct = struct.Struct("@PPPPiii4x").pack
+rope_layout_struct = struct.Struct("@Piii4x").pack
+
+
+_ROWS = _KV4 = _PAGED = _LAYOUT = c_char_p  # see head_rows, kv4_cache_struct, paged_cache_struct and rope_layout_struct
 
 # name -> (restype, argtypes); the exported symbols of include/blk.h
 SIGNATURES = {
@@ -97,6 +103,17 @@ SIGNATURES = {
     "blk_attn_decode_kv4_workspace_bytes": (c_size_t, [c_void_p, c_int, c_int]),
     "blk_attn_decode_kv4": (c_int, [c_void_p, _ROWS, _KV4, c_int, _ROWS, c_void_p, c_size_t,
                                     c_void_p]),
+    "blk_rope_table": (c_int, [c_void_p, c_int, c_int, c_void_p, c_void_p]),
+    "blk_paged_append": (c_int, [c_void_p, _ROWS, _ROWS, _ROWS, c_int, c_void_p, c_void_p, c_int, _PAGED, _LAYOUT,
+                                 c_void_p, c_void_p, _ROWS, c_int, c_void_p]),
+    "blk_attn_paged_workspace_bytes": (c_size_t, [c_void_p, c_int, c_int]),
+    "blk_attn_paged": (c_int, [c_void_p, _ROWS, c_int, c_void_p, c_void_p, c_int, _PAGED, _ROWS, c_void_p, c_size_t,
+                               c_void_p]),
+    "blk_verify_drafts": (c_int, [c_void_p, c_void_p, c_longlong, c_void_p, c_longlong, c_int, c_int, c_void_p,
+                                  c_void_p, c_void_p, c_void_p, c_void_p, c_int, c_void_p, c_void_p, c_void_p,
+                                  c_void_p]),
+    "blk_paged_keep": (c_int, [c_void_p, _PAGED, c_int, c_void_p, c_void_p, c_void_p, c_void_p, c_int, c_int,
+                               c_void_p]),
     "blk_stage_workspace_bytes": (c_size_t, [c_void_p, c_int]),
     "blk_last_status": (c_int, [c_void_p]),
     "blk_xielu_effective": (None, [c_float, c_float, c_float, POINTER(c_float), POINTER(c_float)]),
@@ -573,6 +590,175 @@ class DecoderBlock:
         _check(lib().blk_attn_decode_kv4(self.handle, qi, c, batch, o, ws.data_ptr() if nbytes else None, nbytes,
                                          self._raw_stream(self._dev)))
         return out
+
+    # Speculative decoding over a paged cache: a step's new rows (one token, a chain or a tree of drafts)
+    # are appended, attend, and are verified; what is kept of them then moves lens.
+
+    def paged_cache(self, batch, capacity, page_size=64, n_pages=None, shared=None):
+        """An empty paged KV cache of this handle's type: dict(k, v, pages, lens), each sequence with pages
+        of its own for `capacity` slots. n_pages: pages to make instead, with the page table filled with
+        -1 for the caller to deal them out. shared: another layer's cache, whose pages and lens this one uses."""
+        torch = self._torch
+        if shared is not None:
+            return dict(shared, k=torch.zeros_like(shared["k"]), v=torch.zeros_like(shared["v"]))
+        per = -(-capacity // page_size)
+        if n_pages is None:
+            n_pages = batch * per
+            pages = torch.arange(n_pages, dtype=torch.int32, device=self._device).view(batch, per)
+        else:
+            pages = torch.full((batch, per), -1, dtype=torch.int32, device=self._device)
+        shape = (n_pages, self._sizes[1], page_size, self._sizes[2])
+        return {"k": torch.zeros(shape, dtype=self._dtype, device=self._device),
+                "v": torch.zeros(shape, dtype=self._dtype, device=self._device),
+                "pages": pages, "lens": torch.zeros(batch, dtype=torch.int32, device=self._device)}
+
+    def rope_table(self, dims=None, max_pos=None, stream=None):
+        """The (cos, sin) table [max_pos, dims / 2, 2] of the handle's rotary over the first `dims` channels
+        of a head, for paged_append's rope_table."""
+        if self._elsewhere(stream):
+            with _on_stream(self._device, stream):
+                return self.rope_table(dims, max_pos)
+        dims = self._sizes[2] if dims is None else dims
+        max_pos = self.desc.max_seq if max_pos is None else max_pos
+        if dims < 2 or dims % 2 or max_pos <= 0:
+            raise ValueError("dims, max_pos: an even number of channels and a positive number of positions")
+        t = self._torch.empty(max_pos, dims // 2, 2, dtype=self._torch.float32, device=self._device)
+        _check(lib().blk_rope_table(self.handle, dims, max_pos, t.data_ptr(), self._raw_stream(self._dev)))
+        return t
+
+    def _paged(self, cache):
+        torch, dev = self._torch, self._dev
+        if cache["k"].dim() != 4 or cache["pages"].dim() != 2:
+            raise ValueError("cache: k is [pages, KV heads, page_size, d] and pages [batch, max_pages]")
+        n_pages, _, page_size, _ = cache["k"].shape
+        batch, max_pages = cache["pages"].shape
+        shape = (n_pages, self._sizes[1], page_size, self._sizes[2])
+        return paged_cache_struct(_contiguous(cache["k"], "cache k", self._dtype, dev, shape),
+                                  _contiguous(cache["v"], "cache v", self._dtype, dev, shape),
+                                  _contiguous(cache["pages"], "cache pages", torch.int32, dev, (batch, max_pages)),
+                                  _contiguous(cache["lens"], "cache lens", torch.int32, dev, (batch,)),
+                                  n_pages, page_size, max_pages), batch
+
+    def paged_append(self, cache, q, k, v, cu_seqlens=None, depths=None, q_gain=None, k_gain=None, rope_table=None,
+                     interleaved=False, q_out=None, host_lens_max=-1, stream=None):
+        """Per-head RMSNorm (a qk_norm handle, with gains [d]) and rotary of rows q [N, H, d] and k [N, Hkv, d], of any
+        row and head strides like v [N, Hkv, d]; keys and values go behind the paged cache's lens, which do
+        not move. Row i of sequence b (cu_seqlens as in attn_packed; None: row b alone) has position
+        lens[b] + depths[row] (None: lens[b] + i). rope_table: fp32 [max_pos, dims / 2, 2] (rope_table()), None: the
+        handle's; interleaved: pairs of neighbouring channels. Returns q_out [N, H, d]; pass q to work in
+        place. host_lens_max: the largest slot behind a row, to have the capacity checked here."""
+        if stream is None:
+            r = self._fast.paged_append(self._block, cache, q, k, v, cu_seqlens, depths, q_gain, k_gain, rope_table,
+                                        interleaved, q_out, host_lens_max)
+            if r is not None:
+                return r
+        if self._elsewhere(stream):
+            with _on_stream(self._device, stream):
+                return self.paged_append(cache, q, k, v, cu_seqlens, depths, q_gain, k_gain, rope_table, interleaved,
+                                         q_out, host_lens_max)
+        H, Hkv, d = self._sizes
+        n = q.shape[0]
+        c, batch = self._paged(cache)
+        layout = gq = gk = None
+        if not self.desc.no_rope and (rope_table is not None or interleaved):
+            at, dims, max_pos = None, d, self.desc.max_seq
+            if rope_table is not None:
+                max_pos, half = rope_table.shape[0], rope_table.shape[1] if rope_table.dim() == 3 else 0
+                at, dims = _contiguous(rope_table, "rope_table", self._torch.float32, self._dev, (max_pos, half, 2)), 2 * half
+            layout = rope_layout_struct(at or 0, dims, max_pos, int(bool(interleaved)))
+        if self.desc.qk_norm:
+            if q_gain is None or k_gain is None:
+                raise ValueError("q_gain, k_gain: the handle norms queries and keys")
+            gq = _contiguous(q_gain, "q_gain", self._dtype, self._dev, (d,))
+            gk = _contiguous(k_gain, "k_gain", self._dtype, self._dev, (d,))
+        qs, ks = (n, H, d), (n, Hkv, d)
+        qi, ki, vi = self._rows(q, "q", qs), self._rows(k, "k", ks), self._rows(v, "v", ks)
+        cu, dp = self._int32(cu_seqlens, "cu_seqlens", batch + 1), self._int32(depths, "depths", n)
+        q_out, qo = self._out(q_out, "q_out", qs)
+        _check(lib().blk_paged_append(self.handle, qi, ki, vi, n, cu, dp, batch, c, layout, gq, gk, qo, host_lens_max,
+                                      self._raw_stream(self._dev)))
+        return q_out
+
+    def attn_paged(self, q, cache, cu_seqlens=None, parents=None, out=None, stream=None):
+        """Attention of the appended rows q [N, H, 128], of any row and head strides, over the paged cache: row i of
+        sequence b sees the slots below lens[b] and its ancestors' and its own. parents: int32 [N], each row's
+        parent within its sequence (-1: none), at most 64 rows a sequence; None: chains. Returns out
+        [N, H, 128]; rows of no sequence are left as they were (undefined in an out made here)."""
+        if stream is None:
+            r = self._fast.attn_paged(self._block, q, cache, cu_seqlens, parents, out)
+            if r is not None:
+                return r
+        if self._elsewhere(stream):
+            with _on_stream(self._device, stream):
+                return self.attn_paged(q, cache, cu_seqlens, parents, out)
+        H, _, d = self._sizes
+        n = q.shape[0]
+        c, batch = self._paged(cache)
+        qi = self._rows(q, "q", (n, H, d))
+        cu, up = self._int32(cu_seqlens, "cu_seqlens", batch + 1), self._int32(parents, "parents", n)
+        out, o = self._out(out, "out", (n, H, d))
+        nbytes = lib().blk_attn_paged_workspace_bytes(self.handle, n, batch)
+        ws = self._torch.empty(nbytes, dtype=self._torch.uint8, device=self._device) if nbytes else None
+        _check(lib().blk_attn_paged(self.handle, qi, n, cu, up, batch, c, o, ws.data_ptr() if nbytes else None, nbytes,
+                                    self._raw_stream(self._dev)))
+        return out
+
+    def _probs(self, t, name, shape):
+        """Rows of probabilities (address, row stride), of any row stride."""
+        _check_tensor(t, name, self._torch.float32, self._dev, shape)
+        if t.stride(1) != 1 and shape[1] > 1:
+            raise ValueError(f"{name}: the vocabulary must be contiguous")
+        return t.data_ptr(), t.stride(0)
+
+    def verify_drafts(self, target, tokens, u, u_next, cu_seqlens=None, parents=None, draft=None, stream=None):
+        """Speculative sampling over each sequence's rows, row 0 its last token and the others drafts: target fp32
+        [N, vocab], the target's probabilities of what follows each row; draft None (candidates without
+        probabilities), or likewise the distribution each row's children were drawn from; tokens int32 [N]; u fp32 [N]
+        and u_next [B], uniform in [0, 1). cu_seqlens and parents as in attn_paged, at most 64 rows a sequence.
+        Returns int32 (counts [B], path [N], next [B]): how many rows stay, which (-1 behind them), and the
+        token that follows."""
+        if stream is None:
+            r = self._fast.verify_drafts(self._block, target, tokens, u, u_next, cu_seqlens, parents, draft)
+            if r is not None:
+                return r
+        if self._elsewhere(stream):
+            with _on_stream(self._device, stream):
+                return self.verify_drafts(target, tokens, u, u_next, cu_seqlens, parents, draft)
+        torch, dev = self._torch, self._dev
+        if target.dim() != 2:
+            raise ValueError("target: [rows, vocab] is wanted")
+        n, vocab = target.shape
+        batch = u_next.numel()
+        t, t_row = self._probs(target, "target", (n, vocab))
+        g, g_row = (None, 0) if draft is None else self._probs(draft, "draft", (n, vocab))
+        tok, up = self._int32(tokens, "tokens", n), self._int32(parents, "parents", n)
+        if tok is None:
+            raise ValueError("tokens: the rows' tokens are wanted")
+        cu = self._int32(cu_seqlens, "cu_seqlens", batch + 1)
+        ua, un = _contiguous(u, "u", torch.float32, dev, (n,)), _contiguous(u_next, "u_next", torch.float32, dev, (batch,))
+        counts, path, nxt = (torch.empty(k, dtype=torch.int32, device=self._device) for k in (batch, n, batch))
+        _check(lib().blk_verify_drafts(self.handle, t, t_row, g, g_row, n, vocab, tok, up, cu, ua, un, batch,
+                                       counts.data_ptr(), path.data_ptr(), nxt.data_ptr(), self._raw_stream(dev)))
+        return counts, path, nxt
+
+    def paged_keep(self, caches, counts, path=None, cu_seqlens=None, starts=None, stream=None):
+        """Keeps the first counts[b] rows of path (int32 [B] and [N], as from verify_drafts) of each sequence: their keys
+        and values move to the slots from starts[b] (None: lens[b]) on in every layer's cache (a list; they
+        share pages and lens), and lens[b] behind them. path None: lens alone moves by counts (whole
+        prompts, a chain's first rows)."""
+        if stream is None and self._fast.paged_keep(self._block, caches, counts, path, cu_seqlens, starts):
+            return
+        if self._elsewhere(stream):
+            with _on_stream(self._device, stream):
+                return self.paged_keep(caches, counts, path, cu_seqlens, starts)
+        structs = [self._paged(c) for c in caches]
+        if not structs:
+            raise ValueError("caches: one at least")
+        batch, n = structs[0][1], 0 if path is None else path.shape[0]
+        _check(lib().blk_paged_keep(self.handle, b"".join(s for s, _ in structs), len(structs),
+                                    self._int32(counts, "counts", batch), self._int32(path, "path", n),
+                                    self._int32(cu_seqlens, "cu_seqlens", batch + 1), self._int32(starts, "starts", batch),
+                                    batch, n, self._raw_stream(self._dev)))
 
     def mlp(self, resid, h_normed, weights, out, stream=None):
         rows = resid.numel() // resid.shape[-1]

@@ -932,6 +932,53 @@ blk_status check_weights(const blk_desc& d, const blk_weights* w) {
   return BLK_OK;
 }
 
+// RoPE table [max_pos][dims / 2] of (cos, sin), in double: inv_freq_i = theta^(-2i/dims),
+// stretched by the descriptor's scaling. A frequency f of wavelength lam = 2 pi / f makes
+// r = L / lam turns over the original context L; fast components are kept, slow ones
+// divided by the factor s, and the rest blended. llama3 blends linearly in r:
+// (1 - g) f / s + g f, g = (r - lo) / (hi - lo). YaRN, as its published implementation
+// builds it, blends linearly in the pair index: the index where a component makes R turns
+// is i(R) = d ln(L / (2 pi R)) / (2 ln theta), and between a = floor(i(hi)) and
+// b = ceil(i(lo)) the weight of f / s grows from 0 to 1.
+std::vector<float2> rope_table(const blk_desc& d, int dims, int max_pos) {
+  const int half = dims / 2;
+  std::vector<double> inv_freq(half);
+  const double s_f = d.rope_factor, L = d.rope_orig_max_pos, lo = d.rope_low, hi = d.rope_high;
+  const double theta = (double)d.rope_theta, dd = (double)dims;
+  auto index_of_turns = [&](double r) { return dd * std::log(L / (2.0 * M_PI * r)) / (2.0 * std::log(theta)); };
+  double ya = 0.0, yb = 1.0;
+  if (d.rope_type == BLK_ROPE_YARN) {
+    ya = std::max(std::floor(index_of_turns(hi)), 0.0);
+    yb = std::min(std::ceil(index_of_turns(lo)), dd - 1.0);
+    if (yb == ya) yb = ya + 0.001;
+  }
+  for (int i = 0; i < half; ++i) {
+    const double f = std::pow(theta, -2.0 * i / dd);
+    double fi = f;
+    if (d.rope_type == BLK_ROPE_LLAMA3) {
+      const double lam = 2.0 * M_PI / f;
+      if (lam > L / lo) {
+        fi = f / s_f;
+      } else if (lam >= L / hi) {
+        const double g = (L / lam - lo) / (hi - lo);
+        fi = (1.0 - g) * f / s_f + g * f;
+      }
+    } else if (d.rope_type == BLK_ROPE_YARN) {
+      const double w = std::min(1.0, std::max(0.0, (i - ya) / (yb - ya)));
+      fi = (1.0 - w) * f + w * f / s_f;
+    }
+    inv_freq[i] = d.no_rope ? 0.0 : fi;  // no rotary: every angle 0, the identity rotation
+  }
+  const double att = d.rope_type == BLK_ROPE_YARN ? 0.1 * std::log(s_f) + 1.0 : 1.0;  // YaRN's sqrt(1/t)
+  std::vector<float2> table((size_t)max_pos * half);
+  for (int p = 0; p < max_pos; ++p)
+    for (int i = 0; i < half; ++i) {
+      const double ang = (double)p * inv_freq[i];
+      table[(size_t)p * half + i] = make_float2((float)(att * std::cos(ang)), (float)(att * std::sin(ang)));
+    }
+  return table;
+}
+
 }  // namespace
 
 // ================================================================== C ABI
@@ -1010,49 +1057,7 @@ blk_status blk_create(const blk_desc* desc, blk_handle** out) {
     delete h;
     return cuda_fail(e, "blk_create: device query");
   }
-  // RoPE table [max_seq][head_dim / 2] of (cos, sin), in double: inv_freq_i = theta^(-2i/d),
-  // stretched by the descriptor's scaling. A frequency f of wavelength lam = 2 pi / f makes
-  // r = L / lam turns over the original context L; fast components are kept, slow ones
-  // divided by the factor s, and the rest blended. llama3 blends linearly in r:
-  // (1 - g) f / s + g f, g = (r - lo) / (hi - lo). YaRN, as its published implementation
-  // builds it, blends linearly in the pair index: the index where a component makes R turns
-  // is i(R) = d ln(L / (2 pi R)) / (2 ln theta), and between a = floor(i(hi)) and
-  // b = ceil(i(lo)) the weight of f / s grows from 0 to 1.
-  const int half = d.head_dim / 2;
-  std::vector<double> inv_freq(half);
-  const double s_f = d.rope_factor, L = d.rope_orig_max_pos, lo = d.rope_low, hi = d.rope_high;
-  const double theta = (double)d.rope_theta, dd = (double)d.head_dim;
-  auto index_of_turns = [&](double r) { return dd * std::log(L / (2.0 * M_PI * r)) / (2.0 * std::log(theta)); };
-  double ya = 0.0, yb = 1.0;
-  if (d.rope_type == BLK_ROPE_YARN) {
-    ya = std::max(std::floor(index_of_turns(hi)), 0.0);
-    yb = std::min(std::ceil(index_of_turns(lo)), dd - 1.0);
-    if (yb == ya) yb = ya + 0.001;
-  }
-  for (int i = 0; i < half; ++i) {
-    const double f = std::pow(theta, -2.0 * i / dd);
-    double fi = f;
-    if (d.rope_type == BLK_ROPE_LLAMA3) {
-      const double lam = 2.0 * M_PI / f;
-      if (lam > L / lo) {
-        fi = f / s_f;
-      } else if (lam >= L / hi) {
-        const double g = (L / lam - lo) / (hi - lo);
-        fi = (1.0 - g) * f / s_f + g * f;
-      }
-    } else if (d.rope_type == BLK_ROPE_YARN) {
-      const double w = std::min(1.0, std::max(0.0, (i - ya) / (yb - ya)));
-      fi = (1.0 - w) * f + w * f / s_f;
-    }
-    inv_freq[i] = d.no_rope ? 0.0 : fi;  // no rotary: every angle 0, the identity rotation
-  }
-  const double att = d.rope_type == BLK_ROPE_YARN ? 0.1 * std::log(s_f) + 1.0 : 1.0;  // YaRN's sqrt(1/t)
-  std::vector<float2> table((size_t)d.max_seq * half);
-  for (int p = 0; p < d.max_seq; ++p)
-    for (int i = 0; i < half; ++i) {
-      const double ang = (double)p * inv_freq[i];
-      table[(size_t)p * half + i] = make_float2((float)(att * std::cos(ang)), (float)(att * std::sin(ang)));
-    }
+  const std::vector<float2> table = rope_table(d, d.head_dim, d.max_seq);
   e = cudaMalloc(&h->rope, table.size() * sizeof(float2));
   if (e == cudaSuccess) e = cudaMemcpy(h->rope, table.data(), table.size() * sizeof(float2), cudaMemcpyHostToDevice);
   if (e == cudaSuccess) e = cudaMalloc(&h->status, sizeof(DevStatus));
@@ -1650,6 +1655,200 @@ blk_status blk_attn_decode_kv4(blk_handle* h, const blk_head_rows* q, const blk_
                                            d.n_kv_heads, d.sliding_window, workspace, h->num_sms,
                                            static_cast<cudaStream_t>(stream), &why),
                     "4-bit decode attention", why);
+}
+
+// ------------------------------------------------------------------ paged cache, drafted tokens
+
+namespace {
+blk_status check_paged(const blk_paged_cache* c) {
+  if (!c || !c->k || !c->v || !c->pages || !c->lens) return fail(BLK_ERR_INVALID_ARG, "cache: NULL member");
+  if (c->n_pages <= 0 || c->max_pages <= 0) return fail(BLK_ERR_INVALID_ARG, "cache: n_pages and max_pages must be positive");
+  if (c->page_size < 16 || c->page_size > 256 || (c->page_size & (c->page_size - 1)))
+    return fail(BLK_ERR_UNSUPPORTED, "cache: page_size must be 16, 32, 64, 128 or 256");
+  if (!aligned16(c->k) || !aligned16(c->v)) return fail(BLK_ERR_ALIGNMENT, "cache: k and v must be 16-byte aligned");
+  if (c->k == c->v) return fail(BLK_ERR_INVALID_ARG, "cache: k and v are the same");
+  return BLK_OK;
+}
+
+PagedCache paged_cache(const blk_paged_cache* c) {
+  int shift = 0;
+  while ((1 << shift) < c->page_size) ++shift;
+  return {c->k, c->v, c->pages, c->lens, c->n_pages, shift, c->max_pages};
+}
+
+blk_status check_batch(int rows, int batch, const int* cu_seqlens) {
+  if (rows < 0 || batch < 0) return fail(BLK_ERR_INVALID_ARG, "rows and batch must not be negative");
+  if (!cu_seqlens && rows != batch) return fail(BLK_ERR_INVALID_ARG, "without cu_seqlens: a row per sequence");
+  return BLK_OK;
+}
+}  // namespace
+
+blk_status blk_rope_table(blk_handle* h, int dims, int max_pos, void* table, void* stream) {
+  if (!h || !table) return fail(BLK_ERR_INVALID_ARG, "NULL argument");
+  if (h->d.no_rope) return fail(BLK_ERR_UNSUPPORTED, "rotary table: the handle has no rotary");
+  if (dims < 2 || dims % 2 || dims > h->d.head_dim || max_pos <= 0)
+    return fail(BLK_ERR_INVALID_ARG, "rotary table: dims even and at most head_dim, max_pos positive");
+  if (!aligned16(table)) return fail(BLK_ERR_ALIGNMENT, "rotary table not 16-byte aligned");
+  BLK_TRY(check_device(h));
+  try {
+    const std::vector<float2> host = rope_table(h->d, dims, max_pos);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    cudaError_t e = cudaMemcpyAsync(table, host.data(), host.size() * sizeof(float2), cudaMemcpyHostToDevice, s);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+    return check_cuda(e, "rotary table");
+  } catch (const std::exception&) {
+    return fail(BLK_ERR_INVALID_ARG, "rotary table: too large for the host");
+  }
+}
+
+blk_status blk_paged_append(blk_handle* h, const blk_head_rows* q, const blk_head_rows* k, const blk_head_rows* v,
+                            int rows, const int* cu_seqlens, const int* depths, int batch,
+                            const blk_paged_cache* cache, const blk_rope_layout* rope, const void* q_gain,
+                            const void* k_gain, const blk_head_rows* q_out, int host_lens_max, void* stream) {
+  if (!h) return fail(BLK_ERR_INVALID_ARG, "NULL handle");
+  const blk_desc& d = h->d;
+  BLK_TRY(check_paged(cache));
+  BLK_TRY(check_batch(rows, batch, cu_seqlens));
+  if (d.head_dim % 8) return fail(BLK_ERR_UNSUPPORTED, "paged append: head_dim must be a multiple of 8");
+  BLK_TRY(check_rows(h, q, rows, d.n_heads, false, "q"));
+  BLK_TRY(check_rows(h, k, rows, d.n_kv_heads, false, "k"));
+  BLK_TRY(check_rows(h, v, rows, d.n_kv_heads, false, "v"));
+  BLK_TRY(check_rows(h, q_out, rows, d.n_heads, true, "q_out"));
+  if (rows > 0) {
+    if (q_out->ptr == q->ptr && ((rows > 1 && q_out->row_stride != q->row_stride) ||
+                                 (d.n_heads > 1 && q_out->head_stride != q->head_stride)))
+      return fail(BLK_ERR_INVALID_ARG, "in place: input and output strides must be the same");
+    for (const void* x : {k->ptr, v->ptr, cache->k, cache->v})
+      if (q_out->ptr == x) return fail(BLK_ERR_INVALID_ARG, "q_out is another argument's rows");
+    for (const void* x : {q->ptr, k->ptr, v->ptr})
+      if (cache->k == x || cache->v == x) return fail(BLK_ERR_INVALID_ARG, "the cache is an input");
+  }
+  if (d.qk_norm) {
+    if (!q_gain || !k_gain) return fail(BLK_ERR_INVALID_ARG, "q/k norm gains NULL");
+    if (!aligned16(q_gain) || !aligned16(k_gain)) return fail(BLK_ERR_ALIGNMENT, "q/k norm gains not 16-byte aligned");
+  }
+  const float2* table = d.no_rope ? nullptr : h->rope;
+  int dims = d.head_dim, max_pos = d.max_seq, inter = 0;
+  if (rope && !d.no_rope) {
+    if (rope->interleaved & ~1) return fail(BLK_ERR_INVALID_ARG, "rotary: interleaved is 0 or 1");
+    inter = rope->interleaved;
+    const int unit = d.dtype == BLK_BF16 ? 16 : 8;
+    if (rope->dims <= 0 || rope->dims > d.head_dim) return fail(BLK_ERR_INVALID_ARG, "rotary: dims must be in 1 .. head_dim");
+    if (rope->dims % unit) return fail(BLK_ERR_UNSUPPORTED, "rotary: dims must be a multiple of 16 (bf16) or 8 (fp32)");
+    if (rope->table) {
+      if (rope->max_pos <= 0) return fail(BLK_ERR_INVALID_ARG, "rotary: max_pos must be positive");
+      if (!aligned16(rope->table)) return fail(BLK_ERR_ALIGNMENT, "rotary: the table is not 16-byte aligned");
+      table = static_cast<const float2*>(rope->table);
+      max_pos = rope->max_pos;
+    } else if (rope->dims != d.head_dim) {
+      return fail(BLK_ERR_INVALID_ARG, "rotary: a part of the head needs a table of its own (blk_rope_table)");
+    }
+    dims = rope->dims;
+  }
+  if (host_lens_max > (long long)cache->max_pages * cache->page_size)
+    return fail(BLK_ERR_CACHE_FULL, "the rows do not fit the page list");
+  BLK_TRY(check_device(h));
+  return check_cuda(launch_paged_append(head_rows(q), head_rows(k), head_rows(v), head_rows(q_out), rows, cu_seqlens,
+                                        depths, batch, d.n_heads, d.n_kv_heads, d.head_dim, paged_cache(cache),
+                                        d.qk_norm ? q_gain : nullptr, d.qk_norm ? k_gain : nullptr, d.eps, table, dims,
+                                        max_pos, inter != 0, d.dtype == BLK_BF16, h->num_sms, h->status,
+                                        static_cast<cudaStream_t>(stream)),
+                    "paged append");
+}
+
+size_t blk_attn_paged_workspace_bytes(const blk_handle* h, int rows, int batch) {
+  if (!h || rows <= 0 || batch <= 0) return 0;
+  return attn_paged_ws_bytes(rows, batch, h->d.n_heads, h->d.n_kv_heads, h->num_sms);
+}
+
+blk_status blk_attn_paged(blk_handle* h, const blk_head_rows* q, int rows, const int* cu_seqlens, const int* parents,
+                          int batch, const blk_paged_cache* cache, const blk_head_rows* o, void* workspace,
+                          size_t workspace_bytes, void* stream) {
+  if (!h) return fail(BLK_ERR_INVALID_ARG, "NULL handle");
+  const blk_desc& d = h->d;
+  if (d.dtype != BLK_BF16) return fail(BLK_ERR_UNSUPPORTED, "paged attention takes bf16 handles");
+  BLK_TRY(check_paged(cache));
+  BLK_TRY(check_batch(rows, batch, cu_seqlens));
+  BLK_TRY(check_rows(h, q, rows, d.n_heads, false, "q"));
+  BLK_TRY(check_rows(h, o, rows, d.n_heads, true, "o"));
+  if (rows == 0 || batch == 0) return BLK_OK;
+  for (const void* x : {(const void*)q->ptr, (const void*)cache->k, (const void*)cache->v})
+    if (x == o->ptr) return fail(BLK_ERR_INVALID_ARG, "o must not be an input");
+  if ((__int128)cache->n_pages * d.n_kv_heads * cache->page_size > 0x7fffffff)
+    return fail(BLK_ERR_UNSUPPORTED, "paged attention: the cache has more than 2^31 - 1 rows");
+  const size_t need = attn_paged_ws_bytes(rows, batch, d.n_heads, d.n_kv_heads, h->num_sms);
+  if (need > 0 && (!workspace || workspace_bytes < need))
+    return fail(BLK_ERR_WORKSPACE, "paged attention: workspace missing or too small");
+  if (!aligned16(workspace)) return fail(BLK_ERR_ALIGNMENT, "workspace not 16-byte aligned");
+  BLK_TRY(check_device(h));
+  const char* why = nullptr;
+  return check_cuda(launch_attn_paged(head_rows(q), paged_cache(cache), head_rows(o), rows, cu_seqlens, parents, batch,
+                                      d.n_heads, d.n_kv_heads, d.sliding_window, workspace, h->num_sms, h->status,
+                                      (unsigned long long)g_wait_ns.load(), static_cast<cudaStream_t>(stream), &why),
+                    "paged attention", why);
+}
+
+blk_status blk_verify_drafts(blk_handle* h, const float* target, long long target_stride, const float* draft,
+                             long long draft_stride, int rows, int vocab, const int* tokens, const int* parents,
+                             const int* cu_seqlens, const float* u, const float* u_next, int batch, int* counts,
+                             int* path, int* next, void* stream) {
+  if (!h) return fail(BLK_ERR_INVALID_ARG, "NULL handle");
+  BLK_TRY(check_batch(rows, batch, cu_seqlens));
+  if (vocab <= 0) return fail(BLK_ERR_INVALID_ARG, "vocab must be positive");
+  if (vocab > 1 << 22) return fail(BLK_ERR_UNSUPPORTED, "vocab above 2^22");
+  if (batch == 0) return BLK_OK;
+  if (!u_next || !counts || !next || (rows > 0 && (!target || !tokens || !u || !path)))
+    return fail(BLK_ERR_INVALID_ARG, "NULL argument");
+  if (rows > 1 && (target_stride < vocab || (draft && draft_stride < vocab)))
+    return fail(BLK_ERR_INVALID_ARG, "row strides must be at least vocab");
+  if (target_stride >= 1ll << 31 || (draft && draft_stride >= 1ll << 31))
+    return fail(BLK_ERR_UNSUPPORTED, "row stride too large");
+  BLK_TRY(check_device(h));
+  return check_cuda(launch_verify_drafts(target, target_stride, draft, draft_stride, rows, vocab, tokens, parents,
+                                         cu_seqlens, u, u_next, batch, counts, path, next, h->num_sms, h->status,
+                                         static_cast<cudaStream_t>(stream)),
+                    "verification of drafts");
+}
+
+blk_status blk_paged_keep(blk_handle* h, const blk_paged_cache* caches, int n_caches, const int* counts, const int* path,
+                          const int* cu_seqlens, const int* starts, int batch, int rows, void* stream) {
+  if (!h) return fail(BLK_ERR_INVALID_ARG, "NULL handle");
+  const blk_desc& d = h->d;
+  if (n_caches <= 0 || !caches) return fail(BLK_ERR_INVALID_ARG, "caches: one at least");
+  if (path) BLK_TRY(check_batch(rows, batch, cu_seqlens));
+  if (batch < 0) return fail(BLK_ERR_INVALID_ARG, "batch must not be negative");
+  const size_t row_bytes = (size_t)d.head_dim * esize(d);
+  if (row_bytes % 16) return fail(BLK_ERR_UNSUPPORTED, "paged keep: rows of 16-byte multiples");
+  try {
+    std::vector<void*> kv;
+    for (int i = 0; i < n_caches; ++i) {
+      const blk_paged_cache& c = caches[i];
+      BLK_TRY(check_paged(&c));
+      if (c.pages != caches[0].pages || c.lens != caches[0].lens || c.n_pages != caches[0].n_pages ||
+          c.page_size != caches[0].page_size || c.max_pages != caches[0].max_pages)
+        return fail(BLK_ERR_INVALID_ARG, "caches: they must share pages, lens and sizes");
+      kv.push_back(c.k);
+      kv.push_back(c.v);
+    }
+    std::vector<void*> seen(kv);
+    std::sort(seen.begin(), seen.end());
+    if (std::adjacent_find(seen.begin(), seen.end()) != seen.end())
+      return fail(BLK_ERR_INVALID_ARG, "caches: two have the same k or v");
+    if (batch == 0) return BLK_OK;
+    if (!counts) return fail(BLK_ERR_INVALID_ARG, "counts is NULL");
+    const int* const lens = caches[0].lens;
+    auto on_lens = [&](const int* x, long long n) { return x && x < lens + batch && lens < x + n; };
+    if (on_lens(counts, batch) || (starts != lens && on_lens(starts, batch)) || (path && on_lens(path, rows)) ||
+        (path && on_lens(cu_seqlens, batch + 1ll)))
+      return fail(BLK_ERR_INVALID_ARG, "counts, path, cu_seqlens or starts overlaps lens");
+    BLK_TRY(check_device(h));
+    return check_cuda(launch_paged_keep(kv.data(), n_caches, paged_cache(caches), counts, path,
+                                        path ? cu_seqlens : nullptr, starts, batch, rows, d.n_kv_heads, (int)row_bytes,
+                                        h->num_sms, h->status, static_cast<cudaStream_t>(stream)),
+                      "paged keep");
+  } catch (const std::exception&) {
+    return fail(BLK_ERR_INVALID_ARG, "caches: out of host memory");
+  }
 }
 
 blk_status blk_mlp(blk_handle* h, const void* resid, const void* h_normed, const blk_weights* w, int rows, void* out,

@@ -86,6 +86,53 @@ struct Call {
   at::Tensor scratch(size_t bytes) const {
     return fresh({static_cast<int64_t>(bytes)}, at::kByte);
   }
+  blk_paged_cache paged(PyObject* o, int64_t& batch) {
+    blk_paged_cache c{};
+    if (!ok || !PyDict_Check(o)) {
+      ok = false;
+      return c;
+    }
+    void** const to[2] = {&c.k, &c.v};
+    const char* const names[2] = {"k", "v"};
+    int64_t n_pages = -1, size = -1;
+    for (int i = 0; i < 2; ++i) {
+      PyObject* x = PyDict_GetItemString(o, names[i]);
+      const at::Tensor* t = x ? tensor(x, b->type) : fail();
+      if (!t) return c;
+      ok = t->dim() == 4 && t->is_contiguous() && (n_pages < 0 || t->size(0) == n_pages) && t->size(1) == b->Hkv &&
+           (size < 0 || t->size(2) == size) && t->size(3) == b->d;
+      if (!ok) return c;
+      n_pages = t->size(0);
+      size = t->size(2);
+      *to[i] = t->data_ptr();
+    }
+    PyObject *x = PyDict_GetItemString(o, "pages"), *y = PyDict_GetItemString(o, "lens");
+    const at::Tensor *p = x ? tensor(x, at::kInt) : fail(), *l = y ? tensor(y, at::kInt) : fail();
+    if (!p || !l) return c;
+    ok = p->dim() == 2 && p->is_contiguous() && l->dim() == 1 && l->is_contiguous() && l->size(0) == p->size(0) &&
+         n_pages <= INT32_MAX && size <= INT32_MAX && p->size(0) <= INT32_MAX && p->size(1) <= INT32_MAX;
+    if (!ok) return c;
+    batch = p->size(0);
+    c.pages = static_cast<const int*>(p->data_ptr());
+    c.lens = static_cast<int*>(l->data_ptr());
+    c.n_pages = static_cast<int>(n_pages);
+    c.page_size = static_cast<int>(size);
+    c.max_pages = static_cast<int>(p->size(1));
+    return c;
+  }
+  const float* probs(PyObject* o, int64_t& n, int64_t& vocab, int64_t& stride) {  // [n, vocab]; below 0: any, and set
+    const at::Tensor* t = tensor(o, at::kFloat);
+    if (!t || t->dim() != 2 || (n >= 0 && t->size(0) != n) || (vocab >= 0 && t->size(1) != vocab) ||
+        (t->stride(1) != 1 && t->size(1) > 1)) {
+      ok = false;
+      return nullptr;
+    }
+    n = t->size(0);
+    vocab = t->size(1);
+    stride = t->stride(0);
+    ok = n <= INT32_MAX && vocab <= INT32_MAX;
+    return static_cast<const float*>(t->data_ptr());
+  }
   blk_kv4_cache cache(PyObject* o, int64_t& batch) {
     blk_kv4_cache c{};
     if (!ok || !PyDict_Check(o)) {
@@ -313,6 +360,141 @@ PyObject* attn_decode_kv4(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
   }
 }
 
+// paged_append(block, cache, q, k, v, cu_seqlens, depths, q_gain, k_gain, rope_table, interleaved, q_out, host_lens_max)
+PyObject* paged_append(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
+  if (n_args != 13) return none();
+  try {
+    Call c(a[0]);
+    int64_t batch = -1, n = -1;
+    const blk_paged_cache cache = c.paged(a[1], batch);
+    const blk_head_rows q = c.rows(a[2], n, c.b ? c.b->H : 0);
+    const blk_head_rows k = c.rows(a[3], n, c.b ? c.b->Hkv : 0), v = c.rows(a[4], n, c.b ? c.b->Hkv : 0);
+    if (!c.ok) return none();
+    const int *cu = c.ints(a[5], batch + 1), *depths = c.ints(a[6], n);
+    const void *gq = nullptr, *gk = nullptr;
+    if (c.b->qk_norm) {
+      gq = c.contiguous(a[7], c.b->type, c.b->d);
+      gk = c.contiguous(a[8], c.b->type, c.b->d);
+    }
+    const int inter = PyObject_IsTrue(a[10]);
+    const long most = PyLong_AsLong(a[12]);
+    if (inter < 0 || PyErr_Occurred()) return none();
+    blk_rope_layout layout{nullptr, static_cast<int>(c.b->d), 0, inter};
+    if (a[9] != Py_None) {
+      const at::Tensor* t = c.tensor(a[9], at::kFloat);
+      if (!t || t->dim() != 3 || !t->is_contiguous() || t->size(0) > INT32_MAX || t->size(1) > c.b->d || t->size(2) != 2)
+        return none();
+      layout = {t->data_ptr(), 2 * static_cast<int>(t->size(1)), static_cast<int>(t->size(0)), inter};
+    }
+    const bool plain = c.b->no_rope || (a[9] == Py_None && !inter);
+    at::Tensor to;
+    const blk_head_rows qo = c.out(a[11], n, c.b->H, to);
+    if (!c.ok || most > INT32_MAX || most < INT32_MIN || !launched([&] {
+          return blk_paged_append(c.b->h, &q, &k, &v, static_cast<int>(n), cu, depths, static_cast<int>(batch), &cache,
+                                  plain ? nullptr : &layout, gq, gk, &qo, static_cast<int>(most), c.stream);
+        }))
+      return none();
+    return given(a[11], to);
+  } catch (...) {
+    return none();
+  }
+}
+
+// attn_paged(block, q, cache, cu_seqlens, parents, out)
+PyObject* attn_paged(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
+  if (n_args != 6) return none();
+  try {
+    Call c(a[0]);
+    int64_t batch = -1, n = -1;
+    const blk_paged_cache cache = c.paged(a[2], batch);
+    const blk_head_rows q = c.rows(a[1], n, c.b ? c.b->H : 0);
+    if (!c.ok) return none();
+    const int *cu = c.ints(a[3], batch + 1), *parents = c.ints(a[4], n);
+    at::Tensor to, ws;
+    const blk_head_rows o = c.out(a[5], n, c.b->H, to);
+    if (!c.ok) return none();
+    const size_t bytes = blk_attn_paged_workspace_bytes(c.b->h, static_cast<int>(n), static_cast<int>(batch));
+    if (bytes) ws = c.scratch(bytes);
+    if (!launched([&] {
+          return blk_attn_paged(c.b->h, &q, static_cast<int>(n), cu, parents, static_cast<int>(batch), &cache, &o,
+                                bytes ? ws.data_ptr() : nullptr, bytes, c.stream);
+        }))
+      return none();
+    return given(a[5], to);
+  } catch (...) {
+    return none();
+  }
+}
+
+// verify_drafts(block, target, tokens, u, u_next, cu_seqlens, parents, draft)
+PyObject* verify_drafts(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
+  if (n_args != 8) return none();
+  try {
+    Call c(a[0]);
+    int64_t n = -1, vocab = -1, t_row = 0, d_row = 0;
+    const float* target = c.probs(a[1], n, vocab, t_row);
+    const float* draft = a[7] == Py_None ? nullptr : c.probs(a[7], n, vocab, d_row);
+    const at::Tensor* last = c.tensor(a[4], at::kFloat);
+    if (!c.ok || last->dim() != 1 || !last->is_contiguous() || last->numel() > INT32_MAX) return none();
+    const int64_t batch = last->numel();
+    const int* tokens = static_cast<const int*>(c.contiguous(a[2], at::kInt, n));
+    const float* u = static_cast<const float*>(c.contiguous(a[3], at::kFloat, n));
+    const int *cu = c.ints(a[5], batch + 1), *parents = c.ints(a[6], n);
+    if (!c.ok) return none();
+    const at::Tensor counts = c.fresh({batch}, at::kInt), path = c.fresh({n}, at::kInt), next = c.fresh({batch}, at::kInt);
+    if (!launched([&] {
+          return blk_verify_drafts(c.b->h, target, t_row, draft, d_row, static_cast<int>(n), static_cast<int>(vocab), tokens,
+                                   parents, cu, u, static_cast<const float*>(last->data_ptr()), static_cast<int>(batch),
+                                   static_cast<int*>(counts.data_ptr()), static_cast<int*>(path.data_ptr()),
+                                   static_cast<int*>(next.data_ptr()), c.stream);
+        }))
+      return none();
+    PyObject *x = THPVariable_Wrap(counts), *y = THPVariable_Wrap(path), *z = THPVariable_Wrap(next);
+    PyObject* r = x && y && z ? PyTuple_Pack(3, x, y, z) : nullptr;
+    Py_XDECREF(x);
+    Py_XDECREF(y);
+    Py_XDECREF(z);
+    return r;
+  } catch (...) {
+    return none();
+  }
+}
+
+// paged_keep(block, caches, counts, path, cu_seqlens, starts): True, or None
+PyObject* paged_keep(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
+  if (n_args != 6) return none();
+  try {
+    Call c(a[0]);
+    if (!c.ok || !PyList_Check(a[1]) || PyList_GET_SIZE(a[1]) < 1 || PyList_GET_SIZE(a[1]) > 256) return none();
+    blk_paged_cache caches[256];
+    const int n_caches = static_cast<int>(PyList_GET_SIZE(a[1]));
+    int64_t batch = -1, n = 0;
+    for (int i = 0; i < n_caches; ++i) {
+      int64_t its = -1;
+      caches[i] = c.paged(PyList_GET_ITEM(a[1], i), its);
+      if (!c.ok || (i && its != batch)) return none();
+      batch = its;
+    }
+    const int* path = nullptr;
+    if (a[3] != Py_None) {
+      const at::Tensor* t = c.tensor(a[3], at::kInt);
+      if (!t || t->dim() != 1 || !t->is_contiguous() || t->numel() > INT32_MAX) return none();
+      n = t->numel();
+      path = static_cast<const int*>(t->data_ptr());
+    }
+    const int* counts = a[2] == Py_None ? nullptr : c.ints(a[2], batch);
+    const int *cu = c.ints(a[4], batch + 1), *starts = c.ints(a[5], batch);
+    if (!c.ok || !counts || !launched([&] {
+          return blk_paged_keep(c.b->h, caches, n_caches, counts, path, cu, starts, static_cast<int>(batch),
+                                static_cast<int>(n), c.stream);
+        }))
+      return none();
+    Py_RETURN_TRUE;
+  } catch (...) {
+    return none();
+  }
+}
+
 typedef PyObject* (*Fast)(PyObject*, PyObject* const*, Py_ssize_t);
 PyMethodDef fast(const char* name, Fast f) {
   return {name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f)), METH_FASTCALL, nullptr};
@@ -324,6 +506,10 @@ PyMethodDef methods[] = {{"block", block, METH_VARARGS, nullptr},
                          fast("kv4_store", kv4_store),
                          fast("kv4_load", kv4_load),
                          fast("attn_decode_kv4", attn_decode_kv4),
+                         fast("paged_append", paged_append),
+                         fast("attn_paged", attn_paged),
+                         fast("verify_drafts", verify_drafts),
+                         fast("paged_keep", paged_keep),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_fastcall", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

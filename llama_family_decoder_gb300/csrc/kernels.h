@@ -62,6 +62,46 @@ cudaError_t launch_kv4_store(const HeadRows& k, const HeadRows& v, int rows, con
 cudaError_t launch_kv4_load(const HeadRows& k, const HeadRows& v, int rows, const int* cu, const int* starts, int B,
                             int Hkv, const Kv4Cache& c, int num_sms, DevStatus* st, cudaStream_t s);
 
+// ---------------------------------------------------------------- paged KV cache
+// k, v [n_pages, Hkv, 1 << page_shift, d] in the handle's type; pages [B, max_pages], lens [B].
+struct PagedCache {
+  void *k, *v;
+  const int* pages;
+  int* lens;
+  int n_pages, page_shift, max_pages;
+};
+
+// Rows cu[b] .. cu[b + 1] of sequence b (cu null: row b): norm (gains null: none) and rotary (table
+// [max_pos][dims / 2], null: none) of q and k at positions lens[b] + depths[row] (null: the row's number
+// i in its sequence); q to qo, k and v to slot lens[b] + i. Rows without a slot leave the cache alone
+// and record CACHE_FULL, or INVALID_ARG where the page table names no page.
+cudaError_t launch_paged_append(const HeadRows& q, const HeadRows& k, const HeadRows& v, const HeadRows& qo, int rows,
+                                const int* cu, const int* depths, int B, int H, int Hkv, int d, const PagedCache& c,
+                                const void* q_gain, const void* k_gain, float eps, const float2* table, int dims,
+                                int max_pos, bool interleaved, bool bf16, int num_sms, DevStatus* st, cudaStream_t s);
+
+// Attention of packed new rows over the cache (bf16, head_dim 128): row i of sequence b sees the slots
+// below lens[b] and the slots lens[b] + j of its ancestors and itself (parents null: j <= i), within the
+// window. ws: attn_paged_ws_bytes.
+size_t attn_paged_ws_bytes(int rows, int B, int H, int Hkv, int num_sms);
+cudaError_t launch_attn_paged(const HeadRows& q, const PagedCache& c, const HeadRows& o, int rows, const int* cu,
+                              const int* parents, int B, int H, int Hkv, int window, void* ws, int num_sms,
+                              DevStatus* st, unsigned long long wait_ns, cudaStream_t s, const char** why);
+
+// The walk of each sequence's drafted tree (see blk_verify_drafts). target, draft [rows][vocab] fp32 with
+// row strides in elements; draft, cu and parents may be null.
+cudaError_t launch_verify_drafts(const float* target, long long target_row, const float* draft, long long draft_row,
+                                 int rows, int vocab, const int* tokens, const int* parents, const int* cu,
+                                 const float* u, const float* u_next, int B, int* counts, int* path, int* next,
+                                 int num_sms, DevStatus* st, cudaStream_t s);
+
+// Slot start + path[j] -> start + j in every layer's cache (kv: k, v of each layer; page table and lens
+// shared), lens[b] = start + counts[b]; path null: lens alone.
+constexpr int kKeepLayers = 64;  // of a launch
+cudaError_t launch_paged_keep(void* const* kv, int n_layers, const PagedCache& c, const int* counts, const int* path,
+                              const int* cu, const int* starts, int B, int rows, int Hkv, int row_bytes, int num_sms,
+                              DevStatus* st, cudaStream_t s);
+
 // ---------------------------------------------------------------- embedding
 // out[r, :] = table[tokens[r], :] (row_bytes per row, a multiple of 16); ids outside
 // [0, vocab) give zero rows and set the status word to INVALID_ARG.
