@@ -1,101 +1,795 @@
 // Attention of a sequence's new rows (one token, a chain or a tree of drafted ones) over the paged
-// cache, grouped-query, head_dim 128:
+// cache on the 5th-generation tensor core (tcgen05 + TMEM), grouped-query ("arcee", "Grouped-query
+// attention, 128-wide heads"), head_dim 128:
 //   o = softmax(q k^T / sqrt(128)) v over the sequence's slots and the row's ancestors and itself.
-// A warp takes a row and head, four channels a lane, and goes over the keys one at a time with the
-// running maximum and sum of the softmax.
+//
+// Bound by reading the cache once. All heads of a KV head and all new rows of a sequence share its
+// keys, so they fold into the rows of one matrix tile: row r of a slot is head r % G of row r / G (G = H / Hkv),
+// a slot has 128 of them, and a CTA one or two slots that share each tile of 64 keys. The tensor core's
+// M = 128 costs the same for one row as for 128 and stays below the time a tile takes to arrive (64 keys of K and V
+// are 32 KB: 0.73 us at an SM's share of 6.8 TB/s; the two products take 0.3 us of it).
+//
+// Work is a line of key tiles: units (sequence, KV head, rows of the slots) one after the other, each as
+// many tiles as it has keys. The CTAs, one per SM, take equal stretches of it, whatever the sequences'
+// lengths; a unit that lies in several stretches leaves partial results (unnormalised outputs, the
+// running maximum and sum), which a second kernel joins in the order of the keys, so results do not
+// depend on timing. Lengths are on the device: every CTA adds up the line by itself.
+//
+// Warp 0 loads: its lanes look up the pages of the next 32 boxes (a box: the rows of a page in a tile)
+// and each issues a TMA copy of a box's half of K or V, 128-byte swizzled, into a ring of 32 KB
+// stages. Warp 1 (and 2 for the second slot) issues the products: S = Q K^T of tile j + 1 into one of
+// two TMEM buffers, then O += P V of tile j with P from TMEM. Four warps a slot hold a row a thread: scores
+// from TMEM, the running softmax in the log2 domain with a reference that moves only when a
+// score passes it by 2^8 (exact: softmax does not depend on it), P as bf16 over the scores; and before
+// a unit its queries to shared memory, after it the outputs.
+// Every wait is bounded; on expiry the CTA records a timeout, drains its own copies and MMAs, frees its
+// TMEM and returns.
+#include <algorithm>
+#include <cstring>
+
 #include "paged.cuh"
 
 namespace blk {
 
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kD = 128;
+constexpr int kBQ = 128;               // rows of a slot (MMA M)
+constexpr int kBK = 64;                // keys of a tile
+constexpr int kQSub = kBQ * 128;       // one 64-channel half of a slot's queries (bytes)
+constexpr int kQBytes = 2 * kQSub;
+constexpr int kKVSub = kBK * 128;      // one 64-channel half of a K or V tile
+constexpr int kStageBytes = 4 * kKVSub;
+constexpr float kRescaleLog2 = 8.0f;
 constexpr float kScaleLog2 = 1.4426950408889634f * 0.08838834764831845f;  // log2(e) / sqrt(128)
+constexpr unsigned long long kDrainNs = 2000000000ULL;
+template <int NS>
+struct Cfg {
+  static constexpr int kStages = NS == 1 ? 6 : 5;
+  static constexpr int kThreads = 128 + 128 * NS;
+  static constexpr int kBars = 2 * kStages + 9 * NS;
+  static constexpr int kSmem = 1024 + NS * kQBytes + kStages * kStageBytes + kBars * 8 + 64;
+  static_assert(kSmem <= 227 * 1024, "shared memory");
+};
 
-struct PagedAttnParams {
+struct AttnParams {
+  CUtensorMap tk, tv;  // [n_pages * Hkv * page_size, 128] bf16, boxes of 64 channels x `box` rows
   HeadRows q, o;
   PagedCache c;
   const int *cu, *parents;
-  int rows, B, H, Hkv, window;
+  int rows, B, H, Hkv, G, window;
+  int tq;         // rows of a sequence in a slot: 128 / G
+  int slots;      // slots of a CTA
+  int box_shift;  // log2 of a box's rows: those of a page, at most 64
+  int grid, min_tiles;
+  float2* ml;     // partial results [2 grid][128 slots]: (reference, sum)
+  float* acc;     // ... [2 grid][128 slots][128]
   DevStatus* status;
+  unsigned long long wait_ns;
 };
 
-__global__ void __launch_bounds__(kThreads) attn_paged_kernel(const __grid_constant__ PagedAttnParams p) {
-  pdl_launch_dependents();
-  pdl_wait();
-  const int lane = threadIdx.x & 31, b = blockIdx.y;
-  const SeqRows sr = seq_rows(p.cu, b, p.rows);
+__device__ __forceinline__ float ex2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float fmax3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+// D[tmem] (+)= A[tmem] * B[smem desc], bf16
+__device__ __forceinline__ void tc_mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
+                                          uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// ------------------------------------------------------------------ the line of tiles
+
+// A sequence that has something to do: rows [row0, row0 + n) over `len` slots.
+struct Seq {
+  int row0, n, len;
+};
+__device__ __forceinline__ Seq seq_of(const AttnParams& p, int b) {
+  const SeqRows r = seq_rows(p.cu, b, p.rows);
   const int len = p.c.lens[b];
-  const bool tree = p.parents != nullptr;
-  const bool fits = len >= 0 && (long long)len + sr.n <= page_slots(p.c);
-  const int n = fits ? (tree ? min(sr.n, kMaxNodes) : sr.n) : 0;
-  if (blockIdx.x == 0 && threadIdx.x == 0 && (!fits || seq_bad(p.cu, b, p.rows) || n < sr.n))
-    record(p.status, fits || len < 0 ? kStatusInvalidArg : kStatusCacheFull);
-  for (long long w = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); w < (long long)n * p.H;
-       w += gridDim.x * (kThreads / 32)) {
-    const int i = (int)(w / p.H), h = (int)(w % p.H), kvh = h / (p.H / p.Hkv);
-    unsigned long long kin = 0;
-    int depth = i;
-    if (tree) {
-      depth = 0;
-      for (int j = i; j >= 0;) {
-        if (p.window == 0 || depth < p.window) kin |= 1ull << j;
-        const int up = p.parents[sr.lo + j];
-        if (up >= j) record(p.status, kStatusInvalidArg);
-        if (up < 0 || up >= j) break;
-        j = up;
-        ++depth;
+  const bool fits = len >= 0 && (long long)len + r.n <= page_slots(p.c);
+  return {r.lo, fits ? (p.parents ? min(r.n, kMaxNodes) : r.n) : 0, len};
+}
+__device__ __forceinline__ int units_of(const AttnParams& p, const Seq& s) {
+  return (s.n + p.tq * p.slots - 1) / (p.tq * p.slots);
+}
+// Keys [first, end) that some row of unit t sees, or rather that may be.
+struct Keys {
+  int first, end;
+  __device__ __forceinline__ int tile0() const { return first / kBK; }
+  __device__ __forceinline__ int tiles() const { return (end + kBK - 1) / kBK - first / kBK; }
+};
+__device__ __forceinline__ Keys keys_of(const AttnParams& p, const Seq& s, int t) {
+  const int i0 = p.parents ? 0 : t * p.tq * p.slots;
+  const int i1 = p.parents ? s.n : min(s.n, i0 + p.tq * p.slots);
+  return {p.window > 0 ? max(0, s.len + i0 - p.window + 1) : 0, s.len + i1};
+}
+__device__ __forceinline__ int head_tiles(const AttnParams& p, const Seq& s) {  // of all units of a KV head
+  int n = 0;
+  for (int t = 0; t < units_of(p, s); ++t) n += keys_of(p, s, t).tiles();
+  return n;
+}
+
+// A CTA's stretch [lo, hi) of the line, and the sequence it begins in, whose own tiles begin at `base`.
+struct Stretch {
+  long long lo, hi, base;
+  int b, per;
+};
+// By one warp. Stretch number `c`; an empty one (lo >= hi) if the line ends before.
+__device__ __forceinline__ Stretch stretch_of(const AttnParams& p, int c, int lane) {
+  long long total = 0;
+  for (int b = lane; b < p.B; b += 32) total += (long long)p.Hkv * head_tiles(p, seq_of(p, b));
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+  Stretch s;
+  const long long per = max((total + p.grid - 1) / p.grid, (long long)p.min_tiles);
+  s.per = (int)per;
+  s.lo = c * per;
+  s.hi = min(total, s.lo + per);
+  s.base = 0;
+  s.b = 0;
+  if (s.lo >= s.hi) return s;
+  for (int b0 = 0; b0 < p.B; b0 += 32) {
+    const long long n = b0 + lane < p.B ? (long long)p.Hkv * head_tiles(p, seq_of(p, b0 + lane)) : 0;
+    long long upto = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long x = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += x;
+    }
+    const unsigned past = __ballot_sync(0xffffffffu, s.base + upto > s.lo);
+    if (past) {
+      const int at = __ffs(past) - 1;
+      s.b = b0 + at;
+      s.base += __shfl_sync(0xffffffffu, upto - n, at);
+      break;
+    }
+    s.base += __shfl_sync(0xffffffffu, upto, 31);
+  }
+  return s;
+}
+
+// Walks the units of a stretch: unit t of KV head kvh of sequence b, its tiles [j0, j1) of `tiles`.
+struct Walk {
+  Seq seq;
+  Keys keys;
+  int b, kvh, t, tiles, j0, j1;
+  long long left;
+  __device__ __forceinline__ void unit(const AttnParams& p) {
+    keys = keys_of(p, seq, t);
+    tiles = keys.tiles();
+  }
+  __device__ __forceinline__ Walk(const AttnParams& p, const Stretch& s) {
+    left = s.hi - s.lo;
+    j0 = j1 = tiles = kvh = t = 0;
+    b = s.b;
+    if (left <= 0) return;
+    seq = seq_of(p, b);
+    long long at = s.lo - s.base;
+    const int per_head = head_tiles(p, seq);
+    if (per_head <= 0) {  // lengths that change meanwhile: no walk leaves the lists
+      left = 0;
+      return;
+    }
+    kvh = (int)(at / per_head);
+    int rest = (int)(at - (long long)kvh * per_head);
+    unit(p);
+    while (rest >= tiles) {  // rest < per_head: it ends within the units
+      rest -= tiles;
+      ++t;
+      unit(p);
+    }
+    j0 = rest;
+    j1 = (int)min((long long)tiles, j0 + left);
+  }
+  __device__ __forceinline__ bool on() const { return left > 0; }
+  __device__ __forceinline__ void next(const AttnParams& p) {
+    left -= j1 - j0;
+    if (left <= 0) return;
+    if (++t >= units_of(p, seq)) {
+      t = 0;
+      if (++kvh >= p.Hkv) {
+        kvh = 0;
+        do {
+          if (++b >= p.B) {
+            left = 0;
+            return;
+          }
+          seq = seq_of(p, b);
+        } while (seq.n == 0);
       }
     }
-    const int first = p.window > 0 ? max(0, len + depth - p.window + 1) : 0;
-    const int end = len + (tree ? n : i + 1);
-    float q[4], o[4] = {0.f, 0.f, 0.f, 0.f}, m = -INFINITY, l = 0.f;
-    auto load4 = [](const __nv_bfloat16* x, float (&f)[4]) {
-      const uint2 u = *reinterpret_cast<const uint2*>(x);
-      const float2 a = unpack_bf16x2(u.x), c = unpack_bf16x2(u.y);
-      f[0] = a.x, f[1] = a.y, f[2] = c.x, f[3] = c.y;
-    };
-    load4(static_cast<const __nv_bfloat16*>(p.q.ptr) + (sr.lo + i) * p.q.row + h * p.q.head + 4 * lane, q);
-    for (int s = first; s < end; ++s) {
-      if (tree && s >= len && !(kin >> (s - len) & 1)) continue;
-      const PagePlace at = page_place(p.c, b, s);
-      if (at.page < 0) {
-        record(p.status, kStatusInvalidArg);
+    unit(p);
+    j0 = 0;
+    j1 = (int)min((long long)tiles, left);
+  }
+  __device__ __forceinline__ bool whole() const { return j0 == 0 && j1 == tiles; }
+  // the first row of a slot
+  __device__ __forceinline__ int node0(const AttnParams& p, int g) const { return (t * p.slots + g) * p.tq; }
+};
+
+__device__ __forceinline__ unsigned long long bits_from(int lo) {  // bits lo ..
+  return lo <= 0 ? ~0ull : lo >= 64 ? 0ull : ~0ull << lo;
+}
+__device__ __forceinline__ unsigned long long bits_below(int hi) { return ~bits_from(hi); }
+
+// ------------------------------------------------------------------ the kernel
+
+template <int NS>
+__global__ void __launch_bounds__(Cfg<NS>::kThreads, 1) attn_paged_kernel(const __grid_constant__ AttnParams p) {
+  typedef Cfg<NS> C;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* const smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* const sQ = smem;
+  uint8_t* const ring = smem + NS * kQBytes;
+  uint64_t* const bars = reinterpret_cast<uint64_t*>(ring + C::kStages * kStageBytes);
+  uint32_t* const tmem_holder = reinterpret_cast<uint32_t*>(bars + C::kBars);
+  volatile int* const abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
+  Stretch* const stretch = reinterpret_cast<Stretch*>(tmem_holder + 2);
+  static_assert(sizeof(Stretch) <= 48, "room behind the barriers");
+  auto bar = [&](int i) { return smem_u32(&bars[i]); };
+  auto full = [&](int s) { return bar(s); };
+  auto empty = [&](int s) { return bar(C::kStages + s); };
+  auto mine = [&](int g, int i) { return bar(2 * C::kStages + 9 * g + i); };
+  auto q_full = [&](int g) { return mine(g, 0); };
+  auto s_full = [&](int g, int buf) { return mine(g, 1 + buf); };
+  auto p_ready = [&](int g, int buf) { return mine(g, 3 + buf); };
+  auto pv_done = [&](int g) { return mine(g, 5); };
+  auto o_done = [&](int g) { return mine(g, 6); };
+  auto o_free = [&](int g) { return mine(g, 7); };
+  auto drain = [&](int g) { return mine(g, 8); };
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const unsigned long long budget = p.wait_ns;
+  constexpr int kTmemCols = 256 * NS;  // of slot g: S and P in 256 g and 256 g + 64, O from 256 g + 128
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::kStages; ++s) {
+      mbar_init(full(s), 1);
+      mbar_init(empty(s), NS);
+    }
+    for (int g = 0; g < NS; ++g) {
+      mbar_init(q_full(g), 128);
+      for (int i = 0; i < 2; ++i) {
+        mbar_init(s_full(g, i), 1);
+        mbar_init(p_ready(g, i), 128);
+      }
+      mbar_init(pv_done(g), 1);
+      mbar_init(o_done(g), 1);
+      mbar_init(o_free(g), 128);
+      mbar_init(drain(g), 1);
+    }
+    *abort_flag = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&p.tk);
+    tma_prefetch_desc(&p.tv);
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(tmem_holder), kTmemCols);
+    tmem_relinquish();
+  }
+  pdl_wait();  // queries, cache, lengths and lists come from earlier kernels
+  // only now: what earlier kernels wrote is then there for the second kernel too, which looks its part up
+  // while this one runs
+  pdl_launch_dependents();
+  if (warp == 0) {
+    const Stretch s = stretch_of(p, blockIdx.x, lane);
+    if (lane == 0) *stretch = s;
+  }
+  if (warp == 3 && blockIdx.x == 0) {  // what the lists say that they should not
+    bool bad = false, over = false;
+    for (int b = lane; b < p.B; b += 32) {
+      const SeqRows r = seq_rows(p.cu, b, p.rows);
+      const int len = p.c.lens[b];
+      bad |= seq_bad(p.cu, b, p.rows) || len < 0 || (p.parents && r.n > kMaxNodes);
+      over |= len >= 0 && (long long)len + r.n > page_slots(p.c);
+    }
+    if (bad) record(p.status, kStatusInvalidArg);
+    if (over) record(p.status, kStatusCacheFull);
+    __syncwarp();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_holder;
+  // What is in flight, for the drain after an abort: the stages issued (with the parity of their last
+  // phase) and whether any MMA was.
+  uint32_t issued = 0, parity = 0;
+  bool mma_issued = false;
+
+  if (warp == 0) {
+    // ---------------- the cache's tiles, all lanes
+    const uint64_t once = l2_policy_evict_first();
+    const int page_shift = p.c.page_shift, boxes = kBK >> p.box_shift;
+    int J = 0;
+    bool failed = false;
+    for (Walk w(p, *stretch); w.on() && !failed; w.next(p)) {
+      const int* const pages = p.c.pages + (size_t)w.b * p.c.max_pages;
+      const int box0 = (w.keys.tile0() + w.j0) * boxes;  // the first box of the part
+      const int n_boxes = (w.j1 - w.j0) * boxes;
+      auto look_up = [&](int i) {  // the page of the part's box i + lane, or -1 where nobody needs it
+        const int slot = (box0 + i + lane) << p.box_shift;
+        int page = -1;
+        if (i + lane < n_boxes && slot < w.keys.end && slot + (1 << p.box_shift) > w.keys.first) {
+          page = pages[slot >> page_shift];
+          if (page < 0 || page >= p.c.n_pages) {
+            record(p.status, kStatusInvalidArg);
+            page = 0;
+          }
+        }
+        return page;
+      };
+      int page = look_up(0), ahead = look_up(32);
+      for (int i = 0; i < n_boxes; i += boxes, ++J) {
+        if (i > 0 && (i & 31) == 0) {
+          page = ahead;
+          ahead = look_up(i + 32);
+        }
+        const int s = J % C::kStages;
+        const uint32_t ph = (J / C::kStages) & 1;
+        if (!__all_sync(0xffffffffu, mbar_wait(empty(s), ph ^ 1, budget, abort_flag))) {
+          failed = true;
+          break;
+        }
+        const int box = lane >> 2, part = lane & 3;
+        const int its = __shfl_sync(0xffffffffu, page, (i & 31) + (box < boxes ? box : 0));
+        const bool loads = box < boxes && its >= 0;
+        const int n = __popc(__ballot_sync(0xffffffffu, loads)) >> 2;
+        if (lane == 0) mbar_arrive_expect_tx(full(s), (uint32_t)(n * 512) << p.box_shift);
+        __syncwarp();
+        if (loads) {
+          const int slot = (box0 + i + box) << p.box_shift;
+          const int row = ((its * p.Hkv + w.kvh) << page_shift) + (slot & ((1 << page_shift) - 1));
+          const uint32_t dst = smem_u32(ring + s * kStageBytes) + part * kKVSub + ((box << p.box_shift) << 7);
+          tma_load_2d_hint(dst, part < 2 ? &p.tk : &p.tv, 64 * (part & 1), row, full(s), once);
+        }
+        __syncwarp();
+        issued |= 1u << s;
+        parity = (parity & ~(1u << s)) | (ph << s);
+      }
+    }
+    if (failed && lane == 0) {
+      *abort_flag = 1;
+      report_timeout(p.status, 0x50);
+    }
+  } else if (warp <= NS) {
+    // ---------------- the products of a slot
+    if (lane == 0) {
+      const int g = warp - 1;
+      constexpr uint32_t idesc_s = idesc_bf16_f32(kBQ, kBK);
+      constexpr uint32_t idesc_pv = idesc_bf16_f32(kBQ, kD) | (1u << 16);  // B (V) is MN-major
+      const uint64_t dq = smem_desc_sw128(smem_u32(sQ + g * kQBytes));
+      const uint64_t dk = smem_desc_sw128(smem_u32(ring));
+      const uint64_t dv = smem_desc_sw128_mn(smem_u32(ring + 2 * kKVSub), kKVSub, 1024);
+      const uint32_t s_tmem = tmem + 256 * g, o_tmem = tmem + 256 * g + 128;
+      int J = 0, A = 0, units = 0;  // tiles of the CTA and of this slot, and its units
+      bool failed = false;
+      for (Walk w(p, *stretch); w.on() && !failed; w.next(p)) {
+        const int n = w.j1 - w.j0;
+        if (w.node0(p, g) >= w.seq.n) {  // nothing for this slot: the stages go back
+          for (int j = 0; j < n && !failed; ++j, ++J) {
+            if (!mbar_wait(full(J % C::kStages), (J / C::kStages) & 1, budget, abort_flag)) failed = true;
+            else mbar_arrive(empty(J % C::kStages));
+          }
+          continue;
+        }
+        auto issue_s = [&](int Jn, int An) {
+          const int st = Jn % C::kStages;
+          if (!mbar_wait(full(st), (Jn / C::kStages) & 1, budget, abort_flag)) return false;
+          tc_fence_after();
+          const uint64_t b = dk + (uint64_t)(st * (kStageBytes >> 4));
+#pragma unroll
+          for (int kk = 0; kk < kD / 16; ++kk)
+            tc_mma_bf16(s_tmem + 64 * (An & 1), dq + (uint64_t)((kk >> 2) * (kQSub >> 4) + (kk & 3) * 2),
+                        b + (uint64_t)((kk >> 2) * (kKVSub >> 4) + (kk & 3) * 2), idesc_s, kk > 0 ? 1u : 0u);
+          tc_commit(s_full(g, An & 1));
+          mma_issued = true;
+          return true;
+        };
+        if (!mbar_wait(q_full(g), units & 1, budget, abort_flag) || !issue_s(J, A)) {
+          failed = true;
+          break;
+        }
+        for (int j = 0; j < n; ++j, ++J, ++A) {
+          // the next scores first: they are under way while the softmax works on these. Their buffer's
+          // P has been read: its product was issued before.
+          if (j + 1 < n && !issue_s(J + 1, A + 1)) {
+            failed = true;
+            break;
+          }
+          if ((j == 0 && units > 0 && !mbar_wait(o_free(g), (units - 1) & 1, budget, abort_flag)) ||
+              !mbar_wait(p_ready(g, A & 1), (A >> 1) & 1, budget, abort_flag)) {
+            failed = true;
+            break;
+          }
+          tc_fence_after();
+          const int st = J % C::kStages;
+          const uint64_t b = dv + (uint64_t)(st * (kStageBytes >> 4));
+#pragma unroll
+          for (int kk = 0; kk < kBK / 16; ++kk)
+            tc_mma_ts(o_tmem, s_tmem + 64 * (A & 1) + kk * 8, b + (uint64_t)(kk * (16 * 128 >> 4)), idesc_pv,
+                      (j > 0 || kk > 0) ? 1u : 0u);
+          tc_commit(empty(st));
+          tc_commit(pv_done(g));
+        }
+        if (failed) break;
+        tc_commit(o_done(g));
+        ++units;
+      }
+      if (failed) {
+        *abort_flag = 1;
+        report_timeout(p.status, 0x51);
+      }
+    }
+  } else if (warp >= 4) {
+    // ---------------- a slot's rows, one a thread
+    const int g = (warp - 4) >> 2, quarter = warp & 3;
+    const int r = quarter * 32 + lane;
+    const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
+    const uint32_t s_taddr = tmem + lane_off + 256 * g, o_taddr = s_taddr + 128;
+    const int node_of_row = r / p.G, head_of_row = r - node_of_row * p.G;
+    int J = 0, A = 0, units = 0, part = 2 * blockIdx.x;
+    bool failed = false;
+    for (Walk w(p, *stretch); w.on() && !failed; w.next(p), part = 2 * blockIdx.x + 1) {
+      const int n = w.j1 - w.j0, node0 = w.node0(p, g);
+      if (node0 >= w.seq.n) {
+        J += n;
         continue;
       }
-      const long long row = place_row(p.c, at, p.Hkv, kvh) * 128 + 4 * lane;
-      float k[4], v[4];
-      load4(static_cast<const __nv_bfloat16*>(p.c.k) + row, k);
-      load4(static_cast<const __nv_bfloat16*>(p.c.v) + row, v);
-      const float x = warp_sum(q[0] * k[0] + q[1] * k[1] + q[2] * k[2] + q[3] * k[3]) * kScaleLog2;
-      const float top = fmaxf(m, x), mu = top == -INFINITY ? 0.f : top;
-      const float keep = exp2f(m - mu), e = exp2f(x - mu);
-      m = top;
-      l = l * keep + e;
+      // queries: 16 lanes a row, four rounds of eight rows' loads
+      {
+        const int chunk = lane & 15;
+        const uint32_t dst = smem_u32(sQ + g * kQBytes) + (chunk >> 3) * kQSub;
 #pragma unroll
-      for (int c = 0; c < 4; ++c) o[c] = o[c] * keep + e * v[c];
+        for (int i0 = 0; i0 < 16; i0 += 8) {
+          uint4 u[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int row = quarter * 32 + 2 * (i0 + i) + (lane >> 4);
+            const int nd = row / p.G, hd = row - nd * p.G;
+            u[i] = make_uint4(0, 0, 0, 0);
+            if (nd < p.tq && node0 + nd < w.seq.n)
+              u[i] = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q.ptr) +
+                                                     (w.seq.row0 + node0 + nd) * p.q.row +
+                                                     (long long)(w.kvh * p.G + hd) * p.q.head + 8 * chunk);
+          }
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int row = quarter * 32 + 2 * (i0 + i) + (lane >> 4);
+            st_shared_u4(dst + row * 128 + (((chunk & 7) ^ (row & 7)) << 4), u[i].x, u[i].y, u[i].z, u[i].w);
+          }
+        }
+        fence_proxy_async_smem();
+        mbar_arrive(q_full(g));
+      }
+      const int node = node0 + node_of_row;
+      const bool valid = node_of_row < p.tq && node < w.seq.n;
+      const bool live = __any_sync(0xffffffffu, valid);
+      const int len = w.seq.len;
+      // what the row sees: slots [low, len) and the nodes in kin (a tree), or slots [low, high) (a chain)
+      unsigned long long kin = 0;
+      int depth = node;
+      if (p.parents && valid) {
+        depth = 0;
+        for (int x = node;;) {
+          if (p.window == 0 || depth < p.window) kin |= 1ull << x;
+          const int up = p.parents[w.seq.row0 + x];
+          if (up >= x) record(p.status, kStatusInvalidArg);
+          if (up < 0 || up >= x) break;
+          x = up;
+          ++depth;
+        }
+      }
+      __syncwarp();
+      const int low = p.window > 0 ? len + depth - p.window + 1 : 0;
+      const int high = !valid ? 0 : p.parents ? len : len + node + 1;
+      // tiles whose scores are all seen by all rows
+      const int last = min(w.seq.n, p.parents ? kMaxNodes : node0 + p.tq) - 1;  // the deepest row, or deeper
+      const int plain_lo = p.window > 0 ? len + last - p.window + 1 : 0;
+      const int plain_hi = (p.parents ? len : len + node0 + 1) - kBK;
+      float m_ref = -INFINITY, l = 0.f;
+      for (int j = 0; j < n; ++j, ++J, ++A) {
+        const int n0 = (w.keys.tile0() + w.j0 + j) * kBK;
+        if (!__all_sync(0xffffffffu, mbar_wait(s_full(g, A & 1), (A >> 1) & 1, budget, abort_flag))) {
+          failed = true;
+          break;
+        }
+        __syncwarp();
+        tc_fence_after();
+        // Rows of V that were not loaded, or lie outside the keys, may hold anything: zero, so that P = 0
+        // meets finite values. Both slots write the same zeros, each before its own product.
+        const int v_lo = w.keys.first - n0, v_hi = w.keys.end - n0;
+        if (v_lo > 0 || v_hi < kBK) {
+          const int st = J % C::kStages;
+          if (!__all_sync(0xffffffffu, mbar_wait(full(st), (J / C::kStages) & 1, budget, abort_flag))) {
+            failed = true;
+            break;
+          }
+          const int row = r & 63;  // two threads a row, a half each
+          if (row < v_lo || row >= v_hi) {
+            const uint32_t at = smem_u32(ring + st * kStageBytes + (2 + (r >> 6)) * kKVSub) + row * 128;
+#pragma unroll
+            for (int ch = 0; ch < 8; ++ch) st_shared_u4(at + (((ch + row) & 7) << 4), 0, 0, 0, 0);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+        }
+        if (!live) {  // nobody reads these rows: whatever the score buffer holds may stand for P
+          tc_fence_before();
+          mbar_arrive(p_ready(g, A & 1));
+          continue;
+        }
+        const uint32_t s_buf = s_taddr + 64 * (A & 1);
+        float x[kBK];
+#pragma unroll
+        for (int c = 0; c < kBK; c += 16) tmem_ld16(s_buf + c, *reinterpret_cast<float(*)[16]>(&x[c]));
+        tc_wait_ld();
+        if (n0 < plain_lo || n0 > plain_hi) {
+          unsigned long long seen = bits_from(low - n0) & bits_below(high - n0);
+          if (p.parents) {
+            const int a = len - n0;  // the column of node 0
+            seen |= a >= 64 ? 0ull : a >= 0 ? kin << a : a > -64 ? kin >> -a : 0ull;
+          }
+          const uint32_t s0 = (uint32_t)seen, s1 = (uint32_t)(seen >> 32);
+#pragma unroll
+          for (int c = 0; c < 32; ++c) {
+            if (!(s0 & (1u << c))) x[c] = -INFINITY;
+            if (!(s1 & (1u << c))) x[32 + c] = -INFINITY;
+          }
+        }
+        float mx[4] = {x[0], x[1], x[2], x[3]};
+#pragma unroll
+        for (int c = 4; c < kBK; c += 2) mx[(c >> 1) & 3] = fmax3(mx[(c >> 1) & 3], x[c], x[c + 1]);
+        const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * kScaleLog2;
+        const bool need = mt > m_ref + kRescaleLog2;
+        if (__any_sync(0xffffffffu, need)) {
+          float alpha = 1.f;
+          if (need) {
+            alpha = ex2_approx(m_ref - mt);
+            m_ref = mt;
+          }
+          l *= alpha;
+          if (j > 0) {  // the products so far are to be complete, then O moves to the new reference
+            if (!__all_sync(0xffffffffu, mbar_wait(pv_done(g), (A - 1) & 1, budget, abort_flag))) {
+              failed = true;
+              break;
+            }
+            __syncwarp();
+            tc_fence_after();
+#pragma unroll 1
+            for (int c = 0; c < kD; c += 16) {
+              float ov[16];
+              tmem_ld16(o_taddr + c, ov);
+              tc_wait_ld();
+#pragma unroll
+              for (int i = 0; i < 16; ++i) ov[i] *= alpha;
+              tmem_st16(o_taddr + c, ov);
+            }
+          }
+          __syncwarp();
+        }
+        const float neg_mu = m_ref == -INFINITY ? 0.f : -m_ref;
+        const f32x2 scale2 = f2_make(kScaleLog2, kScaleLog2), mu2 = f2_make(neg_mu, neg_mu);
+        f32x2 sum2[2] = {f2_make(0.f, 0.f), f2_make(0.f, 0.f)};
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          float pw[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            float t0, t1;
+            f2_split(f2_fma(f2_make(x[32 * h + 2 * i], x[32 * h + 2 * i + 1]), scale2, mu2), t0, t1);
+            const float p0 = ex2_approx(t0), p1 = ex2_approx(t1);
+            sum2[i & 1] = f2_add(sum2[i & 1], f2_make(p0, p1));
+            pw[i] = __uint_as_float(pack_bf16x2(p0, p1));
+          }
+          tmem_st16(s_buf + 16 * h, pw);
+        }
+        tc_wait_st();
+        tc_fence_before();
+        mbar_arrive(p_ready(g, A & 1));
+        float a0, a1, b0, b1;
+        f2_split(sum2[0], a0, a1);
+        f2_split(sum2[1], b0, b1);
+        l += (a0 + a1) + (b0 + b1);
+      }
+      if (failed) break;
+      if (!__all_sync(0xffffffffu, mbar_wait(o_done(g), units & 1, budget, abort_flag))) {
+        failed = true;
+        break;
+      }
+      __syncwarp();
+      tc_fence_after();
+      if (live) {
+        const bool whole = w.whole();
+        const size_t at = (size_t)part * (NS * kBQ) + g * kBQ + r;
+        // a row sees itself at least: a sum that is NaN, or 0 where all its scores are -inf, gives NaN
+        const float inv = whole ? 1.f / l : 1.f;
+        __nv_bfloat16* const o = static_cast<__nv_bfloat16*>(p.o.ptr) + (w.seq.row0 + (valid ? node : 0)) * p.o.row +
+                                 (long long)(w.kvh * p.G + head_of_row) * p.o.head;
+        if (valid && !whole) p.ml[at] = make_float2(m_ref, l);
+#pragma unroll 1
+        for (int c = 0; c < kD; c += 16) {
+          float ov[16];
+          tmem_ld16(o_taddr + c, ov);
+          tc_wait_ld();
+          if (valid) {
+            if (whole) {
+#pragma unroll
+              for (int i = 0; i < 16; ++i) ov[i] *= inv;
+              reinterpret_cast<uint4*>(o + c)[0] = make_uint4(pack_bf16x2(ov[0], ov[1]), pack_bf16x2(ov[2], ov[3]),
+                                                              pack_bf16x2(ov[4], ov[5]), pack_bf16x2(ov[6], ov[7]));
+              reinterpret_cast<uint4*>(o + c)[1] = make_uint4(pack_bf16x2(ov[8], ov[9]), pack_bf16x2(ov[10], ov[11]),
+                                                              pack_bf16x2(ov[12], ov[13]), pack_bf16x2(ov[14], ov[15]));
+            } else {
+#pragma unroll
+              for (int i = 0; i < 16; i += 4)
+                *reinterpret_cast<float4*>(p.acc + at * kD + c + i) = make_float4(ov[i], ov[i + 1], ov[i + 2], ov[i + 3]);
+            }
+          }
+          __syncwarp();
+        }
+      }
+      tc_fence_before();
+      mbar_arrive(o_free(g));
+      ++units;
     }
-    uint2 u;
-    u.x = pack_bf16x2(o[0] / l, o[1] / l);
-    u.y = pack_bf16x2(o[2] / l, o[3] / l);
-    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.o.ptr) + (sr.lo + i) * p.o.row + h * p.o.head + 4 * lane) = u;
+    if (failed) {
+      *abort_flag = 1;
+      if (lane == 0) report_timeout(p.status, 0x52);
+    }
   }
+
+  tc_fence_before();
+  __syncthreads();
+  // Every role has stopped issuing. After an abort, copies and MMAs that nobody waited for may still be in
+  // flight: they complete before TMEM is freed and the CTA exits. Every thread reads the same flag.
+  if (*abort_flag) {
+    volatile int never = 0;
+    if (warp == 0 && lane == 0) {
+      for (int s = 0; s < C::kStages; ++s)
+        if (issued & (1u << s)) mbar_wait(full(s), (parity >> s) & 1, kDrainNs, &never);
+    } else if (warp >= 1 && warp <= NS && lane == 0 && mma_issued) {
+      tc_commit(drain(warp - 1));
+      mbar_wait(drain(warp - 1), 0, kDrainNs, &never);
+    }
+    tc_fence_before();
+    __syncthreads();
+  }
+  if (warp == 1) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+// ------------------------------------------------------------------ joining partial results
+
+// Block (c - 1, y): the unit that stretch c continues, if stretch c - 1 began it: the parts of stretches
+// c - 1 .. e, in that order, a warp a row.
+constexpr int kJoinThreads = 256;
+constexpr int kJoinBlocks = 8;
+__global__ void __launch_bounds__(kJoinThreads) attn_paged_join_kernel(const __grid_constant__ AttnParams p) {
+  __shared__ Stretch sh;
+  const int lane = threadIdx.x & 31, c = blockIdx.x + 1;
+  if (threadIdx.x < 32) {
+    const Stretch s = stretch_of(p, c, lane);
+    if (lane == 0) sh = s;
+  }
+  __syncthreads();
+  const Stretch s = sh;
+  const Walk w(p, s);
+  pdl_launch_dependents();
+  pdl_wait();  // for the partial results; the lists are there (see the other kernel)
+  if (!w.on() || w.j0 == 0 || w.j0 > s.per) return;  // no unit goes over, or an earlier block joins it
+  const long long start = s.lo - w.j0;
+  const int e = (int)((start + w.tiles - 1) / s.per);
+  const int slot_rows = p.tq * p.G, most = p.slots * slot_rows;
+  const size_t part_rows = (size_t)p.slots * kBQ;
+  const int first = w.j0 == s.per ? 2 * (c - 1) : 2 * (c - 1) + 1;
+  for (int i = blockIdx.y * (kJoinThreads / 32) + (threadIdx.x >> 5); i < most; i += gridDim.y * (kJoinThreads / 32)) {
+    const int g = i / slot_rows, r = i - g * slot_rows;
+    const int nd = r / p.G, node = w.node0(p, g) + nd;
+    if (node >= w.seq.n) break;  // rows further on are further nodes
+    const size_t row = (size_t)g * kBQ + r;
+    auto at = [&](int k) { return (size_t)(k == c - 1 ? first : 2 * k) * part_rows + row; };
+    float m = -INFINITY;
+    for (int k0 = c - 1; k0 <= e; k0 += 32) {
+      const int k = k0 + lane;
+      m = fmaxf(m, warp_max(k <= e ? p.ml[at(k)].x : -INFINITY));
+    }
+    float l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+    for (int k = c - 1; k <= e; ++k) {
+      const float2 ml = p.ml[at(k)];
+      const float4 a = *reinterpret_cast<const float4*>(p.acc + at(k) * kD + 4 * lane);
+      // a part that saw no key has weight 0
+      const float wt = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - m);
+      l = fmaf(wt, ml.y, l);
+      o[0] = fmaf(wt, a.x, o[0]);
+      o[1] = fmaf(wt, a.y, o[1]);
+      o[2] = fmaf(wt, a.z, o[2]);
+      o[3] = fmaf(wt, a.w, o[3]);
+    }
+    const float inv = 1.f / l;
+    __nv_bfloat16* const to = static_cast<__nv_bfloat16*>(p.o.ptr) + (w.seq.row0 + node) * p.o.row +
+                              (long long)(w.kvh * p.G + r - nd * p.G) * p.o.head + 4 * lane;
+    *reinterpret_cast<uint2*>(to) = make_uint2(pack_bf16x2(o[0] * inv, o[1] * inv), pack_bf16x2(o[2] * inv, o[3] * inv));
+  }
+}
+
+// How a call is cut, from what the host knows of it.
+struct Plan {
+  int slots, grid, min_tiles;
+};
+Plan plan_of(int rows, int B, int H, int Hkv, int num_sms) {
+  Plan pl;
+  const long long per_seq = (long long)rows * (H / Hkv);  // matrix rows of all sequences of a KV head
+  pl.slots = per_seq > 96ll * B ? 2 : 1;
+  pl.grid = num_sms;
+  // a part costs its rows' outputs in fp32, written and read: 1 KB a row against 32 KB a tile
+  const long long avg = std::min<long long>(per_seq / B, pl.slots * kBQ);
+  pl.min_tiles = (int)std::max<long long>(1, avg / 32);
+  return pl;
 }
 
 }  // namespace
 
-size_t attn_paged_ws_bytes(int, int, int, int, int) { return 0; }
+size_t attn_paged_ws_bytes(int rows, int B, int H, int Hkv, int num_sms) {
+  if (rows <= 0 || B <= 0) return 0;
+  const Plan pl = plan_of(rows, B, H, Hkv, num_sms);
+  return (size_t)2 * pl.grid * pl.slots * kBQ * (sizeof(float2) + kD * sizeof(float));
+}
 
 cudaError_t launch_attn_paged(const HeadRows& q, const PagedCache& c, const HeadRows& o, int rows, const int* cu,
-                              const int* parents, int B, int H, int Hkv, int window, void*, int num_sms,
-                              DevStatus* st, unsigned long long, cudaStream_t s, const char** why) {
+                              const int* parents, int B, int H, int Hkv, int window, void* ws, int num_sms,
+                              DevStatus* st, unsigned long long wait_ns, cudaStream_t s, const char** why) {
   if (rows <= 0 || B <= 0) return cudaSuccess;
-  if (B > 65535) {
-    *why = "paged attention: at most 65535 sequences";
+  const Plan pl = plan_of(rows, B, H, Hkv, num_sms);
+  AttnParams p;
+  memset(static_cast<void*>(&p), 0, sizeof(p));
+  const int box = std::min(1 << c.page_shift, kBK);
+  const int cache_rows = (c.n_pages * Hkv) << c.page_shift;  // checked by the caller
+  if (!make_tma_2d_16b(&p.tk, c.k, cache_rows, kD, box, false) || !make_tma_2d_16b(&p.tv, c.v, cache_rows, kD, box, false)) {
+    *why = "cuTensorMapEncodeTiled failed for the cache";
     return cudaErrorInvalidValue;
   }
-  PagedAttnParams p{q, o, c, cu, parents, rows, B, H, Hkv, window, st};
-  return launch_pdl(attn_paged_kernel, dim3(32, (unsigned)B), kThreads, 0, s, p);
+  p.q = q;
+  p.o = o;
+  p.c = c;
+  p.cu = cu;
+  p.parents = parents;
+  p.rows = rows;
+  p.B = B;
+  p.H = H;
+  p.Hkv = Hkv;
+  p.G = H / Hkv;
+  p.window = window > 0 ? window : 0;
+  p.tq = kBQ / p.G;
+  p.slots = pl.slots;
+  while ((1 << p.box_shift) < box) ++p.box_shift;
+  p.grid = pl.grid;
+  p.min_tiles = pl.min_tiles;
+  p.acc = static_cast<float*>(ws);
+  p.ml = reinterpret_cast<float2*>(p.acc + (size_t)2 * pl.grid * pl.slots * kBQ * kD);
+  p.status = st;
+  p.wait_ns = wait_ns;
+  const bool two = pl.slots == 2;
+  const auto kernel = two ? attn_paged_kernel<2> : attn_paged_kernel<1>;
+  const int smem = two ? Cfg<2>::kSmem : Cfg<1>::kSmem, threads = two ? Cfg<2>::kThreads : Cfg<1>::kThreads;
+  static std::atomic<unsigned long long> configured[2];
+  cudaError_t e = set_smem_limit_once(reinterpret_cast<const void*>(kernel), smem, configured[two]);
+  if (e == cudaSuccess) e = launch_pdl(kernel, pl.grid, threads, smem, s, p);
+  if (e != cudaSuccess || pl.grid == 1) return e;
+  return launch_pdl(attn_paged_join_kernel, dim3(pl.grid - 1, kJoinBlocks), kJoinThreads, 0, s, p);
 }
 
 }  // namespace blk
