@@ -42,28 +42,24 @@ constexpr int kKVSub = kBK * 128;      // one 64-channel half of a K or V tile
 constexpr int kStageBytes = 4 * kKVSub;
 constexpr float kRescaleLog2 = 8.0f;
 constexpr float kScaleLog2 = 1.4426950408889634f * 0.08838834764831845f;  // log2(e) / sqrt(128)
+constexpr int kNoBox = -2;             // a box that no row needs; entries below -1 are read as -1
 constexpr unsigned long long kDrainNs = 2000000000ULL;
-template <int NS>
-struct Cfg {
-  static constexpr int kStages = NS == 1 ? 6 : 5;
-  static constexpr int kThreads = 128 + 128 * NS;
-  static constexpr int kBars = 2 * kStages + 9 * NS;
-  static constexpr int kSmem = 1024 + NS * kQBytes + kStages * kStageBytes + kBars * 8 + 64;
-  static_assert(kSmem <= 227 * 1024, "shared memory");
-};
-
 struct AttnParams {
   CUtensorMap tk, tv;  // [n_pages * Hkv * page_size, 128] bf16, boxes of 64 channels x `box` rows
-  HeadRows q, o;
+  CUtensorMap tq_map;  // the query rows: boxes of 64 channels x G heads x tq rows
+  HeadRows o;
   PagedCache c;
   const int *cu, *parents;
   int rows, B, H, Hkv, G, window;
+  int q_bytes;    // of a slot's queries
   int tq;         // rows of a sequence in a slot: 128 / G
   int slots;      // slots of a CTA
   int box_shift;  // log2 of a box's rows: those of a page, at most 64
   int grid, min_tiles;
-  float2* ml;     // partial results [2 grid][128 slots]: (reference, sum)
-  float* acc;     // ... [2 grid][128 slots][128]
+  int unit_cost;  // what a unit counts for on the line besides its tiles, before them
+  float2* ml;     // partial results [2 grid][slots][128]: (reference, sum)
+  float* acc;     // ... [2 grid][slots][32][128][4]: four channels of each row side by side
+  int o_wide;     // the outputs' rows start on 32-byte boundaries
   DevStatus* status;
   unsigned long long wait_ns;
 };
@@ -77,6 +73,12 @@ __device__ __forceinline__ float fmax3(float a, float b, float c) {
   float d;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
+}
+// 32 bytes in one store (a 32-byte boundary)
+__device__ __forceinline__ void st_global_32(void* p, const uint4& a, const uint4& b) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(a.x), "r"(a.y), "r"(a.z),
+               "r"(a.w), "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w)
+               : "memory");
 }
 // D[tmem] (+)= A[tmem] * B[smem desc], bf16
 __device__ __forceinline__ void tc_mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
@@ -114,9 +116,10 @@ __device__ __forceinline__ Keys keys_of(const AttnParams& p, const Seq& s, int t
   const int i1 = p.parents ? s.n : min(s.n, i0 + p.tq * p.slots);
   return {p.window > 0 ? max(0, s.len + i0 - p.window + 1) : 0, s.len + i1};
 }
-__device__ __forceinline__ int head_tiles(const AttnParams& p, const Seq& s) {  // of all units of a KV head
-  int n = 0;
-  for (int t = 0; t < units_of(p, s); ++t) n += keys_of(p, s, t).tiles();
+__device__ __forceinline__ int head_cost(const AttnParams& p, const Seq& s) {  // of all units of a KV head
+  if (s.n == 0) return 0;
+  int n = keys_of(p, s, 0).tiles() + p.unit_cost;
+  for (int t = 1; t * p.tq * p.slots < s.n; ++t) n += keys_of(p, s, t).tiles() + p.unit_cost;
   return n;
 }
 
@@ -126,9 +129,23 @@ struct Stretch {
   int b, per;
 };
 // By one warp. Stretch number `c`; an empty one (lo >= hi) if the line ends before.
+__device__ __forceinline__ long long scan(long long n, int lane) {
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long x = __shfl_up_sync(0xffffffffu, n, o);
+    if (lane >= o) n += x;
+  }
+  return n;
+}
 __device__ __forceinline__ Stretch stretch_of(const AttnParams& p, int c, int lane) {
-  long long total = 0;
-  for (int b = lane; b < p.B; b += 32) total += (long long)p.Hkv * head_tiles(p, seq_of(p, b));
+  auto cost_of = [&](int b) { return b < p.B ? (long long)p.Hkv * head_cost(p, seq_of(p, b)) : 0; };
+  constexpr int kHeld = 4;  // 32 sequences each, looked up once
+  long long held[kHeld], total = 0;
+#pragma unroll
+  for (int i = 0; i < kHeld; ++i) held[i] = cost_of(32 * i + lane);
+#pragma unroll
+  for (int i = 0; i < kHeld; ++i) total += held[i];
+  for (int b = lane + 32 * kHeld; b < p.B; b += 32) total += cost_of(b);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
   Stretch s;
@@ -139,62 +156,65 @@ __device__ __forceinline__ Stretch stretch_of(const AttnParams& p, int c, int la
   s.base = 0;
   s.b = 0;
   if (s.lo >= s.hi) return s;
-  for (int b0 = 0; b0 < p.B; b0 += 32) {
-    const long long n = b0 + lane < p.B ? (long long)p.Hkv * head_tiles(p, seq_of(p, b0 + lane)) : 0;
-    long long upto = n;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long x = __shfl_up_sync(0xffffffffu, upto, o);
-      if (lane >= o) upto += x;
-    }
+  bool found = false;
+  auto look = [&](int b0, long long n) {  // whether the stretch begins in these 32 sequences
+    const long long upto = scan(n, lane);
     const unsigned past = __ballot_sync(0xffffffffu, s.base + upto > s.lo);
-    if (past) {
-      const int at = __ffs(past) - 1;
-      s.b = b0 + at;
-      s.base += __shfl_sync(0xffffffffu, upto - n, at);
-      break;
-    }
-    s.base += __shfl_sync(0xffffffffu, upto, 31);
-  }
+    const int at = past ? __ffs(past) - 1 : 31;
+    s.b = b0 + at;
+    s.base += __shfl_sync(0xffffffffu, past ? upto - n : upto, at);
+    found = past != 0;
+  };
+#pragma unroll
+  for (int i = 0; i < kHeld; ++i)
+    if (!found) look(32 * i, held[i]);
+  for (int b0 = 32 * kHeld; !found && b0 < p.B; b0 += 32) look(b0, cost_of(b0 + lane));
+  if (!found) s.hi = s.lo;  // lengths that change meanwhile
   return s;
 }
 
-// Walks the units of a stretch: unit t of KV head kvh of sequence b, its tiles [j0, j1) of `tiles`.
+// Walks the units of a stretch: unit t of KV head kvh of sequence b, its tiles [j0, j1) of `tiles` (none where
+// the stretch ends in a unit's own cost).
 struct Walk {
   Seq seq;
   Keys keys;
   int b, kvh, t, tiles, j0, j1;
+  int at;  // where in the unit, costs counted, the stretch is
   long long left;
+  Walk() = default;
   __device__ __forceinline__ void unit(const AttnParams& p) {
     keys = keys_of(p, seq, t);
     tiles = keys.tiles();
   }
+  __device__ __forceinline__ void part(const AttnParams& p) {
+    j0 = max(0, at - p.unit_cost);
+    j1 = (int)min((long long)tiles, max(0ll, at + left - p.unit_cost));
+  }
   __device__ __forceinline__ Walk(const AttnParams& p, const Stretch& s) {
     left = s.hi - s.lo;
-    j0 = j1 = tiles = kvh = t = 0;
+    j0 = j1 = tiles = kvh = t = at = 0;
     b = s.b;
     if (left <= 0) return;
     seq = seq_of(p, b);
-    long long at = s.lo - s.base;
-    const int per_head = head_tiles(p, seq);
+    const long long from = s.lo - s.base;
+    const int per_head = head_cost(p, seq);
     if (per_head <= 0) {  // lengths that change meanwhile: no walk leaves the lists
       left = 0;
       return;
     }
-    kvh = (int)(at / per_head);
-    int rest = (int)(at - (long long)kvh * per_head);
+    kvh = (int)(from / per_head);
+    at = (int)(from - (long long)kvh * per_head);
     unit(p);
-    while (rest >= tiles) {  // rest < per_head: it ends within the units
-      rest -= tiles;
+    while (at >= tiles + p.unit_cost) {  // at < per_head: it ends within the units
+      at -= tiles + p.unit_cost;
       ++t;
       unit(p);
     }
-    j0 = rest;
-    j1 = (int)min((long long)tiles, j0 + left);
+    part(p);
   }
   __device__ __forceinline__ bool on() const { return left > 0; }
   __device__ __forceinline__ void next(const AttnParams& p) {
-    left -= j1 - j0;
+    left -= tiles + p.unit_cost - at;
     if (left <= 0) return;
     if (++t >= units_of(p, seq)) {
       t = 0;
@@ -209,12 +229,13 @@ struct Walk {
         } while (seq.n == 0);
       }
     }
+    at = 0;
     unit(p);
-    j0 = 0;
-    j1 = (int)min((long long)tiles, left);
+    part(p);
   }
   __device__ __forceinline__ bool whole() const { return j0 == 0 && j1 == tiles; }
-  // the first row of a slot
+  // whether a slot has rows to work on, and its first one
+  __device__ __forceinline__ bool has(const AttnParams& p, int g) const { return j1 > j0 && node0(p, g) < seq.n; }
   __device__ __forceinline__ int node0(const AttnParams& p, int g) const { return (t * p.slots + g) * p.tq; }
 };
 
@@ -226,6 +247,15 @@ __device__ __forceinline__ unsigned long long bits_below(int hi) { return ~bits_
 // ------------------------------------------------------------------ the kernel
 
 template <int NS>
+struct Cfg {
+  static constexpr int kStages = NS == 1 ? 6 : 5;
+  static constexpr int kThreads = 128 + 128 * NS;
+  static constexpr int kBars = 2 * kStages + 10 * NS;
+  static constexpr int kSmem = 1024 + NS * kQBytes + kStages * kStageBytes + kBars * 8 + 8 + sizeof(Walk);
+  static_assert(kSmem <= 227 * 1024, "shared memory");
+};
+
+template <int NS>
 __global__ void __launch_bounds__(Cfg<NS>::kThreads, 1) attn_paged_kernel(const __grid_constant__ AttnParams p) {
   typedef Cfg<NS> C;
   extern __shared__ uint8_t smem_raw[];
@@ -235,12 +265,11 @@ __global__ void __launch_bounds__(Cfg<NS>::kThreads, 1) attn_paged_kernel(const 
   uint64_t* const bars = reinterpret_cast<uint64_t*>(ring + C::kStages * kStageBytes);
   uint32_t* const tmem_holder = reinterpret_cast<uint32_t*>(bars + C::kBars);
   volatile int* const abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
-  Stretch* const stretch = reinterpret_cast<Stretch*>(tmem_holder + 2);
-  static_assert(sizeof(Stretch) <= 48, "room behind the barriers");
+  Walk* const begin = reinterpret_cast<Walk*>(tmem_holder + 2);  // the CTA's first unit
   auto bar = [&](int i) { return smem_u32(&bars[i]); };
   auto full = [&](int s) { return bar(s); };
   auto empty = [&](int s) { return bar(C::kStages + s); };
-  auto mine = [&](int g, int i) { return bar(2 * C::kStages + 9 * g + i); };
+  auto mine = [&](int g, int i) { return bar(2 * C::kStages + 10 * g + i); };
   auto q_full = [&](int g) { return mine(g, 0); };
   auto s_full = [&](int g, int buf) { return mine(g, 1 + buf); };
   auto p_ready = [&](int g, int buf) { return mine(g, 3 + buf); };
@@ -248,6 +277,7 @@ __global__ void __launch_bounds__(Cfg<NS>::kThreads, 1) attn_paged_kernel(const 
   auto o_done = [&](int g) { return mine(g, 6); };
   auto o_free = [&](int g) { return mine(g, 7); };
   auto drain = [&](int g) { return mine(g, 8); };
+  auto q_free = [&](int g) { return mine(g, 9); };
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const unsigned long long budget = p.wait_ns;
   constexpr int kTmemCols = 256 * NS;  // of slot g: S and P in 256 g and 256 g + 64, O from 256 g + 128
@@ -258,7 +288,8 @@ __global__ void __launch_bounds__(Cfg<NS>::kThreads, 1) attn_paged_kernel(const 
       mbar_init(empty(s), NS);
     }
     for (int g = 0; g < NS; ++g) {
-      mbar_init(q_full(g), 128);
+      mbar_init(q_full(g), 1);
+      mbar_init(q_free(g), 1);
       for (int i = 0; i < 2; ++i) {
         mbar_init(s_full(g, i), 1);
         mbar_init(p_ready(g, i), 128);
@@ -272,6 +303,7 @@ __global__ void __launch_bounds__(Cfg<NS>::kThreads, 1) attn_paged_kernel(const 
     fence_mbar_init();
     tma_prefetch_desc(&p.tk);
     tma_prefetch_desc(&p.tv);
+    tma_prefetch_desc(&p.tq_map);
   }
   if (warp == 1) {
     tmem_alloc(smem_u32(tmem_holder), kTmemCols);
@@ -282,10 +314,10 @@ __global__ void __launch_bounds__(Cfg<NS>::kThreads, 1) attn_paged_kernel(const 
   // while this one runs
   pdl_launch_dependents();
   if (warp == 0) {
-    const Stretch s = stretch_of(p, blockIdx.x, lane);
-    if (lane == 0) *stretch = s;
+    const Walk w(p, stretch_of(p, blockIdx.x, lane));
+    if (lane == 0) *begin = w;
   }
-  if (warp == 3 && blockIdx.x == 0) {  // what the lists say that they should not
+  if (warp == 2 && blockIdx.x == 0) {  // what the lists say that they should not
     bool bad = false, over = false;
     for (int b = lane; b < p.B; b += 32) {
       const SeqRows r = seq_rows(p.cu, b, p.rows);
@@ -303,7 +335,7 @@ __global__ void __launch_bounds__(Cfg<NS>::kThreads, 1) attn_paged_kernel(const 
   const uint32_t tmem = *tmem_holder;
   // What is in flight, for the drain after an abort: the stages issued (with the parity of their last
   // phase) and whether any MMA was.
-  uint32_t issued = 0, parity = 0;
+  uint32_t issued = 0, parity = 0, q_issued = 0, q_parity = 0;
   bool mma_issued = false;
 
   if (warp == 0) {
@@ -312,21 +344,14 @@ __global__ void __launch_bounds__(Cfg<NS>::kThreads, 1) attn_paged_kernel(const 
     const int page_shift = p.c.page_shift, boxes = kBK >> p.box_shift;
     int J = 0;
     bool failed = false;
-    for (Walk w(p, *stretch); w.on() && !failed; w.next(p)) {
+    for (Walk w = *begin; w.on() && !failed; w.next(p)) {
       const int* const pages = p.c.pages + (size_t)w.b * p.c.max_pages;
       const int box0 = (w.keys.tile0() + w.j0) * boxes;  // the first box of the part
       const int n_boxes = (w.j1 - w.j0) * boxes;
-      auto look_up = [&](int i) {  // the page of the part's box i + lane, or -1 where nobody needs it
+      auto look_up = [&](int i) {  // the page of the part's box i + lane
         const int slot = (box0 + i + lane) << p.box_shift;
-        int page = -1;
-        if (i + lane < n_boxes && slot < w.keys.end && slot + (1 << p.box_shift) > w.keys.first) {
-          page = pages[slot >> page_shift];
-          if (page < 0 || page >= p.c.n_pages) {
-            record(p.status, kStatusInvalidArg);
-            page = 0;
-          }
-        }
-        return page;
+        const bool in = i + lane < n_boxes && slot < w.keys.end && slot + (1 << p.box_shift) > w.keys.first;
+        return in ? max(pages[slot >> page_shift], -1) : kNoBox;
       };
       int page = look_up(0), ahead = look_up(32);
       for (int i = 0; i < n_boxes; i += boxes, ++J) {
@@ -341,8 +366,12 @@ __global__ void __launch_bounds__(Cfg<NS>::kThreads, 1) attn_paged_kernel(const 
           break;
         }
         const int box = lane >> 2, part = lane & 3;
-        const int its = __shfl_sync(0xffffffffu, page, (i & 31) + (box < boxes ? box : 0));
-        const bool loads = box < boxes && its >= 0;
+        int its = __shfl_sync(0xffffffffu, page, (i & 31) + (box < boxes ? box : 0));
+        const bool loads = box < boxes && its != kNoBox;
+        if (loads && (its < 0 || its >= p.c.n_pages)) {
+          record(p.status, kStatusInvalidArg);
+          its = 0;
+        }
         const int n = __popc(__ballot_sync(0xffffffffu, loads)) >> 2;
         if (lane == 0) mbar_arrive_expect_tx(full(s), (uint32_t)(n * 512) << p.box_shift);
         __syncwarp();
@@ -373,9 +402,9 @@ __global__ void __launch_bounds__(Cfg<NS>::kThreads, 1) attn_paged_kernel(const 
       const uint32_t s_tmem = tmem + 256 * g, o_tmem = tmem + 256 * g + 128;
       int J = 0, A = 0, units = 0;  // tiles of the CTA and of this slot, and its units
       bool failed = false;
-      for (Walk w(p, *stretch); w.on() && !failed; w.next(p)) {
+      for (Walk w = *begin; w.on() && !failed; w.next(p)) {
         const int n = w.j1 - w.j0;
-        if (w.node0(p, g) >= w.seq.n) {  // nothing for this slot: the stages go back
+        if (!w.has(p, g)) {  // nothing for this slot: the stages go back
           for (int j = 0; j < n && !failed; ++j, ++J) {
             if (!mbar_wait(full(J % C::kStages), (J / C::kStages) & 1, budget, abort_flag)) failed = true;
             else mbar_arrive(empty(J % C::kStages));
@@ -406,6 +435,7 @@ __global__ void __launch_bounds__(Cfg<NS>::kThreads, 1) attn_paged_kernel(const 
             failed = true;
             break;
           }
+          if (j + 1 == max(n - 1, 1)) tc_commit(q_free(g));  // that was the unit's last score product
           if ((j == 0 && units > 0 && !mbar_wait(o_free(g), (units - 1) & 1, budget, abort_flag)) ||
               !mbar_wait(p_ready(g, A & 1), (A >> 1) & 1, budget, abort_flag)) {
             failed = true;
@@ -430,6 +460,35 @@ __global__ void __launch_bounds__(Cfg<NS>::kThreads, 1) attn_paged_kernel(const 
         report_timeout(p.status, 0x51);
       }
     }
+  } else if (warp == 3) {
+    // ---------------- queries, once the last unit's scores are done
+    if (lane == 0) {
+      int units[NS] = {};
+      bool failed = false;
+      for (Walk w = *begin; w.on() && !failed; w.next(p)) {
+#pragma unroll
+        for (int g = 0; g < NS; ++g) {
+          const int node0 = w.node0(p, g);
+          if (failed || !w.has(p, g)) continue;
+          if (units[g] > 0 && !mbar_wait(q_free(g), (units[g] - 1) & 1, budget, abort_flag)) {
+            failed = true;
+            continue;
+          }
+          // rows past the sequence's are others' or zeros: their scores are nobody's
+          mbar_arrive_expect_tx(q_full(g), (uint32_t)p.q_bytes);
+#pragma unroll
+          for (int half = 0; half < 2; ++half)
+            tma_load_3d(smem_u32(sQ + g * kQBytes + half * kQSub), &p.tq_map, 64 * half, w.kvh * p.G, w.seq.row0 + node0, q_full(g));
+          q_issued |= 1u << g;
+          q_parity = (q_parity & ~(1u << g)) | ((uint32_t)(units[g] & 1) << g);
+          ++units[g];
+        }
+      }
+      if (failed) {
+        *abort_flag = 1;
+        report_timeout(p.status, 0x53);
+      }
+    }
   } else if (warp >= 4) {
     // ---------------- a slot's rows, one a thread
     const int g = (warp - 4) >> 2, quarter = warp & 3;
@@ -439,37 +498,11 @@ __global__ void __launch_bounds__(Cfg<NS>::kThreads, 1) attn_paged_kernel(const 
     const int node_of_row = r / p.G, head_of_row = r - node_of_row * p.G;
     int J = 0, A = 0, units = 0, part = 2 * blockIdx.x;
     bool failed = false;
-    for (Walk w(p, *stretch); w.on() && !failed; w.next(p), part = 2 * blockIdx.x + 1) {
+    for (Walk w = *begin; w.on() && !failed; w.next(p), part = 2 * blockIdx.x + 1) {
       const int n = w.j1 - w.j0, node0 = w.node0(p, g);
-      if (node0 >= w.seq.n) {
+      if (!w.has(p, g)) {
         J += n;
         continue;
-      }
-      // queries: 16 lanes a row, four rounds of eight rows' loads
-      {
-        const int chunk = lane & 15;
-        const uint32_t dst = smem_u32(sQ + g * kQBytes) + (chunk >> 3) * kQSub;
-#pragma unroll
-        for (int i0 = 0; i0 < 16; i0 += 8) {
-          uint4 u[8];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int row = quarter * 32 + 2 * (i0 + i) + (lane >> 4);
-            const int nd = row / p.G, hd = row - nd * p.G;
-            u[i] = make_uint4(0, 0, 0, 0);
-            if (nd < p.tq && node0 + nd < w.seq.n)
-              u[i] = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q.ptr) +
-                                                     (w.seq.row0 + node0 + nd) * p.q.row +
-                                                     (long long)(w.kvh * p.G + hd) * p.q.head + 8 * chunk);
-          }
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int row = quarter * 32 + 2 * (i0 + i) + (lane >> 4);
-            st_shared_u4(dst + row * 128 + (((chunk & 7) ^ (row & 7)) << 4), u[i].x, u[i].y, u[i].z, u[i].w);
-          }
-        }
-        fence_proxy_async_smem();
-        mbar_arrive(q_full(g));
       }
       const int node = node0 + node_of_row;
       const bool valid = node_of_row < p.tq && node < w.seq.n;
@@ -610,12 +643,12 @@ __global__ void __launch_bounds__(Cfg<NS>::kThreads, 1) attn_paged_kernel(const 
       tc_fence_after();
       if (live) {
         const bool whole = w.whole();
-        const size_t at = (size_t)part * (NS * kBQ) + g * kBQ + r;
+        float* const acc = p.acc + ((size_t)part * NS + g) * kBQ * kD + 4 * r;
         // a row sees itself at least: a sum that is NaN, or 0 where all its scores are -inf, gives NaN
         const float inv = whole ? 1.f / l : 1.f;
         __nv_bfloat16* const o = static_cast<__nv_bfloat16*>(p.o.ptr) + (w.seq.row0 + (valid ? node : 0)) * p.o.row +
                                  (long long)(w.kvh * p.G + head_of_row) * p.o.head;
-        if (valid && !whole) p.ml[at] = make_float2(m_ref, l);
+        if (valid && !whole) p.ml[((size_t)part * NS + g) * kBQ + r] = make_float2(m_ref, l);
 #pragma unroll 1
         for (int c = 0; c < kD; c += 16) {
           float ov[16];
@@ -625,14 +658,20 @@ __global__ void __launch_bounds__(Cfg<NS>::kThreads, 1) attn_paged_kernel(const 
             if (whole) {
 #pragma unroll
               for (int i = 0; i < 16; ++i) ov[i] *= inv;
-              reinterpret_cast<uint4*>(o + c)[0] = make_uint4(pack_bf16x2(ov[0], ov[1]), pack_bf16x2(ov[2], ov[3]),
-                                                              pack_bf16x2(ov[4], ov[5]), pack_bf16x2(ov[6], ov[7]));
-              reinterpret_cast<uint4*>(o + c)[1] = make_uint4(pack_bf16x2(ov[8], ov[9]), pack_bf16x2(ov[10], ov[11]),
-                                                              pack_bf16x2(ov[12], ov[13]), pack_bf16x2(ov[14], ov[15]));
+              const uint4 a = make_uint4(pack_bf16x2(ov[0], ov[1]), pack_bf16x2(ov[2], ov[3]), pack_bf16x2(ov[4], ov[5]),
+                                         pack_bf16x2(ov[6], ov[7]));
+              const uint4 b = make_uint4(pack_bf16x2(ov[8], ov[9]), pack_bf16x2(ov[10], ov[11]),
+                                         pack_bf16x2(ov[12], ov[13]), pack_bf16x2(ov[14], ov[15]));
+              if (p.o_wide) {
+                st_global_32(o + c, a, b);
+              } else {
+                reinterpret_cast<uint4*>(o + c)[0] = a;
+                reinterpret_cast<uint4*>(o + c)[1] = b;
+              }
             } else {
 #pragma unroll
               for (int i = 0; i < 16; i += 4)
-                *reinterpret_cast<float4*>(p.acc + at * kD + c + i) = make_float4(ov[i], ov[i + 1], ov[i + 2], ov[i + 3]);
+                *reinterpret_cast<float4*>(acc + (c + i) * kBQ) = make_float4(ov[i], ov[i + 1], ov[i + 2], ov[i + 3]);
             }
           }
           __syncwarp();
@@ -657,6 +696,9 @@ __global__ void __launch_bounds__(Cfg<NS>::kThreads, 1) attn_paged_kernel(const 
     if (warp == 0 && lane == 0) {
       for (int s = 0; s < C::kStages; ++s)
         if (issued & (1u << s)) mbar_wait(full(s), (parity >> s) & 1, kDrainNs, &never);
+    } else if (warp == 3 && lane == 0) {
+      for (int g = 0; g < NS; ++g)
+        if (q_issued & (1u << g)) mbar_wait(q_full(g), (q_parity >> g) & 1, kDrainNs, &never);
     } else if (warp >= 1 && warp <= NS && lane == 0 && mma_issued) {
       tc_commit(drain(warp - 1));
       mbar_wait(drain(warp - 1), 0, kDrainNs, &never);
@@ -673,10 +715,10 @@ __global__ void __launch_bounds__(Cfg<NS>::kThreads, 1) attn_paged_kernel(const 
 
 // ------------------------------------------------------------------ joining partial results
 
-// Block (c - 1, y): the unit that stretch c continues, if stretch c - 1 began it: the parts of stretches
-// c - 1 .. e, in that order, a warp a row.
+// Block (c - 1, y): the unit that stretch c goes on with, if stretch c - 1 has its first tile: the parts of
+// stretches c - 1 .. e, in that order.
 constexpr int kJoinThreads = 256;
-constexpr int kJoinBlocks = 8;
+template <int PARTS>
 __global__ void __launch_bounds__(kJoinThreads) attn_paged_join_kernel(const __grid_constant__ AttnParams p) {
   __shared__ Stretch sh;
   const int lane = threadIdx.x & 31, c = blockIdx.x + 1;
@@ -689,46 +731,59 @@ __global__ void __launch_bounds__(kJoinThreads) attn_paged_join_kernel(const __g
   const Walk w(p, s);
   pdl_launch_dependents();
   pdl_wait();  // for the partial results; the lists are there (see the other kernel)
-  if (!w.on() || w.j0 == 0 || w.j0 > s.per) return;  // no unit goes over, or an earlier block joins it
-  const long long start = s.lo - w.j0;
-  const int e = (int)((start + w.tiles - 1) / s.per);
-  const int slot_rows = p.tq * p.G, most = p.slots * slot_rows;
-  const size_t part_rows = (size_t)p.slots * kBQ;
-  const int first = w.j0 == s.per ? 2 * (c - 1) : 2 * (c - 1) + 1;
-  for (int i = blockIdx.y * (kJoinThreads / 32) + (threadIdx.x >> 5); i < most; i += gridDim.y * (kJoinThreads / 32)) {
-    const int g = i / slot_rows, r = i - g * slot_rows;
-    const int nd = r / p.G, node = w.node0(p, g) + nd;
-    if (node >= w.seq.n) break;  // rows further on are further nodes
-    const size_t row = (size_t)g * kBQ + r;
-    auto at = [&](int k) { return (size_t)(k == c - 1 ? first : 2 * k) * part_rows + row; };
-    float m = -INFINITY;
-    for (int k0 = c - 1; k0 <= e; k0 += 32) {
-      const int k = k0 + lane;
-      m = fmaxf(m, warp_max(k <= e ? p.ml[at(k)].x : -INFINITY));
-    }
-    float l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
-    for (int k = c - 1; k <= e; ++k) {
-      const float2 ml = p.ml[at(k)];
-      const float4 a = *reinterpret_cast<const float4*>(p.acc + at(k) * kD + 4 * lane);
-      // a part that saw no key has weight 0
-      const float wt = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - m);
-      l = fmaf(wt, ml.y, l);
-      o[0] = fmaf(wt, a.x, o[0]);
-      o[1] = fmaf(wt, a.y, o[1]);
-      o[2] = fmaf(wt, a.z, o[2]);
-      o[3] = fmaf(wt, a.w, o[3]);
+  const long long tile0 = s.lo - w.at + p.unit_cost;  // the unit's first tile on the line
+  if (!w.on() || w.j0 == 0 || tile0 / s.per != c - 1) return;  // no unit goes over, or an earlier block joins it
+  const int e = (int)((tile0 + w.tiles - 1) / s.per);
+  // a thread has four channels of a row, a warp 32 rows; PARTS parts are under way at a time
+  const int first = s.lo - w.at <= (long long)(c - 1) * s.per ? 2 * (c - 1) : 2 * (c - 1) + 1;  // that stretch's first unit?
+  const int warp = blockIdx.y * (kJoinThreads / 32) + (threadIdx.x >> 5), warps = gridDim.y * (kJoinThreads / 32);
+  for (int i = warp; i < p.slots * (kBQ / 32) * (kD / 4); i += warps) {
+    const int ch = i % (kD / 4), quarter = i / (kD / 4) % (kBQ / 32), g = i / (kD / 4) / (kBQ / 32);
+    const int r = quarter * 32 + lane, nd = r / p.G, node = w.node0(p, g) + nd;
+    if (nd >= p.tq || node >= w.seq.n) continue;
+    float m = -INFINITY, l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int k0 = c - 1; k0 <= e; k0 += PARTS) {
+      float2 ml[PARTS];
+      float4 a[PARTS];
+#pragma unroll
+      for (int j = 0; j < PARTS; ++j) {
+        const int k = k0 + j;
+        const size_t at = (size_t)(k == c - 1 ? first : 2 * k) * p.slots + g;
+        ml[j] = make_float2(-INFINITY, 0.f);
+        a[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (k <= e) {
+          ml[j] = p.ml[at * kBQ + r];
+          a[j] = reinterpret_cast<const float4*>(p.acc + at * kBQ * kD)[ch * kBQ + r];
+        }
+      }
+      float top = m;
+#pragma unroll
+      for (int j = 0; j < PARTS; ++j) top = fmaxf(top, ml[j].x);
+      const float old = m == -INFINITY ? 0.f : ex2_approx(m - top);
+      m = top;
+      l *= old;
+#pragma unroll
+      for (int x = 0; x < 4; ++x) o[x] *= old;
+#pragma unroll
+      for (int j = 0; j < PARTS; ++j) {
+        const float wt = ml[j].x == -INFINITY ? 0.f : ex2_approx(ml[j].x - m);  // 0: a part that saw no key
+        l = fmaf(wt, ml[j].y, l);
+        o[0] = fmaf(wt, a[j].x, o[0]);
+        o[1] = fmaf(wt, a[j].y, o[1]);
+        o[2] = fmaf(wt, a[j].z, o[2]);
+        o[3] = fmaf(wt, a[j].w, o[3]);
+      }
     }
     const float inv = 1.f / l;
     __nv_bfloat16* const to = static_cast<__nv_bfloat16*>(p.o.ptr) + (w.seq.row0 + node) * p.o.row +
-                              (long long)(w.kvh * p.G + r - nd * p.G) * p.o.head + 4 * lane;
+                              (long long)(w.kvh * p.G + r - nd * p.G) * p.o.head + 4 * ch;
     *reinterpret_cast<uint2*>(to) = make_uint2(pack_bf16x2(o[0] * inv, o[1] * inv), pack_bf16x2(o[2] * inv, o[3] * inv));
   }
 }
 
 // How a call is cut, from what the host knows of it.
 struct Plan {
-  int slots, grid, min_tiles;
+  int slots, grid, min_tiles, unit_cost;
 };
 Plan plan_of(int rows, int B, int H, int Hkv, int num_sms) {
   Plan pl;
@@ -738,6 +793,9 @@ Plan plan_of(int rows, int B, int H, int Hkv, int num_sms) {
   // a part costs its rows' outputs in fp32, written and read: 1 KB a row against 32 KB a tile
   const long long avg = std::min<long long>(per_seq / B, pl.slots * kBQ);
   pl.min_tiles = (int)std::max<long long>(1, avg / 32);
+  // A unit's queries, first scores and outputs take the time of about four tiles; where every CTA has about
+  // a unit of its own, that shares the work out better. With fewer units it would leave CTAs without tiles.
+  pl.unit_cost = 2ll * B * Hkv > num_sms ? 4 : 0;
   return pl;
 }
 
@@ -762,7 +820,6 @@ cudaError_t launch_attn_paged(const HeadRows& q, const PagedCache& c, const Head
     *why = "cuTensorMapEncodeTiled failed for the cache";
     return cudaErrorInvalidValue;
   }
-  p.q = q;
   p.o = o;
   p.c = c;
   p.cu = cu;
@@ -774,12 +831,19 @@ cudaError_t launch_attn_paged(const HeadRows& q, const PagedCache& c, const Head
   p.G = H / Hkv;
   p.window = window > 0 ? window : 0;
   p.tq = kBQ / p.G;
+  p.q_bytes = p.tq * p.G * kD * 2;
+  if (!make_tma_heads_bf16(&p.tq_map, q, rows, H, kD, p.G, p.tq)) {
+    *why = "cuTensorMapEncodeTiled failed for the queries";
+    return cudaErrorInvalidValue;
+  }
   p.slots = pl.slots;
   while ((1 << p.box_shift) < box) ++p.box_shift;
   p.grid = pl.grid;
   p.min_tiles = pl.min_tiles;
+  p.unit_cost = pl.unit_cost;
   p.acc = static_cast<float*>(ws);
   p.ml = reinterpret_cast<float2*>(p.acc + (size_t)2 * pl.grid * pl.slots * kBQ * kD);
+  p.o_wide = reinterpret_cast<uintptr_t>(o.ptr) % 32 == 0 && (rows == 1 || o.row % 16 == 0) && (H == 1 || o.head % 16 == 0);
   p.status = st;
   p.wait_ns = wait_ns;
   const bool two = pl.slots == 2;
@@ -789,7 +853,10 @@ cudaError_t launch_attn_paged(const HeadRows& q, const PagedCache& c, const Head
   cudaError_t e = set_smem_limit_once(reinterpret_cast<const void*>(kernel), smem, configured[two]);
   if (e == cudaSuccess) e = launch_pdl(kernel, pl.grid, threads, smem, s, p);
   if (e != cudaSuccess || pl.grid == 1) return e;
-  return launch_pdl(attn_paged_join_kernel, dim3(pl.grid - 1, kJoinBlocks), kJoinThreads, 0, s, p);
+  // few units: many parts each, and all of them loaded at once; many units: a few parts each, more blocks per SM
+  const bool few = 4ll * B * Hkv <= num_sms;
+  return launch_pdl(few ? attn_paged_join_kernel<10> : attn_paged_join_kernel<4>, dim3(pl.grid - 1, two ? 16 : 4),
+                    kJoinThreads, 0, s, p);
 }
 
 }  // namespace blk

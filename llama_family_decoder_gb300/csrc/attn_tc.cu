@@ -1164,8 +1164,6 @@ cudaError_t launch_attn_prefill_tc(const void* q, const void* k, const void* v, 
 
 // ------------------------------------------------------------------ packed sequences
 
-namespace {
-
 // 3-D TMA map over bf16 head rows: boxes of 64 channels x box_heads x box_rows rows, 128-byte
 // swizzle, zero fill out of bounds. Strides in multiples of 8 elements.
 bool make_tma_heads_bf16(CUtensorMap* m, const HeadRows& x, int rows, int heads, int d, int box_heads, int box_rows) {
@@ -1187,6 +1185,8 @@ bool make_tma_heads_bf16(CUtensorMap* m, const HeadRows& x, int rows, int heads,
                 CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
+
+namespace {
 
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanBins = 4096;

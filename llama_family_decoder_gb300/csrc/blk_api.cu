@@ -1774,6 +1774,8 @@ blk_status blk_attn_paged(blk_handle* h, const blk_head_rows* q, int rows, const
   if (rows == 0 || batch == 0) return BLK_OK;
   for (const void* x : {(const void*)q->ptr, (const void*)cache->k, (const void*)cache->v})
     if (x == o->ptr) return fail(BLK_ERR_INVALID_ARG, "o must not be an input");
+  if ((rows > 1 && q->row_stride == 0) || (d.n_heads > 1 && q->head_stride == 0))
+    return fail(BLK_ERR_UNSUPPORTED, "paged attention: broadcast (zero) strides");
   if ((__int128)cache->n_pages * d.n_kv_heads * cache->page_size > 0x7fffffff)
     return fail(BLK_ERR_UNSUPPORTED, "paged attention: the cache has more than 2^31 - 1 rows");
   const size_t need = attn_paged_ws_bytes(rows, batch, d.n_heads, d.n_kv_heads, h->num_sms);

@@ -454,9 +454,8 @@ def test_attn_paged_layouts():
     out = torch.zeros(6, 37, D, dtype=torch.bfloat16, device=DEV)
     got = blk.attn_paged(wide[:, 2:8], c, cu, parents, out=out.transpose(0, 1))
     assert torch.equal(got, want) and torch.equal(out.transpose(0, 1), want)
-    same = q[:, :1].expand(37, 6, D)  # one head's query for all
-    each = blk.attn_paged(same, c, cu, parents)
-    assert torch.equal(each, blk.attn_paged(same.contiguous(), c, cu, parents))
+    with pytest.raises(BlkError, match="broadcast"):
+        blk.attn_paged(q[:, :1].expand(37, 6, D), c, cu, parents)
 
 
 def test_attn_paged_shared_pages():
