@@ -507,9 +507,13 @@ blk_status blk_paged_append(blk_handle* h, const blk_head_rows* q, const blk_hea
  * -inf, gives the row NaN, as the formula does; a NaN or infinity in v of a slot that some row of the sequence
  * sees may reach the others (0 * NaN). The probabilities are rounded to bf16 for
  * their product with v, the output to bf16; everything between is fp32.
- * workspace: blk_attn_paged_workspace_bytes(h, rows, batch); it may be NULL where that is 0.
- * Errors: INVALID_ARG, UNSUPPORTED (fp32 handle), ALIGNMENT, WORKSPACE, CUDA. */
-size_t blk_attn_paged_workspace_bytes(const blk_handle* h, int rows, int batch);
+ * q's rows and heads have strides of their own (no broadcast).
+ * workspace: blk_attn_paged_workspace_bytes (packed: cu_seqlens is given; tree: parents are; of cache its
+ * sizes count), 0 for small batches (then it may be NULL) and for what the call refuses.
+ * Errors: INVALID_ARG, UNSUPPORTED (fp32 handle; zero strides; rows and page lists for more than 2^31 tiles
+ * of 64 keys), ALIGNMENT, WORKSPACE, CUDA. */
+size_t blk_attn_paged_workspace_bytes(const blk_handle* h, int rows, int packed, int tree, int batch,
+                                      const blk_paged_cache* cache);
 blk_status blk_attn_paged(blk_handle* h, const blk_head_rows* q, int rows, const int* cu_seqlens, const int* parents,
                           int batch, const blk_paged_cache* cache, const blk_head_rows* o, void* workspace,
                           size_t workspace_bytes, void* stream);

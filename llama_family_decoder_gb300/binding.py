@@ -106,7 +106,7 @@ SIGNATURES = {
     "blk_rope_table": (c_int, [c_void_p, c_int, c_int, c_void_p, c_void_p]),
     "blk_paged_append": (c_int, [c_void_p, _ROWS, _ROWS, _ROWS, c_int, c_void_p, c_void_p, c_int, _PAGED, _LAYOUT,
                                  c_void_p, c_void_p, _ROWS, c_int, c_void_p]),
-    "blk_attn_paged_workspace_bytes": (c_size_t, [c_void_p, c_int, c_int]),
+    "blk_attn_paged_workspace_bytes": (c_size_t, [c_void_p, c_int, c_int, c_int, c_int, _PAGED]),
     "blk_attn_paged": (c_int, [c_void_p, _ROWS, c_int, c_void_p, c_void_p, c_int, _PAGED, _ROWS, c_void_p, c_size_t,
                                c_void_p]),
     "blk_verify_drafts": (c_int, [c_void_p, c_void_p, c_longlong, c_void_p, c_longlong, c_int, c_int, c_void_p,
@@ -697,7 +697,7 @@ class DecoderBlock:
         qi = self._rows(q, "q", (n, H, d))
         cu, up = self._int32(cu_seqlens, "cu_seqlens", batch + 1), self._int32(parents, "parents", n)
         out, o = self._out(out, "out", (n, H, d))
-        nbytes = lib().blk_attn_paged_workspace_bytes(self.handle, n, batch)
+        nbytes = lib().blk_attn_paged_workspace_bytes(self.handle, n, cu is not None, up is not None, batch, c)
         ws = self._torch.empty(nbytes, dtype=self._torch.uint8, device=self._device) if nbytes else None
         _check(lib().blk_attn_paged(self.handle, qi, n, cu, up, batch, c, o, ws.data_ptr() if nbytes else None, nbytes,
                                     self._raw_stream(self._dev)))

@@ -40,6 +40,7 @@ constexpr int kQSub = kBQ * 128;       // one 64-channel half of a slot's querie
 constexpr int kQBytes = 2 * kQSub;
 constexpr int kKVSub = kBK * 128;      // one 64-channel half of a K or V tile
 constexpr int kStageBytes = 4 * kKVSub;
+constexpr int kClusterTiles = 20;      // a CTA's share of tiles up to which clusters of ragged sequences pay
 constexpr float kRescaleLog2 = 8.0f;
 constexpr float kScaleLog2 = 1.4426950408889634f * 0.08838834764831845f;  // log2(e) / sqrt(128)
 constexpr int kNoBox = -2;             // a box that no row needs; entries below -1 are read as -1
@@ -56,6 +57,8 @@ struct AttnParams {
   int slots;      // slots of a CTA
   int box_shift;  // log2 of a box's rows: those of a page, at most 64
   int grid, min_tiles;
+  int cluster;    // CTAs that share a unit, 1: no clusters
+  int units;      // ... units of a (sequence, KV head), at most
   int unit_cost;  // what a unit counts for on the line besides its tiles, before them
   float2* ml;     // partial results [2 grid][slots][128]: (reference, sum)
   float* acc;     // ... [2 grid][slots][32][128][4]: four channels of each row side by side
@@ -125,40 +128,38 @@ __device__ __forceinline__ int head_cost(const AttnParams& p, const Seq& s) {  /
 
 // A CTA's stretch [lo, hi) of the line, and the sequence it begins in, whose own tiles begin at `base`.
 struct Stretch {
-  long long lo, hi, base;
-  int b, per;
+  int lo, hi, base, b, per;
 };
-// By one warp. Stretch number `c`; an empty one (lo >= hi) if the line ends before.
-__device__ __forceinline__ long long scan(long long n, int lane) {
+// By one warp. Stretch number `c`; an empty one (lo >= hi) if the line ends before. The line is shorter
+// than 2^31 (see plan_of).
+__device__ __forceinline__ int scan(int n, int lane) {
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const long long x = __shfl_up_sync(0xffffffffu, n, o);
+    const int x = __shfl_up_sync(0xffffffffu, n, o);
     if (lane >= o) n += x;
   }
   return n;
 }
 __device__ __forceinline__ Stretch stretch_of(const AttnParams& p, int c, int lane) {
-  auto cost_of = [&](int b) { return b < p.B ? (long long)p.Hkv * head_cost(p, seq_of(p, b)) : 0; };
+  auto cost_of = [&](int b) { return b < p.B ? p.Hkv * head_cost(p, seq_of(p, b)) : 0; };
   constexpr int kHeld = 4;  // 32 sequences each, looked up once
-  long long held[kHeld], total = 0;
+  int held[kHeld], total = 0;
 #pragma unroll
   for (int i = 0; i < kHeld; ++i) held[i] = cost_of(32 * i + lane);
 #pragma unroll
   for (int i = 0; i < kHeld; ++i) total += held[i];
   for (int b = lane + 32 * kHeld; b < p.B; b += 32) total += cost_of(b);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+  total = (int)__reduce_add_sync(0xffffffffu, (unsigned)total);
   Stretch s;
-  const long long per = max((total + p.grid - 1) / p.grid, (long long)p.min_tiles);
-  s.per = (int)per;
-  s.lo = c * per;
-  s.hi = min(total, s.lo + per);
+  s.per = max((int)(((unsigned)total + p.grid - 1) / p.grid), p.min_tiles);
+  s.lo = (int)min((long long)total, (long long)c * s.per);
+  s.hi = (int)min((long long)total, (long long)s.lo + s.per);
   s.base = 0;
   s.b = 0;
   if (s.lo >= s.hi) return s;
   bool found = false;
-  auto look = [&](int b0, long long n) {  // whether the stretch begins in these 32 sequences
-    const long long upto = scan(n, lane);
+  auto look = [&](int b0, int n) {  // whether the stretch begins in these 32 sequences
+    const int upto = scan(n, lane);
     const unsigned past = __ballot_sync(0xffffffffu, s.base + upto > s.lo);
     const int at = past ? __ffs(past) - 1 : 31;
     s.b = b0 + at;
@@ -180,7 +181,7 @@ struct Walk {
   Keys keys;
   int b, kvh, t, tiles, j0, j1;
   int at;  // where in the unit, costs counted, the stretch is
-  long long left;
+  int left;
   Walk() = default;
   __device__ __forceinline__ void unit(const AttnParams& p) {
     keys = keys_of(p, seq, t);
@@ -188,7 +189,7 @@ struct Walk {
   }
   __device__ __forceinline__ void part(const AttnParams& p) {
     j0 = max(0, at - p.unit_cost);
-    j1 = (int)min((long long)tiles, max(0ll, at + left - p.unit_cost));
+    j1 = min(tiles, max(0, at + left - p.unit_cost));
   }
   __device__ __forceinline__ Walk(const AttnParams& p, const Stretch& s) {
     left = s.hi - s.lo;
@@ -196,20 +197,33 @@ struct Walk {
     b = s.b;
     if (left <= 0) return;
     seq = seq_of(p, b);
-    const long long from = s.lo - s.base;
+    const int from = s.lo - s.base;
     const int per_head = head_cost(p, seq);
     if (per_head <= 0) {  // lengths that change meanwhile: no walk leaves the lists
       left = 0;
       return;
     }
-    kvh = (int)(from / per_head);
-    at = (int)(from - (long long)kvh * per_head);
+    kvh = from / per_head;
+    at = from - kvh * per_head;
     unit(p);
     while (at >= tiles + p.unit_cost) {  // at < per_head: it ends within the units
       at -= tiles + p.unit_cost;
       ++t;
       unit(p);
     }
+    part(p);
+  }
+  // The share of CTA `rank` of a cluster of `size` that takes unit number u, or nothing.
+  __device__ __forceinline__ Walk(const AttnParams& p, int u, int rank, int size) {
+    left = j0 = j1 = tiles = at = 0;
+    t = u % p.units;
+    kvh = u / p.units % p.Hkv;
+    b = u / p.units / p.Hkv;
+    seq = seq_of(p, b);
+    if (t >= units_of(p, seq)) return;
+    unit(p);
+    at = (int)((long long)tiles * rank / size);
+    left = (int)((long long)tiles * (rank + 1) / size) - at;
     part(p);
   }
   __device__ __forceinline__ bool on() const { return left > 0; }
@@ -244,6 +258,45 @@ __device__ __forceinline__ unsigned long long bits_from(int lo) {  // bits lo ..
 }
 __device__ __forceinline__ unsigned long long bits_below(int hi) { return ~bits_from(hi); }
 
+// Four channels of a row, joined from parts (reference and sum, unnormalised outputs) one group after
+// the other.
+struct Joined {
+  float m = -INFINITY, l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
+  template <int N>
+  __device__ __forceinline__ void take(const float2 (&ml)[N], const float4 (&a)[N]) {
+    float top = m;
+#pragma unroll
+    for (int j = 0; j < N; ++j) top = fmaxf(top, ml[j].x);
+    const float old = m == -INFINITY ? 0.f : ex2_approx(m - top);
+    m = top;
+    l *= old;
+#pragma unroll
+    for (int x = 0; x < 4; ++x) o[x] *= old;
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      if (ml[j].x == -INFINITY && !(ml[j].y != ml[j].y)) continue;  // a part that saw no key, or is none
+      const float wt = ex2_approx(ml[j].x - m);
+      l = fmaf(wt, ml[j].y, l);
+      o[0] = fmaf(wt, a[j].x, o[0]);
+      o[1] = fmaf(wt, a[j].y, o[1]);
+      o[2] = fmaf(wt, a[j].z, o[2]);
+      o[3] = fmaf(wt, a[j].w, o[3]);
+    }
+  }
+  __device__ __forceinline__ void store(const AttnParams& p, const Walk& w, int node, int head, int ch) const {
+    const float inv = 1.f / l;
+    __nv_bfloat16* const to = static_cast<__nv_bfloat16*>(p.o.ptr) + (w.seq.row0 + node) * p.o.row +
+                              (long long)(w.kvh * p.G + head) * p.o.head + 4 * ch;
+    *reinterpret_cast<uint2*>(to) = make_uint2(pack_bf16x2(o[0] * inv, o[1] * inv), pack_bf16x2(o[2] * inv, o[3] * inv));
+  }
+};
+
+__device__ __forceinline__ float2 ld_dsmem_f2(uint32_t addr) {
+  float2 v;
+  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
+  return v;
+}
+
 // ------------------------------------------------------------------ the kernel
 
 template <int NS>
@@ -255,7 +308,7 @@ struct Cfg {
   static_assert(kSmem <= 227 * 1024, "shared memory");
 };
 
-template <int NS>
+template <int NS, bool CL>
 __global__ void __launch_bounds__(Cfg<NS>::kThreads, 1) attn_paged_kernel(const __grid_constant__ AttnParams p) {
   typedef Cfg<NS> C;
   extern __shared__ uint8_t smem_raw[];
@@ -314,8 +367,13 @@ __global__ void __launch_bounds__(Cfg<NS>::kThreads, 1) attn_paged_kernel(const 
   // while this one runs
   pdl_launch_dependents();
   if (warp == 0) {
-    const Walk w(p, stretch_of(p, blockIdx.x, lane));
-    if (lane == 0) *begin = w;
+    if constexpr (CL) {
+      const Walk w(p, blockIdx.x / p.cluster, cluster_ctarank(), p.cluster);
+      if (lane == 0) *begin = w;
+    } else {
+      const Walk w(p, stretch_of(p, blockIdx.x, lane));
+      if (lane == 0) *begin = w;
+    }
   }
   if (warp == 2 && blockIdx.x == 0) {  // what the lists say that they should not
     bool bad = false, over = false;
@@ -337,6 +395,9 @@ __global__ void __launch_bounds__(Cfg<NS>::kThreads, 1) attn_paged_kernel(const 
   // phase) and whether any MMA was.
   uint32_t issued = 0, parity = 0, q_issued = 0, q_parity = 0;
   bool mma_issued = false;
+  // clusters: a row's reference and sum over the CTA's share (of none, at first)
+  float2 share = make_float2(-INFINITY, 0.f);
+  bool share_live = false;
 
   if (warp == 0) {
     // ---------------- the cache's tiles, all lanes
@@ -641,7 +702,7 @@ __global__ void __launch_bounds__(Cfg<NS>::kThreads, 1) attn_paged_kernel(const 
       }
       __syncwarp();
       tc_fence_after();
-      if (live) {
+      if (!CL && live) {
         const bool whole = w.whole();
         float* const acc = p.acc + ((size_t)part * NS + g) * kBQ * kD + 4 * r;
         // a row sees itself at least: a sum that is NaN, or 0 where all its scores are -inf, gives NaN
@@ -677,6 +738,10 @@ __global__ void __launch_bounds__(Cfg<NS>::kThreads, 1) attn_paged_kernel(const 
           __syncwarp();
         }
       }
+      if constexpr (CL) {  // its outputs stay in tensor memory for the cluster (below)
+        share_live = live;
+        share = make_float2(m_ref, l);
+      }
       tc_fence_before();
       mbar_arrive(o_free(g));
       ++units;
@@ -706,10 +771,66 @@ __global__ void __launch_bounds__(Cfg<NS>::kThreads, 1) attn_paged_kernel(const 
     tc_fence_before();
     __syncthreads();
   }
+  if (CL && warp >= 4) {
+    // the products have read the queries and the ring: a share's sums and outputs take their place
+    tc_fence_after();
+    const int g = (warp - 4) >> 2, r = (warp & 3) * 32 + lane;
+    reinterpret_cast<float2*>(sQ + g * kQBytes)[r] = share;
+    if (share_live && !*abort_flag) {
+      const uint32_t o_taddr = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + 256 * g + 128;
+#pragma unroll 1
+      for (int c = 0; c < kD; c += 16) {
+        float ov[16];
+        tmem_ld16(o_taddr + c, ov);
+        tc_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 16; i += 4)
+          reinterpret_cast<float4*>(ring)[(g * (kD / 4) + (c + i) / 4) * kBQ + r] = make_float4(ov[i], ov[i + 1], ov[i + 2], ov[i + 3]);
+      }
+    }
+    tc_fence_before();
+  }
+  if constexpr (CL) __syncthreads();
   if (warp == 1) {
     __syncwarp();
     tc_fence_after();
     tmem_dealloc(tmem, kTmemCols);
+  }
+  if constexpr (CL) {
+    // The shares of the cluster's CTAs joined in their order, as the second kernel does with parts: a thread
+    // has four channels of a row, the slots' warps of all CTAs take them in turn.
+    __syncwarp();
+    cluster_sync_all();
+    Walk w = *begin;
+    if (warp >= 4 && w.t < units_of(p, w.seq)) {
+      const int rank = cluster_ctarank();
+      for (int i = rank * 4 * NS + warp - 4; i < NS * (kBQ / 32) * (kD / 4); i += p.cluster * 4 * NS) {
+        const int ch = i % (kD / 4), quarter = i / (kD / 4) % (kBQ / 32), g = i / (kD / 4) / (kBQ / 32);
+        const int r = quarter * 32 + lane, nd = r / p.G, node = w.node0(p, g) + nd;
+        const bool valid = nd < p.tq && node < w.seq.n;
+        if (!__any_sync(0xffffffffu, valid)) continue;
+        const uint32_t at_ml = smem_u32(sQ + g * kQBytes) + 8 * r;
+        const uint32_t at_o = smem_u32(ring) + (((g * (kD / 4) + ch) * kBQ + r) << 4);
+        Joined x;
+        for (int k0 = 0; k0 < p.cluster; k0 += 8) {
+          float2 ml[8];
+          float4 a[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            ml[j] = make_float2(-INFINITY, 0.f);
+            a[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (k0 + j < p.cluster) {
+              ml[j] = ld_dsmem_f2(map_shared_rank(at_ml, k0 + j));
+              a[j] = ld_dsmem_f4(map_shared_rank(at_o, k0 + j));
+            }
+          }
+          x.take(ml, a);
+        }
+        if (valid) x.store(p, w, node, r - nd * p.G, ch);
+      }
+    }
+    __syncwarp();
+    cluster_sync_all();  // nobody leaves while its share may be read
   }
 }
 
@@ -731,17 +852,17 @@ __global__ void __launch_bounds__(kJoinThreads) attn_paged_join_kernel(const __g
   const Walk w(p, s);
   pdl_launch_dependents();
   pdl_wait();  // for the partial results; the lists are there (see the other kernel)
-  const long long tile0 = s.lo - w.at + p.unit_cost;  // the unit's first tile on the line
+  const int tile0 = s.lo - w.at + p.unit_cost;  // the unit's first tile on the line
   if (!w.on() || w.j0 == 0 || tile0 / s.per != c - 1) return;  // no unit goes over, or an earlier block joins it
-  const int e = (int)((tile0 + w.tiles - 1) / s.per);
+  const int e = (tile0 + w.tiles - 1) / s.per;
   // a thread has four channels of a row, a warp 32 rows; PARTS parts are under way at a time
-  const int first = s.lo - w.at <= (long long)(c - 1) * s.per ? 2 * (c - 1) : 2 * (c - 1) + 1;  // that stretch's first unit?
+  const int first = s.lo - w.at <= (c - 1) * s.per ? 2 * (c - 1) : 2 * (c - 1) + 1;  // that stretch's first unit?
   const int warp = blockIdx.y * (kJoinThreads / 32) + (threadIdx.x >> 5), warps = gridDim.y * (kJoinThreads / 32);
   for (int i = warp; i < p.slots * (kBQ / 32) * (kD / 4); i += warps) {
     const int ch = i % (kD / 4), quarter = i / (kD / 4) % (kBQ / 32), g = i / (kD / 4) / (kBQ / 32);
     const int r = quarter * 32 + lane, nd = r / p.G, node = w.node0(p, g) + nd;
     if (nd >= p.tq || node >= w.seq.n) continue;
-    float m = -INFINITY, l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
+    Joined x;
     for (int k0 = c - 1; k0 <= e; k0 += PARTS) {
       float2 ml[PARTS];
       float4 a[PARTS];
@@ -756,38 +877,55 @@ __global__ void __launch_bounds__(kJoinThreads) attn_paged_join_kernel(const __g
           a[j] = reinterpret_cast<const float4*>(p.acc + at * kBQ * kD)[ch * kBQ + r];
         }
       }
-      float top = m;
-#pragma unroll
-      for (int j = 0; j < PARTS; ++j) top = fmaxf(top, ml[j].x);
-      const float old = m == -INFINITY ? 0.f : ex2_approx(m - top);
-      m = top;
-      l *= old;
-#pragma unroll
-      for (int x = 0; x < 4; ++x) o[x] *= old;
-#pragma unroll
-      for (int j = 0; j < PARTS; ++j) {
-        const float wt = ml[j].x == -INFINITY ? 0.f : ex2_approx(ml[j].x - m);  // 0: a part that saw no key
-        l = fmaf(wt, ml[j].y, l);
-        o[0] = fmaf(wt, a[j].x, o[0]);
-        o[1] = fmaf(wt, a[j].y, o[1]);
-        o[2] = fmaf(wt, a[j].z, o[2]);
-        o[3] = fmaf(wt, a[j].w, o[3]);
-      }
+      x.take(ml, a);
     }
-    const float inv = 1.f / l;
-    __nv_bfloat16* const to = static_cast<__nv_bfloat16*>(p.o.ptr) + (w.seq.row0 + node) * p.o.row +
-                              (long long)(w.kvh * p.G + r - nd * p.G) * p.o.head + 4 * ch;
-    *reinterpret_cast<uint2*>(to) = make_uint2(pack_bf16x2(o[0] * inv, o[1] * inv), pack_bf16x2(o[2] * inv, o[3] * inv));
+    x.store(p, w, node, r - nd * p.G, ch);
   }
 }
 
 // How a call is cut, from what the host knows of it.
 struct Plan {
-  int slots, grid, min_tiles, unit_cost;
+  int slots, grid, min_tiles, unit_cost, units, cluster;
+  bool fits;  // the line is shorter than 2^31
 };
-Plan plan_of(int rows, int B, int H, int Hkv, int num_sms) {
-  Plan pl;
-  const long long per_seq = (long long)rows * (H / Hkv);  // matrix rows of all sequences of a KV head
+
+// Clusters of `size` CTAs of the kernel that are resident at once, 0 if it cannot be launched so; asked once per device.
+template <int NS>
+int resident_clusters(int size) {
+  static std::atomic<int> known[64][5];
+  int dev = 0, lg = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+  while ((1 << lg) < size) ++lg;
+  const int was = known[dev][lg].load(std::memory_order_relaxed);
+  if (was != 0) return was - 1;
+  const auto kernel = attn_paged_kernel<NS, true>;
+  int n = 0;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)size);
+  cfg.blockDim = dim3(Cfg<NS>::kThreads);
+  cfg.dynamicSmemBytes = Cfg<NS>::kSmem;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)size;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel), cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           Cfg<NS>::kSmem) != cudaSuccess ||
+      cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel), cudaFuncAttributeNonPortableClusterSizeAllowed, 1) !=
+          cudaSuccess ||
+      cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) {
+    cudaGetLastError();
+    n = 0;
+  }
+  known[dev][lg].store(n + 1, std::memory_order_relaxed);
+  return n;
+}
+
+Plan plan_of(int rows, int B, int H, int Hkv, bool cu, bool tree, long long capacity, int window, int num_sms) {
+  Plan pl{};
+  const int G = H / Hkv, tq = kBQ / G;
+  const long long per_seq = (long long)rows * G;  // matrix rows of all sequences of a KV head
   pl.slots = per_seq > 96ll * B ? 2 : 1;
   pl.grid = num_sms;
   // a part costs its rows' outputs in fp32, written and read: 1 KB a row against 32 KB a tile
@@ -796,14 +934,30 @@ Plan plan_of(int rows, int B, int H, int Hkv, int num_sms) {
   // A unit's queries, first scores and outputs take the time of about four tiles; where every CTA has about
   // a unit of its own, that shares the work out better. With fewer units it would leave CTAs without tiles.
   pl.unit_cost = 2ll * B * Hkv > num_sms ? 4 : 0;
+  const int nodes = tq * pl.slots, most = tree ? std::min(rows, kMaxNodes) : cu ? rows : 1;
+  pl.units = (most + nodes - 1) / nodes;
+  const long long keys = std::min(capacity, window > 0 ? (long long)window + (tree ? kMaxNodes : nodes) : capacity);
+  const long long tiles = keys / kBK + 2;
+  pl.fits = ((long long)B + rows / nodes + 1) * Hkv * (tiles + pl.unit_cost) < 0x7fffffffll;
+  // Clusters: a unit each, its keys in equal shares, no list to add up and no second kernel.
+  pl.cluster = 1;
+  const long long units = (long long)B * Hkv * pl.units;
+  for (int size = 16; size > 1; size /= 2)
+    if (units * size <= num_sms && (B == 1 || tiles <= kClusterTiles * size) &&
+        (pl.slots == 2 ? resident_clusters<2>(size) : resident_clusters<1>(size)) >= units) {
+      pl.cluster = size;
+      break;
+    }
   return pl;
 }
 
 }  // namespace
 
-size_t attn_paged_ws_bytes(int rows, int B, int H, int Hkv, int num_sms) {
+size_t attn_paged_ws_bytes(int rows, int B, int H, int Hkv, bool cu, bool tree, long long capacity, int window, int num_sms) {
   if (rows <= 0 || B <= 0) return 0;
-  const Plan pl = plan_of(rows, B, H, Hkv, num_sms);
+  const Plan pl = plan_of(rows, B, H, Hkv, cu, tree, capacity, window, num_sms);
+  if (!pl.fits) return kAttnPagedTooLong;
+  if (pl.cluster > 1) return 0;
   return (size_t)2 * pl.grid * pl.slots * kBQ * (sizeof(float2) + kD * sizeof(float));
 }
 
@@ -811,13 +965,17 @@ cudaError_t launch_attn_paged(const HeadRows& q, const PagedCache& c, const Head
                               const int* parents, int B, int H, int Hkv, int window, void* ws, int num_sms,
                               DevStatus* st, unsigned long long wait_ns, cudaStream_t s, const char** why) {
   if (rows <= 0 || B <= 0) return cudaSuccess;
-  const Plan pl = plan_of(rows, B, H, Hkv, num_sms);
+  const Plan pl = plan_of(rows, B, H, Hkv, cu != nullptr, parents != nullptr, page_slots(c), window, num_sms);
   AttnParams p;
   memset(static_cast<void*>(&p), 0, sizeof(p));
   const int box = std::min(1 << c.page_shift, kBK);
   const int cache_rows = (c.n_pages * Hkv) << c.page_shift;  // checked by the caller
-  if (!make_tma_2d_16b(&p.tk, c.k, cache_rows, kD, box, false) || !make_tma_2d_16b(&p.tv, c.v, cache_rows, kD, box, false)) {
-    *why = "cuTensorMapEncodeTiled failed for the cache";
+  p.G = H / Hkv;
+  p.tq = kBQ / p.G;
+  p.q_bytes = p.tq * p.G * kD * 2;
+  if (!make_tma_2d_16b(&p.tk, c.k, cache_rows, kD, box, false) || !make_tma_2d_16b(&p.tv, c.v, cache_rows, kD, box, false) ||
+      !make_tma_heads_bf16(&p.tq_map, q, rows, H, kD, p.G, p.tq)) {
+    *why = "cuTensorMapEncodeTiled failed for the cache or the queries";
     return cudaErrorInvalidValue;
   }
   p.o = o;
@@ -828,27 +986,25 @@ cudaError_t launch_attn_paged(const HeadRows& q, const PagedCache& c, const Head
   p.B = B;
   p.H = H;
   p.Hkv = Hkv;
-  p.G = H / Hkv;
   p.window = window > 0 ? window : 0;
-  p.tq = kBQ / p.G;
-  p.q_bytes = p.tq * p.G * kD * 2;
-  if (!make_tma_heads_bf16(&p.tq_map, q, rows, H, kD, p.G, p.tq)) {
-    *why = "cuTensorMapEncodeTiled failed for the queries";
-    return cudaErrorInvalidValue;
-  }
   p.slots = pl.slots;
   while ((1 << p.box_shift) < box) ++p.box_shift;
   p.grid = pl.grid;
   p.min_tiles = pl.min_tiles;
-  p.unit_cost = pl.unit_cost;
-  p.acc = static_cast<float*>(ws);
-  p.ml = reinterpret_cast<float2*>(p.acc + (size_t)2 * pl.grid * pl.slots * kBQ * kD);
+  p.cluster = pl.cluster;
+  p.units = pl.units;
+  p.unit_cost = pl.cluster > 1 ? 0 : pl.unit_cost;
   p.o_wide = reinterpret_cast<uintptr_t>(o.ptr) % 32 == 0 && (rows == 1 || o.row % 16 == 0) && (H == 1 || o.head % 16 == 0);
   p.status = st;
   p.wait_ns = wait_ns;
   const bool two = pl.slots == 2;
-  const auto kernel = two ? attn_paged_kernel<2> : attn_paged_kernel<1>;
   const int smem = two ? Cfg<2>::kSmem : Cfg<1>::kSmem, threads = two ? Cfg<2>::kThreads : Cfg<1>::kThreads;
+  if (pl.cluster > 1)  // configured when the resident clusters were asked for
+    return launch_clusters(two ? attn_paged_kernel<2, true> : attn_paged_kernel<1, true>, B * Hkv * pl.units * pl.cluster,
+                           threads, smem, pl.cluster, s, p);
+  p.acc = static_cast<float*>(ws);
+  p.ml = reinterpret_cast<float2*>(p.acc + (size_t)2 * pl.grid * pl.slots * kBQ * kD);
+  const auto kernel = two ? attn_paged_kernel<2, false> : attn_paged_kernel<1, false>;
   static std::atomic<unsigned long long> configured[2];
   cudaError_t e = set_smem_limit_once(reinterpret_cast<const void*>(kernel), smem, configured[two]);
   if (e == cudaSuccess) e = launch_pdl(kernel, pl.grid, threads, smem, s, p);

@@ -1756,9 +1756,12 @@ blk_status blk_paged_append(blk_handle* h, const blk_head_rows* q, const blk_hea
                     "paged append");
 }
 
-size_t blk_attn_paged_workspace_bytes(const blk_handle* h, int rows, int batch) {
-  if (!h || rows <= 0 || batch <= 0) return 0;
-  return attn_paged_ws_bytes(rows, batch, h->d.n_heads, h->d.n_kv_heads, h->num_sms);
+size_t blk_attn_paged_workspace_bytes(const blk_handle* h, int rows, int packed, int tree, int batch,
+                                      const blk_paged_cache* cache) {
+  if (!h || rows <= 0 || batch <= 0 || check_paged(cache) != BLK_OK) return 0;
+  const size_t n = attn_paged_ws_bytes(rows, batch, h->d.n_heads, h->d.n_kv_heads, packed != 0, tree != 0,
+                                       page_slots(paged_cache(cache)), h->d.sliding_window, h->num_sms);
+  return n == kAttnPagedTooLong ? 0 : n;
 }
 
 blk_status blk_attn_paged(blk_handle* h, const blk_head_rows* q, int rows, const int* cu_seqlens, const int* parents,
@@ -1778,7 +1781,9 @@ blk_status blk_attn_paged(blk_handle* h, const blk_head_rows* q, int rows, const
     return fail(BLK_ERR_UNSUPPORTED, "paged attention: broadcast (zero) strides");
   if ((__int128)cache->n_pages * d.n_kv_heads * cache->page_size > 0x7fffffff)
     return fail(BLK_ERR_UNSUPPORTED, "paged attention: the cache has more than 2^31 - 1 rows");
-  const size_t need = attn_paged_ws_bytes(rows, batch, d.n_heads, d.n_kv_heads, h->num_sms);
+  const size_t need = attn_paged_ws_bytes(rows, batch, d.n_heads, d.n_kv_heads, cu_seqlens != nullptr, parents != nullptr,
+                                          page_slots(paged_cache(cache)), d.sliding_window, h->num_sms);
+  if (need == kAttnPagedTooLong) return fail(BLK_ERR_UNSUPPORTED, "paged attention: too many rows over page lists too long");
   if (need > 0 && (!workspace || workspace_bytes < need))
     return fail(BLK_ERR_WORKSPACE, "paged attention: workspace missing or too small");
   if (!aligned16(workspace)) return fail(BLK_ERR_ALIGNMENT, "workspace not 16-byte aligned");

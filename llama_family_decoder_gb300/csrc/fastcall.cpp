@@ -413,7 +413,8 @@ PyObject* attn_paged(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
     at::Tensor to, ws;
     const blk_head_rows o = c.out(a[5], n, c.b->H, to);
     if (!c.ok) return none();
-    const size_t bytes = blk_attn_paged_workspace_bytes(c.b->h, static_cast<int>(n), static_cast<int>(batch));
+    const size_t bytes = blk_attn_paged_workspace_bytes(c.b->h, static_cast<int>(n), cu != nullptr, parents != nullptr,
+                                                        static_cast<int>(batch), &cache);
     if (bytes) ws = c.scratch(bytes);
     if (!launched([&] {
           return blk_attn_paged(c.b->h, &q, static_cast<int>(n), cu, parents, static_cast<int>(batch), &cache, &o,

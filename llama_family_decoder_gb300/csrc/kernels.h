@@ -71,6 +71,12 @@ struct PagedCache {
   int n_pages, page_shift, max_pages;
 };
 
+// Slots of a sequence's page list; at most 2^31 - 1.
+__host__ __device__ inline long long page_slots(const PagedCache& c) {
+  const long long n = (long long)c.max_pages << c.page_shift;
+  return n < 0x7fffffffll ? n : 0x7fffffffll;
+}
+
 // Rows cu[b] .. cu[b + 1] of sequence b (cu null: row b): norm (gains null: none) and rotary (table
 // [max_pos][dims / 2], null: none) of q and k at positions lens[b] + depths[row] (null: the row's number
 // i in its sequence); q to qo, k and v to slot lens[b] + i. Rows without a slot leave the cache alone
@@ -82,8 +88,10 @@ cudaError_t launch_paged_append(const HeadRows& q, const HeadRows& k, const Head
 
 // Attention of packed new rows over the cache (bf16, head_dim 128): row i of sequence b sees the slots
 // below lens[b] and the slots lens[b] + j of its ancestors and itself (parents null: j <= i), within the
-// window. ws: attn_paged_ws_bytes.
-size_t attn_paged_ws_bytes(int rows, int B, int H, int Hkv, int num_sms);
+// window. ws: attn_paged_ws_bytes (capacity: slots of a page list), 0 for small batches, kAttnPagedTooLong for
+// what has more tiles of keys than the kernel counts (no launch).
+constexpr size_t kAttnPagedTooLong = ~size_t(0);
+size_t attn_paged_ws_bytes(int rows, int B, int H, int Hkv, bool cu, bool tree, long long capacity, int window, int num_sms);
 cudaError_t launch_attn_paged(const HeadRows& q, const PagedCache& c, const HeadRows& o, int rows, const int* cu,
                               const int* parents, int B, int H, int Hkv, int window, void* ws, int num_sms,
                               DevStatus* st, unsigned long long wait_ns, cudaStream_t s, const char** why);

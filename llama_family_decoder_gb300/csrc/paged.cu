@@ -334,7 +334,7 @@ cudaError_t launch_paged_keep(void* const* kv, int n_layers, const PagedCache& c
     int size = 1;
     if (path)
       while (size < 8 && 2ll * size * B <= 2ll * num_sms && size * (kKeepThreads / 32) < p.n_layers * 2 * Hkv) size *= 2;
-    const cudaError_t e = launch_clusters(paged_keep_kernel, B * size, kKeepThreads, size, s, p, size);
+    const cudaError_t e = launch_clusters(paged_keep_kernel, B * size, kKeepThreads, 0, size, s, p, size);
     if (e != cudaSuccess || !path) return e;
   }
   return cudaSuccess;

@@ -30,12 +30,6 @@ __device__ __forceinline__ bool seq_bad(const int* cu, int b, int rows) {
   return cu && (cu[b + 1] < cu[b] || cu[b] < 0 || cu[b + 1] > rows);
 }
 
-// Slots of a sequence's page list; at most 2^31 - 1.
-__host__ __device__ inline long long page_slots(const PagedCache& c) {
-  const long long n = (long long)c.max_pages << c.page_shift;
-  return n < 0x7fffffffll ? n : 0x7fffffffll;
-}
-
 // The first row of head 0 of the slot's page, counted in rows of head_dim over the whole cache, and the
 // row within a page: row of head h = at(h). page < 0: the table names no page of the cache.
 struct PagePlace {
@@ -55,10 +49,11 @@ __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.w
 
 // Launch in clusters of `size` CTAs along x, with programmatic stream serialization.
 template <typename... KArgs, typename... Args>
-inline cudaError_t launch_clusters(void (*kern)(KArgs...), int grid, int block, int size, cudaStream_t s, Args... args) {
+inline cudaError_t launch_clusters(void (*kern)(KArgs...), int grid, int block, int smem, int size, cudaStream_t s, Args... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)grid);
   cfg.blockDim = dim3((unsigned)block);
+  cfg.dynamicSmemBytes = (size_t)smem;
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;

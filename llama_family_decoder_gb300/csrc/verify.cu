@@ -303,7 +303,7 @@ cudaError_t launch_verify_drafts(const float* target, long long target_row, cons
   while (p.size < kMaxCluster && (2ll * p.size * B <= 2ll * num_sms || (segs + p.size - 1) / p.size > kCtaSegs) &&
          p.size * kWarps < segs)
     p.size *= 2;
-  return launch_clusters(verify_kernel, B * p.size, kThreads, p.size, s, p);
+  return launch_clusters(verify_kernel, B * p.size, kThreads, 0, p.size, s, p);
 }
 
 }  // namespace blk

@@ -20,7 +20,7 @@ def test_without_a_handle_nothing_is_looked_at():
     assert lib.blk_paged_keep(None, c, 1, 4096, None, None, None, 1, 0, None) == 1
     assert b"NULL handle" in lib.blk_last_error_message()
     assert lib.blk_rope_table(None, 64, 8, 4096, None) == 1
-    assert lib.blk_attn_paged_workspace_bytes(None, 8, 1) == 0
+    assert lib.blk_attn_paged_workspace_bytes(None, 8, 0, 0, 8, c) == 0
 
 
 def test_compiled_argument_handling_leaves_what_is_not_plain():
