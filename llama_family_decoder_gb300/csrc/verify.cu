@@ -13,12 +13,13 @@
 // fp32 numbers (its products and sums with their errors: Dekker 1971, Knuth 1969), sums of 16 of them and then
 // of a warp's likewise, to about 2^-45; everything from there on, and every test, is fp64.
 //
-// A cluster of CTAs takes a sequence. All of them walk the tree alike, from the candidates' p and q
-// values gathered beforehand in one round of loads; only a pass over the vocabulary is shared: CTA r
-// takes the segments of 512 values r, and the cluster's sums meet in distributed shared memory. The
-// pass that ends the walk keeps its segments' sums, from which the next token's segment is found, and
-// a warp looks through that one. Latency-bound: a launch, three dependent rounds of loads, and
-// per pass a row from HBM (or, from the second on, L2) and a cluster barrier.
+// A cluster of CTAs takes a sequence. Warp 0 of each walks the tree, all of them alike, two nodes a lane, from the
+// candidates' p and q values gathered beforehand in one round of loads; fp64 is slow here (two lanes
+// a cycle and SM), so no other warp does any of it. A pass over the vocabulary is shared: CTA r takes the r-th run
+// of segments of 512 values, a warp a segment, and the CTAs' sums meet in distributed shared memory. The pass
+// that ends the walk leaves its segments' sums, in which the next token's segment is found; a warp looks
+// through that one. Latency-bound: a launch, three dependent rounds of loads, and per pass a row from HBM (from the
+// second on, L2) and a cluster barrier.
 #include "paged.cuh"
 
 namespace blk {
@@ -66,25 +67,36 @@ __device__ __forceinline__ Two left_of(float p, float q, Two C) {
   return hi > 0.f || !(hi == hi) ? Two{hi, lo} : Two{0.f, 0.f};
 }
 
-struct Shared {
-  double sums[kCtaSegs];            // of this CTA's segments, in the last pass
-  double warp_sums[kWarps];
-  double total[2];                  // of this CTA, read by its cluster; two passes in turn
-  int parent[kMaxNodes], token[kMaxNodes];
-  float u[kMaxNodes], p[kMaxNodes], q[kMaxNodes];  // p, q: of the candidate's token at its parent
-  int gone[kMaxNodes];              // tokens of rejected candidates (no draft)
-  unsigned long long key;           // the warp's find
+// What warp 0 asks of all: a pass over the row of node cur, with C and without the gone tokens, or nothing more.
+struct Order {
+  int cur, n_gone, done;
+  Two C;
 };
-
-}  // namespace
+struct Shared {
+  Two sums[kCtaSegs];     // of this CTA's segments, in the last pass
+  double total[2];        // of this CTA, read by its cluster; two passes in turn
+  int gone[kMaxNodes];    // tokens of rejected candidates (no draft)
+  Order order;
+};
 
 __device__ __forceinline__ double ld_dsmem_f64(uint32_t addr) {
   double v;
   asm volatile("ld.shared::cluster.f64 %0, [%1];" : "=d"(v) : "r"(addr) : "memory");
   return v;
 }
-
-namespace {
+__device__ __forceinline__ double value_of(Two x) { return (double)x.hi + (double)x.lo; }
+__device__ __forceinline__ Two two_of(double x) {
+  const float hi = (float)x;
+  return {hi, (float)(x - (double)hi)};
+}
+__device__ __forceinline__ double scan(double x, int lane) {
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const double y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  return x;
+}
 
 // 16 consecutive values of a lane, from element `at` of a row, those past the vocabulary 0.
 __device__ __forceinline__ void load16(const float* row, int at, int vocab, bool wide, float (&x)[16]) {
@@ -100,12 +112,56 @@ __device__ __forceinline__ void load16(const float* row, int at, int vocab, bool
   }
 }
 
+// A lane's 16 values of a segment: what is left of the target's distribution at node cur.
+struct Row {
+  const float *p, *q;
+  bool wide_p, wide_q;
+};
+__device__ __forceinline__ void left_values(const Row& row, const Order& o, const int* gone, int vocab, int seg, int lane,
+                                            Two (&v)[16]) {
+  const int at = seg * kSeg + lane * 16;
+  float x[16];
+  load16(row.p, at, vocab, row.wide_p, x);
+  if (o.C.hi > 0.f) {
+    float y[16];
+    load16(row.q, at, vocab, row.wide_q, y);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = left_of(x[i], y[i], o.C);
+    return;
+  }
+  if (o.n_gone > 0) {
+#pragma unroll 1
+    for (int g0 = 0; g0 < o.n_gone; g0 += 32) {
+      const int x_at = g0 + lane < o.n_gone ? gone[g0 + lane] - seg * kSeg : -1;
+      for (unsigned in = __ballot_sync(0xffffffffu, x_at >= 0 && x_at < kSeg); in; in &= in - 1) {
+        const int i = __shfl_sync(0xffffffffu, x_at, __ffs(in) - 1) - lane * 16;
+#pragma unroll
+        for (int k = 0; k < 16; ++k)
+          if (k == i) x[k] = 0.f;
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = Two{x[i], 0.f};
+}
+__device__ __forceinline__ Two sum16(const Two (&v)[16]) {
+  Two s[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) s[i] = add(v[2 * i], v[2 * i + 1]);
+#pragma unroll
+  for (int n = 4; n > 0; n /= 2)
+#pragma unroll
+    for (int i = 0; i < n; ++i) s[i] = add(s[i], s[i + n]);
+  return s[0];
+}
+
 __global__ void __launch_bounds__(kThreads) verify_kernel(const __grid_constant__ VerifyParams p) {
   pdl_launch_dependents();
   pdl_wait();
   __shared__ Shared sh;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int b = blockIdx.x / p.size, rank = blockIdx.x % p.size;
+  const float u_next = p.u_next[b];
   const SeqRows sr = seq_rows(p.cu, b, p.rows);
   const bool bad = seq_bad(p.cu, b, p.rows) || sr.n > kMaxNodes;
   if (bad && tid == 0 && rank == 0) record(p.status, kStatusInvalidArg);
@@ -117,178 +173,195 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const __grid_constant_
     }
     return;
   }
-  const bool wide_p = (reinterpret_cast<uintptr_t>(p.target) & 15) == 0 && p.target_row % 4 == 0;
-  const bool wide_q = p.draft && (reinterpret_cast<uintptr_t>(p.draft) & 15) == 0 && p.draft_row % 4 == 0;
-  if (tid < n) {
-    const int row = sr.lo + tid;
-    int up = p.parents ? p.parents[row] : tid - 1;
-    int x = p.tokens[row];
-    // a parent behind its child, or a token that is none, takes the node out of the tree
-    if (up >= tid || (tid > 0 && up >= 0 && (x < 0 || x >= p.vocab))) {
-      record(p.status, kStatusInvalidArg);
-      up = -1;
-    }
-    sh.parent[tid] = up;
-    sh.token[tid] = x;
-    sh.u[tid] = p.u[row];
-    if (tid > 0 && up >= 0) {
-      sh.p[tid] = p.target[(sr.lo + up) * p.target_row + x];
-      sh.q[tid] = p.draft ? p.draft[(sr.lo + up) * p.draft_row + x] : 1.f;
-    }
-  }
-  __syncthreads();
-
-  int passes = 0;
   const int segs = (p.vocab + kSeg - 1) / kSeg;
   const int per = (segs + p.size - 1) / p.size;  // segments of a CTA, at most kCtaSegs
   const int s0 = min(segs, rank * per), s1 = min(segs, s0 + per);
-  // sums over the cluster of max(0, p - C q) at node cur, less the tokens gone; the CTA's segments in sh.sums
-  auto value = [&](float x, float y, Two C) { return C.hi > 0.f ? left_of(x, y, C) : Two{x, 0.f}; };
-  auto lane_values = [&](int cur, Two C, int n_gone, int seg, float (&x)[16], float (&y)[16]) {
-    const int at = seg * kSeg + lane * 16;
-    load16(p.target + (sr.lo + cur) * p.target_row, at, p.vocab, wide_p, x);
-    if (C.hi > 0.f) load16(p.draft + (sr.lo + cur) * p.draft_row, at, p.vocab, wide_q, y);
-    for (int g = 0; g < n_gone; ++g) {
-      const int i = sh.gone[g] - at;
-      if (sh.gone[g] / kSeg == seg) {
+  const bool wide_p = (reinterpret_cast<uintptr_t>(p.target) & 15) == 0 && p.target_row % 4 == 0;
+  const bool wide_q = p.draft && (reinterpret_cast<uintptr_t>(p.draft) & 15) == 0 && p.draft_row % 4 == 0;
+  auto row_of = [&](int cur) {
+    return Row{p.target + (sr.lo + cur) * p.target_row, p.draft ? p.draft + (sr.lo + cur) * p.draft_row : nullptr, wide_p, wide_q};
+  };
+  // A pass: the segments' sums to sh.sums, all warps.
+  auto pass = [&](const Order& o) {
+    const Row row = row_of(o.cur);
+    for (int seg = s0 + warp; seg < s1; seg += kWarps) {
+      Two v[16];
+      left_values(row, o, sh.gone, p.vocab, seg, lane, v);
+      Two s = sum16(v);
 #pragma unroll
-        for (int k = 0; k < 16; ++k)
-          if (k == i) x[k] = 0.f;
-      }
+      for (int k = 16; k > 0; k >>= 1)
+        s = add(s, Two{__shfl_xor_sync(0xffffffffu, s.hi, k), __shfl_xor_sync(0xffffffffu, s.lo, k)});
+      if (lane == 0) sh.sums[seg - s0] = s;
     }
   };
-  auto pass = [&](int cur, Two C, int n_gone) {
-    __syncthreads();  // sh.gone is written, the last pass's sums are read
-    double mine = 0.0;
-    for (int seg = s0 + warp; seg < s1; seg += kWarps) {
-      float x[16], y[16];
-      lane_values(cur, C, n_gone, seg, x, y);
-      Two s = value(x[0], y[0], C);
-#pragma unroll
-      for (int i = 1; i < 16; ++i) s = add(s, value(x[i], y[i], C));
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1)
-        s = add(s, Two{__shfl_xor_sync(0xffffffffu, s.hi, o), __shfl_xor_sync(0xffffffffu, s.lo, o)});
-      const double d = (double)s.hi + (double)s.lo;
-      mine += d;
-      if (lane == 0) sh.sums[seg - s0] = d;
-    }
-    if (lane == 0) sh.warp_sums[warp] = mine;
+  const int each = (s1 - s0 + 31) / 32;  // of the CTA's segments, a lane of warp 0 has `each`
+  int passes = 0;
+  double upto = 0.0, own = 0.0;          // sums up to and of the lane's segments
+  double cta_upto = 0.0, cta_own = 0.0;  // ... of CTA `lane`
+  // Their sum over the cluster, in warp 0 (which has the sums above too).
+  auto total = [&] {
     __syncthreads();
-    if (tid == 0) {
-      double t = 0.0;
-      for (int w = 0; w < kWarps; ++w) t += sh.warp_sums[w];
-      sh.total[passes & 1] = t;
+    if (warp == 0) {
+      own = 0.0;
+      for (int k = lane * each; k < min((lane + 1) * each, s1 - s0); ++k) own += value_of(sh.sums[k]);
+      upto = scan(own, lane);
+      if (lane == 31) sh.total[passes & 1] = upto;
     }
-    __syncthreads();
+    __syncwarp();
     cluster_sync_all();
     double all = 0.0;
-    for (int r = 0; r < p.size; ++r) all += ld_dsmem_f64(map_shared_rank(smem_u32(&sh.total[passes & 1]), r));
+    if (warp == 0) {
+      cta_own = lane < p.size ? ld_dsmem_f64(map_shared_rank(smem_u32(&sh.total[passes & 1]), lane)) : 0.0;
+      cta_upto = scan(cta_own, lane);
+      all = __shfl_sync(0xffffffffu, cta_upto, 31);
+    }
     ++passes;
     return all;
   };
 
-  // every thread walks alike
-  int cur = 0, kept = 1, n_gone = 0;
+  if (warp != 0) {
+    for (;;) {
+      __syncthreads();  // an order
+      const Order o = sh.order;
+      if (o.done) break;
+      pass(o);
+      total();
+    }
+    __syncwarp();
+    cluster_arrive();
+    cluster_wait();
+    return;
+  }
+  // ---------------- warp 0
+  int parent[2], token[2];
+  float u[2], px[2], qx[2];  // px, qx: of the candidate's token at its parent
+  bool gone[2] = {false, false};
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int i = lane + 32 * h;
+    parent[h] = -1, token[h] = -1, u[h] = px[h] = qx[h] = 0.f;
+    if (i < n) {
+      parent[h] = p.parents ? p.parents[sr.lo + i] : i - 1;
+      token[h] = p.tokens[sr.lo + i];
+      u[h] = p.u[sr.lo + i];
+    }
+  }
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int i = lane + 32 * h;
+    // a parent behind its child, or a token that is none, takes the node out of the tree
+    if (i < n && (parent[h] >= i || (i > 0 && parent[h] >= 0 && (token[h] < 0 || token[h] >= p.vocab)))) {
+      record(p.status, kStatusInvalidArg);
+      parent[h] = -1;
+    }
+    if (i > 0 && parent[h] >= 0) {
+      px[h] = p.target[(sr.lo + parent[h]) * p.target_row + token[h]];
+      qx[h] = p.draft ? p.draft[(sr.lo + parent[h]) * p.draft_row + token[h]] : 1.f;
+    }
+  }
+  __syncwarp();
+  auto pick = [&](auto (&x)[2], int i) { return __shfl_sync(0xffffffffu, i < 32 ? x[0] : x[1], i & 31); };
+  Order o{0, 0, 0, {0.f, 0.f}};
   double c = 1.0, C = 0.0, sum = 0.0;
   bool summed = false;
-  auto two = [](double x) {
-    const float hi = (float)x;
-    return Two{hi, (float)(x - (double)hi)};
+  auto passed = [&] {  // an order and its sum
+    if (lane == 0) sh.order = o;
+    __syncthreads();
+    pass(o);
+    return total();
   };
-  if (rank == 0 && tid == 0) p.path[sr.lo] = 0;
-  for (int i = 1; i < n; ++i) {
-    if (sh.parent[i] != cur) continue;
-    const float px = sh.p[i], qx = sh.q[i];
-    double here;
-    if (p.draft) {
-      here = fmax(0.0, (double)px - C * (double)qx);
-    } else {
-      here = px;
-      for (int g = 0; g < n_gone; ++g)
-        if (sh.gone[g] == sh.token[i]) here = 0.0;
-    }
-    if ((double)sh.u[i] * c * (double)qx < here && here > 0.0) {
-      cur = i;
-      if (rank == 0 && tid == 0) p.path[sr.lo + kept] = i;
-      ++kept;
-      c = 1.0, C = 0.0, n_gone = 0, summed = false;
-    } else if (p.draft) {
-      C += c;
-      c = sum = pass(cur, two(C), 0);
-      summed = true;
-    } else {
-      c -= here;
-      __syncthreads();  // the others have read gone
-      if (tid == 0) sh.gone[n_gone] = sh.token[i];
-      ++n_gone;
-      __syncthreads();
-    }
-  }
-  if (!summed) sum = pass(cur, two(C), n_gone);
-  if (!(sum > 0.0) && (C > 0.0 || n_gone > 0)) {  // nothing is left: the target's own distribution
-    C = 0.0, n_gone = 0;
-    sum = pass(cur, two(0.0), 0);
-  }
-  if (rank == 0) {
-    if (tid == 0) p.counts[b] = kept;
-    for (int i = kept + tid; i < n; i += kThreads) p.path[sr.lo + i] = -1;
-  }
-  // The next token: the CTA, then the segment, then the value where the running sum passes u * sum. Where
-  // none does (u = 1, or a NaN) it is the last one.
-  const double want = (double)p.u_next[b] * sum;
-  double before = 0.0;
-  int owner = p.size - 1;
-  for (int r = 0; r < p.size; ++r) {
-    const double t = ld_dsmem_f64(map_shared_rank(smem_u32(&sh.total[(passes - 1) & 1]), r));
-    if (before + t > want) {
-      owner = r;
-      break;
-    }
-    if (r + 1 < p.size) before += t;
-  }
-  cluster_sync_all();  // no CTA leaves while its sums are read
-  if (rank != owner || warp != 0) return;
-  int seg = max(s1 - 1, s0);
-  for (int k = s0; k < s1; ++k) {
-    const double t = sh.sums[k - s0];
-    if (before + t > want) {
-      seg = k;
-      break;
-    }
-    if (k + 1 < s1) before += t;
-  }
-  float x[16], y[16];
-  lane_values(cur, two(C), n_gone, seg, x, y);
-  double own = 0.0;
-#pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const Two v = value(x[i], y[i], two(C));
-    own += (double)v.hi + (double)v.lo;
-  }
-  double upto = own;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const double t = __shfl_up_sync(0xffffffffu, upto, o);
-    if (lane >= o) upto += t;
-  }
-  const unsigned past = __ballot_sync(0xffffffffu, before + upto > want);
-  const int at = past ? __ffs(past) - 1 : 31;
-  if (lane == at) {
-    double run = before + upto - own;
-    int pick = min(p.vocab, seg * kSeg + lane * 16 + 16) - 1;
-    bool found = false;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const Two v = value(x[i], y[i], two(C));
-      run += (double)v.hi + (double)v.lo;
-      if (!found && run > want) {
-        found = true;
-        pick = seg * kSeg + lane * 16 + i;
+  int kept = 1;
+  if (rank == 0 && lane == 0) p.path[sr.lo] = 0;
+  for (;;) {
+    // the current node's children in order
+    unsigned long long left = __ballot_sync(0xffffffffu, lane > 0 && parent[0] == o.cur) |
+                              (unsigned long long)__ballot_sync(0xffffffffu, parent[1] == o.cur) << 32;
+    int taken = -1;
+    for (; left && taken < 0; left &= left - 1) {
+      const int i = __ffsll((long long)left) - 1;
+      const int x = pick(token, i);
+      const double xp = pick(px, i), xq = pick(qx, i), xu = pick(u, i);
+      double here = xp;
+      if (p.draft) {
+        here = fmax(0.0, xp - C * xq);
+      } else if (__any_sync(0xffffffffu, (gone[0] && token[0] == x) || (gone[1] && token[1] == x))) {
+        here = 0.0;
+      }
+      if (here > 0.0 && xu * c * xq < here) {
+        taken = i;
+      } else if (p.draft) {
+        C += c;
+        o.C = two_of(C);
+        c = sum = passed();
+        summed = true;
+      } else {
+        c -= here;
+        gone[0] |= lane == i;
+        gone[1] |= lane + 32 == i;
+        if (lane == 0) sh.gone[o.n_gone] = x;
+        ++o.n_gone;
       }
     }
-    p.next[b] = min(max(pick, 0), p.vocab - 1);
+    if (taken < 0) break;
+    if (rank == 0 && lane == 0) p.path[sr.lo + kept] = taken;
+    ++kept;
+    o = Order{taken, 0, 0, {0.f, 0.f}};
+    gone[0] = gone[1] = false;
+    c = 1.0, C = 0.0;
+    summed = false;
   }
+  if (!summed) sum = passed();
+  if (!(sum > 0.0) && (C > 0.0 || o.n_gone > 0)) {  // nothing is left: the target's own distribution
+    o.C = {0.f, 0.f};
+    o.n_gone = 0;
+    sum = passed();
+  }
+  if (lane == 0) sh.order.done = 1;
+  __syncthreads();
+  cluster_arrive();  // the other CTAs' sums have been read
+  if (rank == 0) {
+    if (lane == 0) p.counts[b] = kept;
+    for (int i = kept + lane; i < n; i += 32) p.path[sr.lo + i] = -1;
+  }
+  // The next token: the CTA, then the segment, then the value where the running sum passes u * sum. Where
+  // none does (a NaN) it is the last one.
+  const double want = (double)u_next * sum;
+  const unsigned ctas = __ballot_sync(0xffffffffu, lane < p.size && cta_upto > want);
+  const int owner = ctas ? __ffs(ctas) - 1 : p.size - 1;
+  if (rank == owner) {
+    const double before = __shfl_sync(0xffffffffu, cta_upto - cta_own, owner);
+    const unsigned lanes = __ballot_sync(0xffffffffu, before + upto > want);
+    int seg = max(s1 - 1, s0);
+    double run = before + __shfl_sync(0xffffffffu, upto, 31);
+    if (lanes) {
+      const int l = __ffs(lanes) - 1;
+      run = before + __shfl_sync(0xffffffffu, upto - own, l);
+      seg = s0 + l * each;
+      for (const int last = min(s0 + (l + 1) * each, s1) - 1; seg < last; ++seg) {
+        const double next = run + value_of(sh.sums[seg - s0]);
+        if (next > want) break;
+        run = next;
+      }
+    }
+    Two v[16];
+    left_values(row_of(o.cur), o, sh.gone, p.vocab, seg, lane, v);
+    const double mine = value_of(sum16(v)), here = scan(mine, lane);
+    const unsigned past = __ballot_sync(0xffffffffu, run + here > want);
+    const int at = past ? __ffs(past) - 1 : 31;
+    run += __shfl_sync(0xffffffffu, here - mine, at);
+    Two one{0.f, 0.f};  // lane i < 16: value i of that lane
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const Two x{__shfl_sync(0xffffffffu, v[i].hi, at), __shfl_sync(0xffffffffu, v[i].lo, at)};
+      if (lane == i) one = x;
+    }
+    const double here1 = scan(value_of(one), lane);
+    const unsigned found = __ballot_sync(0xffffffffu, lane < 16 && run + here1 > want) & 0xffffu;
+    const int first = seg * kSeg + at * 16;
+    if (lane == 0) p.next[b] = min(max(found ? first + __ffs(found) - 1 : min(first + 15, p.vocab - 1), 0), p.vocab - 1);
+  }
+  __syncwarp();
+  cluster_wait();
 }
 
 }  // namespace
