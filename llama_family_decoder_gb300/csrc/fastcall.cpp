@@ -18,6 +18,9 @@
 
 namespace {
 
+// the keys of a paged cache, made once (PyDict_GetItemString makes a string each time)
+PyObject *key_k, *key_v, *key_pages, *key_lens;
+
 struct Block {
   blk_handle* h;
   int64_t H, Hkv, d;
@@ -86,17 +89,17 @@ struct Call {
   at::Tensor scratch(size_t bytes) const {
     return fresh({static_cast<int64_t>(bytes)}, at::kByte);
   }
-  blk_paged_cache paged(PyObject* o, int64_t& batch) {
+  // like: a cache whose page table and lens were looked at already, or null
+  blk_paged_cache paged(PyObject* o, int64_t& batch, PyObject* like = nullptr, const blk_paged_cache* its = nullptr) {
     blk_paged_cache c{};
     if (!ok || !PyDict_Check(o)) {
       ok = false;
       return c;
     }
     void** const to[2] = {&c.k, &c.v};
-    const char* const names[2] = {"k", "v"};
     int64_t n_pages = -1, size = -1;
     for (int i = 0; i < 2; ++i) {
-      PyObject* x = PyDict_GetItemString(o, names[i]);
+      PyObject* x = PyDict_GetItem(o, i ? key_v : key_k);
       const at::Tensor* t = x ? tensor(x, b->type) : fail();
       if (!t) return c;
       ok = t->dim() == 4 && t->is_contiguous() && (n_pages < 0 || t->size(0) == n_pages) && t->size(1) == b->Hkv &&
@@ -106,17 +109,24 @@ struct Call {
       size = t->size(2);
       *to[i] = t->data_ptr();
     }
-    PyObject *x = PyDict_GetItemString(o, "pages"), *y = PyDict_GetItemString(o, "lens");
+    PyObject *x = PyDict_GetItem(o, key_pages), *y = PyDict_GetItem(o, key_lens);
+    ok = n_pages <= INT32_MAX && size <= INT32_MAX;
+    c.n_pages = static_cast<int>(n_pages);
+    c.page_size = static_cast<int>(size);
+    if (like && x && y && x == PyDict_GetItem(like, key_pages) && y == PyDict_GetItem(like, key_lens)) {
+      c.pages = its->pages;
+      c.lens = its->lens;
+      c.max_pages = its->max_pages;
+      return c;
+    }
     const at::Tensor *p = x ? tensor(x, at::kInt) : fail(), *l = y ? tensor(y, at::kInt) : fail();
     if (!p || !l) return c;
     ok = p->dim() == 2 && p->is_contiguous() && l->dim() == 1 && l->is_contiguous() && l->size(0) == p->size(0) &&
-         n_pages <= INT32_MAX && size <= INT32_MAX && p->size(0) <= INT32_MAX && p->size(1) <= INT32_MAX;
+         p->size(0) <= INT32_MAX && p->size(1) <= INT32_MAX;
     if (!ok) return c;
     batch = p->size(0);
     c.pages = static_cast<const int*>(p->data_ptr());
     c.lens = static_cast<int*>(l->data_ptr());
-    c.n_pages = static_cast<int>(n_pages);
-    c.page_size = static_cast<int>(size);
     c.max_pages = static_cast<int>(p->size(1));
     return c;
   }
@@ -471,8 +481,9 @@ PyObject* paged_keep(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
     const int n_caches = static_cast<int>(PyList_GET_SIZE(a[1]));
     int64_t batch = -1, n = 0;
     for (int i = 0; i < n_caches; ++i) {
-      int64_t its = -1;
-      caches[i] = c.paged(PyList_GET_ITEM(a[1], i), its);
+      int64_t its = batch;
+      caches[i] = i ? c.paged(PyList_GET_ITEM(a[1], i), its, PyList_GET_ITEM(a[1], 0), caches)
+                    : c.paged(PyList_GET_ITEM(a[1], 0), its);
       if (!c.ok || (i && its != batch)) return none();
       batch = its;
     }
@@ -516,4 +527,10 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_fastcall", nullptr, -1, methods, 
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__fastcall() { return PyModule_Create(&module); }
+PyMODINIT_FUNC PyInit__fastcall() {
+  key_k = PyUnicode_InternFromString("k");
+  key_v = PyUnicode_InternFromString("v");
+  key_pages = PyUnicode_InternFromString("pages");
+  key_lens = PyUnicode_InternFromString("lens");
+  return key_k && key_v && key_pages && key_lens ? PyModule_Create(&module) : nullptr;
+}

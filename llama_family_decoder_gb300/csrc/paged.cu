@@ -219,7 +219,7 @@ cudaError_t launch_append(AppendParams p, bool inter, int num_sms, cudaStream_t 
 // of one (layer, K or V, head) at a time, eight of them loaded before any of the eight is stored:
 // path rises, so that no later row's source is behind an earlier row's place. The lengths are written
 // once every CTA of the cluster has read them.
-constexpr int kKeepThreads = 256;
+constexpr int kKeepThreads = 512;
 constexpr int kKeepRows = 128;  // path entries looked up at a time
 struct KeepParams {
   void* kv[2 * kKeepLayers];  // k, v of each layer
@@ -230,7 +230,7 @@ struct KeepParams {
   DevStatus* status;
 };
 
-__global__ void __launch_bounds__(kKeepThreads) paged_keep_kernel(const __grid_constant__ KeepParams p, int size) {
+__global__ void __launch_bounds__(kKeepThreads, 2) paged_keep_kernel(const __grid_constant__ KeepParams p, int size) {
   pdl_launch_dependents();
   pdl_wait();
   __shared__ long long from[kKeepRows], to[kKeepRows];  // rows of head 0; from < 0: nothing to move

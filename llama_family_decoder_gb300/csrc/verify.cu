@@ -155,7 +155,7 @@ __device__ __forceinline__ Two sum16(const Two (&v)[16]) {
   return s[0];
 }
 
-__global__ void __launch_bounds__(kThreads) verify_kernel(const __grid_constant__ VerifyParams p) {
+__global__ void __launch_bounds__(kThreads, 2) verify_kernel(const __grid_constant__ VerifyParams p) {
   pdl_launch_dependents();
   pdl_wait();
   __shared__ Shared sh;
