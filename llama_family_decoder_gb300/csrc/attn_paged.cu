@@ -40,6 +40,7 @@ constexpr int kQSub = kBQ * 128;       // one 64-channel half of a slot's querie
 constexpr int kQBytes = 2 * kQSub;
 constexpr int kKVSub = kBK * 128;      // one 64-channel half of a K or V tile
 constexpr int kStageBytes = 4 * kKVSub;
+constexpr int kMaxCluster = 16;
 constexpr int kClusterTiles = 20;      // a CTA's share of tiles up to which clusters of ragged sequences pay
 constexpr float kRescaleLog2 = 8.0f;
 constexpr float kScaleLog2 = 1.4426950408889634f * 0.08838834764831845f;  // log2(e) / sqrt(128)
@@ -299,22 +300,25 @@ __device__ __forceinline__ float2 ld_dsmem_f2(uint32_t addr) {
 
 // ------------------------------------------------------------------ the kernel
 
-template <int NS>
+// SPLIT (with clusters): two slots of the same rows, which take the tiles of keys in turn.
+template <int NS, bool SPLIT = false>
 struct Cfg {
-  static constexpr int kStages = NS == 1 ? 6 : 5;
+  static constexpr int kQueries = (SPLIT ? 1 : NS) * kQBytes;
+  static constexpr int kStages = kQueries == kQBytes ? 6 : 5;
   static constexpr int kThreads = 128 + 128 * NS;
   static constexpr int kBars = 2 * kStages + 10 * NS;
-  static constexpr int kSmem = 1024 + NS * kQBytes + kStages * kStageBytes + kBars * 8 + 8 + sizeof(Walk);
+  static constexpr int kSmem = 1024 + kQueries + kStages * kStageBytes + kBars * 8 + 8 + sizeof(Walk);
   static_assert(kSmem <= 227 * 1024, "shared memory");
 };
 
-template <int NS, bool CL>
-__global__ void __launch_bounds__(Cfg<NS>::kThreads, 1) attn_paged_kernel(const __grid_constant__ AttnParams p) {
-  typedef Cfg<NS> C;
+template <int NS, bool CL, bool SPLIT>
+__global__ void __launch_bounds__(Cfg<NS, SPLIT>::kThreads, 1) attn_paged_kernel(const __grid_constant__ AttnParams p) {
+  static_assert(!SPLIT || (CL && NS == 2), "two slots of a cluster's CTA");
+  typedef Cfg<NS, SPLIT> C;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* const smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* const sQ = smem;
-  uint8_t* const ring = smem + NS * kQBytes;
+  uint8_t* const ring = smem + C::kQueries;
   uint64_t* const bars = reinterpret_cast<uint64_t*>(ring + C::kStages * kStageBytes);
   uint32_t* const tmem_holder = reinterpret_cast<uint32_t*>(bars + C::kBars);
   volatile int* const abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
@@ -338,7 +342,7 @@ __global__ void __launch_bounds__(Cfg<NS>::kThreads, 1) attn_paged_kernel(const 
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::kStages; ++s) {
       mbar_init(full(s), 1);
-      mbar_init(empty(s), NS);
+      mbar_init(empty(s), SPLIT ? 1 : NS);
     }
     for (int g = 0; g < NS; ++g) {
       mbar_init(q_full(g), 1);
@@ -457,21 +461,25 @@ __global__ void __launch_bounds__(Cfg<NS>::kThreads, 1) attn_paged_kernel(const 
       const int g = warp - 1;
       constexpr uint32_t idesc_s = idesc_bf16_f32(kBQ, kBK);
       constexpr uint32_t idesc_pv = idesc_bf16_f32(kBQ, kD) | (1u << 16);  // B (V) is MN-major
-      const uint64_t dq = smem_desc_sw128(smem_u32(sQ + g * kQBytes));
+      const int rows = SPLIT ? 0 : g;  // the queries' slot
+      const uint64_t dq = smem_desc_sw128(smem_u32(sQ + rows * kQBytes));
       const uint64_t dk = smem_desc_sw128(smem_u32(ring));
       const uint64_t dv = smem_desc_sw128_mn(smem_u32(ring + 2 * kKVSub), kKVSub, 1024);
       const uint32_t s_tmem = tmem + 256 * g, o_tmem = tmem + 256 * g + 128;
+      constexpr int kStep = SPLIT ? 2 : 1;  // from one of the slot's tiles to the next
       int J = 0, A = 0, units = 0;  // tiles of the CTA and of this slot, and its units
       bool failed = false;
       for (Walk w = *begin; w.on() && !failed; w.next(p)) {
-        const int n = w.j1 - w.j0;
-        if (!w.has(p, g)) {  // nothing for this slot: the stages go back
+        const int all = w.j1 - w.j0, n = SPLIT ? (all + 1 - g) / 2 : all;
+        if (SPLIT && n == 0) break;  // (a cluster's CTA has one unit)
+        if (!w.has(p, rows)) {  // nothing for this slot: the stages go back
           for (int j = 0; j < n && !failed; ++j, ++J) {
             if (!mbar_wait(full(J % C::kStages), (J / C::kStages) & 1, budget, abort_flag)) failed = true;
             else mbar_arrive(empty(J % C::kStages));
           }
           continue;
         }
+        if constexpr (SPLIT) J = g;
         auto issue_s = [&](int Jn, int An) {
           const int st = Jn % C::kStages;
           if (!mbar_wait(full(st), (Jn / C::kStages) & 1, budget, abort_flag)) return false;
@@ -485,14 +493,14 @@ __global__ void __launch_bounds__(Cfg<NS>::kThreads, 1) attn_paged_kernel(const 
           mma_issued = true;
           return true;
         };
-        if (!mbar_wait(q_full(g), units & 1, budget, abort_flag) || !issue_s(J, A)) {
+        if (!mbar_wait(q_full(rows), units & 1, budget, abort_flag) || !issue_s(J, A)) {
           failed = true;
           break;
         }
-        for (int j = 0; j < n; ++j, ++J, ++A) {
+        for (int j = 0; j < n; ++j, J += kStep, ++A) {
           // the next scores first: they are under way while the softmax works on these. Their buffer's
           // P has been read: its product was issued before.
-          if (j + 1 < n && !issue_s(J + 1, A + 1)) {
+          if (j + 1 < n && !issue_s(J + kStep, A + 1)) {
             failed = true;
             break;
           }
@@ -528,7 +536,7 @@ __global__ void __launch_bounds__(Cfg<NS>::kThreads, 1) attn_paged_kernel(const 
       bool failed = false;
       for (Walk w = *begin; w.on() && !failed; w.next(p)) {
 #pragma unroll
-        for (int g = 0; g < NS; ++g) {
+        for (int g = 0; g < (SPLIT ? 1 : NS); ++g) {
           const int node0 = w.node0(p, g);
           if (failed || !w.has(p, g)) continue;
           if (units[g] > 0 && !mbar_wait(q_free(g), (units[g] - 1) & 1, budget, abort_flag)) {
@@ -560,11 +568,14 @@ __global__ void __launch_bounds__(Cfg<NS>::kThreads, 1) attn_paged_kernel(const 
     int J = 0, A = 0, units = 0, part = 2 * blockIdx.x;
     bool failed = false;
     for (Walk w = *begin; w.on() && !failed; w.next(p), part = 2 * blockIdx.x + 1) {
-      const int n = w.j1 - w.j0, node0 = w.node0(p, g);
-      if (!w.has(p, g)) {
+      const int rows = SPLIT ? 0 : g, all = w.j1 - w.j0;
+      const int n = SPLIT ? (all + 1 - g) / 2 : all, node0 = w.node0(p, rows);
+      if (SPLIT && n == 0) break;  // (a cluster's CTA has one unit)
+      if (!w.has(p, rows)) {
         J += n;
         continue;
       }
+      if constexpr (SPLIT) J = g;
       const int node = node0 + node_of_row;
       const bool valid = node_of_row < p.tq && node < w.seq.n;
       const bool live = __any_sync(0xffffffffu, valid);
@@ -591,8 +602,9 @@ __global__ void __launch_bounds__(Cfg<NS>::kThreads, 1) attn_paged_kernel(const 
       const int plain_lo = p.window > 0 ? len + last - p.window + 1 : 0;
       const int plain_hi = (p.parents ? len : len + node0 + 1) - kBK;
       float m_ref = -INFINITY, l = 0.f;
-      for (int j = 0; j < n; ++j, ++J, ++A) {
-        const int n0 = (w.keys.tile0() + w.j0 + j) * kBK;
+      constexpr int kStep = SPLIT ? 2 : 1;
+      for (int j = 0; j < n; ++j, J += kStep, ++A) {
+        const int n0 = (w.keys.tile0() + w.j0 + (SPLIT ? J : j)) * kBK;
         if (!__all_sync(0xffffffffu, mbar_wait(s_full(g, A & 1), (A >> 1) & 1, budget, abort_flag))) {
           failed = true;
           break;
@@ -775,7 +787,7 @@ __global__ void __launch_bounds__(Cfg<NS>::kThreads, 1) attn_paged_kernel(const 
     // the products have read the queries and the ring: a share's sums and outputs take their place
     tc_fence_after();
     const int g = (warp - 4) >> 2, r = (warp & 3) * 32 + lane;
-    reinterpret_cast<float2*>(sQ + g * kQBytes)[r] = share;
+    reinterpret_cast<float2*>(sQ)[g * kBQ + r] = share;
     if (share_live && !*abort_flag) {
       const uint32_t o_taddr = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + 256 * g + 128;
 #pragma unroll 1
@@ -803,25 +815,25 @@ __global__ void __launch_bounds__(Cfg<NS>::kThreads, 1) attn_paged_kernel(const 
     cluster_sync_all();
     Walk w = *begin;
     if (warp >= 4 && w.t < units_of(p, w.seq)) {
-      const int rank = cluster_ctarank();
-      for (int i = rank * 4 * NS + warp - 4; i < NS * (kBQ / 32) * (kD / 4); i += p.cluster * 4 * NS) {
+      constexpr int kRowSlots = SPLIT ? 1 : NS, kParts = SPLIT ? 2 : 1;  // parts of a CTA
+      const int rank = cluster_ctarank(), parts = p.cluster * kParts;
+      for (int i = rank * 4 * NS + warp - 4; i < kRowSlots * (kBQ / 32) * (kD / 4); i += p.cluster * 4 * NS) {
         const int ch = i % (kD / 4), quarter = i / (kD / 4) % (kBQ / 32), g = i / (kD / 4) / (kBQ / 32);
         const int r = quarter * 32 + lane, nd = r / p.G, node = w.node0(p, g) + nd;
         const bool valid = nd < p.tq && node < w.seq.n;
         if (!__any_sync(0xffffffffu, valid)) continue;
-        const uint32_t at_ml = smem_u32(sQ + g * kQBytes) + 8 * r;
-        const uint32_t at_o = smem_u32(ring) + (((g * (kD / 4) + ch) * kBQ + r) << 4);
         Joined x;
-        for (int k0 = 0; k0 < p.cluster; k0 += 8) {
+        for (int k0 = 0; k0 < parts; k0 += 8) {
           float2 ml[8];
           float4 a[8];
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
             ml[j] = make_float2(-INFINITY, 0.f);
             a[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (k0 + j < p.cluster) {
-              ml[j] = ld_dsmem_f2(map_shared_rank(at_ml, k0 + j));
-              a[j] = ld_dsmem_f4(map_shared_rank(at_o, k0 + j));
+            if (k0 + j < parts) {
+              const int cta = (k0 + j) / kParts, slot = SPLIT ? (k0 + j) % kParts : g;
+              ml[j] = ld_dsmem_f2(map_shared_rank(smem_u32(sQ) + 8 * (slot * kBQ + r), cta));
+              a[j] = ld_dsmem_f4(map_shared_rank(smem_u32(ring) + (((slot * (kD / 4) + ch) * kBQ + r) << 4), cta));
             }
           }
           x.take(ml, a);
@@ -890,20 +902,19 @@ struct Plan {
 };
 
 // Clusters of `size` CTAs of the kernel that are resident at once, 0 if it cannot be launched so; asked once per device.
-template <int NS>
+template <int NS, bool SPLIT>
 int resident_clusters(int size) {
-  static std::atomic<int> known[64][5];
-  int dev = 0, lg = 0;
+  static std::atomic<int> known[64][kMaxCluster + 1];
+  int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
-  while ((1 << lg) < size) ++lg;
-  const int was = known[dev][lg].load(std::memory_order_relaxed);
+  const int was = known[dev][size].load(std::memory_order_relaxed);
   if (was != 0) return was - 1;
-  const auto kernel = attn_paged_kernel<NS, true>;
+  const auto kernel = attn_paged_kernel<NS, true, SPLIT>;
   int n = 0;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)size);
-  cfg.blockDim = dim3(Cfg<NS>::kThreads);
-  cfg.dynamicSmemBytes = Cfg<NS>::kSmem;
+  cfg.blockDim = dim3(Cfg<NS, SPLIT>::kThreads);
+  cfg.dynamicSmemBytes = Cfg<NS, SPLIT>::kSmem;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = (unsigned)size;
@@ -911,14 +922,14 @@ int resident_clusters(int size) {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   if (cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel), cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           Cfg<NS>::kSmem) != cudaSuccess ||
+                           Cfg<NS, SPLIT>::kSmem) != cudaSuccess ||
       cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel), cudaFuncAttributeNonPortableClusterSizeAllowed, 1) !=
           cudaSuccess ||
       cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) {
     cudaGetLastError();
     n = 0;
   }
-  known[dev][lg].store(n + 1, std::memory_order_relaxed);
+  known[dev][size].store(n + 1, std::memory_order_relaxed);
   return n;
 }
 
@@ -942,9 +953,9 @@ Plan plan_of(int rows, int B, int H, int Hkv, bool cu, bool tree, long long capa
   // Clusters: a unit each, its keys in equal shares, no list to add up and no second kernel.
   pl.cluster = 1;
   const long long units = (long long)B * Hkv * pl.units;
-  for (int size = 16; size > 1; size /= 2)
+  for (int size = kMaxCluster; size > 1; --size)
     if (units * size <= num_sms && (B == 1 || tiles <= kClusterTiles * size) &&
-        (pl.slots == 2 ? resident_clusters<2>(size) : resident_clusters<1>(size)) >= units) {
+        (pl.slots == 2 ? resident_clusters<2, false>(size) : resident_clusters<2, true>(size)) >= units) {
       pl.cluster = size;
       break;
     }
@@ -998,13 +1009,14 @@ cudaError_t launch_attn_paged(const HeadRows& q, const PagedCache& c, const Head
   p.status = st;
   p.wait_ns = wait_ns;
   const bool two = pl.slots == 2;
-  const int smem = two ? Cfg<2>::kSmem : Cfg<1>::kSmem, threads = two ? Cfg<2>::kThreads : Cfg<1>::kThreads;
   if (pl.cluster > 1)  // configured when the resident clusters were asked for
-    return launch_clusters(two ? attn_paged_kernel<2, true> : attn_paged_kernel<1, true>, B * Hkv * pl.units * pl.cluster,
-                           threads, smem, pl.cluster, s, p);
+    return launch_clusters(two ? attn_paged_kernel<2, true, false> : attn_paged_kernel<2, true, true>,
+                           B * Hkv * pl.units * pl.cluster, two ? Cfg<2>::kThreads : Cfg<2, true>::kThreads,
+                           two ? Cfg<2>::kSmem : Cfg<2, true>::kSmem, pl.cluster, s, p);
+  const int smem = two ? Cfg<2>::kSmem : Cfg<1>::kSmem, threads = two ? Cfg<2>::kThreads : Cfg<1>::kThreads;
   p.acc = static_cast<float*>(ws);
   p.ml = reinterpret_cast<float2*>(p.acc + (size_t)2 * pl.grid * pl.slots * kBQ * kD);
-  const auto kernel = two ? attn_paged_kernel<2, false> : attn_paged_kernel<1, false>;
+  const auto kernel = two ? attn_paged_kernel<2, false, false> : attn_paged_kernel<1, false, false>;
   static std::atomic<unsigned long long> configured[2];
   cudaError_t e = set_smem_limit_once(reinterpret_cast<const void*>(kernel), smem, configured[two]);
   if (e == cudaSuccess) e = launch_pdl(kernel, pl.grid, threads, smem, s, p);
