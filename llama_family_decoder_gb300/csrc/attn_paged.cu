@@ -791,22 +791,17 @@ __global__ void __launch_bounds__(Cfg<NS, SPLIT>::kThreads, 1) attn_paged_kernel
     if (share_live && !*abort_flag) {
       const uint32_t o_taddr = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + 256 * g + 128;
 #pragma unroll 1
-      for (int c = 0; c < kD; c += 16) {
-        float ov[16];
-        tmem_ld16(o_taddr + c, ov);
+      for (int c = 0; c < kD; c += 32) {
+        float ov[32];
+        tmem_ld16(o_taddr + c, *reinterpret_cast<float(*)[16]>(&ov[0]));
+        tmem_ld16(o_taddr + c + 16, *reinterpret_cast<float(*)[16]>(&ov[16]));
         tc_wait_ld();
 #pragma unroll
-        for (int i = 0; i < 16; i += 4)
+        for (int i = 0; i < 32; i += 4)
           reinterpret_cast<float4*>(ring)[(g * (kD / 4) + (c + i) / 4) * kBQ + r] = make_float4(ov[i], ov[i + 1], ov[i + 2], ov[i + 3]);
       }
     }
     tc_fence_before();
-  }
-  if constexpr (CL) __syncthreads();
-  if (warp == 1) {
-    __syncwarp();
-    tc_fence_after();
-    tmem_dealloc(tmem, kTmemCols);
   }
   if constexpr (CL) {
     // The shares of the cluster's CTAs joined in their order, as the second kernel does with parts: a thread
@@ -817,20 +812,21 @@ __global__ void __launch_bounds__(Cfg<NS, SPLIT>::kThreads, 1) attn_paged_kernel
     if (warp >= 4 && w.t < units_of(p, w.seq)) {
       constexpr int kRowSlots = SPLIT ? 1 : NS, kParts = SPLIT ? 2 : 1;  // parts of a CTA
       const int rank = cluster_ctarank(), parts = p.cluster * kParts;
-      for (int i = rank * 4 * NS + warp - 4; i < kRowSlots * (kBQ / 32) * (kD / 4); i += p.cluster * 4 * NS) {
+      for (int i = (warp - 4) * p.cluster + rank; i < kRowSlots * (kBQ / 32) * (kD / 4); i += p.cluster * 4 * NS) {
         const int ch = i % (kD / 4), quarter = i / (kD / 4) % (kBQ / 32), g = i / (kD / 4) / (kBQ / 32);
         const int r = quarter * 32 + lane, nd = r / p.G, node = w.node0(p, g) + nd;
         const bool valid = nd < p.tq && node < w.seq.n;
         if (!__any_sync(0xffffffffu, valid)) continue;
         Joined x;
-        for (int k0 = 0; k0 < parts; k0 += 8) {
-          float2 ml[8];
-          float4 a[8];
+        constexpr int kAtOnce = 12;
+        for (int k0 = 0; k0 < parts; k0 += kAtOnce) {
+          float2 ml[kAtOnce];
+          float4 a[kAtOnce];
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
+          for (int j = 0; j < kAtOnce; ++j) {
             ml[j] = make_float2(-INFINITY, 0.f);
             a[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (k0 + j < parts) {
+            if (valid && k0 + j < parts) {
               const int cta = (k0 + j) / kParts, slot = SPLIT ? (k0 + j) % kParts : g;
               ml[j] = ld_dsmem_f2(map_shared_rank(smem_u32(sQ) + 8 * (slot * kBQ + r), cta));
               a[j] = ld_dsmem_f4(map_shared_rank(smem_u32(ring) + (((slot * (kD / 4) + ch) * kBQ + r) << 4), cta));
@@ -843,6 +839,11 @@ __global__ void __launch_bounds__(Cfg<NS, SPLIT>::kThreads, 1) attn_paged_kernel
     }
     __syncwarp();
     cluster_sync_all();  // nobody leaves while its share may be read
+  }
+  if (warp == 1) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
   }
 }
 
