@@ -59,7 +59,7 @@ struct AttnParams {
   int box_shift;  // log2 of a box's rows: those of a page, at most 64
   int grid, min_tiles;
   int cluster;    // CTAs that share a unit, 1: no clusters
-  int units;      // ... units of a (sequence, KV head), at most
+  int single;     // no sequence has more than one unit of a KV head
   int unit_cost;  // what a unit counts for on the line besides its tiles, before them
   float2* ml;     // partial results [2 grid][slots][128]: (reference, sum)
   float* acc;     // ... [2 grid][slots][32][128][4]: four channels of each row side by side
@@ -127,12 +127,11 @@ __device__ __forceinline__ int head_cost(const AttnParams& p, const Seq& s) {  /
   return n;
 }
 
-// A CTA's stretch [lo, hi) of the line, and the sequence it begins in, whose own tiles begin at `base`.
+// A CTA's stretch [lo, hi) of the line, and the sequence it begins in, whose own tiles begin at `base`. per: the
+// stretches' length.
 struct Stretch {
   int lo, hi, base, b, per;
 };
-// By one warp. Stretch number `c`; an empty one (lo >= hi) if the line ends before. The line is shorter
-// than 2^31 (see plan_of).
 __device__ __forceinline__ int scan(int n, int lane) {
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -141,37 +140,55 @@ __device__ __forceinline__ int scan(int n, int lane) {
   }
   return n;
 }
+// Numbers of the sequences, 32 * kHeld of them looked up once, the others again where they are needed; by one warp.
+template <class F>
+struct PerSeq {
+  static constexpr int kHeld = 4;
+  F of;
+  int B, lane, held[kHeld];
+  __device__ __forceinline__ PerSeq(F f, int B_, int lane_) : of(f), B(B_), lane(lane_) {
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) held[i] = 32 * i < B ? number(32 * i + lane) : 0;
+  }
+  __device__ __forceinline__ int number(int b) const {
+    const int n = of(min(b, B - 1));  // without a branch: the loads of all are under way together
+    return b < B ? n : 0;
+  }
+  __device__ __forceinline__ int total() const {
+    int n = 0;
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) n += held[i];
+    for (int b = lane + 32 * kHeld; b < B; b += 32) n += number(b);
+    return (int)__reduce_add_sync(0xffffffffu, (unsigned)n);
+  }
+  // The sequence in whose share place x of the sum lies, and the sum before it; false: x is not below the sum.
+  __device__ __forceinline__ bool find(int x, int& b, int& before) const {
+    before = 0;
+    bool found = false;
+    auto look = [&](int b0, int n) {
+      const int upto = scan(n, lane);
+      const unsigned past = __ballot_sync(0xffffffffu, before + upto > x);
+      const int at = past ? __ffs(past) - 1 : 31;
+      b = b0 + at;
+      before += __shfl_sync(0xffffffffu, past ? upto - n : upto, at);
+      found = past != 0;
+    };
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i)
+      if (!found && 32 * i < B) look(32 * i, held[i]);
+    for (int b0 = 32 * kHeld; !found && b0 < B; b0 += 32) look(b0, number(b0 + lane));
+    return found;
+  }
+};
+// By one warp. Stretch number `c`; an empty one (lo >= hi) if the line ends before. The line is shorter
+// than 2^31 (see plan_of).
 __device__ __forceinline__ Stretch stretch_of(const AttnParams& p, int c, int lane) {
-  auto cost_of = [&](int b) { return b < p.B ? p.Hkv * head_cost(p, seq_of(p, b)) : 0; };
-  constexpr int kHeld = 4;  // 32 sequences each, looked up once
-  int held[kHeld], total = 0;
-#pragma unroll
-  for (int i = 0; i < kHeld; ++i) held[i] = cost_of(32 * i + lane);
-#pragma unroll
-  for (int i = 0; i < kHeld; ++i) total += held[i];
-  for (int b = lane + 32 * kHeld; b < p.B; b += 32) total += cost_of(b);
-  total = (int)__reduce_add_sync(0xffffffffu, (unsigned)total);
-  Stretch s;
-  s.per = max((int)(((unsigned)total + p.grid - 1) / p.grid), p.min_tiles);
+  const PerSeq costs([&](int b) { return p.Hkv * head_cost(p, seq_of(p, b)); }, p.B, lane);
+  const int total = costs.total();
+  Stretch s{0, 0, 0, 0, max((int)(((unsigned)total + p.grid - 1) / p.grid), p.min_tiles)};
   s.lo = (int)min((long long)total, (long long)c * s.per);
   s.hi = (int)min((long long)total, (long long)s.lo + s.per);
-  s.base = 0;
-  s.b = 0;
-  if (s.lo >= s.hi) return s;
-  bool found = false;
-  auto look = [&](int b0, int n) {  // whether the stretch begins in these 32 sequences
-    const int upto = scan(n, lane);
-    const unsigned past = __ballot_sync(0xffffffffu, s.base + upto > s.lo);
-    const int at = past ? __ffs(past) - 1 : 31;
-    s.b = b0 + at;
-    s.base += __shfl_sync(0xffffffffu, past ? upto - n : upto, at);
-    found = past != 0;
-  };
-#pragma unroll
-  for (int i = 0; i < kHeld; ++i)
-    if (!found) look(32 * i, held[i]);
-  for (int b0 = 32 * kHeld; !found && b0 < p.B; b0 += 32) look(b0, cost_of(b0 + lane));
-  if (!found) s.hi = s.lo;  // lengths that change meanwhile
+  if (s.lo < s.hi && !costs.find(s.lo, s.b, s.base)) s.hi = s.lo;  // lengths that change meanwhile
   return s;
 }
 
@@ -214,14 +231,23 @@ struct Walk {
     }
     part(p);
   }
-  // The share of CTA `rank` of a cluster of `size` that takes unit number u, or nothing.
-  __device__ __forceinline__ Walk(const AttnParams& p, int u, int rank, int size) {
-    left = j0 = j1 = tiles = at = 0;
-    t = u % p.units;
-    kvh = u / p.units % p.Hkv;
-    b = u / p.units / p.Hkv;
+  // The share of CTA `rank` of a cluster of `size` that takes unit number u, or nothing (seq.n = 0). By one warp.
+  __device__ __forceinline__ Walk(const AttnParams& p, int u, int rank, int size, int lane) {
+    left = j0 = j1 = tiles = at = b = kvh = t = 0;
+    seq = Seq{0, 0, 0};
+    int before = 0;
+    if (p.single) {
+      b = u / p.Hkv;
+      before = b * p.Hkv;
+    } else {
+      const PerSeq units([&](int x) { return p.Hkv * units_of(p, seq_of(p, x)); }, p.B, lane);
+      if (!units.find(u, b, before)) return;
+    }
     seq = seq_of(p, b);
-    if (t >= units_of(p, seq)) return;
+    const int n = units_of(p, seq);
+    if (n == 0) return;  // a sequence without rows
+    kvh = (u - before) / n;
+    t = u - before - kvh * n;
     unit(p);
     at = (int)((long long)tiles * rank / size);
     left = (int)((long long)tiles * (rank + 1) / size) - at;
@@ -372,7 +398,7 @@ __global__ void __launch_bounds__(Cfg<NS, SPLIT>::kThreads, 1) attn_paged_kernel
   pdl_launch_dependents();
   if (warp == 0) {
     if constexpr (CL) {
-      const Walk w(p, blockIdx.x / p.cluster, cluster_ctarank(), p.cluster);
+      const Walk w(p, blockIdx.x / p.cluster, cluster_ctarank(), p.cluster, lane);
       if (lane == 0) *begin = w;
     } else {
       const Walk w(p, stretch_of(p, blockIdx.x, lane));
@@ -805,36 +831,37 @@ __global__ void __launch_bounds__(Cfg<NS, SPLIT>::kThreads, 1) attn_paged_kernel
   }
   if constexpr (CL) {
     // The shares of the cluster's CTAs joined in their order, as the second kernel does with parts: a thread
-    // has four channels of a row, the slots' warps of all CTAs take them in turn.
+    // has four channels of a row at a time.
     __syncwarp();
     cluster_sync_all();
-    Walk w = *begin;
-    if (warp >= 4 && w.t < units_of(p, w.seq)) {
+    const Walk w = *begin;
+    if (w.seq.n > 0) {
       constexpr int kRowSlots = SPLIT ? 1 : NS, kParts = SPLIT ? 2 : 1;  // parts of a CTA
-      const int rank = cluster_ctarank(), parts = p.cluster * kParts;
-      for (int i = (warp - 4) * p.cluster + rank; i < kRowSlots * (kBQ / 32) * (kD / 4); i += p.cluster * 4 * NS) {
-        const int ch = i % (kD / 4), quarter = i / (kD / 4) % (kBQ / 32), g = i / (kD / 4) / (kBQ / 32);
-        const int r = quarter * 32 + lane, nd = r / p.G, node = w.node0(p, g) + nd;
-        const bool valid = nd < p.tq && node < w.seq.n;
-        if (!__any_sync(0xffffffffu, valid)) continue;
-        Joined x;
-        constexpr int kAtOnce = 12;
-        for (int k0 = 0; k0 < parts; k0 += kAtOnce) {
-          float2 ml[kAtOnce];
-          float4 a[kAtOnce];
+      const int parts = p.cluster * kParts, threads = p.cluster * C::kThreads;
 #pragma unroll
-          for (int j = 0; j < kAtOnce; ++j) {
-            ml[j] = make_float2(-INFINITY, 0.f);
-            a[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (valid && k0 + j < parts) {
-              const int cta = (k0 + j) / kParts, slot = SPLIT ? (k0 + j) % kParts : g;
-              ml[j] = ld_dsmem_f2(map_shared_rank(smem_u32(sQ) + 8 * (slot * kBQ + r), cta));
-              a[j] = ld_dsmem_f4(map_shared_rank(smem_u32(ring) + (((slot * (kD / 4) + ch) * kBQ + r) << 4), cta));
+      for (int g = 0; g < kRowSlots; ++g) {
+        const int n = min(p.tq, w.seq.n - w.node0(p, g)) * p.G;  // rows of the slot
+        for (int i = cluster_ctarank() * C::kThreads + threadIdx.x; i < n * (kD / 4); i += threads) {
+          const int ch = i / n, r = i - ch * n, nd = r / p.G;
+          Joined x;
+          constexpr int kAtOnce = 12;
+          for (int k0 = 0; k0 < parts; k0 += kAtOnce) {
+            float2 ml[kAtOnce];
+            float4 a[kAtOnce];
+#pragma unroll
+            for (int j = 0; j < kAtOnce; ++j) {
+              ml[j] = make_float2(-INFINITY, 0.f);
+              a[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+              if (k0 + j < parts) {
+                const int cta = (k0 + j) / kParts, slot = SPLIT ? (k0 + j) % kParts : g;
+                ml[j] = ld_dsmem_f2(map_shared_rank(smem_u32(sQ) + 8 * (slot * kBQ + r), cta));
+                a[j] = ld_dsmem_f4(map_shared_rank(smem_u32(ring) + (((slot * (kD / 4) + ch) * kBQ + r) << 4), cta));
+              }
             }
+            x.take(ml, a);
           }
-          x.take(ml, a);
+          x.store(p, w, w.node0(p, g) + nd, r - nd * p.G, ch);
         }
-        if (valid) x.store(p, w, node, r - nd * p.G, ch);
       }
     }
     __syncwarp();
@@ -947,13 +974,14 @@ Plan plan_of(int rows, int B, int H, int Hkv, bool cu, bool tree, long long capa
   // a unit of its own, that shares the work out better. With fewer units it would leave CTAs without tiles.
   pl.unit_cost = 2ll * B * Hkv > num_sms ? 4 : 0;
   const int nodes = tq * pl.slots, most = tree ? std::min(rows, kMaxNodes) : cu ? rows : 1;
-  pl.units = (most + nodes - 1) / nodes;
+  // units of a KV head: what fills a unit whole, and one more for each sequence
+  pl.units = (int)std::min<long long>((long long)B * ((most + nodes - 1) / nodes), (long long)B + rows / nodes);
   const long long keys = std::min(capacity, window > 0 ? (long long)window + (tree ? kMaxNodes : nodes) : capacity);
   const long long tiles = keys / kBK + 2;
   pl.fits = ((long long)B + rows / nodes + 1) * Hkv * (tiles + pl.unit_cost) < 0x7fffffffll;
   // Clusters: a unit each, its keys in equal shares, no list to add up and no second kernel.
   pl.cluster = 1;
-  const long long units = (long long)B * Hkv * pl.units;
+  const long long units = (long long)Hkv * pl.units;
   for (int size = kMaxCluster; size > 1; --size)
     if (units * size <= num_sms && (B == 1 || tiles <= kClusterTiles * size) &&
         (pl.slots == 2 ? resident_clusters<2, false>(size) : resident_clusters<2, true>(size)) >= units) {
@@ -1000,19 +1028,19 @@ cudaError_t launch_attn_paged(const HeadRows& q, const PagedCache& c, const Head
   p.Hkv = Hkv;
   p.window = window > 0 ? window : 0;
   p.slots = pl.slots;
+  const bool two = pl.slots == 2;
   while ((1 << p.box_shift) < box) ++p.box_shift;
   p.grid = pl.grid;
   p.min_tiles = pl.min_tiles;
   p.cluster = pl.cluster;
-  p.units = pl.units;
+  p.single = pl.units == B;
   p.unit_cost = pl.cluster > 1 ? 0 : pl.unit_cost;
   p.o_wide = reinterpret_cast<uintptr_t>(o.ptr) % 32 == 0 && (rows == 1 || o.row % 16 == 0) && (H == 1 || o.head % 16 == 0);
   p.status = st;
   p.wait_ns = wait_ns;
-  const bool two = pl.slots == 2;
   if (pl.cluster > 1)  // configured when the resident clusters were asked for
     return launch_clusters(two ? attn_paged_kernel<2, true, false> : attn_paged_kernel<2, true, true>,
-                           B * Hkv * pl.units * pl.cluster, two ? Cfg<2>::kThreads : Cfg<2, true>::kThreads,
+                           Hkv * pl.units * pl.cluster, two ? Cfg<2>::kThreads : Cfg<2, true>::kThreads,
                            two ? Cfg<2>::kSmem : Cfg<2, true>::kSmem, pl.cluster, s, p);
   const int smem = two ? Cfg<2>::kSmem : Cfg<1>::kSmem, threads = two ? Cfg<2>::kThreads : Cfg<1>::kThreads;
   p.acc = static_cast<float*>(ws);
