@@ -16,8 +16,7 @@
 // depend on timing. Lengths are on the device: every CTA adds up the line by itself.
 //
 // Warp 0 loads: its lanes look up the pages of the next 32 boxes (a box: the rows of a page in a tile)
-// and each issues a TMA copy of a box's half of K or V, 128-byte swizzled, into a ring of 32 KB
-// stages. Warp 1 (and 2 for the second slot) issues the products: S = Q K^T of tile j + 1 into one of
+// and each issues a TMA copy of a box's half of K or V, 128-byte swizzled, into rings of 16 KB stages. Warp 1 (and 2 for the second slot) issues the products: S = Q K^T of tile j + 1 into one of
 // two TMEM buffers, then O += P V of tile j with P from TMEM. Four warps a slot hold a row a thread: scores
 // from TMEM, the running softmax in the log2 domain with a reference that moves only when a
 // score passes it by 2^8 (exact: softmax does not depend on it), P as bf16 over the scores; and before
@@ -77,6 +76,18 @@ __device__ __forceinline__ float fmax3(float a, float b, float c) {
   float d;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
+}
+// A tile into L2 alone.
+__device__ __forceinline__ void tma_prefetch_3d(const CUtensorMap* m, int x, int y, int z) {
+  asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(reinterpret_cast<uint64_t>(m)),
+               "r"(x), "r"(y), "r"(z)
+               : "memory");
+}
+// One lane of a converged warp, the same one each time.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r != 0;
 }
 // 32 bytes in one store (a 32-byte boundary)
 __device__ __forceinline__ void st_global_32(void* p, const uint4& a, const uint4& b) {
@@ -154,6 +165,7 @@ struct PerSeq {
     const int n = of(min(b, B - 1));  // without a branch: the loads of all are under way together
     return b < B ? n : 0;
   }
+  template <int = 0>
   __device__ __forceinline__ int total() const {
     int n = 0;
 #pragma unroll
@@ -331,10 +343,15 @@ template <int NS, bool SPLIT = false>
 struct Cfg {
   static constexpr int kQueries = (SPLIT ? 1 : NS) * kQBytes;
   static constexpr int kStages = kQueries == kQBytes ? 6 : 5;
-  static constexpr int kThreads = 128 + 128 * NS;
-  static constexpr int kBars = 2 * kStages + 10 * NS;
+  static constexpr int kThreads = 128 + 128 * NS;  // at most 12 warps: one more would leave 128 registers
+  static constexpr int kBufs = NS == 1 ? 4 : 2;    // a slot's buffers of scores
+  static constexpr int kSlotCols = 64 * kBufs + kD;  // of tensor memory: scores (and P over them), outputs
+  static constexpr int kTmemCols = 512;
+  static_assert(NS * kSlotCols <= kTmemCols, "tensor memory");
+  static constexpr int kBars = 4 * kStages + (5 + 3 * kBufs) * NS;
   static constexpr int kSmem = 1024 + kQueries + kStages * kStageBytes + kBars * 8 + 8 + sizeof(Walk);
   static_assert(kSmem <= 227 * 1024, "shared memory");
+  static_assert(NS * kBQ * kD * 4 <= kStages * kStageBytes, "clusters: the slots' outputs take the ring's place");
 };
 
 template <int NS, bool CL, bool SPLIT>
@@ -350,34 +367,38 @@ __global__ void __launch_bounds__(Cfg<NS, SPLIT>::kThreads, 1) attn_paged_kernel
   volatile int* const abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
   Walk* const begin = reinterpret_cast<Walk*>(tmem_holder + 2);  // the CTA's first unit
   auto bar = [&](int i) { return smem_u32(&bars[i]); };
-  auto full = [&](int s) { return bar(s); };
-  auto empty = [&](int s) { return bar(C::kStages + s); };
-  auto mine = [&](int g, int i) { return bar(2 * C::kStages + 10 * g + i); };
+  auto full = [&](int kv, int s) { return bar(kv * C::kStages + s); };  // K (0) or V (1) of a stage
+  auto empty = [&](int kv, int s) { return bar((2 + kv) * C::kStages + s); };
+  auto mine = [&](int g, int i) { return bar(4 * C::kStages + (5 + 3 * C::kBufs) * g + i); };
   auto q_full = [&](int g) { return mine(g, 0); };
-  auto s_full = [&](int g, int buf) { return mine(g, 1 + buf); };
-  auto p_ready = [&](int g, int buf) { return mine(g, 3 + buf); };
-  auto pv_done = [&](int g) { return mine(g, 5); };
-  auto o_done = [&](int g) { return mine(g, 6); };
-  auto o_free = [&](int g) { return mine(g, 7); };
-  auto drain = [&](int g) { return mine(g, 8); };
-  auto q_free = [&](int g) { return mine(g, 9); };
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  auto q_free = [&](int g) { return mine(g, 1); };
+  auto o_done = [&](int g) { return mine(g, 2); };
+  auto o_free = [&](int g) { return mine(g, 3); };
+  auto drain = [&](int g) { return mine(g, 4); };
+  // of the slot's tile number A, in buffer A % kBufs
+  auto s_full = [&](int g, int A) { return mine(g, 5 + A % C::kBufs); };
+  auto p_ready = [&](int g, int A) { return mine(g, 5 + C::kBufs + A % C::kBufs); };
+  auto pv_done = [&](int g, int A) { return mine(g, 5 + 2 * C::kBufs + A % C::kBufs); };
+  auto phase = [](int A) { return (uint32_t)(A / C::kBufs) & 1; };
+  // the warp's number as the compiler can see that it is the same in all lanes: what the roles compute from it
+  // then goes through uniform registers, where the MMA and TMA instructions want their operands
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const unsigned long long budget = p.wait_ns;
-  constexpr int kTmemCols = 256 * NS;  // of slot g: S and P in 256 g and 256 g + 64, O from 256 g + 128
-
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::kStages; ++s) {
-      mbar_init(full(s), 1);
-      mbar_init(empty(s), SPLIT ? 1 : NS);
+      mbar_init(full(0, s), 1);
+      mbar_init(full(1, s), 1);
+      mbar_init(empty(0, s), SPLIT ? 1 : NS);
+      mbar_init(empty(1, s), SPLIT ? 1 : NS);
     }
     for (int g = 0; g < NS; ++g) {
       mbar_init(q_full(g), 1);
       mbar_init(q_free(g), 1);
-      for (int i = 0; i < 2; ++i) {
+      for (int i = 0; i < C::kBufs; ++i) {
         mbar_init(s_full(g, i), 1);
         mbar_init(p_ready(g, i), 128);
+        mbar_init(pv_done(g, i), 1);
       }
-      mbar_init(pv_done(g), 1);
       mbar_init(o_done(g), 1);
       mbar_init(o_free(g), 128);
       mbar_init(drain(g), 1);
@@ -389,7 +410,7 @@ __global__ void __launch_bounds__(Cfg<NS, SPLIT>::kThreads, 1) attn_paged_kernel
     tma_prefetch_desc(&p.tq_map);
   }
   if (warp == 1) {
-    tmem_alloc(smem_u32(tmem_holder), kTmemCols);
+    tmem_alloc(smem_u32(tmem_holder), C::kTmemCols);
     tmem_relinquish();
   }
   pdl_wait();  // queries, cache, lengths and lists come from earlier kernels
@@ -422,17 +443,22 @@ __global__ void __launch_bounds__(Cfg<NS, SPLIT>::kThreads, 1) attn_paged_kernel
   tc_fence_after();
   const uint32_t tmem = *tmem_holder;
   // What is in flight, for the drain after an abort: the stages issued (with the parity of their last
-  // phase) and whether any MMA was.
-  uint32_t issued = 0, parity = 0, q_issued = 0, q_parity = 0;
+  // phase), the loads of queries so far and whether any MMA was issued.
+  uint32_t issued = 0, parity = 0;
+  int q_loads = 0;
   bool mma_issued = false;
   // clusters: a row's reference and sum over the CTA's share (of none, at first)
   float2 share = make_float2(-INFINITY, 0.f);
   bool share_live = false;
 
-  if (warp == 0) {
-    // ---------------- the cache's tiles, all lanes
+  if (warp == 0 || warp == 3) {
+    // ---------------- the cache's tiles, all lanes: K by warp 0, V by warp 3 (a warp issues about a copy
+    // every 60 cycles: with pages of 16, 8 copies a tile and warp, one warp for both took 1450 cycles a tile)
+    const int kv = warp == 0 ? 0 : 1;
+    const CUtensorMap* const map = kv ? &p.tv : &p.tk;
+    const uint32_t to = smem_u32(ring) + 2 * kv * kKVSub;
     const uint64_t once = l2_policy_evict_first();
-    const int page_shift = p.c.page_shift, boxes = kBK >> p.box_shift;
+    const int page_shift = p.c.page_shift, boxes = kBK >> p.box_shift, box = lane >> 1, half = lane & 1;
     int J = 0;
     bool failed = false;
     for (Walk w = *begin; w.on() && !failed; w.next(p)) {
@@ -452,25 +478,24 @@ __global__ void __launch_bounds__(Cfg<NS, SPLIT>::kThreads, 1) attn_paged_kernel
         }
         const int s = J % C::kStages;
         const uint32_t ph = (J / C::kStages) & 1;
-        if (!__all_sync(0xffffffffu, mbar_wait(empty(s), ph ^ 1, budget, abort_flag))) {
+        if (!__all_sync(0xffffffffu, mbar_wait(empty(kv, s), ph ^ 1, budget, abort_flag))) {
           failed = true;
           break;
         }
-        const int box = lane >> 2, part = lane & 3;
         int its = __shfl_sync(0xffffffffu, page, (i & 31) + (box < boxes ? box : 0));
         const bool loads = box < boxes && its != kNoBox;
         if (loads && (its < 0 || its >= p.c.n_pages)) {
           record(p.status, kStatusInvalidArg);
           its = 0;
         }
-        const int n = __popc(__ballot_sync(0xffffffffu, loads)) >> 2;
-        if (lane == 0) mbar_arrive_expect_tx(full(s), (uint32_t)(n * 512) << p.box_shift);
+        const int n = __popc(__ballot_sync(0xffffffffu, loads));
+        if (lane == 0) mbar_arrive_expect_tx(full(kv, s), (uint32_t)(n * 128) << p.box_shift);
         __syncwarp();
         if (loads) {
           const int slot = (box0 + i + box) << p.box_shift;
           const int row = ((its * p.Hkv + w.kvh) << page_shift) + (slot & ((1 << page_shift) - 1));
-          const uint32_t dst = smem_u32(ring + s * kStageBytes) + part * kKVSub + ((box << p.box_shift) << 7);
-          tma_load_2d_hint(dst, part < 2 ? &p.tk : &p.tv, 64 * (part & 1), row, full(s), once);
+          tma_load_2d_hint(to + s * kStageBytes + half * kKVSub + ((box << p.box_shift) << 7), map, 64 * half, row,
+                           full(kv, s), once);
         }
         __syncwarp();
         issued |= 1u << s;
@@ -479,117 +504,152 @@ __global__ void __launch_bounds__(Cfg<NS, SPLIT>::kThreads, 1) attn_paged_kernel
     }
     if (failed && lane == 0) {
       *abort_flag = 1;
-      report_timeout(p.status, 0x50);
+      report_timeout(p.status, 0x50 + 3 * kv);
     }
-  } else if (warp <= NS) {
-    // ---------------- the products of a slot
-    if (lane == 0) {
-      const int g = warp - 1;
-      constexpr uint32_t idesc_s = idesc_bf16_f32(kBQ, kBK);
-      constexpr uint32_t idesc_pv = idesc_bf16_f32(kBQ, kD) | (1u << 16);  // B (V) is MN-major
-      const int rows = SPLIT ? 0 : g;  // the queries' slot
-      const uint64_t dq = smem_desc_sw128(smem_u32(sQ + rows * kQBytes));
-      const uint64_t dk = smem_desc_sw128(smem_u32(ring));
-      const uint64_t dv = smem_desc_sw128_mn(smem_u32(ring + 2 * kKVSub), kKVSub, 1024);
-      const uint32_t s_tmem = tmem + 256 * g, o_tmem = tmem + 256 * g + 128;
-      constexpr int kStep = SPLIT ? 2 : 1;  // from one of the slot's tiles to the next
-      int J = 0, A = 0, units = 0;  // tiles of the CTA and of this slot, and its units
-      bool failed = false;
-      for (Walk w = *begin; w.on() && !failed; w.next(p)) {
-        const int all = w.j1 - w.j0, n = SPLIT ? (all + 1 - g) / 2 : all;
-        if (SPLIT && n == 0) break;  // (a cluster's CTA has one unit)
-        if (!w.has(p, rows)) {  // nothing for this slot: the stages go back
-          for (int j = 0; j < n && !failed; ++j, ++J) {
-            if (!mbar_wait(full(J % C::kStages), (J / C::kStages) & 1, budget, abort_flag)) failed = true;
-            else mbar_arrive(empty(J % C::kStages));
-          }
-          continue;
-        }
-        if constexpr (SPLIT) J = g;
-        auto issue_s = [&](int Jn, int An) {
-          const int st = Jn % C::kStages;
-          if (!mbar_wait(full(st), (Jn / C::kStages) & 1, budget, abort_flag)) return false;
-          tc_fence_after();
-          const uint64_t b = dk + (uint64_t)(st * (kStageBytes >> 4));
+  } else if (warp >= 1 && warp <= NS) {
+    // ---------------- the products of a slot: all lanes go through the loop, one issues
+    const int g = warp - 1;
+    constexpr uint32_t idesc_s = idesc_bf16_f32(kBQ, kBK);
+    constexpr uint32_t idesc_pv = idesc_bf16_f32(kBQ, kD) | (1u << 16);  // B (V) is MN-major
+    const int rows = SPLIT ? 0 : g;  // the queries' slot
+    const uint64_t dq = smem_desc_sw128(smem_u32(sQ + rows * kQBytes));
+    const uint64_t dk = smem_desc_sw128(smem_u32(ring));
+    const uint64_t dv = smem_desc_sw128_mn(smem_u32(ring + 2 * kKVSub), kKVSub, 1024);
+    const uint32_t s_tmem = tmem + C::kSlotCols * g, o_tmem = s_tmem + 64 * C::kBufs;
+    constexpr int kStep = SPLIT ? 2 : 1;  // from one of the slot's tiles to the next
+    int J = 0, A = 0, units = 0;  // tiles of the CTA and of this slot, and its units
+    bool failed = false;
+    auto there = [](uint32_t bar, uint32_t ph) { return __all_sync(0xffffffffu, mbar_test_wait(bar, ph)) != 0; };
+    auto wait = [&](uint32_t bar, uint32_t ph) { return __all_sync(0xffffffffu, mbar_wait(bar, ph, budget, abort_flag)) != 0; };
+    // The slot's queries: loaded as soon as the last score product of a unit has read its own, and asked into L2 a
+    // unit before that (behind the tiles in flight, a load from HBM would take 4 us).
+    Walk ahead = *begin;
+    auto find = [&] {
+      while (ahead.on() && !ahead.has(p, rows)) ahead.next(p);
+      return ahead.on();
+    };
+    auto load_queries = [&] {
+      if (!ahead.on() || (SPLIT && g != 0)) return;
+      if (elect_one()) {
+        // rows past the sequence's are others' or zeros: their scores are nobody's
+        mbar_arrive_expect_tx(q_full(rows), (uint32_t)p.q_bytes);
 #pragma unroll
-          for (int kk = 0; kk < kD / 16; ++kk)
-            tc_mma_bf16(s_tmem + 64 * (An & 1), dq + (uint64_t)((kk >> 2) * (kQSub >> 4) + (kk & 3) * 2),
-                        b + (uint64_t)((kk >> 2) * (kKVSub >> 4) + (kk & 3) * 2), idesc_s, kk > 0 ? 1u : 0u);
-          tc_commit(s_full(g, An & 1));
-          mma_issued = true;
-          return true;
-        };
-        if (!mbar_wait(q_full(rows), units & 1, budget, abort_flag) || !issue_s(J, A)) {
+        for (int half = 0; half < 2; ++half)
+          tma_load_3d(smem_u32(sQ + rows * kQBytes + half * kQSub), &p.tq_map, 64 * half, ahead.kvh * p.G,
+                      ahead.seq.row0 + ahead.node0(p, rows), q_full(rows));
+      }
+      __syncwarp();
+      q_loads++;
+      ahead.next(p);
+      if (!SPLIT && find() && elect_one())
+#pragma unroll
+        for (int half = 0; half < 2; ++half)
+          tma_prefetch_3d(&p.tq_map, 64 * half, ahead.kvh * p.G, ahead.seq.row0 + ahead.node0(p, rows));
+      __syncwarp();
+    };
+    find();
+    load_queries();
+    for (Walk w = *begin; w.on() && !failed; w.next(p)) {
+      const int all = w.j1 - w.j0, n = SPLIT ? (all + 1 - g) / 2 : all;
+      if (SPLIT && n == 0) break;  // (a cluster's CTA has one unit)
+      if (!w.has(p, rows)) {  // nothing for this slot: the stages go back
+        for (int j = 0; j < n && !failed; ++j, ++J)
+          for (int kv = 0; kv < 2 && !failed; ++kv) {
+            if (!wait(full(kv, J % C::kStages), (J / C::kStages) & 1)) failed = true;
+            else if (lane == 0) mbar_arrive(empty(kv, J % C::kStages));
+          }
+        continue;
+      }
+      if constexpr (SPLIT) J = g;
+      // What can be issued is, whatever it is: scores up to kBufs tiles ahead (their buffer's P has been read: its
+      // product was issued before), the product of a tile whose P is there, the next unit's queries.
+      if (!wait(q_full(rows), units & 1)) {
+        failed = true;
+        break;
+      }
+      int s = 0, v = 0;  // tiles whose scores and products have been issued
+      bool q_wanted = false;
+      unsigned long long idle_since = 0;
+      unsigned idle = 0;  // looks in a row that found nothing
+      while (v < n) {
+        bool did = false;
+        if (s < n && s < v + C::kBufs) {
+          const int at = J + s * kStep, st = at % C::kStages;
+          if (there(full(0, st), (at / C::kStages) & 1)) {
+            tc_fence_after();
+            if (elect_one()) {
+              const uint64_t b = dk + (uint64_t)(st * (kStageBytes >> 4));
+              const uint32_t d = s_tmem + 64 * ((A + s) % C::kBufs);
+#pragma unroll
+              for (int kk = 0; kk < kD / 16; ++kk)
+                tc_mma_bf16(d, dq + (uint64_t)((kk >> 2) * (kQSub >> 4) + (kk & 3) * 2),
+                            b + (uint64_t)((kk >> 2) * (kKVSub >> 4) + (kk & 3) * 2), idesc_s, kk > 0 ? 1u : 0u);
+              tc_commit(s_full(g, A + s));
+              tc_commit(empty(0, st));
+              if (s + 1 == n && !SPLIT) tc_commit(q_free(g));  // no further score product of this unit reads the queries
+            }
+            __syncwarp();
+            mma_issued = true;
+            if (++s == n && !SPLIT) q_wanted = true;
+            did = true;
+          }
+        }
+        if (v < s && there(p_ready(g, A + v), phase(A + v))) {
+          const int at = J + v * kStep, st = at % C::kStages;
+          if (there(full(1, st), (at / C::kStages) & 1) && (v > 0 || units == 0 || there(o_free(g), (units - 1) & 1))) {
+            tc_fence_after();
+            if (elect_one()) {
+              const uint64_t b = dv + (uint64_t)(st * (kStageBytes >> 4));
+              const uint32_t a = s_tmem + 64 * ((A + v) % C::kBufs);
+#pragma unroll
+              for (int kk = 0; kk < kBK / 16; ++kk)
+                tc_mma_ts(o_tmem, a + kk * 8, b + (uint64_t)(kk * (16 * 128 >> 4)), idesc_pv, (v > 0 || kk > 0) ? 1u : 0u);
+              tc_commit(empty(1, st));
+              tc_commit(pv_done(g, A + v));
+              if (v + 1 == n) tc_commit(o_done(g));
+            }
+            __syncwarp();
+            ++v;
+            did = true;
+          }
+        }
+        if (q_wanted && there(q_free(g), units & 1)) {
+          load_queries();
+          q_wanted = false;
+          did = true;
+        }
+        if (did) {
+          idle = 0;
+        } else if ((++idle & 31) == 0) {
+          const unsigned long long now = globaltimer_ns();
+          if (idle == 32) idle_since = now;
+          if (__any_sync(0xffffffffu, *abort_flag != 0 || now - idle_since > budget)) {
+            failed = true;
+            break;
+          }
+        }
+      }
+      if (!failed && q_wanted) {
+        if (wait(q_free(g), units & 1))
+          load_queries();
+        else
           failed = true;
-          break;
-        }
-        for (int j = 0; j < n; ++j, J += kStep, ++A) {
-          // the next scores first: they are under way while the softmax works on these. Their buffer's
-          // P has been read: its product was issued before.
-          if (j + 1 < n && !issue_s(J + kStep, A + 1)) {
-            failed = true;
-            break;
-          }
-          if (j + 1 == max(n - 1, 1)) tc_commit(q_free(g));  // that was the unit's last score product
-          if ((j == 0 && units > 0 && !mbar_wait(o_free(g), (units - 1) & 1, budget, abort_flag)) ||
-              !mbar_wait(p_ready(g, A & 1), (A >> 1) & 1, budget, abort_flag)) {
-            failed = true;
-            break;
-          }
-          tc_fence_after();
-          const int st = J % C::kStages;
-          const uint64_t b = dv + (uint64_t)(st * (kStageBytes >> 4));
-#pragma unroll
-          for (int kk = 0; kk < kBK / 16; ++kk)
-            tc_mma_ts(o_tmem, s_tmem + 64 * (A & 1) + kk * 8, b + (uint64_t)(kk * (16 * 128 >> 4)), idesc_pv,
-                      (j > 0 || kk > 0) ? 1u : 0u);
-          tc_commit(empty(st));
-          tc_commit(pv_done(g));
-        }
-        if (failed) break;
-        tc_commit(o_done(g));
-        ++units;
       }
-      if (failed) {
-        *abort_flag = 1;
-        report_timeout(p.status, 0x51);
-      }
+      J += n * kStep;
+      A += n;
+      ++units;
     }
-  } else if (warp == 3) {
-    // ---------------- queries, once the last unit's scores are done
-    if (lane == 0) {
-      int units[NS] = {};
-      bool failed = false;
-      for (Walk w = *begin; w.on() && !failed; w.next(p)) {
-#pragma unroll
-        for (int g = 0; g < (SPLIT ? 1 : NS); ++g) {
-          const int node0 = w.node0(p, g);
-          if (failed || !w.has(p, g)) continue;
-          if (units[g] > 0 && !mbar_wait(q_free(g), (units[g] - 1) & 1, budget, abort_flag)) {
-            failed = true;
-            continue;
-          }
-          // rows past the sequence's are others' or zeros: their scores are nobody's
-          mbar_arrive_expect_tx(q_full(g), (uint32_t)p.q_bytes);
-#pragma unroll
-          for (int half = 0; half < 2; ++half)
-            tma_load_3d(smem_u32(sQ + g * kQBytes + half * kQSub), &p.tq_map, 64 * half, w.kvh * p.G, w.seq.row0 + node0, q_full(g));
-          q_issued |= 1u << g;
-          q_parity = (q_parity & ~(1u << g)) | ((uint32_t)(units[g] & 1) << g);
-          ++units[g];
-        }
-      }
-      if (failed) {
-        *abort_flag = 1;
-        report_timeout(p.status, 0x53);
-      }
+    if (failed && lane == 0) {
+      *abort_flag = 1;
+      report_timeout(p.status, 0x51);
     }
+    __syncwarp();
   } else if (warp >= 4) {
     // ---------------- a slot's rows, one a thread
     const int g = (warp - 4) >> 2, quarter = warp & 3;
     const int r = quarter * 32 + lane;
     const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
-    const uint32_t s_taddr = tmem + lane_off + 256 * g, o_taddr = s_taddr + 128;
+    const uint32_t s_taddr = tmem + lane_off + C::kSlotCols * g, o_taddr = s_taddr + 64 * C::kBufs;
     const int node_of_row = r / p.G, head_of_row = r - node_of_row * p.G;
     int J = 0, A = 0, units = 0, part = 2 * blockIdx.x;
     bool failed = false;
@@ -631,7 +691,7 @@ __global__ void __launch_bounds__(Cfg<NS, SPLIT>::kThreads, 1) attn_paged_kernel
       constexpr int kStep = SPLIT ? 2 : 1;
       for (int j = 0; j < n; ++j, J += kStep, ++A) {
         const int n0 = (w.keys.tile0() + w.j0 + (SPLIT ? J : j)) * kBK;
-        if (!__all_sync(0xffffffffu, mbar_wait(s_full(g, A & 1), (A >> 1) & 1, budget, abort_flag))) {
+        if (!__all_sync(0xffffffffu, mbar_wait(s_full(g, A), phase(A), budget, abort_flag))) {
           failed = true;
           break;
         }
@@ -642,7 +702,7 @@ __global__ void __launch_bounds__(Cfg<NS, SPLIT>::kThreads, 1) attn_paged_kernel
         const int v_lo = w.keys.first - n0, v_hi = w.keys.end - n0;
         if (v_lo > 0 || v_hi < kBK) {
           const int st = J % C::kStages;
-          if (!__all_sync(0xffffffffu, mbar_wait(full(st), (J / C::kStages) & 1, budget, abort_flag))) {
+          if (!__all_sync(0xffffffffu, mbar_wait(full(1, st), (J / C::kStages) & 1, budget, abort_flag))) {
             failed = true;
             break;
           }
@@ -657,10 +717,10 @@ __global__ void __launch_bounds__(Cfg<NS, SPLIT>::kThreads, 1) attn_paged_kernel
         }
         if (!live) {  // nobody reads these rows: whatever the score buffer holds may stand for P
           tc_fence_before();
-          mbar_arrive(p_ready(g, A & 1));
+          mbar_arrive(p_ready(g, A));
           continue;
         }
-        const uint32_t s_buf = s_taddr + 64 * (A & 1);
+        const uint32_t s_buf = s_taddr + 64 * (A % C::kBufs);
         float x[kBK];
 #pragma unroll
         for (int c = 0; c < kBK; c += 16) tmem_ld16(s_buf + c, *reinterpret_cast<float(*)[16]>(&x[c]));
@@ -691,7 +751,7 @@ __global__ void __launch_bounds__(Cfg<NS, SPLIT>::kThreads, 1) attn_paged_kernel
           }
           l *= alpha;
           if (j > 0) {  // the products so far are to be complete, then O moves to the new reference
-            if (!__all_sync(0xffffffffu, mbar_wait(pv_done(g), (A - 1) & 1, budget, abort_flag))) {
+            if (!__all_sync(0xffffffffu, mbar_wait(pv_done(g, A - 1), phase(A - 1), budget, abort_flag))) {
               failed = true;
               break;
             }
@@ -727,7 +787,7 @@ __global__ void __launch_bounds__(Cfg<NS, SPLIT>::kThreads, 1) attn_paged_kernel
         }
         tc_wait_st();
         tc_fence_before();
-        mbar_arrive(p_ready(g, A & 1));
+        mbar_arrive(p_ready(g, A));
         float a0, a1, b0, b1;
         f2_split(sum2[0], a0, a1);
         f2_split(sum2[1], b0, b1);
@@ -796,15 +856,18 @@ __global__ void __launch_bounds__(Cfg<NS, SPLIT>::kThreads, 1) attn_paged_kernel
   // flight: they complete before TMEM is freed and the CTA exits. Every thread reads the same flag.
   if (*abort_flag) {
     volatile int never = 0;
-    if (warp == 0 && lane == 0) {
+    if ((warp == 0 || warp == 3) && lane == 0) {
       for (int s = 0; s < C::kStages; ++s)
-        if (issued & (1u << s)) mbar_wait(full(s), (parity >> s) & 1, kDrainNs, &never);
-    } else if (warp == 3 && lane == 0) {
-      for (int g = 0; g < NS; ++g)
-        if (q_issued & (1u << g)) mbar_wait(q_full(g), (q_parity >> g) & 1, kDrainNs, &never);
-    } else if (warp >= 1 && warp <= NS && lane == 0 && mma_issued) {
-      tc_commit(drain(warp - 1));
-      mbar_wait(drain(warp - 1), 0, kDrainNs, &never);
+        if (issued & (1u << s)) mbar_wait(full(warp == 0 ? 0 : 1, s), (parity >> s) & 1, kDrainNs, &never);
+    } else if (warp >= 1 && warp <= NS) {
+      if (q_loads > 0) mbar_wait(q_full(warp - 1), (q_loads - 1) & 1, kDrainNs, &never);
+      __syncwarp();
+      if (mma_issued) {
+        if (elect_one()) tc_commit(drain(warp - 1));  // the lane that issued the products
+        __syncwarp();
+        mbar_wait(drain(warp - 1), 0, kDrainNs, &never);
+      }
+      __syncwarp();
     }
     tc_fence_before();
     __syncthreads();
@@ -815,7 +878,7 @@ __global__ void __launch_bounds__(Cfg<NS, SPLIT>::kThreads, 1) attn_paged_kernel
     const int g = (warp - 4) >> 2, r = (warp & 3) * 32 + lane;
     reinterpret_cast<float2*>(sQ)[g * kBQ + r] = share;
     if (share_live && !*abort_flag) {
-      const uint32_t o_taddr = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + 256 * g + 128;
+      const uint32_t o_taddr = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + C::kSlotCols * g + 64 * C::kBufs;
 #pragma unroll 1
       for (int c = 0; c < kD; c += 32) {
         float ov[32];
@@ -870,7 +933,7 @@ __global__ void __launch_bounds__(Cfg<NS, SPLIT>::kThreads, 1) attn_paged_kernel
   if (warp == 1) {
     __syncwarp();
     tc_fence_after();
-    tmem_dealloc(tmem, kTmemCols);
+    tmem_dealloc(tmem, C::kTmemCols);
   }
 }
 
