@@ -809,29 +809,29 @@ __global__ void __launch_bounds__(Cfg<NS, SPLIT>::kThreads, 1) attn_paged_kernel
                                  (long long)(w.kvh * p.G + head_of_row) * p.o.head;
         if (valid && !whole) p.ml[((size_t)part * NS + g) * kBQ + r] = make_float2(m_ref, l);
 #pragma unroll 1
-        for (int c = 0; c < kD; c += 16) {
-          float ov[16];
-          tmem_ld16(o_taddr + c, ov);
+        for (int c = 0; c < kD; c += 32) {
+          float ov[32];
+          tmem_ld16(o_taddr + c, *reinterpret_cast<float(*)[16]>(&ov[0]));
+          tmem_ld16(o_taddr + c + 16, *reinterpret_cast<float(*)[16]>(&ov[16]));
           tc_wait_ld();
-          if (valid) {
-            if (whole) {
+          if (valid && whole) {
 #pragma unroll
-              for (int i = 0; i < 16; ++i) ov[i] *= inv;
-              const uint4 a = make_uint4(pack_bf16x2(ov[0], ov[1]), pack_bf16x2(ov[2], ov[3]), pack_bf16x2(ov[4], ov[5]),
-                                         pack_bf16x2(ov[6], ov[7]));
-              const uint4 b = make_uint4(pack_bf16x2(ov[8], ov[9]), pack_bf16x2(ov[10], ov[11]),
-                                         pack_bf16x2(ov[12], ov[13]), pack_bf16x2(ov[14], ov[15]));
+            for (int h = 0; h < 32; h += 16) {
+              uint4 a, b;
+              uint32_t* const w8[2] = {&a.x, &b.x};
+#pragma unroll
+              for (int i = 0; i < 8; ++i) w8[i >> 2][i & 3] = pack_bf16x2(ov[h + 2 * i] * inv, ov[h + 2 * i + 1] * inv);
               if (p.o_wide) {
-                st_global_32(o + c, a, b);
+                st_global_32(o + c + h, a, b);
               } else {
-                reinterpret_cast<uint4*>(o + c)[0] = a;
-                reinterpret_cast<uint4*>(o + c)[1] = b;
+                reinterpret_cast<uint4*>(o + c + h)[0] = a;
+                reinterpret_cast<uint4*>(o + c + h)[1] = b;
               }
-            } else {
-#pragma unroll
-              for (int i = 0; i < 16; i += 4)
-                *reinterpret_cast<float4*>(acc + (c + i) * kBQ) = make_float4(ov[i], ov[i + 1], ov[i + 2], ov[i + 3]);
             }
+          } else if (valid) {
+#pragma unroll
+            for (int i = 0; i < 32; i += 4)
+              *reinterpret_cast<float4*>(acc + (c + i) * kBQ) = make_float4(ov[i], ov[i + 1], ov[i + 2], ov[i + 3]);
           }
           __syncwarp();
         }
