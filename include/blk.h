@@ -551,6 +551,24 @@ blk_status blk_verify_drafts(blk_handle* h, const float* target, long long targe
 blk_status blk_paged_keep(blk_handle* h, const blk_paged_cache* caches, int n_caches, const int* counts, const int* path,
                           const int* cu_seqlens, const int* starts, int batch, int rows, void* stream);
 
+/* The model around the block over new rows of a paged cache (bf16 handles without attn_gate and sandwich_norm;
+ * prepared weights are not used): the target's side of a speculative step, or a chunk of prompts.
+ * tokens [rows] device int32, packed by cu_seqlens; each layer appends its keys and values to its
+ * cache (host array of n_layers caches that share pages, lens and sizes) at positions lens[b] + depths[row]
+ * and attends, by parents, as blk_paged_append and blk_attn_paged do; lens does not move (blk_paged_keep).
+ * A tree's rows need depths. temperature < 0: out is the logits, bf16 [rows, vocab]; > 0: the probabilities
+ * softmax(logits / temperature), fp32 [rows, vocab], what blk_verify_drafts takes; 0: all of it on the
+ * largest logit (the first of several). The softmax is of the bf16 logits, in fp32. A token outside
+ * [0, vocab) embeds as zeros and sets the status word to INVALID_ARG.
+ * workspace: blk_model_paged_workspace_bytes (of a cache its sizes count; probs: temperature >= 0).
+ * Errors: those of blk_model_forward, blk_paged_append and blk_attn_paged. */
+size_t blk_model_paged_workspace_bytes(const blk_handle* h, int rows, int packed, int tree, int batch,
+                                       const blk_paged_cache* cache, int vocab, int probs);
+blk_status blk_model_forward_paged(blk_handle* h, const blk_model* m, const int* tokens, int rows,
+                                   const int* cu_seqlens, const int* depths, const int* parents, int batch,
+                                   const blk_paged_cache* caches, float temperature, int host_lens_max, void* out,
+                                   void* workspace, size_t workspace_bytes, void* stream);
+
 /* Scratch bytes a stage entry point needs for `rows` token rows. */
 size_t blk_stage_workspace_bytes(const blk_handle* h, int rows);
 

@@ -114,6 +114,9 @@ SIGNATURES = {
                                   c_void_p]),
     "blk_paged_keep": (c_int, [c_void_p, _PAGED, c_int, c_void_p, c_void_p, c_void_p, c_void_p, c_int, c_int,
                                c_void_p]),
+    "blk_model_paged_workspace_bytes": (c_size_t, [c_void_p, c_int, c_int, c_int, c_int, _PAGED, c_int, c_int]),
+    "blk_model_forward_paged": (c_int, [c_void_p, POINTER(blk_model), c_void_p, c_int, c_void_p, c_void_p, c_void_p,
+                                        c_int, _PAGED, c_float, c_int, c_void_p, c_void_p, c_size_t, c_void_p]),
     "blk_stage_workspace_bytes": (c_size_t, [c_void_p, c_int]),
     "blk_last_status": (c_int, [c_void_p]),
     "blk_xielu_effective": (None, [c_float, c_float, c_float, POINTER(c_float), POINTER(c_float)]),
@@ -759,6 +762,60 @@ class DecoderBlock:
                                     self._int32(counts, "counts", batch), self._int32(path, "path", n),
                                     self._int32(cu_seqlens, "cu_seqlens", batch + 1), self._int32(starts, "starts", batch),
                                     batch, n, self._raw_stream(self._dev)))
+
+    def model_forward_paged(self, tokens, layers, embed, norm_g, lm_head, caches, cu_seqlens=None, depths=None,
+                            parents=None, temperature=None, out=None, host_lens_max=-1, stream=None):
+        """The model (as in model_forward) over new rows of paged caches, one per layer (paged_cache, shared): tokens
+        int32 [N], packed by cu_seqlens, are appended behind lens, which do not move, and attend (paged_append,
+        attn_paged; a tree's rows need depths and parents). Returns the logits, bf16 [N, vocab], or with a
+        temperature the probabilities softmax(logits / temperature), fp32 [N, vocab] (0: all on the largest)."""
+        if self._elsewhere(stream):
+            with _on_stream(self._device, stream):
+                return self.model_forward_paged(tokens, layers, embed, norm_g, lm_head, caches, cu_seqlens, depths, parents,
+                                                temperature, out, host_lens_max)
+        torch, dev = self._torch, self._dev
+        if len(caches) != len(layers) or not caches:
+            raise ValueError("caches: one for each layer")
+        if temperature is not None and not temperature >= 0:
+            raise ValueError("temperature: 0 or more")
+        n, vocab = tokens.shape[0], embed.shape[0]
+        structs = [self._paged(c) for c in caches]
+        batch = structs[0][1]
+        tok = self._int32(tokens, "tokens", n)
+        cu = self._int32(cu_seqlens, "cu_seqlens", batch + 1)
+        dp, up = self._int32(depths, "depths", n), self._int32(parents, "parents", n)
+        for t, name, shape in ((embed, "embed", (vocab, self.desc.hidden)), (lm_head, "lm_head", (vocab, self.desc.hidden)),
+                               (norm_g, "norm_g", (self.desc.hidden,))):
+            _contiguous(t, name, self._dtype, dev, shape)
+        dtype = self._dtype if temperature is None else torch.float32
+        if out is None:
+            out = torch.empty(n, vocab, dtype=dtype, device=self._device)
+        else:
+            _contiguous(out, "out", dtype, dev, (n, vocab))
+        wls = (blk_weights * len(layers))(*[make_weights_struct(w) for w in layers])
+        m = blk_model(_ptr(embed), wls, len(layers), _ptr(norm_g), _ptr(lm_head), vocab)
+        nbytes = lib().blk_model_paged_workspace_bytes(self.handle, n, cu is not None, up is not None, batch, structs[0][0],
+                                                       vocab, temperature is not None)
+        ws = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=self._device)
+        _check(lib().blk_model_forward_paged(self.handle, ctypes.byref(m), tok, n, cu, dp, up, batch,
+                                             b"".join(s for s, _ in structs), -1.0 if temperature is None else temperature,
+                                             host_lens_max, out.data_ptr(), ws.data_ptr(), nbytes, self._raw_stream(dev)))
+        return out
+
+    def model_verify(self, tokens, layers, embed, norm_g, lm_head, caches, u, u_next, cu_seqlens=None, depths=None,
+                     parents=None, temperature=1.0, draft=None, host_lens_max=-1, stream=None):
+        """A step of speculative decoding: the model over each sequence's last token and its drafts
+        (model_forward_paged), their verification with the given random numbers (verify_drafts), and the kept
+        rows moved behind lens in every layer's cache (paged_keep). Returns (counts, path, next)."""
+        if self._elsewhere(stream):
+            with _on_stream(self._device, stream):
+                return self.model_verify(tokens, layers, embed, norm_g, lm_head, caches, u, u_next, cu_seqlens, depths, parents,
+                                         temperature, draft, host_lens_max)
+        p = self.model_forward_paged(tokens, layers, embed, norm_g, lm_head, caches, cu_seqlens, depths, parents, temperature,
+                                     host_lens_max=host_lens_max)
+        counts, path, token = self.verify_drafts(p, tokens, u, u_next, cu_seqlens, parents, draft)
+        self.paged_keep(caches, counts, path, cu_seqlens)
+        return counts, path, token
 
     def mlp(self, resid, h_normed, weights, out, stream=None):
         rows = resid.numel() // resid.shape[-1]

@@ -397,6 +397,26 @@ blk_status bf16_mlp_up(const blk_handle* h, const void* y2, int rows, const blk_
   return tc(h, g, s, "MLP up GEMM");
 }
 
+// out[rows, n] = bf16(a[rows, K] W[n, K]^T)
+blk_status bf16_rows(const blk_handle* h, const void* a, int rows, int K, const void* W, int n, void* out, cudaStream_t s,
+                     const char* what) {
+  TcGemmDesc g;
+  g.na = 1;
+  g.a[0] = {a, rows, 0};
+  g.nb = 1;
+  g.b[0] = {W, n, 0};
+  g.K = K;
+  static const int cands[] = {256, 224, 192, 128};
+  const TileChoice t = choose_tile(rows, n, false, cands, 4, h->num_sms, K >= kPairMinK);
+  g.bn = t.bn;
+  g.pair = t.pair;
+  g.epi = Epi::kStore;
+  g.const_op = 2;
+  g.e.out = out;
+  g.e.ldo = n;
+  return tc(h, g, s, what);
+}
+
 // ------------------------------------------------------------------ decode pieces (bf16)
 
 // Split count of a fused decode GEMM (the K splits of a tile form one cluster):
@@ -1284,21 +1304,7 @@ blk_status blk_model_forward(blk_handle* h, const blk_model* m, const int* token
     return check_cuda(launch_gemm_f32(static_cast<const float*>(mw.ynorm), static_cast<const float*>(m->lm_head),
                                       static_cast<float*>(logits), m->vocab, M, m->vocab, d.hidden, s),
                       "lm_head GEMM");
-  TcGemmDesc g;
-  g.na = 1;
-  g.a[0] = {mw.ynorm, M, 0};
-  g.nb = 1;
-  g.b[0] = {m->lm_head, m->vocab, 0};
-  g.K = d.hidden;
-  static const int cands[] = {256, 224, 192, 128};
-  const TileChoice tl = choose_tile(M, m->vocab, false, cands, 4, h->num_sms, d.hidden >= kPairMinK);
-  g.bn = tl.bn;
-  g.pair = tl.pair;
-  g.epi = Epi::kStore;
-  g.const_op = 2;
-  g.e.out = logits;
-  g.e.ldo = m->vocab;
-  return tc(h, g, s, "lm_head GEMM");
+  return bf16_rows(h, mw.ynorm, M, d.hidden, m->lm_head, m->vocab, logits, s, "lm_head GEMM");
 }
 
 struct blk_graph {
@@ -1856,6 +1862,122 @@ blk_status blk_paged_keep(blk_handle* h, const blk_paged_cache* caches, int n_ca
   } catch (const std::exception&) {
     return fail(BLK_ERR_INVALID_ARG, "caches: out of host memory");
   }
+}
+
+// ------------------------------------------------------------------ the model over a paged cache
+
+namespace {
+struct PagedModelWs {
+  void *act0, *act1, *y, *qkv, *o, *mid, *neur, *attn, *logits;
+  float* ss2;
+  size_t attn_bytes, total;
+};
+
+PagedModelWs carve_paged(const blk_handle* h, void* base, int rows, bool packed, bool tree, int batch,
+                         const blk_paged_cache* cache, int vocab, bool probs) {
+  const blk_desc& d = h->d;
+  const size_t M = rows;
+  Carve c(base);
+  PagedModelWs w{};
+  w.act0 = c.take(M * d.hidden * 2);
+  w.act1 = c.take(M * d.hidden * 2);
+  w.y = c.take(M * d.hidden * 2);
+  w.qkv = c.take(M * qkv_cols(d) * 2);
+  w.o = c.take(M * d.n_heads * d.head_dim * 2);
+  w.mid = c.take(M * d.hidden * sizeof(float));
+  w.neur = c.take(M * d.ffn * 2);
+  w.ss2 = static_cast<float*>(c.take(M * norm_parts(d.hidden, 128) * sizeof(float)));
+  w.attn_bytes = blk_attn_paged_workspace_bytes(h, rows, packed, tree, batch, cache);
+  w.attn = c.take(w.attn_bytes);
+  if (probs) w.logits = c.take(M * vocab * 2);
+  w.total = c.off;
+  return w;
+}
+
+blk_status check_paged_model(const blk_handle* h) {
+  const blk_desc& d = h->d;
+  if (d.dtype != BLK_BF16 || d.attn_gate || d.sandwich_norm)
+    return fail(BLK_ERR_UNSUPPORTED, "the model over a paged cache takes bf16 handles without attn_gate and sandwich_norm");
+  return BLK_OK;
+}
+}  // namespace
+
+size_t blk_model_paged_workspace_bytes(const blk_handle* h, int rows, int packed, int tree, int batch,
+                                       const blk_paged_cache* cache, int vocab, int probs) {
+  if (!h || rows <= 0 || batch <= 0 || vocab <= 0 || check_paged_model(h) != BLK_OK || check_paged(cache) != BLK_OK) return 0;
+  return carve_paged(h, nullptr, rows, packed != 0, tree != 0, batch, cache, vocab, probs != 0).total;
+}
+
+blk_status blk_model_forward_paged(blk_handle* h, const blk_model* m, const int* tokens, int rows,
+                                   const int* cu_seqlens, const int* depths, const int* parents, int batch,
+                                   const blk_paged_cache* caches, float temperature, int host_lens_max, void* out,
+                                   void* workspace, size_t workspace_bytes, void* stream) {
+  if (!h || !m || !caches) return fail(BLK_ERR_INVALID_ARG, "handle, model and caches must be non-NULL");
+  const blk_desc& d = h->d;
+  BLK_TRY(check_paged_model(h));
+  if (m->n_layers < 1 || !m->layers || !m->embed || !m->norm_g || !m->lm_head || m->vocab <= 0)
+    return fail(BLK_ERR_INVALID_ARG, "model: n_layers >= 1, layers, embed, norm_g, lm_head and vocab > 0");
+  if (m->vocab % 8) return fail(BLK_ERR_UNSUPPORTED, "model: vocab must be a multiple of 8 (16-byte logit rows)");
+  BLK_TRY(check_batch(rows, batch, cu_seqlens));
+  if (parents && !depths) return fail(BLK_ERR_INVALID_ARG, "the rows of a tree need depths");
+  if (temperature != temperature) return fail(BLK_ERR_INVALID_ARG, "temperature is NaN");
+  for (int l = 0; l < m->n_layers; ++l) {
+    const blk_paged_cache& c = caches[l];
+    BLK_TRY(check_paged(&c));
+    BLK_TRY(check_weights(d, &m->layers[l]));
+    if (c.pages != caches[0].pages || c.lens != caches[0].lens || c.n_pages != caches[0].n_pages ||
+        c.page_size != caches[0].page_size || c.max_pages != caches[0].max_pages)
+      return fail(BLK_ERR_INVALID_ARG, "caches: they must share pages, lens and sizes");
+  }
+  if (rows == 0 || batch == 0) return BLK_OK;
+  if (!tokens || !out) return fail(BLK_ERR_INVALID_ARG, "tokens and out must be non-NULL");
+  if (!aligned16(m->embed) || !aligned16(m->norm_g) || !aligned16(m->lm_head) || !aligned16(out) || !aligned16(workspace))
+    return fail(BLK_ERR_ALIGNMENT, "model: embed, norm_g, lm_head, out and workspace must be 16-byte aligned");
+  const PagedModelWs w = carve_paged(h, workspace, rows, cu_seqlens != nullptr, parents != nullptr, batch, caches, m->vocab,
+                                     temperature >= 0.f);
+  if (!workspace || workspace_bytes < w.total) return fail(BLK_ERR_WORKSPACE, "model workspace missing or too small");
+  BLK_TRY(check_device(h));
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const int Hd = d.n_heads * d.head_dim, KVd = d.n_kv_heads * d.head_dim, cols = qkv_cols(d);
+  BLK_TRY(check_cuda(launch_embed(tokens, m->embed, rows, d.hidden * 2, m->vocab, w.act0, h->status, h->num_sms, s), "embedding"));
+  void* bufs[2] = {w.act0, w.act1};
+  for (int l = 0; l < m->n_layers; ++l) {
+    const blk_weights& lw = m->layers[l];
+    const void* x = bufs[l & 1];
+    BLK_TRY(check_cuda(launch_rmsnorm(x, lw.ln1_g, rows, d.hidden, d.eps, w.y, true, s), "input norm"));
+    // one projection's rows: queries, keys and values side by side
+    uint16_t* const qkv = static_cast<uint16_t*>(w.qkv);
+    TcGemmDesc g;
+    g.na = 1;
+    g.a[0] = {w.y, rows, 0};
+    g.nb = 3;
+    g.b[0] = {lw.wq, Hd, 0};
+    g.b[1] = {lw.wk, KVd, Hd};
+    g.b[2] = {lw.wv, KVd, Hd + KVd};
+    g.K = d.hidden;
+    g.bn = 128;  // whole heads
+    g.epi = Epi::kStore;
+    g.const_op = 2;
+    g.e.out = qkv;
+    g.e.ldo = cols;
+    BLK_TRY(tc(h, g, s, "QKV GEMM"));
+    const blk_head_rows q{qkv, cols, d.head_dim}, k{qkv + Hd, cols, d.head_dim}, v{qkv + Hd + KVd, cols, d.head_dim};
+    BLK_TRY(blk_paged_append(h, &q, &k, &v, rows, cu_seqlens, depths, batch, &caches[l], nullptr, lw.q_norm_g, lw.k_norm_g, &q,
+                             host_lens_max, stream));
+    const blk_head_rows o{w.o, Hd, d.head_dim};
+    BLK_TRY(blk_attn_paged(h, &q, rows, cu_seqlens, parents, batch, &caches[l], &o, w.attn_bytes ? w.attn : nullptr,
+                           w.attn_bytes, stream));
+    BLK_TRY(bf16_linear_resid(h, w.o, rows, Hd, lw.wo, d.hidden, x, false, w.mid, true, nullptr, nullptr, s, "o_proj GEMM",
+                              w.y, lw.ln2_g, w.ss2));
+    BLK_TRY(bf16_mlp_up(h, w.y, rows, &lw, w.neur, s, w.ss2, norm_parts(d.hidden, resid_bn(h, rows, d.hidden, Hd))));
+    BLK_TRY(bf16_linear_resid(h, w.neur, rows, d.ffn, lw.w_down, d.hidden, w.mid, true, bufs[(l + 1) & 1], false, nullptr,
+                              nullptr, s, "down GEMM"));
+  }
+  BLK_TRY(check_cuda(launch_rmsnorm(bufs[m->n_layers & 1], m->norm_g, rows, d.hidden, d.eps, w.y, true, s), "final norm"));
+  const bool probs = temperature >= 0.f;
+  BLK_TRY(bf16_rows(h, w.y, rows, d.hidden, m->lm_head, m->vocab, probs ? w.logits : out, s, "lm_head GEMM"));
+  if (!probs) return BLK_OK;
+  return check_cuda(launch_probs(w.logits, rows, m->vocab, temperature, static_cast<float*>(out), s), "probabilities");
 }
 
 blk_status blk_mlp(blk_handle* h, const void* resid, const void* h_normed, const blk_weights* w, int rows, void* out,

@@ -110,6 +110,10 @@ cudaError_t launch_paged_keep(void* const* kv, int n_layers, const PagedCache& c
                               const int* cu, const int* starts, int B, int rows, int Hkv, int row_bytes, int num_sms,
                               DevStatus* st, cudaStream_t s);
 
+// Rows of probabilities, fp32, of bf16 logits [rows, vocab] (vocab a multiple of 8): softmax(x / temperature), or
+// for temperature 0 one on the first largest logit.
+cudaError_t launch_probs(const void* logits, int rows, int vocab, float temperature, float* out, cudaStream_t s);
+
 // ---------------------------------------------------------------- embedding
 // out[r, :] = table[tokens[r], :] (row_bytes per row, a multiple of 16); ids outside
 // [0, vocab) give zero rows and set the status word to INVALID_ARG.

@@ -1,6 +1,6 @@
 """Speculative decoding over a paged cache: the append with norm and rotary (blk_paged_append), attention of
-chains and trees of new rows (blk_attn_paged), the verification of drafts (blk_verify_drafts) and the
-move of what is kept (blk_paged_keep), against fp64 references.
+chains and trees of new rows (blk_attn_paged), the verification of drafts (blk_verify_drafts), the
+move of what is kept (blk_paged_keep) and the model that calls them (blk_model_forward_paged), against fp64 references.
 
 Bounds count roundings. bf16 rounds by at most u = 2^-8 of the value (half a step), fp32 by 2^-24:
  - append: the fp32 chain of norm and rotary stays under 20 * 2^-24 * 1.5 (|a| + |b|) of a pair (a, b), a
@@ -15,8 +15,9 @@ import pytest
 import torch
 
 import oracle
-from llama_family_decoder_gb300 import BlkError, DecoderBlock
-from tests.helpers import np64
+from llama_family_decoder_gb300 import BlkError, DecoderBlock, set_wait_timeout_ns
+from llama_family_decoder_gb300.synth import Workload, make_model
+from tests.helpers import TOL, cfg_of, np64, rel_err, to_dev, weights_np
 
 pytestmark = pytest.mark.gpu
 
@@ -580,6 +581,29 @@ def test_streams_and_graphs():
     assert blk.last_status() == 0
 
 
+@pytest.mark.parametrize("H,Hkv,lens,rows", [(8, 2, [3000], 1),       # clusters, slots of the same rows
+                                             (8, 2, [3000], 60),      # clusters, two slots of rows
+                                             (32, 8, [3000] * 40, 1),  # equal stretches and a join
+                                             (32, 8, [900] * 24, 60)])
+def test_attn_paged_waits_that_run_out(H, Hkv, lens, rows):
+    """A limit far below the time of a tile: the waits give up, the status says so, the context lives on, and the next
+    call is right."""
+    trees = [tree_of(rows, b) for b in range(len(lens))]
+    blk, c, q, ks, vs, cu, parents = attn_case(H, Hkv, lens, trees, 64)
+    want = blk.attn_paged(q, c, cu, parents)
+    assert blk.last_status() == 0
+    set_wait_timeout_ns(300)
+    try:
+        blk.attn_paged(q, c, cu, parents)
+        torch.cuda.synchronize()
+    finally:
+        set_wait_timeout_ns(0)
+    assert blk.last_status() == 6
+    assert torch.equal(blk.attn_paged(q, c, cu, parents), want)
+    assert blk.last_status() == 0
+    check_attn(want, q, ks[:1], vs[:1], trees[:1], lens[:1])
+
+
 # ------------------------------------------------------------------ verification
 
 def verify_ref(target, draft, tokens, parents, u, u_next):
@@ -880,6 +904,151 @@ def test_a_run_of_steps_is_plain_decoding(page):
     outs = [blk.attn_paged(append(x, [[t] for t in last]), x) for x in (c, plain)]
     assert torch.equal(*outs)
     assert blk.last_status() == 0
+
+
+# ------------------------------------------------------------------ the model
+
+# The bar of a bf16 block (max|err| / RMS <= 2e-2) over two layers whose errors are independent
+TOL_MODEL_2 = TOL["bf16"] * np.sqrt(2)
+
+
+def model_of(act="silu", qk_norm=False, vocab=1024, seed=31, max_seq=256, **kw):
+    wl = Workload("paged_model", "bf16", 2, 8, 512, 8, 2, 128, 1000, act, qk_norm=qk_norm, seed=seed)
+    layers, embed, norm_g, lm_head, _ = make_model(wl, n_layers=2, vocab=vocab)
+    blk = DecoderBlock.from_workload(wl, max_seq=max_seq)
+    dev = [to_dev(w) for w in layers], embed.to(DEV), norm_g.to(DEV), lm_head.to(DEV)
+
+    def exact(tokens):
+        return oracle.model_forward(cfg_of(wl), [weights_np(w) for w in layers], np64(embed), np64(norm_g), np64(lm_head),
+                                    np.asarray([tokens]))[0]
+
+    return blk, dev, exact
+
+
+@pytest.mark.parametrize("act,qk_norm,page", [("silu", False, 64), ("xielu", True, 16)])
+def test_model_over_a_paged_cache(act, qk_norm, page):
+    blk, dev, exact = model_of(act, qk_norm)
+    r = np.random.default_rng(1)
+    prompts = [r.integers(0, 1024, n).tolist() for n in (5, 40)]
+    c = cache_of(blk, [0, 0], [80, 80], page)
+    caches = [c, blk.paged_cache(0, 0, shared=c)]
+    got = blk.model_forward_paged(ints(sum(prompts, [])), *dev, caches, cu_of([5, 40]))
+    assert rel_err(got, np.concatenate([exact(x) for x in prompts])) <= TOL_MODEL_2
+    blk.paged_keep(caches, ints([5, 40]))
+    trees = [tree_of(11, 1), tree_of(7, 2)]
+    new = [r.integers(0, 1024, len(t)).tolist() for t in trees]
+    cu, parents = cu_of([11, 7]), ints(sum(trees, []))
+    depths = ints([int(x) for t in trees for x in kin_of(t)[1]])
+    args = (ints(sum(new, [])), *dev, caches, cu, depths, parents)
+    got = blk.model_forward_paged(*args)
+    want = []
+    for prompt, t, x in zip(prompts, trees, new):
+        for i, kin in enumerate(kin_of(t)[0]):
+            want.append(exact(prompt + [x[j] for j in np.nonzero(kin)[0]])[-1])
+    assert rel_err(got, np.stack(want)) <= TOL_MODEL_2
+    assert c["lens"].tolist() == [5, 40] and blk.last_status() == 0
+    # a token each, without lists
+    one = blk.model_forward_paged(ints([x[0] for x in new]), *dev, caches)
+    assert rel_err(one, np.stack([exact(p + x[:1])[-1] for p, x in zip(prompts, new)])) <= TOL_MODEL_2
+    # probabilities: the logits' softmax. Each exponent is off by at most (|x| + max|x|) / T of fp32's half steps
+    # twice, the exponentials and their sum by a few more
+    x = np64(got)
+    for temperature in (1.0, 0.5, 3.0):
+        p = np64(blk.model_forward_paged(*args, temperature=temperature))
+        e = np.exp((x - x.max(-1, keepdims=True)) / temperature)
+        bound = 2.0 ** -24 * (4 * np.abs(x).max() / temperature + 40)
+        assert np.all(np.abs(p - e / e.sum(-1, keepdims=True)) <= bound * p)
+    hot = blk.model_forward_paged(*args, temperature=0)
+    assert torch.equal(hot.argmax(-1), got.float().argmax(-1)) and torch.equal(hot.sum(-1), torch.ones(18, device=DEV))
+    assert torch.all((hot == 0) | (hot == 1)) and blk.last_status() == 0
+
+
+def test_probabilities_of_rows_with_ties_and_infinities():
+    """One layer whose lm_head repeats rows: the first of equal logits; NaN rows stay NaN."""
+    blk, (layers, embed, norm_g, lm_head), _ = model_of(vocab=64, seed=3)
+    lm_head[32:] = lm_head[:32]
+    c = cache_of(blk, [0, 0], [8, 8], 16)
+    caches = [c, blk.paged_cache(0, 0, shared=c)]
+    logits = blk.model_forward_paged(ints([1, 2, 3]), layers, embed, norm_g, lm_head, caches, ints([0, 1, 3]))
+    hot = blk.model_forward_paged(ints([1, 2, 3]), layers, embed, norm_g, lm_head, caches, ints([0, 1, 3]), temperature=0)
+    assert torch.equal(logits[:, :32], logits[:, 32:])
+    assert hot.argmax(-1).tolist() == logits[:, :32].float().argmax(-1).tolist() and hot.sum().item() == 3
+    embed[2] = float("nan")
+    p = blk.model_forward_paged(ints([1, 2, 3]), layers, embed, norm_g, lm_head, caches, ints([0, 1, 3]), temperature=1)
+    assert torch.isfinite(p[0]).all() and torch.isnan(p[1:]).all()  # the third row sees the second
+
+
+@pytest.mark.parametrize("temperature", [0.0, 0.8])
+def test_model_steps_of_drafts(temperature):
+    """Prompts, then steps of model_verify. Without a temperature every new token is the target's largest, to the
+    error of its logits; with one it has a probability. The cache is that of the tokens that were kept."""
+    blk, dev, exact = model_of(seed=5)
+    r = np.random.default_rng(2)
+    history = [r.integers(0, 1024, n).tolist() for n in (9, 33)]
+    c = cache_of(blk, [0, 0], [120, 120], 16)
+    caches = [c, blk.paged_cache(0, 0, shared=c)]
+    p = blk.model_forward_paged(ints(sum(history, [])), *dev, caches, cu_of([9, 33]), temperature=temperature)
+    blk.paged_keep(caches, ints([9, 33]))
+    last = p[[8, 41]].argmax(-1).tolist()
+    start = [len(h) for h in history]
+    gen, kept = torch.Generator(device=DEV).manual_seed(1), 0
+    for step in range(5):
+        # drafts: a chain of the oracle's own greedy tokens, beside others
+        drafts, trees = [], []
+        for h, x in zip(history, last):
+            chain_tokens, seq = [x], h + [x]
+            for _ in range(3):
+                chain_tokens.append(int(exact(seq)[-1].argmax()))
+                seq = seq + chain_tokens[-1:]
+            drafts.append([chain_tokens[0], 17, chain_tokens[1], chain_tokens[2], 4, chain_tokens[3]])
+            trees.append([-1, 0, 0, 2, 2, 3])
+        cu = cu_of([6, 6])
+        depths = ints([int(x) for t in trees for x in kin_of(t)[1]])
+        counts, path, nxt = blk.model_verify(ints(sum(drafts, [])), *dev, caches, torch.rand(12, generator=gen, device=DEV),
+                                             torch.rand(2, generator=gen, device=DEV), cu, depths, ints(sum(trees, [])),
+                                             temperature=temperature)
+        for b in range(2):
+            n = int(counts[b])
+            history[b] += [drafts[b][x] for x in path[6 * b:6 * b + n].tolist()]
+            kept += n
+            last[b] = int(nxt[b])
+        assert c["lens"].tolist() == [len(h) for h in history]
+    assert blk.last_status() == 0
+    if temperature == 0:
+        assert kept > 2 * 5 + 10  # most drafts stay
+        for h, x, n in zip(history, last, start):
+            logits = exact(h + [x])
+            rms = np.sqrt(np.mean(logits ** 2))
+            for i in range(n, len(h)):
+                assert logits[i - 1].max() - logits[i - 1][h[i]] <= 2 * TOL_MODEL_2 * rms
+    # the next row over the cache of the steps is that of the whole sequence
+    got = blk.model_forward_paged(ints(last), *dev, caches)
+    assert rel_err(got, np.stack([exact(h + [x])[-1] for h, x in zip(history, last)])) <= TOL_MODEL_2
+
+
+def test_model_over_a_paged_cache_refusals():
+    blk, dev, _ = model_of()
+    c = blk.paged_cache(2, 32, 16)
+    caches = [c, blk.paged_cache(0, 0, shared=c)]
+    tok = ints([1, 2])
+    blk.model_forward_paged(tok, *dev, caches)
+    for kw, match in ((dict(caches=caches[:1]), "each layer"), (dict(caches=[c, blk.paged_cache(2, 32, 16)]), "share"),
+                      (dict(parents=ints([-1, -1])), "depths"), (dict(temperature=-1.0), "temperature"),
+                      (dict(temperature=float("nan")), "temperature"), (dict(tokens=tok.long()), "tokens"),
+                      (dict(tokens=tok[:1]), "row per sequence"), (dict(host_lens_max=33), "CACHE_FULL"),
+                      (dict(out=torch.empty(2, 1024, device=DEV)), "out")):
+        with pytest.raises((BlkError, ValueError), match=match):
+            blk.model_forward_paged(**{**dict(tokens=tok, layers=dev[0], embed=dev[1], norm_g=dev[2], lm_head=dev[3], caches=caches), **kw})
+    for kw in (dict(attn_gate=True), dict(dtype="f32", d=64)):
+        other = block(4, 2, **kw)
+        cc = other.paged_cache(1, 32, 16)
+        w = torch.zeros(8, other.desc.hidden, dtype=cc["k"].dtype, device=DEV)
+        with pytest.raises(BlkError, match="UNSUPPORTED"):
+            other.model_forward_paged(ints([1]), [dict()], w, w[0].contiguous(), w, [cc])
+    assert blk.last_status() == 0
+    blk.model_forward_paged(ints([1, 5000]), *dev, caches)
+    assert blk.last_status() == 1
+    assert torch.isfinite(blk.model_forward_paged(tok, *dev, caches)).all()
 
 
 # ------------------------------------------------------------------ refusals
