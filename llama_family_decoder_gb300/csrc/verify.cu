@@ -10,13 +10,13 @@
 //
 // The answers are whole numbers, so what decides them has to be known far better than fp32: a sum
 // over a vocabulary in fp32 would move about one next token in a thousand. p - C q is held as two
-// fp32 numbers (its products and sums with their errors: Dekker 1971, Knuth 1969), sums of 16 of them and then
+// fp32 numbers (its products and sums with their errors: Dekker 1971, Knuth 1969), sums of 8 of them and then
 // of a warp's likewise, to about 2^-45; everything from there on, and every test, is fp64.
 //
 // A cluster of CTAs takes a sequence. Warp 0 of each walks the tree, all of them alike, two nodes a lane, from the
 // candidates' p and q values gathered beforehand in one round of loads; fp64 is slow here (two lanes
 // a cycle and SM), so no other warp does any of it. A pass over the vocabulary is shared: CTA r takes the r-th run
-// of segments of 512 values, a warp a segment, and the CTAs' sums meet in distributed shared memory. The pass
+// of segments of 256 values, a warp a segment, and the CTAs' sums meet in distributed shared memory. The pass
 // that ends the walk leaves its segments' sums, in which the next token's segment is found; a warp looks
 // through that one. Latency-bound: a launch, three dependent rounds of loads, and per pass a row from HBM (from the
 // second on, L2) and a cluster barrier.
@@ -28,8 +28,9 @@ namespace {
 
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
-constexpr int kSeg = 512;        // values of a segment: 16 a lane
-constexpr int kCtaSegs = 1024;   // segments whose sums a CTA keeps
+constexpr int kPer = 8;          // values of a segment that a lane has
+constexpr int kSeg = 32 * kPer;
+constexpr int kCtaSegs = 2048;   // segments whose sums a CTA keeps
 constexpr int kMaxCluster = 8;
 
 struct VerifyParams {
@@ -98,35 +99,35 @@ __device__ __forceinline__ double scan(double x, int lane) {
   return x;
 }
 
-// 16 consecutive values of a lane, from element `at` of a row, those past the vocabulary 0.
-__device__ __forceinline__ void load16(const float* row, int at, int vocab, bool wide, float (&x)[16]) {
-  if (wide && at + 16 <= vocab) {
+// kPer consecutive values of a row, from element `at`, those past the vocabulary 0.
+__device__ __forceinline__ void load_values(const float* row, int at, int vocab, bool wide, float (&x)[kPer]) {
+  if (wide && at + kPer <= vocab) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < kPer / 4; ++i) {
       const float4 v = __ldg(reinterpret_cast<const float4*>(row + at) + i);
       x[4 * i] = v.x, x[4 * i + 1] = v.y, x[4 * i + 2] = v.z, x[4 * i + 3] = v.w;
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) x[i] = at + i < vocab ? __ldg(row + at + i) : 0.f;
+    for (int i = 0; i < kPer; ++i) x[i] = at + i < vocab ? __ldg(row + at + i) : 0.f;
   }
 }
 
-// A lane's 16 values of a segment: what is left of the target's distribution at node cur.
+// A lane's values of a segment: what is left of the target's distribution at node cur.
 struct Row {
   const float *p, *q;
   bool wide_p, wide_q;
 };
 __device__ __forceinline__ void left_values(const Row& row, const Order& o, const int* gone, int vocab, int seg, int lane,
-                                            Two (&v)[16]) {
-  const int at = seg * kSeg + lane * 16;
-  float x[16];
-  load16(row.p, at, vocab, row.wide_p, x);
+                                            Two (&v)[kPer]) {
+  const int at = seg * kSeg + lane * kPer;
+  float x[kPer];
+  load_values(row.p, at, vocab, row.wide_p, x);
   if (o.C.hi > 0.f) {
-    float y[16];
-    load16(row.q, at, vocab, row.wide_q, y);
+    float y[kPer];
+    load_values(row.q, at, vocab, row.wide_q, y);
 #pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] = left_of(x[i], y[i], o.C);
+    for (int i = 0; i < kPer; ++i) v[i] = left_of(x[i], y[i], o.C);
     return;
   }
   if (o.n_gone > 0) {
@@ -134,22 +135,22 @@ __device__ __forceinline__ void left_values(const Row& row, const Order& o, cons
     for (int g0 = 0; g0 < o.n_gone; g0 += 32) {
       const int x_at = g0 + lane < o.n_gone ? gone[g0 + lane] - seg * kSeg : -1;
       for (unsigned in = __ballot_sync(0xffffffffu, x_at >= 0 && x_at < kSeg); in; in &= in - 1) {
-        const int i = __shfl_sync(0xffffffffu, x_at, __ffs(in) - 1) - lane * 16;
+        const int i = __shfl_sync(0xffffffffu, x_at, __ffs(in) - 1) - lane * kPer;
 #pragma unroll
-        for (int k = 0; k < 16; ++k)
+        for (int k = 0; k < kPer; ++k)
           if (k == i) x[k] = 0.f;
       }
     }
   }
 #pragma unroll
-  for (int i = 0; i < 16; ++i) v[i] = Two{x[i], 0.f};
+  for (int i = 0; i < kPer; ++i) v[i] = Two{x[i], 0.f};
 }
-__device__ __forceinline__ Two sum16(const Two (&v)[16]) {
-  Two s[8];
+__device__ __forceinline__ Two sum_of(const Two (&v)[kPer]) {
+  Two s[kPer / 2];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) s[i] = add(v[2 * i], v[2 * i + 1]);
+  for (int i = 0; i < kPer / 2; ++i) s[i] = add(v[2 * i], v[2 * i + 1]);
 #pragma unroll
-  for (int n = 4; n > 0; n /= 2)
+  for (int n = kPer / 4; n > 0; n /= 2)
 #pragma unroll
     for (int i = 0; i < n; ++i) s[i] = add(s[i], s[i + n]);
   return s[0];
@@ -185,9 +186,9 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const __grid_consta
   auto pass = [&](const Order& o) {
     const Row row = row_of(o.cur);
     for (int seg = s0 + warp; seg < s1; seg += kWarps) {
-      Two v[16];
+      Two v[kPer];
       left_values(row, o, sh.gone, p.vocab, seg, lane, v);
-      Two s = sum16(v);
+      Two s = sum_of(v);
 #pragma unroll
       for (int k = 16; k > 0; k >>= 1)
         s = add(s, Two{__shfl_xor_sync(0xffffffffu, s.hi, k), __shfl_xor_sync(0xffffffffu, s.lo, k)});
@@ -343,22 +344,22 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const __grid_consta
         run = next;
       }
     }
-    Two v[16];
+    Two v[kPer];
     left_values(row_of(o.cur), o, sh.gone, p.vocab, seg, lane, v);
-    const double mine = value_of(sum16(v)), here = scan(mine, lane);
+    const double mine = value_of(sum_of(v)), here = scan(mine, lane);
     const unsigned past = __ballot_sync(0xffffffffu, run + here > want);
     const int at = past ? __ffs(past) - 1 : 31;
     run += __shfl_sync(0xffffffffu, here - mine, at);
-    Two one{0.f, 0.f};  // lane i < 16: value i of that lane
+    Two one{0.f, 0.f};  // lane i < kPer: value i of that lane
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
+    for (int i = 0; i < kPer; ++i) {
       const Two x{__shfl_sync(0xffffffffu, v[i].hi, at), __shfl_sync(0xffffffffu, v[i].lo, at)};
       if (lane == i) one = x;
     }
     const double here1 = scan(value_of(one), lane);
-    const unsigned found = __ballot_sync(0xffffffffu, lane < 16 && run + here1 > want) & 0xffffu;
-    const int first = seg * kSeg + at * 16;
-    if (lane == 0) p.next[b] = min(max(found ? first + __ffs(found) - 1 : min(first + 15, p.vocab - 1), 0), p.vocab - 1);
+    const unsigned found = __ballot_sync(0xffffffffu, lane < kPer && run + here1 > want);
+    const int first = seg * kSeg + at * kPer;
+    if (lane == 0) p.next[b] = min(max(found ? first + __ffs(found) - 1 : min(first + kPer - 1, p.vocab - 1), 0), p.vocab - 1);
   }
   __syncwarp();
   cluster_wait();
