@@ -45,6 +45,7 @@ constexpr float kRescaleLog2 = 8.0f;
 constexpr float kScaleLog2 = 1.4426950408889634f * 0.08838834764831845f;  // log2(e) / sqrt(128)
 constexpr int kNoBox = -2;             // a box that no row needs; entries below -1 are read as -1
 constexpr unsigned long long kDrainNs = 2000000000ULL;
+struct Join;  // see below
 struct AttnParams {
   CUtensorMap tk, tv;  // [n_pages * Hkv * page_size, 128] bf16, boxes of 64 channels x `box` rows
   CUtensorMap tq_map;  // the query rows: boxes of 64 channels x G heads x tq rows
@@ -62,6 +63,7 @@ struct AttnParams {
   int unit_cost;  // what a unit counts for on the line besides its tiles, before them
   float2* ml;     // partial results [2 grid][slots][128]: (reference, sum)
   float* acc;     // ... [2 grid][slots][32][128][4]: four channels of each row side by side
+  Join* joins;    // [grid]
   int o_wide;     // the outputs' rows start on 32-byte boundaries
   DevStatus* status;
   unsigned long long wait_ns;
@@ -292,6 +294,21 @@ struct Walk {
   __device__ __forceinline__ int node0(const AttnParams& p, int g) const { return (t * p.slots + g) * p.tq; }
 };
 
+// What the second kernel joins at stretch c, written by its CTA: the unit that the stretch goes on with, if stretch
+// c - 1 has its first tile; its parts are those of stretches c - 1 (number `first`) to `last`. last < 0: nothing.
+struct Join {
+  Seq seq;
+  int kvh, t, first, last;
+};
+__device__ __forceinline__ Join join_of(const AttnParams& p, const Stretch& s, const Walk& w, int c) {
+  Join j{w.seq, w.kvh, w.t, 0, -1};
+  const int tile0 = s.lo - w.at + p.unit_cost;  // the unit's first tile on the line
+  if (!w.on() || w.j0 == 0 || tile0 / s.per != c - 1) return j;  // no unit goes over, or an earlier stretch has it
+  j.last = (tile0 + w.tiles - 1) / s.per;
+  j.first = s.lo - w.at <= (c - 1) * s.per ? 2 * (c - 1) : 2 * (c - 1) + 1;  // was it that stretch's first unit?
+  return j;
+}
+
 __device__ __forceinline__ unsigned long long bits_from(int lo) {  // bits lo ..
   return lo <= 0 ? ~0ull : lo >= 64 ? 0ull : ~0ull << lo;
 }
@@ -322,10 +339,9 @@ struct Joined {
       o[3] = fmaf(wt, a[j].w, o[3]);
     }
   }
-  __device__ __forceinline__ void store(const AttnParams& p, const Walk& w, int node, int head, int ch) const {
+  __device__ __forceinline__ void store(const AttnParams& p, int row, int head, int ch) const {
     const float inv = 1.f / l;
-    __nv_bfloat16* const to = static_cast<__nv_bfloat16*>(p.o.ptr) + (w.seq.row0 + node) * p.o.row +
-                              (long long)(w.kvh * p.G + head) * p.o.head + 4 * ch;
+    __nv_bfloat16* const to = static_cast<__nv_bfloat16*>(p.o.ptr) + row * p.o.row + head * p.o.head + 4 * ch;
     *reinterpret_cast<uint2*>(to) = make_uint2(pack_bf16x2(o[0] * inv, o[1] * inv), pack_bf16x2(o[2] * inv, o[3] * inv));
   }
 };
@@ -414,16 +430,18 @@ __global__ void __launch_bounds__(Cfg<NS, SPLIT>::kThreads, 1) attn_paged_kernel
     tmem_relinquish();
   }
   pdl_wait();  // queries, cache, lengths and lists come from earlier kernels
-  // only now: what earlier kernels wrote is then there for the second kernel too, which looks its part up
-  // while this one runs
   pdl_launch_dependents();
   if (warp == 0) {
     if constexpr (CL) {
       const Walk w(p, blockIdx.x / p.cluster, cluster_ctarank(), p.cluster, lane);
       if (lane == 0) *begin = w;
     } else {
-      const Walk w(p, stretch_of(p, blockIdx.x, lane));
-      if (lane == 0) *begin = w;
+      const Stretch s = stretch_of(p, blockIdx.x, lane);
+      const Walk w(p, s);
+      if (lane == 0) {
+        *begin = w;
+        p.joins[blockIdx.x] = join_of(p, s, w, blockIdx.x);
+      }
     }
   }
   if (warp == 2 && blockIdx.x == 0) {  // what the lists say that they should not
@@ -923,7 +941,7 @@ __global__ void __launch_bounds__(Cfg<NS, SPLIT>::kThreads, 1) attn_paged_kernel
             }
             x.take(ml, a);
           }
-          x.store(p, w, w.node0(p, g) + nd, r - nd * p.G, ch);
+          x.store(p, w.seq.row0 + w.node0(p, g) + nd, w.kvh * p.G + r - nd * p.G, ch);
         }
       }
     }
@@ -939,50 +957,39 @@ __global__ void __launch_bounds__(Cfg<NS, SPLIT>::kThreads, 1) attn_paged_kernel
 
 // ------------------------------------------------------------------ joining partial results
 
-// Block (c - 1, y): the unit that stretch c goes on with, if stretch c - 1 has its first tile: the parts of
-// stretches c - 1 .. e, in that order.
+// Block (c - 1, y): what stretch c says (Join), in the order of the parts; a thread has four channels of a row, a
+// warp 32 rows, PARTS parts are under way at a time.
 constexpr int kJoinThreads = 256;
 template <int PARTS>
 __global__ void __launch_bounds__(kJoinThreads) attn_paged_join_kernel(const __grid_constant__ AttnParams p) {
-  __shared__ Stretch sh;
-  const int lane = threadIdx.x & 31, c = blockIdx.x + 1;
-  if (threadIdx.x < 32) {
-    const Stretch s = stretch_of(p, c, lane);
-    if (lane == 0) sh = s;
-  }
-  __syncthreads();
-  const Stretch s = sh;
-  const Walk w(p, s);
   pdl_launch_dependents();
-  pdl_wait();  // for the partial results; the lists are there (see the other kernel)
-  const int tile0 = s.lo - w.at + p.unit_cost;  // the unit's first tile on the line
-  if (!w.on() || w.j0 == 0 || tile0 / s.per != c - 1) return;  // no unit goes over, or an earlier block joins it
-  const int e = (tile0 + w.tiles - 1) / s.per;
-  // a thread has four channels of a row, a warp 32 rows; PARTS parts are under way at a time
-  const int first = s.lo - w.at <= (c - 1) * s.per ? 2 * (c - 1) : 2 * (c - 1) + 1;  // that stretch's first unit?
+  pdl_wait();
+  const int lane = threadIdx.x & 31, c = blockIdx.x + 1;
+  const Join w = p.joins[c];
+  if (w.last < 0) return;
   const int warp = blockIdx.y * (kJoinThreads / 32) + (threadIdx.x >> 5), warps = gridDim.y * (kJoinThreads / 32);
   for (int i = warp; i < p.slots * (kBQ / 32) * (kD / 4); i += warps) {
     const int ch = i % (kD / 4), quarter = i / (kD / 4) % (kBQ / 32), g = i / (kD / 4) / (kBQ / 32);
-    const int r = quarter * 32 + lane, nd = r / p.G, node = w.node0(p, g) + nd;
+    const int r = quarter * 32 + lane, nd = r / p.G, node = (w.t * p.slots + g) * p.tq + nd;
     if (nd >= p.tq || node >= w.seq.n) continue;
     Joined x;
-    for (int k0 = c - 1; k0 <= e; k0 += PARTS) {
+    for (int k0 = c - 1; k0 <= w.last; k0 += PARTS) {
       float2 ml[PARTS];
       float4 a[PARTS];
 #pragma unroll
       for (int j = 0; j < PARTS; ++j) {
         const int k = k0 + j;
-        const size_t at = (size_t)(k == c - 1 ? first : 2 * k) * p.slots + g;
+        const size_t at = (size_t)(k == c - 1 ? w.first : 2 * k) * p.slots + g;
         ml[j] = make_float2(-INFINITY, 0.f);
         a[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (k <= e) {
+        if (k <= w.last) {
           ml[j] = p.ml[at * kBQ + r];
           a[j] = reinterpret_cast<const float4*>(p.acc + at * kBQ * kD)[ch * kBQ + r];
         }
       }
       x.take(ml, a);
     }
-    x.store(p, w, node, r - nd * p.G, ch);
+    x.store(p, w.seq.row0 + node, w.kvh * p.G + r - nd * p.G, ch);
   }
 }
 
@@ -1061,7 +1068,7 @@ size_t attn_paged_ws_bytes(int rows, int B, int H, int Hkv, bool cu, bool tree, 
   const Plan pl = plan_of(rows, B, H, Hkv, cu, tree, capacity, window, num_sms);
   if (!pl.fits) return kAttnPagedTooLong;
   if (pl.cluster > 1) return 0;
-  return (size_t)2 * pl.grid * pl.slots * kBQ * (sizeof(float2) + kD * sizeof(float));
+  return (size_t)2 * pl.grid * pl.slots * kBQ * (sizeof(float2) + kD * sizeof(float)) + pl.grid * sizeof(Join);
 }
 
 cudaError_t launch_attn_paged(const HeadRows& q, const PagedCache& c, const HeadRows& o, int rows, const int* cu,
@@ -1108,6 +1115,7 @@ cudaError_t launch_attn_paged(const HeadRows& q, const PagedCache& c, const Head
   const int smem = two ? Cfg<2>::kSmem : Cfg<1>::kSmem, threads = two ? Cfg<2>::kThreads : Cfg<1>::kThreads;
   p.acc = static_cast<float*>(ws);
   p.ml = reinterpret_cast<float2*>(p.acc + (size_t)2 * pl.grid * pl.slots * kBQ * kD);
+  p.joins = reinterpret_cast<Join*>(p.ml + (size_t)2 * pl.grid * pl.slots * kBQ);
   const auto kernel = two ? attn_paged_kernel<2, false, false> : attn_paged_kernel<1, false, false>;
   static std::atomic<unsigned long long> configured[2];
   cudaError_t e = set_smem_limit_once(reinterpret_cast<const void*>(kernel), smem, configured[two]);
