@@ -454,7 +454,8 @@ blk_status blk_attn_decode_kv4(blk_handle* h, const blk_head_rows* q, const blk_
  * the slots from lens[b] on, and only blk_paged_keep moves lens. pages and lens are device int32,
  * pages [batch, max_pages]; entries that no row of a call needs are not looked at. An entry that
  * is needed and is not in [0, n_pages) sets the status word to INVALID_ARG; no memory outside the
- * cache is read or written. Two sequences may share pages that no row is written to. */
+ * cache is read or written. Two sequences may share pages that no row is written to. Slots from 2^31 - 2^16 on
+ * lie behind any page list. */
 typedef struct {
   void *k, *v;
   const int* pages;
@@ -556,7 +557,7 @@ blk_status blk_paged_keep(blk_handle* h, const blk_paged_cache* caches, int n_ca
  * tokens [rows] device int32, packed by cu_seqlens; each layer appends its keys and values to its
  * cache (host array of n_layers caches that share pages, lens and sizes) at positions lens[b] + depths[row]
  * and attends, by parents, as blk_paged_append and blk_attn_paged do; lens does not move (blk_paged_keep).
- * A tree's rows need depths. temperature < 0: out is the logits, bf16 [rows, vocab]; > 0: the probabilities
+ * A tree's rows need depths; no two layers may have the same k or v. temperature < 0: out is the logits, bf16 [rows, vocab]; > 0: the probabilities
  * softmax(logits / temperature), fp32 [rows, vocab], what blk_verify_drafts takes; 0: all of it on the
  * largest logit (the first of several). The softmax is of the bf16 logits, in fp32. A token outside
  * [0, vocab) embeds as zeros and sets the status word to INVALID_ARG.

@@ -1676,6 +1676,24 @@ blk_status check_paged(const blk_paged_cache* c) {
   return BLK_OK;
 }
 
+// The caches of a model's layers: one list, own contents.
+blk_status check_paged_layers(const blk_paged_cache* caches, int n) {
+  std::vector<void*> seen;
+  for (int i = 0; i < n; ++i) {
+    const blk_paged_cache& c = caches[i];
+    BLK_TRY(check_paged(&c));
+    if (c.pages != caches[0].pages || c.lens != caches[0].lens || c.n_pages != caches[0].n_pages ||
+        c.page_size != caches[0].page_size || c.max_pages != caches[0].max_pages)
+      return fail(BLK_ERR_INVALID_ARG, "caches: they must share pages, lens and sizes");
+    seen.push_back(c.k);
+    seen.push_back(c.v);
+  }
+  std::sort(seen.begin(), seen.end());
+  if (std::adjacent_find(seen.begin(), seen.end()) != seen.end())
+    return fail(BLK_ERR_INVALID_ARG, "caches: two have the same k or v");
+  return BLK_OK;
+}
+
 PagedCache paged_cache(const blk_paged_cache* c) {
   int shift = 0;
   while ((1 << shift) < c->page_size) ++shift;
@@ -1833,20 +1851,12 @@ blk_status blk_paged_keep(blk_handle* h, const blk_paged_cache* caches, int n_ca
   const size_t row_bytes = (size_t)d.head_dim * esize(d);
   if (row_bytes % 16) return fail(BLK_ERR_UNSUPPORTED, "paged keep: rows of 16-byte multiples");
   try {
+    BLK_TRY(check_paged_layers(caches, n_caches));
     std::vector<void*> kv;
     for (int i = 0; i < n_caches; ++i) {
-      const blk_paged_cache& c = caches[i];
-      BLK_TRY(check_paged(&c));
-      if (c.pages != caches[0].pages || c.lens != caches[0].lens || c.n_pages != caches[0].n_pages ||
-          c.page_size != caches[0].page_size || c.max_pages != caches[0].max_pages)
-        return fail(BLK_ERR_INVALID_ARG, "caches: they must share pages, lens and sizes");
-      kv.push_back(c.k);
-      kv.push_back(c.v);
+      kv.push_back(caches[i].k);
+      kv.push_back(caches[i].v);
     }
-    std::vector<void*> seen(kv);
-    std::sort(seen.begin(), seen.end());
-    if (std::adjacent_find(seen.begin(), seen.end()) != seen.end())
-      return fail(BLK_ERR_INVALID_ARG, "caches: two have the same k or v");
     if (batch == 0) return BLK_OK;
     if (!counts) return fail(BLK_ERR_INVALID_ARG, "counts is NULL");
     const int* const lens = caches[0].lens;
@@ -1921,14 +1931,12 @@ blk_status blk_model_forward_paged(blk_handle* h, const blk_model* m, const int*
   BLK_TRY(check_batch(rows, batch, cu_seqlens));
   if (parents && !depths) return fail(BLK_ERR_INVALID_ARG, "the rows of a tree need depths");
   if (temperature != temperature) return fail(BLK_ERR_INVALID_ARG, "temperature is NaN");
-  for (int l = 0; l < m->n_layers; ++l) {
-    const blk_paged_cache& c = caches[l];
-    BLK_TRY(check_paged(&c));
-    BLK_TRY(check_weights(d, &m->layers[l]));
-    if (c.pages != caches[0].pages || c.lens != caches[0].lens || c.n_pages != caches[0].n_pages ||
-        c.page_size != caches[0].page_size || c.max_pages != caches[0].max_pages)
-      return fail(BLK_ERR_INVALID_ARG, "caches: they must share pages, lens and sizes");
+  try {
+    BLK_TRY(check_paged_layers(caches, m->n_layers));
+  } catch (const std::exception&) {
+    return fail(BLK_ERR_INVALID_ARG, "caches: out of host memory");
   }
+  for (int l = 0; l < m->n_layers; ++l) BLK_TRY(check_weights(d, &m->layers[l]));
   if (rows == 0 || batch == 0) return BLK_OK;
   if (!tokens || !out) return fail(BLK_ERR_INVALID_ARG, "tokens and out must be non-NULL");
   if (!aligned16(m->embed) || !aligned16(m->norm_g) || !aligned16(m->lm_head) || !aligned16(out) || !aligned16(workspace))

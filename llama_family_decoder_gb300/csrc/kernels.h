@@ -71,10 +71,10 @@ struct PagedCache {
   int n_pages, page_shift, max_pages;
 };
 
-// Slots of a sequence's page list; at most 2^31 - 1.
+// Slots of a sequence's page list; so few below 2^31 that the next tiles' numbers are ints too.
 __host__ __device__ inline long long page_slots(const PagedCache& c) {
   const long long n = (long long)c.max_pages << c.page_shift;
-  return n < 0x7fffffffll ? n : 0x7fffffffll;
+  return n < 0x7fff0000ll ? n : 0x7fff0000ll;
 }
 
 // Rows cu[b] .. cu[b + 1] of sequence b (cu null: row b): norm (gains null: none) and rotary (table

@@ -375,6 +375,21 @@ def test_attn_paged_split_keys(lens, H, Hkv, rows):
     assert torch.equal(out, blk.attn_paged(q, c, cu, parents))  # the same sums in the same order
 
 
+@pytest.mark.parametrize("window", [0, 700])
+@pytest.mark.parametrize("kind", ["chain", "tree"])
+def test_attn_paged_many_ragged_sequences(kind, window):
+    """More units than CTAs, from none to 64 rows over none to 6000 slots: stretches that end anywhere in them."""
+    r = np.random.default_rng(4)
+    rows = [int(t) for t in r.choice([0, 1, 1, 2, 16, 17, 33, 64], 90)]
+    lens = [int(n) for n in r.choice([0, 1, 50, 64, 333, 1000], 90)]
+    lens[7], rows[7], lens[50], rows[50] = 6000, 64, 4100, 1
+    trees = [chain(t) if kind == "chain" else tree_of(t, b) if t else [] for b, t in enumerate(rows)]
+    blk, c, q, ks, vs, cu, parents = attn_case(8, 2, lens, trees, 32, window)
+    out = blk.attn_paged(q, c, cu, parents if kind == "tree" else None)
+    assert blk.last_status() == 0
+    check_attn(out, q, ks, vs, trees, lens, window)
+
+
 def test_attn_paged_chain_is_a_tree_of_one_branch():
     trees = [chain(t) for t in (64, 5, 1)]
     blk, c, q, ks, vs, cu, parents = attn_case(8, 2, [90, 0, 400], trees, 16)
@@ -497,6 +512,44 @@ def test_attn_paged_bad_lists_stay_in_bounds():
         assert blk.last_status() == code
         assert torch.all(out[:64] == 5) and torch.equal(out[64:], want[64:])
     assert blk.attn_paged(q[:0], c, ints([0, 0, 0])).shape == (0, 4, D)
+    assert blk.last_status() == 0
+
+
+def test_attn_paged_at_the_last_slots():
+    """A page list of 2^31 slots, all of them one page; a window leaves the last ones of it."""
+    blk = block(2, 1, sliding_window=100)
+    c = blk.paged_cache(1, 64, 64)
+    c["pages"] = torch.zeros(1, 2**25, dtype=torch.int32, device=DEV)
+    for x in "kv":
+        c[x].copy_(randn(5 + ord(x), 1, 1, 64, D))
+    q, end = randn(1, 3, 2, D), 2**31 - 2**16
+    c["lens"].fill_(end - 3)
+    out = blk.attn_paged(q, c, ints([0, 3]))
+    assert blk.last_status() == 0
+    k, v = ([c[x][0].transpose(0, 1)[(torch.arange(end - 110, end) % 64).to(DEV)]] for x in "kv")
+    check_attn(out, q, k, v, [chain(3)], [107], 100)
+    for n in (end - 2, 2**31 - 4, 2**31 - 1):
+        c["lens"].fill_(n)
+        kept = blk.attn_paged(q, c, ints([0, 3]), out=torch.full_like(q, 2.0))
+        assert blk.last_status() == 4 and torch.all(kept == 2)
+
+
+@pytest.mark.parametrize("kind", ["chain", "tree"])
+def test_attn_paged_thousands_of_sequences(kind):
+    """More of them than a warp looks up at once, most without rows."""
+    rows, lens = [0] * 3001, [3] * 3001
+    for b in (0, 31, 127, 128, 129, 1000, 2999, 3000):
+        rows[b], lens[b] = 1 + b % 40, b
+    trees = [chain(t) if kind == "chain" else tree_of(t, b) if t else [] for b, t in enumerate(rows)]
+    blk, c, q, ks, vs, cu, parents = attn_case(8, 2, lens, trees, 64)
+    out = blk.attn_paged(q, c, cu, parents if kind == "tree" else None)
+    assert blk.last_status() == 0
+    check_attn(out, q, ks, vs, trees, lens)
+    one = randn(3, 3001, 8, D)
+    out = blk.attn_paged(one, c)
+    for b in (0, 31, 128, 1000, 1001, 2999, 3000):
+        check_attn(out[b:b + 1], one[b:b + 1], [slots_of(c, "k", b, lens[b] + 1)], [slots_of(c, "v", b, lens[b] + 1)],
+                   [chain(1)], [lens[b]])
     assert blk.last_status() == 0
 
 
@@ -1010,6 +1063,7 @@ def test_model_over_a_paged_cache_refusals():
     tok = ints([1, 2])
     blk.model_forward_paged(tok, *dev, caches)
     for kw, match in ((dict(caches=caches[:1]), "each layer"), (dict(caches=[c, blk.paged_cache(2, 32, 16)]), "share"),
+                      (dict(caches=[c, c]), "same k or v"),
                       (dict(parents=ints([-1, -1])), "depths"), (dict(temperature=-1.0), "temperature"),
                       (dict(temperature=float("nan")), "temperature"), (dict(tokens=tok.long()), "tokens"),
                       (dict(tokens=tok[:1]), "row per sequence"), (dict(host_lens_max=33), "CACHE_FULL"),
