@@ -5,24 +5,40 @@
 //
 // Bound by reading the cache once. All heads of a KV head and all new rows of a sequence share its
 // keys, so they fold into the rows of one matrix tile: row r of a slot is head r % G of row r / G (G = H / Hkv),
-// a slot has 128 of them, and a CTA one or two slots that share each tile of 64 keys. The tensor core's
-// M = 128 costs the same for one row as for 128 and stays below the time a tile takes to arrive (64 keys of K and V
-// are 32 KB: 0.73 us at an SM's share of 6.8 TB/s; the two products take 0.3 us of it).
+// a slot has 128 of them. A CTA has two slots. Where a sequence has more than 96 such rows on average they hold
+// the two halves of its rows and share each tile of 64 keys (units of one slot would read the cache once per 128
+// rows: trees of 64 nodes 72 us against 56); else they take the units in turn, so that one's outputs and first tiles run
+// beside the other's (256 sequences of up to 300 slots, a token each, 62.7 -> 55.7 us; of up to 20 48 -> 37; 64 of up to
+// 8192 199 -> 195). The tensor core's M = 128 costs the same for one row as for 128: 620 cycles a tile and slot, a
+// tile (32 KB) takes 1390 to arrive at an SM's share of 6.8 TB/s.
 //
-// Work is a line of key tiles: units (sequence, KV head, rows of the slots) one after the other, each as
+// Large batches: work is a line of key tiles, units (sequence, KV head, rows of the slots) one after the other, each as
 // many tiles as it has keys. The CTAs, one per SM, take equal stretches of it, whatever the sequences'
 // lengths; a unit that lies in several stretches leaves partial results (unnormalised outputs, the
 // running maximum and sum), which a second kernel joins in the order of the keys, so results do not
-// depend on timing. Lengths are on the device: every CTA adds up the line by itself.
+// depend on timing. Lengths are on the device: every CTA adds up the line by itself, and the CTA that goes on with
+// another's unit writes down what is to be joined there. (Whole units per CTA instead: trees 73 us.)
+// Small batches (plan_of): a cluster of CTAs takes a unit, equal shares of its keys each, joined in the
+// cluster's shared memory: no second kernel, one token over 4000 slots 12.2 -> 9.0 us. With few rows a CTA's two
+// slots hold the same rows and take its tiles in turn there.
 //
-// Warp 0 loads: its lanes look up the pages of the next 32 boxes (a box: the rows of a page in a tile)
-// and each issues a TMA copy of a box's half of K or V, 128-byte swizzled, into rings of 16 KB stages. Warp 1 (and 2 for the second slot) issues the products: S = Q K^T of tile j + 1 into one of
-// two TMEM buffers, then O += P V of tile j with P from TMEM. Four warps a slot hold a row a thread: scores
+// Warps 0 and 3 load K and V: their lanes look up the pages of the next 32 boxes (a box: the rows of a page in a tile)
+// and each issues a TMA copy of a box's half, 128-byte swizzled, into a ring of 16 KB stages. (One warp for
+// both: pages of 16 19.7 us against 17.2.) Warps 1 and 2, one a slot, issue the products as they
+// become possible: S = Q K^T up to two tiles ahead into TMEM buffers, O += P V with P from TMEM, and
+// load the next unit's queries. All its lanes go through that loop and an elected one issues, so that the
+// descriptors stay in uniform registers: from one lane's own branch each MMA cost some 100 cycles more (64 ragged
+// tokens 238 us against 201). Four warps a slot hold a row a thread: scores
 // from TMEM, the running softmax in the log2 domain with a reference that moves only when a
-// score passes it by 2^8 (exact: softmax does not depend on it), P as bf16 over the scores; and before
-// a unit its queries to shared memory, after it the outputs.
+// score passes it by 2^8 (exact: softmax does not depend on it), P as bf16 over the scores, and the outputs.
 // Every wait is bounded; on expiry the CTA records a timeout, drains its own copies and MMAs, frees its
 // TMEM and returns.
+//
+// Measured (8 KV heads of 4 query heads, a graph of calls on cold caches): 64 sequences of up to 8192 slots, a token
+// each, 195 us = 6.6 TB/s, the cache's bandwidth; 16 trees of up to 64 nodes over up to 4096 slots 56 us: two full slots
+// take 1900 cycles a tile (scores 768, bound by shared memory's 128 bytes a cycle, products 512, and exponentials
+// that run while the pipe waits), one 1240; 32 chains of 5 over windows of 2048 in pages of 16 (2 KV
+// heads) 17 us and one token over 4000 slots 9 us: a launch, the list, a page, a tile, one after the other.
 #include <algorithm>
 #include <cstring>
 
@@ -54,10 +70,11 @@ struct AttnParams {
   const int *cu, *parents;
   int rows, B, H, Hkv, G, window;
   int q_bytes;    // of a slot's queries
+  int q_shift;    // units in turn: where the second slot's begin (lanes)
   int tq;         // rows of a sequence in a slot: 128 / G
   int slots;      // slots of a CTA
   int box_shift;  // log2 of a box's rows: those of a page, at most 64
-  int grid, min_tiles;
+  int grid;
   int cluster;    // CTAs that share a unit, 1: no clusters
   int single;     // no sequence has more than one unit of a KV head
   int unit_cost;  // what a unit counts for on the line besides its tiles, before them
@@ -199,7 +216,7 @@ struct PerSeq {
 __device__ __forceinline__ Stretch stretch_of(const AttnParams& p, int c, int lane) {
   const PerSeq costs([&](int b) { return p.Hkv * head_cost(p, seq_of(p, b)); }, p.B, lane);
   const int total = costs.total();
-  Stretch s{0, 0, 0, 0, max((int)(((unsigned)total + p.grid - 1) / p.grid), p.min_tiles)};
+  Stretch s{0, 0, 0, 0, max((int)(((unsigned)total + p.grid - 1) / p.grid), 1)};
   s.lo = (int)min((long long)total, (long long)c * s.per);
   s.hi = (int)min((long long)total, (long long)s.lo + s.per);
   if (s.lo < s.hi && !costs.find(s.lo, s.b, s.base)) s.hi = s.lo;  // lengths that change meanwhile
@@ -354,26 +371,29 @@ __device__ __forceinline__ float2 ld_dsmem_f2(uint32_t addr) {
 
 // ------------------------------------------------------------------ the kernel
 
-// SPLIT (with clusters): two slots of the same rows, which take the tiles of keys in turn.
-template <int NS, bool SPLIT = false>
+// TURNS: units have the rows of one slot; the CTA's two take the units in turn, or with clusters the tiles of its one unit.
+template <bool CL, bool TURNS>
 struct Cfg {
-  static constexpr int kQueries = (SPLIT ? 1 : NS) * kQBytes;
+  static constexpr int NS = 2;
+  static constexpr int kQueries = (CL && TURNS ? 1 : NS) * kQBytes;
   static constexpr int kStages = kQueries == kQBytes ? 6 : 5;
   static constexpr int kThreads = 128 + 128 * NS;  // at most 12 warps: one more would leave 128 registers
-  static constexpr int kBufs = NS == 1 ? 4 : 2;    // a slot's buffers of scores
+  static constexpr int kBufs = 2;                  // a slot's buffers of scores
   static constexpr int kSlotCols = 64 * kBufs + kD;  // of tensor memory: scores (and P over them), outputs
   static constexpr int kTmemCols = 512;
   static_assert(NS * kSlotCols <= kTmemCols, "tensor memory");
-  static constexpr int kBars = 4 * kStages + (5 + 3 * kBufs) * NS;
+  static constexpr int kBars = 4 * kStages + (6 + 3 * kBufs) * NS;
   static constexpr int kSmem = 1024 + kQueries + kStages * kStageBytes + kBars * 8 + 8 + sizeof(Walk);
   static_assert(kSmem <= 227 * 1024, "shared memory");
   static_assert(NS * kBQ * kD * 4 <= kStages * kStageBytes, "clusters: the slots' outputs take the ring's place");
 };
 
-template <int NS, bool CL, bool SPLIT>
-__global__ void __launch_bounds__(Cfg<NS, SPLIT>::kThreads, 1) attn_paged_kernel(const __grid_constant__ AttnParams p) {
-  static_assert(!SPLIT || (CL && NS == 2), "two slots of a cluster's CTA");
-  typedef Cfg<NS, SPLIT> C;
+template <bool CL, bool TURNS>
+__global__ void __launch_bounds__(Cfg<CL, TURNS>::kThreads, 1) attn_paged_kernel(const __grid_constant__ AttnParams p) {
+  typedef Cfg<CL, TURNS> C;
+  constexpr int NS = C::NS;
+  constexpr bool SPLIT = CL && TURNS;  // tiles in turn
+  constexpr bool ALT = !CL && TURNS;   // units in turn
   extern __shared__ uint8_t smem_raw[];
   uint8_t* const smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* const sQ = smem;
@@ -385,12 +405,13 @@ __global__ void __launch_bounds__(Cfg<NS, SPLIT>::kThreads, 1) attn_paged_kernel
   auto bar = [&](int i) { return smem_u32(&bars[i]); };
   auto full = [&](int kv, int s) { return bar(kv * C::kStages + s); };  // K (0) or V (1) of a stage
   auto empty = [&](int kv, int s) { return bar((2 + kv) * C::kStages + s); };
-  auto mine = [&](int g, int i) { return bar(4 * C::kStages + (5 + 3 * C::kBufs) * g + i); };
+  auto mine = [&](int g, int i) { return bar(4 * C::kStages + (6 + 3 * C::kBufs) * g + i); };
   auto q_full = [&](int g) { return mine(g, 0); };
   auto q_free = [&](int g) { return mine(g, 1); };
   auto o_done = [&](int g) { return mine(g, 2); };
   auto o_free = [&](int g) { return mine(g, 3); };
   auto drain = [&](int g) { return mine(g, 4); };
+  auto turn_over = [&](int g) { return mine(g, 5 + 3 * C::kBufs); };
   // of the slot's tile number A, in buffer A % kBufs
   auto s_full = [&](int g, int A) { return mine(g, 5 + A % C::kBufs); };
   auto p_ready = [&](int g, int A) { return mine(g, 5 + C::kBufs + A % C::kBufs); };
@@ -404,8 +425,8 @@ __global__ void __launch_bounds__(Cfg<NS, SPLIT>::kThreads, 1) attn_paged_kernel
     for (int s = 0; s < C::kStages; ++s) {
       mbar_init(full(0, s), 1);
       mbar_init(full(1, s), 1);
-      mbar_init(empty(0, s), SPLIT ? 1 : NS);
-      mbar_init(empty(1, s), SPLIT ? 1 : NS);
+      mbar_init(empty(0, s), TURNS ? 1 : NS);
+      mbar_init(empty(1, s), TURNS ? 1 : NS);
     }
     for (int g = 0; g < NS; ++g) {
       mbar_init(q_full(g), 1);
@@ -418,6 +439,7 @@ __global__ void __launch_bounds__(Cfg<NS, SPLIT>::kThreads, 1) attn_paged_kernel
       mbar_init(o_done(g), 1);
       mbar_init(o_free(g), 128);
       mbar_init(drain(g), 1);
+      mbar_init(turn_over(g), 1);
     }
     *abort_flag = 0;
     fence_mbar_init();
@@ -529,8 +551,8 @@ __global__ void __launch_bounds__(Cfg<NS, SPLIT>::kThreads, 1) attn_paged_kernel
     const int g = warp - 1;
     constexpr uint32_t idesc_s = idesc_bf16_f32(kBQ, kBK);
     constexpr uint32_t idesc_pv = idesc_bf16_f32(kBQ, kD) | (1u << 16);  // B (V) is MN-major
-    const int rows = SPLIT ? 0 : g;  // the queries' slot
-    const uint64_t dq = smem_desc_sw128(smem_u32(sQ + rows * kQBytes));
+    const int rows = TURNS ? 0 : g, qs = SPLIT ? 0 : g;  // the slot's rows of a unit, and its queries' place
+    const uint64_t dq = smem_desc_sw128(smem_u32(sQ + qs * kQBytes));
     const uint64_t dk = smem_desc_sw128(smem_u32(ring));
     const uint64_t dv = smem_desc_sw128_mn(smem_u32(ring + 2 * kKVSub), kKVSub, 1024);
     const uint32_t s_tmem = tmem + C::kSlotCols * g, o_tmem = s_tmem + 64 * C::kBufs;
@@ -542,23 +564,24 @@ __global__ void __launch_bounds__(Cfg<NS, SPLIT>::kThreads, 1) attn_paged_kernel
     // The slot's queries: loaded as soon as the last score product of a unit has read its own, and asked into L2 a
     // unit before that (behind the tiles in flight, a load from HBM would take 4 us).
     Walk ahead = *begin;
+    int turn = 0;  // ahead's number
     auto find = [&] {
-      while (ahead.on() && !ahead.has(p, rows)) ahead.next(p);
+      while (ahead.on() && !(ahead.has(p, rows) && (!ALT || (turn & 1) == g))) ahead.next(p), ++turn;
       return ahead.on();
     };
     auto load_queries = [&] {
       if (!ahead.on() || (SPLIT && g != 0)) return;
       if (elect_one()) {
         // rows past the sequence's are others' or zeros: their scores are nobody's
-        mbar_arrive_expect_tx(q_full(rows), (uint32_t)p.q_bytes);
+        mbar_arrive_expect_tx(q_full(qs), (uint32_t)p.q_bytes);
 #pragma unroll
         for (int half = 0; half < 2; ++half)
-          tma_load_3d(smem_u32(sQ + rows * kQBytes + half * kQSub), &p.tq_map, 64 * half, ahead.kvh * p.G,
-                      ahead.seq.row0 + ahead.node0(p, rows), q_full(rows));
+          tma_load_3d(smem_u32(sQ + qs * kQBytes + half * kQSub) + (ALT && g == 1 ? p.q_shift * 128 : 0), &p.tq_map, 64 * half, ahead.kvh * p.G,
+                      ahead.seq.row0 + ahead.node0(p, rows), q_full(qs));
       }
       __syncwarp();
       q_loads++;
-      ahead.next(p);
+      ahead.next(p), ++turn;
       if (!SPLIT && find() && elect_one())
 #pragma unroll
         for (int half = 0; half < 2; ++half)
@@ -567,9 +590,24 @@ __global__ void __launch_bounds__(Cfg<NS, SPLIT>::kThreads, 1) attn_paged_kernel
     };
     find();
     load_queries();
-    for (Walk w = *begin; w.on() && !failed; w.next(p)) {
+    int number = 0;
+    for (Walk w = *begin; w.on() && !failed; w.next(p), ++number) {
       const int all = w.j1 - w.j0, n = SPLIT ? (all + 1 - g) / 2 : all;
       if (SPLIT && n == 0) break;  // (a cluster's CTA has one unit)
+      if (ALT && (number & 1) != g) {
+        J += n;
+        continue;
+      }
+      // A slot looks at no tile before all tiles of the unit before have been seen there: a barrier's parity tells only
+      // neighbouring phases apart, and no stage is more than one behind then.
+      if (ALT && number > 0 && !wait(turn_over(1 - g), ((number - 1) >> 1) & 1)) {
+        failed = true;
+        break;
+      }
+      if (ALT && n == 0) {
+        if (lane == 0) mbar_arrive(turn_over(g));
+        continue;
+      }
       if (!w.has(p, rows)) {  // nothing for this slot: the stages go back
         for (int j = 0; j < n && !failed; ++j, ++J)
           for (int kv = 0; kv < 2 && !failed; ++kv) {
@@ -581,12 +619,12 @@ __global__ void __launch_bounds__(Cfg<NS, SPLIT>::kThreads, 1) attn_paged_kernel
       if constexpr (SPLIT) J = g;
       // What can be issued is, whatever it is: scores up to kBufs tiles ahead (their buffer's P has been read: its
       // product was issued before), the product of a tile whose P is there, the next unit's queries.
-      if (!wait(q_full(rows), units & 1)) {
+      if (!wait(q_full(qs), units & 1)) {
         failed = true;
         break;
       }
       int s = 0, v = 0;  // tiles whose scores and products have been issued
-      bool q_wanted = false;
+      bool q_wanted = false, over = !ALT;
       unsigned long long idle_since = 0;
       unsigned idle = 0;  // looks in a row that found nothing
       while (v < n) {
@@ -631,6 +669,12 @@ __global__ void __launch_bounds__(Cfg<NS, SPLIT>::kThreads, 1) attn_paged_kernel
             did = true;
           }
         }
+        if (!over && s == n) {  // the next tiles are the other slot's, as soon as V of the last ones is there
+          over = true;
+          for (int x = v; x < n; ++x) over &= there(full(1, (J + x) % C::kStages), ((J + x) / C::kStages) & 1);
+          if (over && lane == 0) mbar_arrive(turn_over(g));
+          __syncwarp();
+        }
         if (q_wanted && there(q_free(g), units & 1)) {
           load_queries();
           q_wanted = false;
@@ -647,6 +691,8 @@ __global__ void __launch_bounds__(Cfg<NS, SPLIT>::kThreads, 1) attn_paged_kernel
           }
         }
       }
+      if (!over && lane == 0) mbar_arrive(turn_over(g));
+      __syncwarp();
       if (!failed && q_wanted) {
         if (wait(q_free(g), units & 1))
           load_queries();
@@ -665,17 +711,19 @@ __global__ void __launch_bounds__(Cfg<NS, SPLIT>::kThreads, 1) attn_paged_kernel
   } else if (warp >= 4) {
     // ---------------- a slot's rows, one a thread
     const int g = (warp - 4) >> 2, quarter = warp & 3;
-    const int r = quarter * 32 + lane;
+    // the row of a lane; of single tokens, the second slot's begin at lane 64, whose warp is on another quarter of the SM
+    // than the first slot's
+    const int r = (quarter * 32 + lane - (ALT && g == 1 ? p.q_shift : 0)) & (kBQ - 1);
     const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
     const uint32_t s_taddr = tmem + lane_off + C::kSlotCols * g, o_taddr = s_taddr + 64 * C::kBufs;
     const int node_of_row = r / p.G, head_of_row = r - node_of_row * p.G;
-    int J = 0, A = 0, units = 0, part = 2 * blockIdx.x;
+    int J = 0, A = 0, units = 0, number = 0;
     bool failed = false;
-    for (Walk w = *begin; w.on() && !failed; w.next(p), part = 2 * blockIdx.x + 1) {
-      const int rows = SPLIT ? 0 : g, all = w.j1 - w.j0;
+    for (Walk w = *begin; w.on() && !failed; w.next(p), ++number) {
+      const int rows = TURNS ? 0 : g, all = w.j1 - w.j0;
       const int n = SPLIT ? (all + 1 - g) / 2 : all, node0 = w.node0(p, rows);
       if (SPLIT && n == 0) break;  // (a cluster's CTA has one unit)
-      if (!w.has(p, rows)) {
+      if (!w.has(p, rows) || (ALT && (number & 1) != g)) {
         J += n;
         continue;
       }
@@ -749,12 +797,9 @@ __global__ void __launch_bounds__(Cfg<NS, SPLIT>::kThreads, 1) attn_paged_kernel
             const int a = len - n0;  // the column of node 0
             seen |= a >= 64 ? 0ull : a >= 0 ? kin << a : a > -64 ? kin >> -a : 0ull;
           }
-          const uint32_t s0 = (uint32_t)seen, s1 = (uint32_t)(seen >> 32);
 #pragma unroll
-          for (int c = 0; c < 32; ++c) {
-            if (!(s0 & (1u << c))) x[c] = -INFINITY;
-            if (!(s1 & (1u << c))) x[32 + c] = -INFINITY;
-          }
+          for (int c = 0; c < kBK; ++c)
+            if (!((seen >> c) & 1)) x[c] = -INFINITY;
         }
         float mx[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
@@ -820,12 +865,13 @@ __global__ void __launch_bounds__(Cfg<NS, SPLIT>::kThreads, 1) attn_paged_kernel
       tc_fence_after();
       if (!CL && live) {
         const bool whole = w.whole();
-        float* const acc = p.acc + ((size_t)part * NS + g) * kBQ * kD + 4 * r;
+        const size_t part = (size_t)(2 * blockIdx.x + min(number, 1)) * p.slots + rows;
+        float* const acc = p.acc + part * kBQ * kD + 4 * r;
         // a row sees itself at least: a sum that is NaN, or 0 where all its scores are -inf, gives NaN
         const float inv = whole ? 1.f / l : 1.f;
         __nv_bfloat16* const o = static_cast<__nv_bfloat16*>(p.o.ptr) + (w.seq.row0 + (valid ? node : 0)) * p.o.row +
                                  (long long)(w.kvh * p.G + head_of_row) * p.o.head;
-        if (valid && !whole) p.ml[((size_t)part * NS + g) * kBQ + r] = make_float2(m_ref, l);
+        if (valid && !whole) p.ml[part * kBQ + r] = make_float2(m_ref, l);
 #pragma unroll 1
         for (int c = 0; c < kD; c += 32) {
           float ov[32];
@@ -995,24 +1041,24 @@ __global__ void __launch_bounds__(kJoinThreads) attn_paged_join_kernel(const __g
 
 // How a call is cut, from what the host knows of it.
 struct Plan {
-  int slots, grid, min_tiles, unit_cost, units, cluster;
+  int slots, grid, unit_cost, units, cluster;
   bool fits;  // the line is shorter than 2^31
 };
 
 // Clusters of `size` CTAs of the kernel that are resident at once, 0 if it cannot be launched so; asked once per device.
-template <int NS, bool SPLIT>
+template <bool TURNS>
 int resident_clusters(int size) {
   static std::atomic<int> known[64][kMaxCluster + 1];
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
   const int was = known[dev][size].load(std::memory_order_relaxed);
   if (was != 0) return was - 1;
-  const auto kernel = attn_paged_kernel<NS, true, SPLIT>;
+  const auto kernel = attn_paged_kernel<true, TURNS>;
   int n = 0;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)size);
-  cfg.blockDim = dim3(Cfg<NS, SPLIT>::kThreads);
-  cfg.dynamicSmemBytes = Cfg<NS, SPLIT>::kSmem;
+  cfg.blockDim = dim3(Cfg<true, TURNS>::kThreads);
+  cfg.dynamicSmemBytes = Cfg<true, TURNS>::kSmem;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = (unsigned)size;
@@ -1020,7 +1066,7 @@ int resident_clusters(int size) {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   if (cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel), cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           Cfg<NS, SPLIT>::kSmem) != cudaSuccess ||
+                           Cfg<true, TURNS>::kSmem) != cudaSuccess ||
       cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel), cudaFuncAttributeNonPortableClusterSizeAllowed, 1) !=
           cudaSuccess ||
       cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) {
@@ -1035,14 +1081,16 @@ Plan plan_of(int rows, int B, int H, int Hkv, bool cu, bool tree, long long capa
   Plan pl{};
   const int G = H / Hkv, tq = kBQ / G;
   const long long per_seq = (long long)rows * G;  // matrix rows of all sequences of a KV head
+  // Two slots cost 2 us more where one would do (16 trees of 32 nodes over 4096 slots 58.5 us against 56.5), one slot
+  // reads the cache twice where it would not (of 40: 92 against 68, ragged ones up to 40 of 121 rows on average 56 against 53).
   pl.slots = per_seq > 96ll * B ? 2 : 1;
   pl.grid = num_sms;
-  // a part costs its rows' outputs in fp32, written and read: 1 KB a row against 32 KB a tile
-  const long long avg = std::min<long long>(per_seq / B, pl.slots * kBQ);
-  pl.min_tiles = (int)std::max<long long>(1, avg / 32);
-  // A unit's queries, first scores and outputs take the time of about four tiles; where every CTA has about
-  // a unit of its own, that shares the work out better. With fewer units it would leave CTAs without tiles.
-  pl.unit_cost = 2ll * B * Hkv > num_sms ? 4 : 0;
+  // A unit's queries, first scores and outputs take the time of about four tiles, of two where the slots take units in
+  // turn; where every CTA has about a unit of its own, that shares the work out better. 16 trees of up to 64 nodes: 58.7 us
+  // with no tiles, 56.5 with 4, 59 to 62 with 7 to 14. 256 sequences of up to 1000 slots, a token each: 111, 114, 117,
+  // 121 and 123 us with 1, 2, 4, 6 and 9, of up to 100 43.6, 40.2, 41.9, 40.4, 42.4. With fewer units it would leave CTAs
+  // without tiles.
+  pl.unit_cost = 2ll * B * Hkv <= num_sms ? 0 : pl.slots == 2 ? 4 : 2;
   const int nodes = tq * pl.slots, most = tree ? std::min(rows, kMaxNodes) : cu ? rows : 1;
   // units of a KV head: what fills a unit whole, and one more for each sequence
   pl.units = (int)std::min<long long>((long long)B * ((most + nodes - 1) / nodes), (long long)B + rows / nodes);
@@ -1057,7 +1105,7 @@ Plan plan_of(int rows, int B, int H, int Hkv, bool cu, bool tree, long long capa
   const long long units = (long long)Hkv * pl.units;
   for (int size = kMaxCluster; size > 1; --size)
     if (units * size <= num_sms && (B == 1 || tiles <= kClusterTiles * size) &&
-        (pl.slots == 2 ? resident_clusters<2, false>(size) : resident_clusters<2, true>(size)) >= units) {
+        (pl.slots == 2 ? resident_clusters<false>(size) : resident_clusters<true>(size)) >= units) {
       pl.cluster = size;
       break;
     }
@@ -1085,9 +1133,11 @@ cudaError_t launch_attn_paged(const HeadRows& q, const PagedCache& c, const Head
   const int cache_rows = (c.n_pages * Hkv) << c.page_shift;  // checked by the caller
   p.G = H / Hkv;
   p.tq = kBQ / p.G;
-  p.q_bytes = p.tq * p.G * kD * 2;
+  const int box_rows = cu ? p.tq : 1;  // without a list no sequence has more than a row
+  p.q_bytes = box_rows * p.G * kD * 2;
+  p.q_shift = cu ? 0 : 64;
   if (!make_tma_2d_16b(&p.tk, c.k, cache_rows, kD, box, false) || !make_tma_2d_16b(&p.tv, c.v, cache_rows, kD, box, false) ||
-      !make_tma_heads_bf16(&p.tq_map, q, rows, H, kD, p.G, p.tq)) {
+      !make_tma_heads_bf16(&p.tq_map, q, rows, H, kD, p.G, box_rows)) {
     *why = "cuTensorMapEncodeTiled failed for the cache or the queries";
     return cudaErrorInvalidValue;
   }
@@ -1104,7 +1154,6 @@ cudaError_t launch_attn_paged(const HeadRows& q, const PagedCache& c, const Head
   const bool two = pl.slots == 2;
   while ((1 << p.box_shift) < box) ++p.box_shift;
   p.grid = pl.grid;
-  p.min_tiles = pl.min_tiles;
   p.cluster = pl.cluster;
   p.single = pl.units == B;
   p.unit_cost = pl.cluster > 1 ? 0 : pl.unit_cost;
@@ -1112,14 +1161,14 @@ cudaError_t launch_attn_paged(const HeadRows& q, const PagedCache& c, const Head
   p.status = st;
   p.wait_ns = wait_ns;
   if (pl.cluster > 1)  // configured when the resident clusters were asked for
-    return launch_clusters(two ? attn_paged_kernel<2, true, false> : attn_paged_kernel<2, true, true>,
-                           Hkv * pl.units * pl.cluster, two ? Cfg<2>::kThreads : Cfg<2, true>::kThreads,
-                           two ? Cfg<2>::kSmem : Cfg<2, true>::kSmem, pl.cluster, s, p);
-  const int smem = two ? Cfg<2>::kSmem : Cfg<1>::kSmem, threads = two ? Cfg<2>::kThreads : Cfg<1>::kThreads;
+    return launch_clusters(two ? attn_paged_kernel<true, false> : attn_paged_kernel<true, true>, Hkv * pl.units * pl.cluster,
+                           Cfg<true, false>::kThreads, two ? Cfg<true, false>::kSmem : Cfg<true, true>::kSmem, pl.cluster, s, p);
+  const int smem = Cfg<false, false>::kSmem, threads = Cfg<false, false>::kThreads;
+  static_assert(Cfg<false, true>::kSmem == Cfg<false, false>::kSmem, "of both");
   p.acc = static_cast<float*>(ws);
   p.ml = reinterpret_cast<float2*>(p.acc + (size_t)2 * pl.grid * pl.slots * kBQ * kD);
   p.joins = reinterpret_cast<Join*>(p.ml + (size_t)2 * pl.grid * pl.slots * kBQ);
-  const auto kernel = two ? attn_paged_kernel<2, false, false> : attn_paged_kernel<1, false, false>;
+  const auto kernel = two ? attn_paged_kernel<false, false> : attn_paged_kernel<false, true>;
   static std::atomic<unsigned long long> configured[2];
   cudaError_t e = set_smem_limit_once(reinterpret_cast<const void*>(kernel), smem, configured[two]);
   if (e == cudaSuccess) e = launch_pdl(kernel, pl.grid, threads, smem, s, p);
