@@ -1985,7 +1985,7 @@ blk_status blk_model_forward_paged(blk_handle* h, const blk_model* m, const int*
   const bool probs = temperature >= 0.f;
   BLK_TRY(bf16_rows(h, w.y, rows, d.hidden, m->lm_head, m->vocab, probs ? w.logits : out, s, "lm_head GEMM"));
   if (!probs) return BLK_OK;
-  return check_cuda(launch_probs(w.logits, rows, m->vocab, temperature, static_cast<float*>(out), s), "probabilities");
+  return check_cuda(launch_probs(w.logits, rows, m->vocab, temperature, static_cast<float*>(out), h->num_sms, s), "probabilities");
 }
 
 blk_status blk_mlp(blk_handle* h, const void* resid, const void* h_normed, const blk_weights* w, int rows, void* out,

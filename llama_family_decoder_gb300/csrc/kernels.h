@@ -112,7 +112,7 @@ cudaError_t launch_paged_keep(void* const* kv, int n_layers, const PagedCache& c
 
 // Rows of probabilities, fp32, of bf16 logits [rows, vocab] (vocab a multiple of 8): softmax(x / temperature), or
 // for temperature 0 one on the first largest logit.
-cudaError_t launch_probs(const void* logits, int rows, int vocab, float temperature, float* out, cudaStream_t s);
+cudaError_t launch_probs(const void* logits, int rows, int vocab, float temperature, float* out, int num_sms, cudaStream_t s);
 
 // ---------------------------------------------------------------- embedding
 // out[r, :] = table[tokens[r], :] (row_bytes per row, a multiple of 16); ids outside

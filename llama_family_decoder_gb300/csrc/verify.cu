@@ -19,7 +19,9 @@
 // of segments of 256 values, a warp a segment, and the CTAs' sums meet in distributed shared memory. The pass
 // that ends the walk leaves its segments' sums, in which the next token's segment is found; a warp looks
 // through that one. Latency-bound: a launch, three dependent rounds of loads, and per pass a row from HBM (from the
-// second on, L2) and a cluster barrier.
+// second on, L2) and a cluster barrier. Measured (a graph of calls): one chain of 5 over 32000 tokens with the draft's
+// distributions 7.9 us, 64 chains of up to 6 11.2, 16 trees of up to 64 over 131072 tokens without them 12.2. (One CTA an
+// SM 9.3, 17.4, 14.9; sums written to all CTAs instead of read 10.0, 12.3, 13.7; segments of 128 values 9.7, 12.0, 11.9.)
 #include "paged.cuh"
 
 namespace blk {
