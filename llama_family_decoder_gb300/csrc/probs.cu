@@ -4,6 +4,9 @@
 // read again (from L1 or L2). Bound by HBM for many rows, by a launch and two dependent rounds of loads for few. What it adds
 // to the model's call: 64 rows of 32000 11.7 us (one CTA a row: 14.6), of 128000 19.8 (36.3; their bytes 7.2), 400 rows
 // of 32000 23.5 (11.3).
+#include <algorithm>
+#include <cfloat>
+
 #include "paged.cuh"
 
 namespace blk {
@@ -14,14 +17,14 @@ constexpr int kThreads = 512;
 constexpr int kMaxCluster = 8;
 constexpr int kAtOnce = 4;  // chunks of eight values of a thread under way
 
-struct Peak {  // a maximum, where it is first, and the sum of 2^(x - maximum)
+struct Peak {  // a maximum, where it is first, and the sum of 2^((x - maximum) scale)
   float m, l;
   int at;
 };
-__device__ __forceinline__ Peak join(const Peak& a, const Peak& b) {
+__device__ __forceinline__ Peak join(const Peak& a, const Peak& b, float scale) {
   const bool first = a.m > b.m || (a.m == b.m && a.at <= b.at);
   const float m = fmaxf(a.m, b.m), mu = m == -INFINITY ? 0.f : m;
-  return {m, a.l * exp2f(a.m - mu) + b.l * exp2f(b.m - mu), first ? a.at : b.at};
+  return {m, a.l * exp2f((a.m - mu) * scale) + b.l * exp2f((b.m - mu) * scale), first ? a.at : b.at};
 }
 
 __device__ __forceinline__ Peak ld_dsmem_peak(uint32_t addr) {
@@ -47,8 +50,8 @@ __global__ void __launch_bounds__(kThreads, 2) probs_kernel(const uint4* __restr
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const float2 t = unpack_bf16x2(w[k]);
-      f[2 * k] = t.x * scale;
-      f[2 * k + 1] = t.y * scale;
+      f[2 * k] = t.x;
+      f[2 * k + 1] = t.y;
     }
   };
   auto each = [&](auto&& use) {  // use(chunk, its values), in order
@@ -72,9 +75,9 @@ __global__ void __launch_bounds__(kThreads, 2) probs_kernel(const uint4* __restr
     for (int k = 0; k < 8; ++k)
       if (f[k] > m) m = f[k], p.at = 8 * i + k;
     const float mu = m == -INFINITY ? 0.f : m;
-    p.l *= exp2f(p.m - mu);
+    p.l *= exp2f((p.m - mu) * scale);
 #pragma unroll
-    for (int k = 0; k < 8; ++k) p.l += exp2f(f[k] - mu);
+    for (int k = 0; k < 8; ++k) p.l += exp2f((f[k] - mu) * scale);
     p.m = m;
   });
   auto reduce = [&](Peak q, int from) {
@@ -82,7 +85,7 @@ __global__ void __launch_bounds__(kThreads, 2) probs_kernel(const uint4* __restr
       const Peak r{__shfl_xor_sync(0xffffffffu, q.m, o), __shfl_xor_sync(0xffffffffu, q.l, o),
                    __shfl_xor_sync(0xffffffffu, q.at, o)};
       // the lower lane's first: both lanes of a pair get the same sum
-      q = lane & o ? join(r, q) : join(q, r);
+      q = lane & o ? join(r, q, scale) : join(q, r, scale);
     }
     return q;
   };
@@ -95,7 +98,7 @@ __global__ void __launch_bounds__(kThreads, 2) probs_kernel(const uint4* __restr
     __syncwarp();
     cluster_sync_all();
     Peak q = ld_dsmem_peak(map_shared_rank(smem_u32(&own), 0));
-    for (int r = 1; r < size; ++r) q = join(q, ld_dsmem_peak(map_shared_rank(smem_u32(&own), r)));
+    for (int r = 1; r < size; ++r) q = join(q, ld_dsmem_peak(map_shared_rank(smem_u32(&own), r)), scale);
     p = q;
     __syncwarp();
     cluster_arrive();  // (waited for below: nobody leaves while its peak may be read)
@@ -104,7 +107,7 @@ __global__ void __launch_bounds__(kThreads, 2) probs_kernel(const uint4* __restr
   float4* const to = out + (size_t)row_at * (vocab / 4);
   each([&](int i, float (&f)[8]) {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) f[k] = greedy ? (8 * i + k == p.at ? 1.f : 0.f) : exp2f(f[k] - mu) * inv;
+    for (int k = 0; k < 8; ++k) f[k] = greedy ? (8 * i + k == p.at ? 1.f : 0.f) : exp2f((f[k] - mu) * scale) * inv;
     to[2 * i] = make_float4(f[0], f[1], f[2], f[3]);
     to[2 * i + 1] = make_float4(f[4], f[5], f[6], f[7]);
   });
@@ -124,8 +127,10 @@ cudaError_t launch_probs(const void* logits, int rows, int vocab, float temperat
   // clusters as long as they are all resident (two CTAs an SM) and a thread has a chunk
   int size = 1;
   while (size < kMaxCluster && 2ll * size * rows <= 2ll * num_sms && size * kThreads < vocab / 8) size *= 2;
-  return launch_clusters(probs_kernel, rows * size, kThreads, 0, size, s, static_cast<const uint4*>(logits), vocab,
-                         greedy ? 1.f : 1.4426950408889634f / temperature, greedy ? 1 : 0, reinterpret_cast<float4*>(out), size);
+  // finite and not 0: the largest logit's exponent is 0, an infinite one's stays infinite
+  const float scale = greedy ? 1.f : std::min(std::max(1.4426950408889634f / temperature, FLT_MIN), FLT_MAX);
+  return launch_clusters(probs_kernel, rows * size, kThreads, 0, size, s, static_cast<const uint4*>(logits), vocab, scale,
+                         greedy ? 1 : 0, reinterpret_cast<float4*>(out), size);
 }
 
 }  // namespace blk

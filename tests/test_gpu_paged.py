@@ -1003,6 +1003,12 @@ def test_probabilities_of_rows_with_ties_and_infinities():
     hot = blk.model_forward_paged(ints([1, 2, 3]), layers, embed, norm_g, lm_head, caches, ints([0, 1, 3]), temperature=0)
     assert torch.equal(logits[:, :32], logits[:, 32:])
     assert hot.argmax(-1).tolist() == logits[:, :32].float().argmax(-1).tolist() and hot.sum().item() == 3
+    # temperatures whose reciprocal is no fp32 number: the limits
+    top = logits == logits.amax(-1, keepdim=True)
+    cold = blk.model_forward_paged(ints([1, 2, 3]), layers, embed, norm_g, lm_head, caches, ints([0, 1, 3]), temperature=1e-40)
+    assert torch.equal(cold, top.float() / top.sum(-1, keepdim=True))
+    warm = blk.model_forward_paged(ints([1, 2, 3]), layers, embed, norm_g, lm_head, caches, ints([0, 1, 3]), temperature=float("inf"))
+    assert torch.equal(warm, torch.full_like(warm, 1 / 64))
     embed[2] = float("nan")
     p = blk.model_forward_paged(ints([1, 2, 3]), layers, embed, norm_g, lm_head, caches, ints([0, 1, 3]), temperature=1)
     assert torch.isfinite(p[0]).all() and torch.isnan(p[1:]).all()  # the third row sees the second
