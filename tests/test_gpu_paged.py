@@ -993,6 +993,28 @@ def test_model_over_a_paged_cache(act, qk_norm, page):
     assert torch.all((hot == 0) | (hot == 1)) and blk.last_status() == 0
 
 
+@pytest.mark.parametrize("hidden,heads,kv,ffn,kw", [(384, 3, 3, 640, {}), (512, 8, 2, 1000, dict(sliding_window=33)),
+                                                    (512, 4, 1, 1544, dict(use_rope=False)),
+                                                    (640, 5, 1, 512, dict(rope_scaling=("yarn", 4.0, 256, 1.0, 32.0)))])
+@pytest.mark.parametrize("chunks", [[1, 64, 65], [700], [129, 1, 300]])
+def test_model_over_a_paged_cache_in_chunks(hidden, heads, kv, ffn, kw, chunks):
+    """A prompt in chunks of one row to hundreds: the whole sequence's logits, whatever the block's options."""
+    wl = Workload("paged_chunks", "bf16", 1, 8, hidden, heads, kv, 128, ffn, "relu2", seed=9, **kw)
+    layers, embed, norm_g, lm_head, _ = make_model(wl, n_layers=2, vocab=512)
+    blk = DecoderBlock.from_workload(wl, max_seq=1024)
+    dev = [to_dev(w) for w in layers], embed.to(DEV), norm_g.to(DEV), lm_head.to(DEV)
+    tokens = np.random.default_rng(3).integers(0, 512, sum(chunks))
+    c = cache_of(blk, [0], [sum(chunks)], 32)
+    caches, got = [c, blk.paged_cache(0, 0, shared=c)], []
+    for n in chunks:
+        at = int(c["lens"].item())
+        got.append(blk.model_forward_paged(ints(tokens[at:at + n].tolist()), *dev, caches, cu_of([n])))
+        blk.paged_keep(caches, ints([n]))
+    assert blk.last_status() == 0 and c["lens"].item() == sum(chunks)
+    want = oracle.model_forward(cfg_of(wl), [weights_np(w) for w in layers], np64(embed), np64(norm_g), np64(lm_head), tokens[None])[0]
+    assert rel_err(torch.cat(got), want) <= TOL_MODEL_2
+
+
 def test_probabilities_of_rows_with_ties_and_infinities():
     """One layer whose lm_head repeats rows: the first of equal logits; NaN rows stay NaN."""
     blk, (layers, embed, norm_g, lm_head), _ = model_of(vocab=64, seed=3)
@@ -1060,6 +1082,53 @@ def test_model_steps_of_drafts(temperature):
     # the next row over the cache of the steps is that of the whole sequence
     got = blk.model_forward_paged(ints(last), *dev, caches)
     assert rel_err(got, np.stack([exact(h + [x])[-1] for h, x in zip(history, last)])) <= TOL_MODEL_2
+
+
+def test_model_steps_captured():
+    """A whole step in a graph, replayed from other lengths and tokens than it was captured with, beside an eager one."""
+    blk, dev, _ = model_of(seed=6)
+    r = np.random.default_rng(5)
+    c = cache_of(blk, [0, 0], [200, 200], 16)
+    caches = [c, blk.paged_cache(0, 0, shared=c)]
+    blk.model_forward_paged(ints(r.integers(0, 1024, 97).tolist()), *dev, caches, cu_of([40, 57]))
+    blk.paged_keep(caches, ints([40, 57]))
+    start = [{k: v.clone() for k, v in x.items()} for x in caches]
+    trees = [tree_of(9, 3), tree_of(5, 4)]
+    cu, parents = cu_of([9, 5]), ints(sum(trees, []))
+    depths = ints([int(x) for t in trees for x in kin_of(t)[1]])
+    steps = [(ints(r.integers(0, 1024, 14).tolist()), torch.rand(14, device=DEV) * 0.02, torch.rand(2, device=DEV)) for _ in range(3)]
+
+    def eager():
+        mine = [dict(start[0], k=start[0]["k"].clone(), v=start[0]["v"].clone(), lens=start[0]["lens"].clone())]
+        mine.append(dict(mine[0], k=start[1]["k"].clone(), v=start[1]["v"].clone()))
+        return [[x.clone() for x in blk.model_verify(t, *dev, mine, u, un, cu, depths, parents, temperature=0.7)] for t, u, un in steps], mine
+
+    want, kept = eager()
+    tok, u, un = (x.clone() for x in steps[0])
+    blk.model_verify(tok, *dev, caches, u, un, cu, depths, parents, temperature=0.7)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = blk.model_verify(tok, *dev, caches, u, un, cu, depths, parents, temperature=0.7)
+    for x, y in zip(caches, start):
+        x["k"].copy_(y["k"])
+        x["v"].copy_(y["v"])
+    c["lens"].copy_(start[0]["lens"])
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        beside, _ = eager()
+    for step, w in zip(steps, want):
+        for x, y in zip((tok, u, un), step):
+            x.copy_(y)
+        g.replay()
+        for x, y in zip(out, w):
+            assert torch.equal(x, y)
+    torch.cuda.synchronize()
+    for a, b in zip(beside, want):
+        assert all(torch.equal(x, y) for x, y in zip(a, b))
+    for x, y in zip(caches, kept):
+        assert all(torch.equal(x[k], y[k]) for k in ("k", "v", "lens"))
+    assert blk.last_status() == 0
 
 
 def test_model_over_a_paged_cache_refusals():
