@@ -385,6 +385,7 @@ struct Cfg {
   static constexpr int kBars = 4 * kStages + (6 + 3 * kBufs) * NS;
   static constexpr int kSmem = 1024 + kQueries + kStages * kStageBytes + kBars * 8 + 8 + sizeof(Walk);
   static_assert(kSmem <= 227 * 1024, "shared memory");
+  static_assert(!(CL && TURNS) || kStages % 2 == 0, "tiles in turn: a stage is always the same slot's, whose waits tell its phases apart");
   static_assert(NS * kBQ * kD * 4 <= kStages * kStageBytes, "clusters: the slots' outputs take the ring's place");
 };
 
@@ -1081,8 +1082,9 @@ Plan plan_of(int rows, int B, int H, int Hkv, bool cu, bool tree, long long capa
   Plan pl{};
   const int G = H / Hkv, tq = kBQ / G;
   const long long per_seq = (long long)rows * G;  // matrix rows of all sequences of a KV head
-  // Two slots cost 2 us more where one would do (16 trees of 32 nodes over 4096 slots 58.5 us against 56.5), one slot
-  // reads the cache twice where it would not (of 40: 92 against 68, ragged ones up to 40 of 121 rows on average 56 against 53).
+  // A unit of both slots costs 1 to 2 us more where one slot would do (16 trees of 32 nodes over 4096 slots 58.3 us against
+  // 56.7), units of one slot read the cache twice where they do not (of 40: 92.1 against 66.4, ragged ones up to 40 of 121 rows
+  // on average 55.9 against 51.5).
   pl.slots = per_seq > 96ll * B ? 2 : 1;
   pl.grid = num_sms;
   // A unit's queries, first scores and outputs take the time of about four tiles, of two where the slots take units in
