@@ -19,7 +19,8 @@
 // depend on timing. Lengths are on the device: every CTA adds up the line by itself, and the CTA that goes on with
 // another's unit writes down what is to be joined there. (Whole units per CTA instead: trees 73 us.)
 // Small batches (plan_of): a cluster of CTAs takes a unit, equal shares of its keys each, joined in the
-// cluster's shared memory: no second kernel, one token over 4000 slots 12.2 -> 9.0 us. With few rows a CTA's two
+// cluster's shared memory: no second kernel, one token over 4000 slots 12.2 -> 9.0 us, or where tiles are few too
+// one CTA (16 sequences of up to 300 12.8 -> 7.9). With few rows a CTA's two
 // slots hold the same rows and take its tiles in turn there.
 //
 // Warps 0 and 3 load K and V: their lanes look up the pages of the next 32 boxes (a box: the rows of a page in a tile)
@@ -57,6 +58,7 @@ constexpr int kKVSub = kBK * 128;      // one 64-channel half of a K or V tile
 constexpr int kStageBytes = 4 * kKVSub;
 constexpr int kMaxCluster = 16;
 constexpr int kClusterTiles = 64;      // a CTA's share of tiles up to which clusters of ragged sequences pay (plan_of)
+constexpr int kWholeTiles = 28;        // a unit's tiles up to which it is one CTA's (plan_of)
 constexpr float kRescaleLog2 = 8.0f;
 constexpr float kScaleLog2 = 1.4426950408889634f * 0.08838834764831845f;  // log2(e) / sqrt(128)
 constexpr int kNoBox = -2;             // a box that no row needs; entries below -1 are read as -1
@@ -75,7 +77,7 @@ struct AttnParams {
   int slots;      // slots of a CTA
   int box_shift;  // log2 of a box's rows: those of a page, at most 64
   int grid;
-  int cluster;    // CTAs that share a unit, 1: no clusters
+  int cluster;    // CTAs that share a unit, 0: the line
   int single;     // no sequence has more than one unit of a KV head
   int unit_cost;  // what a unit counts for on the line besides its tiles, before them
   float2* ml;     // partial results [2 grid][slots][128]: (reference, sum)
@@ -1103,10 +1105,14 @@ Plan plan_of(int rows, int B, int H, int Hkv, bool cu, bool tree, long long capa
   // their CTAs end at different times, up to where the longest sequence alone costs more than the line's second
   // kernel does (8 KV heads, one token each; the line against clusters, us): 4 sequences of 2000 14.6 against 9.2, of
   // 16000 50 against 43, one of 16000 and three of one slot 42 against 32 (63 tiles a CTA), of 32000 53 against 58.
-  pl.cluster = 1;
+  // Single CTAs likewise, where a unit has few tiles and one slot: 16 sequences of up to 300 12.8 against 8.0, of up to 1000
+  // 18.2 against 13.7, of up to 2000 23.8 against 21.0 (but one of 2000 and 15 of one slot 13.1 against 18.6). Not so trees of two
+  // slots (10 over 500 slots 20.9 against 30.7) and more units than SMs (64 sequences of up to 100 14.2 against 28.5).
+  pl.cluster = 0;
   const long long units = (long long)Hkv * pl.units;
-  for (int size = kMaxCluster; size > 1; --size)
-    if (units * size <= num_sms && (B == 1 || tiles <= kClusterTiles * size) &&
+  for (int size = kMaxCluster; size > 0; --size)
+    if (units * size <= num_sms && (size > 1 || pl.slots == 1) &&
+        ((B == 1 && size > 1) || tiles <= (size > 1 ? kClusterTiles * size : kWholeTiles)) &&
         (pl.slots == 2 ? resident_clusters<false>(size) : resident_clusters<true>(size)) >= units) {
       pl.cluster = size;
       break;
@@ -1120,7 +1126,7 @@ size_t attn_paged_ws_bytes(int rows, int B, int H, int Hkv, bool cu, bool tree, 
   if (rows <= 0 || B <= 0) return 0;
   const Plan pl = plan_of(rows, B, H, Hkv, cu, tree, capacity, window, num_sms);
   if (!pl.fits) return kAttnPagedTooLong;
-  if (pl.cluster > 1) return 0;
+  if (pl.cluster > 0) return 0;
   return (size_t)2 * pl.grid * pl.slots * kBQ * (sizeof(float2) + kD * sizeof(float)) + pl.grid * sizeof(Join);
 }
 
@@ -1158,11 +1164,11 @@ cudaError_t launch_attn_paged(const HeadRows& q, const PagedCache& c, const Head
   p.grid = pl.grid;
   p.cluster = pl.cluster;
   p.single = pl.units == B;
-  p.unit_cost = pl.cluster > 1 ? 0 : pl.unit_cost;
+  p.unit_cost = pl.cluster > 0 ? 0 : pl.unit_cost;
   p.o_wide = reinterpret_cast<uintptr_t>(o.ptr) % 32 == 0 && (rows == 1 || o.row % 16 == 0) && (H == 1 || o.head % 16 == 0);
   p.status = st;
   p.wait_ns = wait_ns;
-  if (pl.cluster > 1)  // configured when the resident clusters were asked for
+  if (pl.cluster > 0)  // configured when the resident clusters were asked for
     return launch_clusters(two ? attn_paged_kernel<true, false> : attn_paged_kernel<true, true>, Hkv * pl.units * pl.cluster,
                            Cfg<true, false>::kThreads, two ? Cfg<true, false>::kSmem : Cfg<true, true>::kSmem, pl.cluster, s, p);
   const int smem = Cfg<false, false>::kSmem, threads = Cfg<false, false>::kThreads;

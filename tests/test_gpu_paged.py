@@ -361,7 +361,7 @@ def test_attn_paged_long_chains(H, Hkv, lens, rows, window):
     check_attn(out, q, ks, vs, trees, lens, window)
 
 
-@pytest.mark.parametrize("lens", [[8000], [3000, 10, 0, 4100, 777, 2222, 64, 1], [200] * 100, [20000, 1]])
+@pytest.mark.parametrize("lens", [[8000], [3000, 10, 0, 4100, 777, 2222, 64, 1], [200] * 100, [20000, 1], [700, 0, 64, 1500] * 10])
 @pytest.mark.parametrize("H,Hkv,rows", [(32, 8, 1), (8, 2, 5), (8, 8, 20), (16, 2, 64)])
 def test_attn_paged_split_keys(lens, H, Hkv, rows):
     """Work that many CTAs share, whole and in parts."""
