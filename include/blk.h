@@ -444,7 +444,7 @@ blk_status blk_attn_decode_kv4(blk_handle* h, const blk_head_rows* q, const blk_
  * cu_seqlens[b] .. cu_seqlens[b+1]-1, its row i being number i; cu_seqlens NULL: row b alone
  * (rows == batch). cu_seqlens (device int32 [batch + 1]) rises from >= 0 to <= rows; another list
  * sets the status word to INVALID_ARG, is read clamped, and what a row that several sequences
- * claim gets is that of one of them. Rows of no sequence are ignored and their outputs left as
+ * claim gets is that of one of them; in blk_attn_paged no row of a list that falls gets an output. Rows of no sequence are ignored and their outputs left as
  * they were. Calls run on the handle's device, which must be current; two calls may run at once
  * on different streams if they share no workspace, no output and no cache that either writes.
  *

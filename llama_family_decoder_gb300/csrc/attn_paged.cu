@@ -188,11 +188,11 @@ struct PerSeq {
   }
   template <int = 0>
   __device__ __forceinline__ int total() const {
-    int n = 0;
+    unsigned n = 0;
 #pragma unroll
-    for (int i = 0; i < kHeld; ++i) n += held[i];
-    for (int b = lane + 32 * kHeld; b < B; b += 32) n += number(b);
-    return (int)__reduce_add_sync(0xffffffffu, (unsigned)n);
+    for (int i = 0; i < kHeld; ++i) n += (unsigned)held[i];
+    for (int b = lane + 32 * kHeld; b < B; b += 32) n += (unsigned)number(b);
+    return (int)__reduce_add_sync(0xffffffffu, n);
   }
   // The sequence in whose share place x of the sum lies, and the sum before it; false: x is not below the sum.
   __device__ __forceinline__ bool find(int x, int& b, int& before) const {
@@ -214,7 +214,7 @@ struct PerSeq {
   }
 };
 // By one warp. Stretch number `c`; an empty one (lo >= hi) if the line ends before. The line is shorter
-// than 2^31 (see plan_of).
+// than 2^31 (see plan_of); that of a list that falls need not be, and is not walked.
 __device__ __forceinline__ Stretch stretch_of(const AttnParams& p, int c, int lane) {
   const PerSeq costs([&](int b) { return p.Hkv * head_cost(p, seq_of(p, b)); }, p.B, lane);
   const int total = costs.total();
@@ -255,6 +255,10 @@ struct Walk {
       return;
     }
     kvh = from / per_head;
+    if (kvh >= p.Hkv) {
+      left = 0;
+      return;
+    }
     at = from - kvh * per_head;
     unit(p);
     while (at >= tiles + p.unit_cost) {  // at < per_head: it ends within the units
@@ -323,7 +327,7 @@ __device__ __forceinline__ Join join_of(const AttnParams& p, const Stretch& s, c
   Join j{w.seq, w.kvh, w.t, 0, -1};
   const int tile0 = s.lo - w.at + p.unit_cost;  // the unit's first tile on the line
   if (!w.on() || w.j0 == 0 || tile0 / s.per != c - 1) return j;  // no unit goes over, or an earlier stretch has it
-  j.last = (tile0 + w.tiles - 1) / s.per;
+  j.last = min((tile0 + w.tiles - 1) / s.per, p.grid - 1);
   j.first = s.lo - w.at <= (c - 1) * s.per ? 2 * (c - 1) : 2 * (c - 1) + 1;  // was it that stretch's first unit?
   return j;
 }
@@ -481,8 +485,19 @@ __global__ void __launch_bounds__(Cfg<CL, TURNS>::kThreads, 1) attn_paged_kernel
     if (over) record(p.status, kStatusCacheFull);
     __syncwarp();
   }
+  // Sequences of a list that falls overlap: neither the line nor the units are as long then as the host has them.
+  bool falls = false;
+  if (warp == 2 && p.cu)
+    for (int b = lane; b < p.B; b += 32) falls |= p.cu[b + 1] < p.cu[b];
+  __syncwarp();
   tc_fence_before();
-  __syncthreads();
+  if (__syncthreads_or(falls)) {  // no row gets an output
+    if (threadIdx.x == 0) {
+      begin->left = begin->seq.n = 0;
+      if (!CL) p.joins[blockIdx.x].last = -1;
+    }
+    __syncthreads();
+  }
   tc_fence_after();
   const uint32_t tmem = *tmem_holder;
   // What is in flight, for the drain after an abort: the stages issued (with the parity of their last

@@ -515,6 +515,38 @@ def test_attn_paged_bad_lists_stay_in_bounds():
     assert blk.last_status() == 0
 
 
+@pytest.mark.parametrize("H,Hkv,lens,rows", [(4, 2, [100, 9], [60, 20]),               # clusters
+                                             (32, 8, [300] * 40, [1, 5] * 20)])         # the line and its join
+@pytest.mark.parametrize("kind", ["chain", "tree"])
+def test_attn_paged_a_list_that_falls(H, Hkv, lens, rows, kind):
+    """Its sequences claim rows twice: none gets an output, and the next call is right."""
+    trees = [chain(t) if kind == "chain" else tree_of(t, b) for b, t in enumerate(rows)]
+    blk, c, q, ks, vs, cu, parents = attn_case(H, Hkv, lens, trees, 32)
+    up = parents if kind == "tree" else None
+    n = cu[-1].item()
+    for at, entry in ((0, n), (1, 0), (1, n), (len(rows) - 1, n), (len(rows), 0), (len(rows), -5)):
+        bad = cu.clone()
+        bad[at] = entry
+        falls = bool((bad[1:] < bad[:-1]).any())
+        out = blk.attn_paged(q, c, bad, up, out=torch.full_like(q, 5.0))
+        status = blk.last_status()
+        if falls:
+            assert status == 1 and torch.all(out == 5), (at, entry)
+        check_attn(blk.attn_paged(q, c, cu, up), q, ks[:1], vs[:1], trees[:1], lens[:1])
+    assert blk.last_status() == 0
+
+
+def test_attn_paged_a_list_that_falls_past_32_bits():
+    """Eleven of its sequences claim all rows over 2^28 slots each: more than 2^32 tiles of keys."""
+    blk, rows, B = block(1, 1), 25600, 22
+    c = blk.paged_cache(1, 64, 64)
+    c["pages"] = torch.zeros(B, 2**22, dtype=torch.int32, device=DEV)
+    c["lens"] = torch.full((B,), 2**28 - rows, dtype=torch.int32, device=DEV)
+    q = randn(1, rows, 1, D)
+    out = blk.attn_paged(q, c, ints([0, rows] * (B // 2) + [0]), out=torch.full_like(q, 5.0))
+    assert blk.last_status() == 1 and torch.all(out == 5)
+
+
 def test_attn_paged_at_the_last_slots():
     """A page list of 2^31 slots, all of them one page; a window leaves the last ones of it."""
     blk = block(2, 1, sliding_window=100)
