@@ -546,8 +546,8 @@ blk_status blk_verify_drafts(blk_handle* h, const float* target, long long targe
  * share pages, lens and sizes and differ in k and v), lens[b] = start + counts[b]; start = starts[b], or
  * lens[b] with starts NULL. path NULL: lens alone moves (a chain's first rows, a prompt's; cu_seqlens and rows are then
  * ignored). A sequence with a path that is not rising in its rows, a negative count or start, or
- * more rows than it has is left as it is (status word INVALID_ARG), as is one that the page
- * list has no room for (CACHE_FULL). counts, path, cu_seqlens and starts may not overlap lens, unless starts is lens.
+ * more rows than it has is left as it is (status word INVALID_ARG), as is one whose kept rows, or with a path any of its
+ * rows, pass the page list (CACHE_FULL: blk_attn_paged has no output for any of them then). counts, path, cu_seqlens and starts may not overlap lens, unless starts is lens.
  * Errors: INVALID_ARG, ALIGNMENT, CUDA. */
 blk_status blk_paged_keep(blk_handle* h, const blk_paged_cache* caches, int n_caches, const int* counts, const int* path,
                           const int* cu_seqlens, const int* starts, int batch, int rows, void* stream);

@@ -242,11 +242,12 @@ __global__ void __launch_bounds__(kKeepThreads, 2) paged_keep_kernel(const __gri
   const SeqRows sr = seq_rows(p.cu, b, p.rows);
   const int count = p.counts[b], start = p.starts ? p.starts[b] : p.c.lens[b];
   bool bad = count < 0 || start < 0 || seq_bad(p.cu, b, p.rows) || (p.path && count > sr.n);
-  const bool full = !bad && (long long)start + count > page_slots(p.c);
-  if (p.path && !bad)
+  // with a path, all the sequence's rows are to have slots: attention gave none of them an output otherwise
+  const bool full = !bad && (long long)start + (p.path ? sr.n : count) > page_slots(p.c);
+  if (p.path && !bad && !full)
     for (int j = tid; j < count; j += kKeepThreads) {
       const int x = p.path[sr.lo + j];
-      bad |= x < j || x >= sr.n || (j > 0 && p.path[sr.lo + j - 1] >= x) || (long long)start + x >= page_slots(p.c);
+      bad |= x < j || x >= sr.n || (j > 0 && p.path[sr.lo + j - 1] >= x);
     }
   bad = __syncthreads_or(bad);
   cluster_arrive();

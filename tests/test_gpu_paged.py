@@ -896,6 +896,29 @@ def test_paged_keep_lens_alone_and_refusals():
         blk.paged_keep([c, dict(blk.paged_cache(0, 0, shared=c), lens=c["lens"].clone())], ints([1, 1, 1]))
 
 
+@pytest.mark.parametrize("layers", [1, 70])
+def test_paged_keep_of_rows_that_pass_the_page_list(layers):
+    """A sequence some of whose rows have no slot is left alone, whatever was kept of it: attention saw none of them."""
+    blk = block(2, 2)
+    c = blk.paged_cache(3, 32, 16)
+    caches = [c] + [blk.paged_cache(0, 0, shared=c) for _ in range(layers - 1)]
+    cu, rows = ints([0, 6, 12, 18]), [0, 3, 5, -1, -1, -1]
+    for lens, path, count, code in ((27, rows, 2, 4), (27, rows, 3, 4), (30, rows, 1, 4), (31, rows, 0, 4), (27, rows, 7, 1),
+                                    (26, rows, 3, 0)):
+        for i, x in enumerate(caches):
+            fill(x, 7 + 2 * i, None)
+        c["lens"].copy_(ints([1, lens, 2]))
+        before = [{x: t[x].clone() for x in "kv"} for t in caches]
+        blk.paged_keep(caches, ints([3, count, 2]), ints(rows + path + rows), cu)
+        assert blk.last_status() == code and c["lens"].tolist() == [4, lens + (count if code == 0 else 0), 4]
+        for t, was in zip(caches, before):
+            for x in "kv":
+                same = torch.equal(slots_of(t, x, 1, 32), slots_of(dict(t, **was), x, 1, 32))
+                assert same == (code != 0)
+                assert torch.equal(slots_of(t, x, 0, 4)[1:], slots_of(dict(t, **was), x, 0, 7)[[1, 4, 6]])
+                assert torch.equal(slots_of(t, x, 2, 4)[2:], slots_of(dict(t, **was), x, 2, 8)[[2, 5]])
+
+
 # ------------------------------------------------------------------ together
 
 @pytest.mark.parametrize("page", [16, 64])
