@@ -545,7 +545,7 @@ blk_status blk_verify_drafts(blk_handle* h, const float* target, long long targe
  * each sequence: slot start + path[j] -> start + j in all n_caches (host array: the layers' caches, which
  * share pages, lens and sizes and differ in k and v), lens[b] = start + counts[b]; start = starts[b], or
  * lens[b] with starts NULL. path NULL: lens alone moves (a chain's first rows, a prompt's; cu_seqlens and rows are then
- * ignored). A sequence with a path that is not rising in its rows, a negative count or start, or
+ * ignored). A sequence with a path that is not rising in its rows or has a row whose page is none, a negative count or start, or
  * more rows than it has is left as it is (status word INVALID_ARG), as is one whose kept rows, or with a path any of its
  * rows, pass the page list (CACHE_FULL: blk_attn_paged has no output for any of them then). counts, path, cu_seqlens and starts may not overlap lens, unless starts is lens.
  * Errors: INVALID_ARG, ALIGNMENT, CUDA. */

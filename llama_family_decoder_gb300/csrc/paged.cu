@@ -244,10 +244,19 @@ __global__ void __launch_bounds__(kKeepThreads, 2) paged_keep_kernel(const __gri
   bool bad = count < 0 || start < 0 || seq_bad(p.cu, b, p.rows) || (p.path && count > sr.n);
   // with a path, all the sequence's rows are to have slots: attention gave none of them an output otherwise
   const bool full = !bad && (long long)start + (p.path ? sr.n : count) > page_slots(p.c);
+  // the places of row j0 + j and of the one that it comes from; false: a page of theirs is none
+  auto look_up = [&](int j0, int j, int x) {
+    const PagePlace f = page_place(p.c, b, start + x), t = page_place(p.c, b, start + j0 + j);
+    from[j] = x != j0 + j ? place_row(p.c, f, p.Hkv, 0) : -1;
+    to[j] = place_row(p.c, t, p.Hkv, 0);
+    return f.page >= 0 && t.page >= 0;
+  };
   if (p.path && !bad && !full)
     for (int j = tid; j < count; j += kKeepThreads) {
       const int x = p.path[sr.lo + j];
-      bad |= x < j || x >= sr.n || (j > 0 && p.path[sr.lo + j - 1] >= x);
+      const bool wrong = x < j || x >= sr.n || (j > 0 && p.path[sr.lo + j - 1] >= x);
+      bad |= wrong || (j < kKeepRows ? !look_up(0, j, x)
+                                     : page_place(p.c, b, start + x).page < 0 || page_place(p.c, b, start + j).page < 0);
     }
   bad = __syncthreads_or(bad);
   cluster_arrive();
@@ -259,15 +268,10 @@ __global__ void __launch_bounds__(kKeepThreads, 2) paged_keep_kernel(const __gri
     const int page_rows = 1 << p.c.page_shift;
     for (int j0 = 0; j0 < count; j0 += kKeepRows) {
       const int n = min(kKeepRows, count - j0);
-      for (int j = tid; j < n; j += kKeepThreads) {
-        const int x = p.path[sr.lo + j0 + j];
-        const PagePlace f = page_place(p.c, b, start + x), t = page_place(p.c, b, start + j0 + j);
-        const bool known = f.page >= 0 && t.page >= 0;
-        if (!known) record(p.status, kStatusInvalidArg);
-        from[j] = known && x != j0 + j ? place_row(p.c, f, p.Hkv, 0) : -1;
-        to[j] = known ? place_row(p.c, t, p.Hkv, 0) : 0;
+      if (j0 > 0) {  // the first ones were looked up above
+        for (int j = tid; j < n; j += kKeepThreads) look_up(j0, j, p.path[sr.lo + j0 + j]);
+        __syncthreads();
       }
-      __syncthreads();
       for (int u = rank * warps + (tid >> 5); u < units; u += size * warps) {
         const int head = u % p.Hkv;
         uint8_t* base = static_cast<uint8_t*>(p.kv[u / p.Hkv]) + (size_t)head * page_rows * p.row_bytes;

@@ -919,6 +919,39 @@ def test_paged_keep_of_rows_that_pass_the_page_list(layers):
                 assert torch.equal(slots_of(t, x, 2, 4)[2:], slots_of(dict(t, **was), x, 2, 8)[[2, 5]])
 
 
+@pytest.mark.parametrize("page", [-1, 10**6, 2**31 - 1])
+def test_paged_keep_of_rows_whose_page_is_none(page):
+    """Neither the rows nor lens of a sequence move if one of its kept rows comes from or goes to no page."""
+    blk = block(2, 2)
+    c = cache_of(blk, [14, 3, 20], [40, 20, 300], 16)
+    cu = cu_of([40, 20, 300])
+    whole = c["pages"].clone()
+    long = [i + i // 2 for i in range(200)]  # more rows than are looked up at a time
+    for b, at, path in ((0, 0, [0, 3, 9]),      # goes to
+                        (0, 2, [0, 3, 9, 30]),  # comes from
+                        (0, 1, [0, 1, 2, 3]),   # stays there
+                        (2, 19, long), (2, 13, long)):
+        paths = [[0, 1], [0, 2], [0, 4]]
+        paths[b] = path
+        fill(c, 5, None)
+        c["lens"].copy_(ints([14, 3, 20]))
+        c["pages"].copy_(whole)
+        c["pages"][b, at] = page
+        before = {x: c[x].clone() for x in "kv"}
+        flat = [y for p, n in zip(paths, (40, 20, 300)) for y in p + [-1] * (n - len(p))]
+        blk.paged_keep([c], ints([len(p) for p in paths]), ints(flat), cu)
+        assert blk.last_status() == 1
+        c["pages"].copy_(whole)
+        for s, (n, t) in enumerate(zip((14, 3, 20), (40, 20, 300))):
+            assert c["lens"][s].item() == (n if s == b else n + 2)
+            for x in "kv":
+                now, was = slots_of(c, x, s, n + t), slots_of(dict(c, **before), x, s, n + t)
+                want = was.clone()
+                if s != b:
+                    want[n:n + 2] = was[[n + y for y in paths[s]]]
+                assert torch.equal(now, want)
+
+
 # ------------------------------------------------------------------ together
 
 @pytest.mark.parametrize("page", [16, 64])
