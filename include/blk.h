@@ -560,7 +560,9 @@ blk_status blk_paged_keep(blk_handle* h, const blk_paged_cache* caches, int n_ca
  * A tree's rows need depths; no two layers may have the same k or v. temperature < 0: out is the logits, bf16 [rows, vocab]; > 0: the probabilities
  * softmax(logits / temperature), fp32 [rows, vocab], what blk_verify_drafts takes; 0: all of it on the
  * largest logit (the first of several). The softmax is of the bf16 logits, in fp32. A token outside
- * [0, vocab) embeds as zeros and sets the status word to INVALID_ARG.
+ * [0, vocab) embeds as zeros and sets the status word to INVALID_ARG. For rows without an output of blk_attn_paged (those
+ * of a sequence that passes its page list, of a tree's sequence from the 65th on) attention counts as 0: what out has for
+ * them is the same each time and means nothing; blk_paged_keep leaves such a sequence alone.
  * workspace: blk_model_paged_workspace_bytes (of a cache its sizes count; probs: temperature >= 0).
  * Errors: those of blk_model_forward, blk_paged_append and blk_attn_paged. */
 size_t blk_model_paged_workspace_bytes(const blk_handle* h, int rows, int packed, int tree, int batch,

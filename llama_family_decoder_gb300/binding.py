@@ -806,7 +806,8 @@ class DecoderBlock:
                      parents=None, temperature=1.0, draft=None, host_lens_max=-1, stream=None):
         """A step of speculative decoding: the model over each sequence's last token and its drafts
         (model_forward_paged), their verification with the given random numbers (verify_drafts), and the kept
-        rows moved behind lens in every layer's cache (paged_keep). Returns (counts, path, next)."""
+        rows moved behind lens in every layer's cache (paged_keep). Returns (counts, path, next). A sequence whose rows
+        pass its page list (status CACHE_FULL) is left alone; what is returned for it means nothing."""
         if self._elsewhere(stream):
             with _on_stream(self._device, stream):
                 return self.model_verify(tokens, layers, embed, norm_g, lm_head, caches, u, u_next, cu_seqlens, depths, parents,

@@ -1947,6 +1947,8 @@ blk_status blk_model_forward_paged(blk_handle* h, const blk_model* m, const int*
   BLK_TRY(check_device(h));
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const int Hd = d.n_heads * d.head_dim, KVd = d.n_kv_heads * d.head_dim, cols = qkv_cols(d);
+  // Rows that get no attention (in any layer alike) keep these zeros.
+  BLK_TRY(check_cuda(cudaMemsetAsync(w.o, 0, (size_t)rows * Hd * 2, s), "attention's zeros"));
   BLK_TRY(check_cuda(launch_embed(tokens, m->embed, rows, d.hidden * 2, m->vocab, w.act0, h->status, h->num_sms, s), "embedding"));
   void* bufs[2] = {w.act0, w.act1};
   for (int l = 0; l < m->n_layers; ++l) {

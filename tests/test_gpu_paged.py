@@ -16,6 +16,7 @@ import torch
 
 import oracle
 from llama_family_decoder_gb300 import BlkError, DecoderBlock
+from llama_family_decoder_gb300.binding import lib
 from llama_family_decoder_gb300.synth import Workload, make_model
 from tests.helpers import TOL, cfg_of, np64, rel_err, to_dev, weights_np
 
@@ -1217,6 +1218,57 @@ def test_model_steps_captured():
     for x, y in zip(caches, kept):
         assert all(torch.equal(x[k], y[k]) for k in ("k", "v", "lens"))
     assert blk.last_status() == 0
+
+
+@pytest.mark.parametrize("kind", ["chain", "tree"])
+@pytest.mark.parametrize("room", [2, 5])
+def test_model_verify_at_the_end_of_a_page_list(kind, room):
+    """One of three sequences has no room for all of its rows: it is left as it is, the others' steps are those of a
+    cache where it fits, and what memory held before reaches nothing."""
+    blk, dev, _ = model_of(seed=12)
+    r = np.random.default_rng(8)
+    tree = chain(6) if kind == "chain" else [-1, 0, 0, 1, 1, 2]
+    tokens, new = r.integers(0, 1024, 120).tolist(), ints(r.integers(0, 1024, 18).tolist())
+    cu, parents = cu_of([6] * 3), ints(tree * 3) if kind == "tree" else None
+    depths = ints(kin_of(tree)[1].tolist() * 3) if kind == "tree" else None
+    u, un = torch.zeros(18, device=DEV), torch.tensor([0.1, 0.5, 0.9], device=DEV)  # drafts are accepted
+
+    def step(cap, left, garbage):
+        c = blk.paged_cache(3, cap, 16)
+        caches = [c, blk.paged_cache(0, 0, shared=c)]
+        blk.model_forward_paged(ints(tokens), *dev, caches, cu_of([40] * 3))
+        blk.paged_keep(caches, ints([40] * 3))
+        c["lens"][1] = cap - left if left else 40
+        n = blk.model_verify(new, *dev, caches, u, un, cu, depths, parents, temperature=0.7)[0].numel()
+        assert blk.last_status() == (4 if left else 0) and n == 3
+        # ... and again in memory that holds something else
+        for x in caches:
+            x["lens"].copy_(ints([40, cap - left if left else 40, 40]))
+        nbytes = lib().blk_model_paged_workspace_bytes(blk.handle, 18, 1, parents is not None, 3, blk._paged(c)[0], 1024, 1)
+        junk = [torch.full((nbytes // 4,), garbage, device=DEV) for _ in range(8)]
+        del junk  # the model's workspace is one of these
+        p = blk.model_forward_paged(new, *dev, caches, cu, depths, parents, temperature=0.7)
+        out = blk.model_verify(new, *dev, caches, u, un, cu, depths, parents, temperature=0.7)
+        assert blk.last_status() == (4 if left else 0)
+        return caches, p, out
+
+    whole, p0, (n0, path0, t0) = step(64, 0, 1.0)
+    first = None
+    for garbage in (3e38, float("nan"), -1.0):
+        caches, p, (n, path, t) = step(64, room, garbage)
+        assert torch.isfinite(p).all()
+        if first is None:
+            first = p
+        assert torch.equal(p, first)
+        for b in (0, 2):
+            rows = slice(6 * b, 6 * b + 6)
+            assert torch.equal(p[rows], p0[rows]) and torch.equal(path[rows], path0[rows])
+            assert n[b] == n0[b] and t[b] == t0[b]
+            for x, y in zip(caches, whole):
+                for z in "kv":
+                    m = 40 + int(n[b])
+                    assert torch.equal(slots_of(x, z, b, m), slots_of(y, z, b, m))
+        assert caches[0]["lens"].tolist() == [40 + int(n[0]), 64 - room, 40 + int(n[2])]
 
 
 def test_model_over_a_paged_cache_refusals():
