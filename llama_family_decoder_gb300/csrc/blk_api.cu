@@ -397,9 +397,9 @@ blk_status bf16_mlp_up(const blk_handle* h, const void* y2, int rows, const blk_
   return tc(h, g, s, "MLP up GEMM");
 }
 
-// out[rows, n] = bf16(a[rows, K] W[n, K]^T)
+// out[rows, n] = bf16(a[rows, K] W[n, K]^T); cu (or null): the list of B packed sequences, rows of none are left
 blk_status bf16_rows(const blk_handle* h, const void* a, int rows, int K, const void* W, int n, void* out, cudaStream_t s,
-                     const char* what) {
+                     const char* what, const int* cu = nullptr, int B = 0) {
   TcGemmDesc g;
   g.na = 1;
   g.a[0] = {a, rows, 0};
@@ -414,6 +414,8 @@ blk_status bf16_rows(const blk_handle* h, const void* a, int rows, int K, const 
   g.const_op = 2;
   g.e.out = out;
   g.e.ldo = n;
+  g.e.row_cu = cu;
+  g.e.row_seqs = B;
   return tc(h, g, s, what);
 }
 
@@ -1949,7 +1951,9 @@ blk_status blk_model_forward_paged(blk_handle* h, const blk_model* m, const int*
   const int Hd = d.n_heads * d.head_dim, KVd = d.n_kv_heads * d.head_dim, cols = qkv_cols(d);
   // Rows that get no attention (in any layer alike) keep these zeros.
   BLK_TRY(check_cuda(cudaMemsetAsync(w.o, 0, (size_t)rows * Hd * 2, s), "attention's zeros"));
-  BLK_TRY(check_cuda(launch_embed(tokens, m->embed, rows, d.hidden * 2, m->vocab, w.act0, h->status, h->num_sms, s), "embedding"));
+  BLK_TRY(check_cuda(launch_embed(tokens, m->embed, rows, d.hidden * 2, m->vocab, w.act0, h->status, h->num_sms, s, cu_seqlens,
+                                  batch),
+                     "embedding"));
   void* bufs[2] = {w.act0, w.act1};
   for (int l = 0; l < m->n_layers; ++l) {
     const blk_weights& lw = m->layers[l];
@@ -1985,9 +1989,10 @@ blk_status blk_model_forward_paged(blk_handle* h, const blk_model* m, const int*
   }
   BLK_TRY(check_cuda(launch_rmsnorm(bufs[m->n_layers & 1], m->norm_g, rows, d.hidden, d.eps, w.y, true, s), "final norm"));
   const bool probs = temperature >= 0.f;
-  BLK_TRY(bf16_rows(h, w.y, rows, d.hidden, m->lm_head, m->vocab, probs ? w.logits : out, s, "lm_head GEMM"));
+  BLK_TRY(bf16_rows(h, w.y, rows, d.hidden, m->lm_head, m->vocab, probs ? w.logits : out, s, "lm_head GEMM", cu_seqlens, batch));
   if (!probs) return BLK_OK;
-  return check_cuda(launch_probs(w.logits, rows, m->vocab, temperature, static_cast<float*>(out), h->num_sms, s), "probabilities");
+  return check_cuda(launch_probs(w.logits, rows, m->vocab, cu_seqlens, batch, temperature, static_cast<float*>(out), h->num_sms, s),
+                    "probabilities");
 }
 
 blk_status blk_mlp(blk_handle* h, const void* resid, const void* h_normed, const blk_weights* w, int rows, void* out,

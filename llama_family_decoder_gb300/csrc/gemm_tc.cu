@@ -396,7 +396,9 @@ __device__ __forceinline__ void run_epilogue(const TcParams& p, const Unit& un, 
     return;
   } else {
     const int row = un.m_tile * kBM + r_in_tile;  // activations are a single A segment
-    const bool row_ok = row < p.a_rows[0];
+    bool row_ok = row < p.a_rows[0];
+    if constexpr (EPI == (int)Epi::kStore)
+      if (e.row_cu) row_ok = row_ok && row >= e.row_cu[0] && row < e.row_cu[e.row_seqs];
     if constexpr (EPI == (int)Epi::kQkv) {
       const int d = e.head_dim;  // 128
       const int seg = un.b_seg;

@@ -112,13 +112,17 @@ cudaError_t launch_paged_keep(void* const* kv, int n_layers, const PagedCache& c
 
 // Rows of probabilities, fp32, of bf16 logits [rows, vocab] (vocab a multiple of 8): softmax(x / temperature), or
 // for temperature 0 one on the first largest logit.
-cudaError_t launch_probs(const void* logits, int rows, int vocab, float temperature, float* out, int num_sms, cudaStream_t s);
+// cu (or null): the list of B packed sequences, rows of none are not written.
+cudaError_t launch_probs(const void* logits, int rows, int vocab, const int* cu, int B, float temperature, float* out,
+                         int num_sms, cudaStream_t s);
 
 // ---------------------------------------------------------------- embedding
 // out[r, :] = table[tokens[r], :] (row_bytes per row, a multiple of 16); ids outside
-// [0, vocab) give zero rows and set the status word to INVALID_ARG.
+// [0, vocab) give zero rows and set the status word to INVALID_ARG. cu (or null): the list of B packed
+// sequences, rows of none are zeros whatever their token.
 cudaError_t launch_embed(const int* tokens, const void* table, int rows, int row_bytes, int vocab, void* out,
-                         DevStatus* st, int num_sms, cudaStream_t s);
+                         DevStatus* st, int num_sms, cudaStream_t s,
+                         const int* cu = nullptr, int B = 0);
 
 // attention_mask [B, T] (int32, zeros are padding) -> ranges[b] = [lo, hi) of row b's ones
 // ((T, T) for a row of zeros) and pos0[b] = -lo. A row whose ones are not contiguous records
@@ -179,6 +183,8 @@ struct TcSeg {
 struct TcEpiArgs {
   void* out = nullptr;  // kStore/kResid/activations: bf16 [rows, ldo]; kPartialT: float partial base
   int ldo = 0;
+  const int* row_cu = nullptr;  // kStore: device list of row_seqs packed sequences (or null); rows of none are not written
+  int row_seqs = 0;
   const void* resid = nullptr;  // kResid: [rows, ldo], bf16 or (resid_f32) fp32; null: out = acc
   int resid_f32 = 0;
   int out_f32 = 0;              // kResid: out is fp32 (the block's residual stream)

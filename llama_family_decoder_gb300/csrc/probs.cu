@@ -36,13 +36,14 @@ __device__ __forceinline__ Peak ld_dsmem_peak(uint32_t addr) {
   return p;
 }
 
-__global__ void __launch_bounds__(kThreads, 2) probs_kernel(const uint4* __restrict__ x, int vocab, float scale,
-                                                            int greedy, float4* __restrict__ out, int size) {
+__global__ void __launch_bounds__(kThreads, 2) probs_kernel(const uint4* __restrict__ x, int vocab, const int* __restrict__ cu,
+                                                            int B, float scale, int greedy, float4* __restrict__ out, int size) {
   pdl_launch_dependents();
   pdl_wait();
   __shared__ Peak sh[kThreads / 32], own;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, chunks = vocab / 8;
   const int row_at = blockIdx.x / size, rank = blockIdx.x % size, per = (chunks + size - 1) / size;
+  if (cu && (row_at < cu[0] || row_at >= cu[B])) return;  // a row of no sequence, the whole cluster alike
   const int first = min(chunks, rank * per) + threadIdx.x, end = min(chunks, (rank + 1) * per);
   const uint4* const row = x + (size_t)row_at * chunks;
   auto values = [&](const uint4& u, float (&f)[8]) {
@@ -119,7 +120,8 @@ __global__ void __launch_bounds__(kThreads, 2) probs_kernel(const uint4* __restr
 
 }  // namespace
 
-cudaError_t launch_probs(const void* logits, int rows, int vocab, float temperature, float* out, int num_sms, cudaStream_t s) {
+cudaError_t launch_probs(const void* logits, int rows, int vocab, const int* cu, int B, float temperature, float* out,
+                         int num_sms, cudaStream_t s) {
   if (rows <= 0) return cudaSuccess;
   if (vocab % 8) return cudaErrorInvalidValue;
   const bool greedy = temperature == 0.f;
@@ -129,7 +131,7 @@ cudaError_t launch_probs(const void* logits, int rows, int vocab, float temperat
   while (size < kMaxCluster && 2ll * size * rows <= 2ll * num_sms && size * kThreads < vocab / 8) size *= 2;
   // finite and not 0: the largest logit's exponent is 0, an infinite one's stays infinite
   const float scale = greedy ? 1.f : std::min(std::max(1.4426950408889634f / temperature, FLT_MIN), FLT_MAX);
-  return launch_clusters(probs_kernel, rows * size, kThreads, 0, size, s, static_cast<const uint4*>(logits), vocab, scale,
+  return launch_clusters(probs_kernel, rows * size, kThreads, 0, size, s, static_cast<const uint4*>(logits), vocab, cu, B, scale,
                          greedy ? 1 : 0, reinterpret_cast<float4*>(out), size);
 }
 

@@ -1271,6 +1271,36 @@ def test_model_verify_at_the_end_of_a_page_list(kind, room):
         assert caches[0]["lens"].tolist() == [40 + int(n[0]), 64 - room, 40 + int(n[2])]
 
 
+@pytest.mark.parametrize("vocab", [1024, 4104])
+@pytest.mark.parametrize("temperature", [None, 0.0, 1.0])
+def test_model_rows_of_no_sequence(vocab, temperature):
+    """A padded batch: out is left as it was before the first and behind the last sequence, whatever stands there for
+    tokens, and the status word says nothing of them."""
+    blk, dev, _ = model_of(vocab=vocab, seed=14)
+    r = np.random.default_rng(2)
+    rows, first, behind = [3, 0, 5, 130], 4, 150
+    n = first + sum(rows) + behind
+    tokens = r.integers(0, vocab, sum(rows)).tolist()
+    c = blk.paged_cache(4, 160, 16)
+    caches = [c, blk.paged_cache(0, 0, shared=c)]
+    dtype = torch.bfloat16 if temperature is None else torch.float32
+    plain = blk.model_forward_paged(ints(tokens), *dev, caches, cu_of(rows), temperature=temperature)
+    want = blk.model_forward_paged(ints([0] * first + tokens + [0] * behind), *dev, caches, cu_of(rows, first), temperature=temperature)
+    want = want[first:n - behind]
+    if temperature is None:  # keys may be cut elsewhere for another number of rows
+        assert rel_err(want, np64(plain)) <= 2 * TOL_MODEL_2
+    out = torch.full((n, vocab), 7.0, dtype=dtype, device=DEV)
+    padded = ints([-1] * first + tokens + [2**31 - 1, -1, 5] * (behind // 3))
+    got = blk.model_forward_paged(padded, *dev, caches, cu_of(rows, first), temperature=temperature, out=out)
+    assert blk.last_status() == 0 and got is out
+    assert torch.equal(out[first:n - behind], want)
+    assert torch.all(out[:first] == 7) and torch.all(out[n - behind:] == 7)
+    # a token of a sequence that is none is still said
+    padded[first] = -1
+    blk.model_forward_paged(padded, *dev, caches, cu_of(rows, first), temperature=temperature, out=out)
+    assert blk.last_status() == 1
+
+
 def test_model_over_a_paged_cache_refusals():
     blk, dev, _ = model_of()
     c = blk.paged_cache(2, 32, 16)
