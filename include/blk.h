@@ -559,7 +559,7 @@ blk_status blk_paged_keep(blk_handle* h, const blk_paged_cache* caches, int n_ca
  * and attends, by parents, as blk_paged_append and blk_attn_paged do; lens does not move (blk_paged_keep).
  * A tree's rows need depths; no two layers may have the same k or v. temperature < 0: out is the logits, bf16 [rows, vocab]; > 0: the probabilities
  * softmax(logits / temperature), fp32 [rows, vocab], what blk_verify_drafts takes; 0: all of it on the
- * largest logit (the first of several). The softmax is of the bf16 logits, in fp32. A token of a sequence outside
+ * largest logit (the first of several; a row with a NaN and nothing above -inf: NaN). The softmax is of the bf16 logits, in fp32. A token of a sequence outside
  * [0, vocab) embeds as zeros and sets the status word to INVALID_ARG. For rows without an output of blk_attn_paged (those
  * of a sequence that passes its page list, of a tree's sequence from the 65th on) attention counts as 0: what out has for
  * them is the same each time and means nothing; blk_paged_keep leaves such a sequence alone.

@@ -1,5 +1,6 @@
 // Probabilities of the rows of a model's logits: softmax(x / temperature) in fp32, or for temperature 0 all of it
-// on the largest logit (the first one of several). A cluster of CTAs takes a row, a stretch each: a running maximum and
+// on the largest logit (the first one of several; a NaN is not one, and a row with a NaN and nothing above -inf gives NaN).
+// A cluster of CTAs takes a row, a stretch each: a running maximum and
 // sum in the log2 domain, joined over the CTA and in distributed shared memory, then the probabilities from the logits
 // read again (from L1 or L2). Bound by HBM for many rows, by a launch and two dependent rounds of loads for few. What it adds
 // to the model's call: 64 rows of 32000 11.7 us (one CTA a row: 14.6), of 128000 19.8 (36.3; their bytes 7.2), 400 rows
@@ -17,7 +18,8 @@ constexpr int kThreads = 512;
 constexpr int kMaxCluster = 8;
 constexpr int kAtOnce = 4;  // chunks of eight values of a thread under way
 
-struct Peak {  // a maximum, where it is first, and the sum of 2^((x - maximum) scale)
+constexpr int kNowhere = 0x7fffffff;
+struct Peak {  // a maximum, where it is first (kNowhere: nothing is above -inf), and the sum of 2^((x - maximum) scale)
   float m, l;
   int at;
 };
@@ -69,7 +71,7 @@ __global__ void __launch_bounds__(kThreads, 2) probs_kernel(const uint4* __restr
         }
     }
   };
-  Peak p{-INFINITY, 0.f, 0x7fffffff};
+  Peak p{-INFINITY, 0.f, kNowhere};
   each([&](int i, const float (&f)[8]) {
     float m = p.m;
 #pragma unroll
@@ -105,10 +107,13 @@ __global__ void __launch_bounds__(kThreads, 2) probs_kernel(const uint4* __restr
     cluster_arrive();  // (waited for below: nobody leaves while its peak may be read)
   }
   const float mu = p.m == -INFINITY ? 0.f : p.m, inv = 1.f / p.l;
+  // nothing above -inf: the first -inf is the largest, unless the sum (of zeros) tells of a NaN
+  const int top = p.at == kNowhere ? 0 : p.at;
+  const float none = p.at == kNowhere && p.l != p.l ? p.l : 0.f;
   float4* const to = out + (size_t)row_at * (vocab / 4);
   each([&](int i, float (&f)[8]) {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) f[k] = greedy ? (8 * i + k == p.at ? 1.f : 0.f) : exp2f((f[k] - mu) * scale) * inv;
+    for (int k = 0; k < 8; ++k) f[k] = greedy ? (8 * i + k == top ? 1.f + none : none) : exp2f((f[k] - mu) * scale) * inv;
     to[2 * i] = make_float4(f[0], f[1], f[2], f[3]);
     to[2 * i + 1] = make_float4(f[4], f[5], f[6], f[7]);
   });

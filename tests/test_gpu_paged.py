@@ -1125,6 +1125,40 @@ def test_probabilities_of_rows_with_ties_and_infinities():
     assert torch.isfinite(p[0]).all() and torch.isnan(p[1:]).all()  # the third row sees the second
 
 
+def logits_of(values, seed=3):
+    """A model whose logits in a row are c * values (bf16, as it gives them itself), c > 0 another one in each row: all rows
+    of lm_head are multiples of one vector. Returns a call of it for n tokens and a temperature."""
+    blk, (layers, embed, norm_g, _), _ = model_of(vocab=len(values), seed=seed)
+    lm_head = torch.zeros(len(values), embed.shape[1], dtype=torch.bfloat16, device=DEV)
+    lm_head[:, 0] = values.to(DEV).bfloat16()  # 0 * y is 0 for all finite y
+
+    def call(n, temperature):
+        c = blk.paged_cache(1, n + 1, 256)
+        caches = [c, blk.paged_cache(0, 0, shared=c)]
+        return blk.model_forward_paged(1 + torch.arange(n, device=DEV, dtype=torch.int32) % (len(values) - 1), layers, embed, norm_g,
+                                       lm_head, caches, ints([0, n]), temperature=temperature)
+
+    return call, blk
+
+
+@pytest.mark.parametrize("vocab", [8, 1024, 4104, 32000])
+def test_greedy_rows_without_a_number_above_minus_infinity(vocab):
+    inf, nan = float("inf"), float("nan")
+    call, _ = logits_of(torch.full((vocab,), inf))
+    logits, hot = call(64, None), call(64, 0.0)
+    low = (logits == -inf).all(-1)
+    assert 0 < low.sum() < 64 and ((logits == inf).all(-1) == ~low).all()  # all of one sign in each row
+    assert torch.equal(hot, torch.eye(vocab, device=DEV)[0].expand(64, vocab))  # the first of equal ones
+    for at in (0, vocab // 2, vocab - 1):
+        values = torch.full((vocab,), inf)
+        values[at] = nan
+        hot = logits_of(values)[0](64, 0.0)
+        assert torch.isnan(hot[low]).all()
+        first = 1 if at == 0 else 0
+        assert torch.equal(hot[~low], torch.eye(vocab, device=DEV)[first].expand(int((~low).sum()), vocab))
+    assert torch.isnan(logits_of(torch.full((vocab,), nan))[0](3, 0.0)).all()
+
+
 @pytest.mark.parametrize("temperature", [0.0, 0.8])
 def test_model_steps_of_drafts(temperature):
     """Prompts, then steps of model_verify. Without a temperature every new token is the target's largest, to the
