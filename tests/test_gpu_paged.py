@@ -16,7 +16,7 @@ import torch
 
 import oracle
 from llama_family_decoder_gb300 import BlkError, DecoderBlock
-from llama_family_decoder_gb300.binding import lib
+from llama_family_decoder_gb300.binding import lib, set_wait_timeout_ns
 from llama_family_decoder_gb300.synth import Workload, make_model
 from tests.helpers import TOL, cfg_of, np64, rel_err, to_dev, weights_np
 
@@ -665,6 +665,33 @@ def test_streams_and_graphs():
     torch.cuda.synchronize()
     assert torch.equal(o, want[0]) and torch.equal(r[2], want[3]) and torch.equal(with_stream["lens"], fresh["lens"])
     assert blk.last_status() == 0
+
+
+@pytest.mark.parametrize("H,Hkv,lens,rows", [(8, 2, [3000], 1),        # clusters, slots of the same rows
+                                             (8, 2, [3000], 60),       # clusters, two slots of rows
+                                             (8, 2, [200] * 16, 1),    # a CTA a unit
+                                             (32, 8, [3000] * 40, 1),  # the line, slots that take units in turn
+                                             (32, 8, [900] * 24, 60)])  # the line, two slots of a unit
+@pytest.mark.parametrize("limit", [100, 2000])
+def test_attn_paged_waits_that_run_out(H, Hkv, lens, rows, limit):
+    """A limit below the time of a first tile: waits give up, the status says so, the CTAs' copies and products end, and
+    the next call is right."""
+    trees = [tree_of(rows, b) for b in range(len(lens))]
+    blk, c, q, ks, vs, cu, parents = attn_case(H, Hkv, lens, trees, 64)
+    want = blk.attn_paged(q, c, cu, parents)
+    assert blk.last_status() == 0
+    for _ in range(3):
+        set_wait_timeout_ns(limit)
+        try:
+            blk.attn_paged(q, c, cu, parents)
+            torch.cuda.synchronize()
+        finally:
+            set_wait_timeout_ns(0)
+        status = blk.last_status()
+        assert status == 6 if limit == 100 else status in (0, 6)
+        assert torch.equal(blk.attn_paged(q, c, cu, parents), want)
+        assert blk.last_status() == 0
+    check_attn(want, q, ks[:1], vs[:1], trees[:1], lens[:1])
 
 
 # ------------------------------------------------------------------ verification
