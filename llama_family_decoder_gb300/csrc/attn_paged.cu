@@ -110,15 +110,15 @@ __device__ __forceinline__ bool elect_one() {
   asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
   return r != 0;
 }
-// mbar_wait that holds to a short limit too: a try may suspend its thread past it, a look does not. Of the warps that
-// issue the products alone: they wait for the first queries, longer than a short limit is, and the others see that they
-// gave up (in all waits: trees 56.3 -> 61.1 us).
+// mbar_wait that holds to a short limit too: a try may suspend its thread past it, a look does not. For the waits of a
+// unit, not of each tile: for its queries and for its last product, which takes longer than a short limit for certain. The
+// other roles see the abort flag. (In all waits: trees 56.3 -> 61.1 us.)
 constexpr unsigned long long kShortNs = 100000;
 __device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, unsigned long long budget_ns, volatile int* abort) {
   if (budget_ns >= kShortNs) return mbar_wait(bar, parity, budget_ns, abort);
-  const unsigned long long t0 = globaltimer_ns();
+  const long long t0 = clock64();  // (the global timer may stand for a microsecond); at most 2.07 cycles a ns
   while (!mbar_test_wait(bar, parity))
-    if (*abort || globaltimer_ns() - t0 > budget_ns) return false;
+    if (*abort || clock64() - t0 > (long long)(2 * budget_ns)) return false;
   return true;
 }
 // 32 bytes in one store (a 32-byte boundary)
@@ -886,7 +886,7 @@ __global__ void __launch_bounds__(Cfg<CL, TURNS>::kThreads, 1) attn_paged_kernel
         l += (a0 + a1) + (b0 + b1);
       }
       if (failed) break;
-      if (!__all_sync(0xffffffffu, mbar_wait(o_done(g), units & 1, budget, abort_flag))) {
+      if (!__all_sync(0xffffffffu, wait_for(o_done(g), units & 1, budget, abort_flag))) {
         failed = true;
         break;
       }
