@@ -1155,7 +1155,8 @@ def test_probabilities_of_rows_with_ties_and_infinities():
 def logits_of(values, seed=3):
     """A model whose logits in a row are c * values (bf16, as it gives them itself), c > 0 another one in each row: all rows
     of lm_head are multiples of one vector. Returns a call of it for n tokens and a temperature."""
-    blk, (layers, embed, norm_g, _), _ = model_of(vocab=len(values), seed=seed)
+    blk, (layers, _, norm_g, _), _ = model_of(vocab=64, seed=seed, max_seq=512)
+    embed = randn(seed, len(values), norm_g.numel())
     lm_head = torch.zeros(len(values), embed.shape[1], dtype=torch.bfloat16, device=DEV)
     lm_head[:, 0] = values.to(DEV).bfloat16()  # 0 * y is 0 for all finite y
 
@@ -1166,6 +1167,58 @@ def logits_of(values, seed=3):
                                        lm_head, caches, ints([0, n]), temperature=temperature)
 
     return call, blk
+
+
+def softmax_case(kind, vocab, seed):
+    """What stands in lm_head's one column: the logits are multiples of it, of either sign."""
+    g = torch.Generator().manual_seed(seed)
+    if kind == "rising":  # the maximum moves in every chunk, or never
+        return torch.linspace(-8, 8, vocab)
+    x = torch.randn(vocab, generator=g)
+    if kind == "equal":  # the largest many times in every stretch of a row
+        x = x.clamp(-1, 1)
+    elif kind == "minus inf":
+        x[torch.rand(vocab, generator=g) < 0.5] = float("-inf")
+    elif kind == "plus inf":
+        x[vocab - 5] = float("inf")
+    elif kind == "nan":
+        x[vocab // 3] = float("nan")
+    elif kind == "last":  # far above or below the others
+        x[-1] = 30.0
+    return x
+
+
+@pytest.mark.parametrize("kind", ["normal", "rising", "equal", "minus inf", "plus inf", "nan", "last"])
+@pytest.mark.parametrize("vocab,rows", [(4096, 1), (4104, 3), (8192, 1), (8200, 7), (12296, 40), (32000, 1), (32000, 64), (32000, 400),
+                                        (50264, 100), (128256, 1), (128256, 64), (128256, 160)])
+def test_probabilities_of_long_rows(kind, vocab, rows):
+    """Rows of one to eight CTAs, with uneven ends and more chunks than are under way at a time, against fp64 on the same
+    logits. u = 2^-24 (half a step of fp32), gap = (max - x) / T:
+     - an exponent takes the roundings of the difference, of 1 / T log2(e) (two) and of the product: 4 u gap. Moving a
+       sum to new maxima adds those of the parts that the gap is made of: 4 u gap of each term again, in the weighted mean;
+     - ex2 is within 2 units in the last place, 4 u; a sum is moved at most once a chunk and in 16 joins, by an ex2 and a
+       product, 5 u each; it has 8 additions a chunk and 16 joins, u each;
+     - the result takes an ex2, a division and a product: 6 u."""
+    call, blk = logits_of(softmax_case(kind, vocab, rows))
+    x = call(rows, None).double()
+    top = x.amax(-1, keepdim=True)  # NaN where one is
+    u, chunks = 2.0 ** -24, -(-vocab // 8 // 512)  # a thread's, in a row of one CTA
+    fine = top[:, 0].isfinite()
+    assert kind in ("nan", "plus inf", "minus inf") or fine.all()
+    for temperature in (1.0, 0.3):
+        p = call(rows, temperature).double()
+        assert p[~fine].isnan().all()
+        gap = (top - x)[fine] / float(np.float32(temperature))
+        e = torch.exp(-gap)
+        want = e / e.sum(-1, keepdim=True)
+        gap = torch.where(gap.isinf(), 0.0, gap)
+        bound = u * (4 * gap + 4 * (want * gap).sum(-1, keepdim=True) + 5 * (chunks + 16) + 8 * chunks + 16 + 6)
+        assert torch.all((p[fine] - want).abs() <= 1.01 * bound * want + 2.0 ** -140)
+    best = torch.where(x.isnan(), -float("inf"), x)
+    first = (best == best.amax(-1, keepdim=True)).to(torch.uint8).argmax(-1, keepdim=True)
+    assert torch.all(torch.gather((best == best.amax(-1, keepdim=True)).to(torch.uint8).cumsum(-1), 1, first) == 1)  # the first
+    assert torch.equal(call(rows, 0.0), torch.zeros(rows, vocab, device=DEV).scatter_(1, first, 1.0))
+    assert blk.last_status() == 0
 
 
 @pytest.mark.parametrize("vocab", [8, 1024, 4104, 32000])
