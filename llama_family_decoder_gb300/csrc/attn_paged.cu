@@ -720,7 +720,8 @@ __global__ void __launch_bounds__(Cfg<CL, TURNS>::kThreads, 1) attn_paged_kernel
           }
         }
       }
-      if (!over && lane == 0) mbar_arrive(turn_over(g));
+      // A unit that was given up says nothing on turn_over: the other slot would take stages that are still being filled for
+      // its own, and give them back. It sees the abort flag.
       __syncwarp();
       if (!failed && q_wanted) {
         if (wait(q_free(g), units & 1))
