@@ -63,6 +63,7 @@ constexpr float kRescaleLog2 = 8.0f;
 constexpr float kScaleLog2 = 1.4426950408889634f * 0.08838834764831845f;  // log2(e) / sqrt(128)
 constexpr int kNoBox = -2;             // a box that no row needs; entries below -1 are read as -1
 constexpr unsigned long long kDrainNs = 2000000000ULL;
+constexpr unsigned long long kShortNs = 100000;  // limits below are for tests of what happens then
 struct Join;  // see below
 struct AttnParams {
   CUtensorMap tk, tv;  // [n_pages * Hkv * page_size, 128] bf16, boxes of 64 channels x `box` rows
@@ -109,17 +110,6 @@ __device__ __forceinline__ bool elect_one() {
   uint32_t r;
   asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
   return r != 0;
-}
-// mbar_wait that holds to a short limit too: a try may suspend its thread past it, a look does not. For the waits of a
-// unit, not of each tile: for its queries and for its last product, which takes longer than a short limit for certain. The
-// other roles see the abort flag. (In all waits: trees 56.3 -> 61.1 us.)
-constexpr unsigned long long kShortNs = 100000;
-__device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, unsigned long long budget_ns, volatile int* abort) {
-  if (budget_ns >= kShortNs) return mbar_wait(bar, parity, budget_ns, abort);
-  const long long t0 = clock64();  // (the global timer may stand for a microsecond); at most 2.07 cycles a ns
-  while (!mbar_test_wait(bar, parity))
-    if (*abort || clock64() - t0 > (long long)(2 * budget_ns)) return false;
-  return true;
 }
 // 32 bytes in one store (a 32-byte boundary)
 __device__ __forceinline__ void st_global_32(void* p, const uint4& a, const uint4& b) {
@@ -586,10 +576,13 @@ __global__ void __launch_bounds__(Cfg<CL, TURNS>::kThreads, 1) attn_paged_kernel
     const uint64_t dv = smem_desc_sw128_mn(smem_u32(ring + 2 * kKVSub), kKVSub, 1024);
     const uint32_t s_tmem = tmem + C::kSlotCols * g, o_tmem = s_tmem + 64 * C::kBufs;
     constexpr int kStep = SPLIT ? 2 : 1;  // from one of the slot's tiles to the next
+    // Looks that find nothing before the time is read. Each of them under a short limit: a tile's exponentials are longer
+    // than that, so that one runs out for certain (a try_wait may sleep past any, and the global timer may stand).
+    const unsigned patience = budget < kShortNs ? 1 : 32;
     int J = 0, A = 0, units = 0;  // tiles of the CTA and of this slot, and its units
     bool failed = false;
     auto there = [](uint32_t bar, uint32_t ph) { return __all_sync(0xffffffffu, mbar_test_wait(bar, ph)) != 0; };
-    auto wait = [&](uint32_t bar, uint32_t ph) { return __all_sync(0xffffffffu, wait_for(bar, ph, budget, abort_flag)) != 0; };
+    auto wait = [&](uint32_t bar, uint32_t ph) { return __all_sync(0xffffffffu, mbar_wait(bar, ph, budget, abort_flag)) != 0; };
     // The slot's queries: loaded as soon as the last score product of a unit has read its own, and asked into L2 a
     // unit before that (behind the tiles in flight, a load from HBM would take 4 us).
     Walk ahead = *begin;
@@ -711,10 +704,10 @@ __global__ void __launch_bounds__(Cfg<CL, TURNS>::kThreads, 1) attn_paged_kernel
         }
         if (did) {
           idle = 0;
-        } else if ((++idle & 31) == 0) {
-          const unsigned long long now = globaltimer_ns();
-          if (idle == 32) idle_since = now;
-          if (__any_sync(0xffffffffu, *abort_flag != 0 || now - idle_since > budget)) {
+        } else if ((++idle & (patience - 1)) == 0) {
+          const unsigned long long now = clock64();
+          if (idle == patience) idle_since = now;
+          if (__any_sync(0xffffffffu, *abort_flag != 0 || now - idle_since > 2 * budget)) {  // 2.07 cycles a ns at most
             failed = true;
             break;
           }
@@ -887,7 +880,7 @@ __global__ void __launch_bounds__(Cfg<CL, TURNS>::kThreads, 1) attn_paged_kernel
         l += (a0 + a1) + (b0 + b1);
       }
       if (failed) break;
-      if (!__all_sync(0xffffffffu, wait_for(o_done(g), units & 1, budget, abort_flag))) {
+      if (!__all_sync(0xffffffffu, mbar_wait(o_done(g), units & 1, budget, abort_flag))) {
         failed = true;
         break;
       }
