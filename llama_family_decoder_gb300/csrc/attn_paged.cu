@@ -576,9 +576,9 @@ __global__ void __launch_bounds__(Cfg<CL, TURNS>::kThreads, 1) attn_paged_kernel
     const uint64_t dv = smem_desc_sw128_mn(smem_u32(ring + 2 * kKVSub), kKVSub, 1024);
     const uint32_t s_tmem = tmem + C::kSlotCols * g, o_tmem = s_tmem + 64 * C::kBufs;
     constexpr int kStep = SPLIT ? 2 : 1;  // from one of the slot's tiles to the next
-    // Looks that find nothing before the time is read. Each of them under a short limit: a tile's exponentials are longer
-    // than that, so that one runs out for certain (a try_wait may sleep past any, and the global timer may stand).
-    const unsigned patience = budget < kShortNs ? 1 : 32;
+    // The time is read every 32 looks in a row that find nothing; under a short limit at each, so that one runs out for
+    // certain (a tile's exponentials are longer; a try_wait may sleep past any limit, and the global timer may stand).
+    const unsigned look = budget < kShortNs ? 32 : 1;
     int J = 0, A = 0, units = 0;  // tiles of the CTA and of this slot, and its units
     bool failed = false;
     auto there = [](uint32_t bar, uint32_t ph) { return __all_sync(0xffffffffu, mbar_test_wait(bar, ph)) != 0; };
@@ -704,9 +704,9 @@ __global__ void __launch_bounds__(Cfg<CL, TURNS>::kThreads, 1) attn_paged_kernel
         }
         if (did) {
           idle = 0;
-        } else if ((++idle & (patience - 1)) == 0) {
+        } else if (((idle += look) & 31) == 0) {
           const unsigned long long now = clock64();
-          if (idle == patience) idle_since = now;
+          if (idle == 32) idle_since = now;
           if (__any_sync(0xffffffffu, *abort_flag != 0 || now - idle_since > 2 * budget)) {  // 2.07 cycles a ns at most
             failed = true;
             break;
