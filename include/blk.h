@@ -448,7 +448,7 @@ blk_status blk_attn_decode_kv4(blk_handle* h, const blk_head_rows* q, const blk_
  * they were. Calls run on the handle's device, which must be current; two calls may run at once
  * on different streams if they share no workspace, no output and no cache that either writes.
  *
- * A paged KV cache in the handle's dtype: k, v [n_pages, n_kv_heads, page_size, head_dim],
+ * A paged KV cache in the handle's dtype (fp32 ones can be appended to and kept; attention reads bf16): k, v [n_pages, n_kv_heads, page_size, head_dim],
  * page_size 16, 32, 64, 128 or 256. Slot s of sequence b is row s % page_size of page
  * pages[b * max_pages + s / page_size]. lens[b] slots are filled and kept: a call's new rows go to
  * the slots from lens[b] on, and only blk_paged_keep moves lens. pages and lens are device int32,
@@ -509,6 +509,8 @@ blk_status blk_paged_append(blk_handle* h, const blk_head_rows* q, const blk_hea
  * sees may reach the others (0 * NaN). The probabilities are rounded to bf16 for
  * their product with v, the output to bf16; everything between is fp32.
  * q's rows and heads have strides of their own (no broadcast).
+ * How a small batch is cut goes by the page list's length (max_pages), the lengths being on the device: with lists far
+ * longer than its sequences it takes up to 1.6 times as long (16 sequences of up to 300 slots: 8.2 us, 12.9 with lists for 8192).
  * workspace: blk_attn_paged_workspace_bytes (packed: cu_seqlens is given; tree: parents are; of cache its
  * sizes count), 0 for small batches (then it may be NULL) and for what the call refuses.
  * Errors: INVALID_ARG, UNSUPPORTED (fp32 handle; zero strides; rows and page lists for more than 2^31 tiles

@@ -2,9 +2,9 @@
 // on the largest logit (the first one of several; a NaN is not one, and a row with a NaN and nothing above -inf gives NaN).
 // A cluster of CTAs takes a row, a stretch each: a running maximum and
 // sum in the log2 domain, joined over the CTA and in distributed shared memory, then the probabilities from the logits
-// read again (from L1 or L2). Bound by HBM for many rows, by a launch and two dependent rounds of loads for few. What it adds
-// to the model's call: 64 rows of 32000 11.7 us (one CTA a row: 14.6), of 128000 19.8 (36.3; their bytes 7.2), 400 rows
-// of 32000 23.5 (11.3).
+// read again (from L1 or L2). Few rows: a launch and two dependent rounds of loads. Many: two waves of CTAs above 304 rows, and each
+// value read and its exponential taken twice. What it adds to the model's call: 64 rows of 32000 11.7 us (one CTA a row:
+// 14.6; their bytes at HBM's rate 1.8), of 128000 19.8 (36.3; 7.2), 400 rows of 32000 23.5 (11.3).
 #include <algorithm>
 #include <cfloat>
 
