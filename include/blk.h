@@ -444,18 +444,19 @@ blk_status blk_attn_decode_kv4(blk_handle* h, const blk_head_rows* q, const blk_
  * cu_seqlens[b] .. cu_seqlens[b+1]-1, its row i being number i; cu_seqlens NULL: row b alone
  * (rows == batch). cu_seqlens (device int32 [batch + 1]) rises from >= 0 to <= rows; another list
  * sets the status word to INVALID_ARG, is read clamped, and what a row that several sequences
- * claim gets is that of one of them; in blk_attn_paged no row of a list that falls gets an output. Rows of no sequence are ignored and their outputs left as
- * they were. Calls run on the handle's device, which must be current; two calls may run at once
- * on different streams if they share no workspace, no output and no cache that either writes.
+ * claim gets is that of one of them; in blk_attn_paged no row of a list that falls gets an output. Rows
+ * of no sequence are ignored and their outputs left as they were. Calls run on the handle's device,
+ * which must be current; two calls may run at once on different streams if they share no workspace, no
+ * output and no cache that either writes.
  *
- * A paged KV cache in the handle's dtype (fp32 ones can be appended to and kept; attention reads bf16): k, v [n_pages, n_kv_heads, page_size, head_dim],
- * page_size 16, 32, 64, 128 or 256. Slot s of sequence b is row s % page_size of page
- * pages[b * max_pages + s / page_size]. lens[b] slots are filled and kept: a call's new rows go to
- * the slots from lens[b] on, and only blk_paged_keep moves lens. pages and lens are device int32,
- * pages [batch, max_pages]; entries that no row of a call needs are not looked at. An entry that
- * is needed and is not in [0, n_pages) sets the status word to INVALID_ARG; no memory outside the
- * cache is read or written. Two sequences may share pages that no row is written to. Slots from 2^31 - 2^16 on
- * lie behind any page list. */
+ * A paged KV cache in the handle's dtype (fp32 ones can be appended to and kept; attention reads bf16
+ * ones): k, v [n_pages, n_kv_heads, page_size, head_dim], page_size 16, 32, 64, 128 or 256. Slot s of
+ * sequence b is row s % page_size of page pages[b * max_pages + s / page_size]. lens[b] slots are
+ * filled and kept: a call's new rows go to the slots from lens[b] on, and only blk_paged_keep moves
+ * lens. pages and lens are device int32, pages [batch, max_pages]; entries that no row of a call needs
+ * are not looked at. An entry that is needed and is not in [0, n_pages) sets the status word to
+ * INVALID_ARG; no memory outside the cache is read or written. Two sequences may share pages that no
+ * row is written to. Slots from 2^31 - 2^16 on lie behind any page list. */
 typedef struct {
   void *k, *v;
   const int* pages;
@@ -509,8 +510,9 @@ blk_status blk_paged_append(blk_handle* h, const blk_head_rows* q, const blk_hea
  * sees may reach the others (0 * NaN). The probabilities are rounded to bf16 for
  * their product with v, the output to bf16; everything between is fp32.
  * q's rows and heads have strides of their own (no broadcast).
- * How a small batch is cut goes by the page list's length (max_pages), the lengths being on the device: with lists far
- * longer than its sequences it takes up to 1.6 times as long (16 sequences of up to 300 slots: 8.2 us, 12.9 with lists for 8192).
+ * How a small batch is cut goes by the page list's length (max_pages), the lengths being on the device:
+ * with lists far longer than its sequences it takes up to 1.6 times as long (16 sequences of up to 300
+ * slots: 8.2 us, 12.9 with lists for 8192).
  * workspace: blk_attn_paged_workspace_bytes (packed: cu_seqlens is given; tree: parents are; of cache its
  * sizes count), 0 for small batches (then it may be NULL) and for what the call refuses.
  * Errors: INVALID_ARG, UNSUPPORTED (fp32 handle; zero strides; rows and page lists for more than 2^31 tiles
@@ -547,9 +549,10 @@ blk_status blk_verify_drafts(blk_handle* h, const float* target, long long targe
  * each sequence: slot start + path[j] -> start + j in all n_caches (host array: the layers' caches, which
  * share pages, lens and sizes and differ in k and v), lens[b] = start + counts[b]; start = starts[b], or
  * lens[b] with starts NULL. path NULL: lens alone moves (a chain's first rows, a prompt's; cu_seqlens and rows are then
- * ignored). A sequence with a path that is not rising in its rows or has a row whose page is none, a negative count or start, or
- * more rows than it has is left as it is (status word INVALID_ARG), as is one whose kept rows, or with a path any of its
- * rows, pass the page list (CACHE_FULL: blk_attn_paged has no output for any of them then). counts, path, cu_seqlens and starts may not overlap lens, unless starts is lens.
+ * ignored). A sequence with a path that is not rising in its rows or has a row whose page is none, a
+ * negative count or start, or more rows than it has is left as it is (status word INVALID_ARG), as is
+ * one whose kept rows, or with a path any of its rows, pass the page list (CACHE_FULL: blk_attn_paged
+ * has no output for any of them then). counts, path, cu_seqlens and starts may not overlap lens, unless starts is lens.
  * Errors: INVALID_ARG, ALIGNMENT, CUDA. */
 blk_status blk_paged_keep(blk_handle* h, const blk_paged_cache* caches, int n_caches, const int* counts, const int* path,
                           const int* cu_seqlens, const int* starts, int batch, int rows, void* stream);
@@ -559,12 +562,14 @@ blk_status blk_paged_keep(blk_handle* h, const blk_paged_cache* caches, int n_ca
  * tokens [rows] device int32, packed by cu_seqlens; each layer appends its keys and values to its
  * cache (host array of n_layers caches that share pages, lens and sizes) at positions lens[b] + depths[row]
  * and attends, by parents, as blk_paged_append and blk_attn_paged do; lens does not move (blk_paged_keep).
- * A tree's rows need depths; no two layers may have the same k or v. temperature < 0: out is the logits, bf16 [rows, vocab]; > 0: the probabilities
- * softmax(logits / temperature), fp32 [rows, vocab], what blk_verify_drafts takes; 0: all of it on the
- * largest logit (the first of several; a row with a NaN and nothing above -inf: NaN). The softmax is of the bf16 logits, in fp32. A token of a sequence outside
- * [0, vocab) embeds as zeros and sets the status word to INVALID_ARG. For rows without an output of blk_attn_paged (those
- * of a sequence that passes its page list, of a tree's sequence from the 65th on) attention counts as 0: what out has for
- * them is the same each time and means nothing; blk_paged_keep leaves such a sequence alone.
+ * A tree's rows need depths; no two layers may have the same k or v. temperature < 0: out is the
+ * logits, bf16 [rows, vocab]; > 0: the probabilities softmax(logits / temperature), fp32 [rows, vocab],
+ * what blk_verify_drafts takes; 0: all of it on the largest logit (the first of several; a row with a
+ * NaN and nothing above -inf: NaN). The softmax is of the bf16 logits, in fp32. A token of a sequence
+ * outside [0, vocab) embeds as zeros and sets the status word to INVALID_ARG. For rows without an
+ * output of blk_attn_paged (those of a sequence that passes its page list, of a tree's sequence from
+ * the 65th on) attention counts as 0: what out has for them is the same each time and means nothing;
+ * blk_paged_keep leaves such a sequence alone.
  * workspace: blk_model_paged_workspace_bytes (of a cache its sizes count; probs: temperature >= 0).
  * Errors: those of blk_model_forward, blk_paged_append and blk_attn_paged. */
 size_t blk_model_paged_workspace_bytes(const blk_handle* h, int rows, int packed, int tree, int batch,
